@@ -82,7 +82,8 @@ typedef enum fd_status {
     FD_ERR_WORKSPACE = -3,     /* workspace missing or too small */
     FD_ERR_CUDA = -4,          /* a CUDA runtime call or launch failed */
     FD_ERR_TIMEOUT = -5,       /* an in-kernel wait ran past its limit */
-    FD_ERR_DEVICE_BOUNDS = -6  /* a kernel derived an index outside the plan */
+    FD_ERR_DEVICE_BOUNDS = -6, /* a kernel derived an index outside the plan */
+    FD_ERR_NO_PAGES = -7       /* a page operation found too few free pages */
 } fd_status;
 
 /* Keys per pipeline stage; every chunk length is a multiple of it. */
@@ -409,9 +410,198 @@ int fd_decode_static_workspace(int batch, int num_qo_heads, int num_kv_heads, in
                                float *o, float *lse, void *stream);
 
 /*
+ * ---- Writing and rearranging a paged cache ----
+ *
+ * What a serving step does to the cache around fd_decode_paged: it writes the
+ * new keys and values (with their rotary positions), makes the next step's
+ * page tables, and from time to time moves the pages together.  All of these
+ * take device data and host sizes only, launch on the given stream, make no
+ * host-synchronising call and may be captured in a CUDA graph.  Their errors on
+ * the device go to the status word of the workspace (fd_get_device_status).
+ */
+
+/* How fd_plan_rope scales the frequencies f_i = base^(-2 i / rotary_dim). */
+#define FD_ROPE_PLAIN 0
+#define FD_ROPE_LINEAR 1   /* f / factor */
+#define FD_ROPE_BANDS 2    /* f where it makes more than `high` turns over trained_len
+                              positions, f / factor below `low` turns, a linear
+                              ramp in the number of turns between */
+#define FD_ROPE_YARN 3     /* YaRN: f up to the pair that makes `high` turns over
+                              trained_len, f / factor from the one that makes `low`
+                              (both rounded outwards), a linear ramp in the pair
+                              index between; cos and sin times 0.1 ln(factor) + 1 */
+
+typedef struct fd_rope_config {
+    double base;               /* >= 1 */
+    double factor;             /* >= 1; not read for FD_ROPE_PLAIN */
+    double trained_len;        /* FD_ROPE_BANDS and FD_ROPE_YARN, as are: */
+    double low, high;          /* turns, low < high (YaRN's usual ones are 1 and 32) */
+    int32_t scaling;           /* FD_ROPE_* */
+    int32_t interleaved;       /* pairs (2i, 2i + 1); else (i, i + rotary_dim / 2) */
+} fd_rope_config;
+
+/*
+ * Rotary positions of a model (plain data; fill it with fd_plan_rope).  Pair i
+ * of a head's first rotary_dim values turns by position * f_i; step[i] is f_i
+ * in turns, times 2^64, so that the angle of any 32-bit position is exact to
+ * the rounding of f_i in 64 bits.
+ */
+typedef struct fd_rope_info {
+    int32_t head_dim;
+    int32_t rotary_dim;        /* values of a head that turn, from its start */
+    int32_t interleaved;       /* as in the config */
+    float gain;                /* factor of cos and sin */
+    uint64_t step[64];
+} fd_rope_info;
+
+/*
+ * fd_plan_rope -- the rotary frequencies (host only, no CUDA call).
+ * rotary_dim: a multiple of 16 up to head_dim (128).
+ */
+int fd_plan_rope(int head_dim, int rotary_dim, const fd_rope_config *config, fd_rope_info *info);
+
+/*
+ * fd_append_paged -- one call per step and layer before decode: rotate the new
+ * queries and keys and write the new keys and values into the paged cache.
+ *
+ *     q, k, v        bf16 [num_tokens, heads, D], heads contiguous, any token
+ *                    stride (elements, a multiple of 8, at least heads * D), so
+ *                    they may be parts of one fused projection
+ *     q_out          bf16, the rotated queries; q itself is allowed
+ *     append_indptr  int32 [B+1]  request b's new tokens are rows
+ *                    append_indptr[b] .. append_indptr[b+1]-1
+ *     kv_page_indptr, kv_last_page_len, kv_page_indices   the page tables with
+ *                    the new keys counted in: request b's new keys are the
+ *                    last ones of its table
+ *     positions      int32 [num_tokens] position of each token, or NULL: the
+ *                    token's key index in its table (keys behind a shared prefix
+ *                    that is not in the table need positions)
+ * rope: NULL for no rotation.  num_qo_heads may be 0 (no queries).
+ * num_page_entries: entries of kv_page_indices.  Tokens from append_indptr[B]
+ * on (a padded batch) are left alone, in q_out and in the cache.  A token whose
+ * key or page lies outside the tables or the pool is skipped and sets
+ * FD_ERR_DEVICE_BOUNDS.  Rotation is in fp32; each output is rounded once.
+ * Two tokens of a call must not have the same key.  workspace: at least
+ * FD_WORKSPACE_HEADER_BYTES.
+ *
+ * fd_append_paged_fp8: E4M3(value / scale[head]), nearest even, saturated at
+ * +-448 (k_scale, v_scale as in fd_decode_paged_fp8, read).
+ * fd_append_paged_int4: codes round(value / scale) in -8..7 with scale = the
+ * row's largest magnitude / 7 (1 for a row of zeros, NaN for a row with one),
+ * stored in k_scale, v_scale [Hkv][num_pages * page_size] (written).
+ */
+int fd_append_paged(int batch, int num_tokens, int num_qo_heads, int num_kv_heads, int head_dim,
+                    int page_size, int num_pages, const fd_rope_info *rope, const void *q,
+                    int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                    int64_t v_stride, const int32_t *append_indptr_dev,
+                    const int32_t *kv_page_indptr_dev, const int32_t *kv_last_page_len_dev,
+                    const int32_t *kv_page_indices_dev, int num_page_entries,
+                    const int32_t *positions_dev, void *q_out, int64_t q_out_stride, void *k_pages,
+                    void *v_pages, void *workspace, int64_t workspace_bytes, void *stream);
+
+int fd_append_paged_fp8(int batch, int num_tokens, int num_qo_heads, int num_kv_heads, int head_dim,
+                        int page_size, int num_pages, const fd_rope_info *rope, const void *q,
+                        int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                        int64_t v_stride, const int32_t *append_indptr_dev,
+                        const int32_t *kv_page_indptr_dev, const int32_t *kv_last_page_len_dev,
+                        const int32_t *kv_page_indices_dev, int num_page_entries,
+                        const int32_t *positions_dev, void *q_out, int64_t q_out_stride,
+                        void *k_pages_fp8, void *v_pages_fp8, const float *k_scale,
+                        const float *v_scale, void *workspace, int64_t workspace_bytes,
+                        void *stream);
+
+int fd_append_paged_int4(int batch, int num_tokens, int num_qo_heads, int num_kv_heads,
+                         int head_dim, int page_size, int num_pages, const fd_rope_info *rope,
+                         const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         const void *v, int64_t v_stride, const int32_t *append_indptr_dev,
+                         const int32_t *kv_page_indptr_dev, const int32_t *kv_last_page_len_dev,
+                         const int32_t *kv_page_indices_dev, int num_page_entries,
+                         const int32_t *positions_dev, void *q_out, int64_t q_out_stride,
+                         void *k_pages_int4, void *v_pages_int4, float *k_scale, float *v_scale,
+                         void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * Page tables on the device.  page_refs int32 [num_pages] counts how many
+ * table entries (of these tables, or of others the program keeps, such as a
+ * shared prefix's) hold each page; 0 is a free page.  fd_fork_pages and
+ * fd_compact_pages make the next tables and counts and list the page copies
+ * they need; fd_copy_pages makes those copies in every pool (K and V of every
+ * layer) at once.  new_page_refs may be page_refs itself.
+ *
+ * fd_pages_workspace_bytes -- the workspace of a fork or compaction (host
+ * only).  new_batch: the fork's, 0 for a compaction.  The workspace need not be
+ * zeroed beyond its header.
+ */
+int fd_pages_workspace_bytes(int num_pages, int new_batch, int64_t *bytes);
+
+/*
+ * fd_fork_pages -- the page tables of the next step: requests that fork (beams,
+ * several samples of a prompt), go on, start or end.
+ *
+ * Request i of the new batch goes on from request parent[i] of the old one (-1:
+ * a new request); an old request that is nobody's parent ends.
+ * new_page_indptr [new_batch+1] gives the new tables' sizes: each child has at
+ * least its parent's pages.  Its first entries are its parent's, the rest are
+ * fresh pages.  A partly filled last page of the parent (kv_last_page_len <
+ * page_size) goes on in the lowest child of that parent if its count is 1; every
+ * other child gets a fresh page in its place and copy_src[i] -> copy_dst[i] is
+ * the copy it needs (-1, -1: none).  Fresh pages are the lowest free ones, in
+ * the order of the new tables' entries; pages that this call sets free are not
+ * among them.  new_page_refs = page_refs minus the old entries plus the new.
+ *
+ * With too few free pages (FD_ERR_NO_PAGES), or a parent, table or tail page
+ * outside the arguments' ranges (FD_ERR_DEVICE_BOUNDS), nothing changes:
+ * new_page_refs = page_refs, and the new indices and copies are -1.  Other page
+ * ids outside the pool set FD_ERR_DEVICE_BOUNDS and become -1.
+ * old_batch and new_batch up to 32768 (FD_ERR_UNSUPPORTED above).
+ * kv_page_indices and new_page_indices must be different arrays.
+ */
+int fd_fork_pages(int old_batch, int new_batch, int page_size, int num_pages,
+                  const int32_t *parent_dev, const int32_t *kv_page_indptr_dev,
+                  const int32_t *kv_last_page_len_dev, const int32_t *kv_page_indices_dev,
+                  int num_page_entries, const int32_t *new_page_indptr_dev, int new_page_entries,
+                  const int32_t *page_refs_dev, int32_t *new_page_indices_dev,
+                  int32_t *new_page_refs_dev, int32_t *copy_src_dev, int32_t *copy_dst_dev,
+                  void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * fd_compact_pages -- move the pages in use to the front of the pool.
+ *
+ * The pages in use at or behind `limit` (0: the number of pages in use, a full
+ * compaction) move, in order, to the free pages before it, in order.
+ * copy_src[r] -> copy_dst[r] is the r-th move (-1, -1 past the last), of at most
+ * max_moves; the number of pages in use and that of free ones both bound it.
+ * new_page_indices is kv_page_indices (every table of the pool, concatenated)
+ * with the moved pages renamed; it may be the same array.  With more moves than
+ * free pages before the limit or than max_moves, nothing changes
+ * (FD_ERR_NO_PAGES) and the copies are -1.
+ */
+int fd_compact_pages(int num_pages, const int32_t *page_refs_dev,
+                     const int32_t *kv_page_indices_dev, int num_page_entries, int limit,
+                     int max_moves, int32_t *new_page_indices_dev, int32_t *new_page_refs_dev,
+                     int32_t *copy_src_dev, int32_t *copy_dst_dev, void *workspace,
+                     int64_t workspace_bytes, void *stream);
+
+/*
+ * fd_copy_pages -- copy page src[i] to page dst[i] (i < num_copies, device
+ * lists; src[i] < 0: none) within each of num_pools pools.  pools (host array of
+ * device pointers, 16-byte aligned): pool j holds num_pages pages of
+ * page_bytes[j] bytes (a multiple of 16).  An INT4 cache's scales are
+ * num_kv_heads pools each, of page_size * 4 bytes a page.  No page may be both a
+ * source and a destination, nor a destination twice (the lists of fork and
+ * compact never hold such a pair); what lands in one that is, is undefined.  Ids
+ * outside the pool are skipped and set FD_ERR_DEVICE_BOUNDS (workspace may be
+ * NULL: then only skipped).
+ */
+int fd_copy_pages(int num_pools, void *const *pools, const int64_t *page_bytes, int num_pages,
+                  int num_copies, const int32_t *src_dev, const int32_t *dst_dev, void *workspace,
+                  int64_t workspace_bytes, void *stream);
+
+/*
  * fd_get_device_status -- synchronise the stream, read and clear the status
  * word the kernels write into the workspace.  Returns FD_OK,
- * FD_ERR_TIMEOUT, FD_ERR_DEVICE_BOUNDS, or FD_ERR_CUDA if the read failed.
+ * FD_ERR_TIMEOUT, FD_ERR_DEVICE_BOUNDS, FD_ERR_NO_PAGES, or FD_ERR_CUDA if the
+ * read failed.
  */
 int fd_get_device_status(void *workspace, void *stream);
 

@@ -17,6 +17,10 @@ Entry points (same names as the C ABI, minus the ``fd_`` prefix):
   decode_int4(...), decode_paged_int4() INT4 K/V, one scale per key row and KV head
   plan_graph(...), decode_graph(...)    graph-capturable decode (device-side plan)
   merge_states(...)                     merge attention states (sequence shards)
+  plan_rope(...), append_paged(...)     rotary positions and the write of new keys and
+  append_paged_fp8(), append_paged_int4()  values into a paged cache
+  fork_pages(...), compact_pages(...)   next page tables on the device, and the page
+  copy_pages(...)                       copies they need
   get_device_status(workspace)          read and clear the kernels' error word
 
 There is no CPU fallback: if libfd.so cannot be loaded, importing the library
@@ -39,7 +43,7 @@ DEFAULT_TIMEOUT_NS = 1_000_000_000
 FD_OK = 0
 STATUS_NAMES = {
     0: "FD_OK", -1: "FD_ERR_INVALID_ARG", -2: "FD_ERR_UNSUPPORTED", -3: "FD_ERR_WORKSPACE",
-    -4: "FD_ERR_CUDA", -5: "FD_ERR_TIMEOUT", -6: "FD_ERR_DEVICE_BOUNDS",
+    -4: "FD_ERR_CUDA", -5: "FD_ERR_TIMEOUT", -6: "FD_ERR_DEVICE_BOUNDS", -7: "FD_ERR_NO_PAGES",
 }
 
 
@@ -73,12 +77,40 @@ class PlanInfo(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class RopeInfo(ctypes.Structure):
+    """Mirror of fd_rope_info (include/fd.h)."""
+    _fields_ = [
+        ("head_dim", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+        ("gain", ctypes.c_float),
+        ("step", ctypes.c_uint64 * 64),
+    ]
+
+
+class RopeConfig(ctypes.Structure):
+    """Mirror of fd_rope_config (include/fd.h)."""
+    _fields_ = [
+        ("base", ctypes.c_double),
+        ("factor", ctypes.c_double),
+        ("trained_len", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+        ("scaling", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32),
+    ]
+
+
+ROPE_SCALINGS = {"linear": 1, "bands": 2, "yarn": 3}
+
 _lock = threading.Lock()
 _lib = None
 
 # Every symbol include/fd.h declares, with its ctypes signature.
 _P, _I, _I64, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 _PI = ctypes.POINTER(PlanInfo)
+_APPEND = [_I, _I, _I, _I, _I, _I, _I, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I, _P, _P,
+           _I64, _P, _P]
 SIGNATURES = {
     "fd_status_string": ([_I], ctypes.c_char_p),
     "fd_version": ([], _I),
@@ -102,6 +134,14 @@ SIGNATURES = {
     "fd_decode_int4": ([_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _I64, _P], _I),
     "fd_decode_paged_int4": ([_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _F,
                               _P, _P, _P, _I64, _P], _I),
+    "fd_plan_rope": ([_I, _I, ctypes.POINTER(RopeConfig), ctypes.POINTER(RopeInfo)], _I),
+    "fd_append_paged": (_APPEND + [_P, _I64, _P], _I),
+    "fd_append_paged_fp8": (_APPEND + [_P, _P, _P, _I64, _P], _I),
+    "fd_append_paged_int4": (_APPEND + [_P, _P, _P, _I64, _P], _I),
+    "fd_pages_workspace_bytes": ([_I, _I, ctypes.POINTER(ctypes.c_int64)], _I),
+    "fd_fork_pages": ([_I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I64, _P], _I),
+    "fd_compact_pages": ([_I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _I64, _P], _I),
+    "fd_copy_pages": ([_I, _P, _P, _I, _I, _P, _P, _P, _I64, _P], _I),
 }
 
 
@@ -459,6 +499,247 @@ def merge_states(o_states, lse_states, *, o=None, lse=None, stream=None):
     return o, lse
 
 
+class _Same:
+    """No change of the current device."""
+
+    def __enter__(self):
+        pass
+
+    def __exit__(self, *exc):
+        return False
+
+
+_SAME = _Same()
+
+
+def _on(tensor):
+    """The tensor's device, made current for the call (launches go to the
+    current device; the default stream is that device's current one)."""
+    import torch
+    return _SAME if tensor.get_device() == torch.cuda.current_device() else torch.cuda.device(tensor.device)
+
+
+def _need(what: str, t, dtype, like=None):
+    """t is a contiguous CUDA tensor of this type (and on `like`'s device)."""
+    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or \
+            (like is not None and t.get_device() != like.get_device()):
+        raise FdError(-1, f"{what} must be a contiguous {dtype} CUDA tensor on the inputs' device")
+    return t.data_ptr()
+
+
+def _ws(workspace, like):
+    """(address, bytes) of a workspace on the inputs' device."""
+    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != like.get_device():
+        raise FdError(-3, "workspace must be a contiguous CUDA tensor on the inputs' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def plan_rope(head_dim: int, rotary_dim: int, *, interleaved: bool = False, base: float = 10000.0,
+              scaling=None) -> RopeInfo:
+    """fd_plan_rope: the rotary frequencies (host only).  scaling: None,
+    ("linear", factor), ("bands", factor, trained_len, low, high) or
+    ("yarn", factor, trained_len, low, high)."""
+    info = RopeInfo()
+    kind, args = 0, []
+    if scaling is not None:
+        if scaling[0] not in ROPE_SCALINGS or len(scaling) != (2 if scaling[0] == "linear" else 5):
+            raise FdError(-1, f"plan_rope: unknown scaling {scaling!r}")
+        kind, args = ROPE_SCALINGS[scaling[0]], [float(x) for x in scaling[1:]]
+    args += [0.0] * (4 - len(args))
+    config = RopeConfig(float(base), *args, kind, int(bool(interleaved)))
+    _check(lib().fd_plan_rope(head_dim, rotary_dim, ctypes.byref(config), ctypes.byref(info)), "fd_plan_rope")
+    return info
+
+
+def _heads(what: str, x):
+    """Token stride (elements) of a bf16 [N, H, D] CUDA tensor with contiguous heads."""
+    import torch
+    if x.dtype is not torch.bfloat16 or not x.is_cuda or x.dim() != 3 or \
+            (x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]))):
+        raise FdError(-1, f"{what} must be a bfloat16 CUDA tensor [tokens, heads, head_dim] with contiguous heads")
+    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1] * x.shape[2])
+
+
+def _append(name, pool_dtypes, per_row, q, k, v, k_pages, v_pages, append_indptr, kv_page_indptr,
+            kv_last_page_len, kv_page_indices, rope, positions, q_out, workspace, stream, scales):
+    import torch
+    N, Hkv, D = k.shape
+    Hq = 0 if q is None else q.shape[1]
+    B = append_indptr.numel() - 1
+    if v.shape != k.shape or (q is not None and (q.shape[0] != N or q.shape[2] != D)):
+        raise FdError(-1, f"{name}: q, k and v must have the same tokens and head_dim")
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[2] != Hkv or \
+            k_pages.shape[3] != per_row * D or k_pages.dtype not in pool_dtypes or \
+            v_pages.dtype not in pool_dtypes:
+        raise FdError(-1, f"{name}: pools of another shape or type")
+    if kv_page_indptr.numel() != B + 1 or kv_last_page_len.numel() < B:
+        raise FdError(-1, f"{name}: kv_page_indptr must have batch+1 and kv_last_page_len batch entries")
+    if positions is not None and positions.numel() < N:
+        raise FdError(-1, f"{name}: positions must have an entry for every token")
+    num_pages, page_size = k_pages.shape[0], k_pages.shape[1]
+    i32 = torch.int32
+    with _on(k):
+        if q is not None and q_out is None:
+            q_out = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
+        if q is not None and q_out.shape != q.shape:
+            raise FdError(-1, f"{name}: q_out must have q's shape")
+        if workspace is None:
+            workspace = torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=k.device)
+        _check(getattr(lib(), name)(
+            B, N, Hq, Hkv, D, page_size, num_pages, None if rope is None else ctypes.byref(rope),
+            _ptr(q), 0 if q is None else _heads("q", q), _ptr(k), _heads("k", k), _ptr(v), _heads("v", v),
+            _need("append_indptr", append_indptr, i32, k), _need("kv_page_indptr", kv_page_indptr, i32, k),
+            _need("kv_last_page_len", kv_last_page_len, i32, k),
+            _need("kv_page_indices", kv_page_indices, i32, k), kv_page_indices.numel(),
+            None if positions is None else _need("positions", positions, i32, k),
+            None if q is None else q_out.data_ptr(), 0 if q is None else _heads("q_out", q_out),
+            _need("k_pages", k_pages, k_pages.dtype, k), _need("v_pages", v_pages, v_pages.dtype, k),
+            *scales, *_ws(workspace, k), _stream(stream)), name)
+    return q_out
+
+
+def append_paged(q, k, v, k_pages, v_pages, append_indptr, kv_page_indptr, kv_last_page_len,
+                 kv_page_indices, *, rope=None, positions=None, q_out=None, workspace=None, stream=None):
+    """fd_append_paged: rotate q [N,Hq,D] and k [N,Hkv,D] and write k, v into the
+    bf16 page pools; returns the rotated queries (q_out; None when q is None).
+
+    All tables are int32 CUDA tensors (include/fd.h); they count the new keys in.
+    """
+    import torch
+    return _append("fd_append_paged", (torch.bfloat16,), 1, q, k, v, k_pages, v_pages, append_indptr,
+                   kv_page_indptr, kv_last_page_len, kv_page_indices, rope, positions, q_out, workspace,
+                   stream, ())
+
+
+def append_paged_fp8(q, k, v, k_pages_fp8, v_pages_fp8, k_scale, v_scale, append_indptr, kv_page_indptr,
+                     kv_last_page_len, kv_page_indices, *, rope=None, positions=None, q_out=None,
+                     workspace=None, stream=None):
+    """fd_append_paged_fp8: append_paged into E4M3 pools (uint8 or
+    float8_e4m3fn) with the given per-KV-head scales fp32 [Hkv]."""
+    import torch
+    f32 = torch.float32
+    if k_scale.numel() != k.shape[1] or v_scale.numel() != k.shape[1]:
+        raise FdError(-1, "fd_append_paged_fp8: one scale per KV head")
+    return _append("fd_append_paged_fp8", (torch.uint8, torch.float8_e4m3fn), 1, q, k, v, k_pages_fp8,
+                   v_pages_fp8, append_indptr, kv_page_indptr, kv_last_page_len, kv_page_indices, rope,
+                   positions, q_out, workspace, stream,
+                   (_need("k_scale", k_scale, f32, k), _need("v_scale", v_scale, f32, k)))
+
+
+def append_paged_int4(q, k, v, k_pages_int4, v_pages_int4, k_scale, v_scale, append_indptr,
+                      kv_page_indptr, kv_last_page_len, kv_page_indices, *, rope=None, positions=None,
+                      q_out=None, workspace=None, stream=None):
+    """fd_append_paged_int4: append_paged into packed INT4 pools
+    [num_pages, page_size, Hkv, D/2]; writes each new row's scale into k_scale,
+    v_scale fp32 [Hkv, num_pages * page_size]."""
+    import torch
+    f32 = torch.float32
+    rows = k_pages_int4.shape[0] * k_pages_int4.shape[1]
+    if k_scale.shape != (k.shape[1], rows) or v_scale.shape != (k.shape[1], rows):
+        raise FdError(-1, "fd_append_paged_int4: scales must be [Hkv, num_pages * page_size]")
+    return _append("fd_append_paged_int4", (torch.uint8,), 0.5, q, k, v, k_pages_int4, v_pages_int4,
+                   append_indptr, kv_page_indptr, kv_last_page_len, kv_page_indices, rope, positions, q_out,
+                   workspace, stream, (_need("k_scale", k_scale, f32, k), _need("v_scale", v_scale, f32, k)))
+
+
+def pages_workspace_bytes(num_pages: int, new_batch: int = 0) -> int:
+    """fd_pages_workspace_bytes: workspace of fork_pages (new_batch children) or
+    compact_pages (new_batch 0)."""
+    out = ctypes.c_int64(0)
+    _check(lib().fd_pages_workspace_bytes(num_pages, new_batch, ctypes.byref(out)), "fd_pages_workspace_bytes")
+    return out.value
+
+
+def fork_pages(parent, kv_page_indptr, kv_last_page_len, kv_page_indices, new_page_indptr,
+               new_page_entries: int, page_size: int, page_refs, *, new_page_indices=None,
+               new_page_refs=None, copy_src=None, copy_dst=None, workspace=None, stream=None):
+    """fd_fork_pages: the next step's page tables on the device (int32 CUDA
+    tensors; new_page_entries = new_page_indptr[-1], known to the host) ->
+    (new_page_indices, new_page_refs, copy_src, copy_dst); hand the last two to
+    copy_pages."""
+    import torch
+    i32, like = torch.int32, page_refs
+    n_new, n_old, pages = parent.numel(), kv_page_indptr.numel() - 1, page_refs.numel()
+    if new_page_indptr.numel() != n_new + 1 or kv_last_page_len.numel() < n_old:
+        raise FdError(-1, "fd_fork_pages: new_page_indptr must have new_batch+1 and kv_last_page_len batch entries")
+    with _on(like):
+        new = lambda n: torch.empty(n, dtype=i32, device=like.device)  # noqa: E731
+        new_page_indices = new(new_page_entries) if new_page_indices is None else new_page_indices
+        new_page_refs = new(pages) if new_page_refs is None else new_page_refs
+        copy_src = new(n_new) if copy_src is None else copy_src
+        copy_dst = new(n_new) if copy_dst is None else copy_dst
+        if new_page_indices.numel() < new_page_entries or new_page_refs.numel() != pages or \
+                copy_src.numel() < n_new or copy_dst.numel() < n_new:
+            raise FdError(-1, "fd_fork_pages: an output is too small")
+        if workspace is None:
+            workspace = torch.zeros(pages_workspace_bytes(pages, n_new), dtype=torch.uint8, device=like.device)
+        _check(lib().fd_fork_pages(
+            n_old, n_new, page_size, pages, _need("parent", parent, i32, like),
+            _need("kv_page_indptr", kv_page_indptr, i32, like),
+            _need("kv_last_page_len", kv_last_page_len, i32, like),
+            _need("kv_page_indices", kv_page_indices, i32, like), kv_page_indices.numel(),
+            _need("new_page_indptr", new_page_indptr, i32, like), new_page_entries,
+            _need("page_refs", page_refs, i32, like), _need("new_page_indices", new_page_indices, i32, like),
+            _need("new_page_refs", new_page_refs, i32, like), _need("copy_src", copy_src, i32, like),
+            _need("copy_dst", copy_dst, i32, like), *_ws(workspace, like),
+            _stream(stream)), "fd_fork_pages")
+    return new_page_indices, new_page_refs, copy_src, copy_dst
+
+
+def compact_pages(page_refs, kv_page_indices, max_moves: int, *, limit: int = 0, new_page_indices=None,
+                  new_page_refs=None, copy_src=None, copy_dst=None, workspace=None, stream=None):
+    """fd_compact_pages: rename the pages in use at or behind `limit` (0: the
+    number in use) to the lowest free ones -> (new_page_indices, new_page_refs,
+    copy_src, copy_dst); hand the last two (max_moves entries) to copy_pages."""
+    import torch
+    i32, like = torch.int32, page_refs
+    pages, entries = page_refs.numel(), kv_page_indices.numel()
+    with _on(like):
+        new = lambda n: torch.empty(n, dtype=i32, device=like.device)  # noqa: E731
+        new_page_indices = new(entries) if new_page_indices is None else new_page_indices
+        new_page_refs = new(pages) if new_page_refs is None else new_page_refs
+        copy_src = new(max_moves) if copy_src is None else copy_src
+        copy_dst = new(max_moves) if copy_dst is None else copy_dst
+        if new_page_indices.numel() < entries or new_page_refs.numel() != pages or \
+                copy_src.numel() < max_moves or copy_dst.numel() < max_moves:
+            raise FdError(-1, "fd_compact_pages: an output is too small")
+        if workspace is None:
+            workspace = torch.zeros(pages_workspace_bytes(pages), dtype=torch.uint8, device=like.device)
+        _check(lib().fd_compact_pages(
+            pages, _need("page_refs", page_refs, i32, like),
+            _need("kv_page_indices", kv_page_indices, i32, like), entries, int(limit), int(max_moves),
+            _need("new_page_indices", new_page_indices, i32, like),
+            _need("new_page_refs", new_page_refs, i32, like), _need("copy_src", copy_src, i32, like),
+            _need("copy_dst", copy_dst, i32, like), *_ws(workspace, like),
+            _stream(stream)), "fd_compact_pages")
+    return new_page_indices, new_page_refs, copy_src, copy_dst
+
+
+def copy_pages(pools, src, dst, *, workspace=None, stream=None):
+    """fd_copy_pages: page src[i] -> dst[i] (int32 CUDA tensors; src < 0: none)
+    of every pool in `pools`, contiguous CUDA tensors [num_pages, ...] (K and V
+    of all layers; an INT4 cache's scales [Hkv, num_pages * page_size] as
+    ``*scales.view(Hkv, num_pages, page_size)``)."""
+    import torch
+    if not pools or src.numel() == 0:
+        return
+    pages, n = pools[0].shape[0], len(pools)
+    if dst.numel() != src.numel():
+        raise FdError(-1, "fd_copy_pages: src and dst must have the same length")
+    for x in pools:
+        if x.shape[0] != pages or not x.is_cuda or not x.is_contiguous() or x.get_device() != src.get_device():
+            raise FdError(-1, "fd_copy_pages: pools must be contiguous CUDA tensors of as many pages, on one device")
+    if pages == 0:
+        return
+    ptrs = (ctypes.c_void_p * n)(*[x.data_ptr() for x in pools])
+    size = (ctypes.c_int64 * n)(*[x.numel() // pages * x.element_size() for x in pools])
+    with _on(src):
+        _check(lib().fd_copy_pages(n, ptrs, size, pages, src.numel(), _need("src", src, torch.int32),
+                                   _need("dst", dst, torch.int32, src),
+                                   *((None, 0) if workspace is None else _ws(workspace, src)),
+                                   _stream(stream)), "fd_copy_pages")
+
+
 def get_device_status(workspace, stream=None) -> int:
     """fd_get_device_status: synchronise, read and clear the kernels' status word."""
     return lib().fd_get_device_status(_ptr(workspace), _stream(stream))
@@ -468,7 +749,8 @@ __all__ = [
     "PlanInfo", "FdError", "lib", "build", "plan", "plan_work_items", "decode_split", "merge",
     "decode", "decode_static_workspace", "plan_paged", "decode_paged", "decode_fp8",
     "decode_paged_fp8", "decode_int4", "decode_paged_int4", "plan_graph", "decode_graph", "merge_states", "get_device_status",
-    "workspace_bytes", "num_sms",
+    "RopeInfo", "plan_rope", "append_paged", "append_paged_fp8", "append_paged_int4",
+    "pages_workspace_bytes", "fork_pages", "compact_pages", "copy_pages", "workspace_bytes", "num_sms",
     "status_string",
     "TILE_TOKENS", "WORKSPACE_HEADER_BYTES", "DEFAULT_TIMEOUT_NS",
 ]

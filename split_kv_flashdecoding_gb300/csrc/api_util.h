@@ -1,0 +1,43 @@
+// api_util.h -- small host helpers shared by the files that hold C entry points.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace fd {
+
+inline bool aligned(const void *p, uintptr_t a)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
+}
+
+inline int64_t round_up(int64_t x, int64_t m)
+{
+    return (x + m - 1) / m * m;
+}
+
+inline cudaStream_t as_stream(void *s)
+{
+    return reinterpret_cast<cudaStream_t>(s);
+}
+
+// Launch as a programmatic dependent of the preceding grid in the stream (the
+// kernel waits for that grid before it touches global memory).
+template <typename Kernel, typename... Args>
+cudaError_t launch_dependent(Kernel kern, dim3 grid, int threads, int smem_bytes, cudaStream_t stream,
+                             Args... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = (size_t)smem_bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+}  // namespace fd

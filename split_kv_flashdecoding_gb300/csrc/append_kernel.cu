@@ -1,0 +1,271 @@
+// append_kernel.cu -- rotary positions on new queries and keys, and the write
+// of the new keys and values into a paged cache (bf16, FP8 E4M3 or INT4).
+//
+// Mathematics: pair i of a head's first rotary_dim values is turned by the
+// angle position * f_i: (a, b) -> gain (a cos - b sin, b cos + a sin).  The
+// angle is kept in turns as a 64-bit fixed-point fraction: step_i = f_i / 2 pi
+// * 2^64, and position * step_i modulo 2^64 is the exact fraction of a turn of
+// that step (the plan's rounding of f_i, 2^-53 of it, is all that a far
+// position loses), so one integer product replaces a long range reduction.
+// The arithmetic is fp32; each output is rounded once.
+//
+// Bound: bytes of q (in and out), k, v and the cache rows.  A CTA takes one
+// token (short calls, whose time is the chain token -> request -> page -> row)
+// or several (long calls); the tokens' angles are computed once in shared
+// memory for all of the token's heads.  A thread's unit is two 8-value chunks
+// that hold both halves of 8 pairs, read and written 16 bytes at a time.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "api_util.h"
+#include "cache_kernels.h"
+#include "device_common.cuh"
+#include "kernels.h"
+
+namespace fd {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 8;      // tokens of one CTA
+constexpr int kUnits = kHeadDim / 16;   // two-chunk units of a head
+
+__device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8])
+{
+    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 f = bf16x2_to_float2(u[i]);
+        x[2 * i] = f.x;
+        x[2 * i + 1] = f.y;
+    }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8])
+{
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x[2 * i], x[2 * i + 1]);
+        u[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    return make_uint4(u[0], u[1], u[2], u[3]);
+}
+
+// Eight values times `inv` as E4M3 bytes, round to nearest even, saturated to
+// +-448 (NaN stays NaN).  Multiplying by the reciprocal of the scale instead of
+// dividing moves a value by at most 2^-23 of itself before the rounding.
+__device__ __forceinline__ uint2 pack8_fp8(const float (&x)[8], float inv)
+{
+    uint32_t u[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        u[i] = lo | (hi << 16);
+    }
+    return make_uint2(u[0], u[1]);
+}
+
+// Eight values as four-bit codes round(x / scale) in -8..7, value j in nibble j.
+__device__ __forceinline__ uint32_t pack8_int4(const float (&x)[8], float scale)
+{
+    uint32_t w = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int c = min(max(__float2int_rn(__fdiv_rn(x[i], scale)), -8), 7);
+        w |= (uint32_t)(c & 0xF) << (4 * i);
+    }
+    return w;
+}
+
+template <int KVT>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p)
+{
+    __shared__ float2 s_cs[kMaxTokens][kHeadDim / 2];
+    __shared__ int64_t s_row[kMaxTokens];    // cache row of the token, -1: none
+    __shared__ int s_pos[kMaxTokens], s_ok[kMaxTokens], s_count[kMaxTokens];
+
+    const int tid = threadIdx.x;
+    const int t0 = blockIdx.x * p.tokens_per_cta;
+    const int nt = min(p.tokens_per_cta, p.num_tokens - t0);
+    if (tid < kMaxTokens)
+        s_count[tid] = 0;
+    griddep_wait();
+    griddep_launch_dependents();
+    __syncthreads();
+
+    // request of each token: how many of append_indptr[1..B] are at or below it
+    {
+        int cnt[kMaxTokens];
+#pragma unroll
+        for (int i = 0; i < kMaxTokens; ++i)
+            cnt[i] = 0;
+        for (int b = tid; b < p.batch; b += kThreads) {
+            const int e = __ldg(p.append_indptr + b + 1);
+#pragma unroll
+            for (int i = 0; i < kMaxTokens; ++i)
+                cnt[i] += e <= t0 + i;
+        }
+#pragma unroll
+        for (int i = 0; i < kMaxTokens; ++i) {
+            if (i < nt) {
+                const int c = __reduce_add_sync(0xffffffffu, cnt[i]);
+                if ((tid & 31) == 0 && c)
+                    atomicAdd(&s_count[i], c);
+            }
+        }
+    }
+    __syncthreads();
+    if (tid < nt) {
+        const int t = t0 + tid, b = s_count[tid];
+        int64_t row = -1;
+        int pos = 0, ok = 0;
+        if (b < p.batch) {   // else: a padded row behind the last request, left as it is
+            const int a0 = __ldg(p.append_indptr + b), a1 = __ldg(p.append_indptr + b + 1);
+            const int e0 = __ldg(p.kv_page_indptr + b), e1 = __ldg(p.kv_page_indptr + b + 1);
+            const int last = __ldg(p.kv_last_page_len + b);
+            if (p.positions)
+                pos = __ldg(p.positions + t);
+            const int64_t len = (int64_t)(e1 - e0 - 1) * p.page_size + last;
+            const int64_t key = len - (a1 - t);
+            ok = t >= a0 && e0 >= 0 && e1 > e0 && e1 <= p.num_page_entries && last >= 1 &&
+                 last <= p.page_size && key >= 0;
+            if (ok) {
+                const int page = __ldg(p.kv_page_indices + e0 + (int)(key / p.page_size));
+                ok = page >= 0 && page < p.num_pages;
+                row = (int64_t)page * p.page_size + key % p.page_size;
+                if (!p.positions)
+                    pos = (int)key;
+            }
+            if (!ok)
+                report(p.status, FD_ERR_DEVICE_BOUNDS);
+        }
+        s_row[tid] = row;
+        s_pos[tid] = pos;
+        s_ok[tid] = ok;
+    }
+    __syncthreads();
+    for (int i = tid; i < nt * (p.rope.rotary_dim / 2); i += kThreads) {
+        const int tt = i / (p.rope.rotary_dim / 2), j = i % (p.rope.rotary_dim / 2);
+        const uint64_t turn = (uint64_t)(int64_t)s_pos[tt] * p.rope.step[j];
+        float s, c;
+        sincospif((float)(int64_t)turn * 1.0842021724855044e-19f, &s, &c);   // turn / 2^63 half turns
+        s_cs[tt][j] = make_float2(c * p.rope.gain, s * p.rope.gain);
+    }
+    __syncthreads();
+
+    const int heads = p.num_qo_heads + 2 * p.num_kv_heads;
+    const int per_token = heads * kUnits;
+    const int rot_units = p.rope.rotary_dim / 16;
+    // the 8 lanes of a head stay together (a warp holds 4 heads' units), which
+    // the INT4 scale's reduction relies on; a warp past the end leaves whole
+    for (int i = tid; i < nt * per_token; i += kThreads) {
+        const int tt = i / per_token, r = i - tt * per_token;
+        const int head = r / kUnits, u = r % kUnits;
+        if (!s_ok[tt])
+            continue;
+        const int64_t t = t0 + tt;
+        int c0, c1;   // first value of the unit's two chunks
+        if (p.rope.interleaved || u >= rot_units) {
+            c0 = u < rot_units ? 16 * u : p.rope.rotary_dim + 16 * (u - rot_units);
+            c1 = c0 + 8;
+        } else {
+            c0 = 8 * u;
+            c1 = p.rope.rotary_dim / 2 + 8 * u;
+        }
+        const bool is_q = head < p.num_qo_heads;
+        const int kvh = (head - p.num_qo_heads) % p.num_kv_heads;
+        const bool is_v = !is_q && head >= p.num_qo_heads + p.num_kv_heads;
+        const uint16_t *src = is_q   ? p.q + t * p.q_stride + head * kHeadDim
+                              : is_v ? p.v + t * p.v_stride + kvh * kHeadDim
+                                     : p.k + t * p.k_stride + kvh * kHeadDim;
+        float a[8], b[8];
+        unpack8(*reinterpret_cast<const uint4 *>(src + c0), a);
+        unpack8(*reinterpret_cast<const uint4 *>(src + c1), b);
+        if (!is_v && u < rot_units) {
+            const float2 *cs = &s_cs[tt][8 * u];
+            if (p.rope.interleaved) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = cs[j], g = cs[4 + j];
+                    const float x = a[2 * j], y = a[2 * j + 1], z = b[2 * j], w = b[2 * j + 1];
+                    a[2 * j] = x * f.x - y * f.y;
+                    a[2 * j + 1] = y * f.x + x * f.y;
+                    b[2 * j] = z * g.x - w * g.y;
+                    b[2 * j + 1] = w * g.x + z * g.y;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 f = cs[j];
+                    const float x = a[j], y = b[j];
+                    a[j] = x * f.x - y * f.y;
+                    b[j] = y * f.x + x * f.y;
+                }
+            }
+        }
+        if (is_q) {
+            uint16_t *dst = p.q_out + t * p.q_out_stride + head * kHeadDim;
+            *reinterpret_cast<uint4 *>(dst + c0) = pack8(a);
+            *reinterpret_cast<uint4 *>(dst + c1) = pack8(b);
+            continue;
+        }
+        const int64_t row = s_row[tt];
+        const int64_t at = (row * p.num_kv_heads + kvh) * kHeadDim;   // values before this head's row
+        uint8_t *pool = static_cast<uint8_t *>(is_v ? p.v_pages : p.k_pages);
+        if constexpr (KVT == kKvTypeBf16) {
+            *reinterpret_cast<uint4 *>(pool + 2 * (at + c0)) = pack8(a);
+            *reinterpret_cast<uint4 *>(pool + 2 * (at + c1)) = pack8(b);
+        } else if constexpr (KVT == kKvTypeFp8) {
+            const float inv = 1.f / __ldg((is_v ? p.v_scale : p.k_scale) + kvh);
+            *reinterpret_cast<uint2 *>(pool + at + c0) = pack8_fp8(a, inv);
+            *reinterpret_cast<uint2 *>(pool + at + c1) = pack8_fp8(b, inv);
+        } else {
+            // one scale per (row, head): largest magnitude / 7 over the head's 8
+            // lanes (1 for a row of zeros; NaN when the row holds one)
+            float m = 0.f;
+            bool nan = false;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                m = fmaxf(m, fmaxf(fabsf(a[j]), fabsf(b[j])));
+                nan |= a[j] != a[j] || b[j] != b[j];
+            }
+            if (nan)
+                m = __int_as_float(0x7fffffff);
+            const unsigned lanes = 0xffu << (tid & 24);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                const float n = __shfl_xor_sync(lanes, m, o);
+                m = (m != m || n != n) ? __int_as_float(0x7fffffff) : fmaxf(m, n);
+            }
+            float scale = __fdiv_rn(m, 7.f);
+            if (scale == 0.f)
+                scale = 1.f;
+            *reinterpret_cast<uint32_t *>(pool + (at + c0) / 2) = pack8_int4(a, scale);
+            *reinterpret_cast<uint32_t *>(pool + (at + c1) / 2) = pack8_int4(b, scale);
+            if (u == 0)
+                (is_v ? p.v_scale_out : p.k_scale_out)[(int64_t)kvh * p.num_pages * p.page_size + row] = scale;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AppendParams &params, int kv_type, cudaStream_t stream)
+{
+    AppendParams p = params;
+    // Up to one wave of CTAs at one token each (a short call is a chain of
+    // dependent loads: more CTAs, shorter chains), several tokens past it.
+    p.tokens_per_cta = p.num_tokens <= 1024 ? 1 : 4;
+    const dim3 grid((unsigned)((p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta));
+    switch (kv_type) {
+    case kKvTypeBf16: return launch_dependent(append_kernel<kKvTypeBf16>, grid, kThreads, 0, stream, p);
+    case kKvTypeFp8: return launch_dependent(append_kernel<kKvTypeFp8>, grid, kThreads, 0, stream, p);
+    default: return launch_dependent(append_kernel<kKvTypeInt4>, grid, kThreads, 0, stream, p);
+    }
+}
+
+}  // namespace fd

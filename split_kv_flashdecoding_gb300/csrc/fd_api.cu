@@ -12,8 +12,13 @@
 #include <algorithm>
 #include <vector>
 
+#include "api_util.h"
 #include "fd.h"
 #include "kernels.h"
+
+using fd::aligned;
+using fd::as_stream;
+using fd::round_up;
 
 namespace {
 
@@ -24,16 +29,6 @@ constexpr int kBoxCols = 64;     // one 128-byte swizzle span of bf16
 constexpr int kClaimOffset = 64;
 constexpr int kDoneOffset = 128;
 constexpr int kBoxRows = FD_TILE_TOKENS;
-
-bool aligned(const void *p, uintptr_t a)
-{
-    return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;
-}
-
-int64_t round_up(int64_t x, int64_t m)
-{
-    return (x + m - 1) / m * m;
-}
 
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
@@ -114,11 +109,6 @@ int check_info(const fd_plan_info *info)
     return FD_OK;
 }
 
-cudaStream_t as_stream(void *s)
-{
-    return reinterpret_cast<cudaStream_t>(s);
-}
-
 // A token unique to each fused call (never 0, the value of a zeroed flag):
 // the split kernel's CTAs publish their partial rows by writing it into their
 // flags, so flags left by earlier calls never match.
@@ -166,6 +156,7 @@ extern "C" const char *fd_status_string(int status)
     case FD_ERR_CUDA: return "FD_ERR_CUDA";
     case FD_ERR_TIMEOUT: return "FD_ERR_TIMEOUT";
     case FD_ERR_DEVICE_BOUNDS: return "FD_ERR_DEVICE_BOUNDS";
+    case FD_ERR_NO_PAGES: return "FD_ERR_NO_PAGES";
     default: return "FD_ERR_UNKNOWN";
     }
 }
