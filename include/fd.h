@@ -410,6 +410,86 @@ int fd_decode_static_workspace(int batch, int num_qo_heads, int num_kv_heads, in
                                float *o, float *lse, void *stream);
 
 /*
+ * ---- Decode attention over shared prefixes ----
+ *
+ * For a batch whose requests share long prefixes (a system prompt, a document,
+ * samples of one prompt): each prefix's keys are read and attended once for all
+ * of its requests, each request's own keys (its suffix) as in fd_decode, and
+ * the two states are merged by LSE.  The result is fd_decode's over the prefix
+ * followed by the suffix.
+ *
+ * Layout: consecutive requests share a prefix.  prefix_req_indptr int32 [P+1]:
+ * prefix g's requests are prefix_req_indptr[g] .. prefix_req_indptr[g+1]-1; it
+ * starts at 0 and ends at the batch, so a request without a prefix sits under
+ * one of no keys.
+ *   ragged  k_prefix, v_prefix bf16 [Tp, Hkv, D], prefix g's keys are rows
+ *           prefix_indptr[g] .. prefix_indptr[g+1]-1; k, v and kv_indptr hold the
+ *           suffixes, as for fd_decode
+ *   paged   prefix g's pages are prefix_page_indices[prefix_page_indptr[g] ..],
+ *           the last one filled to prefix_last_page_len[g]; the suffixes' tables
+ *           kv_page_indptr, kv_last_page_len, kv_page_indices, as for
+ *           fd_decode_paged; all in the same page pools
+ *
+ * The plan is made once on the host for the prefixes and a room for suffix
+ * keys; a call takes device data only, makes no host-synchronising call and may
+ * be captured in a CUDA graph.  Replays see the suffixes' current lengths; the
+ * prefixes' tables must hold what the plan was made for.
+ */
+typedef struct fd_shared_plan {
+    fd_plan_info suffix;       /* the requests' own keys (as fd_plan_graph) */
+    int32_t num_prefixes;
+    int32_t chunk;             /* max prefix keys per split, a multiple of 128 */
+    int32_t num_items;         /* CTAs over the prefixes */
+    int32_t num_partial_rows;  /* partial (O, LSE) rows over the prefixes */
+    int32_t page_size;         /* 0: ragged */
+    int32_t reserved;
+    int64_t prefix_rows;       /* prefix_indptr[P]: key rows or page-list entries */
+    int64_t workspace_bytes;   /* workspace a call needs (zero-filled once) */
+    int64_t timeout_ns;        /* as in fd_plan_info */
+} fd_shared_plan;
+
+/*
+ * fd_plan_shared, fd_plan_shared_paged -- host only (no CUDA call unless
+ * num_sms == 0).  max_suffix_tokens: room for the requests' own keys, all
+ * together; 0: there are none (k, v and the suffix tables may then be NULL).
+ * chunk: 0, or the chunk length to use (a multiple of 128).
+ */
+int fd_plan_shared(int batch, int num_qo_heads, int num_kv_heads, int head_dim, int num_prefixes,
+                   const int32_t *prefix_req_indptr_host, const int32_t *prefix_indptr_host,
+                   int64_t max_suffix_tokens, int num_sms, int chunk, fd_shared_plan *plan);
+
+int fd_plan_shared_paged(int batch, int num_qo_heads, int num_kv_heads, int head_dim,
+                         int page_size, int num_prefixes, const int32_t *prefix_req_indptr_host,
+                         const int32_t *prefix_page_indptr_host,
+                         const int32_t *prefix_last_page_len_host, int64_t max_suffix_tokens,
+                         int num_sms, int chunk, fd_shared_plan *plan);
+
+/*
+ * fd_decode_shared, fd_decode_shared_paged -- one decode step.  Ragged: k and v
+ * must hold max_suffix_tokens rows.  scale must be finite.  A request without any
+ * key gets O = 0, LSE = -inf.  More suffix keys than the plan's room, prefix
+ * tables beyond it, or a page outside [0, num_pages) set FD_ERR_DEVICE_BOUNDS
+ * (the outputs are then not valid).  num_page_entries: entries of
+ * kv_page_indices.  Workspace as for fd_decode: zeroed once, calls that share it
+ * in the order of one stream.
+ */
+int fd_decode_shared(const fd_shared_plan *plan, const int32_t *prefix_req_indptr_dev,
+                     const int32_t *prefix_indptr_dev, const int32_t *kv_indptr_dev, const void *q,
+                     const void *k_prefix, const void *v_prefix, const void *k, const void *v,
+                     float scale, float *o, float *lse, void *workspace, int64_t workspace_bytes,
+                     void *stream);
+
+int fd_decode_shared_paged(const fd_shared_plan *plan, int num_pages,
+                           const int32_t *prefix_req_indptr_dev,
+                           const int32_t *prefix_page_indptr_dev,
+                           const int32_t *prefix_last_page_len_dev,
+                           const int32_t *prefix_page_indices_dev,
+                           const int32_t *kv_page_indptr_dev, const int32_t *kv_last_page_len_dev,
+                           const int32_t *kv_page_indices_dev, int num_page_entries, const void *q,
+                           const void *k_pages, const void *v_pages, float scale, float *o,
+                           float *lse, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
  * ---- Writing and rearranging a paged cache ----
  *
  * What a serving step does to the cache around fd_decode_paged: it writes the

@@ -17,6 +17,8 @@ Entry points (same names as the C ABI, minus the ``fd_`` prefix):
   decode_int4(...), decode_paged_int4() INT4 K/V, one scale per key row and KV head
   plan_graph(...), decode_graph(...)    graph-capturable decode (device-side plan)
   merge_states(...)                     merge attention states (sequence shards)
+  plan_shared(...), decode_shared(...)  decode over prefixes that requests share
+  plan_shared_paged(), decode_shared_paged()  (each prefix attended once), ragged and paged
   plan_rope(...), append_paged(...)     rotary positions and the write of new keys and
   append_paged_fp8(), append_paged_int4()  values into a paged cache
   fork_pages(...), compact_pages(...)   next page tables on the device, and the page
@@ -33,6 +35,11 @@ import os
 import threading
 
 import numpy as np
+
+try:
+    import torch
+except ImportError:  # pragma: no cover  (host planning works without it)
+    torch = None
 
 from ._build_lib import LIB as _LIB_PATH, build
 
@@ -77,6 +84,22 @@ class PlanInfo(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class SharedPlan(ctypes.Structure):
+    """Mirror of fd_shared_plan (include/fd.h)."""
+    _fields_ = [
+        ("suffix", PlanInfo),
+        ("num_prefixes", ctypes.c_int32),
+        ("chunk", ctypes.c_int32),
+        ("num_items", ctypes.c_int32),
+        ("num_partial_rows", ctypes.c_int32),
+        ("page_size", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("prefix_rows", ctypes.c_int64),
+        ("workspace_bytes", ctypes.c_int64),
+        ("timeout_ns", ctypes.c_int64),
+    ]
+
+
 class RopeInfo(ctypes.Structure):
     """Mirror of fd_rope_info (include/fd.h)."""
     _fields_ = [
@@ -109,6 +132,7 @@ _lib = None
 # Every symbol include/fd.h declares, with its ctypes signature.
 _P, _I, _I64, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 _PI = ctypes.POINTER(PlanInfo)
+_PS = ctypes.POINTER(SharedPlan)
 _APPEND = [_I, _I, _I, _I, _I, _I, _I, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I, _P, _P,
            _I64, _P, _P]
 SIGNATURES = {
@@ -134,6 +158,11 @@ SIGNATURES = {
     "fd_decode_int4": ([_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _I64, _P], _I),
     "fd_decode_paged_int4": ([_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _F,
                               _P, _P, _P, _I64, _P], _I),
+    "fd_plan_shared": ([_I, _I, _I, _I, _I, _P, _P, _I64, _I, _I, _PS], _I),
+    "fd_plan_shared_paged": ([_I, _I, _I, _I, _I, _I, _P, _P, _P, _I64, _I, _I, _PS], _I),
+    "fd_decode_shared": ([_PS, _P, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _I64, _P], _I),
+    "fd_decode_shared_paged": ([_PS, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _F, _P, _P, _P,
+                                _I64, _P], _I),
     "fd_plan_rope": ([_I, _I, ctypes.POINTER(RopeConfig), ctypes.POINTER(RopeInfo)], _I),
     "fd_append_paged": (_APPEND + [_P, _I64, _P], _I),
     "fd_append_paged_fp8": (_APPEND + [_P, _P, _P, _I64, _P], _I),
@@ -185,10 +214,9 @@ def _ptr(t) -> int | None:
 
 
 def _stream(stream):
-    import torch
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+    if stream is None:   # the current stream's handle, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def status_string(code: int) -> str:
@@ -515,7 +543,8 @@ _SAME = _Same()
 def _on(tensor):
     """The tensor's device, made current for the call (launches go to the
     current device; the default stream is that device's current one)."""
-    import torch
+    if not tensor.is_cuda:
+        raise FdError(-1, "the inputs must be CUDA tensors")
     return _SAME if tensor.get_device() == torch.cuda.current_device() else torch.cuda.device(tensor.device)
 
 
@@ -531,7 +560,7 @@ def _ws(workspace, like):
     """(address, bytes) of a workspace on the inputs' device."""
     if not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != like.get_device():
         raise FdError(-3, "workspace must be a contiguous CUDA tensor on the inputs' device")
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def plan_rope(head_dim: int, rotary_dim: int, *, interleaved: bool = False, base: float = 10000.0,
@@ -553,16 +582,16 @@ def plan_rope(head_dim: int, rotary_dim: int, *, interleaved: bool = False, base
 
 def _heads(what: str, x):
     """Token stride (elements) of a bf16 [N, H, D] CUDA tensor with contiguous heads."""
-    import torch
-    if x.dtype is not torch.bfloat16 or not x.is_cuda or x.dim() != 3 or \
-            (x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2]))):
-        raise FdError(-1, f"{what} must be a bfloat16 CUDA tensor [tokens, heads, head_dim] with contiguous heads")
-    return x.stride(0) if x.shape[0] > 1 else max(x.stride(0), x.shape[1] * x.shape[2])
+    if x.dtype is torch.bfloat16 and x.is_cuda and x.dim() == 3:
+        n, h, d = x.shape
+        token, head, value = x.stride()
+        if (value == 1 and (head == d or h <= 1)) or n * h * d == 0:
+            return token if n > 1 else max(token, h * d)
+    raise FdError(-1, f"{what} must be a bfloat16 CUDA tensor [tokens, heads, head_dim] with contiguous heads")
 
 
 def _append(name, pool_dtypes, per_row, q, k, v, k_pages, v_pages, append_indptr, kv_page_indptr,
             kv_last_page_len, kv_page_indices, rope, positions, q_out, workspace, stream, scales):
-    import torch
     N, Hkv, D = k.shape
     Hq = 0 if q is None else q.shape[1]
     B = append_indptr.numel() - 1
@@ -605,7 +634,6 @@ def append_paged(q, k, v, k_pages, v_pages, append_indptr, kv_page_indptr, kv_la
 
     All tables are int32 CUDA tensors (include/fd.h); they count the new keys in.
     """
-    import torch
     return _append("fd_append_paged", (torch.bfloat16,), 1, q, k, v, k_pages, v_pages, append_indptr,
                    kv_page_indptr, kv_last_page_len, kv_page_indices, rope, positions, q_out, workspace,
                    stream, ())
@@ -616,7 +644,6 @@ def append_paged_fp8(q, k, v, k_pages_fp8, v_pages_fp8, k_scale, v_scale, append
                      workspace=None, stream=None):
     """fd_append_paged_fp8: append_paged into E4M3 pools (uint8 or
     float8_e4m3fn) with the given per-KV-head scales fp32 [Hkv]."""
-    import torch
     f32 = torch.float32
     if k_scale.numel() != k.shape[1] or v_scale.numel() != k.shape[1]:
         raise FdError(-1, "fd_append_paged_fp8: one scale per KV head")
@@ -632,7 +659,6 @@ def append_paged_int4(q, k, v, k_pages_int4, v_pages_int4, k_scale, v_scale, app
     """fd_append_paged_int4: append_paged into packed INT4 pools
     [num_pages, page_size, Hkv, D/2]; writes each new row's scale into k_scale,
     v_scale fp32 [Hkv, num_pages * page_size]."""
-    import torch
     f32 = torch.float32
     rows = k_pages_int4.shape[0] * k_pages_int4.shape[1]
     if k_scale.shape != (k.shape[1], rows) or v_scale.shape != (k.shape[1], rows):
@@ -650,6 +676,13 @@ def pages_workspace_bytes(num_pages: int, new_batch: int = 0) -> int:
     return out.value
 
 
+def _int32_outputs(like, given, sizes):
+    """The given outputs, the missing ones in one new buffer."""
+    sizes = [0 if g is not None else n for g, n in zip(given, sizes)]
+    new = torch.empty(sum(sizes), dtype=torch.int32, device=like.device).split(sizes)
+    return [n if g is None else g for g, n in zip(given, new)]
+
+
 def fork_pages(parent, kv_page_indptr, kv_last_page_len, kv_page_indices, new_page_indptr,
                new_page_entries: int, page_size: int, page_refs, *, new_page_indices=None,
                new_page_refs=None, copy_src=None, copy_dst=None, workspace=None, stream=None):
@@ -657,17 +690,14 @@ def fork_pages(parent, kv_page_indptr, kv_last_page_len, kv_page_indices, new_pa
     tensors; new_page_entries = new_page_indptr[-1], known to the host) ->
     (new_page_indices, new_page_refs, copy_src, copy_dst); hand the last two to
     copy_pages."""
-    import torch
     i32, like = torch.int32, page_refs
     n_new, n_old, pages = parent.numel(), kv_page_indptr.numel() - 1, page_refs.numel()
     if new_page_indptr.numel() != n_new + 1 or kv_last_page_len.numel() < n_old:
         raise FdError(-1, "fd_fork_pages: new_page_indptr must have new_batch+1 and kv_last_page_len batch entries")
     with _on(like):
-        new = lambda n: torch.empty(n, dtype=i32, device=like.device)  # noqa: E731
-        new_page_indices = new(new_page_entries) if new_page_indices is None else new_page_indices
-        new_page_refs = new(pages) if new_page_refs is None else new_page_refs
-        copy_src = new(n_new) if copy_src is None else copy_src
-        copy_dst = new(n_new) if copy_dst is None else copy_dst
+        new_page_indices, new_page_refs, copy_src, copy_dst = _int32_outputs(
+            like, (new_page_indices, new_page_refs, copy_src, copy_dst),
+            (new_page_entries, pages, n_new, n_new))
         if new_page_indices.numel() < new_page_entries or new_page_refs.numel() != pages or \
                 copy_src.numel() < n_new or copy_dst.numel() < n_new:
             raise FdError(-1, "fd_fork_pages: an output is too small")
@@ -691,15 +721,12 @@ def compact_pages(page_refs, kv_page_indices, max_moves: int, *, limit: int = 0,
     """fd_compact_pages: rename the pages in use at or behind `limit` (0: the
     number in use) to the lowest free ones -> (new_page_indices, new_page_refs,
     copy_src, copy_dst); hand the last two (max_moves entries) to copy_pages."""
-    import torch
     i32, like = torch.int32, page_refs
     pages, entries = page_refs.numel(), kv_page_indices.numel()
     with _on(like):
-        new = lambda n: torch.empty(n, dtype=i32, device=like.device)  # noqa: E731
-        new_page_indices = new(entries) if new_page_indices is None else new_page_indices
-        new_page_refs = new(pages) if new_page_refs is None else new_page_refs
-        copy_src = new(max_moves) if copy_src is None else copy_src
-        copy_dst = new(max_moves) if copy_dst is None else copy_dst
+        new_page_indices, new_page_refs, copy_src, copy_dst = _int32_outputs(
+            like, (new_page_indices, new_page_refs, copy_src, copy_dst),
+            (entries, pages, max_moves, max_moves))
         if new_page_indices.numel() < entries or new_page_refs.numel() != pages or \
                 copy_src.numel() < max_moves or copy_dst.numel() < max_moves:
             raise FdError(-1, "fd_compact_pages: an output is too small")
@@ -720,24 +747,158 @@ def copy_pages(pools, src, dst, *, workspace=None, stream=None):
     of every pool in `pools`, contiguous CUDA tensors [num_pages, ...] (K and V
     of all layers; an INT4 cache's scales [Hkv, num_pages * page_size] as
     ``*scales.view(Hkv, num_pages, page_size)``)."""
-    import torch
     if not pools or src.numel() == 0:
         return
     pages, n = pools[0].shape[0], len(pools)
     if dst.numel() != src.numel():
         raise FdError(-1, "fd_copy_pages: src and dst must have the same length")
+    device = src.get_device()
     for x in pools:
-        if x.shape[0] != pages or not x.is_cuda or not x.is_contiguous() or x.get_device() != src.get_device():
+        if not x.is_cuda or x.get_device() != device or x.shape[0] != pages or not x.is_contiguous():
             raise FdError(-1, "fd_copy_pages: pools must be contiguous CUDA tensors of as many pages, on one device")
     if pages == 0:
         return
     ptrs = (ctypes.c_void_p * n)(*[x.data_ptr() for x in pools])
-    size = (ctypes.c_int64 * n)(*[x.numel() // pages * x.element_size() for x in pools])
+    size = (ctypes.c_int64 * n)(*[x.nbytes // pages for x in pools])
     with _on(src):
         _check(lib().fd_copy_pages(n, ptrs, size, pages, src.numel(), _need("src", src, torch.int32),
                                    _need("dst", dst, torch.int32, src),
                                    *((None, 0) if workspace is None else _ws(workspace, src)),
                                    _stream(stream)), "fd_copy_pages")
+
+
+def _host_ptr(a):
+    return a.ctypes.data_as(ctypes.c_void_p)
+
+
+def plan_shared(batch: int, num_qo_heads: int, num_kv_heads: int, head_dim: int, prefix_req_indptr,
+                prefix_indptr, max_suffix_tokens: int, *, num_sms: int = 0, chunk: int = 0,
+                timeout_ns: int | None = None) -> SharedPlan:
+    """fd_plan_shared: a plan for these prefixes (host int32 [P+1]: requests and
+    keys of each) and room for max_suffix_tokens keys of the requests' own."""
+    req, ip = _host_indptr(prefix_req_indptr), _host_indptr(prefix_indptr)
+    if req.size != ip.size:
+        raise FdError(-1, "prefix_req_indptr and prefix_indptr must have num_prefixes+1 entries")
+    plan_ = SharedPlan()
+    _check(lib().fd_plan_shared(batch, num_qo_heads, num_kv_heads, head_dim, req.size - 1, _host_ptr(req),
+                                _host_ptr(ip), int(max_suffix_tokens), num_sms, chunk, ctypes.byref(plan_)),
+           "fd_plan_shared")
+    if timeout_ns is not None:
+        plan_.timeout_ns = timeout_ns
+    return plan_
+
+
+def plan_shared_paged(batch: int, num_qo_heads: int, num_kv_heads: int, head_dim: int, page_size: int,
+                      prefix_req_indptr, prefix_page_indptr, prefix_last_page_len, max_suffix_tokens: int, *,
+                      num_sms: int = 0, chunk: int = 0, timeout_ns: int | None = None) -> SharedPlan:
+    """fd_plan_shared_paged: plan_shared for prefixes in a paged cache (host
+    page-list indptr [P+1] and last-page lengths [P])."""
+    req, ip = _host_indptr(prefix_req_indptr), _host_indptr(prefix_page_indptr)
+    ll = _host_indptr(prefix_last_page_len)
+    if req.size != ip.size or ll.size != ip.size - 1:
+        raise FdError(-1, "prefix indptrs must have num_prefixes+1 entries, last-page lengths num_prefixes")
+    plan_ = SharedPlan()
+    _check(lib().fd_plan_shared_paged(batch, num_qo_heads, num_kv_heads, head_dim, page_size, req.size - 1,
+                                      _host_ptr(req), _host_ptr(ip), _host_ptr(ll), int(max_suffix_tokens),
+                                      num_sms, chunk, ctypes.byref(plan_)), "fd_plan_shared_paged")
+    if timeout_ns is not None:
+        plan_.timeout_ns = timeout_ns
+    return plan_
+
+
+def _shared_outputs(name, plan_, q, kv, o, lse, workspace):
+    """Shapes of a decode_shared call; allocates what was not given."""
+    s = plan_.suffix
+    shape = (s.batch, s.num_qo_heads, s.head_dim)
+    if tuple(q.shape) != shape or any(x is not None and (x.shape[-2] != s.num_kv_heads or
+                                                         x.shape[-1] != s.head_dim) for x in kv):
+        raise FdError(-1, f"{name}: q or K/V are not of the plan's heads")
+    if o is None:
+        o = torch.empty(shape, dtype=torch.float32, device=q.device)
+    if lse is None:
+        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.zeros(plan_.workspace_bytes, dtype=torch.uint8, device=q.device)
+    if o.numel() != q.numel() or lse.numel() != shape[0] * shape[1]:
+        raise FdError(-1, f"{name}: o or lse of another size")
+    return o, lse, workspace
+
+
+def _maybe(what, t, dtype, like):
+    return None if t is None else _need(what, t, dtype, like)
+
+
+def _decode_shared(name, kv_dtypes, plan_, q, k_prefix, v_prefix, k, v, scales, prefix_req_indptr,
+                   prefix_indptr, kv_indptr, scale, o, lse, workspace, stream):
+    i32 = torch.int32
+    with _on(q):
+        o, lse, workspace = _shared_outputs(name, plan_, q, (k_prefix, v_prefix, k, v), o, lse, workspace)
+        P, room = plan_.num_prefixes, plan_.suffix.total_tokens
+        if prefix_req_indptr.numel() != P + 1 or prefix_indptr.numel() != P + 1 or \
+                (room and (kv_indptr is None or kv_indptr.numel() != plan_.suffix.batch + 1)):
+            raise FdError(-1, f"{name}: tables of another length than the plan's")
+        if plan_.num_items and (k_prefix.shape[0] < plan_.prefix_rows or v_prefix.shape[0] < plan_.prefix_rows) or \
+                (room and (k is None or v is None or k.shape[0] < room or v.shape[0] < room)):
+            raise FdError(-1, f"{name}: K/V hold fewer rows than the plan's")
+        for x in (k_prefix, v_prefix, k, v):
+            if x is not None and x.dtype not in kv_dtypes:
+                raise FdError(-1, f"{name}: K/V of another type")
+        _check(getattr(lib(), name)(
+            ctypes.byref(plan_), _need("prefix_req_indptr", prefix_req_indptr, i32, q),
+            _need("prefix_indptr", prefix_indptr, i32, q), _maybe("kv_indptr", kv_indptr, i32, q),
+            _need("q", q, torch.bfloat16), *[None if x is None else _need("K/V", x, x.dtype, q)
+                                             for x in (k_prefix, v_prefix, k, v)], *scales, float(scale),
+            _need("o", o, torch.float32, q), _need("lse", lse, torch.float32, q), *_ws(workspace, q),
+            _stream(stream)), name)
+    return o, lse
+
+
+def decode_shared(plan, q, k_prefix, v_prefix, k, v, prefix_req_indptr, prefix_indptr, kv_indptr,
+                  scale: float, *, o=None, lse=None, workspace=None, stream=None):
+    """fd_decode_shared: q [B,Hq,D], prefixes' K/V [Tp,Hkv,D] and the requests' own
+    K/V [max_suffix_tokens,Hkv,D] (bf16), tables int32 CUDA tensors -> (O, LSE) fp32."""
+    return _decode_shared("fd_decode_shared", (torch.bfloat16,), plan, q, k_prefix, v_prefix, k, v, (),
+                          prefix_req_indptr, prefix_indptr, kv_indptr, scale, o, lse, workspace, stream)
+
+
+def _decode_shared_paged(name, kv_dtypes, plan_, q, k_pages, v_pages, scales, prefix_req_indptr,
+                         prefix_page_indptr, prefix_last_page_len, prefix_page_indices, kv_page_indptr,
+                         kv_last_page_len, kv_page_indices, scale, o, lse, workspace, stream):
+    i32 = torch.int32
+    with _on(q):
+        o, lse, workspace = _shared_outputs(name, plan_, q, (k_pages, v_pages), o, lse, workspace)
+        P, B = plan_.num_prefixes, plan_.suffix.batch
+        if prefix_req_indptr.numel() != P + 1 or prefix_page_indptr.numel() != P + 1 or \
+                prefix_last_page_len.numel() < P or prefix_page_indices.numel() < plan_.prefix_rows or \
+                (plan_.suffix.total_tokens and (kv_page_indptr is None or kv_page_indptr.numel() != B + 1 or
+                                                kv_last_page_len.numel() < B)):
+            raise FdError(-1, f"{name}: tables of another length than the plan's")
+        if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[1] != plan_.page_size or \
+                k_pages.dtype not in kv_dtypes or v_pages.dtype not in kv_dtypes:
+            raise FdError(-1, f"{name}: pools of another shape or type")
+        _check(getattr(lib(), name)(
+            ctypes.byref(plan_), k_pages.shape[0], _need("prefix_req_indptr", prefix_req_indptr, i32, q),
+            _need("prefix_page_indptr", prefix_page_indptr, i32, q),
+            _need("prefix_last_page_len", prefix_last_page_len, i32, q),
+            _need("prefix_page_indices", prefix_page_indices, i32, q),
+            _maybe("kv_page_indptr", kv_page_indptr, i32, q), _maybe("kv_last_page_len", kv_last_page_len, i32, q),
+            _maybe("kv_page_indices", kv_page_indices, i32, q),
+            0 if kv_page_indices is None else kv_page_indices.numel(), _need("q", q, torch.bfloat16),
+            _need("k_pages", k_pages, k_pages.dtype, q), _need("v_pages", v_pages, v_pages.dtype, q), *scales,
+            float(scale), _need("o", o, torch.float32, q), _need("lse", lse, torch.float32, q),
+            *_ws(workspace, q), _stream(stream)), name)
+    return o, lse
+
+
+def decode_shared_paged(plan, q, k_pages, v_pages, prefix_req_indptr, prefix_page_indptr,
+                        prefix_last_page_len, prefix_page_indices, kv_page_indptr, kv_last_page_len,
+                        kv_page_indices, scale: float, *, o=None, lse=None, workspace=None, stream=None):
+    """fd_decode_shared_paged: prefixes and the requests' own keys in the same
+    bf16 page pools; tables int32 CUDA tensors (include/fd.h) -> (O, LSE) fp32."""
+    return _decode_shared_paged("fd_decode_shared_paged", (torch.bfloat16,), plan, q, k_pages, v_pages, (),
+                                prefix_req_indptr, prefix_page_indptr, prefix_last_page_len,
+                                prefix_page_indices, kv_page_indptr, kv_last_page_len, kv_page_indices,
+                                scale, o, lse, workspace, stream)
 
 
 def get_device_status(workspace, stream=None) -> int:
@@ -749,6 +910,7 @@ __all__ = [
     "PlanInfo", "FdError", "lib", "build", "plan", "plan_work_items", "decode_split", "merge",
     "decode", "decode_static_workspace", "plan_paged", "decode_paged", "decode_fp8",
     "decode_paged_fp8", "decode_int4", "decode_paged_int4", "plan_graph", "decode_graph", "merge_states", "get_device_status",
+    "SharedPlan", "plan_shared", "plan_shared_paged", "decode_shared", "decode_shared_paged",
     "RopeInfo", "plan_rope", "append_paged", "append_paged_fp8", "append_paged_int4",
     "pages_workspace_bytes", "fork_pages", "compact_pages", "copy_pages", "workspace_bytes", "num_sms",
     "status_string",

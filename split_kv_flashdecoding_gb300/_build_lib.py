@@ -20,7 +20,8 @@ LIB = os.path.join(BUILD, "libfd.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_SOURCES = ["split_kernel.cu", "split_kernel_fp8.cu", "split_kernel_int4.cu", "merge_kernel.cu",
-                "fd_api.cu", "fd_static_ws.cu", "append_kernel.cu", "pages_kernel.cu", "fd_cache_api.cu"]
+                "fd_api.cu", "fd_static_ws.cu", "append_kernel.cu", "pages_kernel.cu", "fd_cache_api.cu",
+                "shared_kernel.cu", "fd_shared_api.cu"]
 HOST_SOURCES = ["plan.cpp"]
 
 

@@ -15,6 +15,7 @@
 #include "api_util.h"
 #include "fd.h"
 #include "kernels.h"
+#include "stage1.h"
 
 using fd::aligned;
 using fd::as_stream;
@@ -30,7 +31,9 @@ constexpr int kClaimOffset = 64;
 constexpr int kDoneOffset = 128;
 constexpr int kBoxRows = FD_TILE_TOKENS;
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
+}  // namespace
+
+PFN_cuTensorMapEncodeTiled_v12000 fd::tensor_map_encoder()
 {
     static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
     static std::once_flag once;
@@ -52,10 +55,9 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 // pages that are not a multiple of 32 keys) in one copy, laid out in shared
 // memory as [half][row][64].  The block dimension comes last with a 128-byte
 // stride, smaller than the row stride: TMA takes any 16-byte-multiple strides.
-int make_kv_map(CUtensorMap *map, const void *base, int64_t rows, int num_kv_heads,
-                int box_rows = kBoxRows)
+int fd::make_kv_map(CUtensorMap *map, const void *base, int64_t rows, int num_kv_heads, int box_rows)
 {
-    auto encode = tensor_map_encoder();
+    auto encode = fd::tensor_map_encoder();
     if (!encode)
         return FD_ERR_CUDA;
     const cuuint64_t dims[3] = {kBoxCols, (cuuint64_t)rows, (cuuint64_t)num_kv_heads * 2};
@@ -69,12 +71,14 @@ int make_kv_map(CUtensorMap *map, const void *base, int64_t rows, int num_kv_hea
     return r == CUDA_SUCCESS ? FD_OK : FD_ERR_INVALID_ARG;
 }
 
+namespace {
+
 // FP8 K or V [rows, Hkv, 128] (one byte per value) as a 2-D tensor of rows x
 // Hkv*128 bytes; one box = box_rows rows x the head's 128 bytes, 128-byte
 // swizzle, zero fill past the last row.
 int make_kv_map_fp8(CUtensorMap *map, const void *base, int64_t rows, int num_kv_heads, int box_rows)
 {
-    auto encode = tensor_map_encoder();
+    auto encode = fd::tensor_map_encoder();
     if (!encode)
         return FD_ERR_CUDA;
     const cuuint64_t dims[2] = {(cuuint64_t)num_kv_heads * kHeadDim, (cuuint64_t)rows};
@@ -88,7 +92,9 @@ int make_kv_map_fp8(CUtensorMap *map, const void *base, int64_t rows, int num_kv
     return r == CUDA_SUCCESS ? FD_OK : FD_ERR_INVALID_ARG;
 }
 
-int check_info(const fd_plan_info *info)
+}  // namespace
+
+int fd::check_info(const fd_plan_info *info)
 {
     if (!info)
         return FD_ERR_INVALID_ARG;
@@ -109,6 +115,8 @@ int check_info(const fd_plan_info *info)
     return FD_OK;
 }
 
+namespace {
+
 // A token unique to each fused call (never 0, the value of a zeroed flag):
 // the split kernel's CTAs publish their partial rows by writing it into their
 // flags, so flags left by earlier calls never match.
@@ -121,16 +129,9 @@ int32_t next_call_token()
     return static_cast<int32_t>(t);
 }
 
-// Where fd_decode keeps its scratch in a workspace of a plan:
-// status header | tickets [B * Hkv] | partial LSE | partial O | flags [num_work].
-struct WorkspaceLayout {
-    int *counters;
-    float *partial_lse;
-    float *partial_o;
-    int *flags;
-};
+}  // namespace
 
-WorkspaceLayout workspace_layout(void *workspace, int64_t batch, int64_t num_kv_heads,
+fd::WorkspaceLayout fd::workspace_layout(void *workspace, int64_t batch, int64_t num_kv_heads,
                                  int64_t num_partial_rows)
 {
     uint8_t *ws = static_cast<uint8_t *>(workspace);
@@ -143,8 +144,6 @@ WorkspaceLayout workspace_layout(void *workspace, int64_t batch, int64_t num_kv_
     l.flags = reinterpret_cast<int *>(po + num_partial_rows * kHeadDim * 4);
     return l;
 }
-
-}  // namespace
 
 extern "C" const char *fd_status_string(int status)
 {
@@ -186,37 +185,23 @@ extern "C" int fd_num_sms(int device, int *num_sms)
     return FD_OK;
 }
 
-namespace {
-
-// Quantised K/V: the element type (fd::kKvTypeFp8 or fd::kKvTypeInt4) and the
-// device scales -- FP8: [Hkv] each; INT4: [Hkv][rows] each.
-struct QuantKV {
-    int type;
-    const float *k_scale;
-    const float *v_scale;
-};
-
-// The page-pool description of a paged KV cache (see fd_decode_paged).
-struct PagedKV {
-    int32_t page_size;
-    int32_t num_pages;
-    const int32_t *last_len_dev;
-    const int32_t *last_len_host;
-    const int32_t *page_indices_dev;
-    int32_t num_page_entries;   // kv_page_indptr[batch]
-};
+using fd::check_info;
+using fd::launch_stage1;
+using fd::PagedKV;
+using fd::QuantKV;
+using fd::WorkspaceLayout;
+using fd::workspace_layout;
 
 // Stage 1 launch shared by fd_decode_split (partials only), fd_decode and
 // fd_decode_paged (stage 2 fused into the split kernel: o/lse/counters
 // non-null).  kv_indptr_* is the key-row prefix, or the page-list prefix when
 // `paged` is given.
 
-int launch_stage1(const fd_plan_info *info, const void *q, const void *k, const void *v,
-                  const int32_t *kv_indptr_dev, float scale, float *partial_o, float *partial_lse,
-                  void *workspace, float *o, float *lse, int *counters,
-                  const int32_t *kv_indptr_host, cudaStream_t stream,
-                  const PagedKV *paged = nullptr, const QuantKV *quant = nullptr,
-                  bool device_plan = false, int *flags = nullptr)
+int fd::launch_stage1(const fd_plan_info *info, const void *q, const void *k, const void *v,
+                      const int32_t *kv_indptr_dev, float scale, float *partial_o, float *partial_lse,
+                      void *workspace, float *o, float *lse, int *counters,
+                      const int32_t *kv_indptr_host, cudaStream_t stream, const PagedKV *paged,
+                      const QuantKV *quant, bool device_plan, int *flags)
 {
     if (!q || !k || !v || !kv_indptr_dev || !partial_o || !partial_lse)
         return FD_ERR_INVALID_ARG;
@@ -297,8 +282,6 @@ int launch_stage1(const fd_plan_info *info, const void *q, const void *k, const 
     const cudaError_t e = fd::launch_split(maps, p, info->group_size, num_ctas, stream);
     return e == cudaSuccess ? FD_OK : FD_ERR_CUDA;
 }
-
-}  // namespace
 
 extern "C" int fd_decode_split(const fd_plan_info *info, const void *q, const void *k,
                                const void *v, const int32_t *kv_indptr_dev, float scale,

@@ -1,0 +1,738 @@
+// shared_kernel.cuh -- decode attention over prefixes that many requests
+// share, on sm_103a: each prefix's keys are read once for all of its requests.
+//
+// Mathematics: with R requests behind a prefix, the R * G queries of a KV head
+// are the rows of one matrix, S = Q K^T, P = exp2(S c - m) by row with a
+// running maximum, O += P V: the split-KV partial of `fd_decode`, with up to
+// 256 query rows instead of 8.  Every (prefix, split, KV head, block of 256
+// rows) is one CTA; the partials (normalised O, LSE) go to a workspace and a
+// second kernel merges them with the state of the request's own keys by LSE.
+//
+// Bound: up to 128 rows a KV head the bytes of K and V (a 128-key tile of both
+// is 64 KB), above that the tensor cores.  The products run on tcgen05 with
+// their accumulators in tensor memory: S and O of one 128-row tile take 256
+// columns, so a CTA holds two such streams.  With more than 128 rows the
+// streams are two row tiles that share each K and V tile; with fewer, both
+// take the same rows and every other key tile, so that one stream's softmax
+// runs under the other's products, and their states are merged at the end.
+//
+// P enters the second product as a sum of two 16-bit parts, hi + lo, which
+// keeps 16 bits of each weight (one part alone would be off by 2^-9, and the
+// output by more than its fp32 type says): three products of 128 x 128 x 128 a
+// tile for the two that the definition has.
+//
+// Warps: 0-3 and 4-7 the softmax of stream 0 and 1 (a thread owns a row, and
+// with tcgen05.ld its 128 scores), 8 the producer (TMA), 9 issues the products.
+// The running maximum is only raised, and O rescaled, when a row's maximum
+// grew by more than 2^8: until then the weights are at most 256.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "api_util.h"
+#include "device_common.cuh"
+#include "kernels.h"
+#include "shared_kernels.h"
+#include "tcgen05.cuh"
+
+namespace fd {
+namespace {
+
+constexpr int kBufBytes = kSharedTile * kHeadDim * 2;   // a K, V or Q tile of 16-bit values: 32 KB
+constexpr int kHalfBytes = kBufBytes / 2;
+constexpr int kBuffers = 7;                             // Q tiles and ring together
+constexpr int kSoftmaxThreads = 256;
+constexpr int kThreads = 320;
+constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kTmemCols = 512;
+constexpr int kStreamCols = 256;                        // S (and P over it) 128, O 128
+constexpr float kRaise = 8.f;                           // log2 of the growth that raises the maximum
+constexpr int kOutStride = kHeadDim + 4;                // floats between rows of the epilogue's staging
+
+struct SharedSmem {
+    uint64_t full[kBuffers], empty[kBuffers];
+    uint64_t s_full[2], p_ready[2], o_done[2];
+    uint64_t q_ready, tail, drain;
+    uint32_t tmem;
+    int abort;
+    int issued;             // ring fills issued (for the drain after an error)
+    int tail_issued;
+    // the CTA's item
+    int ok, req0, rows, kvh, row0, key0, keys, base, pages, part_row, part_stride, q_tiles;
+};
+constexpr int kSharedAlloc = kBuffers * kBufBytes + (int)sizeof(SharedSmem) + 1024;
+static_assert(kSharedAlloc <= 232448, "shared memory of one CTA");
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t pack2_bf16(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// The registers a tcgen05.ld wrote may be read from here on (an empty barrier
+// for the compiler, behind tcgen05.wait::ld).
+template <int N>
+__device__ __forceinline__ void settle(uint32_t (&r)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]),
+                          "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
+
+// Wait for a phase; false (and the CTA's abort flag set) when the time limit
+// passed or another warp gave up.
+__device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, const SharedParams &p, SharedSmem *sm)
+{
+    const uint32_t a = smem_addr(bar);
+    if (p.timeout_ns > 0) {
+        if (mbar_try_wait(a, parity))
+            return true;
+        const uint64_t t0 = global_timer_ns();
+        while (!*reinterpret_cast<volatile int *>(&sm->abort)) {
+            if (mbar_try_wait(a, parity))
+                return true;
+            if ((int64_t)(global_timer_ns() - t0) > p.timeout_ns)
+                break;
+        }
+    }
+    if (!*reinterpret_cast<volatile int *>(&sm->abort)) {
+        *reinterpret_cast<volatile int *>(&sm->abort) = 1;
+        report(p.status, FD_ERR_TIMEOUT);
+    }
+    return false;
+}
+
+// --------------------------------------------------- where a CTA's work lies
+
+struct PrefixCoord {
+    int32_t g, req0, reqs;     // prefix, its first request and their number
+    int32_t base, len, pages;  // first key row or page-list entry, keys, entries
+    int32_t splits, blocks;    // splits of the keys, 256-row blocks of a KV head's rows
+    int32_t item0, row0;       // items and partial rows of the prefixes before
+};
+
+// Whole warp: the prefix that holds item `j` (or request `j`).  False when
+// there is none or the tables are outside what the plan was made for.
+__device__ __forceinline__ bool locate_prefix(const SharedParams &p, int32_t j, bool by_request, PrefixCoord &out)
+{
+    const int lane = threadIdx.x & 31;
+    int32_t item_carry = 0, row_carry = 0;
+    for (int g0 = 0; g0 < p.num_prefixes; g0 += 32) {
+        const int g = g0 + lane;
+        int32_t r0 = 0, reqs = 0, base = 0, len = 0, pages = 0, splits = 0, blocks = 0;
+        if (g < p.num_prefixes) {
+            r0 = __ldg(p.req_indptr + g);
+            reqs = __ldg(p.req_indptr + g + 1) - r0;
+            base = __ldg(p.prefix_indptr + g);
+            len = __ldg(p.prefix_indptr + g + 1) - base;
+            if (p.page_size) {
+                pages = len;
+                len = pages > 0 ? (pages - 1) * p.page_size + __ldg(p.prefix_last_len + g) : 0;
+            }
+            if (reqs > 0 && len > 0) {
+                splits = shared_splits(len, p.chunk);
+                blocks = (reqs * p.group + kSharedBlockRows - 1) / kSharedBlockRows;
+            }
+        }
+        const int32_t items = splits * blocks * p.num_kv_heads, rows = splits * reqs * p.num_qo_heads;
+        int32_t item_incl = items, row_incl = rows;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t t = __shfl_up_sync(0xffffffffu, item_incl, o);
+            const int32_t u = __shfl_up_sync(0xffffffffu, row_incl, o);
+            if (lane >= o) {
+                item_incl += t;
+                row_incl += u;
+            }
+        }
+        item_incl += item_carry;
+        row_incl += row_carry;
+        const bool hit = g < p.num_prefixes && (by_request ? j >= r0 && j < r0 + reqs
+                                                           : j >= item_incl - items && j < item_incl);
+        const unsigned mask = __ballot_sync(0xffffffffu, hit);
+        if (mask) {
+            const int src = __ffs(mask) - 1;
+            out.g = g0 + src;
+            out.req0 = __shfl_sync(0xffffffffu, r0, src);
+            out.reqs = __shfl_sync(0xffffffffu, reqs, src);
+            out.base = __shfl_sync(0xffffffffu, base, src);
+            out.len = __shfl_sync(0xffffffffu, len, src);
+            out.pages = __shfl_sync(0xffffffffu, pages, src);
+            out.splits = __shfl_sync(0xffffffffu, splits, src);
+            out.blocks = __shfl_sync(0xffffffffu, blocks, src);
+            out.item0 = __shfl_sync(0xffffffffu, item_incl - items, src);
+            out.row0 = __shfl_sync(0xffffffffu, row_incl - rows, src);
+            const int32_t held = p.page_size ? out.pages : out.len;
+            return out.req0 >= 0 && out.req0 + out.reqs <= p.batch && out.base >= 0 &&
+                   out.base + held <= p.prefix_rows && out.row0 >= 0 &&
+                   (int64_t)out.row0 + (int64_t)out.splits * out.reqs * p.num_qo_heads <= p.num_partial_rows;
+        }
+        item_carry = __shfl_sync(0xffffffffu, item_incl, 31);
+        row_carry = __shfl_sync(0xffffffffu, row_incl, 31);
+    }
+    return false;
+}
+
+// Ring position of tile t's K and V of n tiles: K0, K1, V0, K2, V1, ..., the
+// order in which the products take them.
+__device__ __forceinline__ int k_pos(int t)
+{
+    return t == 0 ? 0 : 2 * t - 1;
+}
+
+__device__ __forceinline__ int v_pos(int t, int n)
+{
+    return t < n - 1 ? 2 * t + 2 : 2 * n - 1;
+}
+
+// ------------------------------------------------------------------- kernel
+
+// Layout of a 16-bit tile of 128 rows x 128 values, 128-byte swizzle.
+//  ragged: [64-value half][128 rows][128 bytes]; paged: [8-row group][half][8
+//  rows][128 bytes], which one box of a page's rows lands as.
+template <bool PAGED>
+struct TileLayout {
+    static constexpr uint32_t kHalf = PAGED ? 1024 : kHalfBytes;   // between halves
+    static constexpr uint32_t kGroup = PAGED ? 2048 : 1024;        // between 8-row groups
+};
+
+template <bool PAGED>
+__global__ void __launch_bounds__(kThreads, 1)
+    shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+                  const __grid_constant__ SharedParams p)
+{
+    using TL = TileLayout<PAGED>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    SharedSmem *sm = reinterpret_cast<SharedSmem *>(smem + kBuffers * kBufBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    if (warp == kProducerWarp && lane == 0) {
+        for (int i = 0; i < kBuffers; ++i) {
+            mbar_init(smem_addr(&sm->full[i]), 1);
+            mbar_init(smem_addr(&sm->empty[i]), 1);
+        }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_addr(&sm->s_full[s]), 1);
+            mbar_init(smem_addr(&sm->p_ready[s]), 4);   // the stream's four warps
+            mbar_init(smem_addr(&sm->o_done[s]), 1);
+        }
+        mbar_init(smem_addr(&sm->q_ready), kSoftmaxThreads / 32);
+        mbar_init(smem_addr(&sm->tail), 1);
+        mbar_init(smem_addr(&sm->drain), 1);
+        fence_mbar_init();
+        sm->abort = 0;
+        sm->issued = 0;
+        sm->tail_issued = 0;
+    }
+    if (warp == kMmaWarp)
+        tmem_alloc(smem_addr(&sm->tmem), kTmemCols);
+    griddep_wait();
+    if (warp == kProducerWarp) {
+        PrefixCoord c;
+        const int w = blockIdx.x;
+        const bool found = locate_prefix(p, w, false, c);
+        if (lane == 0) {
+            sm->ok = found;
+            if (found) {
+                const int rest = w - c.item0;
+                const int qb = rest % c.blocks, sk = rest / c.blocks;
+                const int split = sk / p.num_kv_heads;
+                const int len = shared_split_len(c.len, c.splits);
+                sm->kvh = sk % p.num_kv_heads;
+                sm->req0 = c.req0;
+                sm->row0 = qb * kSharedBlockRows;
+                sm->rows = min(c.reqs * p.group - sm->row0, kSharedBlockRows);
+                sm->key0 = split * len;
+                sm->keys = min(c.len - sm->key0, len);
+                sm->base = c.base;
+                sm->pages = c.pages;
+                sm->part_row = c.row0 + split;
+                sm->part_stride = c.splits;
+                sm->q_tiles = sm->rows > kSharedQRows ? 2 : 1;
+            } else {
+                sm->q_tiles = 1;
+                report(p.status, FD_ERR_DEVICE_BOUNDS);
+            }
+        }
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    const uint32_t tmem = sm->tmem;
+    const bool ok = sm->ok;
+    const int q_tiles = sm->q_tiles, nb = kBuffers - q_tiles;   // ring buffers
+    const int n = ok ? (sm->keys + kSharedTile - 1) / kSharedTile : 0;
+    // local steps of stream s: every tile (two row tiles) or every other one
+    auto steps = [&](int s) { return q_tiles == 2 ? n : (n + 1 - s) / 2; };
+    const uint32_t q_smem = smem_addr(smem), ring = q_smem + q_tiles * kBufBytes;
+
+    if (warp == kProducerWarp && ok) {
+        // --------------------------------------------------------- producer
+        const uint64_t pol = l2_evict_first_policy();
+        const int box = PAGED ? p.box_rows : kSharedTile;
+        const int boxes = kSharedTile / box;
+        // page row of this lane's box of tile t (paged), -1: past the prefix
+        auto box_row = [&](int t) -> int {
+            const int key = t * kSharedTile + lane * box;
+            if (lane >= boxes || key >= sm->keys)
+                return -1;
+            const int at = sm->key0 + key;
+            int page = __ldg(p.prefix_indices + sm->base + at / p.page_size);
+            if (page < 0 || page >= p.num_pages) {   // read page 0 in its place
+                report(p.status, FD_ERR_DEVICE_BOUNDS);
+                page = 0;
+            }
+            return page * p.page_size + at % p.page_size;
+        };
+        auto load = [&](const CUtensorMap *map, int pos, int row, uint64_t *bar, uint32_t bytes) {
+            const uint32_t dst = ring + (pos % nb) * kBufBytes, b = smem_addr(bar);
+            if (lane == 0)
+                mbar_arrive_expect_tx(b, bytes);
+            __syncwarp();
+            if constexpr (PAGED) {
+                if (row >= 0)
+                    asm volatile(
+                        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(
+                            dst + lane * box * kHeadDim * 2),
+                        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row & 7), "r"(2 * sm->kvh),
+                        "r"(row >> 3), "r"(b), "l"(pol)
+                        : "memory");
+            } else if (lane == 0) {
+                tma_load_3d(dst, map, 0, row, 2 * sm->kvh, b, pol);
+            }
+        };
+        int row_k = PAGED ? box_row(0) : sm->base + sm->key0, row_v = row_k;
+        bool go = true;
+        for (int pos = 0; pos < 2 * n && go; ++pos) {
+            // position pos holds K of tile t, or V of tile t (see k_pos, v_pos)
+            const bool is_k = pos == 0 || ((pos & 1) && pos < 2 * n - 1);
+            const int t = is_k ? (pos + 1) / 2 : pos == 2 * n - 1 ? n - 1 : (pos - 2) / 2;
+            if (is_k && t > 0)
+                row_k = PAGED ? box_row(t) : row_k + kSharedTile;
+            if (pos >= nb)
+                go = wait_phase(&sm->empty[pos % nb], (pos / nb - 1) & 1, p, sm);
+            go = __all_sync(0xffffffffu, go);
+            if (!go)
+                break;
+            if (lane == 0)
+                sm->issued = pos + 1;
+            const int valid = min(sm->keys - t * kSharedTile, kSharedTile);
+            uint32_t bytes = kBufBytes;
+            if constexpr (PAGED)
+                bytes = (valid + box - 1) / box * box * kHeadDim * 2;
+            if (is_k) {
+                load(&tm_k, pos, row_k, &sm->full[pos % nb], bytes);
+            } else if (valid == kSharedTile) {
+                load(&tm_v, pos, row_v, &sm->full[pos % nb], bytes);
+            } else {
+                // The rows past the last key (another prefix's, or nobody's) get
+                // weight 0, but 0 * NaN would still reach O: zero them before the
+                // products see the tile.
+                load(&tm_v, pos, row_v, &sm->tail, bytes);
+                if (lane == 0)
+                    sm->tail_issued = 1;
+                go = __all_sync(0xffffffffu, wait_phase(&sm->tail, 0, p, sm));
+                if (!go)
+                    break;
+                uint8_t *v = smem + q_tiles * kBufBytes + (pos % nb) * kBufBytes;
+                for (int i = lane; i < (kSharedTile - valid) * 16; i += 32) {
+                    const int r = valid + i / 16, c = i % 16;
+                    const uint32_t off = (c >> 3) * TL::kHalf + (r >> 3) * TL::kGroup + (r & 7) * 128 + (c & 7) * 16;
+                    *reinterpret_cast<uint4 *>(v + off) = make_uint4(0u, 0u, 0u, 0u);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&sm->full[pos % nb]));
+            }
+            if (!is_k)
+                row_v = PAGED ? row_k : row_v + kSharedTile;
+        }
+    } else if (warp == kMmaWarp && ok) {
+        // ------------------------------------------------------ the products
+        if (lane == 0) {
+            constexpr uint32_t id_s = mma_idesc(128, kSharedTile, true, false);
+            constexpr uint32_t id_o = mma_idesc(128, kHeadDim, true, true);
+            bool go = wait_phase(&sm->q_ready, 0, p, sm);
+            // S of stream s's step i: K of its tile; frees the buffer after the
+            // last stream that takes it.
+            auto scores = [&](int s, int i) {
+                const int t = q_tiles == 2 ? i : 2 * i + s, pos = k_pos(t), b = pos % nb;
+                if (!wait_phase(&sm->full[b], (pos / nb) & 1, p, sm))
+                    return false;
+                tcgen05_fence_after();
+                const uint32_t qa = q_smem + (q_tiles == 2 ? s : 0) * kBufBytes, kb = ring + b * kBufBytes;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)   // 16 head dimensions a step
+                    mma_ss(tmem + s * kStreamCols,
+                           smem_desc(qa + (k >> 2) * kHalfBytes + (k & 3) * 32, 16, 1024),
+                           smem_desc(kb + (k >> 2) * TL::kHalf + (k & 3) * 32, 16, TL::kGroup), id_s, k > 0);
+                tcgen05_commit(smem_addr(&sm->s_full[s]));
+                if (q_tiles == 1 || s == 1)
+                    tcgen05_commit(smem_addr(&sm->empty[b]));
+                return true;
+            };
+            // O += P V of stream s's step i.
+            auto values = [&](int s, int i) {
+                const int t = q_tiles == 2 ? i : 2 * i + s, pos = v_pos(t, n), b = pos % nb;
+                if (!wait_phase(&sm->full[b], (pos / nb) & 1, p, sm) || !wait_phase(&sm->p_ready[s], i & 1, p, sm))
+                    return false;
+                tcgen05_fence_after();
+                const uint32_t vb = ring + b * kBufBytes, pa = tmem + s * kStreamCols;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {   // 16 keys a step, hi then lo
+                    const uint64_t vd = smem_desc(vb + k * 2 * TL::kGroup, TL::kHalf, TL::kGroup);
+                    mma_ts(pa + 128, pa + 8 * k, vd, id_o, i > 0 || k > 0);
+                    mma_ts(pa + 128, pa + 64 + 8 * k, vd, id_o, 1);
+                }
+                if (q_tiles == 1 || s == 1)
+                    tcgen05_commit(smem_addr(&sm->empty[b]));
+                if (i == steps(s) - 1)
+                    tcgen05_commit(smem_addr(&sm->o_done[s]));
+                return true;
+            };
+            for (int s = 0; s < 2 && go; ++s)
+                if (steps(s) > 0)
+                    go = scores(s, 0);
+            for (int i = 0; i < steps(0) && go; ++i)
+                for (int s = 0; s < 2 && go; ++s) {
+                    if (i < steps(s))
+                        go = values(s, i);
+                    if (go && i + 1 < steps(s))
+                        go = scores(s, i + 1);
+                }
+            // whatever the others saw, the products in flight end before tensor
+            // memory is freed
+            tcgen05_commit(smem_addr(&sm->drain));
+            mbar_wait(smem_addr(&sm->drain), 0, kDrainTimeoutNs);
+        }
+        __syncwarp();
+    } else if (warp < kProducerWarp) {
+        // -------------------------------------------------------- the softmax
+        const int s = warp >> 2;
+        const int trow = (warp & 3) * 32 + lane;   // row of the stream's tile: lane of tensor memory
+        const uint32_t quad = (uint32_t)(warp & 3) << 21;
+        const uint32_t s_col = tmem + quad + s * kStreamCols, o_col = s_col + 128;
+        // log2 e times the scale; never 0, so that a masked score (-inf) stays -inf
+        const float c2 = fmaxf(fabsf(p.scale) * kLog2e, 1.17549435e-38f);
+        const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;   // a negative scale turns q around
+        if (ok) {
+            // Q rows into shared memory, [half][128 rows][128 bytes] a tile
+            for (int i = tid; i < q_tiles * kSharedQRows * 16; i += kSoftmaxThreads) {
+                const int r = i >> 4, ch = i & 15;
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (r < sm->rows) {
+                    const int gr = sm->row0 + r;
+                    const int64_t row = (int64_t)(sm->req0 + gr / p.group) * p.num_qo_heads + sm->kvh * p.group +
+                                        gr % p.group;
+                    v = __ldg(reinterpret_cast<const uint4 *>(p.q + row * kHeadDim) + ch);
+                    v.x ^= flip;
+                    v.y ^= flip;
+                    v.z ^= flip;
+                    v.w ^= flip;
+                }
+                const int rr = r & 127;
+                *reinterpret_cast<uint4 *>(smem + (r >> 7) * kBufBytes + (ch >> 3) * kHalfBytes + rr * 128 +
+                                           (((ch & 7) ^ (rr & 7)) << 4)) = v;
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&sm->q_ready));
+        }
+        float m_ref = -INFINITY, l = 0.f;   // maximum of the raw scores that the weights refer to
+        bool go = ok;
+        for (int i = 0; i < steps(s) && go; ++i) {
+            const int t = q_tiles == 2 ? i : 2 * i + s;
+            const int valid = sm->keys - t * kSharedTile;
+            go = __all_sync(0xffffffffu, wait_phase(&sm->s_full[s], i & 1, p, sm));
+            if (!go)
+                break;
+            tcgen05_fence_after();
+            uint32_t r0[32], r1[32], r2[32], r3[32];
+            tmem_ld32(s_col, r0);
+            tmem_ld32(s_col + 32, r1);
+            tmem_ld32(s_col + 64, r2);
+            tmem_ld32(s_col + 96, r3);
+            tmem_wait_ld();
+            settle(r0);
+            settle(r1);
+            settle(r2);
+            settle(r3);
+            if (valid < kSharedTile) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    if (j >= valid) r0[j] = 0xff800000u;
+                    if (32 + j >= valid) r1[j] = 0xff800000u;
+                    if (64 + j >= valid) r2[j] = 0xff800000u;
+                    if (96 + j >= valid) r3[j] = 0xff800000u;
+                }
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                mx[0] = fmaxf(mx[0], __uint_as_float(r0[j]));
+                mx[1] = fmaxf(mx[1], __uint_as_float(r1[j]));
+                mx[2] = fmaxf(mx[2], __uint_as_float(r2[j]));
+                mx[3] = fmaxf(mx[3], __uint_as_float(r3[j]));
+            }
+            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const bool raise = mt > m_ref && (m_ref == -INFINITY || (mt - m_ref) * c2 > kRaise);
+            if (__any_sync(0xffffffffu, raise)) {
+                // the products up to the last step are done: s_full followed them
+                const float m_new = raise ? mt : m_ref;
+                const float f = m_ref == -INFINITY ? 0.f : ex2((m_ref - m_new) * c2);
+                l *= f;
+                m_ref = m_new;
+                if (i > 0) {
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[32];
+                        tmem_ld32(o_col + 32 * c, o);
+                        tmem_wait_ld();
+                        settle(o);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                        tmem_st32(o_col + 32 * c, o);
+                    }
+                }
+            }
+            // a row whose scores are all -inf so far keeps weights of 0
+            const float off = m_ref == -INFINITY ? 0.f : m_ref * c2;
+            float sum[2] = {0.f, 0.f};
+            auto weights = [&](const uint32_t (&r)[32], int c) {
+                uint32_t hi[16], lo[16];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float a = ex2(fmaf(__uint_as_float(r[2 * j]), c2, -off));
+                    const float b = ex2(fmaf(__uint_as_float(r[2 * j + 1]), c2, -off));
+                    sum[0] += a;
+                    sum[1] += b;
+                    hi[j] = pack2_bf16(a, b);
+                    const float2 h = bf16x2_to_float2(hi[j]);
+                    lo[j] = pack2_bf16(a - h.x, b - h.y);
+                }
+                tmem_st16(s_col + 16 * c, hi);
+                tmem_st16(s_col + 64 + 16 * c, lo);
+            };
+            weights(r0, 0);
+            weights(r1, 1);
+            weights(r2, 2);
+            weights(r3, 3);
+            l += sum[0] + sum[1];
+            tmem_wait_st();
+            tcgen05_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&sm->p_ready[s]));
+        }
+        // ----------------------------------------------------- the partial
+        for (int x = 0; x < 2 && go; ++x)   // both streams' products are done with the ring
+            if (steps(x) > 0)
+                go = __all_sync(0xffffffffu, wait_phase(&sm->o_done[x], 0, p, sm));
+        tcgen05_fence_after();
+        float *stage = reinterpret_cast<float *>(smem);          // [q_tiles * 128][kOutStride]
+        float *stage_ml = stage + 2 * kSharedQRows * kOutStride;   // stream 1's m, l (one row tile)
+        const bool two = q_tiles == 2;
+        float *mine = stage + ((two ? s * kSharedQRows : 0) + trow) * kOutStride;
+        if (go && !two && s == 1) {
+            // one row tile: stream 1 hands its state to stream 0
+            stage_ml[trow] = m_ref;
+            stage_ml[kSharedQRows + trow] = l;
+            if (steps(1) > 0) {
+#pragma unroll 1
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t o[32];
+                    tmem_ld32(o_col + 32 * c, o);
+                    tmem_wait_ld();
+                    settle(o);
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4)
+                        *reinterpret_cast<uint4 *>(mine + 32 * c + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                }
+            }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        float lse = 0.f;
+        if (go && (two || s == 0)) {
+            float f0 = 1.f, f1 = 0.f, m = m_ref, den = l;
+            if (!two && steps(1) > 0) {
+                const float m1 = stage_ml[trow], l1 = stage_ml[kSharedQRows + trow];
+                m = fmaxf(m_ref, m1);
+                f0 = m_ref == -INFINITY ? 0.f : ex2((m_ref - m) * c2);
+                f1 = m1 == -INFINITY ? 0.f : ex2((m1 - m) * c2);
+                den = l * f0 + l1 * f1;
+            }
+            lse = den == 0.f ? -INFINITY : (m * c2 + log2f(den)) * kLn2;
+            const float inv = 1.f / den;
+            f0 *= inv;
+            f1 *= inv;
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+                uint32_t o[32];
+                tmem_ld32(o_col + 32 * c, o);
+                tmem_wait_ld();
+                settle(o);
+#pragma unroll
+                for (int j = 0; j < 32; j += 4) {
+                    float4 v = make_float4(__uint_as_float(o[j]) * f0, __uint_as_float(o[j + 1]) * f0,
+                                           __uint_as_float(o[j + 2]) * f0, __uint_as_float(o[j + 3]) * f0);
+                    float4 *d = reinterpret_cast<float4 *>(mine + 32 * c + j);
+                    if (!two && steps(1) > 0) {
+                        const float4 w = *d;
+                        v.x = fmaf(w.x, f1, v.x);
+                        v.y = fmaf(w.y, f1, v.y);
+                        v.z = fmaf(w.z, f1, v.z);
+                        v.w = fmaf(w.w, f1, v.w);
+                    }
+                    *d = v;
+                }
+            }
+            const int r = (two ? s * kSharedQRows : 0) + trow;
+            if (r < sm->rows) {
+                const int gr = sm->row0 + r;
+                const int64_t out = (int64_t)(gr / p.group) * p.num_qo_heads + sm->kvh * p.group + gr % p.group;
+                p.partial_lse[sm->part_row + out * sm->part_stride] = lse;
+            }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        if (go) {   // whole rows, a warp at a time
+            for (int r = warp; r < sm->rows; r += kSoftmaxThreads / 32) {
+                const int gr = sm->row0 + r;
+                const int64_t out = (int64_t)(gr / p.group) * p.num_qo_heads + sm->kvh * p.group + gr % p.group;
+                const float4 v = *reinterpret_cast<const float4 *>(stage + r * kOutStride + 4 * lane);
+                reinterpret_cast<float4 *>(p.partial_o + (sm->part_row + out * sm->part_stride) * kHeadDim)[lane] = v;
+            }
+        }
+    }
+    tcgen05_fence_before();
+    __syncthreads();
+    griddep_launch_dependents();
+    if (warp == kMmaWarp) {
+        tcgen05_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+    // After an error nobody waited for the copies in flight: do so before the
+    // CTA ends and its shared memory may be handed on.
+    if (warp == kProducerWarp && lane == 0 && ok && sm->abort) {
+        for (int i = 0; i < nb; ++i) {
+            const int last = sm->issued - 1 - i;   // the newest fill of each buffer
+            if (last >= 0 && !(sm->tail_issued && last == 2 * n - 1))
+                mbar_wait(smem_addr(&sm->full[last % nb]), (last / nb) & 1, kDrainTimeoutNs);
+        }
+        if (sm->tail_issued)
+            mbar_wait(smem_addr(&sm->tail), 0, kDrainTimeoutNs);
+    }
+}
+
+// Stage 2: for each (request, query head) the merge of its prefix's partials
+// and, where there is one, the state of its own keys (in o, lse).  One warp per
+// row, lane = 4 output columns, kBatch rows of loads in flight.
+constexpr int kMergeWarps = 4;
+constexpr int kMergeBatch = 8;
+
+__global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __grid_constant__ SharedParams p)
+{
+    const int lane = threadIdx.x & 31;
+    const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    griddep_wait();
+    griddep_launch_dependents();
+    if (row >= p.batch * p.num_qo_heads)
+        return;
+    if (row == 0 && p.has_suffix) {   // more own keys than the plan has room for: some were not attended
+        int64_t keys = 0;
+        for (int i = lane; i < p.batch; i += 32) {
+            const int32_t d = __ldg(p.suffix_indptr + i + 1) - __ldg(p.suffix_indptr + i);
+            keys += !p.page_size ? d : d > 0 ? (int64_t)(d - 1) * p.page_size + __ldg(p.suffix_last_len + i) : 0;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1)
+            keys += __shfl_xor_sync(0xffffffffu, keys, o);
+        if (lane == 0 && keys > p.max_suffix_tokens)
+            report(p.status, FD_ERR_DEVICE_BOUNDS);
+    }
+    const int b = row / p.num_qo_heads;
+    PrefixCoord c;
+    int n = 0;
+    int64_t first = 0;
+    if (locate_prefix(p, b, true, c)) {
+        n = c.splits;
+        first = c.row0 + (int64_t)(row - c.req0 * p.num_qo_heads) * n;
+    } else if (lane == 0) {
+        report(p.status, FD_ERR_DEVICE_BOUNDS);
+    }
+    float4 *o_row = reinterpret_cast<float4 *>(p.o + (int64_t)row * kHeadDim) + lane;
+    float m = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (p.has_suffix) {
+        m = p.lse[row];
+        if (m != -INFINITY) {
+            den = 1.f;
+            acc = *o_row;
+        }
+    }
+    const float *lse_in = p.partial_lse + first;
+    const float4 *o_in = reinterpret_cast<const float4 *>(p.partial_o + first * kHeadDim) + lane;
+    for (int i0 = 0; i0 < n; i0 += kMergeBatch) {
+        float l[kMergeBatch];
+        float4 v[kMergeBatch];
+#pragma unroll
+        for (int u = 0; u < kMergeBatch; ++u) {
+            l[u] = -INFINITY;
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + u < n) {
+                l[u] = __ldcg(lse_in + i0 + u);
+                v[u] = __ldcg(o_in + (int64_t)(i0 + u) * (kHeadDim / 4));
+            }
+        }
+        float m_new = m;
+        bool nan = false;
+#pragma unroll
+        for (int u = 0; u < kMergeBatch; ++u) {
+            m_new = fmaxf(m_new, l[u]);
+            nan |= l[u] != l[u];
+        }
+        if (m_new == -INFINITY && !nan)
+            continue;
+        const float f = expf(m - m_new);
+        den *= f;
+        acc.x *= f;
+        acc.y *= f;
+        acc.z *= f;
+        acc.w *= f;
+#pragma unroll
+        for (int u = 0; u < kMergeBatch; ++u) {
+            const float w = expf(l[u] - m_new);
+            if (w == 0.f)   // no keys, or none that counts: its O may be anything
+                continue;
+            den += w;
+            acc.x = fmaf(w, v[u].x, acc.x);
+            acc.y = fmaf(w, v[u].y, acc.y);
+            acc.z = fmaf(w, v[u].z, acc.z);
+            acc.w = fmaf(w, v[u].w, acc.w);
+        }
+        m = m_new;
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;   // no keys at all: O = 0, LSE = -inf
+    *o_row = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    __syncwarp();
+    if (lane == 0)
+        p.lse[row] = den == 0.f ? -INFINITY : m + logf(den);
+}
+
+}  // namespace
+}  // namespace fd

@@ -1,0 +1,63 @@
+// shared_kernels.h -- parameters and launchers of shared-prefix decode
+// attention (internal).
+#pragma once
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fd.h"
+#include "plan_rule.h"
+
+namespace fd {
+
+constexpr int kSharedTile = 128;       // keys of a tile: rows of a K or V buffer
+constexpr int kSharedQRows = 128;      // query rows of one tensor-core tile
+constexpr int kSharedBlockRows = 256;  // query rows of one CTA: two such tiles
+
+// Splits of a prefix of `len` keys for chunk length `chunk` (a multiple of
+// kSharedTile), and their length: equal within the prefix, whole tiles.
+FD_HD int32_t shared_splits(int32_t len, int32_t chunk)
+{
+    return len > 0 ? (len - 1) / chunk + 1 : 0;
+}
+
+FD_HD int32_t shared_split_len(int32_t len, int32_t splits)
+{
+    const int32_t even = (len - 1) / splits + 1;
+    return (even + kSharedTile - 1) / kSharedTile * kSharedTile;
+}
+
+struct SharedParams {
+    const uint16_t *q;               // bf16 [B, Hq, D]
+    const int32_t *req_indptr;       // [P+1] requests of each prefix
+    const int32_t *prefix_indptr;    // [P+1] key rows (ragged) or page-list entries (paged)
+    const int32_t *prefix_last_len;  // paged: keys of each prefix's last page
+    const int32_t *prefix_indices;   // paged: page of each entry
+    const float *k_scale, *v_scale;  // FP8: [Hkv]
+    float *partial_o;                // [rows, D]
+    float *partial_lse;              // [rows]
+    float *o, *lse;                  // [B, Hq, D], [B, Hq]; hold the suffix states when has_suffix
+    int *status;
+    int32_t batch, num_qo_heads, num_kv_heads, group;
+    int32_t num_prefixes, chunk, num_items, num_partial_rows;
+    int32_t prefix_rows;             // ragged: rows of K/V; paged: entries of prefix_indices
+    int32_t page_size, num_pages;    // page_size 0: ragged
+    int32_t box_rows;                // paged: rows of a page box
+    int32_t has_suffix;
+    // the requests' own keys, to check them against the plan's capacity
+    const int32_t *suffix_indptr, *suffix_last_len;
+    int32_t max_suffix_tokens;
+    float scale;                     // softmax scale
+    int64_t timeout_ns;
+};
+
+struct SharedMaps {
+    CUtensorMap k, v;
+};
+
+// Stage 1 over the prefixes (p.num_items CTAs) and the merge with the suffix
+// states.
+cudaError_t launch_shared(const SharedMaps &maps, const SharedParams &p, int kv_type, cudaStream_t stream);
+
+}  // namespace fd
