@@ -490,6 +490,28 @@ int fd_decode_shared_paged(const fd_shared_plan *plan, int num_pages,
                            float *lse, void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
+ * fd_decode_shared_fp8, fd_decode_shared_paged_fp8 -- the same over E4M3 K/V
+ * (prefixes and suffixes), with the scales of fd_decode_fp8.  The bytes widen to
+ * f16 exactly; byte 0x7F / 0xFF (NaN) propagates as NaN.
+ */
+int fd_decode_shared_fp8(const fd_shared_plan *plan, const int32_t *prefix_req_indptr_dev,
+                     const int32_t *prefix_indptr_dev, const int32_t *kv_indptr_dev, const void *q,
+                     const void *k_prefix_fp8, const void *v_prefix_fp8, const void *k, const void *v,
+                     const float *k_scale, const float *v_scale, float scale, float *o, float *lse, void *workspace, int64_t workspace_bytes,
+                     void *stream);
+
+int fd_decode_shared_paged_fp8(const fd_shared_plan *plan, int num_pages,
+                           const int32_t *prefix_req_indptr_dev,
+                           const int32_t *prefix_page_indptr_dev,
+                           const int32_t *prefix_last_page_len_dev,
+                           const int32_t *prefix_page_indices_dev,
+                           const int32_t *kv_page_indptr_dev, const int32_t *kv_last_page_len_dev,
+                           const int32_t *kv_page_indices_dev, int num_page_entries, const void *q,
+                           const void *k_pages_fp8, const void *v_pages_fp8, const float *k_scale,
+                           const float *v_scale, float scale, float *o,
+                           float *lse, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
  * ---- Writing and rearranging a paged cache ----
  *
  * What a serving step does to the cache around fd_decode_paged: it writes the

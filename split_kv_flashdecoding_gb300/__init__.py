@@ -18,7 +18,8 @@ Entry points (same names as the C ABI, minus the ``fd_`` prefix):
   plan_graph(...), decode_graph(...)    graph-capturable decode (device-side plan)
   merge_states(...)                     merge attention states (sequence shards)
   plan_shared(...), decode_shared(...)  decode over prefixes that requests share
-  plan_shared_paged(), decode_shared_paged()  (each prefix attended once), ragged and paged
+  plan_shared_paged(), decode_shared_paged()  (each prefix attended once), ragged and paged;
+  decode_shared_fp8(), decode_shared_paged_fp8()  FP8 (E4M3) K/V
   plan_rope(...), append_paged(...)     rotary positions and the write of new keys and
   append_paged_fp8(), append_paged_int4()  values into a paged cache
   fork_pages(...), compact_pages(...)   next page tables on the device, and the page
@@ -163,6 +164,9 @@ SIGNATURES = {
     "fd_decode_shared": ([_PS, _P, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _I64, _P], _I),
     "fd_decode_shared_paged": ([_PS, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _F, _P, _P, _P,
                                 _I64, _P], _I),
+    "fd_decode_shared_fp8": ([_PS, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _I64, _P], _I),
+    "fd_decode_shared_paged_fp8": ([_PS, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _F, _P,
+                                    _P, _P, _I64, _P], _I),
     "fd_plan_rope": ([_I, _I, ctypes.POINTER(RopeConfig), ctypes.POINTER(RopeInfo)], _I),
     "fd_append_paged": (_APPEND + [_P, _I64, _P], _I),
     "fd_append_paged_fp8": (_APPEND + [_P, _P, _P, _I64, _P], _I),
@@ -861,6 +865,23 @@ def decode_shared(plan, q, k_prefix, v_prefix, k, v, prefix_req_indptr, prefix_i
                           prefix_req_indptr, prefix_indptr, kv_indptr, scale, o, lse, workspace, stream)
 
 
+def _head_scales(k_scale, v_scale, plan_, q):
+    Hkv = plan_.suffix.num_kv_heads
+    if k_scale.numel() != Hkv or v_scale.numel() != Hkv:
+        raise FdError(-1, "k_scale and v_scale must have one entry per KV head")
+    return _need("k_scale", k_scale, torch.float32, q), _need("v_scale", v_scale, torch.float32, q)
+
+
+def decode_shared_fp8(plan, q, k_prefix_fp8, v_prefix_fp8, k_fp8, v_fp8, k_scale, v_scale,
+                      prefix_req_indptr, prefix_indptr, kv_indptr, scale: float, *, o=None, lse=None,
+                      workspace=None, stream=None):
+    """fd_decode_shared_fp8: decode_shared over E4M3 K/V (uint8 or float8_e4m3fn)
+    with per-KV-head scales fp32 [Hkv]."""
+    return _decode_shared("fd_decode_shared_fp8", (torch.uint8, torch.float8_e4m3fn), plan, q, k_prefix_fp8,
+                          v_prefix_fp8, k_fp8, v_fp8, _head_scales(k_scale, v_scale, plan, q),
+                          prefix_req_indptr, prefix_indptr, kv_indptr, scale, o, lse, workspace, stream)
+
+
 def _decode_shared_paged(name, kv_dtypes, plan_, q, k_pages, v_pages, scales, prefix_req_indptr,
                          prefix_page_indptr, prefix_last_page_len, prefix_page_indices, kv_page_indptr,
                          kv_last_page_len, kv_page_indices, scale, o, lse, workspace, stream):
@@ -901,6 +922,19 @@ def decode_shared_paged(plan, q, k_pages, v_pages, prefix_req_indptr, prefix_pag
                                 scale, o, lse, workspace, stream)
 
 
+def decode_shared_paged_fp8(plan, q, k_pages_fp8, v_pages_fp8, k_scale, v_scale, prefix_req_indptr,
+                            prefix_page_indptr, prefix_last_page_len, prefix_page_indices,
+                            kv_page_indptr, kv_last_page_len, kv_page_indices, scale: float, *, o=None,
+                            lse=None, workspace=None, stream=None):
+    """fd_decode_shared_paged_fp8: decode_shared_paged over E4M3 page pools with
+    per-KV-head scales fp32 [Hkv]."""
+    return _decode_shared_paged("fd_decode_shared_paged_fp8", (torch.uint8, torch.float8_e4m3fn), plan, q,
+                                k_pages_fp8, v_pages_fp8, _head_scales(k_scale, v_scale, plan, q),
+                                prefix_req_indptr, prefix_page_indptr, prefix_last_page_len,
+                                prefix_page_indices, kv_page_indptr, kv_last_page_len, kv_page_indices,
+                                scale, o, lse, workspace, stream)
+
+
 def get_device_status(workspace, stream=None) -> int:
     """fd_get_device_status: synchronise, read and clear the kernels' status word."""
     return lib().fd_get_device_status(_ptr(workspace), _stream(stream))
@@ -911,6 +945,7 @@ __all__ = [
     "decode", "decode_static_workspace", "plan_paged", "decode_paged", "decode_fp8",
     "decode_paged_fp8", "decode_int4", "decode_paged_int4", "plan_graph", "decode_graph", "merge_states", "get_device_status",
     "SharedPlan", "plan_shared", "plan_shared_paged", "decode_shared", "decode_shared_paged",
+    "decode_shared_fp8", "decode_shared_paged_fp8",
     "RopeInfo", "plan_rope", "append_paged", "append_paged_fp8", "append_paged_int4",
     "pages_workspace_bytes", "fork_pages", "compact_pages", "copy_pages", "workspace_bytes", "num_sms",
     "status_string",

@@ -71,12 +71,10 @@ int fd::make_kv_map(CUtensorMap *map, const void *base, int64_t rows, int num_kv
     return r == CUDA_SUCCESS ? FD_OK : FD_ERR_INVALID_ARG;
 }
 
-namespace {
-
 // FP8 K or V [rows, Hkv, 128] (one byte per value) as a 2-D tensor of rows x
 // Hkv*128 bytes; one box = box_rows rows x the head's 128 bytes, 128-byte
 // swizzle, zero fill past the last row.
-int make_kv_map_fp8(CUtensorMap *map, const void *base, int64_t rows, int num_kv_heads, int box_rows)
+int fd::make_kv_map_fp8(CUtensorMap *map, const void *base, int64_t rows, int num_kv_heads, int box_rows)
 {
     auto encode = fd::tensor_map_encoder();
     if (!encode)
@@ -91,8 +89,6 @@ int make_kv_map_fp8(CUtensorMap *map, const void *base, int64_t rows, int num_kv
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? FD_OK : FD_ERR_INVALID_ARG;
 }
-
-}  // namespace
 
 int fd::check_info(const fd_plan_info *info)
 {

@@ -293,8 +293,9 @@ int decode_shared(const fd_shared_plan *plan, const SharedTables &t, const void 
         const void *base[2] = {k_prefix, v_prefix};
         CUtensorMap *map[2] = {&maps.k, &maps.v};
         for (int i = 0; i < 2; ++i) {
-            rc = paged ? make_page_map(map[i], base[i], rows, s.num_kv_heads, box_rows)
-                       : fd::make_kv_map(map[i], base[i], rows, s.num_kv_heads, box_rows);
+            rc = quant ? fd::make_kv_map_fp8(map[i], base[i], rows, s.num_kv_heads, box_rows)
+                 : paged ? make_page_map(map[i], base[i], rows, s.num_kv_heads, box_rows)
+                         : fd::make_kv_map(map[i], base[i], rows, s.num_kv_heads, box_rows);
             if (rc != FD_OK)
                 return rc;
         }
@@ -380,4 +381,37 @@ extern "C" int fd_decode_shared_paged(const fd_shared_plan *plan, int num_pages,
                          num_pages, num_page_entries};
     return decode_shared(plan, t, q, k_pages, v_pages, k_pages, v_pages, scale, o, lse, workspace, workspace_bytes,
                          stream, nullptr);
+}
+
+extern "C" int fd_decode_shared_fp8(const fd_shared_plan *plan, const int32_t *prefix_req_indptr_dev,
+                                const int32_t *prefix_indptr_dev, const int32_t *kv_indptr_dev, const void *q,
+                                const void *k_prefix_fp8, const void *v_prefix_fp8, const void *k, const void *v,
+                                const float *k_scale, const float *v_scale, float scale, float *o, float *lse, void *workspace, int64_t workspace_bytes,
+                                void *stream)
+{
+    if (plan && plan->page_size != 0)
+        return FD_ERR_INVALID_ARG;
+    const SharedTables t{prefix_req_indptr_dev, prefix_indptr_dev, nullptr, nullptr, kv_indptr_dev, nullptr, nullptr, 0, 0};
+    const fd::QuantKV f{fd::kKvTypeFp8, k_scale, v_scale};
+    return decode_shared(plan, t, q, k_prefix_fp8, v_prefix_fp8, k, v, scale, o, lse, workspace, workspace_bytes, stream,
+                         &f);
+}
+
+extern "C" int fd_decode_shared_paged_fp8(const fd_shared_plan *plan, int num_pages,
+                                      const int32_t *prefix_req_indptr_dev, const int32_t *prefix_page_indptr_dev,
+                                      const int32_t *prefix_last_page_len_dev,
+                                      const int32_t *prefix_page_indices_dev, const int32_t *kv_page_indptr_dev,
+                                      const int32_t *kv_last_page_len_dev, const int32_t *kv_page_indices_dev,
+                                      int num_page_entries, const void *q, const void *k_pages_fp8,
+                                      const void *v_pages_fp8, const float *k_scale, const float *v_scale, float scale, float *o, float *lse, void *workspace,
+                                      int64_t workspace_bytes, void *stream)
+{
+    if (plan && plan->page_size <= 0)
+        return FD_ERR_INVALID_ARG;
+    const SharedTables t{prefix_req_indptr_dev, prefix_page_indptr_dev, prefix_last_page_len_dev,
+                         prefix_page_indices_dev, kv_page_indptr_dev, kv_last_page_len_dev, kv_page_indices_dev,
+                         num_pages, num_page_entries};
+    const fd::QuantKV f{fd::kKvTypeFp8, k_scale, v_scale};
+    return decode_shared(plan, t, q, k_pages_fp8, v_pages_fp8, k_pages_fp8, v_pages_fp8, scale, o, lse, workspace, workspace_bytes,
+                         stream, &f);
 }

@@ -5,33 +5,37 @@
 namespace fd {
 namespace {
 
-template <typename Kernel>
-cudaError_t launch_prefixes(Kernel kern, bool (&configured)[64], const SharedMaps &maps, const SharedParams &p,
-                            cudaStream_t stream)
+template <bool PAGED, int DT>
+cudaError_t launch_prefixes(const SharedMaps &maps, const SharedParams &p, cudaStream_t stream)
 {
+    static bool configured[64] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess)
         return e;
     if (dev >= 64 || !configured[dev]) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedAlloc);
+        e = cudaFuncSetAttribute(shared_kernel<PAGED, DT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSharedAlloc);
         if (e != cudaSuccess)
             return e;
         if (dev < 64)
             configured[dev] = true;
     }
-    return launch_dependent(kern, dim3((unsigned)p.num_items), kThreads, kSharedAlloc, stream, maps.k, maps.v, p);
+    return launch_dependent(shared_kernel<PAGED, DT>, dim3((unsigned)p.num_items), kThreads, kSharedAlloc, stream,
+                            maps.k, maps.v, p);
 }
 
 }  // namespace
 
 cudaError_t launch_shared(const SharedMaps &maps, const SharedParams &p, int kv_type, cudaStream_t stream)
 {
-    (void)kv_type;
     if (p.num_items > 0) {
-        static bool configured[2][64] = {};
-        const cudaError_t e = p.page_size ? launch_prefixes(shared_kernel<true>, configured[1], maps, p, stream)
-                                          : launch_prefixes(shared_kernel<false>, configured[0], maps, p, stream);
+        cudaError_t e;
+        if (kv_type == kKvTypeFp8)
+            e = p.page_size ? launch_prefixes<true, kKvTypeFp8>(maps, p, stream)
+                            : launch_prefixes<false, kKvTypeFp8>(maps, p, stream);
+        else
+            e = p.page_size ? launch_prefixes<true, kKvTypeBf16>(maps, p, stream)
+                            : launch_prefixes<false, kKvTypeBf16>(maps, p, stream);
         if (e != cudaSuccess)
             return e;
     }

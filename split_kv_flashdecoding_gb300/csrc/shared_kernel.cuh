@@ -9,9 +9,9 @@
 // second kernel merges them with the state of the request's own keys by LSE.
 //
 // Bound: up to 128 rows a KV head the bytes of K and V (a 128-key tile of both
-// is 64 KB), above that the tensor cores.  The products run on tcgen05 with
-// their accumulators in tensor memory: S and O of one 128-row tile take 256
-// columns, so a CTA holds two such streams.  With more than 128 rows the
+// is 64 KB in bf16), above that the tensor cores.  The products run on tcgen05
+// with their accumulators in tensor memory: S and O of one 128-row tile take
+// 256 columns, so a CTA holds two such streams.  With more than 128 rows the
 // streams are two row tiles that share each K and V tile; with fewer, both
 // take the same rows and every other key tile, so that one stream's softmax
 // runs under the other's products, and their states are merged at the end.
@@ -21,8 +21,17 @@
 // output by more than its fp32 type says): three products of 128 x 128 x 128 a
 // tile for the two that the definition has.
 //
-// Warps: 0-3 and 4-7 the softmax of stream 0 and 1 (a thread owns a row, and
-// with tcgen05.ld its 128 scores), 8 the producer (TMA), 9 issues the products.
+// FP8 K and V: the products are in f16 (every E4M3 value is an f16 value); two
+// warps widen each raw tile into an operand tile in shared memory, and q
+// rows are scaled into f16 by a power of two.
+//
+// Warps: 0-15 the softmax -- two warpgroups a stream, one a half of the tile's
+// keys; a thread owns a row and 64 of its scores (tcgen05.ld gives it the row's
+// columns), and the two warps that share rows agree on the row's maximum by a
+// barrier with a vote.  With one warpgroup a stream the softmax of a tile took
+// over twice as long as the other stream's products, and the tensor cores
+// waited: they were busy for 41 % of 416 us (256 x 64 heads behind 32768 keys).
+// 16 the producer (TMA), 17 issues the products, 18 and 19 the widening (FP8).
 // The running maximum is only raised, and O rescaled, when a row's maximum
 // grew by more than 2^8: until then the weights are at most 256.
 #pragma once
@@ -42,18 +51,23 @@ namespace {
 
 constexpr int kBufBytes = kSharedTile * kHeadDim * 2;   // a K, V or Q tile of 16-bit values: 32 KB
 constexpr int kHalfBytes = kBufBytes / 2;
-constexpr int kBuffers = 7;                             // Q tiles and ring together
-constexpr int kSoftmaxThreads = 256;
-constexpr int kThreads = 320;
-constexpr int kProducerWarp = 8, kMmaWarp = 9;
+constexpr int kBuffers = 7;                             // Q tiles and rings together
+constexpr int kWideBuffers = 3;                         // FP8: operand tiles; the rest of the ring is raw
+constexpr int kRawBytes = kBufBytes / 2;                // FP8: a raw tile
+constexpr int kMaxRing = 6;
+constexpr int kSoftmaxThreads = 512;
+constexpr int kStreamWarps = 8;
+constexpr int kProducerWarp = 16, kMmaWarp = 17, kWidenWarp = 18, kWidenWarps = 2;
+constexpr int kThreads = 640;
 constexpr int kTmemCols = 512;
 constexpr int kStreamCols = 256;                        // S (and P over it) 128, O 128
 constexpr float kRaise = 8.f;                           // log2 of the growth that raises the maximum
 constexpr int kOutStride = kHeadDim + 4;                // floats between rows of the epilogue's staging
 
 struct SharedSmem {
-    uint64_t full[kBuffers], empty[kBuffers];
-    uint64_t s_full[2], p_ready[2], o_done[2];
+    uint64_t full[kMaxRing], empty[kMaxRing];           // operand tiles
+    uint64_t raw_full[kMaxRing], raw_empty[kMaxRing];   // FP8: raw tiles
+    uint64_t s_full[2], p_ready[2][2], o_done[2];
     uint64_t q_ready, tail, drain;
     uint32_t tmem;
     int abort;
@@ -61,8 +75,20 @@ struct SharedSmem {
     int tail_issued;
     // the CTA's item
     int ok, req0, rows, kvh, row0, key0, keys, base, pages, part_row, part_stride, q_tiles;
+    union {
+        float q_scale[kSharedBlockRows];      // FP8, before the first step: a row's factor of the scores
+        float row_max[2][2][kSharedQRows];    // a stream's row maxima, by half of the keys
+    };
 };
-constexpr int kSharedAlloc = kBuffers * kBufBytes + (int)sizeof(SharedSmem) + 1024;
+// At the end, behind the staged rows: the streams' sums by half, stream 1's maxima.
+struct SharedEnd {
+    float row_sum[2][2][kSharedQRows];
+    float row_ref[kSharedQRows];
+};
+constexpr int kEndOffset = kSharedBlockRows * kOutStride * 4;
+static_assert(kEndOffset + (int)sizeof(SharedEnd) <= kBuffers * kBufBytes, "the epilogue works over the ring");
+constexpr int kSharedAlloc = kBuffers * kBufBytes + (int)((sizeof(SharedSmem) + 15) / 16 * 16);
+// the dynamic shared memory of a CTA starts 1024-byte aligned (the kernel checks)
 static_assert(kSharedAlloc <= 232448, "shared memory of one CTA");
 
 __device__ __forceinline__ float ex2(float x)
@@ -72,10 +98,66 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-__device__ __forceinline__ uint32_t pack2_bf16(float a, float b)
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
 {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-    return *reinterpret_cast<const uint32_t *>(&h);
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+
+// Two floats as a pair of 16-bit values (round to nearest), and back.
+template <int DT>
+__device__ __forceinline__ uint32_t pack2(float2 a)
+{
+    if constexpr (DT == kKvTypeFp8) {
+        const __half2 h = __floats2half2_rn(a.x, a.y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    } else {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(a.x, a.y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+}
+
+template <int DT>
+__device__ __forceinline__ float2 unpack2(uint32_t w)
+{
+    if constexpr (DT == kKvTypeFp8)
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    else
+        return bf16x2_to_float2(w);
+}
+
+// Barrier of `threads` threads with the OR of a predicate over them.
+__device__ __forceinline__ bool barrier_or(int id, int threads, bool x)
+{
+    int r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.s32 p, %3, 0;\n\t"
+                 "barrier.cta.red.or.pred q, %1, %2, p;\n\tselp.s32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r)
+                 : "r"(id), "r"(threads), "r"((int)x)
+                 : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void barrier(int id, int threads)
+{
+    asm volatile("barrier.cta.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 // The registers a tcgen05.ld wrote may be read from here on (an empty barrier
@@ -197,35 +279,37 @@ __device__ __forceinline__ int v_pos(int t, int n)
 
 // ------------------------------------------------------------------- kernel
 
-// Layout of a 16-bit tile of 128 rows x 128 values, 128-byte swizzle.
-//  ragged: [64-value half][128 rows][128 bytes]; paged: [8-row group][half][8
+// Layout of a 16-bit operand tile of 128 rows x 128 values, 128-byte swizzle.
+//  [64-value half][128 rows][128 bytes]; bf16 pages: [8-row group][half][8
 //  rows][128 bytes], which one box of a page's rows lands as.
-template <bool PAGED>
+template <bool GROUPED>
 struct TileLayout {
-    static constexpr uint32_t kHalf = PAGED ? 1024 : kHalfBytes;   // between halves
-    static constexpr uint32_t kGroup = PAGED ? 2048 : 1024;        // between 8-row groups
+    static constexpr uint32_t kHalf = GROUPED ? 1024 : kHalfBytes;   // between halves
+    static constexpr uint32_t kGroup = GROUPED ? 2048 : 1024;        // between 8-row groups
 };
 
-template <bool PAGED>
+template <bool PAGED, int DT>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ SharedParams p)
 {
-    using TL = TileLayout<PAGED>;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                ~static_cast<uintptr_t>(1023));
+    constexpr bool kFp8 = DT == kKvTypeFp8;
+    using TL = TileLayout<PAGED && !kFp8>;
+    extern __shared__ __align__(1024) uint8_t smem[];
     SharedSmem *sm = reinterpret_cast<SharedSmem *>(smem + kBuffers * kBufBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
     if (warp == kProducerWarp && lane == 0) {
-        for (int i = 0; i < kBuffers; ++i) {
-            mbar_init(smem_addr(&sm->full[i]), 1);
+        for (int i = 0; i < kMaxRing; ++i) {
+            mbar_init(smem_addr(&sm->full[i]), kFp8 ? kWidenWarps : 1);
             mbar_init(smem_addr(&sm->empty[i]), 1);
+            mbar_init(smem_addr(&sm->raw_full[i]), 1);
+            mbar_init(smem_addr(&sm->raw_empty[i]), kWidenWarps);
         }
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_addr(&sm->s_full[s]), 1);
-            mbar_init(smem_addr(&sm->p_ready[s]), 4);   // the stream's four warps
+            mbar_init(smem_addr(&sm->p_ready[s][0]), kStreamWarps);
+            mbar_init(smem_addr(&sm->p_ready[s][1]), kStreamWarps);
             mbar_init(smem_addr(&sm->o_done[s]), 1);
         }
         mbar_init(smem_addr(&sm->q_ready), kSoftmaxThreads / 32);
@@ -242,9 +326,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == kProducerWarp) {
         PrefixCoord c;
         const int w = blockIdx.x;
-        const bool found = locate_prefix(p, w, false, c);
+        // operand tiles of a 1024-byte swizzle pattern: the base must be aligned
+        const bool found = locate_prefix(p, w, false, c) && (smem_addr(smem) & 1023) == 0;
         if (lane == 0) {
             sm->ok = found;
+            sm->q_tiles = 1;
             if (found) {
                 const int rest = w - c.item0;
                 const int qb = rest % c.blocks, sk = rest / c.blocks;
@@ -262,7 +348,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 sm->part_stride = c.splits;
                 sm->q_tiles = sm->rows > kSharedQRows ? 2 : 1;
             } else {
-                sm->q_tiles = 1;
                 report(p.status, FD_ERR_DEVICE_BOUNDS);
             }
         }
@@ -272,17 +357,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     tcgen05_fence_after();
     const uint32_t tmem = sm->tmem;
     const bool ok = sm->ok;
-    const int q_tiles = sm->q_tiles, nb = kBuffers - q_tiles;   // ring buffers
+    const int q_tiles = sm->q_tiles;
+    // the ring that TMA fills: operand tiles, or raw ones (FP8)
+    const int nb = kFp8 ? 2 * (kBuffers - q_tiles - kWideBuffers) : kBuffers - q_tiles;
+    const int nw = kFp8 ? kWideBuffers : nb;   // operand tiles
     const int n = ok ? (sm->keys + kSharedTile - 1) / kSharedTile : 0;
     // local steps of stream s: every tile (two row tiles) or every other one
     auto steps = [&](int s) { return q_tiles == 2 ? n : (n + 1 - s) / 2; };
     const uint32_t q_smem = smem_addr(smem), ring = q_smem + q_tiles * kBufBytes;
+    uint8_t *ring_ptr = smem + q_tiles * kBufBytes;
+    // Position pos of the stream holds K of tile t, or V of tile t (see k_pos, v_pos).
+    auto at_pos = [&](int pos, bool &is_k) {
+        is_k = pos == 0 || ((pos & 1) && pos < 2 * n - 1);
+        return is_k ? (pos + 1) / 2 : pos == 2 * n - 1 ? n - 1 : (pos - 2) / 2;
+    };
 
     if (warp == kProducerWarp && ok) {
         // --------------------------------------------------------- producer
         const uint64_t pol = l2_evict_first_policy();
         const int box = PAGED ? p.box_rows : kSharedTile;
         const int boxes = kSharedTile / box;
+        constexpr int kRow = kFp8 ? kHeadDim : 2 * kHeadDim, kTileBytes = kSharedTile * kRow;
+        uint64_t *bar_full = kFp8 ? sm->raw_full : sm->full, *bar_empty = kFp8 ? sm->raw_empty : sm->empty;
+        const uint32_t raw0 = ring + (kFp8 ? kWideBuffers * kBufBytes : 0);
         // page row of this lane's box of tile t (paged), -1: past the prefix
         auto box_row = [&](int t) -> int {
             const int key = t * kSharedTile + lane * box;
@@ -297,57 +394,53 @@ __global__ void __launch_bounds__(kThreads, 1)
             return page * p.page_size + at % p.page_size;
         };
         auto load = [&](const CUtensorMap *map, int pos, int row, uint64_t *bar, uint32_t bytes) {
-            const uint32_t dst = ring + (pos % nb) * kBufBytes, b = smem_addr(bar);
+            const uint32_t dst = raw0 + (pos % nb) * kTileBytes, b = smem_addr(bar);
             if (lane == 0)
                 mbar_arrive_expect_tx(b, bytes);
             __syncwarp();
-            if constexpr (PAGED) {
+            if constexpr (kFp8) {
+                if (PAGED ? row >= 0 : lane == 0)
+                    tma_load_2d(dst + (PAGED ? lane * box * kRow : 0), map, sm->kvh * kHeadDim, row, b, pol);
+            } else if constexpr (PAGED) {
                 if (row >= 0)
                     asm volatile(
                         "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(
-                            dst + lane * box * kHeadDim * 2),
-                        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row & 7), "r"(2 * sm->kvh),
-                        "r"(row >> 3), "r"(b), "l"(pol)
+                        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst + lane * box * kRow),
+                        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(0), "r"(2 * sm->kvh), "r"(row >> 3),
+                        "r"(b), "l"(pol)
                         : "memory");
             } else if (lane == 0) {
                 tma_load_3d(dst, map, 0, row, 2 * sm->kvh, b, pol);
             }
         };
         int row_k = PAGED ? box_row(0) : sm->base + sm->key0, row_v = row_k;
-        bool go = true;
-        for (int pos = 0; pos < 2 * n && go; ++pos) {
-            // position pos holds K of tile t, or V of tile t (see k_pos, v_pos)
-            const bool is_k = pos == 0 || ((pos & 1) && pos < 2 * n - 1);
-            const int t = is_k ? (pos + 1) / 2 : pos == 2 * n - 1 ? n - 1 : (pos - 2) / 2;
+        for (int pos = 0; pos < 2 * n; ++pos) {
+            bool is_k;
+            const int t = at_pos(pos, is_k);
             if (is_k && t > 0)
                 row_k = PAGED ? box_row(t) : row_k + kSharedTile;
-            if (pos >= nb)
-                go = wait_phase(&sm->empty[pos % nb], (pos / nb - 1) & 1, p, sm);
-            go = __all_sync(0xffffffffu, go);
-            if (!go)
+            if (pos >= nb && !__all_sync(0xffffffffu, wait_phase(&bar_empty[pos % nb], (pos / nb - 1) & 1, p, sm)))
                 break;
             if (lane == 0)
                 sm->issued = pos + 1;
             const int valid = min(sm->keys - t * kSharedTile, kSharedTile);
-            uint32_t bytes = kBufBytes;
-            if constexpr (PAGED)
-                bytes = (valid + box - 1) / box * box * kHeadDim * 2;
+            const uint32_t bytes = PAGED ? (valid + box - 1) / box * box * kRow : kTileBytes;
             if (is_k) {
-                load(&tm_k, pos, row_k, &sm->full[pos % nb], bytes);
-            } else if (valid == kSharedTile) {
-                load(&tm_v, pos, row_v, &sm->full[pos % nb], bytes);
+                load(&tm_k, pos, row_k, &bar_full[pos % nb], bytes);
+                continue;
+            }
+            if (kFp8 || valid == kSharedTile) {
+                load(&tm_v, pos, row_v, &bar_full[pos % nb], bytes);
             } else {
                 // The rows past the last key (another prefix's, or nobody's) get
                 // weight 0, but 0 * NaN would still reach O: zero them before the
-                // products see the tile.
+                // products see the tile (FP8: the widening warps do).
                 load(&tm_v, pos, row_v, &sm->tail, bytes);
                 if (lane == 0)
                     sm->tail_issued = 1;
-                go = __all_sync(0xffffffffu, wait_phase(&sm->tail, 0, p, sm));
-                if (!go)
+                if (!__all_sync(0xffffffffu, wait_phase(&sm->tail, 0, p, sm)))
                     break;
-                uint8_t *v = smem + q_tiles * kBufBytes + (pos % nb) * kBufBytes;
+                uint8_t *v = ring_ptr + (pos % nb) * kBufBytes;
                 for (int i = lane; i < (kSharedTile - valid) * 16; i += 32) {
                     const int r = valid + i / 16, c = i % 16;
                     const uint32_t off = (c >> 3) * TL::kHalf + (r >> 3) * TL::kGroup + (r & 7) * 128 + (c & 7) * 16;
@@ -356,22 +449,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(smem_addr(&sm->full[pos % nb]));
+                    mbar_arrive(smem_addr(&bar_full[pos % nb]));
             }
-            if (!is_k)
-                row_v = PAGED ? row_k : row_v + kSharedTile;
+            row_v = PAGED ? row_k : row_v + kSharedTile;
         }
     } else if (warp == kMmaWarp && ok) {
         // ------------------------------------------------------ the products
         if (lane == 0) {
-            constexpr uint32_t id_s = mma_idesc(128, kSharedTile, true, false);
-            constexpr uint32_t id_o = mma_idesc(128, kHeadDim, true, true);
+            constexpr uint32_t id_s = mma_idesc(128, kSharedTile, !kFp8, false);
+            constexpr uint32_t id_o = mma_idesc(128, kHeadDim, !kFp8, true);
             bool go = wait_phase(&sm->q_ready, 0, p, sm);
             // S of stream s's step i: K of its tile; frees the buffer after the
             // last stream that takes it.
             auto scores = [&](int s, int i) {
-                const int t = q_tiles == 2 ? i : 2 * i + s, pos = k_pos(t), b = pos % nb;
-                if (!wait_phase(&sm->full[b], (pos / nb) & 1, p, sm))
+                const int t = q_tiles == 2 ? i : 2 * i + s, pos = k_pos(t), b = pos % nw;
+                if (!wait_phase(&sm->full[b], (pos / nw) & 1, p, sm))
                     return false;
                 tcgen05_fence_after();
                 const uint32_t qa = q_smem + (q_tiles == 2 ? s : 0) * kBufBytes, kb = ring + b * kBufBytes;
@@ -385,18 +477,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     tcgen05_commit(smem_addr(&sm->empty[b]));
                 return true;
             };
-            // O += P V of stream s's step i.
+            // O += P V of stream s's step i, in two parts: each half of the keys
+            // is ready in two parts of 32.
             auto values = [&](int s, int i) {
-                const int t = q_tiles == 2 ? i : 2 * i + s, pos = v_pos(t, n), b = pos % nb;
-                if (!wait_phase(&sm->full[b], (pos / nb) & 1, p, sm) || !wait_phase(&sm->p_ready[s], i & 1, p, sm))
+                const int t = q_tiles == 2 ? i : 2 * i + s, pos = v_pos(t, n), b = pos % nw;
+                if (!wait_phase(&sm->full[b], (pos / nw) & 1, p, sm))
                     return false;
-                tcgen05_fence_after();
                 const uint32_t vb = ring + b * kBufBytes, pa = tmem + s * kStreamCols;
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {   // 16 keys a step, hi then lo
-                    const uint64_t vd = smem_desc(vb + k * 2 * TL::kGroup, TL::kHalf, TL::kGroup);
-                    mma_ts(pa + 128, pa + 8 * k, vd, id_o, i > 0 || k > 0);
-                    mma_ts(pa + 128, pa + 64 + 8 * k, vd, id_o, 1);
+                for (int part = 0; part < 2; ++part) {
+                    if (!wait_phase(&sm->p_ready[s][part], i & 1, p, sm))
+                        return false;
+                    tcgen05_fence_after();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {   // 16 keys a step, hi then lo
+                        const int c = (j >> 1) * 2 + part, k = 2 * c + (j & 1);   // chunk of 32 keys; step
+                        const uint64_t vd = smem_desc(vb + k * 2 * TL::kGroup, TL::kHalf, TL::kGroup);
+                        mma_ts(pa + 128, pa + 32 * c + 8 * (j & 1), vd, id_o, i > 0 || part > 0 || j > 0);
+                        mma_ts(pa + 128, pa + 32 * c + 16 + 8 * (j & 1), vd, id_o, 1);
+                    }
                 }
                 if (q_tiles == 1 || s == 1)
                     tcgen05_commit(smem_addr(&sm->empty[b]));
@@ -420,17 +519,70 @@ __global__ void __launch_bounds__(kThreads, 1)
             mbar_wait(smem_addr(&sm->drain), 0, kDrainTimeoutNs);
         }
         __syncwarp();
+    } else if (kFp8 && warp >= kWidenWarp && ok) {
+        // ------------------------------------- FP8: raw tiles to f16 operands
+        // A warp takes 8 rows at a time, 16 values a lane: a raw row is 8 chunks
+        // of 16 bytes, chunk c at c ^ (row % 8), and becomes two chunks of the
+        // operand's half c / 4.  The lanes of a quarter warp are two rows r and
+        // r ^ 5 and four chunks of a half, which meet no bank twice on either side.
+        const uint8_t *raw0 = ring_ptr + kWideBuffers * kBufBytes;
+        const int ph = lane >> 3, r8 = ph ^ (((lane >> 2) & 1) * 5), cc = lane & 3;
+        for (int pos = 0; pos < 2 * n; ++pos) {
+            bool is_k;
+            const int t = at_pos(pos, is_k);
+            const int valid = sm->keys - t * kSharedTile;
+            bool go = wait_phase(&sm->raw_full[pos % nb], (pos / nb) & 1, p, sm);
+            if (go && pos >= kWideBuffers)
+                go = wait_phase(&sm->empty[pos % kWideBuffers], (pos / kWideBuffers - 1) & 1, p, sm);
+            if (!__all_sync(0xffffffffu, go))
+                break;
+            const uint8_t *src = raw0 + (pos % nb) * kRawBytes;
+            uint8_t *dst = ring_ptr + (pos % kWideBuffers) * kBufBytes;
+#pragma unroll 4
+            for (int j = 0; j < 32 / kWidenWarps; ++j) {   // group of 8 rows, half
+                const int g = (warp - kWidenWarp) * (16 / kWidenWarps) + (j >> 1), half = j & 1;
+                const int row = 8 * g + r8;
+                const uint4 x = *reinterpret_cast<const uint4 *>(src + row * 128 + (((4 * half + cc) ^ r8) << 4));
+                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                uint32_t f[8];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+                        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+                        : "=r"(f[2 * q]), "=r"(f[2 * q + 1])
+                        : "r"(w[q]));
+                if (!is_k && row >= valid) {   // rows past the last key
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        f[q] = 0u;
+                }
+                uint8_t *d = dst + half * kHalfBytes + row * 128;
+                *reinterpret_cast<uint4 *>(d + (((2 * cc) ^ r8) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
+                *reinterpret_cast<uint4 *>(d + (((2 * cc + 1) ^ r8) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
+            }
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(smem_addr(&sm->raw_empty[pos % nb]));
+                mbar_arrive(smem_addr(&sm->full[pos % kWideBuffers]));
+            }
+        }
     } else if (warp < kProducerWarp) {
         // -------------------------------------------------------- the softmax
-        const int s = warp >> 2;
-        const int trow = (warp & 3) * 32 + lane;   // row of the stream's tile: lane of tensor memory
-        const uint32_t quad = (uint32_t)(warp & 3) << 21;
-        const uint32_t s_col = tmem + quad + s * kStreamCols, o_col = s_col + 128;
-        // log2 e times the scale; never 0, so that a masked score (-inf) stays -inf
-        const float c2 = fmaxf(fabsf(p.scale) * kLog2e, 1.17549435e-38f);
-        const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;   // a negative scale turns q around
+        const int s = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
+        const int trow = quad * 32 + lane;   // row of the stream's tile: lane of tensor memory
+        const uint32_t s_col = tmem + ((uint32_t)quad << 21) + s * kStreamCols + half * 64, o_col = s_col + 128;
+        const int pair_bar = 2 + s * 4 + quad;   // barrier of the two warps that share rows
+        const bool two = q_tiles == 2;
+        float factor = p.scale, v_scale = 1.f;
+        if constexpr (kFp8) {
+            factor *= ok ? __ldg(p.k_scale + sm->kvh) : 1.f;
+            v_scale = ok ? __ldg(p.v_scale + sm->kvh) : 1.f;
+        }
         if (ok) {
-            // Q rows into shared memory, [half][128 rows][128 bytes] a tile
+            // Q rows into shared memory, [half][128 rows][128 bytes] a tile; a
+            // negative factor of the scores turns q around.
+            const uint32_t flip = factor < 0.f ? 0x80008000u : 0u;
             for (int i = tid; i < q_tiles * kSharedQRows * 16; i += kSoftmaxThreads) {
                 const int r = i >> 4, ch = i & 15;
                 uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -439,10 +591,39 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const int64_t row = (int64_t)(sm->req0 + gr / p.group) * p.num_qo_heads + sm->kvh * p.group +
                                         gr % p.group;
                     v = __ldg(reinterpret_cast<const uint4 *>(p.q + row * kHeadDim) + ch);
-                    v.x ^= flip;
-                    v.y ^= flip;
-                    v.z ^= flip;
-                    v.w ^= flip;
+                }
+                v.x ^= flip;
+                v.y ^= flip;
+                v.z ^= flip;
+                v.w ^= flip;
+                if constexpr (kFp8) {
+                    // to f16, times the power of two that puts the row's largest
+                    // magnitude in [2^8, 2^9): exact down to 2^-22 of it
+                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    float amax = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 a = bf16x2_to_float2(w[j]);
+                        amax = fmaxf(amax, fmaxf(fabsf(a.x), fabsf(a.y)));
+                    }
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1)
+                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    int sh = 0;
+                    if (amax > 0.f) {
+                        int e;
+                        frexpf(amax, &e);
+                        sh = min(max(9 - e, -100), 100);
+                    }
+                    const float up = __int_as_float((127 + sh) << 23);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 a = bf16x2_to_float2(w[j]);
+                        w[j] = pack2<DT>(make_float2(a.x * up, a.y * up));
+                    }
+                    v = make_uint4(w[0], w[1], w[2], w[3]);
+                    if (ch == 0)
+                        sm->q_scale[r] = __int_as_float((127 - sh) << 23);
                 }
                 const int rr = r & 127;
                 *reinterpret_cast<uint4 *>(smem + (r >> 7) * kBufBytes + (ch >> 3) * kHalfBytes + rr * 128 +
@@ -453,146 +634,168 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0)
                 mbar_arrive(smem_addr(&sm->q_ready));
         }
+        barrier(1, kSoftmaxThreads);   // q_scale is written
+        // log2 e times the factor of the scores; never 0, so that a masked score
+        // (-inf) stays -inf
+        float c2 = fabsf(factor) * kLog2e;
+        if constexpr (kFp8) {
+            c2 *= sm->q_scale[(two ? s * kSharedQRows : 0) + trow];
+            barrier(1, kSoftmaxThreads);   // row_max takes its place
+        }
+        c2 = c2 == 0.f ? 1.17549435e-38f : c2;
+        // FP8: weights are 2^7 times larger, which keeps seven more bits of the
+        // small ones in f16; it cancels in O
+        constexpr float kBias = kFp8 ? 7.f : 0.f;
         float m_ref = -INFINITY, l = 0.f;   // maximum of the raw scores that the weights refer to
         bool go = ok;
-        for (int i = 0; i < steps(s) && go; ++i) {
-            const int t = q_tiles == 2 ? i : 2 * i + s;
-            const int valid = sm->keys - t * kSharedTile;
-            go = __all_sync(0xffffffffu, wait_phase(&sm->s_full[s], i & 1, p, sm));
-            if (!go)
-                break;
-            tcgen05_fence_after();
-            uint32_t r0[32], r1[32], r2[32], r3[32];
-            tmem_ld32(s_col, r0);
-            tmem_ld32(s_col + 32, r1);
-            tmem_ld32(s_col + 64, r2);
-            tmem_ld32(s_col + 96, r3);
-            tmem_wait_ld();
-            settle(r0);
-            settle(r1);
-            settle(r2);
-            settle(r3);
-            if (valid < kSharedTile) {
+        for (int i = 0; i < steps(s); ++i) {
+            // After an error the steps go on without work, so that the barrier
+            // of the two warps always meets.
+            if (go)
+                go = __all_sync(0xffffffffu, wait_phase(&sm->s_full[s], i & 1, p, sm));
+            const int valid = sm->keys - (two ? i : 2 * i + s) * kSharedTile - half * 64;
+            uint32_t r0[32], r1[32];
+            float mt = -INFINITY;
+            bool raise = false;
+            if (go) {
+                tcgen05_fence_after();
+                tmem_ld32(s_col, r0);
+                tmem_ld32(s_col + 32, r1);
+                tmem_wait_ld();
+                settle(r0);
+                settle(r1);
+                if (valid < 64) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) {
+                        if (j >= valid)
+                            r0[j] = 0xff800000u;
+                        if (32 + j >= valid)
+                            r1[j] = 0xff800000u;
+                    }
+                }
+                float mx[2] = {-INFINITY, -INFINITY};
 #pragma unroll
                 for (int j = 0; j < 32; ++j) {
-                    if (j >= valid) r0[j] = 0xff800000u;
-                    if (32 + j >= valid) r1[j] = 0xff800000u;
-                    if (64 + j >= valid) r2[j] = 0xff800000u;
-                    if (96 + j >= valid) r3[j] = 0xff800000u;
+                    mx[0] = fmaxf(mx[0], __uint_as_float(r0[j]));
+                    mx[1] = fmaxf(mx[1], __uint_as_float(r1[j]));
                 }
+                mt = fmaxf(mx[0], mx[1]);
+                raise = mt > m_ref && (m_ref == -INFINITY || (mt - m_ref) * c2 > kRaise);
             }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                mx[0] = fmaxf(mx[0], __uint_as_float(r0[j]));
-                mx[1] = fmaxf(mx[1], __uint_as_float(r1[j]));
-                mx[2] = fmaxf(mx[2], __uint_as_float(r2[j]));
-                mx[3] = fmaxf(mx[3], __uint_as_float(r3[j]));
-            }
-            const float mt = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const bool raise = mt > m_ref && (m_ref == -INFINITY || (mt - m_ref) * c2 > kRaise);
-            if (__any_sync(0xffffffffu, raise)) {
-                // the products up to the last step are done: s_full followed them
-                const float m_new = raise ? mt : m_ref;
+            if (barrier_or(pair_bar, 64, raise)) {
+                // a row's maximum is that of both halves of its keys
+                sm->row_max[s][half][trow] = mt;
+                barrier(pair_bar, 64);
+                const float both = fmaxf(mt, sm->row_max[s][half ^ 1][trow]);
+                const bool up = both > m_ref && (m_ref == -INFINITY || (both - m_ref) * c2 > kRaise);
+                const float m_new = up ? both : m_ref;
                 const float f = m_ref == -INFINITY ? 0.f : ex2((m_ref - m_new) * c2);
                 l *= f;
                 m_ref = m_new;
-                if (i > 0) {
+                if (i > 0 && go) {   // the products up to the last step are done: s_full followed them
 #pragma unroll 1
                     for (int c = 0; c < 4; ++c) {
-                        uint32_t o[32];
-                        tmem_ld32(o_col + 32 * c, o);
+                        uint32_t o[16];
+                        tmem_ld16(o_col + 16 * c, o);
                         tmem_wait_ld();
                         settle(o);
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
+                        for (int j = 0; j < 16; ++j)
                             o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_st32(o_col + 32 * c, o);
+                        tmem_st16(o_col + 16 * c, o);
                     }
                 }
+                barrier(pair_bar, 64);   // row_max is read before the next step writes it
             }
+            if (!go)
+                continue;
             // a row whose scores are all -inf so far keeps weights of 0
-            const float off = m_ref == -INFINITY ? 0.f : m_ref * c2;
-            float sum[2] = {0.f, 0.f};
-            auto weights = [&](const uint32_t (&r)[32], int c) {
-                uint32_t hi[16], lo[16];
+            const float off = (m_ref == -INFINITY ? 0.f : -m_ref * c2) + kBias;
+            const float2 c22 = make_float2(c2, c2), off2 = make_float2(off, off);
+            float2 sum = make_float2(0.f, 0.f);
+            // 32 keys: hi in the first 16 of their columns, lo in the others
+            auto weights = [&](const uint32_t (&r)[32], uint32_t col) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float a = ex2(fmaf(__uint_as_float(r[2 * j]), c2, -off));
-                    const float b = ex2(fmaf(__uint_as_float(r[2 * j + 1]), c2, -off));
-                    sum[0] += a;
-                    sum[1] += b;
-                    hi[j] = pack2_bf16(a, b);
-                    const float2 h = bf16x2_to_float2(hi[j]);
-                    lo[j] = pack2_bf16(a - h.x, b - h.y);
+                for (int q = 0; q < 2; ++q) {
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float2 x = fma2(make_float2(__uint_as_float(r[16 * q + 2 * j]),
+                                                          __uint_as_float(r[16 * q + 2 * j + 1])), c22, off2);
+                        const float2 w = make_float2(ex2(x.x), ex2(x.y));
+                        sum = add2(sum, w);
+                        hi[j] = pack2<DT>(w);
+                        const float2 h = unpack2<DT>(hi[j]);
+                        lo[j] = pack2<DT>(fma2(h, make_float2(-1.f, -1.f), w));
+                    }
+                    tmem_st8(col + 8 * q, hi);
+                    tmem_st8(col + 16 + 8 * q, lo);
                 }
-                tmem_st16(s_col + 16 * c, hi);
-                tmem_st16(s_col + 64 + 16 * c, lo);
+                tmem_wait_st();
+                tcgen05_fence_before();
+                __syncwarp();
             };
-            weights(r0, 0);
-            weights(r1, 1);
-            weights(r2, 2);
-            weights(r3, 3);
-            l += sum[0] + sum[1];
-            tmem_wait_st();
-            tcgen05_fence_before();
-            __syncwarp();
+            weights(r0, s_col);
             if (lane == 0)
-                mbar_arrive(smem_addr(&sm->p_ready[s]));
+                mbar_arrive(smem_addr(&sm->p_ready[s][0]));
+            weights(r1, s_col + 32);
+            if (lane == 0)
+                mbar_arrive(smem_addr(&sm->p_ready[s][1]));
+            l += sum.x + sum.y;
         }
         // ----------------------------------------------------- the partial
-        for (int x = 0; x < 2 && go; ++x)   // both streams' products are done with the ring
-            if (steps(x) > 0)
+        for (int x = 0; x < 2; ++x)   // both streams' products are done with the ring
+            if (go && steps(x) > 0)
                 go = __all_sync(0xffffffffu, wait_phase(&sm->o_done[x], 0, p, sm));
         tcgen05_fence_after();
-        float *stage = reinterpret_cast<float *>(smem);          // [q_tiles * 128][kOutStride]
-        float *stage_ml = stage + 2 * kSharedQRows * kOutStride;   // stream 1's m, l (one row tile)
-        const bool two = q_tiles == 2;
-        float *mine = stage + ((two ? s * kSharedQRows : 0) + trow) * kOutStride;
-        if (go && !two && s == 1) {
+        float *stage = reinterpret_cast<float *>(smem);   // [q_tiles * 128][kOutStride]
+        SharedEnd *end = reinterpret_cast<SharedEnd *>(smem + kEndOffset);
+        float *mine = stage + ((two ? s * kSharedQRows : 0) + trow) * kOutStride + half * 64;
+        if (go)
+            end->row_sum[s][half][trow] = l;
+        if (!two && s == 1) {
             // one row tile: stream 1 hands its state to stream 0
-            stage_ml[trow] = m_ref;
-            stage_ml[kSharedQRows + trow] = l;
-            if (steps(1) > 0) {
+            if (go && half == 0)
+                end->row_ref[trow] = m_ref;
+            if (go && steps(1) > 0) {
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
-                    uint32_t o[32];
-                    tmem_ld32(o_col + 32 * c, o);
+                    uint32_t o[16];
+                    tmem_ld16(o_col + 16 * c, o);
                     tmem_wait_ld();
                     settle(o);
 #pragma unroll
-                    for (int j = 0; j < 32; j += 4)
-                        *reinterpret_cast<uint4 *>(mine + 32 * c + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<uint4 *>(mine + 16 * c + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                 }
             }
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
-        float lse = 0.f;
+        barrier(1, kSoftmaxThreads);
         if (go && (two || s == 0)) {
-            float f0 = 1.f, f1 = 0.f, m = m_ref, den = l;
-            if (!two && steps(1) > 0) {
-                const float m1 = stage_ml[trow], l1 = stage_ml[kSharedQRows + trow];
+            float f0 = 1.f, f1 = 0.f, m = m_ref, den = end->row_sum[s][0][trow] + end->row_sum[s][1][trow];
+            const bool join = !two && steps(1) > 0;
+            if (join) {
+                const float m1 = end->row_ref[trow], l1 = end->row_sum[1][0][trow] + end->row_sum[1][1][trow];
                 m = fmaxf(m_ref, m1);
                 f0 = m_ref == -INFINITY ? 0.f : ex2((m_ref - m) * c2);
                 f1 = m1 == -INFINITY ? 0.f : ex2((m1 - m) * c2);
-                den = l * f0 + l1 * f1;
+                den = den * f0 + l1 * f1;
             }
-            lse = den == 0.f ? -INFINITY : (m * c2 + log2f(den)) * kLn2;
-            const float inv = 1.f / den;
+            const float inv = v_scale / den;
             f0 *= inv;
             f1 *= inv;
 #pragma unroll 1
             for (int c = 0; c < 4; ++c) {
-                uint32_t o[32];
-                tmem_ld32(o_col + 32 * c, o);
+                uint32_t o[16];
+                tmem_ld16(o_col + 16 * c, o);
                 tmem_wait_ld();
                 settle(o);
 #pragma unroll
-                for (int j = 0; j < 32; j += 4) {
+                for (int j = 0; j < 16; j += 4) {
                     float4 v = make_float4(__uint_as_float(o[j]) * f0, __uint_as_float(o[j + 1]) * f0,
                                            __uint_as_float(o[j + 2]) * f0, __uint_as_float(o[j + 3]) * f0);
-                    float4 *d = reinterpret_cast<float4 *>(mine + 32 * c + j);
-                    if (!two && steps(1) > 0) {
+                    float4 *d = reinterpret_cast<float4 *>(mine + 16 * c + j);
+                    if (join) {
                         const float4 w = *d;
                         v.x = fmaf(w.x, f1, v.x);
                         v.y = fmaf(w.y, f1, v.y);
@@ -603,13 +806,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             const int r = (two ? s * kSharedQRows : 0) + trow;
-            if (r < sm->rows) {
+            if (half == 0 && r < sm->rows) {
                 const int gr = sm->row0 + r;
                 const int64_t out = (int64_t)(gr / p.group) * p.num_qo_heads + sm->kvh * p.group + gr % p.group;
-                p.partial_lse[sm->part_row + out * sm->part_stride] = lse;
+                p.partial_lse[sm->part_row + out * sm->part_stride] =
+                    den == 0.f ? -INFINITY : (m * c2 + log2f(den) - kBias) * kLn2;
             }
         }
-        asm volatile("bar.sync 1, 256;" ::: "memory");
+        barrier(1, kSoftmaxThreads);
         if (go) {   // whole rows, a warp at a time
             for (int r = warp; r < sm->rows; r += kSoftmaxThreads / 32) {
                 const int gr = sm->row0 + r;
@@ -629,10 +833,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     // After an error nobody waited for the copies in flight: do so before the
     // CTA ends and its shared memory may be handed on.
     if (warp == kProducerWarp && lane == 0 && ok && sm->abort) {
+        uint64_t *bar_full = kFp8 ? sm->raw_full : sm->full;
         for (int i = 0; i < nb; ++i) {
             const int last = sm->issued - 1 - i;   // the newest fill of each buffer
             if (last >= 0 && !(sm->tail_issued && last == 2 * n - 1))
-                mbar_wait(smem_addr(&sm->full[last % nb]), (last / nb) & 1, kDrainTimeoutNs);
+                mbar_wait(smem_addr(&bar_full[last % nb]), (last / nb) & 1, kDrainTimeoutNs);
         }
         if (sm->tail_issued)
             mbar_wait(smem_addr(&sm->tail), 0, kDrainTimeoutNs);

@@ -46,6 +46,9 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // K or V [rows, Hkv, 128] bf16 as a tensor map of one head's box_rows rows.
 int make_kv_map(CUtensorMap *map, const void *base, int64_t rows, int num_kv_heads, int box_rows);
 
+// FP8 K or V [rows, Hkv, 128], one byte a value, likewise.
+int make_kv_map_fp8(CUtensorMap *map, const void *base, int64_t rows, int num_kv_heads, int box_rows);
+
 // Argument checks and the split kernel's launch (see fd_api.cu).
 int check_info(const fd_plan_info *info);
 int launch_stage1(const fd_plan_info *info, const void *q, const void *k, const void *v,

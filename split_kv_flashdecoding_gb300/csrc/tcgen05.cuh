@@ -90,14 +90,20 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r)
         : "r"(addr));
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const uint32_t *r)
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r)
 {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-        "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-        FD_W4(0), FD_W4(4), FD_W4(8), FD_W4(12), FD_W4(16), FD_W4(20), FD_W4(24), FD_W4(28)
-        : "memory");
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : FD_R4(0), FD_R4(4), FD_R4(8), FD_R4(12)
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t *r)
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr),
+                 FD_W4(0), FD_W4(4)
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t *r)

@@ -356,3 +356,107 @@ def test_binding_refusals(cuda_device):
         bad[at] = x
         with pytest.raises(fd.FdError):
             fd.decode_shared(*bad)
+
+
+# ------------------------------------------------------------------------ FP8
+
+def to_fp8(i, seed=0):
+    """Random E4M3 codes for the keys and values (NaN codes only past the last
+    key), with scales per head, one of them negative; and what they stand for."""
+    rng = np.random.RandomState(seed)
+    f = dict(i)
+    sc = {n: (rng.uniform(0.3, 1.0, i["Hkv"]) / 64).astype(np.float32) for n in "kv"}
+    sc["k"][0] *= -1
+    for n in "kv":
+        for part in ("p", ""):
+            x = i[n + part]
+            nan = torch.isnan(x.float()).numpy()
+            codes = rng.randint(0, 256, x.shape).astype(np.uint8)
+            codes[(codes & 0x7F) == 0x7F] = 0x3A
+            codes[(codes & 0x78) == 0x78] &= 0xB7   # magnitudes up to 30: scores of a softmax
+            f[n + part + "8"] = torch.from_numpy(np.where(nan, 0x7F, codes).astype(np.uint8))
+            f[n + part + "d"] = oracle.dequant_fp8(np.where(nan, 0, codes).astype(np.uint8), sc[n])
+    f["sk"], f["sv"] = (torch.from_numpy(sc[n]).cuda() for n in "kv")
+    return f
+
+
+def fp8_reference(f):
+    """fp64 attention over the dequantised values, request by request."""
+    pi, oi, g = indptr(f["lens"]), indptr(f["own"]), f["Hq"] // f["Hkv"]
+    q = f["q"].double().numpy()
+    o, lse, b = np.zeros((f["B"], f["Hq"], D)), np.full((f["B"], f["Hq"]), -np.inf), 0
+    for p, r in enumerate(f["reqs"]):
+        for _ in range(r):
+            K = np.concatenate([f["kpd"][pi[p]: pi[p + 1]], f["kd"][oi[b]: oi[b + 1]]])
+            V = np.concatenate([f["vpd"][pi[p]: pi[p + 1]], f["vd"][oi[b]: oi[b + 1]]])
+            if len(K):
+                s = np.einsum("hd,lhd->hl", q[b], np.repeat(K, g, 1)) * f["scale"]
+                m = s.max(1, keepdims=True)
+                w = np.exp(s - m)
+                lse[b] = m[:, 0] + np.log(w.sum(1))
+                o[b] = np.einsum("hl,lhd->hd", w / w.sum(1, keepdims=True), np.repeat(V, g, 1))
+            b += 1
+    return o, lse
+
+
+def ragged_fp8(f, chunk=0):
+    req, pi = indptr(f["reqs"]), indptr(f["lens"])
+    p = fd.plan_shared(f["B"], f["Hq"], f["Hkv"], D, req, pi, f["room"], chunk=chunk)
+    ws = torch.zeros(p.workspace_bytes, dtype=torch.uint8, device="cuda")
+    d = {n: f[n].cuda() for n in ("q", "kp8", "vp8", "k8", "v8")}
+    o, lse = fd.decode_shared_fp8(p, d["q"], d["kp8"], d["vp8"], d["k8"], d["v8"], f["sk"], f["sv"], i32(req), i32(pi),
+                                  i32(indptr(f["own"])), f["scale"], workspace=ws)
+    return o, lse, fd.get_device_status(ws)
+
+
+def paged_fp8(f, page, seed=0):
+    j = dict(f, **{n + part: f[n + part + "8"] for n in "kv" for part in ("p", "")})
+    pg = to_pages(dict(j, **{n: j[n].float() for n in ("kp", "vp", "k", "v")}), page, seed)
+    pools = {n: torch.where(torch.isnan(x.float()), torch.tensor(127.0), x.float()).to(torch.uint8).cuda()
+             for n, x in pg["pools"].items()}
+    req = indptr(f["reqs"])
+    p = fd.plan_shared_paged(f["B"], f["Hq"], f["Hkv"], D, page, req, indptr(pg["pc"]), pg["pl"], f["room"])
+    ws = torch.zeros(p.workspace_bytes, dtype=torch.uint8, device="cuda")
+    o, lse = fd.decode_shared_paged_fp8(p, f["q"].cuda(), pools["k"], pools["v"], f["sk"], f["sv"], i32(req),
+                                        i32(indptr(pg["pc"])), i32(pg["pl"]), i32(np.append(pg["pids"], 0)),
+                                        i32(indptr(pg["oc"])), i32(pg["ol"]), i32(np.append(pg["oids"], 0)),
+                                        f["scale"], workspace=ws)
+    return o, lse, fd.get_device_status(ws)
+
+
+@pytest.mark.parametrize("name,Hq,Hkv,reqs,lens", SMALL, ids=[c[0] for c in SMALL])
+def test_fp8_matches_64_bits(cuda_device, name, Hq, Hkv, reqs, lens):
+    f = to_fp8(make(Hq, Hkv, reqs, lens, own_lengths(sum(reqs), 40), seed=len(name)), seed=len(name))
+    ref = fp8_reference(f)
+    # scores reach tens: fp32 steps of the LSE grow with it
+    lse_abs = 2e-5 * max(1.0, np.abs(ref[1][np.isfinite(ref[1])]).max(initial=0) / 16)
+    for what, out in (("ragged", ragged_fp8(f)), ("chunks", ragged_fp8(f, 128)), ("paged 16", paged_fp8(f, 16, 1)),
+                      ("paged 48", paged_fp8(f, 48, 2)), ("paged 256", paged_fp8(f, 256, 3))):
+        o, lse, status = out
+        assert status == 0
+        assert_within(errors(o.cpu().numpy(), lse.cpu().numpy(), *ref), max_abs=1e-4, rel_l2=1e-5, lse_abs=lse_abs,
+                      what=f"{name} {what}")
+
+
+def test_fp8_nan_codes_spread(cuda_device):
+    f = to_fp8(make(8, 8, [3, 2], [300, 200], np.full(5, 4), spare=0))
+    f["vp8"][350, 5, 7] = 0xFF
+    o, lse, status = ragged_fp8(f)
+    bad = torch.isnan(o).cpu()
+    want = torch.zeros(5, 8, 128, dtype=torch.bool)
+    want[3:, 5, 7] = True
+    assert status == 0 and torch.equal(bad, want) and torch.isfinite(lse).all()
+
+
+def test_fp8_binding_refusals(cuda_device):
+    f = to_fp8(make(8, 8, [4], [300], [5, 6, 7, 8]))
+    req, pi, oi = i32(indptr(f["reqs"])), i32(indptr(f["lens"])), i32(indptr(f["own"]))
+    p = fd.plan_shared(4, 8, 8, D, indptr(f["reqs"]), indptr(f["lens"]), 26)
+    d = {n: f[n].cuda() for n in ("q", "kp8", "vp8", "k8", "v8", "kp")}
+    good = [p, d["q"], d["kp8"], d["vp8"], d["k8"], d["v8"], f["sk"], f["sv"], req, pi, oi, SCALE]
+    fd.decode_shared_fp8(*good)
+    for at, x in ((2, d["kp"]), (6, f["sk"][:7]), (7, f["sv"].double()), (7, f["sv"].cpu())):
+        bad = list(good)
+        bad[at] = x
+        with pytest.raises(fd.FdError):
+            fd.decode_shared_fp8(*bad)
