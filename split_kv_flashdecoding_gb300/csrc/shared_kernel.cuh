@@ -62,6 +62,7 @@ constexpr int kThreads = 640;
 constexpr int kTmemCols = 512;
 constexpr int kStreamCols = 256;                        // S (and P over it) 128, O 128
 constexpr float kRaise = 8.f;                           // log2 of the growth that raises the maximum
+constexpr uint32_t kSleepNs = 100000;                    // a wait's sleep between looks at the timer
 constexpr int kOutStride = kHeadDim + 4;                // floats between rows of the epilogue's staging
 
 struct SharedSmem {
@@ -177,11 +178,14 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, const
 {
     const uint32_t a = smem_addr(bar);
     if (p.timeout_ns > 0) {
-        if (mbar_try_wait(a, parity))
+        // These waits are the pipeline's hand-overs: a waiting warp sleeps until
+        // the phase completes (polling takes issue slots from the warps at
+        // work), and looks at the timer only when it woke for nothing.
+        if (mbar_try_wait_for(a, parity, kSleepNs))
             return true;
         const uint64_t t0 = global_timer_ns();
         while (!*reinterpret_cast<volatile int *>(&sm->abort)) {
-            if (mbar_try_wait(a, parity))
+            if (mbar_try_wait_for(a, parity, kSleepNs))
                 return true;
             if ((int64_t)(global_timer_ns() - t0) > p.timeout_ns)
                 break;
@@ -265,17 +269,24 @@ __device__ __forceinline__ bool locate_prefix(const SharedParams &p, int32_t j, 
     return false;
 }
 
-// Ring position of tile t's K and V of n tiles: K0, K1, V0, K2, V1, ..., the
-// order in which the products take them.
-__device__ __forceinline__ int k_pos(int t)
-{
-    return t == 0 ? 0 : 2 * t - 1;
-}
+// The stream of K and V tiles of n tiles goes K0, K1, V0, K2, V1, ..., the order
+// in which the products take them.  A place in it: its buffer and the parity
+// of the buffer's use.
+struct Place {
+    int slot, size;
+    uint32_t phase;
 
-__device__ __forceinline__ int v_pos(int t, int n)
-{
-    return t < n - 1 ? 2 * t + 2 : 2 * n - 1;
-}
+    __device__ __forceinline__ Place(int first, int size_) : slot(first), size(size_), phase(0) {}
+    // by at most `size`, which is 3 or more
+    __device__ __forceinline__ void advance(int by)
+    {
+        slot += by;
+        if (slot >= size) {
+            slot -= size;
+            phase ^= 1;
+        }
+    }
+};
 
 // ------------------------------------------------------------------- kernel
 
@@ -366,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto steps = [&](int s) { return q_tiles == 2 ? n : (n + 1 - s) / 2; };
     const uint32_t q_smem = smem_addr(smem), ring = q_smem + q_tiles * kBufBytes;
     uint8_t *ring_ptr = smem + q_tiles * kBufBytes;
-    // Position pos of the stream holds K of tile t, or V of tile t (see k_pos, v_pos).
+    // Position pos of the stream (see Place) holds K of tile t, or V of tile t.
     auto at_pos = [&](int pos, bool &is_k) {
         is_k = pos == 0 || ((pos & 1) && pos < 2 * n - 1);
         return is_k ? (pos + 1) / 2 : pos == 2 * n - 1 ? n - 1 : (pos - 2) / 2;
@@ -393,8 +404,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             return page * p.page_size + at % p.page_size;
         };
-        auto load = [&](const CUtensorMap *map, int pos, int row, uint64_t *bar, uint32_t bytes) {
-            const uint32_t dst = raw0 + (pos % nb) * kTileBytes, b = smem_addr(bar);
+        Place at(0, nb);
+        auto load = [&](const CUtensorMap *map, int row, uint64_t *bar, uint32_t bytes) {
+            const uint32_t dst = raw0 + at.slot * kTileBytes, b = smem_addr(bar);
             if (lane == 0)
                 mbar_arrive_expect_tx(b, bytes);
             __syncwarp();
@@ -414,33 +426,33 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         };
         int row_k = PAGED ? box_row(0) : sm->base + sm->key0, row_v = row_k;
-        for (int pos = 0; pos < 2 * n; ++pos) {
+        for (int pos = 0; pos < 2 * n; ++pos, at.advance(1)) {
             bool is_k;
             const int t = at_pos(pos, is_k);
             if (is_k && t > 0)
                 row_k = PAGED ? box_row(t) : row_k + kSharedTile;
-            if (pos >= nb && !__all_sync(0xffffffffu, wait_phase(&bar_empty[pos % nb], (pos / nb - 1) & 1, p, sm)))
+            if (pos >= nb && !__all_sync(0xffffffffu, wait_phase(&bar_empty[at.slot], at.phase ^ 1, p, sm)))
                 break;
             if (lane == 0)
                 sm->issued = pos + 1;
             const int valid = min(sm->keys - t * kSharedTile, kSharedTile);
             const uint32_t bytes = PAGED ? (valid + box - 1) / box * box * kRow : kTileBytes;
             if (is_k) {
-                load(&tm_k, pos, row_k, &bar_full[pos % nb], bytes);
+                load(&tm_k, row_k, &bar_full[at.slot], bytes);
                 continue;
             }
             if (kFp8 || valid == kSharedTile) {
-                load(&tm_v, pos, row_v, &bar_full[pos % nb], bytes);
+                load(&tm_v, row_v, &bar_full[at.slot], bytes);
             } else {
                 // The rows past the last key (another prefix's, or nobody's) get
                 // weight 0, but 0 * NaN would still reach O: zero them before the
                 // products see the tile (FP8: the widening warps do).
-                load(&tm_v, pos, row_v, &sm->tail, bytes);
+                load(&tm_v, row_v, &sm->tail, bytes);
                 if (lane == 0)
                     sm->tail_issued = 1;
                 if (!__all_sync(0xffffffffu, wait_phase(&sm->tail, 0, p, sm)))
                     break;
-                uint8_t *v = ring_ptr + (pos % nb) * kBufBytes;
+                uint8_t *v = ring_ptr + at.slot * kBufBytes;
                 for (int i = lane; i < (kSharedTile - valid) * 16; i += 32) {
                     const int r = valid + i / 16, c = i % 16;
                     const uint32_t off = (c >> 3) * TL::kHalf + (r >> 3) * TL::kGroup + (r & 7) * 128 + (c & 7) * 16;
@@ -449,75 +461,87 @@ __global__ void __launch_bounds__(kThreads, 1)
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0)
-                    mbar_arrive(smem_addr(&bar_full[pos % nb]));
+                    mbar_arrive(smem_addr(&bar_full[at.slot]));
             }
             row_v = PAGED ? row_k : row_v + kSharedTile;
         }
     } else if (warp == kMmaWarp && ok) {
         // ------------------------------------------------------ the products
-        if (lane == 0) {
-            constexpr uint32_t id_s = mma_idesc(128, kSharedTile, !kFp8, false);
-            constexpr uint32_t id_o = mma_idesc(128, kHeadDim, !kFp8, true);
-            bool go = wait_phase(&sm->q_ready, 0, p, sm);
-            // S of stream s's step i: K of its tile; frees the buffer after the
-            // last stream that takes it.
-            auto scores = [&](int s, int i) {
-                const int t = q_tiles == 2 ? i : 2 * i + s, pos = k_pos(t), b = pos % nw;
-                if (!wait_phase(&sm->full[b], (pos / nw) & 1, p, sm))
+        constexpr uint32_t id_s = mma_idesc(128, kSharedTile, !kFp8, false);
+        constexpr uint32_t id_o = mma_idesc(128, kHeadDim, !kFp8, true);
+        const uint32_t leader = elect_one();
+        const bool two = q_tiles == 2;
+        const int steps0 = steps(0), steps1 = steps(1);
+        const uint64_t qd = smem_desc(q_smem, 16, 1024);
+        const uint64_t kd = smem_desc(ring, 16, TL::kGroup), vd = smem_desc(ring, TL::kHalf, TL::kGroup);
+        constexpr uint32_t kBuf16 = kBufBytes / 16;   // descriptors count 16 bytes
+        Place k_at(0, nw), v_at(n > 1 ? 2 : 1, nw);
+        int k_tile = 0, v_tile = 0;
+        bool go = wait_phase(&sm->q_ready, 0, p, sm);
+        // S of stream s's next step: K of its tile; frees the buffer after the
+        // last stream that takes it.
+        auto scores = [&](int s) {
+            if (!wait_phase(&sm->full[k_at.slot], k_at.phase, p, sm))
+                return false;
+            tcgen05_fence_after();
+            const uint64_t qs = qd + (two ? s : 0) * kBuf16, ks = kd + k_at.slot * kBuf16;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)   // 16 head dimensions a step
+                mma_ss(tmem + s * kStreamCols, qs + ((k >> 2) * kHalfBytes + (k & 3) * 32) / 16,
+                       ks + ((k >> 2) * TL::kHalf + (k & 3) * 32) / 16, id_s, k > 0, leader);
+            tcgen05_commit(smem_addr(&sm->s_full[s]), leader);
+            if (!two || s == 1) {
+                tcgen05_commit(smem_addr(&sm->empty[k_at.slot]), leader);
+                k_at.advance(k_tile == 0 ? 1 : 2);
+                ++k_tile;
+            }
+            return true;
+        };
+        // O += P V of stream s's step i, in two parts: each half of the keys is
+        // ready in two parts of 32.
+        auto values = [&](int s, int i, bool last) {
+            if (!wait_phase(&sm->full[v_at.slot], v_at.phase, p, sm))
+                return false;
+            const uint32_t pa = tmem + s * kStreamCols;
+            const uint64_t vs = vd + v_at.slot * kBuf16;
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                if (!wait_phase(&sm->p_ready[s][part], i & 1, p, sm))
                     return false;
                 tcgen05_fence_after();
-                const uint32_t qa = q_smem + (q_tiles == 2 ? s : 0) * kBufBytes, kb = ring + b * kBufBytes;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)   // 16 head dimensions a step
-                    mma_ss(tmem + s * kStreamCols,
-                           smem_desc(qa + (k >> 2) * kHalfBytes + (k & 3) * 32, 16, 1024),
-                           smem_desc(kb + (k >> 2) * TL::kHalf + (k & 3) * 32, 16, TL::kGroup), id_s, k > 0);
-                tcgen05_commit(smem_addr(&sm->s_full[s]));
-                if (q_tiles == 1 || s == 1)
-                    tcgen05_commit(smem_addr(&sm->empty[b]));
-                return true;
-            };
-            // O += P V of stream s's step i, in two parts: each half of the keys
-            // is ready in two parts of 32.
-            auto values = [&](int s, int i) {
-                const int t = q_tiles == 2 ? i : 2 * i + s, pos = v_pos(t, n), b = pos % nw;
-                if (!wait_phase(&sm->full[b], (pos / nw) & 1, p, sm))
-                    return false;
-                const uint32_t vb = ring + b * kBufBytes, pa = tmem + s * kStreamCols;
-#pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    if (!wait_phase(&sm->p_ready[s][part], i & 1, p, sm))
-                        return false;
-                    tcgen05_fence_after();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {   // 16 keys a step, hi then lo
-                        const int c = (j >> 1) * 2 + part, k = 2 * c + (j & 1);   // chunk of 32 keys; step
-                        const uint64_t vd = smem_desc(vb + k * 2 * TL::kGroup, TL::kHalf, TL::kGroup);
-                        mma_ts(pa + 128, pa + 32 * c + 8 * (j & 1), vd, id_o, i > 0 || part > 0 || j > 0);
-                        mma_ts(pa + 128, pa + 32 * c + 16 + 8 * (j & 1), vd, id_o, 1);
-                    }
+                for (int j = 0; j < 4; ++j) {   // 16 keys a step, hi then lo
+                    const int c = (j >> 1) * 2 + part, k = 2 * c + (j & 1);   // chunk of 32 keys; step
+                    const uint64_t d = vs + k * 2 * TL::kGroup / 16;
+                    mma_ts(pa + 128, pa + 32 * c + 8 * (j & 1), d, id_o, i > 0 || part > 0 || j > 0, leader);
+                    mma_ts(pa + 128, pa + 32 * c + 16 + 8 * (j & 1), d, id_o, 1, leader);
                 }
-                if (q_tiles == 1 || s == 1)
-                    tcgen05_commit(smem_addr(&sm->empty[b]));
-                if (i == steps(s) - 1)
-                    tcgen05_commit(smem_addr(&sm->o_done[s]));
-                return true;
-            };
-            for (int s = 0; s < 2 && go; ++s)
-                if (steps(s) > 0)
-                    go = scores(s, 0);
-            for (int i = 0; i < steps(0) && go; ++i)
-                for (int s = 0; s < 2 && go; ++s) {
-                    if (i < steps(s))
-                        go = values(s, i);
-                    if (go && i + 1 < steps(s))
-                        go = scores(s, i + 1);
-                }
-            // whatever the others saw, the products in flight end before tensor
-            // memory is freed
-            tcgen05_commit(smem_addr(&sm->drain));
-            mbar_wait(smem_addr(&sm->drain), 0, kDrainTimeoutNs);
+            }
+            if (!two || s == 1) {
+                tcgen05_commit(smem_addr(&sm->empty[v_at.slot]), leader);
+                v_at.advance(v_tile == n - 2 ? 1 : 2);
+                ++v_tile;
+            }
+            if (last)
+                tcgen05_commit(smem_addr(&sm->o_done[s]), leader);
+            return true;
+        };
+        go = go && scores(0);
+        if (steps1 > 0)
+            go = go && scores(1);
+        for (int i = 0; i < steps0 && go; ++i) {
+            go = values(0, i, i == steps0 - 1);
+            if (i + 1 < steps0)
+                go = go && scores(0);
+            if (i < steps1)
+                go = go && values(1, i, i == steps1 - 1);
+            if (i + 1 < steps1)
+                go = go && scores(1);
         }
+        // whatever the others saw, the products in flight end before tensor
+        // memory is freed
+        tcgen05_commit(smem_addr(&sm->drain), leader);
+        mbar_wait(smem_addr(&sm->drain), 0, kDrainTimeoutNs);
         __syncwarp();
     } else if (kFp8 && warp >= kWidenWarp && ok) {
         // ------------------------------------- FP8: raw tiles to f16 operands
@@ -527,17 +551,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         // r ^ 5 and four chunks of a half, which meet no bank twice on either side.
         const uint8_t *raw0 = ring_ptr + kWideBuffers * kBufBytes;
         const int ph = lane >> 3, r8 = ph ^ (((lane >> 2) & 1) * 5), cc = lane & 3;
-        for (int pos = 0; pos < 2 * n; ++pos) {
+        Place from(0, nb), to(0, kWideBuffers);
+        for (int pos = 0; pos < 2 * n; ++pos, from.advance(1), to.advance(1)) {
             bool is_k;
             const int t = at_pos(pos, is_k);
             const int valid = sm->keys - t * kSharedTile;
-            bool go = wait_phase(&sm->raw_full[pos % nb], (pos / nb) & 1, p, sm);
+            bool go = wait_phase(&sm->raw_full[from.slot], from.phase, p, sm);
             if (go && pos >= kWideBuffers)
-                go = wait_phase(&sm->empty[pos % kWideBuffers], (pos / kWideBuffers - 1) & 1, p, sm);
+                go = wait_phase(&sm->empty[to.slot], to.phase ^ 1, p, sm);
             if (!__all_sync(0xffffffffu, go))
                 break;
-            const uint8_t *src = raw0 + (pos % nb) * kRawBytes;
-            uint8_t *dst = ring_ptr + (pos % kWideBuffers) * kBufBytes;
+            const uint8_t *src = raw0 + from.slot * kRawBytes;
+            uint8_t *dst = ring_ptr + to.slot * kBufBytes;
 #pragma unroll 4
             for (int j = 0; j < 32 / kWidenWarps; ++j) {   // group of 8 rows, half
                 const int g = (warp - kWidenWarp) * (16 / kWidenWarps) + (j >> 1), half = j & 1;
@@ -563,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(smem_addr(&sm->raw_empty[pos % nb]));
-                mbar_arrive(smem_addr(&sm->full[pos % kWideBuffers]));
+                mbar_arrive(smem_addr(&sm->raw_empty[from.slot]));
+                mbar_arrive(smem_addr(&sm->full[to.slot]));
             }
         }
     } else if (warp < kProducerWarp) {

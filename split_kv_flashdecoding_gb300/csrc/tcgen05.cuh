@@ -30,10 +30,22 @@ __device__ __forceinline__ void tcgen05_fence_after()
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
-// One arrival on `bar` once every tcgen05.mma this thread issued has completed.
-__device__ __forceinline__ void tcgen05_commit(uint32_t bar)
+// One lane of a converged warp: nonzero there.  The instructions below are run
+// by the whole warp and issued by that lane (`leader`), so that their operands
+// are computed once for the warp.
+__device__ __forceinline__ uint32_t elect_one()
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+    uint32_t x;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(x));
+    return x;
+}
+
+// One arrival on `bar` once every tcgen05.mma the leader issued has completed.
+__device__ __forceinline__ void tcgen05_commit(uint32_t bar, uint32_t leader)
+{
+    asm volatile("{\n\t.reg .pred l;\n\tsetp.ne.u32 l, %1, 0;\n\t"
+                 "@l tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+                 "r"(leader)
                  : "memory");
 }
 
@@ -57,22 +69,24 @@ __host__ __device__ constexpr uint32_t mma_idesc(int m, int n, bool bf16, bool b
 }
 
 // D (+)= A B, A and B in shared memory; accumulate: 0 overwrites D.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t leader)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, l;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 l, %5, 0;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
 
 // D (+)= A B, A in tensor memory (two 16-bit elements a column), B in shared.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t leader)
 {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "{\n\t.reg .pred p, l;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 l, %5, 0;\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
 
