@@ -27,13 +27,19 @@
 //
 // Warps: 0-15 the softmax -- two warpgroups a stream, one a half of the tile's
 // keys; a thread owns a row and 64 of its scores (tcgen05.ld gives it the row's
-// columns), and the two warps that share rows agree on the row's maximum by a
-// barrier with a vote.  With one warpgroup a stream the softmax of a tile took
-// over twice as long as the other stream's products, and the tensor cores
-// waited: they were busy for 41 % of 416 us (256 x 64 heads behind 32768 keys).
-// 16 the producer (TMA), 17 issues the products, 18 and 19 the widening (FP8).
-// The running maximum is only raised, and O rescaled, when a row's maximum
-// grew by more than 2^8: until then the weights are at most 256.
+// columns).  16 the producer (TMA), 17 issues the products, 18 and 19 the
+// widening (FP8).
+//
+// The reference m of a row's weights only has to keep them in their type's
+// range: the weights are floating-point numbers, their size costs no accuracy.
+// So m is the maximum of the row's first tile, and the steps behind it turn
+// scores into weights as they arrive, with no maximum and no exchange between
+// the warps of a row on the way.  A row whose later scores are out of that
+// range (its sum over 2^40 in bf16; a weight over f16's with FP8 K/V) is seen
+// at the end, and the CTA then does its item again with careful steps, which
+// raise m and rescale O.  Careful steps alone took 310 us where these take
+// 250 us (256 x 64 heads behind 32768 keys): the tensor cores waited for the
+// maximum, the vote of a row's two warps, and then for the weights.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -61,7 +67,12 @@ constexpr int kProducerWarp = 16, kMmaWarp = 17, kWidenWarp = 18, kWidenWarps = 
 constexpr int kThreads = 640;
 constexpr int kTmemCols = 512;
 constexpr int kStreamCols = 256;                        // S (and P over it) 128, O 128
-constexpr float kRaise = 8.f;                           // log2 of the growth that raises the maximum
+// Careful steps: log2 of the growth of a row's maximum that raises m.
+constexpr float kRaise = 8.f;
+// The other steps: the most that a row's sum (bf16) or largest weight (FP8 K/V,
+// f16 weights, 2^7 times larger) may be; beyond it the item is done again.
+template <int DT>
+constexpr float kMostWeight = DT == kKvTypeFp8 ? 65000.f : 1099511627776.f;
 constexpr uint32_t kSleepNs = 100000;                    // a wait's sleep between looks at the timer
 constexpr int kOutStride = kHeadDim + 4;                // floats between rows of the epilogue's staging
 
@@ -72,6 +83,7 @@ struct SharedSmem {
     uint64_t q_ready, tail, drain;
     uint32_t tmem;
     int abort;
+    int redo;               // a row's weights left their type's range
     int issued;             // ring fills issued (for the drain after an error)
     int tail_issued;
     // the CTA's item
@@ -181,7 +193,7 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, const
         // These waits are the pipeline's hand-overs: a waiting warp sleeps until
         // the phase completes (polling takes issue slots from the warps at
         // work), and looks at the timer only when it woke for nothing.
-        if (mbar_try_wait_for(a, parity, kSleepNs))
+        if (mbar_try_wait(a, parity))
             return true;
         const uint64_t t0 = global_timer_ns();
         while (!*reinterpret_cast<volatile int *>(&sm->abort)) {
@@ -310,26 +322,36 @@ __global__ void __launch_bounds__(kThreads, 1)
     SharedSmem *sm = reinterpret_cast<SharedSmem *>(smem + kBuffers * kBufBytes);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    if (warp == kProducerWarp && lane == 0) {
+    // One thread: all barriers before their first phase.
+    auto init_barriers = [&](bool again) {
+        auto init = [&](uint64_t *bar, uint32_t count) {
+            if (again)
+                mbar_inval(smem_addr(bar));
+            mbar_init(smem_addr(bar), count);
+        };
         for (int i = 0; i < kMaxRing; ++i) {
-            mbar_init(smem_addr(&sm->full[i]), kFp8 ? kWidenWarps : 1);
-            mbar_init(smem_addr(&sm->empty[i]), 1);
-            mbar_init(smem_addr(&sm->raw_full[i]), 1);
-            mbar_init(smem_addr(&sm->raw_empty[i]), kWidenWarps);
+            init(&sm->full[i], kFp8 ? kWidenWarps : 1);
+            init(&sm->empty[i], 1);
+            init(&sm->raw_full[i], 1);
+            init(&sm->raw_empty[i], kWidenWarps);
         }
         for (int s = 0; s < 2; ++s) {
-            mbar_init(smem_addr(&sm->s_full[s]), 1);
-            mbar_init(smem_addr(&sm->p_ready[s][0]), kStreamWarps);
-            mbar_init(smem_addr(&sm->p_ready[s][1]), kStreamWarps);
-            mbar_init(smem_addr(&sm->o_done[s]), 1);
+            init(&sm->s_full[s], 1);
+            init(&sm->p_ready[s][0], kStreamWarps);
+            init(&sm->p_ready[s][1], kStreamWarps);
+            init(&sm->o_done[s], 1);
         }
-        mbar_init(smem_addr(&sm->q_ready), kSoftmaxThreads / 32);
-        mbar_init(smem_addr(&sm->tail), 1);
-        mbar_init(smem_addr(&sm->drain), 1);
+        init(&sm->q_ready, kSoftmaxThreads / 32);
+        init(&sm->tail, 1);
+        init(&sm->drain, 1);
         fence_mbar_init();
-        sm->abort = 0;
         sm->issued = 0;
         sm->tail_issued = 0;
+    };
+    if (warp == kProducerWarp && lane == 0) {
+        init_barriers(false);
+        sm->abort = 0;
+        sm->redo = 0;
     }
     if (warp == kMmaWarp)
         tmem_alloc(smem_addr(&sm->tmem), kTmemCols);
@@ -383,6 +405,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         return is_k ? (pos + 1) / 2 : pos == 2 * n - 1 ? n - 1 : (pos - 2) / 2;
     };
 
+    // At most two passes over the item: the second with careful steps, when the
+    // first left the weights' range.
+    float c2 = 0.f;   // softmax warps: what a score is multiplied by
+    for (int pass = 0; pass < 2; ++pass) {
+    const bool careful = pass > 0;
     if (warp == kProducerWarp && ok) {
         // --------------------------------------------------------- producer
         const uint64_t pol = l2_evict_first_policy();
@@ -478,8 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         Place k_at(0, nw), v_at(n > 1 ? 2 : 1, nw);
         int k_tile = 0, v_tile = 0;
         bool go = wait_phase(&sm->q_ready, 0, p, sm);
-        // S of stream s's next step: K of its tile; frees the buffer after the
-        // last stream that takes it.
+        // S of stream s's next step: K of its tile.
         auto scores = [&](int s) {
             if (!wait_phase(&sm->full[k_at.slot], k_at.phase, p, sm))
                 return false;
@@ -491,7 +517,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                        ks + ((k >> 2) * TL::kHalf + (k & 3) * 32) / 16, id_s, k > 0, leader);
             tcgen05_commit(smem_addr(&sm->s_full[s]), leader);
             if (!two || s == 1) {
-                tcgen05_commit(smem_addr(&sm->empty[k_at.slot]), leader);
                 k_at.advance(k_tile == 0 ? 1 : 2);
                 ++k_tile;
             }
@@ -518,7 +543,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
             }
             if (!two || s == 1) {
-                tcgen05_commit(smem_addr(&sm->empty[v_at.slot]), leader);
                 v_at.advance(v_tile == n - 2 ? 1 : 2);
                 ++v_tile;
             }
@@ -604,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             factor *= ok ? __ldg(p.k_scale + sm->kvh) : 1.f;
             v_scale = ok ? __ldg(p.v_scale + sm->kvh) : 1.f;
         }
-        if (ok) {
+        if (ok && !careful) {
             // Q rows into shared memory, [half][128 rows][128 bytes] a tile; a
             // negative factor of the scores turns q around.
             const uint32_t flip = factor < 0.f ? 0x80008000u : 0u;
@@ -655,60 +679,125 @@ __global__ void __launch_bounds__(kThreads, 1)
                                            (((ch & 7) ^ (rr & 7)) << 4)) = v;
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_addr(&sm->q_ready));
         }
-        barrier(1, kSoftmaxThreads);   // q_scale is written
+        __syncwarp();
+        if (lane == 0 && ok)
+            mbar_arrive(smem_addr(&sm->q_ready));
         // log2 e times the factor of the scores; never 0, so that a masked score
         // (-inf) stays -inf
-        float c2 = fabsf(factor) * kLog2e;
-        if constexpr (kFp8) {
-            c2 *= sm->q_scale[(two ? s * kSharedQRows : 0) + trow];
-            barrier(1, kSoftmaxThreads);   // row_max takes its place
+        if (!careful) {
+            c2 = fabsf(factor) * kLog2e;
+            if constexpr (kFp8) {
+                barrier(1, kSoftmaxThreads);   // q_scale is written
+                c2 *= sm->q_scale[(two ? s * kSharedQRows : 0) + trow];
+                barrier(1, kSoftmaxThreads);   // row_max takes its place
+            }
+            c2 = c2 == 0.f ? 1.17549435e-38f : c2;
         }
-        c2 = c2 == 0.f ? 1.17549435e-38f : c2;
         // FP8: weights are 2^7 times larger, which keeps seven more bits of the
         // small ones in f16; it cancels in O
         constexpr float kBias = kFp8 ? 7.f : 0.f;
-        float m_ref = -INFINITY, l = 0.f;   // maximum of the raw scores that the weights refer to
+        // One lane frees the buffers of the products that s_full shows done: the
+        // step's K, and the V of the step before.
+        const bool frees = (half == 0 && quad == 0 && lane == 0) && (!two || s == 1);
+        float m_ref = -INFINITY, l = 0.f;   // what the weights refer to (a raw score), their sum
+        float most = 0.f;                   // FP8: the largest weight
         bool go = ok;
+        // 32 scores to weights: hi in the first 16 of their columns, lo in the others
+        auto weights = [&](const uint32_t (&r)[32], uint32_t col, float off, float2 &sum) {
+            const float2 c22 = make_float2(c2, c2), off2 = make_float2(off, off);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 x = fma2(make_float2(__uint_as_float(r[16 * q + 2 * j]),
+                                                      __uint_as_float(r[16 * q + 2 * j + 1])), c22, off2);
+                    const float2 w = make_float2(ex2(x.x), ex2(x.y));
+                    sum = add2(sum, w);
+                    if constexpr (kFp8)
+                        most = fmaxf(most, fmaxf(w.x, w.y));
+                    hi[j] = pack2<DT>(w);
+                    const float2 h = unpack2<DT>(hi[j]);
+                    lo[j] = pack2<DT>(fma2(h, make_float2(-1.f, -1.f), w));
+                }
+                tmem_st8(col + 8 * q, hi);
+                tmem_st8(col + 16 + 8 * q, lo);
+            }
+        };
+        auto publish = [&](int part) {
+            tmem_wait_st();
+            tcgen05_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&sm->p_ready[s][part]));
+        };
+        auto mask = [&](uint32_t (&r)[32], int valid) {   // scores past the last key
+            if (valid < 32) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    if (j >= valid)
+                        r[j] = 0xff800000u;
+            }
+        };
+        auto largest = [](const uint32_t (&r0)[32], const uint32_t (&r1)[32]) {
+            float mx[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                mx[j] = fmaxf(__uint_as_float(r0[j]), __uint_as_float(r1[j]));
+#pragma unroll
+            for (int j = 4; j < 32; ++j)
+                mx[j & 3] = fmaxf(fmaxf(mx[j & 3], __uint_as_float(r0[j])), __uint_as_float(r1[j]));
+            return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        };
         for (int i = 0; i < steps(s); ++i) {
-            // After an error the steps go on without work, so that the barrier
-            // of the two warps always meets.
+            // After an error the steps go on without work, so that the barriers
+            // of a row's two warps always meet.
             if (go)
                 go = __all_sync(0xffffffffu, wait_phase(&sm->s_full[s], i & 1, p, sm));
-            const int valid = sm->keys - (two ? i : 2 * i + s) * kSharedTile - half * 64;
+            const int t = two ? i : 2 * i + s;
+            const int valid = sm->keys - t * kSharedTile - half * 64;
+            float2 sum = make_float2(0.f, 0.f);
             uint32_t r0[32], r1[32];
-            float mt = -INFINITY;
-            bool raise = false;
             if (go) {
                 tcgen05_fence_after();
                 tmem_ld32(s_col, r0);
-                tmem_ld32(s_col + 32, r1);
+                if (frees) {
+                    mbar_arrive(smem_addr(&sm->empty[(t == 0 ? 0 : 2 * t - 1) % nw]));
+                    if (i > 0)   // V of tile t - 1, or t - 2 (every other one)
+                        mbar_arrive(smem_addr(&sm->empty[(two ? 2 * t : 2 * t - 2) % nw]));
+                }
                 tmem_wait_ld();
                 settle(r0);
+                tmem_ld32(s_col + 32, r1);
+                mask(r0, valid);
+            }
+            if (i > 0 && !careful) {
+                if (!go)
+                    continue;
+                const float off = kBias - m_ref * c2;
+                weights(r0, s_col, off, sum);
+                publish(0);
+                tmem_wait_ld();
                 settle(r1);
-                if (valid < 64) {
-#pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        if (j >= valid)
-                            r0[j] = 0xff800000u;
-                        if (32 + j >= valid)
-                            r1[j] = 0xff800000u;
-                    }
-                }
-                float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    mx[0] = fmaxf(mx[0], __uint_as_float(r0[j]));
-                    mx[1] = fmaxf(mx[1], __uint_as_float(r1[j]));
-                }
-                mt = fmaxf(mx[0], mx[1]);
+                mask(r1, valid - 32);
+                weights(r1, s_col + 32, off, sum);
+                publish(1);
+                l += sum.x + sum.y;
+                continue;
+            }
+            // The first step, and every careful one: a row's maximum is that of
+            // both halves of its keys.
+            float mt = -INFINITY;
+            bool raise = false;
+            if (go) {
+                tmem_wait_ld();
+                settle(r1);
+                mask(r1, valid - 32);
+                mt = largest(r0, r1);
                 raise = mt > m_ref && (m_ref == -INFINITY || (mt - m_ref) * c2 > kRaise);
             }
             if (barrier_or(pair_bar, 64, raise)) {
-                // a row's maximum is that of both halves of its keys
                 sm->row_max[s][half][trow] = mt;
                 barrier(pair_bar, 64);
                 const float both = fmaxf(mt, sm->row_max[s][half ^ 1][trow]);
@@ -736,43 +825,23 @@ __global__ void __launch_bounds__(kThreads, 1)
                 continue;
             // a row whose scores are all -inf so far keeps weights of 0
             const float off = (m_ref == -INFINITY ? 0.f : -m_ref * c2) + kBias;
-            const float2 c22 = make_float2(c2, c2), off2 = make_float2(off, off);
-            float2 sum = make_float2(0.f, 0.f);
-            // 32 keys: hi in the first 16 of their columns, lo in the others
-            auto weights = [&](const uint32_t (&r)[32], uint32_t col) {
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    uint32_t hi[8], lo[8];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float2 x = fma2(make_float2(__uint_as_float(r[16 * q + 2 * j]),
-                                                          __uint_as_float(r[16 * q + 2 * j + 1])), c22, off2);
-                        const float2 w = make_float2(ex2(x.x), ex2(x.y));
-                        sum = add2(sum, w);
-                        hi[j] = pack2<DT>(w);
-                        const float2 h = unpack2<DT>(hi[j]);
-                        lo[j] = pack2<DT>(fma2(h, make_float2(-1.f, -1.f), w));
-                    }
-                    tmem_st8(col + 8 * q, hi);
-                    tmem_st8(col + 16 + 8 * q, lo);
-                }
-                tmem_wait_st();
-                tcgen05_fence_before();
-                __syncwarp();
-            };
-            weights(r0, s_col);
-            if (lane == 0)
-                mbar_arrive(smem_addr(&sm->p_ready[s][0]));
-            weights(r1, s_col + 32);
-            if (lane == 0)
-                mbar_arrive(smem_addr(&sm->p_ready[s][1]));
+            weights(r0, s_col, off, sum);
+            publish(0);
+            weights(r1, s_col + 32, off, sum);
+            publish(1);
             l += sum.x + sum.y;
         }
+        // Out of range: a weight too large for its type, or no score to refer to
+        // in the first tile.
+        if (go && !careful && steps(s) > 0 && (m_ref == -INFINITY || (kFp8 ? most : l) > kMostWeight<DT>))
+            sm->redo = 1;
         // ----------------------------------------------------- the partial
         for (int x = 0; x < 2; ++x)   // both streams' products are done with the ring
             if (go && steps(x) > 0)
                 go = __all_sync(0xffffffffu, wait_phase(&sm->o_done[x], 0, p, sm));
         tcgen05_fence_after();
+        barrier(1, kSoftmaxThreads);
+        if (careful || !sm->redo) {
         float *stage = reinterpret_cast<float *>(smem);   // [q_tiles * 128][kOutStride]
         SharedEnd *end = reinterpret_cast<SharedEnd *>(smem + kEndOffset);
         float *mine = stage + ((two ? s * kSharedQRows : 0) + trow) * kOutStride + half * 64;
@@ -847,9 +916,17 @@ __global__ void __launch_bounds__(kThreads, 1)
                 reinterpret_cast<float4 *>(p.partial_o + (sm->part_row + out * sm->part_stride) * kHeadDim)[lane] = v;
             }
         }
+        }
     }
     tcgen05_fence_before();
     __syncthreads();
+    if (careful || !sm->redo || sm->abort)
+        break;
+    if (warp == kProducerWarp && lane == 0)
+        init_barriers(true);   // every phase of the first pass has completed
+    __syncthreads();
+    tcgen05_fence_after();
+    }
     griddep_launch_dependents();
     if (warp == kMmaWarp) {
         tcgen05_fence_after();
