@@ -27,8 +27,9 @@
 //
 // Warps: 0-15 the softmax -- two warpgroups a stream, one a half of the tile's
 // keys; a thread owns a row and 64 of its scores (tcgen05.ld gives it the row's
-// columns).  16 the producer (TMA), 17 issues the products, 18 and 19 the
-// widening (FP8).
+// columns).  16 the producer (TMA), 17 issues the products of both streams in
+// turn (a warp for each let the two streams' products run through one another:
+// both then ended late, 359 us for 296 us), 18 and 19 do the widening (FP8).
 //
 // The reference m of a row's weights only has to keep them in their type's
 // range: the weights are floating-point numbers, their size costs no accuracy.
@@ -289,7 +290,7 @@ struct Place {
     uint32_t phase;
 
     __device__ __forceinline__ Place(int first, int size_) : slot(first), size(size_), phase(0) {}
-    // by at most `size`, which is 3 or more
+    // by at most `size`
     __device__ __forceinline__ void advance(int by)
     {
         slot += by;
@@ -348,11 +349,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm->issued = 0;
         sm->tail_issued = 0;
     };
-    if (warp == kProducerWarp && lane == 0) {
-        init_barriers(false);
-        sm->abort = 0;
-        sm->redo = 0;
-    }
     if (warp == kMmaWarp)
         tmem_alloc(smem_addr(&sm->tmem), kTmemCols);
     griddep_wait();
@@ -383,6 +379,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             } else {
                 report(p.status, FD_ERR_DEVICE_BOUNDS);
             }
+            init_barriers(false);
+            sm->abort = 0;
+            sm->redo = 0;
         }
     }
     tcgen05_fence_before();
@@ -418,18 +417,39 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kRow = kFp8 ? kHeadDim : 2 * kHeadDim, kTileBytes = kSharedTile * kRow;
         uint64_t *bar_full = kFp8 ? sm->raw_full : sm->full, *bar_empty = kFp8 ? sm->raw_empty : sm->empty;
         const uint32_t raw0 = ring + (kFp8 ? kWideBuffers * kBufBytes : 0);
-        // page row of this lane's box of tile t (paged), -1: past the prefix
-        auto box_row = [&](int t) -> int {
-            const int key = t * kSharedTile + lane * box;
-            if (lane >= boxes || key >= sm->keys)
-                return -1;
-            const int at = sm->key0 + key;
-            int page = __ldg(p.prefix_indices + sm->base + at / p.page_size);
-            if (page < 0 || page >= p.num_pages) {   // read page 0 in its place
-                report(p.status, FD_ERR_DEVICE_BOUNDS);
-                page = 0;
+        // Paged: the lane's box of the next tile is at row `off` of the request's
+        // page `pg`; a tile on, that is a fixed number of pages and rows further.
+        int pg = 0, off = 0, key = sm->keys;
+        const int pages_on = PAGED ? kSharedTile / p.page_size : 0;
+        const int rows_on = PAGED ? kSharedTile % p.page_size : 0;
+        if (PAGED && lane < boxes) {
+            key = lane * box;
+            pg = (sm->key0 + key) / p.page_size;
+            off = (sm->key0 + key) % p.page_size;
+        }
+        // The next tile's page is looked up a tile ahead and used when its turn
+        // comes; -1: no box of this lane (past the last key).
+        int id_next = -1, off_next = 0;
+        auto look_up = [&]() {
+            const bool has = key < sm->keys;
+            id_next = has ? __ldg(p.prefix_indices + sm->base + pg) : -1;
+            off_next = has ? off : -1;
+            key += lane < boxes ? kSharedTile : 0;
+            pg += pages_on;
+            off += rows_on;
+            if (off >= p.page_size) {
+                off -= p.page_size;
+                ++pg;
             }
-            return page * p.page_size + at % p.page_size;
+        };
+        auto pool_row = [&]() -> int {
+            if (off_next < 0)
+                return -1;
+            if (id_next < 0 || id_next >= p.num_pages) {   // read page 0 in its place
+                report(p.status, FD_ERR_DEVICE_BOUNDS);
+                id_next = 0;
+            }
+            return id_next * p.page_size + off_next;
         };
         Place at(0, nb);
         auto load = [&](const CUtensorMap *map, int row, uint64_t *bar, uint32_t bytes) {
@@ -452,12 +472,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tma_load_3d(dst, map, 0, row, 2 * sm->kvh, b, pol);
             }
         };
-        int row_k = PAGED ? box_row(0) : sm->base + sm->key0, row_v = row_k;
+        if (PAGED)
+            look_up();
+        int row_k = sm->base + sm->key0 - kSharedTile, row_v = 0;
         for (int pos = 0; pos < 2 * n; ++pos, at.advance(1)) {
             bool is_k;
             const int t = at_pos(pos, is_k);
-            if (is_k && t > 0)
-                row_k = PAGED ? box_row(t) : row_k + kSharedTile;
+            if (is_k) {
+                row_v = row_k;
+                if constexpr (PAGED) {
+                    row_k = pool_row();
+                    look_up();
+                } else {
+                    row_k += kSharedTile;
+                }
+            }
             if (pos >= nb && !__all_sync(0xffffffffu, wait_phase(&bar_empty[at.slot], at.phase ^ 1, p, sm)))
                 break;
             if (lane == 0)
@@ -468,13 +497,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 load(&tm_k, row_k, &bar_full[at.slot], bytes);
                 continue;
             }
+            const int row_t = t == n - 1 ? row_k : row_v;   // K of tile t + 1 has gone before, but for the last
             if (kFp8 || valid == kSharedTile) {
-                load(&tm_v, row_v, &bar_full[at.slot], bytes);
+                load(&tm_v, row_t, &bar_full[at.slot], bytes);
             } else {
                 // The rows past the last key (another prefix's, or nobody's) get
                 // weight 0, but 0 * NaN would still reach O: zero them before the
                 // products see the tile (FP8: the widening warps do).
-                load(&tm_v, row_v, &sm->tail, bytes);
+                load(&tm_v, row_t, &sm->tail, bytes);
                 if (lane == 0)
                     sm->tail_issued = 1;
                 if (!__all_sync(0xffffffffu, wait_phase(&sm->tail, 0, p, sm)))
@@ -490,77 +520,77 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (lane == 0)
                     mbar_arrive(smem_addr(&bar_full[at.slot]));
             }
-            row_v = PAGED ? row_k : row_v + kSharedTile;
         }
     } else if (warp == kMmaWarp && ok) {
         // ------------------------------------------------------ the products
+        // A wait that gave up is reported; the products then work on what there
+        // is, so that no branch depends on it.
         constexpr uint32_t id_s = mma_idesc(128, kSharedTile, !kFp8, false);
         constexpr uint32_t id_o = mma_idesc(128, kHeadDim, !kFp8, true);
         const uint32_t leader = elect_one();
         const bool two = q_tiles == 2;
         const int steps0 = steps(0), steps1 = steps(1);
-        const uint64_t qd = smem_desc(q_smem, 16, 1024);
-        const uint64_t kd = smem_desc(ring, 16, TL::kGroup), vd = smem_desc(ring, TL::kHalf, TL::kGroup);
-        constexpr uint32_t kBuf16 = kBufBytes / 16;   // descriptors count 16 bytes
+        const uint32_t q_lo = smem_desc_lo(q_smem, 16);
+        const uint32_t k_lo = smem_desc_lo(ring, 16);
+        const uint32_t v_lo = smem_desc_lo(ring, TL::kHalf);
+        constexpr uint32_t q_hi = smem_desc_hi(1024), kv_hi = smem_desc_hi(TL::kGroup);
+        constexpr uint32_t kBuf16 = kBufBytes / 16;
         Place k_at(0, nw), v_at(n > 1 ? 2 : 1, nw);
         int k_tile = 0, v_tile = 0;
-        bool go = wait_phase(&sm->q_ready, 0, p, sm);
-        // S of stream s's next step: K of its tile.
+        wait_phase(&sm->q_ready, 0, p, sm);
+        // S of stream s's next step: K of its tile; frees the buffer after the
+        // last stream that takes it.
         auto scores = [&](int s) {
-            if (!wait_phase(&sm->full[k_at.slot], k_at.phase, p, sm))
-                return false;
+            wait_phase(&sm->full[k_at.slot], k_at.phase, p, sm);
             tcgen05_fence_after();
-            const uint64_t qs = qd + (two ? s : 0) * kBuf16, ks = kd + k_at.slot * kBuf16;
+            const uint32_t qa = q_lo + (two ? s : 0) * kBuf16, ka = k_lo + k_at.slot * kBuf16;
 #pragma unroll
             for (int k = 0; k < 8; ++k)   // 16 head dimensions a step
-                mma_ss(tmem + s * kStreamCols, qs + ((k >> 2) * kHalfBytes + (k & 3) * 32) / 16,
-                       ks + ((k >> 2) * TL::kHalf + (k & 3) * 32) / 16, id_s, k > 0, leader);
+                mma_ss(tmem + s * kStreamCols, qa + ((k >> 2) * kHalfBytes + (k & 3) * 32) / 16, q_hi,
+                       ka + ((k >> 2) * TL::kHalf + (k & 3) * 32) / 16, kv_hi, id_s, k > 0, leader);
             tcgen05_commit(smem_addr(&sm->s_full[s]), leader);
             if (!two || s == 1) {
+                tcgen05_commit(smem_addr(&sm->empty[k_at.slot]), leader);
                 k_at.advance(k_tile == 0 ? 1 : 2);
                 ++k_tile;
             }
-            return true;
         };
         // O += P V of stream s's step i, in two parts: each half of the keys is
         // ready in two parts of 32.
         auto values = [&](int s, int i, bool last) {
-            if (!wait_phase(&sm->full[v_at.slot], v_at.phase, p, sm))
-                return false;
-            const uint32_t pa = tmem + s * kStreamCols;
-            const uint64_t vs = vd + v_at.slot * kBuf16;
+            wait_phase(&sm->full[v_at.slot], v_at.phase, p, sm);
+            const uint32_t pa = tmem + s * kStreamCols, va = v_lo + v_at.slot * kBuf16;
 #pragma unroll
             for (int part = 0; part < 2; ++part) {
-                if (!wait_phase(&sm->p_ready[s][part], i & 1, p, sm))
-                    return false;
+                wait_phase(&sm->p_ready[s][part], i & 1, p, sm);
                 tcgen05_fence_after();
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {   // 16 keys a step, hi then lo
                     const int c = (j >> 1) * 2 + part, k = 2 * c + (j & 1);   // chunk of 32 keys; step
-                    const uint64_t d = vs + k * 2 * TL::kGroup / 16;
-                    mma_ts(pa + 128, pa + 32 * c + 8 * (j & 1), d, id_o, i > 0 || part > 0 || j > 0, leader);
-                    mma_ts(pa + 128, pa + 32 * c + 16 + 8 * (j & 1), d, id_o, 1, leader);
+                    const uint32_t vk = va + k * 2 * TL::kGroup / 16;
+                    mma_ts(pa + 128, pa + 32 * c + 8 * (j & 1), vk, kv_hi, id_o, i > 0 || part > 0 || j > 0, leader);
+                    mma_ts(pa + 128, pa + 32 * c + 16 + 8 * (j & 1), vk, kv_hi, id_o, 1, leader);
                 }
             }
             if (!two || s == 1) {
+                tcgen05_commit(smem_addr(&sm->empty[v_at.slot]), leader);
                 v_at.advance(v_tile == n - 2 ? 1 : 2);
                 ++v_tile;
             }
             if (last)
                 tcgen05_commit(smem_addr(&sm->o_done[s]), leader);
-            return true;
         };
-        go = go && scores(0);
+        scores(0);
         if (steps1 > 0)
-            go = go && scores(1);
-        for (int i = 0; i < steps0 && go; ++i) {
-            go = values(0, i, i == steps0 - 1);
+            scores(1);
+        for (int i = 0; i < steps0; ++i) {
+            values(0, i, i == steps0 - 1);
             if (i + 1 < steps0)
-                go = go && scores(0);
+                scores(0);
             if (i < steps1)
-                go = go && values(1, i, i == steps1 - 1);
+                values(1, i, i == steps1 - 1);
             if (i + 1 < steps1)
-                go = go && scores(1);
+                scores(1);
         }
         // whatever the others saw, the products in flight end before tensor
         // memory is freed
@@ -697,9 +727,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // FP8: weights are 2^7 times larger, which keeps seven more bits of the
         // small ones in f16; it cancels in O
         constexpr float kBias = kFp8 ? 7.f : 0.f;
-        // One lane frees the buffers of the products that s_full shows done: the
-        // step's K, and the V of the step before.
-        const bool frees = (half == 0 && quad == 0 && lane == 0) && (!two || s == 1);
         float m_ref = -INFINITY, l = 0.f;   // what the weights refer to (a raw score), their sum
         float most = 0.f;                   // FP8: the largest weight
         bool go = ok;
@@ -762,11 +789,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (go) {
                 tcgen05_fence_after();
                 tmem_ld32(s_col, r0);
-                if (frees) {
-                    mbar_arrive(smem_addr(&sm->empty[(t == 0 ? 0 : 2 * t - 1) % nw]));
-                    if (i > 0)   // V of tile t - 1, or t - 2 (every other one)
-                        mbar_arrive(smem_addr(&sm->empty[(two ? 2 * t : 2 * t - 2) % nw]));
-                }
                 tmem_wait_ld();
                 settle(r0);
                 tmem_ld32(s_col + 32, r1);

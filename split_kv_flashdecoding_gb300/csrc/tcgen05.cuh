@@ -54,10 +54,16 @@ __device__ __forceinline__ void tcgen05_commit(uint32_t bar, uint32_t leader)
 //  K-major operand: 8-row groups of 128-byte rows `sbo` apart (lbo unused).
 //  MN-major operand: 128-byte rows of 64 MN elements, one row per K index;
 //    8-row groups of K `sbo` apart, blocks of 64 MN elements `lbo` apart.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo)
+// In two words: the first counts 16 bytes in its low bits, so that an operand
+// further on is the first word plus a constant.
+__device__ __forceinline__ uint32_t smem_desc_lo(uint32_t addr, uint32_t lbo)
 {
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | ((uint64_t)(lbo >> 4) << 16) | ((uint64_t)(sbo >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
+    return ((addr & 0x3FFFF) >> 4) | ((lbo >> 4) << 16);
+}
+
+__host__ __device__ constexpr uint32_t smem_desc_hi(uint32_t sbo)
+{
+    return (sbo >> 4) | (1u << 14) | (2u << 29);
 }
 
 // Instruction descriptor of kind::f16 with fp32 accumulation, M x N tile.
@@ -68,25 +74,28 @@ __host__ __device__ constexpr uint32_t mma_idesc(int m, int n, bool bf16, bool b
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
 }
 
-// D (+)= A B, A and B in shared memory; accumulate: 0 overwrites D.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
-                                       uint32_t leader)
+// D (+)= A B, A and B in shared memory (descriptor words); accumulate: 0
+// overwrites D.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t accumulate, uint32_t leader)
 {
     asm volatile(
-        "{\n\t.reg .pred p, l;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 l, %5, 0;\n\t"
-        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+        "{\n\t.reg .pred p, l;\n\t.reg .b64 a, b;\n\tsetp.ne.u32 p, %6, 0;\n\tsetp.ne.u32 l, %7, 0;\n\t"
+        "mov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
 
 // D (+)= A B, A in tensor memory (two 16-bit elements a column), B in shared.
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate,
-                                       uint32_t leader)
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                                       uint32_t accumulate, uint32_t leader)
 {
     asm volatile(
-        "{\n\t.reg .pred p, l;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 l, %5, 0;\n\t"
-        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader)
+        "{\n\t.reg .pred p, l;\n\t.reg .b64 b;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 l, %6, 0;\n\t"
+        "mov.b64 b, {%2, %3};\n\t"
+        "@l tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(leader)
         : "memory");
 }
 
