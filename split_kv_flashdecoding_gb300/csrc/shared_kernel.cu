@@ -20,7 +20,7 @@ cudaError_t launch_prefixes(const SharedMaps &maps, const SharedParams &p, cudaS
         if (dev < 64)
             configured[dev] = true;
     }
-    return launch_dependent(shared_kernel<PAGED, DT>, dim3((unsigned)p.num_items), kThreads, kSharedAlloc, stream,
+    return launch_dependent(shared_kernel<PAGED, DT>, dim3((unsigned)p.num_items), kThreads<DT>, kSharedAlloc, stream,
                             maps.k, maps.v, p);
 }
 

@@ -21,7 +21,7 @@
 // output by more than its fp32 type says): three products of 128 x 128 x 128 a
 // tile for the two that the definition has.
 //
-// FP8 K and V: the products are in f16 (every E4M3 value is an f16 value); two
+// FP8 K and V: the products are in f16 (every E4M3 value is an f16 value); four
 // warps widen each raw tile into an operand tile in shared memory, and q
 // rows are scaled into f16 by a power of two.
 //
@@ -29,7 +29,7 @@
 // keys; a thread owns a row and 64 of its scores (tcgen05.ld gives it the row's
 // columns).  16 the producer (TMA), 17 issues the products of both streams in
 // turn (a warp for each let the two streams' products run through one another:
-// both then ended late, 359 us for 296 us), 18 and 19 do the widening (FP8).
+// both then ended late, 359 us for 296 us), 18-21 do the widening (FP8).
 //
 // The reference m of a row's weights only has to keep them in their type's
 // range: the weights are floating-point numbers, their size costs no accuracy.
@@ -59,13 +59,14 @@ namespace {
 constexpr int kBufBytes = kSharedTile * kHeadDim * 2;   // a K, V or Q tile of 16-bit values: 32 KB
 constexpr int kHalfBytes = kBufBytes / 2;
 constexpr int kBuffers = 7;                             // Q tiles and rings together
-constexpr int kWideBuffers = 3;                         // FP8: operand tiles; the rest of the ring is raw
+constexpr int kWideBuffers = 4;                         // FP8: operand tiles; the rest of the ring is raw
 constexpr int kRawBytes = kBufBytes / 2;                // FP8: a raw tile
 constexpr int kMaxRing = 6;
 constexpr int kSoftmaxThreads = 512;
 constexpr int kStreamWarps = 8;
-constexpr int kProducerWarp = 16, kMmaWarp = 17, kWidenWarp = 18, kWidenWarps = 2;
-constexpr int kThreads = 640;
+constexpr int kProducerWarp = 16, kMmaWarp = 17, kWidenWarp = 18, kWidenWarps = 4;
+template <int DT>
+constexpr int kThreads = DT == kKvTypeFp8 ? 704 : 640;
 constexpr int kTmemCols = 512;
 constexpr int kStreamCols = 256;                        // S (and P over it) 128, O 128
 // Careful steps: log2 of the growth of a row's maximum that raises m.
@@ -313,7 +314,7 @@ struct TileLayout {
 };
 
 template <bool PAGED, int DT>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<DT>, 1)
     shared_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ SharedParams p)
 {
@@ -566,10 +567,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 tcgen05_fence_after();
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {   // 16 keys a step, hi then lo
-                    const int c = (j >> 1) * 2 + part, k = 2 * c + (j & 1);   // chunk of 32 keys; step
+                    const int k = (j >> 1) * 4 + part * 2 + (j & 1);
                     const uint32_t vk = va + k * 2 * TL::kGroup / 16;
-                    mma_ts(pa + 128, pa + 32 * c + 8 * (j & 1), vk, kv_hi, id_o, i > 0 || part > 0 || j > 0, leader);
-                    mma_ts(pa + 128, pa + 32 * c + 16 + 8 * (j & 1), vk, kv_hi, id_o, 1, leader);
+                    mma_ts(pa + 128, pa + 16 * k, vk, kv_hi, id_o, i > 0 || part > 0 || j > 0, leader);
+                    mma_ts(pa + 128, pa + 16 * k + 8, vk, kv_hi, id_o, 1, leader);
                 }
             }
             if (!two || s == 1) {
@@ -597,7 +598,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tcgen05_commit(smem_addr(&sm->drain), leader);
         mbar_wait(smem_addr(&sm->drain), 0, kDrainTimeoutNs);
         __syncwarp();
-    } else if (kFp8 && warp >= kWidenWarp && ok) {
+    } else if (kFp8 && warp >= kWidenWarp && warp < kWidenWarp + kWidenWarps && ok) {
         // ------------------------------------- FP8: raw tiles to f16 operands
         // A warp takes 8 rows at a time, 16 values a lane: a raw row is 8 chunks
         // of 16 bytes, chunk c at c ^ (row % 8), and becomes two chunks of the
@@ -605,6 +606,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         // r ^ 5 and four chunks of a half, which meet no bank twice on either side.
         const uint8_t *raw0 = ring_ptr + kWideBuffers * kBufBytes;
         const int ph = lane >> 3, r8 = ph ^ (((lane >> 2) & 1) * 5), cc = lane & 3;
+        constexpr int kWarpRows = kSharedTile / kWidenWarps;
+        const int row0 = (warp - kWidenWarp) * kWarpRows + r8;   // the lane's first row of a tile
+        // the lane's chunk within its 8-row group: raw, and the first of its two of the operand
+        const uint32_t lane_src = r8 * 128 + ((cc ^ r8) << 4), lane_dst = r8 * 128 + (((2 * cc) ^ r8) << 4);
         Place from(0, nb), to(0, kWideBuffers);
         for (int pos = 0; pos < 2 * n; ++pos, from.advance(1), to.advance(1)) {
             bool is_k;
@@ -615,29 +620,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 go = wait_phase(&sm->empty[to.slot], to.phase ^ 1, p, sm);
             if (!__all_sync(0xffffffffu, go))
                 break;
-            const uint8_t *src = raw0 + from.slot * kRawBytes;
-            uint8_t *dst = ring_ptr + to.slot * kBufBytes;
-#pragma unroll 4
-            for (int j = 0; j < 32 / kWidenWarps; ++j) {   // group of 8 rows, half
-                const int g = (warp - kWidenWarp) * (16 / kWidenWarps) + (j >> 1), half = j & 1;
-                const int row = 8 * g + r8;
-                const uint4 x = *reinterpret_cast<const uint4 *>(src + row * 128 + (((4 * half + cc) ^ r8) << 4));
-                const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                uint32_t f[8];
+            const uint8_t *src = raw0 + from.slot * kRawBytes + (warp - kWidenWarp) * kWarpRows * 128;
+            uint8_t *dst = ring_ptr + to.slot * kBufBytes + (warp - kWidenWarp) * kWarpRows * 128;
+            constexpr int kBatch = 2;   // raw chunks of a lane in flight
+            const int first = is_k ? kSharedTile : valid;   // V rows from here on are past the last key
+#pragma unroll 1
+            for (int j0 = 0; j0 < 32 / kWidenWarps; j0 += kBatch) {
+                uint4 x[kBatch];
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-                        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-                        : "=r"(f[2 * q]), "=r"(f[2 * q + 1])
-                        : "r"(w[q]));
-                if (!is_k && row >= valid) {   // rows past the last key
+                for (int j = 0; j < kBatch; ++j)
+                    x[j] = *reinterpret_cast<const uint4 *>(src + (j0 + j) / 2 * 1024 + ((4 * (j & 1)) << 4 ^ lane_src));
 #pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        f[q] = 0u;
+                for (int j = 0; j < kBatch; ++j) {
+                    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                    uint32_t f[8];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+                            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+                            : "=r"(f[2 * q]), "=r"(f[2 * q + 1])
+                            : "r"(w[q]));
+                    if (row0 + (j0 + j) / 2 * 8 >= first) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            f[q] = 0u;
+                    }
+                    uint8_t *d = dst + (j & 1) * kHalfBytes + (j0 + j) / 2 * 1024;
+                    *reinterpret_cast<uint4 *>(d + lane_dst) = make_uint4(f[0], f[1], f[2], f[3]);
+                    *reinterpret_cast<uint4 *>(d + (lane_dst ^ 16)) = make_uint4(f[4], f[5], f[6], f[7]);
                 }
-                uint8_t *d = dst + half * kHalfBytes + row * 128;
-                *reinterpret_cast<uint4 *>(d + (((2 * cc) ^ r8) << 4)) = make_uint4(f[0], f[1], f[2], f[3]);
-                *reinterpret_cast<uint4 *>(d + (((2 * cc + 1) ^ r8) << 4)) = make_uint4(f[4], f[5], f[6], f[7]);
             }
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             __syncwarp();
@@ -730,27 +741,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         float m_ref = -INFINITY, l = 0.f;   // what the weights refer to (a raw score), their sum
         float most = 0.f;                   // FP8: the largest weight
         bool go = ok;
-        // 32 scores to weights: hi in the first 16 of their columns, lo in the others
-        auto weights = [&](const uint32_t (&r)[32], uint32_t col, float off, float2 &sum) {
+        // 16 scores to weights, over their columns: hi in the first 8, lo in the others
+        auto weights = [&](const uint32_t (&r)[16], int j16, float off, float2 &sum) {
             const float2 c22 = make_float2(c2, c2), off2 = make_float2(off, off);
+            uint32_t hi[8], lo[8];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t hi[8], lo[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 x = fma2(make_float2(__uint_as_float(r[16 * q + 2 * j]),
-                                                      __uint_as_float(r[16 * q + 2 * j + 1])), c22, off2);
-                    const float2 w = make_float2(ex2(x.x), ex2(x.y));
-                    sum = add2(sum, w);
-                    if constexpr (kFp8)
-                        most = fmaxf(most, fmaxf(w.x, w.y));
-                    hi[j] = pack2<DT>(w);
-                    const float2 h = unpack2<DT>(hi[j]);
-                    lo[j] = pack2<DT>(fma2(h, make_float2(-1.f, -1.f), w));
-                }
-                tmem_st8(col + 8 * q, hi);
-                tmem_st8(col + 16 + 8 * q, lo);
+            for (int j = 0; j < 8; ++j) {
+                const float2 x = fma2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), c22, off2);
+                const float2 w = make_float2(ex2(x.x), ex2(x.y));
+                sum = add2(sum, w);
+                if constexpr (kFp8)
+                    most = fmaxf(most, fmaxf(w.x, w.y));
+                hi[j] = pack2<DT>(w);
+                const float2 h = unpack2<DT>(hi[j]);
+                lo[j] = pack2<DT>(fma2(h, make_float2(-1.f, -1.f), w));
             }
+            tmem_st8(s_col + 16 * j16, hi);
+            tmem_st8(s_col + 16 * j16 + 8, lo);
         };
         auto publish = [&](int part) {
             tmem_wait_st();
@@ -759,23 +766,34 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (lane == 0)
                 mbar_arrive(smem_addr(&sm->p_ready[s][part]));
         };
-        auto mask = [&](uint32_t (&r)[32], int valid) {   // scores past the last key
-            if (valid < 32) {
+        auto load = [&](uint32_t (&r)[16], int j16) { tmem_ld16(s_col + 16 * j16, r); };
+        auto ready = [&](uint32_t (&r)[16], int valid) {   // loaded, scores past the last key masked
+            tmem_wait_ld();
+            settle(r);
+            if (valid < 16) {
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
+                for (int j = 0; j < 16; ++j)
                     if (j >= valid)
                         r[j] = 0xff800000u;
             }
         };
-        auto largest = [](const uint32_t (&r0)[32], const uint32_t (&r1)[32]) {
-            float mx[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                mx[j] = fmaxf(__uint_as_float(r0[j]), __uint_as_float(r1[j]));
-#pragma unroll
-            for (int j = 4; j < 32; ++j)
-                mx[j & 3] = fmaxf(fmaxf(mx[j & 3], __uint_as_float(r0[j])), __uint_as_float(r1[j]));
-            return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        // All 64 scores to weights, the next 16 on their way meanwhile.
+        auto step = [&](uint32_t (&r0)[16], uint32_t (&r1)[16], int valid, float off) {   // r0: loaded
+            float2 sum = make_float2(0.f, 0.f);
+            ready(r0, valid);
+            load(r1, 1);
+            weights(r0, 0, off, sum);
+            ready(r1, valid - 16);
+            load(r0, 2);
+            weights(r1, 1, off, sum);
+            publish(0);
+            ready(r0, valid - 32);
+            load(r1, 3);
+            weights(r0, 2, off, sum);
+            ready(r1, valid - 48);
+            weights(r1, 3, off, sum);
+            publish(1);
+            l += sum.x + sum.y;
         };
         for (int i = 0; i < steps(s); ++i) {
             // After an error the steps go on without work, so that the barriers
@@ -784,28 +802,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 go = __all_sync(0xffffffffu, wait_phase(&sm->s_full[s], i & 1, p, sm));
             const int t = two ? i : 2 * i + s;
             const int valid = sm->keys - t * kSharedTile - half * 64;
-            float2 sum = make_float2(0.f, 0.f);
-            uint32_t r0[32], r1[32];
-            if (go) {
-                tcgen05_fence_after();
-                tmem_ld32(s_col, r0);
-                tmem_wait_ld();
-                settle(r0);
-                tmem_ld32(s_col + 32, r1);
-                mask(r0, valid);
-            }
+            uint32_t r0[16], r1[16];
             if (i > 0 && !careful) {
-                if (!go)
-                    continue;
-                const float off = kBias - m_ref * c2;
-                weights(r0, s_col, off, sum);
-                publish(0);
-                tmem_wait_ld();
-                settle(r1);
-                mask(r1, valid - 32);
-                weights(r1, s_col + 32, off, sum);
-                publish(1);
-                l += sum.x + sum.y;
+                if (go) {
+                    tcgen05_fence_after();
+                    load(r0, 0);
+                    step(r0, r1, valid, kBias - m_ref * c2);
+                }
                 continue;
             }
             // The first step, and every careful one: a row's maximum is that of
@@ -813,10 +816,15 @@ __global__ void __launch_bounds__(kThreads, 1)
             float mt = -INFINITY;
             bool raise = false;
             if (go) {
-                tmem_wait_ld();
-                settle(r1);
-                mask(r1, valid - 32);
-                mt = largest(r0, r1);
+                tcgen05_fence_after();
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    load(r0, c);
+                    ready(r0, valid - 16 * c);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        mt = fmaxf(mt, __uint_as_float(r0[j]));
+                }
                 raise = mt > m_ref && (m_ref == -INFINITY || (mt - m_ref) * c2 > kRaise);
             }
             if (barrier_or(pair_bar, 64, raise)) {
@@ -845,13 +853,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             if (!go)
                 continue;
+            load(r0, 0);
             // a row whose scores are all -inf so far keeps weights of 0
-            const float off = (m_ref == -INFINITY ? 0.f : -m_ref * c2) + kBias;
-            weights(r0, s_col, off, sum);
-            publish(0);
-            weights(r1, s_col + 32, off, sum);
-            publish(1);
-            l += sum.x + sum.y;
+            step(r0, r1, valid, (m_ref == -INFINITY ? 0.f : -m_ref * c2) + kBias);
         }
         // Out of range: a weight too large for its type, or no score to refer to
         // in the first tile.
