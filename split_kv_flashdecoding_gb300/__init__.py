@@ -552,17 +552,16 @@ def _on(tensor):
     return _SAME if tensor.get_device() == torch.cuda.current_device() else torch.cuda.device(tensor.device)
 
 
-def _need(what: str, t, dtype, like=None):
-    """t is a contiguous CUDA tensor of this type (and on `like`'s device)."""
-    if t.dtype is not dtype or not t.is_cuda or not t.is_contiguous() or \
-            (like is not None and t.get_device() != like.get_device()):
-        raise FdError(-1, f"{what} must be a contiguous {dtype} CUDA tensor on the inputs' device")
-    return t.data_ptr()
+def _need(what: str, t, dtype, dev: int) -> int:
+    """Address of t, a contiguous tensor of this type on CUDA device `dev`."""
+    if t.dtype is dtype and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise FdError(-1, f"{what} must be a contiguous {dtype} CUDA tensor on the inputs' device")
 
 
-def _ws(workspace, like):
+def _ws(workspace, dev: int):
     """(address, bytes) of a workspace on the inputs' device."""
-    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.get_device() != like.get_device():
+    if workspace.get_device() != dev or not workspace.is_contiguous():
         raise FdError(-3, "workspace must be a contiguous CUDA tensor on the inputs' device")
     return workspace.data_ptr(), workspace.nbytes
 
@@ -584,9 +583,9 @@ def plan_rope(head_dim: int, rotary_dim: int, *, interleaved: bool = False, base
     return info
 
 
-def _heads(what: str, x):
+def _heads(what: str, x, dev: int):
     """Token stride (elements) of a bf16 [N, H, D] CUDA tensor with contiguous heads."""
-    if x.dtype is torch.bfloat16 and x.is_cuda and x.dim() == 3:
+    if x.dtype is torch.bfloat16 and x.get_device() == dev and x.dim() == 3:
         n, h, d = x.shape
         token, head, value = x.stride()
         if (value == 1 and (head == d or h <= 1)) or n * h * d == 0:
@@ -609,8 +608,8 @@ def _append(name, pool_dtypes, per_row, q, k, v, k_pages, v_pages, append_indptr
         raise FdError(-1, f"{name}: kv_page_indptr must have batch+1 and kv_last_page_len batch entries")
     if positions is not None and positions.numel() < N:
         raise FdError(-1, f"{name}: positions must have an entry for every token")
-    num_pages, page_size = k_pages.shape[0], k_pages.shape[1]
-    i32 = torch.int32
+    num_pages, page_size = k_pages.shape[:2]
+    i32, dev = torch.int32, k.get_device()
     with _on(k):
         if q is not None and q_out is None:
             q_out = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
@@ -620,14 +619,14 @@ def _append(name, pool_dtypes, per_row, q, k, v, k_pages, v_pages, append_indptr
             workspace = torch.zeros(WORKSPACE_HEADER_BYTES, dtype=torch.uint8, device=k.device)
         _check(getattr(lib(), name)(
             B, N, Hq, Hkv, D, page_size, num_pages, None if rope is None else ctypes.byref(rope),
-            _ptr(q), 0 if q is None else _heads("q", q), _ptr(k), _heads("k", k), _ptr(v), _heads("v", v),
-            _need("append_indptr", append_indptr, i32, k), _need("kv_page_indptr", kv_page_indptr, i32, k),
-            _need("kv_last_page_len", kv_last_page_len, i32, k),
-            _need("kv_page_indices", kv_page_indices, i32, k), kv_page_indices.numel(),
-            None if positions is None else _need("positions", positions, i32, k),
-            None if q is None else q_out.data_ptr(), 0 if q is None else _heads("q_out", q_out),
-            _need("k_pages", k_pages, k_pages.dtype, k), _need("v_pages", v_pages, v_pages.dtype, k),
-            *scales, *_ws(workspace, k), _stream(stream)), name)
+            _ptr(q), 0 if q is None else _heads("q", q, dev), _ptr(k), _heads("k", k, dev), _ptr(v), _heads("v", v, dev),
+            _need("append_indptr", append_indptr, i32, dev), _need("kv_page_indptr", kv_page_indptr, i32, dev),
+            _need("kv_last_page_len", kv_last_page_len, i32, dev),
+            _need("kv_page_indices", kv_page_indices, i32, dev), kv_page_indices.numel(),
+            None if positions is None else _need("positions", positions, i32, dev),
+            None if q is None else q_out.data_ptr(), 0 if q is None else _heads("q_out", q_out, dev),
+            _need("k_pages", k_pages, k_pages.dtype, dev), _need("v_pages", v_pages, v_pages.dtype, dev),
+            *scales, *_ws(workspace, dev), _stream(stream)), name)
     return q_out
 
 
@@ -654,7 +653,7 @@ def append_paged_fp8(q, k, v, k_pages_fp8, v_pages_fp8, k_scale, v_scale, append
     return _append("fd_append_paged_fp8", (torch.uint8, torch.float8_e4m3fn), 1, q, k, v, k_pages_fp8,
                    v_pages_fp8, append_indptr, kv_page_indptr, kv_last_page_len, kv_page_indices, rope,
                    positions, q_out, workspace, stream,
-                   (_need("k_scale", k_scale, f32, k), _need("v_scale", v_scale, f32, k)))
+                   (_need("k_scale", k_scale, f32, k.get_device()), _need("v_scale", v_scale, f32, k.get_device())))
 
 
 def append_paged_int4(q, k, v, k_pages_int4, v_pages_int4, k_scale, v_scale, append_indptr,
@@ -669,7 +668,7 @@ def append_paged_int4(q, k, v, k_pages_int4, v_pages_int4, k_scale, v_scale, app
         raise FdError(-1, "fd_append_paged_int4: scales must be [Hkv, num_pages * page_size]")
     return _append("fd_append_paged_int4", (torch.uint8,), 0.5, q, k, v, k_pages_int4, v_pages_int4,
                    append_indptr, kv_page_indptr, kv_last_page_len, kv_page_indices, rope, positions, q_out,
-                   workspace, stream, (_need("k_scale", k_scale, f32, k), _need("v_scale", v_scale, f32, k)))
+                   workspace, stream, (_need("k_scale", k_scale, f32, k.get_device()), _need("v_scale", v_scale, f32, k.get_device())))
 
 
 def pages_workspace_bytes(num_pages: int, new_batch: int = 0) -> int:
@@ -680,13 +679,6 @@ def pages_workspace_bytes(num_pages: int, new_batch: int = 0) -> int:
     return out.value
 
 
-def _int32_outputs(like, given, sizes):
-    """The given outputs, the missing ones in one new buffer."""
-    sizes = [0 if g is not None else n for g, n in zip(given, sizes)]
-    new = torch.empty(sum(sizes), dtype=torch.int32, device=like.device).split(sizes)
-    return [n if g is None else g for g, n in zip(given, new)]
-
-
 def fork_pages(parent, kv_page_indptr, kv_last_page_len, kv_page_indices, new_page_indptr,
                new_page_entries: int, page_size: int, page_refs, *, new_page_indices=None,
                new_page_refs=None, copy_src=None, copy_dst=None, workspace=None, stream=None):
@@ -694,28 +686,30 @@ def fork_pages(parent, kv_page_indptr, kv_last_page_len, kv_page_indices, new_pa
     tensors; new_page_entries = new_page_indptr[-1], known to the host) ->
     (new_page_indices, new_page_refs, copy_src, copy_dst); hand the last two to
     copy_pages."""
-    i32, like = torch.int32, page_refs
+    i32, like, dev = torch.int32, page_refs, page_refs.get_device()
     n_new, n_old, pages = parent.numel(), kv_page_indptr.numel() - 1, page_refs.numel()
     if new_page_indptr.numel() != n_new + 1 or kv_last_page_len.numel() < n_old:
         raise FdError(-1, "fd_fork_pages: new_page_indptr must have new_batch+1 and kv_last_page_len batch entries")
     with _on(like):
-        new_page_indices, new_page_refs, copy_src, copy_dst = _int32_outputs(
-            like, (new_page_indices, new_page_refs, copy_src, copy_dst),
-            (new_page_entries, pages, n_new, n_new))
+        new = like.new_empty
+        new_page_indices = new(new_page_entries) if new_page_indices is None else new_page_indices
+        new_page_refs = new(pages) if new_page_refs is None else new_page_refs
+        copy_src = new(n_new) if copy_src is None else copy_src
+        copy_dst = new(n_new) if copy_dst is None else copy_dst
         if new_page_indices.numel() < new_page_entries or new_page_refs.numel() != pages or \
                 copy_src.numel() < n_new or copy_dst.numel() < n_new:
             raise FdError(-1, "fd_fork_pages: an output is too small")
         if workspace is None:
             workspace = torch.zeros(pages_workspace_bytes(pages, n_new), dtype=torch.uint8, device=like.device)
         _check(lib().fd_fork_pages(
-            n_old, n_new, page_size, pages, _need("parent", parent, i32, like),
-            _need("kv_page_indptr", kv_page_indptr, i32, like),
-            _need("kv_last_page_len", kv_last_page_len, i32, like),
-            _need("kv_page_indices", kv_page_indices, i32, like), kv_page_indices.numel(),
-            _need("new_page_indptr", new_page_indptr, i32, like), new_page_entries,
-            _need("page_refs", page_refs, i32, like), _need("new_page_indices", new_page_indices, i32, like),
-            _need("new_page_refs", new_page_refs, i32, like), _need("copy_src", copy_src, i32, like),
-            _need("copy_dst", copy_dst, i32, like), *_ws(workspace, like),
+            n_old, n_new, page_size, pages, _need("parent", parent, i32, dev),
+            _need("kv_page_indptr", kv_page_indptr, i32, dev),
+            _need("kv_last_page_len", kv_last_page_len, i32, dev),
+            _need("kv_page_indices", kv_page_indices, i32, dev), kv_page_indices.numel(),
+            _need("new_page_indptr", new_page_indptr, i32, dev), new_page_entries,
+            _need("page_refs", page_refs, i32, dev), _need("new_page_indices", new_page_indices, i32, dev),
+            _need("new_page_refs", new_page_refs, i32, dev), _need("copy_src", copy_src, i32, dev),
+            _need("copy_dst", copy_dst, i32, dev), *_ws(workspace, dev),
             _stream(stream)), "fd_fork_pages")
     return new_page_indices, new_page_refs, copy_src, copy_dst
 
@@ -725,23 +719,25 @@ def compact_pages(page_refs, kv_page_indices, max_moves: int, *, limit: int = 0,
     """fd_compact_pages: rename the pages in use at or behind `limit` (0: the
     number in use) to the lowest free ones -> (new_page_indices, new_page_refs,
     copy_src, copy_dst); hand the last two (max_moves entries) to copy_pages."""
-    i32, like = torch.int32, page_refs
+    i32, like, dev = torch.int32, page_refs, page_refs.get_device()
     pages, entries = page_refs.numel(), kv_page_indices.numel()
     with _on(like):
-        new_page_indices, new_page_refs, copy_src, copy_dst = _int32_outputs(
-            like, (new_page_indices, new_page_refs, copy_src, copy_dst),
-            (entries, pages, max_moves, max_moves))
+        new = like.new_empty
+        new_page_indices = new(entries) if new_page_indices is None else new_page_indices
+        new_page_refs = new(pages) if new_page_refs is None else new_page_refs
+        copy_src = new(max_moves) if copy_src is None else copy_src
+        copy_dst = new(max_moves) if copy_dst is None else copy_dst
         if new_page_indices.numel() < entries or new_page_refs.numel() != pages or \
                 copy_src.numel() < max_moves or copy_dst.numel() < max_moves:
             raise FdError(-1, "fd_compact_pages: an output is too small")
         if workspace is None:
             workspace = torch.zeros(pages_workspace_bytes(pages), dtype=torch.uint8, device=like.device)
         _check(lib().fd_compact_pages(
-            pages, _need("page_refs", page_refs, i32, like),
-            _need("kv_page_indices", kv_page_indices, i32, like), entries, int(limit), int(max_moves),
-            _need("new_page_indices", new_page_indices, i32, like),
-            _need("new_page_refs", new_page_refs, i32, like), _need("copy_src", copy_src, i32, like),
-            _need("copy_dst", copy_dst, i32, like), *_ws(workspace, like),
+            pages, _need("page_refs", page_refs, i32, dev),
+            _need("kv_page_indices", kv_page_indices, i32, dev), entries, int(limit), int(max_moves),
+            _need("new_page_indices", new_page_indices, i32, dev),
+            _need("new_page_refs", new_page_refs, i32, dev), _need("copy_src", copy_src, i32, dev),
+            _need("copy_dst", copy_dst, i32, dev), *_ws(workspace, dev),
             _stream(stream)), "fd_compact_pages")
     return new_page_indices, new_page_refs, copy_src, copy_dst
 
@@ -753,23 +749,21 @@ def copy_pages(pools, src, dst, *, workspace=None, stream=None):
     ``*scales.view(Hkv, num_pages, page_size)``)."""
     if not pools or src.numel() == 0:
         return
-    pages, n = pools[0].shape[0], len(pools)
+    pages, n, dev = pools[0].shape[0], len(pools), src.get_device()
     if dst.numel() != src.numel():
         raise FdError(-1, "fd_copy_pages: src and dst must have the same length")
-    device = src.get_device()
-    for x in pools:
-        if not x.is_cuda or x.get_device() != device or x.shape[0] != pages or not x.is_contiguous():
+    ptrs, size = (ctypes.c_void_p * n)(), (ctypes.c_int64 * n)()
+    for i, x in enumerate(pools):
+        if x.get_device() != dev or dev < 0 or x.shape[0] != pages or not x.is_contiguous():
             raise FdError(-1, "fd_copy_pages: pools must be contiguous CUDA tensors of as many pages, on one device")
+        ptrs[i], size[i] = x.data_ptr(), x.nbytes // max(pages, 1)
     if pages == 0:
         return
-    ptrs = (ctypes.c_void_p * n)(*[x.data_ptr() for x in pools])
-    size = (ctypes.c_int64 * n)(*[x.nbytes // pages for x in pools])
     with _on(src):
-        _check(lib().fd_copy_pages(n, ptrs, size, pages, src.numel(), _need("src", src, torch.int32),
-                                   _need("dst", dst, torch.int32, src),
-                                   *((None, 0) if workspace is None else _ws(workspace, src)),
+        _check(lib().fd_copy_pages(n, ptrs, size, pages, src.numel(), _need("src", src, torch.int32, dev),
+                                   _need("dst", dst, torch.int32, dev),
+                                   *((None, 0) if workspace is None else _ws(workspace, dev)),
                                    _stream(stream)), "fd_copy_pages")
-
 
 def _host_ptr(a):
     return a.ctypes.data_as(ctypes.c_void_p)
@@ -814,32 +808,37 @@ def _shared_outputs(name, plan_, q, kv, o, lse, workspace):
     """Shapes of a decode_shared call; allocates what was not given."""
     s = plan_.suffix
     shape = (s.batch, s.num_qo_heads, s.head_dim)
-    if tuple(q.shape) != shape or any(x is not None and (x.shape[-2] != s.num_kv_heads or
-                                                         x.shape[-1] != s.head_dim) for x in kv):
-        raise FdError(-1, f"{name}: q or K/V are not of the plan's heads")
+    heads = (s.num_kv_heads, s.head_dim)
+    if q.shape != shape:
+        raise FdError(-1, f"{name}: q is not of the plan's heads")
+    for x in kv:
+        if x is not None and x.shape[-2:] != heads:
+            raise FdError(-1, f"{name}: K/V are not of the plan's heads")
     if o is None:
         o = torch.empty(shape, dtype=torch.float32, device=q.device)
+    elif o.shape != shape:
+        raise FdError(-1, f"{name}: o of another shape than q")
     if lse is None:
         lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device)
+    elif lse.shape != shape[:2]:
+        raise FdError(-1, f"{name}: lse must be [batch, num_qo_heads]")
     if workspace is None:
         workspace = torch.zeros(plan_.workspace_bytes, dtype=torch.uint8, device=q.device)
-    if o.numel() != q.numel() or lse.numel() != shape[0] * shape[1]:
-        raise FdError(-1, f"{name}: o or lse of another size")
-    return o, lse, workspace
+    return o, lse, workspace, s.batch, s.total_tokens
 
 
-def _maybe(what, t, dtype, like):
-    return None if t is None else _need(what, t, dtype, like)
+def _maybe(what, t, dtype, dev):
+    return None if t is None else _need(what, t, dtype, dev)
 
 
 def _decode_shared(name, kv_dtypes, plan_, q, k_prefix, v_prefix, k, v, scales, prefix_req_indptr,
                    prefix_indptr, kv_indptr, scale, o, lse, workspace, stream):
-    i32 = torch.int32
+    i32, dev = torch.int32, q.get_device()
     with _on(q):
-        o, lse, workspace = _shared_outputs(name, plan_, q, (k_prefix, v_prefix, k, v), o, lse, workspace)
-        P, room = plan_.num_prefixes, plan_.suffix.total_tokens
+        o, lse, workspace, B, room = _shared_outputs(name, plan_, q, (k_prefix, v_prefix, k, v), o, lse, workspace)
+        P = plan_.num_prefixes
         if prefix_req_indptr.numel() != P + 1 or prefix_indptr.numel() != P + 1 or \
-                (room and (kv_indptr is None or kv_indptr.numel() != plan_.suffix.batch + 1)):
+                (room and (kv_indptr is None or kv_indptr.numel() != B + 1)):
             raise FdError(-1, f"{name}: tables of another length than the plan's")
         if plan_.num_items and (k_prefix.shape[0] < plan_.prefix_rows or v_prefix.shape[0] < plan_.prefix_rows) or \
                 (room and (k is None or v is None or k.shape[0] < room or v.shape[0] < room)):
@@ -848,11 +847,11 @@ def _decode_shared(name, kv_dtypes, plan_, q, k_prefix, v_prefix, k, v, scales, 
             if x is not None and x.dtype not in kv_dtypes:
                 raise FdError(-1, f"{name}: K/V of another type")
         _check(getattr(lib(), name)(
-            ctypes.byref(plan_), _need("prefix_req_indptr", prefix_req_indptr, i32, q),
-            _need("prefix_indptr", prefix_indptr, i32, q), _maybe("kv_indptr", kv_indptr, i32, q),
-            _need("q", q, torch.bfloat16), *[None if x is None else _need("K/V", x, x.dtype, q)
+            ctypes.byref(plan_), _need("prefix_req_indptr", prefix_req_indptr, i32, dev),
+            _need("prefix_indptr", prefix_indptr, i32, dev), _maybe("kv_indptr", kv_indptr, i32, dev),
+            _need("q", q, torch.bfloat16, dev), *[None if x is None else _need("K/V", x, x.dtype, dev)
                                              for x in (k_prefix, v_prefix, k, v)], *scales, float(scale),
-            _need("o", o, torch.float32, q), _need("lse", lse, torch.float32, q), *_ws(workspace, q),
+            _need("o", o, torch.float32, dev), _need("lse", lse, torch.float32, dev), *_ws(workspace, dev),
             _stream(stream)), name)
     return o, lse
 
@@ -869,7 +868,8 @@ def _head_scales(k_scale, v_scale, plan_, q):
     Hkv = plan_.suffix.num_kv_heads
     if k_scale.numel() != Hkv or v_scale.numel() != Hkv:
         raise FdError(-1, "k_scale and v_scale must have one entry per KV head")
-    return _need("k_scale", k_scale, torch.float32, q), _need("v_scale", v_scale, torch.float32, q)
+    dev = q.get_device()
+    return _need("k_scale", k_scale, torch.float32, dev), _need("v_scale", v_scale, torch.float32, dev)
 
 
 def decode_shared_fp8(plan, q, k_prefix_fp8, v_prefix_fp8, k_fp8, v_fp8, k_scale, v_scale,
@@ -885,29 +885,29 @@ def decode_shared_fp8(plan, q, k_prefix_fp8, v_prefix_fp8, k_fp8, v_fp8, k_scale
 def _decode_shared_paged(name, kv_dtypes, plan_, q, k_pages, v_pages, scales, prefix_req_indptr,
                          prefix_page_indptr, prefix_last_page_len, prefix_page_indices, kv_page_indptr,
                          kv_last_page_len, kv_page_indices, scale, o, lse, workspace, stream):
-    i32 = torch.int32
+    i32, dev = torch.int32, q.get_device()
     with _on(q):
-        o, lse, workspace = _shared_outputs(name, plan_, q, (k_pages, v_pages), o, lse, workspace)
-        P, B = plan_.num_prefixes, plan_.suffix.batch
+        o, lse, workspace, B, room = _shared_outputs(name, plan_, q, (k_pages, v_pages), o, lse, workspace)
+        P = plan_.num_prefixes
         if prefix_req_indptr.numel() != P + 1 or prefix_page_indptr.numel() != P + 1 or \
                 prefix_last_page_len.numel() < P or prefix_page_indices.numel() < plan_.prefix_rows or \
-                (plan_.suffix.total_tokens and (kv_page_indptr is None or kv_page_indptr.numel() != B + 1 or
-                                                kv_last_page_len.numel() < B)):
+                (room and (kv_page_indptr is None or kv_page_indptr.numel() != B + 1 or
+                           kv_last_page_len.numel() < B)):
             raise FdError(-1, f"{name}: tables of another length than the plan's")
         if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[1] != plan_.page_size or \
                 k_pages.dtype not in kv_dtypes or v_pages.dtype not in kv_dtypes:
             raise FdError(-1, f"{name}: pools of another shape or type")
         _check(getattr(lib(), name)(
-            ctypes.byref(plan_), k_pages.shape[0], _need("prefix_req_indptr", prefix_req_indptr, i32, q),
-            _need("prefix_page_indptr", prefix_page_indptr, i32, q),
-            _need("prefix_last_page_len", prefix_last_page_len, i32, q),
-            _need("prefix_page_indices", prefix_page_indices, i32, q),
-            _maybe("kv_page_indptr", kv_page_indptr, i32, q), _maybe("kv_last_page_len", kv_last_page_len, i32, q),
-            _maybe("kv_page_indices", kv_page_indices, i32, q),
-            0 if kv_page_indices is None else kv_page_indices.numel(), _need("q", q, torch.bfloat16),
-            _need("k_pages", k_pages, k_pages.dtype, q), _need("v_pages", v_pages, v_pages.dtype, q), *scales,
-            float(scale), _need("o", o, torch.float32, q), _need("lse", lse, torch.float32, q),
-            *_ws(workspace, q), _stream(stream)), name)
+            ctypes.byref(plan_), k_pages.shape[0], _need("prefix_req_indptr", prefix_req_indptr, i32, dev),
+            _need("prefix_page_indptr", prefix_page_indptr, i32, dev),
+            _need("prefix_last_page_len", prefix_last_page_len, i32, dev),
+            _need("prefix_page_indices", prefix_page_indices, i32, dev),
+            _maybe("kv_page_indptr", kv_page_indptr, i32, dev), _maybe("kv_last_page_len", kv_last_page_len, i32, dev),
+            _maybe("kv_page_indices", kv_page_indices, i32, dev),
+            0 if kv_page_indices is None else kv_page_indices.numel(), _need("q", q, torch.bfloat16, dev),
+            _need("k_pages", k_pages, k_pages.dtype, dev), _need("v_pages", v_pages, v_pages.dtype, dev), *scales,
+            float(scale), _need("o", o, torch.float32, dev), _need("lse", lse, torch.float32, dev),
+            *_ws(workspace, dev), _stream(stream)), name)
     return o, lse
 
 
