@@ -197,7 +197,7 @@ int fd::launch_stage1(const fd_plan_info *info, const void *q, const void *k, co
                       const int32_t *kv_indptr_dev, float scale, float *partial_o, float *partial_lse,
                       void *workspace, float *o, float *lse, int *counters,
                       const int32_t *kv_indptr_host, cudaStream_t stream, const PagedKV *paged,
-                      const QuantKV *quant, bool device_plan, int *flags)
+                      const QuantKV *quant, bool device_plan, int *flags, bool early_next)
 {
     if (!q || !k || !v || !kv_indptr_dev || !partial_o || !partial_lse)
         return FD_ERR_INVALID_ARG;
@@ -235,6 +235,7 @@ int fd::launch_stage1(const fd_plan_info *info, const void *q, const void *k, co
     p.claim = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + kClaimOffset);
     p.done = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + kDoneOffset);
     p.device_plan = device_plan;
+    p.early_next = early_next && device_plan;
     p.batch = info->batch;
     p.num_qo_heads = info->num_qo_heads;
     p.num_kv_heads = info->num_kv_heads;

@@ -328,7 +328,7 @@ int decode_shared(const fd_shared_plan *plan, const SharedTables &t, const void 
         info.timeout_ns = plan->timeout_ns;
         const fd::PagedKV pk{plan->page_size, t.num_pages, t.kv_last_len, nullptr, t.kv_indices, t.num_page_entries};
         rc = fd::launch_stage1(&info, q, k, v, t.kv_indptr, scale, wl.partial_o, wl.partial_lse, workspace, o, lse,
-                               wl.counters, nullptr, cs, paged ? &pk : nullptr, quant, true);
+                               wl.counters, nullptr, cs, paged ? &pk : nullptr, quant, true, nullptr, has_prefix);
         if (rc != FD_OK)
             return rc;
     }

@@ -49,6 +49,9 @@ struct SplitParams {
     // from the device kv_indptr alone, num_work is only an upper bound, and an
     // empty request is one split of no keys (it writes O = 0, LSE = -inf).
     int32_t device_plan;
+    // Device-side plan: let the next grid start while this one runs (it must not
+    // touch what this one reads or writes before this one has ended).
+    int32_t early_next;
     int32_t indptr_in_params;   // 1: indptr_param (and last_len_param) hold the device arrays
     int32_t indptr_param[kParamIndptr];
     // Paged KV (kv_last_len non-null): K/V are page pools [num_pages, page_size,

@@ -231,13 +231,13 @@ __device__ __forceinline__ bool locate_prefix(const SharedParams &p, int32_t j, 
         const int g = g0 + lane;
         int32_t r0 = 0, reqs = 0, base = 0, len = 0, pages = 0, splits = 0, blocks = 0;
         if (g < p.num_prefixes) {
-            r0 = __ldg(p.req_indptr + g);
-            reqs = __ldg(p.req_indptr + g + 1) - r0;
-            base = __ldg(p.prefix_indptr + g);
-            len = __ldg(p.prefix_indptr + g + 1) - base;
+            r0 = __ldcg(p.req_indptr + g);
+            reqs = __ldcg(p.req_indptr + g + 1) - r0;
+            base = __ldcg(p.prefix_indptr + g);
+            len = __ldcg(p.prefix_indptr + g + 1) - base;
             if (p.page_size) {
                 pages = len;
-                len = pages > 0 ? (pages - 1) * p.page_size + __ldg(p.prefix_last_len + g) : 0;
+                len = pages > 0 ? (pages - 1) * p.page_size + __ldcg(p.prefix_last_len + g) : 0;
             }
             if (reqs > 0 && len > 0) {
                 splits = shared_splits(len, p.chunk);
@@ -352,7 +352,13 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
     };
     if (warp == kMmaWarp)
         tmem_alloc(smem_addr(&sm->tmem), kTmemCols);
-    griddep_wait();
+    // With suffixes, the grid before this one is theirs and lets this one start
+    // once its own wait is over: what was written before the call is there then,
+    // and nothing here depends on the suffixes' grid but its end, which this one
+    // awaits at its own (the merge needs both).  Data of earlier grids are read
+    // through L2, as no wait of this grid has come before.
+    if (!p.has_suffix)
+        griddep_wait();
     if (warp == kProducerWarp) {
         PrefixCoord c;
         const int w = blockIdx.x;
@@ -433,7 +439,7 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
         int id_next = -1, off_next = 0;
         auto look_up = [&]() {
             const bool has = key < sm->keys;
-            id_next = has ? __ldg(p.prefix_indices + sm->base + pg) : -1;
+            id_next = has ? __ldcg(p.prefix_indices + sm->base + pg) : -1;
             off_next = has ? off : -1;
             key += lane < boxes ? kSharedTile : 0;
             pg += pages_on;
@@ -600,14 +606,15 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
         __syncwarp();
     } else if (kFp8 && warp >= kWidenWarp && warp < kWidenWarp + kWidenWarps && ok) {
         // ------------------------------------- FP8: raw tiles to f16 operands
-        // A warp takes 8 rows at a time, 16 values a lane: a raw row is 8 chunks
-        // of 16 bytes, chunk c at c ^ (row % 8), and becomes two chunks of the
-        // operand's half c / 4.  The lanes of a quarter warp are two rows r and
-        // r ^ 5 and four chunks of a half, which meet no bank twice on either side.
+        // A unit of work is 8 rows of one half of the head, 16 values a lane: a raw
+        // row is 8 chunks of 16 bytes, chunk c at c ^ (row % 8), and becomes two
+        // chunks of the operand's half c / 4.  The lanes of a quarter warp are two
+        // rows r and r ^ 5 and four chunks, which meet no bank twice on either side.
+        // All of a warp's units of a tile are loaded before the first is stored.
+        constexpr int kUnits = 2 * kSharedTile / 8, kMine = (kUnits + kWidenWarps - 1) / kWidenWarps;
         const uint8_t *raw0 = ring_ptr + kWideBuffers * kBufBytes;
-        const int ph = lane >> 3, r8 = ph ^ (((lane >> 2) & 1) * 5), cc = lane & 3;
-        constexpr int kWarpRows = kSharedTile / kWidenWarps;
-        const int row0 = (warp - kWidenWarp) * kWarpRows + r8;   // the lane's first row of a tile
+        const int me = warp - kWidenWarp;
+        const int r8 = (lane >> 3) ^ (((lane >> 2) & 1) * 5), cc = lane & 3;
         // the lane's chunk within its 8-row group: raw, and the first of its two of the operand
         const uint32_t lane_src = r8 * 128 + ((cc ^ r8) << 4), lane_dst = r8 * 128 + (((2 * cc) ^ r8) << 4);
         Place from(0, nb), to(0, kWideBuffers);
@@ -620,18 +627,20 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
                 go = wait_phase(&sm->empty[to.slot], to.phase ^ 1, p, sm);
             if (!__all_sync(0xffffffffu, go))
                 break;
-            const uint8_t *src = raw0 + from.slot * kRawBytes + (warp - kWidenWarp) * kWarpRows * 128;
-            uint8_t *dst = ring_ptr + to.slot * kBufBytes + (warp - kWidenWarp) * kWarpRows * 128;
-            constexpr int kBatch = 2;   // raw chunks of a lane in flight
+            const uint8_t *src = raw0 + from.slot * kRawBytes;
+            uint8_t *dst = ring_ptr + to.slot * kBufBytes;
             const int first = is_k ? kSharedTile : valid;   // V rows from here on are past the last key
-#pragma unroll 1
-            for (int j0 = 0; j0 < 32 / kWidenWarps; j0 += kBatch) {
-                uint4 x[kBatch];
+            uint4 x[kMine];
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j)
-                    x[j] = *reinterpret_cast<const uint4 *>(src + (j0 + j) / 2 * 1024 + ((4 * (j & 1)) << 4 ^ lane_src));
+            for (int j = 0; j < kMine; ++j) {
+                const int u = me + j * kWidenWarps;   // 8 rows u / 2, half u % 2
+                if (u < kUnits)
+                    x[j] = *reinterpret_cast<const uint4 *>(src + (u >> 1) * 1024 + (((u & 1) * 64) ^ lane_src));
+            }
 #pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
+            for (int j = 0; j < kMine; ++j) {
+                const int u = me + j * kWidenWarps;
+                if (u < kUnits) {
                     const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
                     uint32_t f[8];
 #pragma unroll
@@ -640,12 +649,12 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
                             "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
                             : "=r"(f[2 * q]), "=r"(f[2 * q + 1])
                             : "r"(w[q]));
-                    if (row0 + (j0 + j) / 2 * 8 >= first) {
+                    if ((u >> 1) * 8 + r8 >= first) {
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             f[q] = 0u;
                     }
-                    uint8_t *d = dst + (j & 1) * kHalfBytes + (j0 + j) / 2 * 1024;
+                    uint8_t *d = dst + (u & 1) * kHalfBytes + (u >> 1) * 1024;
                     *reinterpret_cast<uint4 *>(d + lane_dst) = make_uint4(f[0], f[1], f[2], f[3]);
                     *reinterpret_cast<uint4 *>(d + (lane_dst ^ 16)) = make_uint4(f[4], f[5], f[6], f[7]);
                 }
@@ -666,8 +675,8 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
         const bool two = q_tiles == 2;
         float factor = p.scale, v_scale = 1.f;
         if constexpr (kFp8) {
-            factor *= ok ? __ldg(p.k_scale + sm->kvh) : 1.f;
-            v_scale = ok ? __ldg(p.v_scale + sm->kvh) : 1.f;
+            factor *= ok ? __ldcg(p.k_scale + sm->kvh) : 1.f;
+            v_scale = ok ? __ldcg(p.v_scale + sm->kvh) : 1.f;
         }
         if (ok && !careful) {
             // Q rows into shared memory, [half][128 rows][128 bytes] a tile; a
@@ -680,7 +689,7 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
                     const int gr = sm->row0 + r;
                     const int64_t row = (int64_t)(sm->req0 + gr / p.group) * p.num_qo_heads + sm->kvh * p.group +
                                         gr % p.group;
-                    v = __ldg(reinterpret_cast<const uint4 *>(p.q + row * kHeadDim) + ch);
+                    v = __ldcg(reinterpret_cast<const uint4 *>(p.q + row * kHeadDim) + ch);
                 }
                 v.x ^= flip;
                 v.y ^= flip;
@@ -954,6 +963,8 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
     tcgen05_fence_after();
     }
     griddep_launch_dependents();
+    if (p.has_suffix)
+        griddep_wait();
     if (warp == kMmaWarp) {
         tcgen05_fence_after();
         tmem_dealloc(tmem, kTmemCols);

@@ -1612,6 +1612,8 @@ __global__ void __launch_bounds__((NC + 1) * 32, MIN_CTAS)
     const bool early_derive = p.indptr_in_params && warp == NC;
     if (!early_derive)
         griddep_wait();
+    if (p.early_next)
+        griddep_launch_dependents();
 
     float vscale = 1.f;              // FP8: the head's V scale
     Consumer<G, KV, DT> cs;          // consumer warps: set up by begin()
@@ -1940,6 +1942,8 @@ __global__ void __launch_bounds__((NC + 2) * 32, MIN_CTAS)
     const bool early_derive = p.indptr_in_params && warp == kProducer;
     if (!early_derive)
         griddep_wait();
+    if (p.early_next)
+        griddep_launch_dependents();
 
     if (warp == kProducer) {
         // ---------------------------------------------------------- producer

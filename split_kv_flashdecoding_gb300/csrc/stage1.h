@@ -49,13 +49,14 @@ int make_kv_map(CUtensorMap *map, const void *base, int64_t rows, int num_kv_hea
 // FP8 K or V [rows, Hkv, 128], one byte a value, likewise.
 int make_kv_map_fp8(CUtensorMap *map, const void *base, int64_t rows, int num_kv_heads, int box_rows);
 
-// Argument checks and the split kernel's launch (see fd_api.cu).
+// Argument checks and the split kernel's launch (see fd_api.cu).  early_next: see
+// SplitParams (device_plan only).
 int check_info(const fd_plan_info *info);
 int launch_stage1(const fd_plan_info *info, const void *q, const void *k, const void *v,
                   const int32_t *kv_indptr_dev, float scale, float *partial_o, float *partial_lse,
                   void *workspace, float *o, float *lse, int *counters,
                   const int32_t *kv_indptr_host, cudaStream_t stream,
                   const PagedKV *paged = nullptr, const QuantKV *quant = nullptr,
-                  bool device_plan = false, int *flags = nullptr);
+                  bool device_plan = false, int *flags = nullptr, bool early_next = false);
 
 }  // namespace fd
