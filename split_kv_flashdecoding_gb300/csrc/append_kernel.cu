@@ -18,6 +18,8 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "api_util.h"
 #include "cache_kernels.h"
 #include "device_common.cuh"
@@ -29,6 +31,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 8;      // tokens of one CTA
 constexpr int kUnits = kHeadDim / 16;   // two-chunk units of a head
+constexpr int kHeadLanes = kThreads / kUnits;
 
 __device__ __forceinline__ void unpack8(const uint4 &w, float (&x)[8])
 {
@@ -81,10 +84,18 @@ __device__ __forceinline__ uint32_t pack8_int4(const float (&x)[8], float scale)
     return w;
 }
 
+// (a, b) turned by the angle of (c, s).
+__device__ __forceinline__ void turn(float &a, float &b, float c, float s)
+{
+    const float x = a, y = b;
+    a = x * c - y * s;
+    b = y * c + x * s;
+}
+
 template <int KVT>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p)
 {
-    __shared__ float2 s_cs[kMaxTokens][kHeadDim / 2];
+    __shared__ __align__(16) float2 s_cs[kMaxTokens][kHeadDim / 2];
     __shared__ int64_t s_row[kMaxTokens];    // cache row of the token, -1: none
     __shared__ int s_pos[kMaxTokens], s_ok[kMaxTokens], s_count[kMaxTokens];
 
@@ -93,8 +104,52 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const int nt = min(p.tokens_per_cta, p.num_tokens - t0);
     if (tid < kMaxTokens)
         s_count[tid] = 0;
+    // Thread (head lane, unit u): the same unit of every 32nd head of the CTA's
+    // tokens, one after another, so that nothing is divided and all lanes are at
+    // work.  The 8 lanes of a head stay together, which the INT4 scale's reduction
+    // relies on.
+    const int heads = p.num_qo_heads + 2 * p.num_kv_heads;
+    const int u = tid % kUnits, lane_head = tid / kUnits;
+    // The unit's two chunks start at c0 and c1, which run on over the 8 lanes;
+    // pairs of an interleaved layout lie within a chunk, those of the other one in
+    // the two chunks of a unit.
+    const int rot = p.rope.rotary_dim, rot_units = rot / 16;
+    int c0 = 8 * u, c1 = kHeadDim / 2 + 8 * u;
+    if (!p.rope.interleaved) {
+        c0 = u < rot_units ? 8 * u : rot + 8 * (u - rot_units);
+        c1 = c0 + (u < rot_units ? rot : kHeadDim - rot) / 2;
+    }
+    const bool turns0 = c0 < rot, turns1 = c1 < rot;
+    int tt = 0, head = lane_head;   // of the unit to load next
+    auto settle = [&]() {           // into a token's heads
+        while (head >= heads) {
+            head -= heads;
+            ++tt;
+        }
+    };
+    settle();
+    // The next unit is loaded while the one before is worked on; the first while
+    // the tables are looked up.
+    int next_tt, next_head;
+    uint4 next0, next1;
+    auto load_unit = [&]() {
+        next_tt = tt;
+        next_head = head;
+        if (tt < nt) {
+            const int kv = head - p.num_qo_heads;
+            const int64_t t = t0 + tt;
+            const uint16_t *src = kv < 0                ? p.q + t * p.q_stride + head * kHeadDim
+                                  : kv < p.num_kv_heads ? p.k + t * p.k_stride + kv * kHeadDim
+                                                        : p.v + t * p.v_stride + (kv - p.num_kv_heads) * kHeadDim;
+            next0 = *reinterpret_cast<const uint4 *>(src + c0);
+            next1 = *reinterpret_cast<const uint4 *>(src + c1);
+        }
+        head += kHeadLanes;
+        settle();
+    };
     griddep_wait();
     griddep_launch_dependents();
+    load_unit();
     __syncthreads();
 
     // request of each token: how many of append_indptr[1..B] are at or below it
@@ -150,70 +205,57 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     __syncthreads();
     for (int i = tid; i < nt * (p.rope.rotary_dim / 2); i += kThreads) {
         const int tt = i / (p.rope.rotary_dim / 2), j = i % (p.rope.rotary_dim / 2);
-        const uint64_t turn = (uint64_t)(int64_t)s_pos[tt] * p.rope.step[j];
+        const uint64_t turns = (uint64_t)(int64_t)s_pos[tt] * p.rope.step[j];
         float s, c;
-        sincospif((float)(int64_t)turn * 1.0842021724855044e-19f, &s, &c);   // turn / 2^63 half turns
+        sincospif((float)(int64_t)turns * 1.0842021724855044e-19f, &s, &c);   // turns / 2^63: half turns
         s_cs[tt][j] = make_float2(c * p.rope.gain, s * p.rope.gain);
     }
     __syncthreads();
 
-    const int heads = p.num_qo_heads + 2 * p.num_kv_heads;
-    const int per_token = heads * kUnits;
-    const int rot_units = p.rope.rotary_dim / 16;
-    // the 8 lanes of a head stay together (a warp holds 4 heads' units), which
-    // the INT4 scale's reduction relies on; a warp past the end leaves whole
-    for (int i = tid; i < nt * per_token; i += kThreads) {
-        const int tt = i / per_token, r = i - tt * per_token;
-        const int head = r / kUnits, u = r % kUnits;
-        if (!s_ok[tt])
-            continue;
-        const int64_t t = t0 + tt;
-        int c0, c1;   // first value of the unit's two chunks
-        if (p.rope.interleaved || u >= rot_units) {
-            c0 = u < rot_units ? 16 * u : p.rope.rotary_dim + 16 * (u - rot_units);
-            c1 = c0 + 8;
-        } else {
-            c0 = 8 * u;
-            c1 = p.rope.rotary_dim / 2 + 8 * u;
-        }
-        const bool is_q = head < p.num_qo_heads;
-        const int kvh = (head - p.num_qo_heads) % p.num_kv_heads;
-        const bool is_v = !is_q && head >= p.num_qo_heads + p.num_kv_heads;
-        const uint16_t *src = is_q   ? p.q + t * p.q_stride + head * kHeadDim
-                              : is_v ? p.v + t * p.v_stride + kvh * kHeadDim
-                                     : p.k + t * p.k_stride + kvh * kHeadDim;
+    while (next_tt < nt) {
+        const int token = next_tt, head = next_head, kv = head - p.num_qo_heads;
+        const bool is_v = kv >= p.num_kv_heads;
         float a[8], b[8];
-        unpack8(*reinterpret_cast<const uint4 *>(src + c0), a);
-        unpack8(*reinterpret_cast<const uint4 *>(src + c1), b);
-        if (!is_v && u < rot_units) {
-            const float2 *cs = &s_cs[tt][8 * u];
+        unpack8(next0, a);
+        unpack8(next1, b);
+        load_unit();
+        if (!s_ok[token])
+            continue;
+        const int64_t t = t0 + token, row = s_row[token];
+        if (!is_v && turns0) {
+            // the pairs' (cos, sin): of each chunk's 4 pairs, or of the unit's 8
+            const float4 *cs = reinterpret_cast<const float4 *>(s_cs[token]);
             if (p.rope.interleaved) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = cs[j], g = cs[4 + j];
-                    const float x = a[2 * j], y = a[2 * j + 1], z = b[2 * j], w = b[2 * j + 1];
-                    a[2 * j] = x * f.x - y * f.y;
-                    a[2 * j + 1] = y * f.x + x * f.y;
-                    b[2 * j] = z * g.x - w * g.y;
-                    b[2 * j + 1] = w * g.x + z * g.y;
+                for (int j = 0; j < 2; ++j) {
+                    const float4 f = cs[c0 / 4 + j];
+                    turn(a[4 * j], a[4 * j + 1], f.x, f.y);
+                    turn(a[4 * j + 2], a[4 * j + 3], f.z, f.w);
+                }
+                if (turns1) {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const float4 f = cs[c1 / 4 + j];
+                        turn(b[4 * j], b[4 * j + 1], f.x, f.y);
+                        turn(b[4 * j + 2], b[4 * j + 3], f.z, f.w);
+                    }
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const float2 f = cs[j];
-                    const float x = a[j], y = b[j];
-                    a[j] = x * f.x - y * f.y;
-                    b[j] = y * f.x + x * f.y;
+                for (int j = 0; j < 4; ++j) {
+                    const float4 f = cs[c0 / 2 + j];
+                    turn(a[2 * j], b[2 * j], f.x, f.y);
+                    turn(a[2 * j + 1], b[2 * j + 1], f.z, f.w);
                 }
             }
         }
-        if (is_q) {
+        if (kv < 0) {
             uint16_t *dst = p.q_out + t * p.q_out_stride + head * kHeadDim;
             *reinterpret_cast<uint4 *>(dst + c0) = pack8(a);
             *reinterpret_cast<uint4 *>(dst + c1) = pack8(b);
             continue;
         }
-        const int64_t row = s_row[tt];
+        const int kvh = is_v ? kv - p.num_kv_heads : kv;
         const int64_t at = (row * p.num_kv_heads + kvh) * kHeadDim;   // values before this head's row
         uint8_t *pool = static_cast<uint8_t *>(is_v ? p.v_pages : p.k_pages);
         if constexpr (KVT == kKvTypeBf16) {
@@ -224,8 +266,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             *reinterpret_cast<uint2 *>(pool + at + c0) = pack8_fp8(a, inv);
             *reinterpret_cast<uint2 *>(pool + at + c1) = pack8_fp8(b, inv);
         } else {
-            // one scale per (row, head): largest magnitude / 7 over the head's 8
-            // lanes (1 for a row of zeros; NaN when the row holds one)
+            // one scale per (row, head): largest magnitude / 7 over the head's
+            // 8 lanes (1 for a row of zeros; NaN when the row holds one)
             float m = 0.f;
             bool nan = false;
 #pragma unroll
@@ -257,9 +299,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 cudaError_t launch_append(const AppendParams &params, int kv_type, cudaStream_t stream)
 {
     AppendParams p = params;
-    // Up to one wave of CTAs at one token each (a short call is a chain of
-    // dependent loads: more CTAs, shorter chains), several tokens past it.
-    p.tokens_per_cta = p.num_tokens <= 1024 ? 1 : 4;
+    // One token a CTA up to one wave of resident CTAs (a short call is a chain of
+    // dependent loads: more CTAs, shorter chains), then as few CTAs as a wave, up
+    // to kMaxTokens tokens each (32768 tokens of 48 heads: 8 a CTA 133 us, 4 134).
+    constexpr int kWave = 152 * 4;
+    p.tokens_per_cta = std::min(kMaxTokens, (p.num_tokens + kWave - 1) / kWave);
     const dim3 grid((unsigned)((p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta));
     switch (kv_type) {
     case kKvTypeBf16: return launch_dependent(append_kernel<kKvTypeBf16>, grid, kThreads, 0, stream, p);
