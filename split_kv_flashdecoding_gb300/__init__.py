@@ -691,11 +691,15 @@ def fork_pages(parent, kv_page_indptr, kv_last_page_len, kv_page_indices, new_pa
     if new_page_indptr.numel() != n_new + 1 or kv_last_page_len.numel() < n_old:
         raise FdError(-1, "fd_fork_pages: new_page_indptr must have new_batch+1 and kv_last_page_len batch entries")
     with _on(like):
-        new = like.new_empty
-        new_page_indices = new(new_page_entries) if new_page_indices is None else new_page_indices
-        new_page_refs = new(pages) if new_page_refs is None else new_page_refs
-        copy_src = new(n_new) if copy_src is None else copy_src
-        copy_dst = new(n_new) if copy_dst is None else copy_dst
+        at = like.device
+        if new_page_indices is None:
+            new_page_indices = torch.empty(new_page_entries, dtype=i32, device=at)
+        if new_page_refs is None:
+            new_page_refs = torch.empty(pages, dtype=i32, device=at)
+        if copy_src is None:
+            copy_src = torch.empty(n_new, dtype=i32, device=at)
+        if copy_dst is None:
+            copy_dst = torch.empty(n_new, dtype=i32, device=at)
         if new_page_indices.numel() < new_page_entries or new_page_refs.numel() != pages or \
                 copy_src.numel() < n_new or copy_dst.numel() < n_new:
             raise FdError(-1, "fd_fork_pages: an output is too small")
@@ -722,11 +726,15 @@ def compact_pages(page_refs, kv_page_indices, max_moves: int, *, limit: int = 0,
     i32, like, dev = torch.int32, page_refs, page_refs.get_device()
     pages, entries = page_refs.numel(), kv_page_indices.numel()
     with _on(like):
-        new = like.new_empty
-        new_page_indices = new(entries) if new_page_indices is None else new_page_indices
-        new_page_refs = new(pages) if new_page_refs is None else new_page_refs
-        copy_src = new(max_moves) if copy_src is None else copy_src
-        copy_dst = new(max_moves) if copy_dst is None else copy_dst
+        at = like.device
+        if new_page_indices is None:
+            new_page_indices = torch.empty(entries, dtype=i32, device=at)
+        if new_page_refs is None:
+            new_page_refs = torch.empty(pages, dtype=i32, device=at)
+        if copy_src is None:
+            copy_src = torch.empty(max_moves, dtype=i32, device=at)
+        if copy_dst is None:
+            copy_dst = torch.empty(max_moves, dtype=i32, device=at)
         if new_page_indices.numel() < entries or new_page_refs.numel() != pages or \
                 copy_src.numel() < max_moves or copy_dst.numel() < max_moves:
             raise FdError(-1, "fd_compact_pages: an output is too small")

@@ -73,7 +73,8 @@ def fork(parent, ip, last, ids, nip, refs, page, inplace=False, ws=None):
 
 
 CASES = [(1, 1, 5, 1), (3, 7, 40, 4), (8, 32, 1024, 20), (5, 1, 1023, 30), (17, 40, 1025, 12),
-         (64, 251, 5000, 40), (2, 0, 33, 3), (1500, 2100, 9000, 2)]
+         (64, 251, 5000, 40), (2, 0, 33, 3), (1500, 2100, 9000, 2),
+         (30, 90, 65537, 25), (9, 20, 300000, 300)]
 
 
 @pytest.mark.parametrize("batch,children,num_pages,most", CASES)
