@@ -152,6 +152,13 @@ int suffix_chunk(int batch, int num_kv_heads, int64_t tokens, int num_sms)
     return c <= kMostSuffixChunk ? (int)c : 0;
 }
 
+// Where the items' streams add up their O, when one has over kFlush steps (a
+// step is a tile; with one row tile the streams take every other one).
+int64_t flush_bytes(int64_t items, int32_t chunk)
+{
+    return chunk / fd::kSharedTile > fd::kFlush ? items * 2 * fd::kSharedQRows * kHeadDim * 4 : 0;
+}
+
 int make_plan(int batch, int num_qo_heads, int num_kv_heads, int head_dim, const Prefixes &x,
               int64_t max_suffix_tokens, int num_sms, int chunk, fd_shared_plan *plan)
 {
@@ -200,7 +207,7 @@ int make_plan(int batch, int num_qo_heads, int num_kv_heads, int head_dim, const
     plan->page_size = x.page_size;
     plan->prefix_rows = x.indptr[x.count];
     plan->workspace_bytes = round_up(suffix.workspace_bytes, 256) + round_up(z.rows * 4, 256) +
-                            z.rows * kHeadDim * 4;
+                            z.rows * kHeadDim * 4 + flush_bytes(z.items, chunk);
     plan->timeout_ns = FD_DEFAULT_TIMEOUT_NS;
     return FD_OK;
 }
@@ -344,6 +351,7 @@ int decode_shared(const fd_shared_plan *plan, const SharedTables &t, const void 
     p.v_scale = quant ? quant->v_scale : nullptr;
     p.partial_lse = reinterpret_cast<float *>(part);
     p.partial_o = reinterpret_cast<float *>(part + round_up((int64_t)plan->num_partial_rows * 4, 256));
+    p.flush = p.partial_o + (int64_t)plan->num_partial_rows * kHeadDim;
     p.o = o;
     p.lse = lse;
     p.status = static_cast<int *>(workspace);

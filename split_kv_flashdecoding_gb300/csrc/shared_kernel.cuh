@@ -186,6 +186,34 @@ __device__ __forceinline__ void settle(uint32_t (&r)[N])
                           "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7]));
 }
 
+// 16 values of O to memory that only this thread uses (four at a time, the
+// stream's rows apart): added, or the first ones.
+__device__ __forceinline__ void flush16(float *dst, const uint32_t (&o)[16], bool add)
+{
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+        if (add)
+            asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(dst + j * kSharedQRows),
+                         "f"(__uint_as_float(o[j])), "f"(__uint_as_float(o[j + 1])), "f"(__uint_as_float(o[j + 2])),
+                         "f"(__uint_as_float(o[j + 3]))
+                         : "memory");
+        else
+            __stcg(reinterpret_cast<uint4 *>(dst + j * kSharedQRows), make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]));
+    }
+}
+
+__device__ __forceinline__ void add_flushed16(const float *src, uint32_t (&o)[16])
+{
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(src + j * kSharedQRows));
+        o[j] = __float_as_uint(__uint_as_float(o[j]) + v.x);
+        o[j + 1] = __float_as_uint(__uint_as_float(o[j + 1]) + v.y);
+        o[j + 2] = __float_as_uint(__uint_as_float(o[j + 2]) + v.z);
+        o[j + 3] = __float_as_uint(__uint_as_float(o[j + 3]) + v.w);
+    }
+}
+
 // Wait for a phase; false (and the CTA's abort flag set) when the time limit
 // passed or another warp gave up.
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, const SharedParams &p, SharedSmem *sm)
@@ -564,7 +592,12 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
         };
         // O += P V of stream s's step i, in two parts: each half of the keys is
         // ready in two parts of 32.
+        const int run0 = shared_run(steps0), run1 = shared_run(steps1);
+        int anew[2] = {0, 0};   // the step at which O of a stream next starts anew
         auto values = [&](int s, int i, bool last) {
+            const bool fresh = i == anew[s];
+            if (fresh)
+                anew[s] += careful ? steps0 : s ? run1 : run0;
             wait_phase(&sm->full[v_at.slot], v_at.phase, p, sm);
             const uint32_t pa = tmem + s * kStreamCols, va = v_lo + v_at.slot * kBuf16;
 #pragma unroll
@@ -575,7 +608,7 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
                 for (int j = 0; j < 4; ++j) {   // 16 keys a step, hi then lo
                     const int k = (j >> 1) * 4 + part * 2 + (j & 1);
                     const uint32_t vk = va + k * 2 * TL::kGroup / 16;
-                    mma_ts(pa + 128, pa + 16 * k, vk, kv_hi, id_o, i > 0 || part > 0 || j > 0, leader);
+                    mma_ts(pa + 128, pa + 16 * k, vk, kv_hi, id_o, !fresh || part > 0 || j > 0, leader);
                     mma_ts(pa + 128, pa + 16 * k + 8, vk, kv_hi, id_o, 1, leader);
                 }
             }
@@ -747,6 +780,12 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
         // FP8: weights are 2^7 times larger, which keeps seven more bits of the
         // small ones in f16; it cancels in O
         constexpr float kBias = kFp8 ? 7.f : 0.f;
+        // Where the thread adds up its 64 values of O (see kFlush): 16 bytes of each
+        // of the stream's rows side by side, so that a warp writes whole lines.
+        const bool flushed = !careful && steps(s) > kFlush;
+        const int run = shared_run(steps(s));
+        int next_flush = run;
+        float *my_flush = p.flush + (((int64_t)blockIdx.x * 2 + s) * 32 + half * 16) * (4 * kSharedQRows) + 4 * trow;
         float m_ref = -INFINITY, l = 0.f;   // what the weights refer to (a raw score), their sum
         float most = 0.f;                   // FP8: the largest weight
         bool go = ok;
@@ -815,6 +854,16 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
             if (i > 0 && !careful) {
                 if (go) {
                     tcgen05_fence_after();
+                    if (i == next_flush) {   // O of the steps so far: their products are done
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            tmem_ld16(o_col + 16 * c, r0);
+                            tmem_wait_ld();
+                            settle(r0);
+                            flush16(my_flush + c * (16 * kSharedQRows), r0, i > run);
+                        }
+                        next_flush += run;
+                    }
                     load(r0, 0);
                     step(r0, r1, valid, kBias - m_ref * c2);
                 }
@@ -893,6 +942,8 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
                     tmem_ld16(o_col + 16 * c, o);
                     tmem_wait_ld();
                     settle(o);
+                    if (flushed)
+                        add_flushed16(my_flush + c * (16 * kSharedQRows), o);
 #pragma unroll
                     for (int j = 0; j < 16; j += 4)
                         *reinterpret_cast<uint4 *>(mine + 16 * c + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
@@ -919,6 +970,8 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
                 tmem_ld16(o_col + 16 * c, o);
                 tmem_wait_ld();
                 settle(o);
+                if (flushed)
+                    add_flushed16(my_flush + c * (16 * kSharedQRows), o);
 #pragma unroll
                 for (int j = 0; j < 16; j += 4) {
                     float4 v = make_float4(__uint_as_float(o[j]) * f0, __uint_as_float(o[j + 1]) * f0,

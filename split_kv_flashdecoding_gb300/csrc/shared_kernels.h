@@ -15,6 +15,22 @@ constexpr int kSharedTile = 128;       // keys of a tile: rows of a K or V buffe
 constexpr int kSharedQRows = 128;      // query rows of one tensor-core tile
 constexpr int kSharedBlockRows = 256;  // query rows of one CTA: two such tiles
 
+// The most steps of a stream that O accumulates over in tensor memory.  The
+// tensor cores cut the sum of products and accumulator off (they do not round
+// it), which with a tile's 16 products takes about 2.5e-7 of O: 37 tiles in a row
+// left it short by 1.1e-5, more than its fp32 type says.  So a stream with more
+// steps adds O up in global memory, where fp32 sums round, in runs of equal length
+// of up to kFlush steps, and starts anew.  A flush takes 2.2 us of a CTA's 70
+// (256 x 64 heads behind 32768 keys, 37 steps: none 276 us and 1.1e-5, one 283 and
+// 5.5e-6, four 303 and 3.3e-6).
+constexpr int kFlush = 20;
+
+FD_HD int32_t shared_run(int32_t steps)   // steps between flushes
+{
+    const int32_t runs = (steps + kFlush - 1) / kFlush;
+    return runs > 0 ? (steps + runs - 1) / runs : 1;
+}
+
 // Splits of a prefix of `len` keys for chunk length `chunk` (a multiple of
 // kSharedTile), and their length: equal within the prefix, whole tiles.
 FD_HD int32_t shared_splits(int32_t len, int32_t chunk)
@@ -37,6 +53,7 @@ struct SharedParams {
     const float *k_scale, *v_scale;  // FP8: [Hkv]
     float *partial_o;                // [rows, D]
     float *partial_lse;              // [rows]
+    float *flush;                    // [items, 2, D / 4, 128, 4]; not used where no stream has over kFlush steps
     float *o, *lse;                  // [B, Hq, D], [B, Hq]; hold the suffix states when has_suffix
     int *status;
     int32_t batch, num_qo_heads, num_kv_heads, group;

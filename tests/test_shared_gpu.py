@@ -149,6 +149,15 @@ def test_long_prefixes(cuda_device, Hq, Hkv, B, L):
     check(i, paged(i, 16), ref, f"{B} x {L} paged")
 
 
+@pytest.mark.parametrize("L", [1024, 1025, 2176, 2177, 4100, 20000])
+@pytest.mark.parametrize("B", [5, 33, 64])
+def test_long_splits(cuda_device, B, L):
+    """One split for all keys: O goes over to fp32 sums every few tiles, in one
+    row tile (two streams of keys) and in two."""
+    i = make(8, 2, [B], [L], np.zeros(B, int), seed=L, room=0)
+    check(i, ragged(i, -(-L // 128) * 128), what=f"{B} x {L}")
+
+
 @pytest.mark.parametrize("rows", [3, 40])
 def test_no_suffix_and_no_keys(cuda_device, rows):
     i = make(32, 8, [rows, 2], [700, 0], np.zeros(rows + 2, int), room=0)
