@@ -89,7 +89,7 @@ struct SharedSmem {
     int issued;             // ring fills issued (for the drain after an error)
     int tail_issued;
     // the CTA's item
-    int ok, req0, rows, kvh, row0, key0, keys, base, pages, part_row, part_stride, q_tiles;
+    int ok, req0, rows, kvh, row0, key0, keys, base, part_row, part_stride, q_tiles;
     union {
         float q_scale[kSharedBlockRows];      // FP8, before the first step: a row's factor of the scores
         float row_max[2][2][kSharedQRows];    // a stream's row maxima, by half of the keys
@@ -214,6 +214,16 @@ __device__ __forceinline__ void add_flushed16(const float *src, uint32_t (&o)[16
     }
 }
 
+__device__ __forceinline__ void scale_flushed16(float *dst, float f)
+{
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+        float4 *d = reinterpret_cast<float4 *>(dst + j * kSharedQRows);
+        const float4 v = __ldcg(d);
+        __stcg(d, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+    }
+}
+
 // Wait for a phase; false (and the CTA's abort flag set) when the time limit
 // passed or another warp gave up.
 __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, const SharedParams &p, SharedSmem *sm)
@@ -244,7 +254,7 @@ __device__ __forceinline__ bool wait_phase(uint64_t *bar, uint32_t parity, const
 
 struct PrefixCoord {
     int32_t g, req0, reqs;     // prefix, its first request and their number
-    int32_t base, len, pages;  // first key row or page-list entry, keys, entries
+    int32_t base, len;         // first key row or page-list entry, keys
     int32_t splits, blocks;    // splits of the keys, 256-row blocks of a KV head's rows
     int32_t item0, row0;       // items and partial rows of the prefixes before
 };
@@ -257,22 +267,34 @@ __device__ __forceinline__ bool locate_prefix(const SharedParams &p, int32_t j, 
     int32_t item_carry = 0, row_carry = 0;
     for (int g0 = 0; g0 < p.num_prefixes; g0 += 32) {
         const int g = g0 + lane;
-        int32_t r0 = 0, reqs = 0, base = 0, len = 0, pages = 0, splits = 0, blocks = 0;
+        int32_t r0 = 0, reqs = 0, base = 0, len = 0, splits = 0, blocks = 0;
         if (g < p.num_prefixes) {
+            const int32_t r1 = __ldcg(p.req_indptr + g + 1), b1 = __ldcg(p.prefix_indptr + g + 1);
             r0 = __ldcg(p.req_indptr + g);
-            reqs = __ldcg(p.req_indptr + g + 1) - r0;
             base = __ldcg(p.prefix_indptr + g);
-            len = __ldcg(p.prefix_indptr + g + 1) - base;
-            if (p.page_size) {
-                pages = len;
-                len = pages > 0 ? (pages - 1) * p.page_size + __ldcg(p.prefix_last_len + g) : 0;
-            }
-            if (reqs > 0 && len > 0) {
-                splits = shared_splits(len, p.chunk);
-                blocks = (reqs * p.group + kSharedBlockRows - 1) / kSharedBlockRows;
+            const int32_t last = p.page_size ? __ldcg(p.prefix_last_len + g) : 1;
+            // a prefix outside the batch or the rows is nobody's; no sum below
+            // overflows for what is left
+            if (r0 >= 0 && r0 <= r1 && r1 <= p.batch && base >= 0 && base <= b1 && b1 <= p.prefix_rows) {
+                const int64_t keys = !p.page_size ? b1 - base
+                                     : b1 == base ? 0 : (int64_t)(b1 - base - 1) * p.page_size + last;
+                reqs = r1 - r0;
+                if (reqs > 0 && keys > 0 && keys <= INT32_MAX - kSharedTile && last >= 1 &&
+                    (!p.page_size || last <= p.page_size)) {
+                    len = (int32_t)keys;
+                    splits = shared_splits(len, p.chunk);
+                    blocks = (int32_t)(((int64_t)reqs * p.group + kSharedBlockRows - 1) / kSharedBlockRows);
+                } else if (keys != 0) {
+                    reqs = 0;
+                }
             }
         }
-        const int32_t items = splits * blocks * p.num_kv_heads, rows = splits * reqs * p.num_qo_heads;
+        const int64_t items64 = (int64_t)splits * blocks * p.num_kv_heads;
+        const int64_t rows64 = (int64_t)splits * reqs * p.num_qo_heads;
+        const bool fits = items64 <= p.num_items && rows64 <= p.num_partial_rows;
+        if (!fits)
+            reqs = 0;
+        const int32_t items = fits ? (int32_t)items64 : 0, rows = fits ? (int32_t)rows64 : 0;
         int32_t item_incl = items, row_incl = rows;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -295,14 +317,12 @@ __device__ __forceinline__ bool locate_prefix(const SharedParams &p, int32_t j, 
             out.reqs = __shfl_sync(0xffffffffu, reqs, src);
             out.base = __shfl_sync(0xffffffffu, base, src);
             out.len = __shfl_sync(0xffffffffu, len, src);
-            out.pages = __shfl_sync(0xffffffffu, pages, src);
             out.splits = __shfl_sync(0xffffffffu, splits, src);
             out.blocks = __shfl_sync(0xffffffffu, blocks, src);
             out.item0 = __shfl_sync(0xffffffffu, item_incl - items, src);
             out.row0 = __shfl_sync(0xffffffffu, row_incl - rows, src);
-            const int32_t held = p.page_size ? out.pages : out.len;
-            return out.req0 >= 0 && out.req0 + out.reqs <= p.batch && out.base >= 0 &&
-                   out.base + held <= p.prefix_rows && out.row0 >= 0 &&
+            // by int32 sums that may have wrapped: the item and its rows are in range all the same
+            return out.item0 >= 0 && out.row0 >= 0 &&
                    (int64_t)out.row0 + (int64_t)out.splits * out.reqs * p.num_qo_heads <= p.num_partial_rows;
         }
         item_carry = __shfl_sync(0xffffffffu, item_incl, 31);
@@ -407,7 +427,6 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
                 sm->key0 = split * len;
                 sm->keys = min(c.len - sm->key0, len);
                 sm->base = c.base;
-                sm->pages = c.pages;
                 sm->part_row = c.row0 + split;
                 sm->part_stride = c.splits;
                 sm->q_tiles = sm->rows > kSharedQRows ? 2 : 1;
@@ -443,577 +462,589 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
     // first left the weights' range.
     float c2 = 0.f;   // softmax warps: what a score is multiplied by
     for (int pass = 0; pass < 2; ++pass) {
-    const bool careful = pass > 0;
-    if (warp == kProducerWarp && ok) {
-        // --------------------------------------------------------- producer
-        const uint64_t pol = l2_evict_first_policy();
-        const int box = PAGED ? p.box_rows : kSharedTile;
-        const int boxes = kSharedTile / box;
-        constexpr int kRow = kFp8 ? kHeadDim : 2 * kHeadDim, kTileBytes = kSharedTile * kRow;
-        uint64_t *bar_full = kFp8 ? sm->raw_full : sm->full, *bar_empty = kFp8 ? sm->raw_empty : sm->empty;
-        const uint32_t raw0 = ring + (kFp8 ? kWideBuffers * kBufBytes : 0);
-        // Paged: the lane's box of the next tile is at row `off` of the request's
-        // page `pg`; a tile on, that is a fixed number of pages and rows further.
-        int pg = 0, off = 0, key = sm->keys;
-        const int pages_on = PAGED ? kSharedTile / p.page_size : 0;
-        const int rows_on = PAGED ? kSharedTile % p.page_size : 0;
-        if (PAGED && lane < boxes) {
-            key = lane * box;
-            pg = (sm->key0 + key) / p.page_size;
-            off = (sm->key0 + key) % p.page_size;
-        }
-        // The next tile's page is looked up a tile ahead and used when its turn
-        // comes; -1: no box of this lane (past the last key).
-        int id_next = -1, off_next = 0;
-        auto look_up = [&]() {
-            const bool has = key < sm->keys;
-            id_next = has ? __ldcg(p.prefix_indices + sm->base + pg) : -1;
-            off_next = has ? off : -1;
-            key += lane < boxes ? kSharedTile : 0;
-            pg += pages_on;
-            off += rows_on;
-            if (off >= p.page_size) {
-                off -= p.page_size;
-                ++pg;
+        const bool careful = pass > 0;
+        if (warp == kProducerWarp && ok) {
+            // --------------------------------------------------------- producer
+            const uint64_t pol = l2_evict_first_policy();
+            const int box = PAGED ? p.box_rows : kSharedTile;
+            const int boxes = kSharedTile / box;
+            constexpr int kRow = kFp8 ? kHeadDim : 2 * kHeadDim, kTileBytes = kSharedTile * kRow;
+            uint64_t *bar_full = kFp8 ? sm->raw_full : sm->full, *bar_empty = kFp8 ? sm->raw_empty : sm->empty;
+            const uint32_t raw0 = ring + (kFp8 ? kWideBuffers * kBufBytes : 0);
+            // Paged: the lane's box of the next tile is at row `off` of the request's
+            // page `pg`; a tile on, that is a fixed number of pages and rows further.
+            int pg = 0, off = 0, key = sm->keys;
+            const int pages_on = PAGED ? kSharedTile / p.page_size : 0;
+            const int rows_on = PAGED ? kSharedTile % p.page_size : 0;
+            if (PAGED && lane < boxes) {
+                key = lane * box;
+                pg = (sm->key0 + key) / p.page_size;
+                off = (sm->key0 + key) % p.page_size;
             }
-        };
-        auto pool_row = [&]() -> int {
-            if (off_next < 0)
-                return -1;
-            if (id_next < 0 || id_next >= p.num_pages) {   // read page 0 in its place
-                report(p.status, FD_ERR_DEVICE_BOUNDS);
-                id_next = 0;
-            }
-            return id_next * p.page_size + off_next;
-        };
-        Place at(0, nb);
-        auto load = [&](const CUtensorMap *map, int row, uint64_t *bar, uint32_t bytes) {
-            const uint32_t dst = raw0 + at.slot * kTileBytes, b = smem_addr(bar);
-            if (lane == 0)
-                mbar_arrive_expect_tx(b, bytes);
-            __syncwarp();
-            if constexpr (kFp8) {
-                if (PAGED ? row >= 0 : lane == 0)
-                    tma_load_2d(dst + (PAGED ? lane * box * kRow : 0), map, sm->kvh * kHeadDim, row, b, pol);
-            } else if constexpr (PAGED) {
-                if (row >= 0)
-                    asm volatile(
-                        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-                        ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst + lane * box * kRow),
-                        "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(0), "r"(2 * sm->kvh), "r"(row >> 3),
-                        "r"(b), "l"(pol)
-                        : "memory");
-            } else if (lane == 0) {
-                tma_load_3d(dst, map, 0, row, 2 * sm->kvh, b, pol);
-            }
-        };
-        if (PAGED)
-            look_up();
-        int row_k = sm->base + sm->key0 - kSharedTile, row_v = 0;
-        for (int pos = 0; pos < 2 * n; ++pos, at.advance(1)) {
-            bool is_k;
-            const int t = at_pos(pos, is_k);
-            if (is_k) {
-                row_v = row_k;
-                if constexpr (PAGED) {
-                    row_k = pool_row();
-                    look_up();
+            // The next tile's page is looked up a tile ahead and used when its turn
+            // comes; -1: no box of this lane (past the last key).
+            int id_next = -1, off_next = 0;
+            auto look_up = [&]() {
+                const bool has = key < sm->keys;
+                id_next = has ? __ldcg(p.prefix_indices + sm->base + pg) : -1;
+                off_next = has ? off : -1;
+                key += lane < boxes ? kSharedTile : 0;
+                pg += pages_on;
+                off += rows_on;
+                if (off >= p.page_size) {
+                    off -= p.page_size;
+                    ++pg;
+                }
+            };
+            auto pool_row = [&]() -> int {
+                if (off_next < 0)
+                    return -1;
+                if (id_next < 0 || id_next >= p.num_pages) {   // read page 0 in its place
+                    report(p.status, FD_ERR_DEVICE_BOUNDS);
+                    id_next = 0;
+                }
+                return id_next * p.page_size + off_next;
+            };
+            Place at(0, nb);
+            auto load = [&](const CUtensorMap *map, int row, uint64_t *bar, uint32_t bytes) {
+                const uint32_t dst = raw0 + at.slot * kTileBytes, b = smem_addr(bar);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(b, bytes);
+                __syncwarp();
+                if constexpr (kFp8) {
+                    if (PAGED ? row >= 0 : lane == 0)
+                        tma_load_2d(dst + (PAGED ? lane * box * kRow : 0), map, sm->kvh * kHeadDim, row, b, pol);
+                } else if constexpr (PAGED) {
+                    if (row >= 0)
+                        asm volatile(
+                            "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                            ".L2::cache_hint [%0], [%1, {%2, %3, %4, %5}], [%6], %7;" ::"r"(dst + lane * box * kRow),
+                            "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(0), "r"(2 * sm->kvh), "r"(row >> 3),
+                            "r"(b), "l"(pol)
+                            : "memory");
+                } else if (lane == 0) {
+                    tma_load_3d(dst, map, 0, row, 2 * sm->kvh, b, pol);
+                }
+            };
+            if (PAGED)
+                look_up();
+            int row_k = sm->base + sm->key0 - kSharedTile, row_v = 0;
+            for (int pos = 0; pos < 2 * n; ++pos, at.advance(1)) {
+                bool is_k;
+                const int t = at_pos(pos, is_k);
+                if (is_k) {
+                    row_v = row_k;
+                    if constexpr (PAGED) {
+                        row_k = pool_row();
+                        look_up();
+                    } else {
+                        row_k += kSharedTile;
+                    }
+                }
+                if (pos >= nb && !__all_sync(0xffffffffu, wait_phase(&bar_empty[at.slot], at.phase ^ 1, p, sm)))
+                    break;
+                if (lane == 0)
+                    sm->issued = pos + 1;
+                const int valid = min(sm->keys - t * kSharedTile, kSharedTile);
+                const uint32_t bytes = PAGED ? (valid + box - 1) / box * box * kRow : kTileBytes;
+                if (is_k) {
+                    load(&tm_k, row_k, &bar_full[at.slot], bytes);
+                    continue;
+                }
+                const int row_t = t == n - 1 ? row_k : row_v;   // K of tile t + 1 has gone before, but for the last
+                if (kFp8 || valid == kSharedTile) {
+                    load(&tm_v, row_t, &bar_full[at.slot], bytes);
                 } else {
-                    row_k += kSharedTile;
+                    // The rows past the last key (another prefix's, or nobody's) get
+                    // weight 0, but 0 * NaN would still reach O: zero them before the
+                    // products see the tile (FP8: the widening warps do).
+                    load(&tm_v, row_t, &sm->tail, bytes);
+                    if (lane == 0)
+                        sm->tail_issued = 1;
+                    if (!__all_sync(0xffffffffu, wait_phase(&sm->tail, 0, p, sm)))
+                        break;
+                    uint8_t *v = ring_ptr + at.slot * kBufBytes;
+                    for (int i = lane; i < (kSharedTile - valid) * 16; i += 32) {
+                        const int r = valid + i / 16, c = i % 16;
+                        const uint32_t off = (c >> 3) * TL::kHalf + (r >> 3) * TL::kGroup + (r & 7) * 128 +
+                                             (c & 7) * 16;
+                        *reinterpret_cast<uint4 *>(v + off) = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&bar_full[at.slot]));
                 }
             }
-            if (pos >= nb && !__all_sync(0xffffffffu, wait_phase(&bar_empty[at.slot], at.phase ^ 1, p, sm)))
-                break;
-            if (lane == 0)
-                sm->issued = pos + 1;
-            const int valid = min(sm->keys - t * kSharedTile, kSharedTile);
-            const uint32_t bytes = PAGED ? (valid + box - 1) / box * box * kRow : kTileBytes;
-            if (is_k) {
-                load(&tm_k, row_k, &bar_full[at.slot], bytes);
-                continue;
+        } else if (warp == kMmaWarp && ok) {
+            // ------------------------------------------------------ the products
+            // A wait that gave up is reported; the products then work on what there
+            // is, so that no branch depends on it.
+            constexpr uint32_t id_s = mma_idesc(128, kSharedTile, !kFp8, false);
+            constexpr uint32_t id_o = mma_idesc(128, kHeadDim, !kFp8, true);
+            const uint32_t leader = elect_one();
+            const bool two = q_tiles == 2;
+            const int steps0 = steps(0), steps1 = steps(1);
+            const uint32_t q_lo = smem_desc_lo(q_smem, 16);
+            const uint32_t k_lo = smem_desc_lo(ring, 16);
+            const uint32_t v_lo = smem_desc_lo(ring, TL::kHalf);
+            constexpr uint32_t q_hi = smem_desc_hi(1024), kv_hi = smem_desc_hi(TL::kGroup);
+            constexpr uint32_t kBuf16 = kBufBytes / 16;
+            Place k_at(0, nw), v_at(n > 1 ? 2 : 1, nw);
+            int k_tile = 0, v_tile = 0;
+            wait_phase(&sm->q_ready, 0, p, sm);
+            // S of stream s's next step: K of its tile; frees the buffer after the
+            // last stream that takes it.
+            auto scores = [&](int s) {
+                wait_phase(&sm->full[k_at.slot], k_at.phase, p, sm);
+                tcgen05_fence_after();
+                const uint32_t qa = q_lo + (two ? s : 0) * kBuf16, ka = k_lo + k_at.slot * kBuf16;
+#pragma unroll
+                for (int k = 0; k < 8; ++k)   // 16 head dimensions a step
+                    mma_ss(tmem + s * kStreamCols, qa + ((k >> 2) * kHalfBytes + (k & 3) * 32) / 16, q_hi,
+                           ka + ((k >> 2) * TL::kHalf + (k & 3) * 32) / 16, kv_hi, id_s, k > 0, leader);
+                tcgen05_commit(smem_addr(&sm->s_full[s]), leader);
+                if (!two || s == 1) {
+                    tcgen05_commit(smem_addr(&sm->empty[k_at.slot]), leader);
+                    k_at.advance(k_tile == 0 ? 1 : 2);
+                    ++k_tile;
+                }
+            };
+            // O += P V of stream s's step i, in two parts: each half of the keys is
+            // ready in two parts of 32.
+            const int run0 = shared_run(steps0), run1 = shared_run(steps1);
+            int anew[2] = {0, 0};   // the step at which O of a stream next starts anew
+            auto values = [&](int s, int i, bool last) {
+                const bool fresh = i == anew[s];
+                if (fresh)
+                    anew[s] += s ? run1 : run0;
+                wait_phase(&sm->full[v_at.slot], v_at.phase, p, sm);
+                const uint32_t pa = tmem + s * kStreamCols, va = v_lo + v_at.slot * kBuf16;
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    wait_phase(&sm->p_ready[s][part], i & 1, p, sm);
+                    tcgen05_fence_after();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {   // 16 keys a step, hi then lo
+                        const int k = (j >> 1) * 4 + part * 2 + (j & 1);
+                        const uint32_t vk = va + k * 2 * TL::kGroup / 16;
+                        mma_ts(pa + 128, pa + 16 * k, vk, kv_hi, id_o, !fresh || part > 0 || j > 0, leader);
+                        mma_ts(pa + 128, pa + 16 * k + 8, vk, kv_hi, id_o, 1, leader);
+                    }
+                }
+                if (!two || s == 1) {
+                    tcgen05_commit(smem_addr(&sm->empty[v_at.slot]), leader);
+                    v_at.advance(v_tile == n - 2 ? 1 : 2);
+                    ++v_tile;
+                }
+                if (last)
+                    tcgen05_commit(smem_addr(&sm->o_done[s]), leader);
+            };
+            scores(0);
+            if (steps1 > 0)
+                scores(1);
+            for (int i = 0; i < steps0; ++i) {
+                values(0, i, i == steps0 - 1);
+                if (i + 1 < steps0)
+                    scores(0);
+                if (i < steps1)
+                    values(1, i, i == steps1 - 1);
+                if (i + 1 < steps1)
+                    scores(1);
             }
-            const int row_t = t == n - 1 ? row_k : row_v;   // K of tile t + 1 has gone before, but for the last
-            if (kFp8 || valid == kSharedTile) {
-                load(&tm_v, row_t, &bar_full[at.slot], bytes);
-            } else {
-                // The rows past the last key (another prefix's, or nobody's) get
-                // weight 0, but 0 * NaN would still reach O: zero them before the
-                // products see the tile (FP8: the widening warps do).
-                load(&tm_v, row_t, &sm->tail, bytes);
-                if (lane == 0)
-                    sm->tail_issued = 1;
-                if (!__all_sync(0xffffffffu, wait_phase(&sm->tail, 0, p, sm)))
+            // whatever the others saw, the products in flight end before tensor
+            // memory is freed
+            tcgen05_commit(smem_addr(&sm->drain), leader);
+            mbar_wait(smem_addr(&sm->drain), 0, kDrainTimeoutNs);
+            __syncwarp();
+        } else if (kFp8 && warp >= kWidenWarp && warp < kWidenWarp + kWidenWarps && ok) {
+            // ------------------------------------- FP8: raw tiles to f16 operands
+            // A unit of work is 8 rows of one half of the head, 16 values a lane: a raw
+            // row is 8 chunks of 16 bytes, chunk c at c ^ (row % 8), and becomes two
+            // chunks of the operand's half c / 4.  The lanes of a quarter warp are two
+            // rows r and r ^ 5 and four chunks, which meet no bank twice on either side.
+            // All of a warp's units of a tile are loaded before the first is stored.
+            constexpr int kUnits = 2 * kSharedTile / 8, kMine = (kUnits + kWidenWarps - 1) / kWidenWarps;
+            const uint8_t *raw0 = ring_ptr + kWideBuffers * kBufBytes;
+            const int me = warp - kWidenWarp;
+            const int r8 = (lane >> 3) ^ (((lane >> 2) & 1) * 5), cc = lane & 3;
+            // the lane's chunk within its 8-row group: raw, and the first of its two of the operand
+            const uint32_t lane_src = r8 * 128 + ((cc ^ r8) << 4), lane_dst = r8 * 128 + (((2 * cc) ^ r8) << 4);
+            Place from(0, nb), to(0, kWideBuffers);
+            for (int pos = 0; pos < 2 * n; ++pos, from.advance(1), to.advance(1)) {
+                bool is_k;
+                const int t = at_pos(pos, is_k);
+                const int valid = sm->keys - t * kSharedTile;
+                bool go = wait_phase(&sm->raw_full[from.slot], from.phase, p, sm);
+                if (go && pos >= kWideBuffers)
+                    go = wait_phase(&sm->empty[to.slot], to.phase ^ 1, p, sm);
+                if (!__all_sync(0xffffffffu, go))
                     break;
-                uint8_t *v = ring_ptr + at.slot * kBufBytes;
-                for (int i = lane; i < (kSharedTile - valid) * 16; i += 32) {
-                    const int r = valid + i / 16, c = i % 16;
-                    const uint32_t off = (c >> 3) * TL::kHalf + (r >> 3) * TL::kGroup + (r & 7) * 128 + (c & 7) * 16;
-                    *reinterpret_cast<uint4 *>(v + off) = make_uint4(0u, 0u, 0u, 0u);
+                const uint8_t *src = raw0 + from.slot * kRawBytes;
+                uint8_t *dst = ring_ptr + to.slot * kBufBytes;
+                const int first = is_k ? kSharedTile : valid;   // V rows from here on are past the last key
+                uint4 x[kMine];
+#pragma unroll
+                for (int j = 0; j < kMine; ++j) {
+                    const int u = me + j * kWidenWarps;   // 8 rows u / 2, half u % 2
+                    if (u < kUnits)
+                        x[j] = *reinterpret_cast<const uint4 *>(src + (u >> 1) * 1024 + (((u & 1) * 64) ^ lane_src));
+                }
+#pragma unroll
+                for (int j = 0; j < kMine; ++j) {
+                    const int u = me + j * kWidenWarps;
+                    if (u < kUnits) {
+                        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                        uint32_t f[8];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+                                "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+                                : "=r"(f[2 * q]), "=r"(f[2 * q + 1])
+                                : "r"(w[q]));
+                        if ((u >> 1) * 8 + r8 >= first) {
+#pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                f[q] = 0u;
+                        }
+                        uint8_t *d = dst + (u & 1) * kHalfBytes + (u >> 1) * 1024;
+                        *reinterpret_cast<uint4 *>(d + lane_dst) = make_uint4(f[0], f[1], f[2], f[3]);
+                        *reinterpret_cast<uint4 *>(d + (lane_dst ^ 16)) = make_uint4(f[4], f[5], f[6], f[7]);
+                    }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&bar_full[at.slot]));
-            }
-        }
-    } else if (warp == kMmaWarp && ok) {
-        // ------------------------------------------------------ the products
-        // A wait that gave up is reported; the products then work on what there
-        // is, so that no branch depends on it.
-        constexpr uint32_t id_s = mma_idesc(128, kSharedTile, !kFp8, false);
-        constexpr uint32_t id_o = mma_idesc(128, kHeadDim, !kFp8, true);
-        const uint32_t leader = elect_one();
-        const bool two = q_tiles == 2;
-        const int steps0 = steps(0), steps1 = steps(1);
-        const uint32_t q_lo = smem_desc_lo(q_smem, 16);
-        const uint32_t k_lo = smem_desc_lo(ring, 16);
-        const uint32_t v_lo = smem_desc_lo(ring, TL::kHalf);
-        constexpr uint32_t q_hi = smem_desc_hi(1024), kv_hi = smem_desc_hi(TL::kGroup);
-        constexpr uint32_t kBuf16 = kBufBytes / 16;
-        Place k_at(0, nw), v_at(n > 1 ? 2 : 1, nw);
-        int k_tile = 0, v_tile = 0;
-        wait_phase(&sm->q_ready, 0, p, sm);
-        // S of stream s's next step: K of its tile; frees the buffer after the
-        // last stream that takes it.
-        auto scores = [&](int s) {
-            wait_phase(&sm->full[k_at.slot], k_at.phase, p, sm);
-            tcgen05_fence_after();
-            const uint32_t qa = q_lo + (two ? s : 0) * kBuf16, ka = k_lo + k_at.slot * kBuf16;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)   // 16 head dimensions a step
-                mma_ss(tmem + s * kStreamCols, qa + ((k >> 2) * kHalfBytes + (k & 3) * 32) / 16, q_hi,
-                       ka + ((k >> 2) * TL::kHalf + (k & 3) * 32) / 16, kv_hi, id_s, k > 0, leader);
-            tcgen05_commit(smem_addr(&sm->s_full[s]), leader);
-            if (!two || s == 1) {
-                tcgen05_commit(smem_addr(&sm->empty[k_at.slot]), leader);
-                k_at.advance(k_tile == 0 ? 1 : 2);
-                ++k_tile;
-            }
-        };
-        // O += P V of stream s's step i, in two parts: each half of the keys is
-        // ready in two parts of 32.
-        const int run0 = shared_run(steps0), run1 = shared_run(steps1);
-        int anew[2] = {0, 0};   // the step at which O of a stream next starts anew
-        auto values = [&](int s, int i, bool last) {
-            const bool fresh = i == anew[s];
-            if (fresh)
-                anew[s] += careful ? steps0 : s ? run1 : run0;
-            wait_phase(&sm->full[v_at.slot], v_at.phase, p, sm);
-            const uint32_t pa = tmem + s * kStreamCols, va = v_lo + v_at.slot * kBuf16;
-#pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                wait_phase(&sm->p_ready[s][part], i & 1, p, sm);
-                tcgen05_fence_after();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {   // 16 keys a step, hi then lo
-                    const int k = (j >> 1) * 4 + part * 2 + (j & 1);
-                    const uint32_t vk = va + k * 2 * TL::kGroup / 16;
-                    mma_ts(pa + 128, pa + 16 * k, vk, kv_hi, id_o, !fresh || part > 0 || j > 0, leader);
-                    mma_ts(pa + 128, pa + 16 * k + 8, vk, kv_hi, id_o, 1, leader);
+                if (lane == 0) {
+                    mbar_arrive(smem_addr(&sm->raw_empty[from.slot]));
+                    mbar_arrive(smem_addr(&sm->full[to.slot]));
                 }
             }
-            if (!two || s == 1) {
-                tcgen05_commit(smem_addr(&sm->empty[v_at.slot]), leader);
-                v_at.advance(v_tile == n - 2 ? 1 : 2);
-                ++v_tile;
-            }
-            if (last)
-                tcgen05_commit(smem_addr(&sm->o_done[s]), leader);
-        };
-        scores(0);
-        if (steps1 > 0)
-            scores(1);
-        for (int i = 0; i < steps0; ++i) {
-            values(0, i, i == steps0 - 1);
-            if (i + 1 < steps0)
-                scores(0);
-            if (i < steps1)
-                values(1, i, i == steps1 - 1);
-            if (i + 1 < steps1)
-                scores(1);
-        }
-        // whatever the others saw, the products in flight end before tensor
-        // memory is freed
-        tcgen05_commit(smem_addr(&sm->drain), leader);
-        mbar_wait(smem_addr(&sm->drain), 0, kDrainTimeoutNs);
-        __syncwarp();
-    } else if (kFp8 && warp >= kWidenWarp && warp < kWidenWarp + kWidenWarps && ok) {
-        // ------------------------------------- FP8: raw tiles to f16 operands
-        // A unit of work is 8 rows of one half of the head, 16 values a lane: a raw
-        // row is 8 chunks of 16 bytes, chunk c at c ^ (row % 8), and becomes two
-        // chunks of the operand's half c / 4.  The lanes of a quarter warp are two
-        // rows r and r ^ 5 and four chunks, which meet no bank twice on either side.
-        // All of a warp's units of a tile are loaded before the first is stored.
-        constexpr int kUnits = 2 * kSharedTile / 8, kMine = (kUnits + kWidenWarps - 1) / kWidenWarps;
-        const uint8_t *raw0 = ring_ptr + kWideBuffers * kBufBytes;
-        const int me = warp - kWidenWarp;
-        const int r8 = (lane >> 3) ^ (((lane >> 2) & 1) * 5), cc = lane & 3;
-        // the lane's chunk within its 8-row group: raw, and the first of its two of the operand
-        const uint32_t lane_src = r8 * 128 + ((cc ^ r8) << 4), lane_dst = r8 * 128 + (((2 * cc) ^ r8) << 4);
-        Place from(0, nb), to(0, kWideBuffers);
-        for (int pos = 0; pos < 2 * n; ++pos, from.advance(1), to.advance(1)) {
-            bool is_k;
-            const int t = at_pos(pos, is_k);
-            const int valid = sm->keys - t * kSharedTile;
-            bool go = wait_phase(&sm->raw_full[from.slot], from.phase, p, sm);
-            if (go && pos >= kWideBuffers)
-                go = wait_phase(&sm->empty[to.slot], to.phase ^ 1, p, sm);
-            if (!__all_sync(0xffffffffu, go))
-                break;
-            const uint8_t *src = raw0 + from.slot * kRawBytes;
-            uint8_t *dst = ring_ptr + to.slot * kBufBytes;
-            const int first = is_k ? kSharedTile : valid;   // V rows from here on are past the last key
-            uint4 x[kMine];
-#pragma unroll
-            for (int j = 0; j < kMine; ++j) {
-                const int u = me + j * kWidenWarps;   // 8 rows u / 2, half u % 2
-                if (u < kUnits)
-                    x[j] = *reinterpret_cast<const uint4 *>(src + (u >> 1) * 1024 + (((u & 1) * 64) ^ lane_src));
-            }
-#pragma unroll
-            for (int j = 0; j < kMine; ++j) {
-                const int u = me + j * kWidenWarps;
-                if (u < kUnits) {
-                    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                    uint32_t f[8];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-                            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-                            : "=r"(f[2 * q]), "=r"(f[2 * q + 1])
-                            : "r"(w[q]));
-                    if ((u >> 1) * 8 + r8 >= first) {
-#pragma unroll
-                        for (int q = 0; q < 8; ++q)
-                            f[q] = 0u;
-                    }
-                    uint8_t *d = dst + (u & 1) * kHalfBytes + (u >> 1) * 1024;
-                    *reinterpret_cast<uint4 *>(d + lane_dst) = make_uint4(f[0], f[1], f[2], f[3]);
-                    *reinterpret_cast<uint4 *>(d + (lane_dst ^ 16)) = make_uint4(f[4], f[5], f[6], f[7]);
-                }
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) {
-                mbar_arrive(smem_addr(&sm->raw_empty[from.slot]));
-                mbar_arrive(smem_addr(&sm->full[to.slot]));
-            }
-        }
-    } else if (warp < kProducerWarp) {
-        // -------------------------------------------------------- the softmax
-        const int s = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
-        const int trow = quad * 32 + lane;   // row of the stream's tile: lane of tensor memory
-        const uint32_t s_col = tmem + ((uint32_t)quad << 21) + s * kStreamCols + half * 64, o_col = s_col + 128;
-        const int pair_bar = 2 + s * 4 + quad;   // barrier of the two warps that share rows
-        const bool two = q_tiles == 2;
-        float factor = p.scale, v_scale = 1.f;
-        if constexpr (kFp8) {
-            factor *= ok ? __ldcg(p.k_scale + sm->kvh) : 1.f;
-            v_scale = ok ? __ldcg(p.v_scale + sm->kvh) : 1.f;
-        }
-        if (ok && !careful) {
-            // Q rows into shared memory, [half][128 rows][128 bytes] a tile; a
-            // negative factor of the scores turns q around.
-            const uint32_t flip = factor < 0.f ? 0x80008000u : 0u;
-            for (int i = tid; i < q_tiles * kSharedQRows * 16; i += kSoftmaxThreads) {
-                const int r = i >> 4, ch = i & 15;
-                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                if (r < sm->rows) {
-                    const int gr = sm->row0 + r;
-                    const int64_t row = (int64_t)(sm->req0 + gr / p.group) * p.num_qo_heads + sm->kvh * p.group +
-                                        gr % p.group;
-                    v = __ldcg(reinterpret_cast<const uint4 *>(p.q + row * kHeadDim) + ch);
-                }
-                v.x ^= flip;
-                v.y ^= flip;
-                v.z ^= flip;
-                v.w ^= flip;
-                if constexpr (kFp8) {
-                    // to f16, times the power of two that puts the row's largest
-                    // magnitude in [2^8, 2^9): exact down to 2^-22 of it
-                    uint32_t w[4] = {v.x, v.y, v.z, v.w};
-                    float amax = 0.f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 a = bf16x2_to_float2(w[j]);
-                        amax = fmaxf(amax, fmaxf(fabsf(a.x), fabsf(a.y)));
-                    }
-#pragma unroll
-                    for (int o = 1; o < 16; o <<= 1)
-                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                    int sh = 0;
-                    if (amax > 0.f) {
-                        int e;
-                        frexpf(amax, &e);
-                        sh = min(max(9 - e, -100), 100);
-                    }
-                    const float up = __int_as_float((127 + sh) << 23);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 a = bf16x2_to_float2(w[j]);
-                        w[j] = pack2<DT>(make_float2(a.x * up, a.y * up));
-                    }
-                    v = make_uint4(w[0], w[1], w[2], w[3]);
-                    if (ch == 0)
-                        sm->q_scale[r] = __int_as_float((127 - sh) << 23);
-                }
-                const int rr = r & 127;
-                *reinterpret_cast<uint4 *>(smem + (r >> 7) * kBufBytes + (ch >> 3) * kHalfBytes + rr * 128 +
-                                           (((ch & 7) ^ (rr & 7)) << 4)) = v;
-            }
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-        }
-        __syncwarp();
-        if (lane == 0 && ok)
-            mbar_arrive(smem_addr(&sm->q_ready));
-        // log2 e times the factor of the scores; never 0, so that a masked score
-        // (-inf) stays -inf
-        if (!careful) {
-            c2 = fabsf(factor) * kLog2e;
+        } else if (warp < kProducerWarp) {
+            // -------------------------------------------------------- the softmax
+            const int s = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
+            const int trow = quad * 32 + lane;   // row of the stream's tile: lane of tensor memory
+            const uint32_t s_col = tmem + ((uint32_t)quad << 21) + s * kStreamCols + half * 64, o_col = s_col + 128;
+            const int pair_bar = 2 + s * 4 + quad;   // barrier of the two warps that share rows
+            const bool two = q_tiles == 2;
+            float factor = p.scale, v_scale = 1.f;
             if constexpr (kFp8) {
-                barrier(1, kSoftmaxThreads);   // q_scale is written
-                c2 *= sm->q_scale[(two ? s * kSharedQRows : 0) + trow];
-                barrier(1, kSoftmaxThreads);   // row_max takes its place
+                factor *= ok ? __ldcg(p.k_scale + sm->kvh) : 1.f;
+                v_scale = ok ? __ldcg(p.v_scale + sm->kvh) : 1.f;
             }
-            c2 = c2 == 0.f ? 1.17549435e-38f : c2;
-        }
-        // FP8: weights are 2^7 times larger, which keeps seven more bits of the
-        // small ones in f16; it cancels in O
-        constexpr float kBias = kFp8 ? 7.f : 0.f;
-        // Where the thread adds up its 64 values of O (see kFlush): 16 bytes of each
-        // of the stream's rows side by side, so that a warp writes whole lines.
-        const bool flushed = !careful && steps(s) > kFlush;
-        const int run = shared_run(steps(s));
-        int next_flush = run;
-        float *my_flush = p.flush + (((int64_t)blockIdx.x * 2 + s) * 32 + half * 16) * (4 * kSharedQRows) + 4 * trow;
-        float m_ref = -INFINITY, l = 0.f;   // what the weights refer to (a raw score), their sum
-        float most = 0.f;                   // FP8: the largest weight
-        bool go = ok;
-        // 16 scores to weights, over their columns: hi in the first 8, lo in the others
-        auto weights = [&](const uint32_t (&r)[16], int j16, float off, float2 &sum) {
-            const float2 c22 = make_float2(c2, c2), off2 = make_float2(off, off);
-            uint32_t hi[8], lo[8];
+            if (ok && !careful) {
+                // Q rows into shared memory, [half][128 rows][128 bytes] a tile; a
+                // negative factor of the scores turns q around.
+                const uint32_t flip = factor < 0.f ? 0x80008000u : 0u;
+                for (int i = tid; i < q_tiles * kSharedQRows * 16; i += kSoftmaxThreads) {
+                    const int r = i >> 4, ch = i & 15;
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < sm->rows) {
+                        const int gr = sm->row0 + r;
+                        const int64_t row = (int64_t)(sm->req0 + gr / p.group) * p.num_qo_heads + sm->kvh * p.group +
+                                            gr % p.group;
+                        v = __ldcg(reinterpret_cast<const uint4 *>(p.q + row * kHeadDim) + ch);
+                    }
+                    v.x ^= flip;
+                    v.y ^= flip;
+                    v.z ^= flip;
+                    v.w ^= flip;
+                    if constexpr (kFp8) {
+                        // to f16, times the power of two that puts the row's largest
+                        // magnitude in [2^8, 2^9): exact down to 2^-22 of it
+                        uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                        float amax = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 x = fma2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), c22, off2);
-                const float2 w = make_float2(ex2(x.x), ex2(x.y));
-                sum = add2(sum, w);
-                if constexpr (kFp8)
-                    most = fmaxf(most, fmaxf(w.x, w.y));
-                hi[j] = pack2<DT>(w);
-                const float2 h = unpack2<DT>(hi[j]);
-                lo[j] = pack2<DT>(fma2(h, make_float2(-1.f, -1.f), w));
-            }
-            tmem_st8(s_col + 16 * j16, hi);
-            tmem_st8(s_col + 16 * j16 + 8, lo);
-        };
-        auto publish = [&](int part) {
-            tmem_wait_st();
-            tcgen05_fence_before();
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive(smem_addr(&sm->p_ready[s][part]));
-        };
-        auto load = [&](uint32_t (&r)[16], int j16) { tmem_ld16(s_col + 16 * j16, r); };
-        auto ready = [&](uint32_t (&r)[16], int valid) {   // loaded, scores past the last key masked
-            tmem_wait_ld();
-            settle(r);
-            if (valid < 16) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    if (j >= valid)
-                        r[j] = 0xff800000u;
-            }
-        };
-        // All 64 scores to weights, the next 16 on their way meanwhile.
-        auto step = [&](uint32_t (&r0)[16], uint32_t (&r1)[16], int valid, float off) {   // r0: loaded
-            float2 sum = make_float2(0.f, 0.f);
-            ready(r0, valid);
-            load(r1, 1);
-            weights(r0, 0, off, sum);
-            ready(r1, valid - 16);
-            load(r0, 2);
-            weights(r1, 1, off, sum);
-            publish(0);
-            ready(r0, valid - 32);
-            load(r1, 3);
-            weights(r0, 2, off, sum);
-            ready(r1, valid - 48);
-            weights(r1, 3, off, sum);
-            publish(1);
-            l += sum.x + sum.y;
-        };
-        for (int i = 0; i < steps(s); ++i) {
-            // After an error the steps go on without work, so that the barriers
-            // of a row's two warps always meet.
-            if (go)
-                go = __all_sync(0xffffffffu, wait_phase(&sm->s_full[s], i & 1, p, sm));
-            const int t = two ? i : 2 * i + s;
-            const int valid = sm->keys - t * kSharedTile - half * 64;
-            uint32_t r0[16], r1[16];
-            if (i > 0 && !careful) {
-                if (go) {
-                    tcgen05_fence_after();
-                    if (i == next_flush) {   // O of the steps so far: their products are done
-#pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
-                            tmem_ld16(o_col + 16 * c, r0);
-                            tmem_wait_ld();
-                            settle(r0);
-                            flush16(my_flush + c * (16 * kSharedQRows), r0, i > run);
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 a = bf16x2_to_float2(w[j]);
+                            amax = fmaxf(amax, fmaxf(fabsf(a.x), fabsf(a.y)));
                         }
-                        next_flush += run;
+#pragma unroll
+                        for (int o = 1; o < 16; o <<= 1)
+                            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                        int sh = 0;
+                        if (amax > 0.f) {
+                            int e;
+                            frexpf(amax, &e);
+                            sh = min(max(9 - e, -100), 100);
+                        }
+                        const float up = __int_as_float((127 + sh) << 23);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 a = bf16x2_to_float2(w[j]);
+                            w[j] = pack2<DT>(make_float2(a.x * up, a.y * up));
+                        }
+                        v = make_uint4(w[0], w[1], w[2], w[3]);
+                        if (ch == 0)
+                            sm->q_scale[r] = __int_as_float((127 - sh) << 23);
                     }
-                    load(r0, 0);
-                    step(r0, r1, valid, kBias - m_ref * c2);
+                    const int rr = r & 127;
+                    *reinterpret_cast<uint4 *>(smem + (r >> 7) * kBufBytes + (ch >> 3) * kHalfBytes + rr * 128 +
+                                               (((ch & 7) ^ (rr & 7)) << 4)) = v;
                 }
-                continue;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
-            // The first step, and every careful one: a row's maximum is that of
-            // both halves of its keys.
-            float mt = -INFINITY;
-            bool raise = false;
-            if (go) {
-                tcgen05_fence_after();
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    load(r0, c);
-                    ready(r0, valid - 16 * c);
-#pragma unroll
-                    for (int j = 0; j < 16; ++j)
-                        mt = fmaxf(mt, __uint_as_float(r0[j]));
+            __syncwarp();
+            if (lane == 0 && ok)
+                mbar_arrive(smem_addr(&sm->q_ready));
+            // log2 e times the factor of the scores; never 0, so that a masked score
+            // (-inf) stays -inf
+            if (!careful) {
+                c2 = fabsf(factor) * kLog2e;
+                if constexpr (kFp8) {
+                    barrier(1, kSoftmaxThreads);   // q_scale is written
+                    c2 *= sm->q_scale[(two ? s * kSharedQRows : 0) + trow];
+                    barrier(1, kSoftmaxThreads);   // row_max takes its place
                 }
-                raise = mt > m_ref && (m_ref == -INFINITY || (mt - m_ref) * c2 > kRaise);
+                c2 = c2 == 0.f ? 1.17549435e-38f : c2;
             }
-            if (barrier_or(pair_bar, 64, raise)) {
-                sm->row_max[s][half][trow] = mt;
-                barrier(pair_bar, 64);
-                const float both = fmaxf(mt, sm->row_max[s][half ^ 1][trow]);
-                const bool up = both > m_ref && (m_ref == -INFINITY || (both - m_ref) * c2 > kRaise);
-                const float m_new = up ? both : m_ref;
-                const float f = m_ref == -INFINITY ? 0.f : ex2((m_ref - m_new) * c2);
-                l *= f;
-                m_ref = m_new;
-                if (i > 0 && go) {   // the products up to the last step are done: s_full followed them
-#pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
-                        uint32_t o[16];
-                        tmem_ld16(o_col + 16 * c, o);
-                        tmem_wait_ld();
-                        settle(o);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                        tmem_st16(o_col + 16 * c, o);
-                    }
-                }
-                barrier(pair_bar, 64);   // row_max is read before the next step writes it
-            }
-            if (!go)
-                continue;
-            load(r0, 0);
-            // a row whose scores are all -inf so far keeps weights of 0
-            step(r0, r1, valid, (m_ref == -INFINITY ? 0.f : -m_ref * c2) + kBias);
-        }
-        // Out of range: a weight too large for its type, or no score to refer to
-        // in the first tile.
-        if (go && !careful && steps(s) > 0 && (m_ref == -INFINITY || (kFp8 ? most : l) > kMostWeight<DT>))
-            sm->redo = 1;
-        // ----------------------------------------------------- the partial
-        for (int x = 0; x < 2; ++x)   // both streams' products are done with the ring
-            if (go && steps(x) > 0)
-                go = __all_sync(0xffffffffu, wait_phase(&sm->o_done[x], 0, p, sm));
-        tcgen05_fence_after();
-        barrier(1, kSoftmaxThreads);
-        if (careful || !sm->redo) {
-        float *stage = reinterpret_cast<float *>(smem);   // [q_tiles * 128][kOutStride]
-        SharedEnd *end = reinterpret_cast<SharedEnd *>(smem + kEndOffset);
-        float *mine = stage + ((two ? s * kSharedQRows : 0) + trow) * kOutStride + half * 64;
-        if (go)
-            end->row_sum[s][half][trow] = l;
-        if (!two && s == 1) {
-            // one row tile: stream 1 hands its state to stream 0
-            if (go && half == 0)
-                end->row_ref[trow] = m_ref;
-            if (go && steps(1) > 0) {
+            // FP8: weights are 2^7 times larger, which keeps seven more bits of the
+            // small ones in f16; it cancels in O
+            constexpr float kBias = kFp8 ? 7.f : 0.f;
+            // Where the thread adds up its 64 values of O (see kFlush): 16 bytes of each
+            // of the stream's rows side by side, so that a warp writes whole lines.
+            const bool flushed = steps(s) > kFlush;
+            const int run = shared_run(steps(s));
+            int next_flush = run;
+            float *my_flush = p.flush + (((int64_t)blockIdx.x * 2 + s) * 32 + half * 16) * (4 * kSharedQRows) +
+                              4 * trow;
+            auto flush = [&](int i) {   // O of the steps before step i: their products are done
 #pragma unroll 1
                 for (int c = 0; c < 4; ++c) {
                     uint32_t o[16];
                     tmem_ld16(o_col + 16 * c, o);
                     tmem_wait_ld();
                     settle(o);
-                    if (flushed)
-                        add_flushed16(my_flush + c * (16 * kSharedQRows), o);
-#pragma unroll
-                    for (int j = 0; j < 16; j += 4)
-                        *reinterpret_cast<uint4 *>(mine + 16 * c + j) = make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                    flush16(my_flush + c * (16 * kSharedQRows), o, i > run);
                 }
-            }
-        }
-        barrier(1, kSoftmaxThreads);
-        if (go && (two || s == 0)) {
-            float f0 = 1.f, f1 = 0.f, m = m_ref, den = end->row_sum[s][0][trow] + end->row_sum[s][1][trow];
-            const bool join = !two && steps(1) > 0;
-            if (join) {
-                const float m1 = end->row_ref[trow], l1 = end->row_sum[1][0][trow] + end->row_sum[1][1][trow];
-                m = fmaxf(m_ref, m1);
-                f0 = m_ref == -INFINITY ? 0.f : ex2((m_ref - m) * c2);
-                f1 = m1 == -INFINITY ? 0.f : ex2((m1 - m) * c2);
-                den = den * f0 + l1 * f1;
-            }
-            const float inv = v_scale / den;
-            f0 *= inv;
-            f1 *= inv;
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-                uint32_t o[16];
-                tmem_ld16(o_col + 16 * c, o);
+                next_flush += run;
+            };
+            float m_ref = -INFINITY, l = 0.f;   // what the weights refer to (a raw score), their sum
+            float most = 0.f;                   // FP8: the largest weight
+            bool go = ok;
+            // 16 scores to weights, over their columns: hi in the first 8, lo in the others
+            auto weights = [&](const uint32_t (&r)[16], int j16, float off, float2 &sum) {
+                const float2 c22 = make_float2(c2, c2), off2 = make_float2(off, off);
+                uint32_t hi[8], lo[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float2 score = make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                    const float2 x = fma2(score, c22, off2);
+                    const float2 w = make_float2(ex2(x.x), ex2(x.y));
+                    sum = add2(sum, w);
+                    if constexpr (kFp8)
+                        most = fmaxf(most, fmaxf(w.x, w.y));
+                    hi[j] = pack2<DT>(w);
+                    const float2 h = unpack2<DT>(hi[j]);
+                    lo[j] = pack2<DT>(fma2(h, make_float2(-1.f, -1.f), w));
+                }
+                tmem_st8(s_col + 16 * j16, hi);
+                tmem_st8(s_col + 16 * j16 + 8, lo);
+            };
+            auto publish = [&](int part) {
+                tmem_wait_st();
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&sm->p_ready[s][part]));
+            };
+            auto load = [&](uint32_t (&r)[16], int j16) { tmem_ld16(s_col + 16 * j16, r); };
+            auto ready = [&](uint32_t (&r)[16], int valid) {   // loaded, scores past the last key masked
                 tmem_wait_ld();
-                settle(o);
-                if (flushed)
-                    add_flushed16(my_flush + c * (16 * kSharedQRows), o);
+                settle(r);
+                if (valid < 16) {
 #pragma unroll
-                for (int j = 0; j < 16; j += 4) {
-                    float4 v = make_float4(__uint_as_float(o[j]) * f0, __uint_as_float(o[j + 1]) * f0,
-                                           __uint_as_float(o[j + 2]) * f0, __uint_as_float(o[j + 3]) * f0);
-                    float4 *d = reinterpret_cast<float4 *>(mine + 16 * c + j);
-                    if (join) {
-                        const float4 w = *d;
-                        v.x = fmaf(w.x, f1, v.x);
-                        v.y = fmaf(w.y, f1, v.y);
-                        v.z = fmaf(w.z, f1, v.z);
-                        v.w = fmaf(w.w, f1, v.w);
+                    for (int j = 0; j < 16; ++j)
+                        if (j >= valid)
+                            r[j] = 0xff800000u;
+                }
+            };
+            // All 64 scores to weights, the next 16 on their way meanwhile.
+            auto step = [&](uint32_t (&r0)[16], uint32_t (&r1)[16], int valid, float off) {   // r0: loaded
+                float2 sum = make_float2(0.f, 0.f);
+                ready(r0, valid);
+                load(r1, 1);
+                weights(r0, 0, off, sum);
+                ready(r1, valid - 16);
+                load(r0, 2);
+                weights(r1, 1, off, sum);
+                publish(0);
+                ready(r0, valid - 32);
+                load(r1, 3);
+                weights(r0, 2, off, sum);
+                ready(r1, valid - 48);
+                weights(r1, 3, off, sum);
+                publish(1);
+                l += sum.x + sum.y;
+            };
+            for (int i = 0; i < steps(s); ++i) {
+                // After an error the steps go on without work, so that the barriers
+                // of a row's two warps always meet.
+                if (go)
+                    go = __all_sync(0xffffffffu, wait_phase(&sm->s_full[s], i & 1, p, sm));
+                const int t = two ? i : 2 * i + s;
+                const int valid = sm->keys - t * kSharedTile - half * 64;
+                uint32_t r0[16], r1[16];
+                if (i > 0 && !careful) {
+                    if (go) {
+                        tcgen05_fence_after();
+                        if (i == next_flush)
+                            flush(i);
+                        load(r0, 0);
+                        step(r0, r1, valid, kBias - m_ref * c2);
                     }
-                    *d = v;
+                    continue;
+                }
+                // The first step, and every careful one: a row's maximum is that of
+                // both halves of its keys.
+                float mt = -INFINITY;
+                bool raise = false;
+                if (go) {
+                    tcgen05_fence_after();
+                    if (i == next_flush)
+                        flush(i);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        load(r0, c);
+                        ready(r0, valid - 16 * c);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            mt = fmaxf(mt, __uint_as_float(r0[j]));
+                    }
+                    raise = mt > m_ref && (m_ref == -INFINITY || (mt - m_ref) * c2 > kRaise);
+                }
+                if (barrier_or(pair_bar, 64, raise)) {
+                    sm->row_max[s][half][trow] = mt;
+                    barrier(pair_bar, 64);
+                    const float both = fmaxf(mt, sm->row_max[s][half ^ 1][trow]);
+                    const bool up = both > m_ref && (m_ref == -INFINITY || (both - m_ref) * c2 > kRaise);
+                    const float m_new = up ? both : m_ref;
+                    const float f = m_ref == -INFINITY ? 0.f : ex2((m_ref - m_new) * c2);
+                    l *= f;
+                    m_ref = m_new;
+                    if (i > 0 && go) {   // the products up to the last step are done: s_full followed them
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(o_col + 16 * c, o);
+                            tmem_wait_ld();
+                            settle(o);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st16(o_col + 16 * c, o);
+                            if (i >= run)
+                                scale_flushed16(my_flush + c * (16 * kSharedQRows), f);
+                        }
+                    }
+                    barrier(pair_bar, 64);   // row_max is read before the next step writes it
+                }
+                if (!go)
+                    continue;
+                load(r0, 0);
+                // a row whose scores are all -inf so far keeps weights of 0
+                step(r0, r1, valid, (m_ref == -INFINITY ? 0.f : -m_ref * c2) + kBias);
+            }
+            // Out of range: a weight too large for its type, or no score to refer to
+            // in the first tile.
+            if (go && !careful && steps(s) > 0 && (m_ref == -INFINITY || (kFp8 ? most : l) > kMostWeight<DT>))
+                sm->redo = 1;
+            // ----------------------------------------------------- the partial
+            for (int x = 0; x < 2; ++x)   // both streams' products are done with the ring
+                if (go && steps(x) > 0)
+                    go = __all_sync(0xffffffffu, wait_phase(&sm->o_done[x], 0, p, sm));
+            tcgen05_fence_after();
+            barrier(1, kSoftmaxThreads);
+            if (careful || !sm->redo) {
+                float *stage = reinterpret_cast<float *>(smem);   // [q_tiles * 128][kOutStride]
+                SharedEnd *end = reinterpret_cast<SharedEnd *>(smem + kEndOffset);
+                float *mine = stage + ((two ? s * kSharedQRows : 0) + trow) * kOutStride + half * 64;
+                if (go)
+                    end->row_sum[s][half][trow] = l;
+                if (!two && s == 1) {
+                    // one row tile: stream 1 hands its state to stream 0
+                    if (go && half == 0)
+                        end->row_ref[trow] = m_ref;
+                    if (go && steps(1) > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(o_col + 16 * c, o);
+                            tmem_wait_ld();
+                            settle(o);
+                            if (flushed)
+                                add_flushed16(my_flush + c * (16 * kSharedQRows), o);
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4)
+                                *reinterpret_cast<uint4 *>(mine + 16 * c + j) =
+                                    make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        }
+                    }
+                }
+                barrier(1, kSoftmaxThreads);
+                if (go && (two || s == 0)) {
+                    float f0 = 1.f, f1 = 0.f, m = m_ref, den = end->row_sum[s][0][trow] + end->row_sum[s][1][trow];
+                    const bool join = !two && steps(1) > 0;
+                    if (join) {
+                        const float m1 = end->row_ref[trow], l1 = end->row_sum[1][0][trow] + end->row_sum[1][1][trow];
+                        m = fmaxf(m_ref, m1);
+                        f0 = m_ref == -INFINITY ? 0.f : ex2((m_ref - m) * c2);
+                        f1 = m1 == -INFINITY ? 0.f : ex2((m1 - m) * c2);
+                        den = den * f0 + l1 * f1;
+                    }
+                    const float inv = v_scale / den;
+                    f0 *= inv;
+                    f1 *= inv;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[16];
+                        tmem_ld16(o_col + 16 * c, o);
+                        tmem_wait_ld();
+                        settle(o);
+                        if (flushed)
+                            add_flushed16(my_flush + c * (16 * kSharedQRows), o);
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            float4 v = make_float4(__uint_as_float(o[j]) * f0, __uint_as_float(o[j + 1]) * f0,
+                                                   __uint_as_float(o[j + 2]) * f0, __uint_as_float(o[j + 3]) * f0);
+                            float4 *d = reinterpret_cast<float4 *>(mine + 16 * c + j);
+                            if (join) {
+                                const float4 w = *d;
+                                v.x = fmaf(w.x, f1, v.x);
+                                v.y = fmaf(w.y, f1, v.y);
+                                v.z = fmaf(w.z, f1, v.z);
+                                v.w = fmaf(w.w, f1, v.w);
+                            }
+                            *d = v;
+                        }
+                    }
+                    const int r = (two ? s * kSharedQRows : 0) + trow;
+                    if (half == 0 && r < sm->rows) {
+                        const int gr = sm->row0 + r;
+                        const int64_t out = (int64_t)(gr / p.group) * p.num_qo_heads + sm->kvh * p.group + gr % p.group;
+                        p.partial_lse[sm->part_row + out * sm->part_stride] =
+                            den == 0.f ? -INFINITY : (m * c2 + log2f(den) - kBias) * kLn2;
+                    }
+                }
+                barrier(1, kSoftmaxThreads);
+                if (go) {   // whole rows, a warp at a time
+                    for (int r = warp; r < sm->rows; r += kSoftmaxThreads / 32) {
+                        const int gr = sm->row0 + r;
+                        const int64_t out = (int64_t)(gr / p.group) * p.num_qo_heads + sm->kvh * p.group + gr % p.group;
+                        const float4 v = *reinterpret_cast<const float4 *>(stage + r * kOutStride + 4 * lane);
+                        float *dst = p.partial_o + (sm->part_row + out * sm->part_stride) * kHeadDim;
+                        reinterpret_cast<float4 *>(dst)[lane] = v;
+                    }
                 }
             }
-            const int r = (two ? s * kSharedQRows : 0) + trow;
-            if (half == 0 && r < sm->rows) {
-                const int gr = sm->row0 + r;
-                const int64_t out = (int64_t)(gr / p.group) * p.num_qo_heads + sm->kvh * p.group + gr % p.group;
-                p.partial_lse[sm->part_row + out * sm->part_stride] =
-                    den == 0.f ? -INFINITY : (m * c2 + log2f(den) - kBias) * kLn2;
-            }
         }
-        barrier(1, kSoftmaxThreads);
-        if (go) {   // whole rows, a warp at a time
-            for (int r = warp; r < sm->rows; r += kSoftmaxThreads / 32) {
-                const int gr = sm->row0 + r;
-                const int64_t out = (int64_t)(gr / p.group) * p.num_qo_heads + sm->kvh * p.group + gr % p.group;
-                const float4 v = *reinterpret_cast<const float4 *>(stage + r * kOutStride + 4 * lane);
-                reinterpret_cast<float4 *>(p.partial_o + (sm->part_row + out * sm->part_stride) * kHeadDim)[lane] = v;
-            }
-        }
-        }
-    }
-    tcgen05_fence_before();
-    __syncthreads();
-    if (careful || !sm->redo || sm->abort)
-        break;
-    if (warp == kProducerWarp && lane == 0)
-        init_barriers(true);   // every phase of the first pass has completed
-    __syncthreads();
-    tcgen05_fence_after();
+        tcgen05_fence_before();
+        __syncthreads();
+        if (careful || !sm->redo || sm->abort)
+            break;
+        if (warp == kProducerWarp && lane == 0)
+            init_barriers(true);   // every phase of the first pass has completed
+        __syncthreads();
+        tcgen05_fence_after();
     }
     griddep_launch_dependents();
     if (p.has_suffix)

@@ -158,6 +158,45 @@ def test_long_splits(cuda_device, B, L):
     check(i, ragged(i, -(-L // 128) * 128), what=f"{B} x {L}")
 
 
+def levels(L):
+    """A key's first value when the queries' first value is the same for all: the
+    last third counts most, the others are 8.5 below it by SCALE with queries of
+    16 (in nats), the first three tiles 45, 40 and 30.  The weights of the first
+    pass, which refer to the first tile, leave their range."""
+    x = torch.zeros(L)
+    x[: L * 2 // 3] = -6.0
+    x[:128], x[128:256], x[256:384] = -32.0, -28.0, -21.0
+    return x
+
+
+@pytest.mark.parametrize("L", [1500, 6000, 12001])
+@pytest.mark.parametrize("B", [5, 64])
+def test_long_splits_out_of_range(cuda_device, B, L):
+    """One split whose first pass leaves the weights' range: the second raises
+    the maximum and goes over to fp32 sums as well."""
+    i = make(8, 2, [B], [L], np.zeros(B, int), seed=L, room=0)
+    i["q"][..., 0] = 16.0
+    i["kp"][:L, :, 0] = levels(L)[:, None].to(torch.bfloat16)
+    ref = reference(i)
+    check(i, ragged(i, -(-L // 128) * 128), ref, f"{B} x {L}")
+    check(i, paged(i, 16, -(-L // 128) * 128), ref, f"{B} x {L} paged")
+
+
+@pytest.mark.parametrize("B", [5, 64])
+def test_fp8_long_splits_out_of_range(cuda_device, B):
+    L = 6000
+    f = to_fp8(make(8, 2, [B], [L], np.full(B, 3), seed=7), seed=7)
+    sk = f["sk"].cpu()
+    f["q"][..., 0] = 1024.0   # the scales are up to 1 / 64
+    f["kp8"][:L, :, 0] = (levels(L)[:, None] * sk.sign()).to(torch.float8_e4m3fn).view(torch.uint8)
+    f["kpd"][:L, :, 0] = (levels(L)[:, None] * sk.abs()).double().numpy()
+    o, lse, status = ragged_fp8(f, -(-L // 128) * 128)
+    ref = fp8_reference(f)
+    assert status == 0
+    assert_within(errors(o.cpu().numpy(), lse.cpu().numpy(), *ref), max_abs=1e-4, rel_l2=1e-5,
+                  lse_abs=2e-5 * max(1.0, np.abs(ref[1]).max() / 16))
+
+
 @pytest.mark.parametrize("rows", [3, 40])
 def test_no_suffix_and_no_keys(cuda_device, rows):
     i = make(32, 8, [rows, 2], [700, 0], np.zeros(rows + 2, int), room=0)
@@ -332,6 +371,24 @@ def test_tables_beyond_the_plan_are_flagged(cuda_device):
         fd.decode_shared(p, d["q"], d["kp"], d["vp"], d["k"], d["v"], i32(req), i32(pre), i32(own_ip), SCALE,
                          workspace=ws)
         assert fd.get_device_status(ws) == code
+
+
+BIG = 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("req,pre", [
+    ([0, 4, 9], [0, 300, BIG]), ([0, 4, 9], [0, -1, 430]), ([0, 4, 9], [0, 500, 430]), ([0, 4, BIG], [0, 300, 430]),
+    ([0, -5, 9], [0, 300, 430]), ([5, 4, 9], [0, 300, 430]), ([0, 10, -BIG], [0, 300, 430]),
+    ([0, 4, 9], [-BIG, 300, 430]), ([-BIG, BIG, 9], [-BIG, BIG, 430]), ([0, 0, 9], [0, 0, 430]),
+])
+def test_torn_tables_are_flagged(cuda_device, req, pre):
+    """Tables that are no lists of lengths, or longer ones than the plan's."""
+    i = make(32, 8, [4, 5], [300, 130], np.zeros(9, int), room=0)
+    d = {n: i[n].cuda() for n in ("q", "kp", "vp")}
+    p = fd.plan_shared(9, 32, 8, D, [0, 4, 9], [0, 300, 430], 0, chunk=128)
+    ws = torch.zeros(p.workspace_bytes, dtype=torch.uint8, device="cuda")
+    fd.decode_shared(p, d["q"], d["kp"], d["vp"], None, None, i32(req), i32(pre), None, SCALE, workspace=ws)
+    assert fd.get_device_status(ws) == -6
 
 
 def test_page_outside_the_pool_is_flagged(cuda_device):
