@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
                 pos = __ldg(p.positions + t);
             const int64_t len = (int64_t)(e1 - e0 - 1) * p.page_size + last;
             const int64_t key = len - (a1 - t);
-            ok = t >= a0 && e0 >= 0 && e1 > e0 && e1 <= p.num_page_entries && last >= 1 &&
+            ok = t >= a0 && t < a1 && e0 >= 0 && e1 > e0 && e1 <= p.num_page_entries && last >= 1 &&
                  last <= p.page_size && key >= 0;
             if (ok) {
                 const int page = __ldg(p.kv_page_indices + e0 + (int)(key / p.page_size));

@@ -139,11 +139,11 @@ __device__ __forceinline__ Child read_child(const ForkParams &p, int i)
     Child c{0, 0, 0, -1, true};
     const int par = p.parent[i], a = p.new_indptr[i], e = p.new_indptr[i + 1];
     c.next = e - a;
-    c.ok = par >= -1 && par < p.old_batch && a >= 0 && c.next >= 0 && e <= p.new_entries;
+    c.ok = par >= -1 && par < p.old_batch && a >= 0 && e >= a && e <= p.new_entries;
     if (c.ok && par >= 0) {
         const int b = p.page_indptr[par], f = p.page_indptr[par + 1];
         c.have = f - b;
-        c.ok = b >= 0 && c.have >= 0 && f <= p.old_entries && c.have <= c.next;
+        c.ok = b >= 0 && f >= b && f <= p.old_entries && c.have <= c.next;
         if (c.ok && c.have > 0) {
             c.last = p.last_len[par];
             c.tail = p.indices[f - 1];

@@ -191,6 +191,22 @@ def test_tokens_outside_the_tables_are_skipped_and_flagged(cuda_device):
         assert fd.get_device_status(ws) == 0   # cleared
 
 
+@pytest.mark.parametrize("torn", [[0, 9, 1, 2], [0, 9, 1, 9], [5, 4, 8, 9], [-3, -2, -1, 0], [0, 4, 2 ** 31 - 1, 9]])
+def test_torn_append_lists_write_no_row_twice(cuda_device, torn):
+    """Lists that do not rise: a token whose request does not hold it is skipped
+    or flagged; every row written is one of a new key."""
+    i = make([0, 5, 2], [4, 4, 1], 2, 2, 16)
+    t, tables = to_dev(i, cuda_device)
+    tables[0] = torch.tensor(torn, dtype=torch.int32, device=cuda_device)
+    pools = [torch.zeros((i["num_pages"], 16, 2, D), dtype=torch.bfloat16, device=cuda_device) for _ in "kv"]
+    ws = torch.zeros(256, dtype=torch.uint8, device=cuda_device)
+    fd.append_paged(t["q"], t["k"], t["v"], *pools, *tables, workspace=ws)
+    assert fd.get_device_status(ws) == (0 if torn[-1] == 0 else -6)
+    pages = {int(x) for x in i["ids"] if x >= 0}
+    written = pools[0].view(i["num_pages"], -1).ne(0).any(1).nonzero().flatten().tolist()
+    assert set(written) <= pages
+
+
 def test_quantised_rows_of_zeros_infinities_and_nan(cuda_device):
     i = make([0], [4], 1, 1, 16)
     t, tables = to_dev(i, cuda_device)

@@ -139,6 +139,20 @@ def test_a_refused_fork_changes_nothing(cuda_device, what):
     assert np.all(got[0] == -1) and np.array_equal(got[1], refs) and np.all(got[2] == -1) and np.all(got[3] == -1)
 
 
+LOWEST = -2 ** 31
+
+
+@pytest.mark.parametrize("ip,nip", [
+    ([0, 2, 3], [0, LOWEST, 4, 5]), ([0, 2, 3], [1, LOWEST, 4, 5]), ([0, 2, 3], [3, 1, 4, 5]), ([0, 2, 3], [0, 6, 4, 5]),
+    ([1, LOWEST, 3], [0, 2, 4, 5]), ([3, 1, 3], [0, 2, 4, 5]), ([-1, 2, 3], [0, 2, 4, 5]),
+])
+def test_torn_tables_change_nothing(cuda_device, ip, nip):
+    last, ids, refs = np.array([3, 16]), np.array([4, 1, 2]), np.array([0, 1, 1, 0, 1, 0])
+    got, status = fork(np.array([0, 0, 1]), np.array(ip), last, ids, np.array(nip), refs, 16)
+    assert status == -6
+    assert np.all(got[0] == -1) and np.array_equal(got[1], refs) and np.all(got[2] == -1) and np.all(got[3] == -1)
+
+
 def compact_reference(refs, ids, limit):
     live = np.flatnonzero(refs > 0)
     limit = limit or len(live)
