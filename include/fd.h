@@ -470,8 +470,9 @@ int fd_plan_shared_paged(int batch, int num_qo_heads, int num_kv_heads, int head
  * key gets O = 0, LSE = -inf.  More suffix keys than the plan's room, prefix
  * tables beyond it, or a page outside [0, num_pages) set FD_ERR_DEVICE_BOUNDS
  * (the outputs are then not valid).  num_page_entries: entries of
- * kv_page_indices.  Workspace as for fd_decode: zeroed once, calls that share it
- * in the order of one stream.
+ * kv_page_indices.  O adds up in fp32 with weights of up to 2^40: V of up to 2^80
+ * in magnitude.  Workspace as for fd_decode: zeroed once, calls that share it in
+ * the order of one stream.
  */
 int fd_decode_shared(const fd_shared_plan *plan, const int32_t *prefix_req_indptr_dev,
                      const int32_t *prefix_indptr_dev, const int32_t *kv_indptr_dev, const void *q,
@@ -497,8 +498,8 @@ int fd_decode_shared_paged(const fd_shared_plan *plan, int num_pages,
 int fd_decode_shared_fp8(const fd_shared_plan *plan, const int32_t *prefix_req_indptr_dev,
                      const int32_t *prefix_indptr_dev, const int32_t *kv_indptr_dev, const void *q,
                      const void *k_prefix_fp8, const void *v_prefix_fp8, const void *k, const void *v,
-                     const float *k_scale, const float *v_scale, float scale, float *o, float *lse, void *workspace, int64_t workspace_bytes,
-                     void *stream);
+                     const float *k_scale, const float *v_scale, float scale, float *o, float *lse,
+                     void *workspace, int64_t workspace_bytes, void *stream);
 
 int fd_decode_shared_paged_fp8(const fd_shared_plan *plan, int num_pages,
                            const int32_t *prefix_req_indptr_dev,
@@ -628,7 +629,8 @@ int fd_append_paged_int4(int batch, int num_tokens, int num_qo_heads, int num_kv
  * shared prefix's) hold each page; 0 is a free page.  fd_fork_pages and
  * fd_compact_pages make the next tables and counts and list the page copies
  * they need; fd_copy_pages makes those copies in every pool (K and V of every
- * layer) at once.  new_page_refs may be page_refs itself.
+ * layer) at once.  new_page_refs may be page_refs itself; otherwise they share no
+ * memory.
  *
  * fd_pages_workspace_bytes -- the workspace of a fork or compaction (host
  * only).  new_batch: the fork's, 0 for a compaction.  The workspace need not be
@@ -656,7 +658,7 @@ int fd_pages_workspace_bytes(int num_pages, int new_batch, int64_t *bytes);
  * new_page_refs = page_refs, and the new indices and copies are -1.  Other page
  * ids outside the pool set FD_ERR_DEVICE_BOUNDS and become -1.
  * old_batch and new_batch up to 32768 (FD_ERR_UNSUPPORTED above).
- * kv_page_indices and new_page_indices must be different arrays.
+ * kv_page_indices and new_page_indices must not share memory.
  */
 int fd_fork_pages(int old_batch, int new_batch, int page_size, int num_pages,
                   const int32_t *parent_dev, const int32_t *kv_page_indptr_dev,
@@ -674,7 +676,7 @@ int fd_fork_pages(int old_batch, int new_batch, int page_size, int num_pages,
  * copy_src[r] -> copy_dst[r] is the r-th move (-1, -1 past the last), of at most
  * max_moves; the number of pages in use and that of free ones both bound it.
  * new_page_indices is kv_page_indices (every table of the pool, concatenated)
- * with the moved pages renamed; it may be the same array.  With more moves than
+ * with the moved pages renamed; it may be the same array (in part: refused).  With more moves than
  * free pages before the limit or than max_moves, nothing changes
  * (FD_ERR_NO_PAGES) and the copies are -1.
  */

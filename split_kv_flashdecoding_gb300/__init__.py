@@ -544,11 +544,15 @@ class _Same:
 _SAME = _Same()
 
 
-def _on(tensor):
-    """The tensor's device, made current for the call (launches go to the
-    current device; the default stream is that device's current one)."""
+def _on(tensor, stream=None):
+    """The tensor's device and the call's stream, made current for the call: its
+    launches go there, and what it allocates belongs to that stream."""
     if not tensor.is_cuda:
         raise FdError(-1, "the inputs must be CUDA tensors")
+    if stream is not None:
+        if stream.device != tensor.device:
+            raise FdError(-1, "the stream belongs to another device than the inputs")
+        return torch.cuda.stream(stream)
     return _SAME if tensor.get_device() == torch.cuda.current_device() else torch.cuda.device(tensor.device)
 
 
@@ -610,7 +614,7 @@ def _append(name, pool_dtypes, per_row, q, k, v, k_pages, v_pages, append_indptr
         raise FdError(-1, f"{name}: positions must have an entry for every token")
     num_pages, page_size = k_pages.shape[:2]
     i32, dev = torch.int32, k.get_device()
-    with _on(k):
+    with _on(k, stream):
         if q is not None and q_out is None:
             q_out = torch.empty((N, Hq, D), dtype=q.dtype, device=q.device)
         if q is not None and q_out.shape != q.shape:
@@ -690,7 +694,7 @@ def fork_pages(parent, kv_page_indptr, kv_last_page_len, kv_page_indices, new_pa
     n_new, n_old, pages = parent.numel(), kv_page_indptr.numel() - 1, page_refs.numel()
     if new_page_indptr.numel() != n_new + 1 or kv_last_page_len.numel() < n_old:
         raise FdError(-1, "fd_fork_pages: new_page_indptr must have new_batch+1 and kv_last_page_len batch entries")
-    with _on(like):
+    with _on(like, stream):
         at = like.device
         if new_page_indices is None:
             new_page_indices = torch.empty(new_page_entries, dtype=i32, device=at)
@@ -725,7 +729,7 @@ def compact_pages(page_refs, kv_page_indices, max_moves: int, *, limit: int = 0,
     copy_src, copy_dst); hand the last two (max_moves entries) to copy_pages."""
     i32, like, dev = torch.int32, page_refs, page_refs.get_device()
     pages, entries = page_refs.numel(), kv_page_indices.numel()
-    with _on(like):
+    with _on(like, stream):
         at = like.device
         if new_page_indices is None:
             new_page_indices = torch.empty(entries, dtype=i32, device=at)
@@ -767,11 +771,12 @@ def copy_pages(pools, src, dst, *, workspace=None, stream=None):
         ptrs[i], size[i] = x.data_ptr(), x.nbytes // max(pages, 1)
     if pages == 0:
         return
-    with _on(src):
+    with _on(src, stream):
         _check(lib().fd_copy_pages(n, ptrs, size, pages, src.numel(), _need("src", src, torch.int32, dev),
                                    _need("dst", dst, torch.int32, dev),
                                    *((None, 0) if workspace is None else _ws(workspace, dev)),
                                    _stream(stream)), "fd_copy_pages")
+
 
 def _host_ptr(a):
     return a.ctypes.data_as(ctypes.c_void_p)
@@ -842,7 +847,7 @@ def _maybe(what, t, dtype, dev):
 def _decode_shared(name, kv_dtypes, plan_, q, k_prefix, v_prefix, k, v, scales, prefix_req_indptr,
                    prefix_indptr, kv_indptr, scale, o, lse, workspace, stream):
     i32, dev = torch.int32, q.get_device()
-    with _on(q):
+    with _on(q, stream):
         o, lse, workspace, B, room = _shared_outputs(name, plan_, q, (k_prefix, v_prefix, k, v), o, lse, workspace)
         P = plan_.num_prefixes
         if prefix_req_indptr.numel() != P + 1 or prefix_indptr.numel() != P + 1 or \
@@ -894,7 +899,7 @@ def _decode_shared_paged(name, kv_dtypes, plan_, q, k_pages, v_pages, scales, pr
                          prefix_page_indptr, prefix_last_page_len, prefix_page_indices, kv_page_indptr,
                          kv_last_page_len, kv_page_indices, scale, o, lse, workspace, stream):
     i32, dev = torch.int32, q.get_device()
-    with _on(q):
+    with _on(q, stream):
         o, lse, workspace, B, room = _shared_outputs(name, plan_, q, (k_pages, v_pages), o, lse, workspace)
         P = plan_.num_prefixes
         if prefix_req_indptr.numel() != P + 1 or prefix_page_indptr.numel() != P + 1 or \

@@ -29,6 +29,13 @@ uint64_t turns_to_fixed(double turns)
     return ((uint64_t)hi << 32) + (uint64_t)lo;
 }
 
+// Whether two lists share memory.
+bool overlap(const int32_t *a, int64_t na, const int32_t *b, int64_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && x < y + nb * sizeof(int32_t) && y < x + na * sizeof(int32_t);
+}
+
 bool finite_positive(double x)
 {
     return x > 0 && x <= 1e300;
@@ -325,7 +332,9 @@ extern "C" int fd_fork_pages(int old_batch, int new_batch, int page_size, int nu
     if ((new_batch > 0 && (!parent_dev || !new_page_indptr_dev || !copy_src_dev || !copy_dst_dev)) ||
         (new_page_entries > 0 && !new_page_indices_dev))
         return FD_ERR_INVALID_ARG;
-    if (new_page_entries > 0 && new_page_indices_dev == kv_page_indices_dev)
+    if (new_page_refs_dev != page_refs_dev && overlap(new_page_refs_dev, num_pages, page_refs_dev, num_pages))
+        return FD_ERR_INVALID_ARG;
+    if (overlap(new_page_indices_dev, new_page_entries, kv_page_indices_dev, num_page_entries))
         return FD_ERR_INVALID_ARG;   // a child's table is read after another's is written
     const void *ptrs[] = {parent_dev, kv_page_indptr_dev, kv_last_page_len_dev, kv_page_indices_dev,
                           new_page_indptr_dev, page_refs_dev, new_page_indices_dev, new_page_refs_dev,
@@ -371,6 +380,11 @@ extern "C" int fd_compact_pages(int num_pages, const int32_t *page_refs_dev, con
         return FD_ERR_WORKSPACE;
     if (!page_refs_dev || !new_page_refs_dev || (num_page_entries > 0 && (!kv_page_indices_dev || !new_page_indices_dev)) ||
         (max_moves > 0 && (!copy_src_dev || !copy_dst_dev)))
+        return FD_ERR_INVALID_ARG;
+    // in place, entry by entry, or apart
+    if ((new_page_indices_dev != kv_page_indices_dev &&
+         overlap(new_page_indices_dev, num_page_entries, kv_page_indices_dev, num_page_entries)) ||
+        (new_page_refs_dev != page_refs_dev && overlap(new_page_refs_dev, num_pages, page_refs_dev, num_pages)))
         return FD_ERR_INVALID_ARG;
     const void *ptrs[] = {page_refs_dev, kv_page_indices_dev, new_page_indices_dev, new_page_refs_dev,
                           copy_src_dev, copy_dst_dev};

@@ -122,6 +122,7 @@ def _fork(**kw):
     (dict(ne=-1), -1), (dict(old=32769), -2), (dict(new=32769, wsb=1 << 30), -2), (dict(ws=None), -3),
     (dict(wsb=512), -3), (dict(refs=None), -1), (dict(nrefs=None), -1), (dict(parent=None), -1),
     (dict(ip=None), -1), (dict(src=None), -1), (dict(nids=P(512)), -1), (dict(last=P(257)), -1),
+    (dict(e=4, nids=P(524)), -1), (dict(ne=4, nids=P(500)), -1), (dict(nrefs=P(260)), -1),
 ], ids=str)
 def test_fork_refusals(kw, code):
     assert _fork(**kw) == code
@@ -137,7 +138,7 @@ def _compact(**kw):
 @pytest.mark.parametrize("kw,code", [
     (dict(pages=0), -1), (dict(e=-1), -1), (dict(limit=-1), -1), (dict(moves=-1), -1), (dict(ws=None), -3),
     (dict(wsb=1000), -3), (dict(refs=None), -1), (dict(ids=None), -1), (dict(src=None), -1),
-    (dict(dst=P(255)), -1),
+    (dict(dst=P(255)), -1), (dict(e=4, nids=P(264)), -1), (dict(nrefs=P(268)), -1),
 ], ids=str)
 def test_compact_refusals(kw, code):
     assert _compact(**kw) == code

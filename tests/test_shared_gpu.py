@@ -294,6 +294,34 @@ def test_repeats_are_identical_and_other_streams_work(cuda_device):
         assert torch.equal(first[0], other[0]) and torch.equal(first[1], other[1]), what
 
 
+def test_what_a_call_allocates_belongs_to_its_stream(cuda_device):
+    """No workspace or outputs given, and the current stream busy: nothing of
+    the call waits for it, and its memory is not handed on meanwhile."""
+    i = make(32, 8, [50], [3000], own_lengths(50, 40))
+    req, pi, oi = indptr(i["reqs"]), indptr(i["lens"]), indptr(i["own"])
+    p = fd.plan_shared(50, 32, 8, D, req, pi, i["room"])
+    d = {n: i[n].cuda() for n in ("q", "kp", "vp", "k", "v")}
+    args = (p, d["q"], d["kp"], d["vp"], d["k"], d["v"], i32(req), i32(pi), i32(oi), SCALE)
+    s, x = torch.cuda.Stream(), torch.ones(4096, 4096, device="cuda")
+    torch.full((p.workspace_bytes,), 255, dtype=torch.uint8, device="cuda")   # freed: what torch hands out next
+    torch.cuda.synchronize()
+    for _ in range(8):
+        x = x @ x * 1e-4
+    o, lse = fd.decode_shared(*args, stream=s)
+    torch.full((p.workspace_bytes,), 255, dtype=torch.uint8, device="cuda")
+    s.synchronize()
+    check(i, (o, lse, 0))
+
+
+def test_a_stream_of_another_device_is_refused(cuda_device):
+    refs = torch.zeros(4, dtype=torch.int32, device="cuda")
+
+    class Other:
+        device, cuda_stream = torch.device("cuda", 1), 0
+    with pytest.raises(fd.FdError):
+        fd.compact_pages(refs, refs, 0, stream=Other())
+
+
 def test_workspace_serves_call_after_call(cuda_device):
     """Calls queued on one workspace without waiting, of two inputs in turn."""
     a, b = (make(32, 8, [20, 9], [1000, 333], own_lengths(29, 60, s), seed=s, room=2000) for s in (1, 2))
