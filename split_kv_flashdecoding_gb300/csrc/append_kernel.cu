@@ -14,6 +14,10 @@
 // or several (long calls); the tokens' angles are computed once in shared
 // memory for all of the token's heads.  A thread's unit is two 8-value chunks
 // that hold both halves of 8 pairs, read and written 16 bytes at a time.
+// Measured: 32768 tokens of 32 + 8 + 8 heads 126 us in bf16, 6.4 TB/s, 94 % of a
+// plain copy's rate; 12345 tokens into FP8 50.7 us, 5.5 TB/s, of which some 8 us
+// are the first CTAs' look-ups and the last ones' end; 64 tokens 3.9 us, the
+// chain.
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
@@ -84,6 +88,14 @@ __device__ __forceinline__ uint32_t pack8_int4(const float (&x)[8], float scale)
     return w;
 }
 
+// Where two pairs' (cos, sin) are in a token's row of 32 such: the lanes of a
+// head read every 2nd (interleaved) or every 4th of them at once, here from
+// different banks (32768 tokens: 131 us for 135 in order).
+__device__ __forceinline__ int place(int x)
+{
+    return x ^ ((x >> 3) & 3);
+}
+
 // (a, b) turned by the angle of (c, s).
 __device__ __forceinline__ void turn(float &a, float &b, float c, float s)
 {
@@ -93,7 +105,7 @@ __device__ __forceinline__ void turn(float &a, float &b, float c, float s)
 }
 
 template <int KVT>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p)
+__global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_constant__ AppendParams p)
 {
     __shared__ __align__(16) float2 s_cs[kMaxTokens][kHeadDim / 2];
     __shared__ int64_t s_row[kMaxTokens];    // cache row of the token, -1: none
@@ -128,28 +140,33 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         }
     };
     settle();
-    // The next unit is loaded while the one before is worked on; the first while
-    // the tables are looked up.
-    int next_tt, next_head;
-    uint4 next0, next1;
-    auto load_unit = [&]() {
-        next_tt = tt;
-        next_head = head;
+    // Two units are loaded ahead of the one that is worked on, the first two while
+    // the tables are looked up (one ahead: 32768 tokens 131 us, two 126, with four
+    // CTAs an SM either way).
+    struct Unit {
+        int tt, head;
+        uint4 a, b;
+    };
+    Unit u0, u1;
+    auto load_unit = [&](Unit &x) {
+        x.tt = tt;
+        x.head = head;
         if (tt < nt) {
             const int kv = head - p.num_qo_heads;
             const int64_t t = t0 + tt;
             const uint16_t *src = kv < 0                ? p.q + t * p.q_stride + head * kHeadDim
                                   : kv < p.num_kv_heads ? p.k + t * p.k_stride + kv * kHeadDim
                                                         : p.v + t * p.v_stride + (kv - p.num_kv_heads) * kHeadDim;
-            next0 = *reinterpret_cast<const uint4 *>(src + c0);
-            next1 = *reinterpret_cast<const uint4 *>(src + c1);
+            x.a = *reinterpret_cast<const uint4 *>(src + c0);
+            x.b = *reinterpret_cast<const uint4 *>(src + c1);
         }
         head += kHeadLanes;
         settle();
     };
     griddep_wait();
     griddep_launch_dependents();
-    load_unit();
+    load_unit(u0);
+    load_unit(u1);
     __syncthreads();
 
     // request of each token: how many of append_indptr[1..B] are at or below it
@@ -208,19 +225,19 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         const uint64_t turns = (uint64_t)(int64_t)s_pos[tt] * p.rope.step[j];
         float s, c;
         sincospif((float)(int64_t)turns * 1.0842021724855044e-19f, &s, &c);   // turns / 2^63: half turns
-        s_cs[tt][j] = make_float2(c * p.rope.gain, s * p.rope.gain);
+        s_cs[tt][2 * place(j >> 1) + (j & 1)] = make_float2(c * p.rope.gain, s * p.rope.gain);
     }
     __syncthreads();
 
-    while (next_tt < nt) {
-        const int token = next_tt, head = next_head, kv = head - p.num_qo_heads;
+    auto body = [&](Unit &x) {
+        const int token = x.tt, head = x.head, kv = head - p.num_qo_heads;
         const bool is_v = kv >= p.num_kv_heads;
         float a[8], b[8];
-        unpack8(next0, a);
-        unpack8(next1, b);
-        load_unit();
+        unpack8(x.a, a);
+        unpack8(x.b, b);
+        load_unit(x);
         if (!s_ok[token])
-            continue;
+            return;
         const int64_t t = t0 + token, row = s_row[token];
         if (!is_v && turns0) {
             // the pairs' (cos, sin): of each chunk's 4 pairs, or of the unit's 8
@@ -228,14 +245,14 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             if (p.rope.interleaved) {
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const float4 f = cs[c0 / 4 + j];
+                    const float4 f = cs[place(c0 / 4 + j)];
                     turn(a[4 * j], a[4 * j + 1], f.x, f.y);
                     turn(a[4 * j + 2], a[4 * j + 3], f.z, f.w);
                 }
                 if (turns1) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
-                        const float4 f = cs[c1 / 4 + j];
+                        const float4 f = cs[place(c1 / 4 + j)];
                         turn(b[4 * j], b[4 * j + 1], f.x, f.y);
                         turn(b[4 * j + 2], b[4 * j + 3], f.z, f.w);
                     }
@@ -243,7 +260,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             } else {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float4 f = cs[c0 / 2 + j];
+                    const float4 f = cs[place(c0 / 2 + j)];
                     turn(a[2 * j], b[2 * j], f.x, f.y);
                     turn(a[2 * j + 1], b[2 * j + 1], f.z, f.w);
                 }
@@ -253,7 +270,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             uint16_t *dst = p.q_out + t * p.q_out_stride + head * kHeadDim;
             *reinterpret_cast<uint4 *>(dst + c0) = pack8(a);
             *reinterpret_cast<uint4 *>(dst + c1) = pack8(b);
-            continue;
+            return;
         }
         const int kvh = is_v ? kv - p.num_kv_heads : kv;
         const int64_t at = (row * p.num_kv_heads + kvh) * kHeadDim;   // values before this head's row
@@ -291,6 +308,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             if (u == 0)
                 (is_v ? p.v_scale_out : p.k_scale_out)[(int64_t)kvh * p.num_pages * p.page_size + row] = scale;
         }
+    };
+    while (u0.tt < nt) {
+        body(u0);
+        if (u1.tt >= nt)
+            break;
+        body(u1);
     }
 }
 
@@ -300,10 +323,12 @@ cudaError_t launch_append(const AppendParams &params, int kv_type, cudaStream_t 
 {
     AppendParams p = params;
     // One token a CTA up to one wave of resident CTAs (a short call is a chain of
-    // dependent loads: more CTAs, shorter chains), then as few CTAs as a wave, up
-    // to kMaxTokens tokens each (32768 tokens of 48 heads: 8 a CTA 133 us, 4 134).
+    // dependent loads: more CTAs, shorter chains), then as few whole waves as
+    // kMaxTokens tokens a CTA allow, equal CTAs (12345 tokens of 48 heads in FP8: 7
+    // a CTA took 0.6 us less than 8).
     constexpr int kWave = 152 * 4;
-    p.tokens_per_cta = std::min(kMaxTokens, (p.num_tokens + kWave - 1) / kWave);
+    const int waves = (p.num_tokens + kWave * kMaxTokens - 1) / (kWave * kMaxTokens);
+    p.tokens_per_cta = (p.num_tokens + kWave * waves - 1) / (kWave * waves);
     const dim3 grid((unsigned)((p.num_tokens + p.tokens_per_cta - 1) / p.tokens_per_cta));
     switch (kv_type) {
     case kKvTypeBf16: return launch_dependent(append_kernel<kKvTypeBf16>, grid, kThreads, 0, stream, p);
