@@ -44,7 +44,7 @@ cudaError_t launch_copy_pages(const CopyPagesParams &p, int num_pools, cudaStrea
 struct PagesScratch {
     int *info;           // [16] counts of the call, see pages_kernel.cu
     int *block_count;    // [blocks]
-    int *list;           // [num_pages] fresh pages in order (fork), ranks of the moving pages (compact)
+    int *list;           // [num_pages] ranks of the moving pages (compact); free pages, a bit each (fork)
     int *child_rank;     // [max_batch] fresh pages before each child's (fork)
     int *child_copy;     // [max_batch] 1: its last page is a copy of its parent's
 };

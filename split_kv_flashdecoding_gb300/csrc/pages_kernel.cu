@@ -8,9 +8,11 @@
 //
 // Bound: the copies move each page once in and once out (HBM); the table
 // kernels read and write a few words per page and table entry, so their time
-// is that of three short dependent launches, 7.2-8 us a call up to 65536 pages
-// and 51200 entries (one launch of an 8-CTA cluster with its barrier between the
-// steps took 7.5-10 us at 1000-4096 pages, 22-28 us at 65536).
+// is that of two (fork) or three (compaction) short dependent launches: 6.7-7.9
+// and 6.9-7.5 us a call up to 65536 pages and 51200 entries.  A fork in three
+// launches, with the fresh pages listed by one of its own, took 7.4-7.9 us and
+// 1.9 us more of the host; one launch of an 8-CTA cluster with its barrier
+// between the steps 7.5-10 us at 1000-4096 pages, 22-28 us at 65536.
 #include <cuda_runtime.h>
 
 #include "api_util.h"
@@ -24,6 +26,8 @@ namespace {
 enum Info { kFail, kNeeded, kInfoWords };
 
 constexpr int kScanThreads = kPagesPerBlock / 4;
+constexpr int kBlockWords = kPagesPerBlock / 32;
+static_assert(kBlockWords == 32, "a block's bits are a word of each lane");
 static_assert(kScanThreads % 32 == 0, "whole warps");
 
 constexpr int kChildThreads = 1024;
@@ -175,6 +179,15 @@ __global__ void __launch_bounds__(kChildThreads) fork_count_kernel(const __grid_
             if (i + 1 < p.num_pages) p.refs_out[i + 1] = r.y;
             if (i + 2 < p.num_pages) p.refs_out[i + 2] = r.z;
             if (i + 3 < p.num_pages) p.refs_out[i + 3] = r.w;
+            // which of the block's pages are free, a bit each: the next launch
+            // looks for them while it changes the counts
+            unsigned bits = (unsigned)((r.x == 0) | (r.y == 0) << 1 | (r.z == 0) << 2 | (r.w == 0) << 3)
+                            << (4 * (tid & 7));
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1)
+                bits |= __shfl_xor_sync(0xffffffffu, bits, o);
+            if ((tid & 7) == 0)
+                p.s.list[blk * kBlockWords + tid / 8] = (int)bits;
         }
         n = cta_sum(n, s_scan);
         if (tid == 0)
@@ -223,46 +236,24 @@ __global__ void __launch_bounds__(kChildThreads) fork_count_kernel(const __grid_
     }
 }
 
-// Launch 2.  The free pages of rank below the number needed, in order.
-__global__ void __launch_bounds__(kScanThreads) fork_free_kernel(const __grid_constant__ ForkParams p)
-{
-    __shared__ int s_scan[33];
-    const int tid = threadIdx.x, blk = blockIdx.x;
-    griddep_wait();
-    griddep_launch_dependents();
-    const int needed = p.s.info[kNeeded];
-    int before = 0;
-    for (int i = tid; i < blk; i += kScanThreads)
-        before += p.s.block_count[i];
-    before = cta_sum(before, s_scan);
-    if (before >= needed)
-        return;
-    const int4 r = load_refs(p.refs_in, p.num_pages, blk);
-    const int f[4] = {r.x == 0, r.y == 0, r.z == 0, r.w == 0};
-    int total;
-    int rank = before + cta_exclusive_scan(f[0] + f[1] + f[2] + f[3], s_scan, total);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if (f[j]) {
-            if (rank < needed)
-                p.s.list[rank] = blk * kPagesPerBlock + 4 * tid + j;
-            ++rank;
-        }
-    }
-}
-
-// Launch 3.  CTAs 0..new_batch-1 write a child's table, its copy and its
-// references; the others take an old request's references away.
+// Launch 2.  CTAs 0..new_batch-1 write a child's table, its copy and its
+// references; the others take an old request's references away.  The fresh
+// page of rank r is the r-th free one: a block's share from the blocks' counts,
+// its place there from the bits, a word a lane.
 __global__ void __launch_bounds__(kTableThreads) fork_table_kernel(const __grid_constant__ ForkParams p)
 {
     __shared__ int s_scan[33];
+    __shared__ int s_before[kTableThreads];   // free pages before each of 256 blocks
     const int tid = threadIdx.x;
     griddep_wait();
     griddep_launch_dependents();
-    int free_pages = 0;
-    for (int i = tid; i < p.blocks; i += kTableThreads)
-        free_pages += p.s.block_count[i];
-    free_pages = cta_sum(free_pages, s_scan);
+    int free_pages = 0, count = 0;
+    for (int b0 = 0; b0 < p.blocks; b0 += kTableThreads) {
+        int total;
+        count = b0 + tid < p.blocks ? p.s.block_count[b0 + tid] : 0;
+        s_before[tid] = free_pages + cta_exclusive_scan(count, s_scan, total);
+        free_pages += total;
+    }
     const bool outside = p.s.info[kFail] != 0;
     const bool fail = outside || p.s.info[kNeeded] > free_pages;   // nothing changes then
     if (fail) {
@@ -297,9 +288,8 @@ __global__ void __launch_bounds__(kTableThreads) fork_table_kernel(const __grid_
     const Child c = read_child(p, i);
     const int copy = p.s.child_copy[i], rank = p.s.child_rank[i], a = p.new_indptr[i];
     const int *old = c.have > 0 ? p.indices + p.page_indptr[p.parent[i]] : nullptr;
-    const int kept = c.have - copy;   // entries that are the parent's own
-    for (int j = tid; j < c.next; j += kTableThreads) {
-        int page = j < kept ? old[j] : p.s.list[rank + j - kept];
+    const int kept = c.have - copy, fresh = c.next - kept;   // entries that are the parent's own, and not
+    auto enter = [&](int j, int page) {
         if (page >= 0 && page < p.num_pages) {
             atomicAdd(p.refs_out + page, 1);
         } else {
@@ -307,10 +297,53 @@ __global__ void __launch_bounds__(kTableThreads) fork_table_kernel(const __grid_
             report(p.status, FD_ERR_DEVICE_BOUNDS);
         }
         p.new_indices[a + j] = page;
-    }
+    };
+    for (int j = tid; j < kept; j += kTableThreads)
+        enter(j, old[j]);
     if (tid == 0) {
         p.copy_src[i] = copy ? c.tail : -1;
-        p.copy_dst[i] = copy ? p.s.list[rank] : -1;
+        if (!copy)
+            p.copy_dst[i] = -1;
+    }
+    if (fresh == 0)
+        return;
+    const int warp = tid >> 5, lane = tid & 31;
+    int before = 0;
+    for (int b0 = 0; b0 < p.blocks; b0 += kTableThreads) {
+        if (p.blocks > kTableThreads) {   // else they are there
+            int total;
+            count = b0 + tid < p.blocks ? p.s.block_count[b0 + tid] : 0;
+            __syncthreads();
+            s_before[tid] = before + cta_exclusive_scan(count, s_scan, total);
+            before += total;
+        }
+        __syncthreads();
+        const int n = min(p.blocks - b0, kTableThreads);
+        for (int b = warp; b < n; b += kTableThreads / 32) {
+            const int first = s_before[b];
+            if (first >= rank + fresh || first + kPagesPerBlock <= rank)
+                continue;
+            unsigned bits = (unsigned)p.s.list[(b0 + b) * kBlockWords + lane];
+            int r = __popc(bits);
+            const int mine = r;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int t = __shfl_up_sync(0xffffffffu, r, o);
+                if (lane >= o)
+                    r += t;
+            }
+            r += first - mine;   // rank of the lane's first free page
+            if (r + mine <= rank || r >= rank + fresh)
+                bits = 0;
+            for (; bits; bits &= bits - 1, ++r) {
+                if (r < rank || r >= rank + fresh)
+                    continue;
+                const int page = (b0 + b) * kPagesPerBlock + 32 * lane + __ffs(bits) - 1;
+                enter(kept + r - rank, page);
+                if (copy && r == rank)
+                    p.copy_dst[i] = page;
+            }
+        }
     }
 }
 
@@ -444,8 +477,6 @@ cudaError_t launch_fork(const ForkParams &p, cudaStream_t stream)
         e = cudaFuncSetAttribute(fork_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e == cudaSuccess)
         e = launch_dependent(fork_count_kernel, dim3((unsigned)(1 + p.blocks)), kChildThreads, smem, stream, p);
-    if (e == cudaSuccess)
-        e = launch_dependent(fork_free_kernel, dim3((unsigned)p.blocks), kScanThreads, 0, stream, p);
     if (e == cudaSuccess && p.new_batch + p.old_batch > 0)
         e = launch_dependent(fork_table_kernel, dim3((unsigned)(p.new_batch + p.old_batch)), kTableThreads, 0,
                              stream, p);
