@@ -1068,20 +1068,39 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
 }
 
 // Stage 2: for each (request, query head) the merge of its prefix's partials
-// and, where there is one, the state of its own keys (in o, lse).  One warp per
-// row, lane = 4 output columns, kBatch rows of loads in flight.
+// and, where there is one, the state of its own keys (in o, lse).  A row is
+// WARPS warps', lane = 4 output columns, kMergeBatch partials of loads in flight
+// a warp; with several warps each takes every WARPS-th batch and the first one
+// adds their states up.
 constexpr int kMergeWarps = 4;
 constexpr int kMergeBatch = 8;
 
+struct MergeState {
+    float m, den;   // maximum of the LSEs, sum of the weights that refer to it
+    float4 acc;
+};
+
+template <int WARPS>
 __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __grid_constant__ SharedParams p)
 {
-    const int lane = threadIdx.x & 31;
-    const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    __shared__ MergeState s_state[kMergeWarps][32];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WARPS;
+    const int row = blockIdx.x * (kMergeWarps / WARPS) + warp / WARPS;
+    const bool has_row = row < p.batch * p.num_qo_heads;
+    // The tables were there before the prefixes' grid, which this one's start
+    // follows: they are read before the wait for its partials.
+    const int b = row / p.num_qo_heads;
+    PrefixCoord c;
+    int n = 0;
+    int64_t first = 0;
+    const bool found = has_row && locate_prefix(p, b, true, c);
+    if (found) {
+        n = c.splits;
+        first = c.row0 + (int64_t)(row - c.req0 * p.num_qo_heads) * n;
+    }
     griddep_wait();
     griddep_launch_dependents();
-    if (row >= p.batch * p.num_qo_heads)
-        return;
-    if (row == 0 && p.has_suffix) {   // more own keys than the plan has room for: some were not attended
+    if (row == 0 && part == 0 && p.has_suffix) {   // more own keys than the plan has room for: some were not attended
         int64_t keys = 0;
         for (int i = lane; i < p.batch; i += 32) {
             const int32_t d = __ldg(p.suffix_indptr + i + 1) - __ldg(p.suffix_indptr + i);
@@ -1093,29 +1112,22 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
         if (lane == 0 && keys > p.max_suffix_tokens)
             report(p.status, FD_ERR_DEVICE_BOUNDS);
     }
-    const int b = row / p.num_qo_heads;
-    PrefixCoord c;
-    int n = 0;
-    int64_t first = 0;
-    if (locate_prefix(p, b, true, c)) {
-        n = c.splits;
-        first = c.row0 + (int64_t)(row - c.req0 * p.num_qo_heads) * n;
-    } else if (lane == 0) {
+    if (has_row && !found && lane == 0)
         report(p.status, FD_ERR_DEVICE_BOUNDS);
-    }
     float4 *o_row = reinterpret_cast<float4 *>(p.o + (int64_t)row * kHeadDim) + lane;
     float m = -INFINITY, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (p.has_suffix) {
+    if (p.has_suffix && has_row && part == 0) {
         m = p.lse[row];
-        if (m != -INFINITY) {
+        acc = *o_row;
+        if (m != -INFINITY)
             den = 1.f;
-            acc = *o_row;
-        }
+        else
+            acc = make_float4(0.f, 0.f, 0.f, 0.f);
     }
     const float *lse_in = p.partial_lse + first;
     const float4 *o_in = reinterpret_cast<const float4 *>(p.partial_o + first * kHeadDim) + lane;
-    for (int i0 = 0; i0 < n; i0 += kMergeBatch) {
+    for (int i0 = part * kMergeBatch; i0 < n; i0 += WARPS * kMergeBatch) {
         float l[kMergeBatch];
         float4 v[kMergeBatch];
 #pragma unroll
@@ -1155,6 +1167,34 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
         }
         m = m_new;
     }
+    if constexpr (WARPS > 1) {
+        s_state[warp][lane] = MergeState{m, den, acc};
+        __syncthreads();
+        if (part > 0)
+            return;
+        float m_all = m;
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w)
+            m_all = fmaxf(m_all, s_state[warp + w][lane].m);
+        const float f = den == 0.f ? 0.f : expf(m - m_all);
+        den *= f;
+        acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w) {
+            const MergeState x = s_state[warp + w][lane];
+            if (x.den == 0.f)   // no partials, or no keys
+                continue;
+            const float g = expf(x.m - m_all);
+            den = fmaf(g, x.den, den);
+            acc.x = fmaf(g, x.acc.x, acc.x);
+            acc.y = fmaf(g, x.acc.y, acc.y);
+            acc.z = fmaf(g, x.acc.z, acc.z);
+            acc.w = fmaf(g, x.acc.w, acc.w);
+        }
+        m = m_all;
+    }
+    if (!has_row)
+        return;
     const float inv = den == 0.f ? 0.f : 1.f / den;   // no keys at all: O = 0, LSE = -inf
     *o_row = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
     __syncwarp();

@@ -149,6 +149,21 @@ def test_long_prefixes(cuda_device, Hq, Hkv, B, L):
     check(i, paged(i, 16), ref, f"{B} x {L} paged")
 
 
+@pytest.mark.parametrize("Hq,Hkv,B,L", [(1, 1, 1, 9000), (8, 8, 3, 1100), (32, 8, 8, 4100), (64, 8, 5, 3000)])
+def test_few_rows_of_many_splits(cuda_device, Hq, Hkv, B, L):
+    """More partials a row than a warp of the merge loads at once."""
+    i = make(Hq, Hkv, [B], [L], own_lengths(B, 40), seed=L)
+    check(i, ragged(i, 128), what="own keys")
+    j = make(Hq, Hkv, [B, 1], [L, 130], np.zeros(B + 1, int), seed=L, room=0)
+    check(j, ragged(j, 128), what="prefixes alone")
+    j["kp"][L // 2, 0, 3] = float("nan")
+    o, lse, status = ragged(j, 128)
+    bad = torch.isnan(o).any(-1).cpu()
+    want = torch.zeros(B + 1, Hq, dtype=torch.bool)
+    want[:B, : Hq // Hkv] = True
+    assert status == 0 and torch.equal(bad, want) and torch.equal(torch.isnan(lse).cpu(), want)
+
+
 @pytest.mark.parametrize("L", [1024, 1025, 2176, 2177, 4100, 20000])
 @pytest.mark.parametrize("B", [5, 33, 64])
 def test_long_splits(cuda_device, B, L):
