@@ -9,7 +9,10 @@
 // second kernel merges them with the state of the request's own keys by LSE.
 //
 // Bound: up to 128 rows a KV head the bytes of K and V (a 128-key tile of both
-// is 64 KB in bf16), above that the tensor cores.  The products run on tcgen05
+// is 64 KB in bf16; 32 requests of 32 heads behind 65536 keys 50-52 us, 5.3 TB/s),
+// above that the tensor cores (a tile of two row tiles 1.9-2.1 us, 1.9 PFLOP/s
+// with the products of both parts of P; 256 requests of 64 heads behind 32768
+// keys 285 us).  The products run on tcgen05
 // with their accumulators in tensor memory: S and O of one 128-row tile take
 // 256 columns, so a CTA holds two such streams.  With more than 128 rows the
 // streams are two row tiles that share each K and V tile; with fewer, both
@@ -23,13 +26,16 @@
 //
 // FP8 K and V: the products are in f16 (every E4M3 value is an f16 value); four
 // warps widen each raw tile into an operand tile in shared memory, and q
-// rows are scaled into f16 by a power of two.
+// rows are scaled into f16 by a power of two.  A tile of one row tile takes 1.47
+// us: neither HBM nor the tensor cores but the chain of its steps (1.17 without
+// the widening's work, 1.30 without the softmax's).
 //
 // Warps: 0-15 the softmax -- two warpgroups a stream, one a half of the tile's
 // keys; a thread owns a row and 64 of its scores (tcgen05.ld gives it the row's
 // columns).  16 the producer (TMA), 17 issues the products of both streams in
 // turn (a warp for each let the two streams' products run through one another:
-// both then ended late, 359 us for 296 us), 18-21 do the widening (FP8).
+// both then ended late, and the call took a fifth longer), 18-21 do the widening
+// (FP8).
 //
 // The reference m of a row's weights only has to keep them in their type's
 // range: the weights are floating-point numbers, their size costs no accuracy.
@@ -38,9 +44,9 @@
 // the warps of a row on the way.  A row whose later scores are out of that
 // range (its sum over 2^40 in bf16; a weight over f16's with FP8 K/V) is seen
 // at the end, and the CTA then does its item again with careful steps, which
-// raise m and rescale O.  Careful steps alone took 310 us where these take
-// 250 us (256 x 64 heads behind 32768 keys): the tensor cores waited for the
-// maximum, the vote of a row's two warps, and then for the weights.
+// raise m and rescale O.  Careful steps alone took a quarter longer (310 us for
+// 250 of the prefixes' grid, 256 x 64 heads behind 32768 keys): the tensor cores
+// waited for the maximum, the vote of a row's two warps, and then for the weights.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -1071,7 +1077,8 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
 // and, where there is one, the state of its own keys (in o, lse).  A row is
 // WARPS warps', lane = 4 output columns, kMergeBatch partials of loads in flight
 // a warp; with several warps each takes every WARPS-th batch and the first one
-// adds their states up.
+// adds their states up.  Bound: a chain of loads (tables, partials, a batch at a
+// time), 4-5 us behind the prefixes' grid.
 constexpr int kMergeWarps = 4;
 constexpr int kMergeBatch = 8;
 

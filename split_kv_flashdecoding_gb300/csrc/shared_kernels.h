@@ -20,9 +20,8 @@ constexpr int kSharedBlockRows = 256;  // query rows of one CTA: two such tiles
 // it), which with a tile's 16 products takes about 2.5e-7 of O: 37 tiles in a row
 // left it short by 1.1e-5, more than its fp32 type says.  So a stream with more
 // steps adds O up in global memory, where fp32 sums round, in runs of equal length
-// of up to kFlush steps, and starts anew.  A flush takes 2.2 us of a CTA's 70
-// (256 x 64 heads behind 32768 keys, 37 steps: none 276 us and 1.1e-5, one 283 and
-// 5.5e-6, four 303 and 3.3e-6).
+// of up to kFlush steps, and starts anew (256 x 64 heads behind 32768 keys, 37
+// steps: none 275 us and 1.1e-5, one flush 285 and 5.9e-6, three 299 and 3.3e-6).
 constexpr int kFlush = 20;
 
 FD_HD int32_t shared_run(int32_t steps)   // steps between flushes
