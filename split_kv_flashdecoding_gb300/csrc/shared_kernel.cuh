@@ -696,6 +696,12 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
                     if (u < kUnits)
                         x[j] = *reinterpret_cast<const uint4 *>(src + (u >> 1) * 1024 + (((u & 1) * 64) ^ lane_src));
                 }
+                if (first < kSharedTile) {   // the last tile; each tile's own selects made it 0.3 us longer
+#pragma unroll
+                    for (int j = 0; j < kMine; ++j)
+                        if (((me + j * kWidenWarps) >> 1) * 8 + r8 >= first)
+                            x[j] = make_uint4(0u, 0u, 0u, 0u);
+                }
 #pragma unroll
                 for (int j = 0; j < kMine; ++j) {
                     const int u = me + j * kWidenWarps;
@@ -708,11 +714,6 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
                                 "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
                                 : "=r"(f[2 * q]), "=r"(f[2 * q + 1])
                                 : "r"(w[q]));
-                        if ((u >> 1) * 8 + r8 >= first) {
-#pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                f[q] = 0u;
-                        }
                         uint8_t *d = dst + (u & 1) * kHalfBytes + (u >> 1) * 1024;
                         *reinterpret_cast<uint4 *>(d + lane_dst) = make_uint4(f[0], f[1], f[2], f[3]);
                         *reinterpret_cast<uint4 *>(d + (lane_dst ^ 16)) = make_uint4(f[4], f[5], f[6], f[7]);
