@@ -26,9 +26,10 @@
 //
 // FP8 K and V: the products are in f16 (every E4M3 value is an f16 value); four
 // warps widen each raw tile into an operand tile in shared memory, and q
-// rows are scaled into f16 by a power of two.  A tile of one row tile takes 1.47
-// us: neither HBM nor the tensor cores but the chain of its steps (1.17 without
-// the widening's work, 1.30 without the softmax's).
+// rows are scaled into f16 by a power of two.  A tile of one row tile takes 1.1 us
+// on contiguous keys (4.4 TB/s over the SMs) and 1.5 in 16-key pages (16 boxes a
+// tile): the chain of its steps, in which each instruction of the widening counts
+// (a select for each value past the last key made it 1.46).
 //
 // Warps: 0-15 the softmax -- two warpgroups a stream, one a half of the tile's
 // keys; a thread owns a row and 64 of its scores (tcgen05.ld gives it the row's
@@ -42,11 +43,11 @@
 // So m is the maximum of the row's first tile, and the steps behind it turn
 // scores into weights as they arrive, with no maximum and no exchange between
 // the warps of a row on the way.  A row whose later scores are out of that
-// range (its sum over 2^40 in bf16; a weight over f16's with FP8 K/V) is seen
-// at the end, and the CTA then does its item again with careful steps, which
-// raise m and rescale O.  Careful steps alone took a quarter longer (310 us for
-// 250 of the prefixes' grid, 256 x 64 heads behind 32768 keys): the tensor cores
-// waited for the maximum, the vote of a row's two warps, and then for the weights.
+// range (its sum over 2^40; a weight over f16's with FP8 K/V) is seen at the
+// end, and the CTA then does its item again with careful steps, which raise m
+// and rescale O.  Careful steps alone took a quarter longer (310 us for 250 of
+// the prefixes' grid, 256 x 64 heads behind 32768 keys): the tensor cores waited
+// for the maximum, the vote of a row's two warps, and then for the weights.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -77,10 +78,10 @@ constexpr int kTmemCols = 512;
 constexpr int kStreamCols = 256;                        // S (and P over it) 128, O 128
 // Careful steps: log2 of the growth of a row's maximum that raises m.
 constexpr float kRaise = 8.f;
-// The other steps: the most that a row's sum (bf16) or largest weight (FP8 K/V,
-// f16 weights, 2^7 times larger) may be; beyond it the item is done again.
-template <int DT>
-constexpr float kMostWeight = DT == kKvTypeFp8 ? 65000.f : 1099511627776.f;
+// The other steps: the most that a row's sum may be; beyond it the item is done
+// again.  (FP8 K/V has weights in f16: one past their range is inf, its lo part
+// -inf, and the row's O NaN, which tells without a look at each weight.)
+constexpr float kMostSum = 1099511627776.f;
 constexpr uint32_t kSleepNs = 100000;                    // a wait's sleep between looks at the timer
 constexpr int kOutStride = kHeadDim + 4;                // floats between rows of the epilogue's staging
 
@@ -670,12 +671,16 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
             // chunks of the operand's half c / 4.  The lanes of a quarter warp are two
             // rows r and r ^ 5 and four chunks, which meet no bank twice on either side.
             // All of a warp's units of a tile are loaded before the first is stored.
-            constexpr int kUnits = 2 * kSharedTile / 8, kMine = (kUnits + kWidenWarps - 1) / kWidenWarps;
+            constexpr int kMine = 2 * kSharedTile / 8 / kWidenWarps;
+            constexpr uint32_t kStep = kWidenWarps / 2 * 1024;   // bytes between a warp's units, raw and widened
+            static_assert(kWidenWarps % 2 == 0 && kMine * kWidenWarps * 4 == kSharedTile, "whole units a warp");
             const uint8_t *raw0 = ring_ptr + kWideBuffers * kBufBytes;
-            const int me = warp - kWidenWarp;
+            const int me = warp - kWidenWarp;   // first unit: rows 8 (me / 2) .., half me % 2
             const int r8 = (lane >> 3) ^ (((lane >> 2) & 1) * 5), cc = lane & 3;
-            // the lane's chunk within its 8-row group: raw, and the first of its two of the operand
-            const uint32_t lane_src = r8 * 128 + ((cc ^ r8) << 4), lane_dst = r8 * 128 + (((2 * cc) ^ r8) << 4);
+            const int row = (me >> 1) * 8 + r8;
+            // the lane's chunk of the first unit: raw, and the first of its two of the operand
+            const uint32_t lane_src = (me >> 1) * 1024 + r8 * 128 + ((((me & 1) * 4 + cc) ^ r8) << 4);
+            const uint32_t lane_dst = (me >> 1) * 1024 + (me & 1) * kHalfBytes + r8 * 128 + (((2 * cc) ^ r8) << 4);
             Place from(0, nb), to(0, kWideBuffers);
             for (int pos = 0; pos < 2 * n; ++pos, from.advance(1), to.advance(1)) {
                 bool is_k;
@@ -686,38 +691,31 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
                     go = wait_phase(&sm->empty[to.slot], to.phase ^ 1, p, sm);
                 if (!__all_sync(0xffffffffu, go))
                     break;
-                const uint8_t *src = raw0 + from.slot * kRawBytes;
+                const uint8_t *src = raw0 + from.slot * kRawBytes + lane_src;
                 uint8_t *dst = ring_ptr + to.slot * kBufBytes;
-                const int first = is_k ? kSharedTile : valid;   // V rows from here on are past the last key
+                uint8_t *dst0 = dst + lane_dst, *dst1 = dst + (lane_dst ^ 16);
                 uint4 x[kMine];
 #pragma unroll
-                for (int j = 0; j < kMine; ++j) {
-                    const int u = me + j * kWidenWarps;   // 8 rows u / 2, half u % 2
-                    if (u < kUnits)
-                        x[j] = *reinterpret_cast<const uint4 *>(src + (u >> 1) * 1024 + (((u & 1) * 64) ^ lane_src));
-                }
-                if (first < kSharedTile) {   // the last tile; each tile's own selects made it 0.3 us longer
+                for (int j = 0; j < kMine; ++j)
+                    x[j] = *reinterpret_cast<const uint4 *>(src + j * kStep);
+                if (!is_k && valid < kSharedTile) {   // V rows past the last key
 #pragma unroll
                     for (int j = 0; j < kMine; ++j)
-                        if (((me + j * kWidenWarps) >> 1) * 8 + r8 >= first)
+                        if (row + j * (kWidenWarps * 4) >= valid)
                             x[j] = make_uint4(0u, 0u, 0u, 0u);
                 }
 #pragma unroll
                 for (int j = 0; j < kMine; ++j) {
-                    const int u = me + j * kWidenWarps;
-                    if (u < kUnits) {
-                        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                        uint32_t f[8];
+                    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                    uint32_t f[8];
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
-                                "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-                                : "=r"(f[2 * q]), "=r"(f[2 * q + 1])
-                                : "r"(w[q]));
-                        uint8_t *d = dst + (u & 1) * kHalfBytes + (u >> 1) * 1024;
-                        *reinterpret_cast<uint4 *>(d + lane_dst) = make_uint4(f[0], f[1], f[2], f[3]);
-                        *reinterpret_cast<uint4 *>(d + (lane_dst ^ 16)) = make_uint4(f[4], f[5], f[6], f[7]);
-                    }
+                    for (int q = 0; q < 4; ++q)
+                        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+                            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+                            : "=r"(f[2 * q]), "=r"(f[2 * q + 1])
+                            : "r"(w[q]));
+                    *reinterpret_cast<uint4 *>(dst0 + j * kStep) = make_uint4(f[0], f[1], f[2], f[3]);
+                    *reinterpret_cast<uint4 *>(dst1 + j * kStep) = make_uint4(f[4], f[5], f[6], f[7]);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -826,7 +824,6 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
                 next_flush += run;
             };
             float m_ref = -INFINITY, l = 0.f;   // what the weights refer to (a raw score), their sum
-            float most = 0.f;                   // FP8: the largest weight
             bool go = ok;
             // 16 scores to weights, over their columns: hi in the first 8, lo in the others
             auto weights = [&](const uint32_t (&r)[16], int j16, float off, float2 &sum) {
@@ -838,8 +835,6 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
                     const float2 x = fma2(score, c22, off2);
                     const float2 w = make_float2(ex2(x.x), ex2(x.y));
                     sum = add2(sum, w);
-                    if constexpr (kFp8)
-                        most = fmaxf(most, fmaxf(w.x, w.y));
                     hi[j] = pack2<DT>(w);
                     const float2 h = unpack2<DT>(hi[j]);
                     lo[j] = pack2<DT>(fma2(h, make_float2(-1.f, -1.f), w));
@@ -951,15 +946,26 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
                 // a row whose scores are all -inf so far keeps weights of 0
                 step(r0, r1, valid, (m_ref == -INFINITY ? 0.f : -m_ref * c2) + kBias);
             }
-            // Out of range: a weight too large for its type, or no score to refer to
-            // in the first tile.
-            if (go && !careful && steps(s) > 0 && (m_ref == -INFINITY || (kFp8 ? most : l) > kMostWeight<DT>))
-                sm->redo = 1;
             // ----------------------------------------------------- the partial
             for (int x = 0; x < 2; ++x)   // both streams' products are done with the ring
                 if (go && steps(x) > 0)
                     go = __all_sync(0xffffffffu, wait_phase(&sm->o_done[x], 0, p, sm));
             tcgen05_fence_after();
+            // Out of range: a weight too large for its type, or no score to refer to
+            // in the first tile.
+            if (go && !careful && steps(s) > 0) {
+                bool again = m_ref == -INFINITY || l > kMostSum;
+                if constexpr (kFp8) {
+                    uint32_t o[16];
+                    tmem_ld16(o_col, o);
+                    tmem_wait_ld();
+                    settle(o);
+                    const float sum = __uint_as_float(o[0]) + (flushed ? __ldcg(my_flush) : 0.f);
+                    again |= sum != sum;
+                }
+                if (again)
+                    sm->redo = 1;
+            }
             barrier(1, kSoftmaxThreads);
             if (careful || !sm->redo) {
                 float *stage = reinterpret_cast<float *>(smem);   // [q_tiles * 128][kOutStride]
