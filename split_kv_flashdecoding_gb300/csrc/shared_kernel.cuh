@@ -451,8 +451,13 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
     const uint32_t tmem = sm->tmem;
     const bool ok = sm->ok;
     const int q_tiles = sm->q_tiles;
-    // the ring that TMA fills: operand tiles, or raw ones (FP8)
-    const int nb = kFp8 ? 2 * (kBuffers - q_tiles - kWideBuffers) : kBuffers - q_tiles;
+    // The ring that TMA fills: raw tiles (FP8), or operand tiles.  Two tiles of K and
+    // V on their way a CTA suffice on contiguous keys, and with more of them the
+    // 152 CTAs slow one another at the memory (32 requests behind 131072 keys: 4
+    // buffers 92.7 us, 6 98.9); pages, whose tiles are several boxes, take one more
+    // (pages of 128 keys: 4 93.0, 5 92.3, 6 94.8; of 16: 96.4, 94.9, 94.4).
+    const int nb = kFp8 ? 2 * (kBuffers - q_tiles - kWideBuffers) : PAGED ? 5 : 4;
+    static_assert(kBuffers >= 2 + 5, "two Q tiles and the ring");
     const int nw = kFp8 ? kWideBuffers : nb;   // operand tiles
     const int n = ok ? (sm->keys + kSharedTile - 1) / kSharedTile : 0;
     // local steps of stream s: every tile (two row tiles) or every other one
