@@ -8,8 +8,8 @@
 //
 // Bound: the copies move each page once in and once out (HBM); the table
 // kernels read and write a few words per page and table entry, so their time
-// is that of two (fork) or three (compaction) short dependent launches: 6.7-7.9
-// and 6.9-7.5 us a call up to 65536 pages and 51200 entries.  A fork in three
+// is that of short dependent launches, two for a fork and two or three for a
+// compaction: 6.6-7.9 and 5.6-7.5 us a call up to 65536 pages and 51200 entries.  A fork in three
 // launches, with the fresh pages listed by one of its own, took 7.4-7.9 us and
 // 1.9 us more of the host; one launch of an 8-CTA cluster with its barrier
 // between the steps 7.5-10 us at 1000-4096 pages, 22-28 us at 65536.
@@ -350,6 +350,10 @@ __global__ void __launch_bounds__(kTableThreads) fork_table_kernel(const __grid_
 
 // ------------------------------------------------------------------ compact
 
+// Up to so many blocks of pages every CTA of the next launch counts them all
+// itself: 1000 pages 5.6 us for 6.4, 4096 7.1 for 7.2, 8192 would be 8.6 for 7.3.
+constexpr int kFewBlocks = 4;
+
 // Launch 1.  Pages in use in each block.
 __global__ void __launch_bounds__(kScanThreads) compact_count_kernel(const __grid_constant__ CompactParams p)
 {
@@ -371,17 +375,27 @@ struct Division {
 // All threads of a CTA; `before` gets the pages in use before block blk.
 __device__ __forceinline__ Division divide_pages(const CompactParams &p, int blk, int *scratch, int &before)
 {
+    const bool few = p.blocks <= kFewBlocks;   // counted here, else by the launch before
     int all = 0, ahead = 0;
-    for (int i = threadIdx.x; i < p.blocks; i += blockDim.x) {
-        const int n = p.s.block_count[i];
-        all += n;
-        ahead += i < blk ? n : 0;
+    if (few) {
+        for (int i = 0; i < p.blocks; ++i) {
+            const int4 r = load_refs(p.refs_in, p.num_pages, i);
+            const int n = (r.x > 0) + (r.y > 0) + (r.z > 0) + (r.w > 0);
+            all += n;
+            ahead += i < blk ? n : 0;
+        }
+    } else {
+        for (int i = threadIdx.x; i < p.blocks; i += blockDim.x) {
+            const int n = p.s.block_count[i];
+            all += n;
+            ahead += i < blk ? n : 0;
+        }
     }
     before = cta_sum(ahead, scratch);
     const int live = cta_sum(all, scratch);
     Division d;
     d.limit = p.limit > 0 ? min(p.limit, p.num_pages) : live;
-    const int lb = d.limit / kPagesPerBlock;   // the limit's block
+    const int lb = few ? 0 : d.limit / kPagesPerBlock;   // the limit's block
     int n = 0;
     for (int i = threadIdx.x; i < min(lb, p.blocks); i += blockDim.x)
         n += p.s.block_count[i];
@@ -486,7 +500,9 @@ cudaError_t launch_fork(const ForkParams &p, cudaStream_t stream)
 
 cudaError_t launch_compact(const CompactParams &p, cudaStream_t stream)
 {
-    cudaError_t e = launch_dependent(compact_count_kernel, dim3((unsigned)p.blocks), kScanThreads, 0, stream, p);
+    cudaError_t e = cudaSuccess;
+    if (p.blocks > kFewBlocks)
+        e = launch_dependent(compact_count_kernel, dim3((unsigned)p.blocks), kScanThreads, 0, stream, p);
     if (e == cudaSuccess)
         e = launch_dependent(compact_rank_kernel, dim3((unsigned)p.blocks), kScanThreads, 0, stream, p);
     const int n = p.entries > p.max_moves ? p.entries : p.max_moves;
