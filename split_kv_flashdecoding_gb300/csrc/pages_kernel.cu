@@ -197,9 +197,20 @@ __global__ void __launch_bounds__(kChildThreads) fork_count_kernel(const __grid_
     }
     if (tid == 0)
         s_fail = 0;
+    // Every old table is within its array, the ended requests' too: the next
+    // launch, which takes their references away, starts only on tables that are.
+    // (The first of a thread's tables is on its way while the parents are read.)
+    const bool has_table = tid < p.old_batch;
+    const int first_a = has_table ? p.page_indptr[tid] : 0, first_e = has_table ? p.page_indptr[tid + 1] : 0;
+    auto inside = [&](int a, int e) { return a >= 0 && e >= a && e <= p.old_entries; };
     for (int i = tid; i < p.old_batch; i += kChildThreads)
         s_first[i] = p.new_batch;
     __syncthreads();
+    bool torn = has_table && !inside(first_a, first_e);
+    for (int i = tid + kChildThreads; i < p.old_batch; i += kChildThreads)
+        torn |= !inside(p.page_indptr[i], p.page_indptr[i + 1]);
+    if (torn)
+        s_fail = 1;
     for (int i = tid; i < p.new_batch; i += kChildThreads) {
         const int par = p.parent[i];
         if (par >= 0 && par < p.old_batch)
@@ -270,12 +281,7 @@ __global__ void __launch_bounds__(kTableThreads) fork_table_kernel(const __grid_
     }
     if ((int)blockIdx.x >= p.new_batch) {
         const int b = blockIdx.x - p.new_batch;
-        const int a = p.page_indptr[b], e = p.page_indptr[b + 1];
-        if (a < 0 || e > p.old_entries) {
-            if (tid == 0)
-                report(p.status, FD_ERR_DEVICE_BOUNDS);
-            return;
-        }
+        const int a = p.page_indptr[b], e = p.page_indptr[b + 1];   // within the array, or the call had failed
         for (int i = a + tid; i < e; i += kTableThreads) {
             const int page = p.indices[i];
             if (page >= 0 && page < p.num_pages)

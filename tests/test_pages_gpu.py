@@ -153,6 +153,24 @@ def test_torn_tables_change_nothing(cuda_device, ip, nip):
     assert np.all(got[0] == -1) and np.array_equal(got[1], refs) and np.all(got[2] == -1) and np.all(got[3] == -1)
 
 
+@pytest.mark.parametrize("batch", [3, 1500])
+@pytest.mark.parametrize("at,bad", [(1, LOWEST), (1, 3), (1, -1), (0, 2), (0, -2), (2, 0), (2, 4), (2, 2 ** 31 - 1)])
+def test_a_torn_table_of_a_request_that_ends_changes_nothing(cuda_device, batch, at, bad):
+    """Nobody's parent has the torn range: it lies outside the entries, or falls."""
+    n = batch - 3   # requests of no pages before the three that the ranges are of
+    ip, last = np.concatenate([np.zeros(n), [0, 1, 2, 3]]), np.concatenate([np.zeros(n), [3, 16, 7]])
+    ids, refs = np.array([4, 1, 2]), np.array([0, 1, 1, 0, 1, 0])
+    going_on = {0: 2, 1: 2, 2: 0}[at]   # its range does not touch the torn entry
+    parent, nip = np.array([n + going_on]), np.array([0, 1])
+    good, status = fork(parent, ip, last, ids, nip, refs, 16)
+    assert status == 0 and good[1].sum() == 1
+    ip = ip.copy()
+    ip[n + at] = bad
+    got, status = fork(parent, ip, last, ids, nip, refs, 16)
+    assert status == -6
+    assert np.all(got[0] == -1) and np.array_equal(got[1], refs) and np.all(got[2] == -1) and np.all(got[3] == -1)
+
+
 def compact_reference(refs, ids, limit):
     live = np.flatnonzero(refs > 0)
     limit = limit or len(live)
