@@ -652,6 +652,8 @@ int fd_pages_workspace_bytes(int num_pages, int new_batch, int64_t *bytes);
  * the copy it needs (-1, -1: none).  Fresh pages are the lowest free ones, in
  * the order of the new tables' entries; pages that this call sets free are not
  * among them.  new_page_refs = page_refs minus the old entries plus the new.
+ * Entries of new_page_indices that no table has (new_page_entries may be more
+ * than new_page_indptr[new_batch], as in a captured call) become -1.
  *
  * With too few free pages (FD_ERR_NO_PAGES), or a parent, table or tail page
  * outside the arguments' ranges (FD_ERR_DEVICE_BOUNDS), nothing changes:
@@ -676,9 +678,10 @@ int fd_fork_pages(int old_batch, int new_batch, int page_size, int num_pages,
  * copy_src[r] -> copy_dst[r] is the r-th move (-1, -1 past the last), of at most
  * max_moves; the number of pages in use and that of free ones both bound it.
  * new_page_indices is kv_page_indices (every table of the pool, concatenated)
- * with the moved pages renamed; it may be the same array (in part: refused).  With more moves than
- * free pages before the limit or than max_moves, nothing changes
- * (FD_ERR_NO_PAGES) and the copies are -1.
+ * with the moved pages renamed; it may be the same array (in part: refused).
+ * Entries of -1 (no page) stay; other ids outside the pool stay too and set
+ * FD_ERR_DEVICE_BOUNDS.  With more moves than free pages before the limit or
+ * than max_moves, nothing changes (FD_ERR_NO_PAGES) and the copies are -1.
  */
 int fd_compact_pages(int num_pages, const int32_t *page_refs_dev,
                      const int32_t *kv_page_indices_dev, int num_page_entries, int limit,

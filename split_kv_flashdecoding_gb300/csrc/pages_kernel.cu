@@ -159,8 +159,10 @@ __device__ __forceinline__ Child read_child(const ForkParams &p, int i)
 }
 
 // Launch 1.  CTA 0: every child's fresh pages and their first rank, whether
-// its last page is a copy.  CTAs 1..: free pages of each block, and
-// refs_out = refs_in.
+// its last page is a copy.  CTAs 1..: free pages of each block, refs_out =
+// refs_in, and -1 in the entries that are no child's (in front of the first table
+// and behind the last; here, as these CTAs end long before CTA 0: 0.3 us more of a
+// fork in the next launch).
 __global__ void __launch_bounds__(kChildThreads) fork_count_kernel(const __grid_constant__ ForkParams p)
 {
     extern __shared__ int s_first[];   // [old_batch] lowest child of each request (CTA 0)
@@ -171,6 +173,8 @@ __global__ void __launch_bounds__(kChildThreads) fork_count_kernel(const __grid_
     griddep_launch_dependents();
     if (blockIdx.x > 0) {
         const int blk = blockIdx.x - 1;
+        const int used0 = p.new_batch > 0 ? p.new_indptr[0] : 0;
+        const int used1 = p.new_batch > 0 ? max(p.new_indptr[p.new_batch], 0) : 0;   // in range if the call is
         int n = 0;
         if (tid < kScanThreads) {
             const int4 r = load_refs(p.refs_in, p.num_pages, blk);
@@ -193,6 +197,11 @@ __global__ void __launch_bounds__(kChildThreads) fork_count_kernel(const __grid_
         n = cta_sum(n, s_scan);
         if (tid == 0)
             p.s.block_count[blk] = n;
+        const int64_t at = (int64_t)blk * kChildThreads + tid, step = (int64_t)p.blocks * kChildThreads;
+        for (int64_t i = at; i < min(used0, p.new_entries); i += step)
+            p.new_indices[i] = -1;
+        for (int64_t i = used1 + at; i < p.new_entries; i += step)
+            p.new_indices[i] = -1;
         return;
     }
     if (tid == 0)
@@ -471,9 +480,9 @@ __global__ void __launch_bounds__(kTableThreads) compact_table_kernel(const __gr
     }
     if (i < p.entries) {
         int page = p.indices[i];
-        if (page < 0 || page >= p.num_pages) {
+        if (page < -1 || page >= p.num_pages) {   // -1: no page
             report(p.status, FD_ERR_DEVICE_BOUNDS);
-        } else {
+        } else if (page >= 0) {
             const int rank = p.s.list[page];
             if (rank >= 0)
                 page = p.copy_dst[rank];

@@ -276,3 +276,44 @@ def test_captured_fork_and_copy_follow_their_tables(cuda_device):
         ok = want[2] >= 0
         b[want[3][ok]] = b[want[2][ok]]
         assert torch.equal(pool, b)
+
+
+@pytest.mark.parametrize("batch,children", [(0, 0), (4, 0), (0, 3), (5, 12)])
+@pytest.mark.parametrize("head,tail", [(0, 1), (0, 700), (3, 2000), (300, 0)])
+def test_entries_that_no_table_has_become_none(cuda_device, batch, children, head, tail):
+    """A list with room in front of its tables and behind them; the compaction of
+    the whole list renames the tables' pages and reports nothing."""
+    rng, pages, page = np.random.RandomState(batch + tail), 400, 16
+    ip, last, ids, refs = random_tables(rng, batch, page, pages, 8)
+    parent = rng.randint(-1, batch, children) if batch else np.full(children, -1)
+    grow = np.where(parent < 0, 0, (ip[1:] - ip[:-1])[np.maximum(parent, 0)] if batch else 0) + 1
+    nip = indptr(grow)
+    want = fork_reference(parent, ip, last, ids, nip, refs, page)
+    t = dev(parent, ip, last, ids, nip + head, refs)
+    n = head + int(nip[-1]) + tail
+    out = dev(np.full(n, 12345))[0]
+    ws = torch.zeros(fd.pages_workspace_bytes(pages, children), dtype=torch.uint8, device="cuda")
+    got = fd.fork_pages(*t[:5], n, page, t[5], new_page_indices=out, workspace=ws)
+    assert fd.get_device_status(ws) == 0
+    whole = np.concatenate([np.full(head, -1), want[0], np.full(tail, -1)])
+    for g, w in zip(got, (whole, *want[1:])):
+        assert np.array_equal(g.cpu().numpy(), w)
+    live = np.flatnonzero(want[1] > 0)
+    to, refs2, move, slot = compact_reference(want[1], np.arange(pages), 0)
+    most = min(len(live), pages - len(live))
+    for inplace in (False, True):
+        kw = dict(new_page_indices=got[0].clone()) if not inplace else dict(new_page_indices=got[0])
+        moved = fd.compact_pages(got[1], got[0], most, workspace=ws, **kw)
+        assert fd.get_device_status(ws) == 0
+        assert np.array_equal(moved[0].cpu().numpy(), np.where(whole < 0, -1, to[whole]))
+        assert np.array_equal(moved[1].cpu().numpy(), refs2)
+
+
+def test_compaction_reports_other_ids_outside_the_pool(cuda_device):
+    refs = np.array([0, 1, 1])
+    for bad in (-2, 3, LOWEST):
+        r, i = dev(refs, [2, -1, bad, 1])
+        ws = torch.zeros(fd.pages_workspace_bytes(3), dtype=torch.uint8, device="cuda")
+        got = fd.compact_pages(r, i, 1, workspace=ws)
+        assert fd.get_device_status(ws) == -6
+        assert got[0].tolist() == [0, -1, bad, 1]
