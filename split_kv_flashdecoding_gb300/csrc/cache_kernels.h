@@ -49,6 +49,7 @@ struct PagesScratch {
     int *child_copy;     // [max_batch] 1: its last page is a copy of its parent's
 };
 constexpr int kPagesPerBlock = 1024;
+constexpr int kMaxTableBatch = 32768;   // requests of a fork's tables (their index in shared memory)
 
 struct ForkParams {
     const int32_t *parent, *page_indptr, *last_len, *indices, *new_indptr, *refs_in;

@@ -18,7 +18,6 @@ using fd::round_up;
 namespace {
 
 constexpr int kHeadDim = 128;
-constexpr int kMaxTableBatch = 32768;   // requests of a fork's tables (their shared-memory index)
 
 // The fraction of `turns` as a 64-bit fixed-point number.
 uint64_t turns_to_fixed(double turns)
@@ -318,7 +317,7 @@ extern "C" int fd_fork_pages(int old_batch, int new_batch, int page_size, int nu
     if (old_batch < 0 || new_batch < 0 || num_pages <= 0 || num_page_entries < 0 || new_page_entries < 0 ||
         page_size <= 0)
         return FD_ERR_INVALID_ARG;
-    if (old_batch > kMaxTableBatch || new_batch > kMaxTableBatch)
+    if (old_batch > fd::kMaxTableBatch || new_batch > fd::kMaxTableBatch)
         return FD_ERR_UNSUPPORTED;
     int64_t need;
     fd_pages_workspace_bytes(num_pages, new_batch, &need);

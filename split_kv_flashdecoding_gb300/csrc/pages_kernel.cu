@@ -503,8 +503,11 @@ cudaError_t launch_fork(const ForkParams &p, cudaStream_t stream)
 {
     const int smem = p.old_batch * (int)sizeof(int);
     cudaError_t e = cudaSuccess;
+    // The limit is the kernel's, not the call's: always the most that a fork may
+    // need, so that no call lowers it between another thread's setting and launch.
     if (smem > 40 * 1024)
-        e = cudaFuncSetAttribute(fork_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        e = cudaFuncSetAttribute(fork_count_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kMaxTableBatch * (int)sizeof(int));
     if (e == cudaSuccess)
         e = launch_dependent(fork_count_kernel, dim3((unsigned)(1 + p.blocks)), kChildThreads, smem, stream, p);
     if (e == cudaSuccess && p.new_batch + p.old_batch > 0)

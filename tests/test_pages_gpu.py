@@ -1,5 +1,7 @@
 """fd_fork_pages, fd_compact_pages and fd_copy_pages on the GPU against their
 definitions written out entry by entry.  Whole numbers: everything is equal."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -317,3 +319,33 @@ def test_compaction_reports_other_ids_outside_the_pool(cuda_device):
         got = fd.compact_pages(r, i, 1, workspace=ws)
         assert fd.get_device_status(ws) == -6
         assert got[0].tolist() == [0, -1, bad, 1]
+
+
+def test_forks_of_many_requests_from_several_threads(cuda_device):
+    """Tables too large for the shared memory that a launch has by default, of
+    different sizes at once: no call takes the room of another."""
+    rounds, errors = 5000, []
+    start = threading.Barrier(4)
+
+    def run(batch):
+        try:
+            s = torch.cuda.Stream()
+            with torch.cuda.stream(s):
+                t = dev([batch - 1], np.zeros(batch + 1), np.zeros(batch), np.zeros(1), [0, 1], np.zeros(64))
+                ws = torch.zeros(fd.pages_workspace_bytes(64, 1), dtype=torch.uint8, device="cuda")
+                out = fd.fork_pages(*t[:5], 1, 16, t[5], workspace=ws)
+                kw = dict(zip(("new_page_indices", "new_page_refs", "copy_src", "copy_dst"), out))
+                start.wait()
+                for _ in range(rounds):
+                    fd.fork_pages(*t[:5], 1, 16, t[5], workspace=ws, **kw)
+                assert fd.get_device_status(ws, s) == 0 and out[0].tolist() == [0]
+        except Exception as e:   # to the test's thread
+            errors.append((batch, e))
+            start.abort()
+
+    threads = [threading.Thread(target=run, args=(b,)) for b in (10300, 32768, 12000, 30000)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors, errors
