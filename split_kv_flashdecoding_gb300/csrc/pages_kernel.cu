@@ -101,7 +101,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const __grid_c
     griddep_wait();
     griddep_launch_dependents();
     const int c = blockIdx.x / p.segments, seg = blockIdx.x - c * p.segments;
-    const int src = __ldg(p.src + c), dst = __ldg(p.dst + c);
+    // plain loads: the grid before may have written these while this one already ran
+    const int src = p.src[c], dst = p.dst[c];
     if (src < 0)
         return;
     if (src >= p.num_pages || dst < 0 || dst >= p.num_pages) {

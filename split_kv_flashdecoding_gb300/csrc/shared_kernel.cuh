@@ -1122,8 +1122,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
     if (row == 0 && part == 0 && p.has_suffix) {   // more own keys than the plan has room for: some were not attended
         int64_t keys = 0;
         for (int i = lane; i < p.batch; i += 32) {
-            const int32_t d = __ldg(p.suffix_indptr + i + 1) - __ldg(p.suffix_indptr + i);
-            keys += !p.page_size ? d : d > 0 ? (int64_t)(d - 1) * p.page_size + __ldg(p.suffix_last_len + i) : 0;
+            const int32_t d = __ldcg(p.suffix_indptr + i + 1) - __ldcg(p.suffix_indptr + i);
+            keys += !p.page_size ? d : d > 0 ? (int64_t)(d - 1) * p.page_size + __ldcg(p.suffix_last_len + i) : 0;
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1)

@@ -3,6 +3,7 @@ fd_append_paged, fd_fork_pages, fd_compact_pages and fd_copy_pages, all before
 any CUDA call."""
 import ctypes
 import math
+import os
 
 import numpy as np
 import pytest
@@ -181,3 +182,13 @@ def test_bindings_refuse_cpu_tensors():
         fd.append_paged(x, x, x, pool, pool, z[:2], z[:2], z[:1], z[:1], workspace=z)
     with pytest.raises(fd.FdError):
         fd.copy_pages([pool], z[:1], z[:1])
+
+
+@pytest.mark.parametrize("name", ["append_kernel.cu", "pages_kernel.cu", "shared_kernel.cuh"])
+def test_no_load_past_the_coherent_path(name):
+    """Every kernel of these files starts while the grid before it may still write
+    its inputs, so none may read them by loads for constant memory."""
+    source = open(os.path.join(os.path.dirname(fd.__file__), "csrc", name)).read()
+    code = "\n".join(line.split("//")[0] for line in source.splitlines())
+    for word in ("__ldg", "ld.global.nc", "__restrict__"):
+        assert word not in code, word
