@@ -1106,8 +1106,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WARPS;
     const int row = blockIdx.x * (kMergeWarps / WARPS) + warp / WARPS;
     const bool has_row = row < p.batch * p.num_qo_heads;
-    // The tables were there before the prefixes' grid, which this one's start
-    // follows: they are read before the wait for its partials.
+    // The tables were there before the prefixes' grid (or the suffixes'), which this
+    // one's start follows: they are read before the wait for its partials.  With no
+    // keys at all this grid is the call's first, and what it follows may still be
+    // writing them.
+    if (p.num_items == 0 && !p.has_suffix)
+        griddep_wait();
     const int b = row / p.num_qo_heads;
     PrefixCoord c;
     int n = 0;

@@ -222,6 +222,25 @@ def test_no_suffix_and_no_keys(cuda_device, rows):
     assert status == 0 and torch.all(o == 0) and torch.all(lse == -float("inf"))
 
 
+def test_a_call_without_keys_waits_for_its_tables(cuda_device):
+    """The tables come from page copies, whose grid lets the next one start early;
+    the only grid of a call without any key reads them."""
+    B, pages = 6, 600
+    p = fd.plan_shared(B, 8, 8, D, [0, B], [0, 0], 0)
+    q = torch.zeros((B, 8, D), dtype=torch.bfloat16, device="cuda")
+    big = torch.zeros((pages, 65536), dtype=torch.uint8, device="cuda")
+    small = torch.zeros((pages, 4), dtype=torch.int32, device="cuda")   # page 0: [0, B, 0, 0], the last: torn
+    small[0, 1] = B
+    src, dst = i32(np.arange(pages // 2)), i32(np.arange(pages - 1, pages // 2 - 1, -1))
+    ws = torch.zeros(p.workspace_bytes, dtype=torch.uint8, device="cuda")
+    for _ in range(20):
+        small[-1] = -7
+        fd.copy_pages([big, small], src, dst)   # page 0 to the last
+        o, lse = fd.decode_shared(p, q, None, None, None, None, small[-1, :2], small[-1, 2:], None, SCALE, workspace=ws)
+        assert fd.get_device_status(ws) == 0
+        assert torch.all(o == 0) and torch.all(lse == -float("inf"))
+
+
 @pytest.mark.parametrize("scale", [-0.1, 0.0, 1.5])
 def test_scales(cuda_device, scale):
     i = make(32, 8, [5, 60], [513, 300], own_lengths(65, 40))
