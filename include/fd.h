@@ -467,8 +467,8 @@ int fd_plan_shared_paged(int batch, int num_qo_heads, int num_kv_heads, int head
 /*
  * fd_decode_shared, fd_decode_shared_paged -- one decode step.  Ragged: k and v
  * must hold max_suffix_tokens rows.  scale must be finite.  A request without any
- * key gets O = 0, LSE = -inf.  More suffix keys than the plan's room, prefix
- * tables beyond it, or a page outside [0, num_pages) set FD_ERR_DEVICE_BOUNDS
+ * key gets O = 0, LSE = -inf.  More suffix keys than the plan's room (any, in
+ * suffix tables that are given to a plan without room), prefix tables beyond it, or a page outside [0, num_pages) set FD_ERR_DEVICE_BOUNDS
  * (the outputs are then not valid).  num_page_entries: entries of
  * kv_page_indices.  O adds up in fp32 with weights of up to 2^40: V of up to 2^80
  * in magnitude.  Workspace as for fd_decode: zeroed once, calls that share it in

@@ -851,7 +851,7 @@ def _decode_shared(name, kv_dtypes, plan_, q, k_prefix, v_prefix, k, v, scales, 
         o, lse, workspace, B, room = _shared_outputs(name, plan_, q, (k_prefix, v_prefix, k, v), o, lse, workspace)
         P = plan_.num_prefixes
         if prefix_req_indptr.numel() != P + 1 or prefix_indptr.numel() != P + 1 or \
-                (room and (kv_indptr is None or kv_indptr.numel() != B + 1)):
+                (room and kv_indptr is None) or (kv_indptr is not None and kv_indptr.numel() != B + 1):
             raise FdError(-1, f"{name}: tables of another length than the plan's")
         if plan_.num_items and (k_prefix.shape[0] < plan_.prefix_rows or v_prefix.shape[0] < plan_.prefix_rows) or \
                 (room and (k is None or v is None or k.shape[0] < room or v.shape[0] < room)):
@@ -904,8 +904,9 @@ def _decode_shared_paged(name, kv_dtypes, plan_, q, k_pages, v_pages, scales, pr
         P = plan_.num_prefixes
         if prefix_req_indptr.numel() != P + 1 or prefix_page_indptr.numel() != P + 1 or \
                 prefix_last_page_len.numel() < P or prefix_page_indices.numel() < plan_.prefix_rows or \
-                (room and (kv_page_indptr is None or kv_page_indptr.numel() != B + 1 or
-                           kv_last_page_len.numel() < B)):
+                (room and (kv_page_indptr is None or kv_last_page_len is None)) or \
+                (kv_page_indptr is not None and kv_page_indptr.numel() != B + 1) or \
+                (kv_last_page_len is not None and kv_last_page_len.numel() < B):
             raise FdError(-1, f"{name}: tables of another length than the plan's")
         if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or k_pages.shape[1] != plan_.page_size or \
                 k_pages.dtype not in kv_dtypes or v_pages.dtype not in kv_dtypes:

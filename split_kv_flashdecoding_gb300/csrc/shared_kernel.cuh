@@ -1123,11 +1123,14 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const __
     }
     griddep_wait();
     griddep_launch_dependents();
-    if (row == 0 && part == 0 && p.has_suffix) {   // more own keys than the plan has room for: some were not attended
+    // More own keys than the plan has room for (or any, where it has none): some were
+    // not attended.
+    if (row == 0 && part == 0 && p.suffix_indptr) {
         int64_t keys = 0;
         for (int i = lane; i < p.batch; i += 32) {
-            const int32_t d = __ldcg(p.suffix_indptr + i + 1) - __ldcg(p.suffix_indptr + i);
-            keys += !p.page_size ? d : d > 0 ? (int64_t)(d - 1) * p.page_size + __ldcg(p.suffix_last_len + i) : 0;
+            const int64_t d = (int64_t)__ldcg(p.suffix_indptr + i + 1) - __ldcg(p.suffix_indptr + i);
+            if (d > 0)
+                keys += p.page_size && p.suffix_last_len ? (d - 1) * p.page_size + __ldcg(p.suffix_last_len + i) : d;
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1)

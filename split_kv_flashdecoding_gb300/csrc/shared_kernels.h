@@ -61,7 +61,7 @@ struct SharedParams {
     int32_t page_size, num_pages;    // page_size 0: ragged
     int32_t box_rows;                // paged: rows of a page box
     int32_t has_suffix;
-    // the requests' own keys, to check them against the plan's capacity
+    // the requests' own keys, to check them against the plan's capacity (null: none)
     const int32_t *suffix_indptr, *suffix_last_len;
     int32_t max_suffix_tokens;
     float scale;                     // softmax scale

@@ -435,6 +435,28 @@ def test_tables_beyond_the_plan_are_flagged(cuda_device):
         assert fd.get_device_status(ws) == code
 
 
+@pytest.mark.parametrize("own,code", [([0, 0, 0, 0], 0), ([0, 0, 1, 0], -6), ([5, 6, 7, 8], -6)])
+def test_own_keys_without_room_are_flagged(cuda_device, own, code):
+    """A plan without room for own keys, called with their tables all the same."""
+    i = make(8, 8, [4], [300], own)
+    req, pg = indptr(i["reqs"]), to_pages(i, 16)
+    p = fd.plan_shared(4, 8, 8, D, req, indptr(i["lens"]), 0)
+    ws = torch.zeros(p.workspace_bytes, dtype=torch.uint8, device="cuda")
+    d = {n: i[n].cuda() for n in ("q", "kp", "vp", "k", "v")}
+    for k, v in ((d["k"], d["v"]), (None, None)):
+        fd.decode_shared(p, d["q"], d["kp"], d["vp"], k, v, i32(req), i32(indptr(i["lens"])), i32(indptr(own)), SCALE,
+                         workspace=ws)
+        assert fd.get_device_status(ws) == code
+    p = fd.plan_shared_paged(4, 8, 8, D, 16, req, indptr(pg["pc"]), pg["pl"], 0)
+    tables = i32(req), i32(indptr(pg["pc"])), i32(pg["pl"]), i32(pg["pids"])
+    for last, ids in ((i32(pg["ol"]), i32(np.append(pg["oids"], 0))), (None, None)):
+        fd.decode_shared_paged(p, d["q"], pg["pools"]["k"].cuda(), pg["pools"]["v"].cuda(), *tables, i32(indptr(pg["oc"])),
+                               last, ids, SCALE, workspace=ws)
+        assert fd.get_device_status(ws) == code
+    with pytest.raises(fd.FdError):   # a table of another length than the batch's
+        fd.decode_shared(p, d["q"], d["kp"], d["vp"], None, None, i32(req), i32(indptr(i["lens"])), i32([0, 0]), SCALE)
+
+
 BIG = 2 ** 31 - 1
 
 
