@@ -55,6 +55,12 @@
  * at the end of every successful call; after a call that reported an error
  * status, zero the workspace again before reusing it.  Calls that share one
  * workspace must be ordered on one stream.
+ *   Which calls may share one: fd_decode and its forms (paged, FP8, INT4, graph)
+ * lay their tickets and partials out by batch and KV heads, so a workspace of theirs
+ * serves calls of one batch and head count (with fd_append_paged* and
+ * fd_copy_pages, which use the header alone); zero it again before another use.
+ * fd_decode_shared* of any plans, fd_fork_pages, fd_compact_pages, fd_append_paged*
+ * and fd_copy_pages may all share one that is large enough for each.
  *
  * Launches: the kernels are launched with programmatic stream serialisation:
  * each may begin launching while the previous grid in the stream finishes,
@@ -471,8 +477,8 @@ int fd_plan_shared_paged(int batch, int num_qo_heads, int num_kv_heads, int head
  * suffix tables that are given to a plan without room), prefix tables beyond it, or a page outside [0, num_pages) set FD_ERR_DEVICE_BOUNDS
  * (the outputs are then not valid).  num_page_entries: entries of
  * kv_page_indices.  O adds up in fp32 with weights of up to 2^40: V of up to 2^80
- * in magnitude.  Workspace as for fd_decode: zeroed once, calls that share it in
- * the order of one stream.
+ * in magnitude.  Workspace: zeroed once, calls that share it in the order of one
+ * stream; calls of other plans and the page operators below may be among them.
  */
 int fd_decode_shared(const fd_shared_plan *plan, const int32_t *prefix_req_indptr_dev,
                      const int32_t *prefix_indptr_dev, const int32_t *kv_indptr_dev, const void *q,
@@ -633,8 +639,9 @@ int fd_append_paged_int4(int batch, int num_tokens, int num_qo_heads, int num_kv
  * memory.
  *
  * fd_pages_workspace_bytes -- the workspace of a fork or compaction (host
- * only).  new_batch: the fork's, 0 for a compaction.  The workspace need not be
- * zeroed beyond its header.
+ * only).  new_batch: the fork's, 0 for a compaction.  For these calls alone the
+ * workspace need not be zeroed beyond its header; one that is shared with
+ * fd_decode_shared* is zeroed whole, once.
  */
 int fd_pages_workspace_bytes(int num_pages, int new_batch, int64_t *bytes);
 

@@ -6,6 +6,12 @@
 
 namespace fd {
 
+// The first bytes behind a workspace's header, which the calls over prefixes, forks
+// and compactions keep for merge tickets: zero between calls, wherever the rest
+// of a plan's or a page operation's scratch begins, so that one workspace serves
+// calls of different plans and operators.  Room for 16384 (request, KV head) groups.
+constexpr int64_t kTicketBytes = 64 * 1024;
+
 inline bool aligned(const void *p, uintptr_t a)
 {
     return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0;

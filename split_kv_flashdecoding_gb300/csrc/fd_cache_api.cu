@@ -282,10 +282,11 @@ int page_blocks(int num_pages)
     return (num_pages + fd::kPagesPerBlock - 1) / fd::kPagesPerBlock;
 }
 
-// header | info (256 bytes) | block counts | list [num_pages] | child arrays [max_batch] x 2
+// header | the tickets of other calls, left as they are | info (256 bytes) | block counts |
+// list [num_pages] | child arrays [max_batch] x 2
 fd::PagesScratch pages_scratch(void *workspace, int num_pages, int max_batch)
 {
-    uint8_t *w = static_cast<uint8_t *>(workspace) + FD_WORKSPACE_HEADER_BYTES;
+    uint8_t *w = static_cast<uint8_t *>(workspace) + FD_WORKSPACE_HEADER_BYTES + fd::kTicketBytes;
     fd::PagesScratch s;
     s.info = reinterpret_cast<int *>(w);
     s.block_count = reinterpret_cast<int *>(w += 256);
@@ -301,7 +302,7 @@ extern "C" int fd_pages_workspace_bytes(int num_pages, int new_batch, int64_t *b
 {
     if (!bytes || num_pages < 0 || new_batch < 0)
         return FD_ERR_INVALID_ARG;
-    *bytes = FD_WORKSPACE_HEADER_BYTES + 256 + round_up((int64_t)page_blocks(num_pages) * 4, 256) +
+    *bytes = FD_WORKSPACE_HEADER_BYTES + fd::kTicketBytes + 256 + round_up((int64_t)page_blocks(num_pages) * 4, 256) +
              round_up((int64_t)num_pages * 4, 256) + 2 * round_up((int64_t)new_batch * 4, 256);
     return FD_OK;
 }

@@ -152,6 +152,13 @@ int suffix_chunk(int batch, int num_kv_heads, int64_t tokens, int num_sms)
     return c <= kMostSuffixChunk ? (int)c : 0;
 }
 
+// Workspace of a plan: header | tickets | the suffix plan's scratch, laid out as in a
+// workspace of its own (from kTicketBytes on) | partial LSE | partial O | sums of O.
+int64_t suffix_bytes(const fd_plan_info &suffix)
+{
+    return fd::kTicketBytes + round_up(suffix.workspace_bytes, 256);
+}
+
 // Where the items' streams add up their O, when one has over kFlush steps (a
 // step is a tile; with one row tile the streams take every other one).
 int64_t flush_bytes(int64_t items, int32_t chunk)
@@ -206,8 +213,8 @@ int make_plan(int batch, int num_qo_heads, int num_kv_heads, int head_dim, const
     plan->num_partial_rows = (int32_t)z.rows;
     plan->page_size = x.page_size;
     plan->prefix_rows = x.indptr[x.count];
-    plan->workspace_bytes = round_up(suffix.workspace_bytes, 256) + round_up(z.rows * 4, 256) +
-                            z.rows * kHeadDim * 4 + flush_bytes(z.items, chunk);
+    plan->workspace_bytes = suffix_bytes(suffix) + round_up(z.rows * 4, 256) + z.rows * kHeadDim * 4 +
+                            flush_bytes(z.items, chunk);
     plan->timeout_ns = FD_DEFAULT_TIMEOUT_NS;
     return FD_OK;
 }
@@ -330,16 +337,28 @@ int decode_shared(const fd_shared_plan *plan, const SharedTables &t, const void 
     // The requests' own keys: the split kernel, planned on the device, its
     // merged states into o and lse.
     if (has_suffix) {
-        const fd::WorkspaceLayout wl = fd::workspace_layout(workspace, s.batch, s.num_kv_heads, s.num_partial_rows);
+        const fd::WorkspaceLayout wl = fd::workspace_layout(static_cast<uint8_t *>(workspace) + fd::kTicketBytes, s.batch,
+                                                            s.num_kv_heads, s.num_partial_rows);
+        // The split kernel counts a request's splits up from zero and leaves zero.
+        // More groups than the tickets' own place holds: other calls' scratch may have
+        // been where they are, so the call clears them (2 us of a call of at least
+        // 16385 groups).
+        const int64_t ticket_bytes = (int64_t)s.batch * s.num_kv_heads * 4;
+        int *tickets = reinterpret_cast<int *>(static_cast<uint8_t *>(workspace) + FD_WORKSPACE_HEADER_BYTES);
+        if (ticket_bytes > fd::kTicketBytes) {
+            tickets = wl.counters;
+            if (cudaMemsetAsync(tickets, 0, (size_t)ticket_bytes, cs) != cudaSuccess)
+                return FD_ERR_CUDA;
+        }
         fd_plan_info info = s;
         info.timeout_ns = plan->timeout_ns;
         const fd::PagedKV pk{plan->page_size, t.num_pages, t.kv_last_len, nullptr, t.kv_indices, t.num_page_entries};
         rc = fd::launch_stage1(&info, q, k, v, t.kv_indptr, scale, wl.partial_o, wl.partial_lse, workspace, o, lse,
-                               wl.counters, nullptr, cs, paged ? &pk : nullptr, quant, true, nullptr, has_prefix);
+                               tickets, nullptr, cs, paged ? &pk : nullptr, quant, true, nullptr, has_prefix);
         if (rc != FD_OK)
             return rc;
     }
-    uint8_t *part = static_cast<uint8_t *>(workspace) + round_up(s.workspace_bytes, 256);
+    uint8_t *part = static_cast<uint8_t *>(workspace) + suffix_bytes(s);
     fd::SharedParams p;
     memset(&p, 0, sizeof p);
     p.q = static_cast<const uint16_t *>(q);

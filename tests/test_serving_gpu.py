@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 import torch
 
+import oracle
 import split_kv_flashdecoding_gb300 as fd
 from tests.parity_util import assert_within, errors
 
@@ -128,3 +129,52 @@ def test_prompt_fork_steps_and_compaction(cuda_device, fp8):
             whole = indptr([len(t) for t in tables])
             o2, lse2 = fd.decode_paged(q, *c.pools, whole, last.astype(np.int32), i32(whole), i32(last), torch.cat(tables), SCALE)
             assert (o - o2).abs().max() < 2e-5 and (lse - lse2).abs().max() < 2e-5
+
+
+@pytest.mark.parametrize("big", [(64, 32, 8), (4200, 4, 4)], ids=str)
+def test_one_workspace_for_plans_and_page_operators(cuda_device, big):
+    """Zeroed once: a small plan, a fork and a compaction leave their partials and
+    lists where they may; a larger plan's requests of several splits, before and
+    behind them, are merged all the same."""
+    def inputs(B, Hq, Hkv, own, seed):
+        g = torch.Generator().manual_seed(seed)
+        rand = lambda n, h: torch.randn((n, h, D), generator=g).to(torch.bfloat16)  # noqa: E731
+        return dict(B=B, Hq=Hq, Hkv=Hkv, own=own, q=rand(B, Hq), kp=rand(130, Hkv), vp=rand(130, Hkv),
+                    k=rand(int(own.sum()), Hkv), v=rand(int(own.sum()), Hkv))
+
+    own = np.random.RandomState(1).randint(0, 4, big[0])
+    own[::50] = 700
+    own[big[0] // 2] = 3000
+    cases = [inputs(2, 8, 8, np.array([300, 900]), 1), inputs(*big, own, 2)]
+    pages = 5000
+    plans = [fd.plan_shared(c["B"], c["Hq"], c["Hkv"], D, [0, c["B"]], [0, 130], int(c["own"].sum())) for c in cases]
+    assert all((c["own"] > p.suffix.chunk).any() for c, p in zip(cases, plans))
+    ws = torch.zeros(max(fd.pages_workspace_bytes(pages, 40), *(p.workspace_bytes for p in plans)), dtype=torch.uint8,
+                     device="cuda")
+    dev = [{n: c[n].cuda() for n in ("q", "kp", "vp", "k", "v")} for c in cases]
+
+    def decode(j):
+        d = dev[j]
+        return fd.decode_shared(plans[j], d["q"], d["kp"], d["vp"], d["k"], d["v"], i32([0, cases[j]["B"]]),
+                                i32([0, 130]), i32(indptr(cases[j]["own"])), SCALE, workspace=ws)
+
+    refs = torch.ones(pages, dtype=torch.int32, device="cuda")
+    refs[::3] = 0
+    outs = []
+    for j in (0, 1, 0, "fork", 1, "compact", 0, 1, 1):
+        if j == "fork":
+            fd.fork_pages(i32(np.full(40, -1)), i32([0]), i32([]), i32([]), i32(np.arange(41)), 40, P, refs, workspace=ws)
+        elif j == "compact":
+            fd.compact_pages(refs, i32(np.flatnonzero(refs.cpu().numpy())), pages, workspace=ws)
+        else:
+            outs.append((j, decode(j)))
+    assert fd.get_device_status(ws) == 0
+    for j, c in enumerate(cases):
+        K, V, at = [], [], indptr(c["own"])
+        for b in range(c["B"]):
+            K += [c["kp"], c["k"][at[b]: at[b + 1]]]
+            V += [c["vp"], c["v"][at[b]: at[b + 1]]]
+        o_ref, lse_ref = oracle.decode(c["q"], torch.cat(K), torch.cat(V), indptr(130 + c["own"]), SCALE)
+        for _, (o, lse) in (x for x in outs if x[0] == j):
+            assert_within(errors(o.cpu().numpy(), lse.cpu().numpy(), o_ref.reshape(o.shape), lse_ref.reshape(lse.shape)),
+                          **TIGHT, what=f"case {j}")
