@@ -227,6 +227,26 @@ def test_quantised_rows_of_zeros_infinities_and_nan(cuda_device):
     assert torch.all(p4[1].view(-1, D // 2)[i["rows"][0]] == 0)
 
 
+@pytest.mark.parametrize("scales", [(0.03, 0.3, 0.02, 1 / 3, 0.7, 7.0, 0.0123, 3 / 448),
+                                    (1e-39, 1e-40, 2e-38, 1.0, 3e38, 2.0 ** -126, -0.03, 448.0)], ids=["usual", "far"])
+def test_fp8_codes_of_every_value_are_the_rounded_quotients(cuda_device, scales):
+    """Every finite bf16 value over each scale: E4M3 of the quotient, ties to even.
+    Both roundings are IEEE's, so the codes are equal."""
+    x = torch.arange(-2 ** 15, 2 ** 15, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = x[torch.isfinite(x)].view(-1, 1, D).expand(-1, 8, D).contiguous()
+    n, page = len(x), 16
+    scale = torch.tensor(scales)
+    pages = -(-n // page)
+    pools = [torch.zeros((pages, page, 8, D), dtype=torch.uint8, device=cuda_device) for _ in "kv"]
+    i32 = lambda v: torch.tensor(v, dtype=torch.int32, device=cuda_device)  # noqa: E731
+    v = x.to(cuda_device)
+    fd.append_paged_fp8(None, v, v, *pools, scale.to(cuda_device), scale.to(cuda_device), i32([0, n]), i32([0, pages]),
+                        i32([n - (pages - 1) * page]), torch.arange(pages, dtype=torch.int32, device=cuda_device))
+    want = (x.float() / scale[:, None]).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    for pool in pools:   # K without a rotation is stored as V is
+        assert torch.equal(pool.view(-1, 8, D)[:n].cpu(), want)
+
+
 def test_captured_append_follows_its_tables(cuda_device):
     """One captured step, replayed with new positions, tables and inputs."""
     i, j = make([5, 40], [1, 1], 4, 2, 16, seed=1), make([21, 2], [1, 1], 4, 2, 16, seed=2)
