@@ -636,7 +636,7 @@ int fd_append_paged_int4(int batch, int num_tokens, int num_qo_heads, int num_kv
  * fd_compact_pages make the next tables and counts and list the page copies
  * they need; fd_copy_pages makes those copies in every pool (K and V of every
  * layer) at once.  new_page_refs may be page_refs itself; otherwise they share no
- * memory.
+ * memory.  num_pages is at most (2^31 - 1) / 16.
  *
  * fd_pages_workspace_bytes -- the workspace of a fork or compaction (host
  * only).  new_batch: the fork's, 0 for a compaction.  For these calls alone the

@@ -277,6 +277,9 @@ extern "C" int fd_copy_pages(int num_pools, void *const *pools, const int64_t *p
 
 namespace {
 
+// The most pages that a cache can have (16 keys each, key rows are 32-bit numbers).
+constexpr int kMaxPages = INT32_MAX / 16;
+
 int page_blocks(int num_pages)
 {
     return (num_pages + fd::kPagesPerBlock - 1) / fd::kPagesPerBlock;
@@ -300,7 +303,7 @@ fd::PagesScratch pages_scratch(void *workspace, int num_pages, int max_batch)
 
 extern "C" int fd_pages_workspace_bytes(int num_pages, int new_batch, int64_t *bytes)
 {
-    if (!bytes || num_pages < 0 || new_batch < 0)
+    if (!bytes || num_pages < 0 || num_pages > kMaxPages || new_batch < 0)
         return FD_ERR_INVALID_ARG;
     *bytes = FD_WORKSPACE_HEADER_BYTES + fd::kTicketBytes + 256 + round_up((int64_t)page_blocks(num_pages) * 4, 256) +
              round_up((int64_t)num_pages * 4, 256) + 2 * round_up((int64_t)new_batch * 4, 256);
@@ -315,7 +318,7 @@ extern "C" int fd_fork_pages(int old_batch, int new_batch, int page_size, int nu
                              int32_t *copy_src_dev, int32_t *copy_dst_dev, void *workspace,
                              int64_t workspace_bytes, void *stream)
 {
-    if (old_batch < 0 || new_batch < 0 || num_pages <= 0 || num_page_entries < 0 || new_page_entries < 0 ||
+    if (old_batch < 0 || new_batch < 0 || num_pages <= 0 || num_pages > kMaxPages || num_page_entries < 0 || new_page_entries < 0 ||
         page_size <= 0)
         return FD_ERR_INVALID_ARG;
     if (old_batch > fd::kMaxTableBatch || new_batch > fd::kMaxTableBatch)
@@ -372,7 +375,7 @@ extern "C" int fd_compact_pages(int num_pages, const int32_t *page_refs_dev, con
                                 int32_t *new_page_refs_dev, int32_t *copy_src_dev, int32_t *copy_dst_dev,
                                 void *workspace, int64_t workspace_bytes, void *stream)
 {
-    if (num_pages <= 0 || num_page_entries < 0 || limit < 0 || max_moves < 0)
+    if (num_pages <= 0 || num_pages > kMaxPages || num_page_entries < 0 || limit < 0 || max_moves < 0)
         return FD_ERR_INVALID_ARG;
     int64_t need;
     fd_pages_workspace_bytes(num_pages, 0, &need);

@@ -169,6 +169,16 @@ def test_pages_workspace_grows_with_pages_and_children():
         fd.pages_workspace_bytes(-1)
 
 
+@pytest.mark.parametrize("pages", [2 ** 27, 2 ** 31 - 1024, 2 ** 31 - 1])
+def test_more_pages_than_a_cache_has_are_refused(pages):
+    with pytest.raises(fd.FdError) as e:
+        fd.pages_workspace_bytes(pages)
+    assert e.value.code == -1
+    assert _fork(pages=pages, wsb=1 << 40) == -1
+    assert _compact(pages=pages, wsb=1 << 40) == -1
+    assert fd.pages_workspace_bytes(2 ** 27 - 1) > 4 * (2 ** 27 - 1)
+
+
 def test_new_status_has_a_name():
     assert fd.status_string(-7) == "FD_ERR_NO_PAGES" == fd.STATUS_NAMES[-7]
 
