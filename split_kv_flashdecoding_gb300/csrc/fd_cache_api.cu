@@ -243,8 +243,10 @@ extern "C" int fd_copy_pages(int num_pools, void *const *pools, const int64_t *p
         return FD_ERR_WORKSPACE;
     if (!aligned(workspace, 16))
         return FD_ERR_INVALID_ARG;
-    for (int i = 0; i < num_pools; ++i) {
-        if (!pools[i] || !aligned(pools[i], 16) || page_bytes[i] <= 0 || page_bytes[i] % 16 != 0)
+    auto segments = [](int64_t bytes) { return (bytes - 1) / fd::kCopySegment + 1; };
+    for (int i = 0; i < num_pools; ++i) {   // all of them, before the first is copied
+        if (!pools[i] || !aligned(pools[i], 16) || page_bytes[i] <= 0 || page_bytes[i] % 16 != 0 ||
+            (num_copies > 0 && segments(page_bytes[i]) > INT32_MAX / num_copies))
             return FD_ERR_INVALID_ARG;
     }
     if (num_pools == 0 || num_copies == 0 || num_pages == 0)
@@ -265,10 +267,7 @@ extern "C" int fd_copy_pages(int num_pools, void *const *pools, const int64_t *p
             p.page_bytes[i] = page_bytes[i0 + i];
             most = page_bytes[i0 + i] > most ? page_bytes[i0 + i] : most;
         }
-        const int64_t segments = (most + fd::kCopySegment - 1) / fd::kCopySegment;
-        if (segments * num_copies > INT32_MAX)
-            return FD_ERR_INVALID_ARG;
-        p.segments = (int32_t)segments;
+        p.segments = (int32_t)segments(most);
         if (fd::launch_copy_pages(p, n, as_stream(stream)) != cudaSuccess)
             return FD_ERR_CUDA;
     }

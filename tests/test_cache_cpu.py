@@ -162,6 +162,16 @@ def test_copy_refusals(kw, code):
     assert _copy(**kw) == code
 
 
+@pytest.mark.parametrize("size,copies", [(1 << 40, 64), ((1 << 63) - 16, 1), (1 << 62, 1 << 20)])
+@pytest.mark.parametrize("at", [0, 127, 128, 299])
+def test_copies_too_many_for_a_launch_are_refused_before_the_first(size, copies, at):
+    """More segments than a grid has, in any of the pools: no pool is copied (which
+    would fail here, without a GPU, in another way)."""
+    sizes = [64] * 300
+    sizes[at] = size
+    assert _copy(n=300, pools=(P * 300)(*[256] * 300), size=(ctypes.c_int64 * 300)(*sizes), copies=copies) == -1
+
+
 def test_pages_workspace_grows_with_pages_and_children():
     a, b, c = fd.pages_workspace_bytes(1000), fd.pages_workspace_bytes(100000), fd.pages_workspace_bytes(1000, 500)
     assert 256 + 4000 < a < c < b
