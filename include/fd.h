@@ -576,7 +576,8 @@ int fd_plan_rope(int head_dim, int rotary_dim, const fd_rope_config *config, fd_
  *     q, k, v        bf16 [num_tokens, heads, D], heads contiguous, any token
  *                    stride (elements, a multiple of 8, at least heads * D), so
  *                    they may be parts of one fused projection
- *     q_out          bf16, the rotated queries; q itself is allowed
+ *     q_out          bf16, the rotated queries; q itself is allowed (with its
+ *                    stride), other rows that share memory with q, k or v are not
  *     append_indptr  int32 [B+1]  request b's new tokens are rows
  *                    append_indptr[b] .. append_indptr[b+1]-1
  *     kv_page_indptr, kv_last_page_len, kv_page_indices   the page tables with

@@ -178,6 +178,30 @@ def test_in_place_queries_no_queries_and_strides(cuda_device):
     assert torch.equal(t["q"], want)
 
 
+@pytest.mark.parametrize("at", [0, 1, 2])
+def test_queries_between_the_rows_of_the_inputs(cuda_device, at):
+    """q_out as further heads of the fused buffer that q, k and v lie in: in front
+    of them, behind them, and over the queries of one token."""
+    i = make([0, 9], [20, 3], 4, 2, 16)
+    t, tables = to_dev(i, cuda_device)
+    info = fd.plan_rope(D, 128)
+    pools = [torch.zeros((i["num_pages"], 16, 2, D), dtype=torch.bfloat16, device=cuda_device) for _ in "kv"]
+    want = fd.append_paged(t["q"], t["k"], t["v"], *pools, *tables, rope=info)
+    if at < 2:
+        buf = torch.zeros((i["n"], 12, D), dtype=torch.bfloat16, device=cuda_device)
+        x = buf[:, 4:] if at == 0 else buf[:, :8]
+        x[:, :4], x[:, 4:6], x[:, 6:] = t["q"], t["k"], t["v"]
+        q_out = buf[:, :4] if at == 0 else buf[:, 8:]
+        got = fd.append_paged(x[:, :4], x[:, 4:6], x[:, 6:], *pools, *tables, rope=info, q_out=q_out)
+    else:
+        tables[0] = torch.tensor([0, 0, 1], dtype=torch.int32, device=cuda_device)   # the last key of request 1
+        q, k, v = (t[n][-1:].contiguous() for n in "qkv")
+        got = fd.append_paged(q, k, v, *pools, *tables, rope=info, q_out=q)
+        want = want[-1:]
+    torch.cuda.synchronize()
+    assert torch.equal(got, want)
+
+
 def test_tokens_outside_the_tables_are_skipped_and_flagged(cuda_device):
     i = make([0, 5], [4, 4], 2, 2, 16)
     t, tables = to_dev(i, cuda_device)

@@ -98,6 +98,18 @@ def test_append_refusals(name, kw, code):
     assert _append(name, **kw) == code
 
 
+@pytest.mark.parametrize("name", ["fd_append_paged", "fd_append_paged_fp8", "fd_append_paged_int4"])
+@pytest.mark.parametrize("n,at,stride", [
+    # q, k, v of 8, 4 and 4 heads at values 0, 1024 and 1536 of rows of 2176
+    (5, 0, 1024), (5, 8, 2176), (5, 512, 2176), (5, 1024, 2176), (5, 1600, 2176), (5, 2040, 2176), (5, 2176, 2176),
+    (5, 4 * 2176 + 2040, 2176), (1, -1016, 2176), (5, -1024, 1024),
+], ids=str)
+def test_append_refuses_queries_written_over_inputs(name, n, at, stride):
+    base, pool = 1 << 20, P(1 << 30)
+    inputs = dict(n=n, hq=8, hkv=4, q=P(base), qs=2176, k=P(base + 2 * 1024), ks=2176, v=P(base + 2 * 1536), vs=2176)
+    assert _append(name, **inputs, qo=P(base + 2 * at), qos=stride, kp=pool, vp=pool) == -1
+
+
 def test_append_refuses_missing_scales():
     for name in ("fd_append_paged_fp8", "fd_append_paged_int4"):
         assert _append(name, sk=None) == -1
