@@ -853,7 +853,8 @@ def _decode_shared(name, kv_dtypes, plan_, q, k_prefix, v_prefix, k, v, scales, 
         if prefix_req_indptr.numel() != P + 1 or prefix_indptr.numel() != P + 1 or \
                 (room and kv_indptr is None) or (kv_indptr is not None and kv_indptr.numel() != B + 1):
             raise FdError(-1, f"{name}: tables of another length than the plan's")
-        if plan_.num_items and (k_prefix.shape[0] < plan_.prefix_rows or v_prefix.shape[0] < plan_.prefix_rows) or \
+        if plan_.num_items and (k_prefix is None or v_prefix is None or k_prefix.shape[0] < plan_.prefix_rows or
+                                v_prefix.shape[0] < plan_.prefix_rows) or \
                 (room and (k is None or v is None or k.shape[0] < room or v.shape[0] < room)):
             raise FdError(-1, f"{name}: K/V hold fewer rows than the plan's")
         for x in (k_prefix, v_prefix, k, v):

@@ -508,6 +508,26 @@ def test_binding_refusals(cuda_device):
             fd.decode_shared(*bad)
 
 
+def test_missing_tensors_are_refused(cuda_device):
+    i = make(8, 8, [4], [300], [5, 6, 7, 8])
+    pg = to_pages(i, 16)
+    d = {n: i[n].cuda() for n in ("q", "kp", "vp", "k", "v")}
+    p = fd.plan_shared(4, 8, 8, D, indptr(i["reqs"]), indptr(i["lens"]), 26)
+    good = [p, d["q"], d["kp"], d["vp"], d["k"], d["v"], i32(indptr(i["reqs"])), i32(indptr(i["lens"])),
+            i32(indptr(i["own"])), SCALE]
+    pp = fd.plan_shared_paged(4, 8, 8, D, 16, indptr(i["reqs"]), indptr(pg["pc"]), pg["pl"], 26)
+    paged_good = [pp, d["q"], pg["pools"]["k"].cuda(), pg["pools"]["v"].cuda(), i32(indptr(i["reqs"])),
+                  i32(indptr(pg["pc"])), i32(pg["pl"]), i32(pg["pids"]), i32(indptr(pg["oc"])), i32(pg["ol"]),
+                  i32(pg["oids"]), SCALE]
+    for call, args, missing in ((fd.decode_shared, good, (2, 3, 4, 5, 8)), (fd.decode_shared_paged, paged_good, (8, 9))):
+        call(*args)
+        for at in missing:
+            bad = list(args)
+            bad[at] = None
+            with pytest.raises(fd.FdError):
+                call(*bad)
+
+
 # ------------------------------------------------------------------------ FP8
 
 def to_fp8(i, seed=0):
