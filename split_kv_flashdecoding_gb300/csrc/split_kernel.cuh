@@ -771,7 +771,7 @@ struct TileSource {
 
     __device__ __forceinline__ int32_t fetch_ids(int32_t first) const
     {
-        return first + lane < req_pages ? __ldg(p.page_indices + req_base + first + lane) : 0;
+        return first + lane < req_pages ? p.page_indices[req_base + first + lane] : 0;
     }
 
     // Physical page of the request's page `pg`; a page outside the pool is
@@ -930,7 +930,9 @@ __device__ __forceinline__ KeyIndex key_index(const SplitParams &p, bool paged)
 
 // Q fragments (A operand of S = Q K^T) for the 8 k-steps of 16 dims from the
 // G bf16 query rows at `qrows` (global or shared); rows g >= G and the padding
-// rows 8-15 are zero.  Returns the factor the logits must be multiplied by.
+// rows 8-15 are zero.  Global rows, like the page list and the scales, are read by
+// plain loads: __ldg is for what nobody writes while the kernel runs, and the grid
+// before may still write them when this one starts (fd_append_paged, forks).  Returns the factor the logits must be multiplied by.
 // COLS: the same registers as the B operand of S^T = K Q^T, column g holding
 // query row g mod G (every column filled).
 //  bf16: qa[c] = dims 16c + 2t4 (+1) and 16c + 8 + 2t4 (+1), as stored; 1.
@@ -942,7 +944,7 @@ __device__ __forceinline__ KeyIndex key_index(const SplitParams &p, bool paged)
 //  INT4 (f16 MMA): qa[2c + h] = dims 32c + 8t4 + 2h (+4) and 32c + 8t4 + 2h + 1
 //    (+4), the order consume_tile reads K in, each row scaled into f16 as for
 //    FP8; returns the inverse power.
-template <int G, int DT, bool GLOBAL, bool COLS = false>
+template <int G, int DT, bool COLS = false>
 __device__ __forceinline__ float load_q(const uint16_t *qrows, int lane, uint32_t (&qa)[8][2])
 {
     const int g_row = COLS ? (lane >> 2) & (G - 1) : lane >> 2, t4 = lane & 3;
@@ -954,13 +956,8 @@ __device__ __forceinline__ float load_q(const uint16_t *qrows, int lane, uint32_
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             raw[c] = make_uint4(0u, 0u, 0u, 0u);   // dims 32c + 8t4 .. +7
-            if constexpr (GLOBAL) {
-                if (valid)
-                    raw[c] = __ldg(row + 4 * c + t4);
-            } else {
-                if (valid)
-                    raw[c] = row[4 * c + t4];
-            }
+            if (valid)
+                raw[c] = row[4 * c + t4];
             const uint32_t w[4] = {raw[c].x, raw[c].y, raw[c].z, raw[c].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -995,10 +992,7 @@ __device__ __forceinline__ float load_q(const uint16_t *qrows, int lane, uint32_
         float amax = 0.f;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            if constexpr (GLOBAL)
-                raw[c] = valid ? __ldg(row + 4 * c + t4) : make_uint2(0u, 0u);
-            else
-                raw[c] = valid ? row[4 * c + t4] : make_uint2(0u, 0u);
+            raw[c] = valid ? row[4 * c + t4] : make_uint2(0u, 0u);
             const float2 a = bf16x2_to_float2(raw[c].x), b = bf16x2_to_float2(raw[c].y);
             amax = fmaxf(amax, fmaxf(fmaxf(fabsf(a.x), fabsf(a.y)), fmaxf(fabsf(b.x), fabsf(b.y))));
         }
@@ -1022,13 +1016,8 @@ __device__ __forceinline__ float load_q(const uint16_t *qrows, int lane, uint32_
         const uint32_t *qrow = reinterpret_cast<const uint32_t *>(qrows) + (valid ? g_row : 0) * (kHeadDim / 2);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
-            if constexpr (GLOBAL) {
-                qa[kk][0] = valid ? __ldg(qrow + kk * 8 + t4) : 0u;       // cols 16kk + 2t4 (+1)
-                qa[kk][1] = valid ? __ldg(qrow + kk * 8 + 4 + t4) : 0u;   // cols 16kk + 8 + 2t4 (+1)
-            } else {
-                qa[kk][0] = valid ? qrow[kk * 8 + t4] : 0u;
-                qa[kk][1] = valid ? qrow[kk * 8 + 4 + t4] : 0u;
-            }
+            qa[kk][0] = valid ? qrow[kk * 8 + t4] : 0u;       // cols 16kk + 2t4 (+1)
+            qa[kk][1] = valid ? qrow[kk * 8 + 4 + t4] : 0u;   // cols 16kk + 8 + 2t4 (+1)
         }
         return 1.f;
     }
@@ -1767,11 +1756,11 @@ __global__ void __launch_bounds__((NC + 1) * 32, MIN_CTAS)
         const Item it = read_item(desc);
         if (it.state == kItemOk) {
             uint32_t qa[8][2];
-            float qk = p.q_scale * load_q<G, DT, true, kColumnForm<G, DT>>(
+            float qk = p.q_scale * load_q<G, DT, kColumnForm<G, DT>>(
                                        p.q + ((int64_t)it.b * p.num_qo_heads + kvh * G) * kHeadDim, lane, qa);
             if constexpr (DT == kKvFp8) {   // the head's dequantisation scales
-                qk *= __ldg(p.k_scale + kvh);
-                vscale = __ldg(p.v_scale + kvh);
+                qk *= p.k_scale[kvh];
+                vscale = p.v_scale[kvh];
             }
             cs.begin(qk, lane);
             const uint32_t ring = smem_addr(smem);
@@ -2085,8 +2074,8 @@ __global__ void __launch_bounds__((NC + 2) * 32, MIN_CTAS)
                 if (go) {
                     float ks = 1.f, vs = 1.f;
                     if constexpr (DT == kKvFp8) {   // the head's dequantisation scales
-                        ks = __ldg(p.k_scale + kvh);
-                        vs = __ldg(p.v_scale + kvh);
+                        ks = p.k_scale[kvh];
+                        vs = p.v_scale[kvh];
                     }
                     write_desc(desc + slot * kDescInts, c, t0, t1, kvh, gt, ok ? kItemOk : kItemBad,
                                ks, vs);
@@ -2140,7 +2129,7 @@ __global__ void __launch_bounds__((NC + 2) * 32, MIN_CTAS)
             uint32_t qa[8][2];
             Consumer<G, KV, DT> cs;
             cs.begin(p.q_scale * __int_as_float(it.ks) *
-                         load_q<G, DT, false, kColumnForm<G, DT>>(
+                         load_q<G, DT, kColumnForm<G, DT>>(
                              reinterpret_cast<const uint16_t *>(qslots + slot * L::kQSlot), lane, qa),
                      lane);
             const int n_tiles = (it.t1 - it.t0 + kTile - 1) / kTile;

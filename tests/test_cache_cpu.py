@@ -216,7 +216,7 @@ def test_bindings_refuse_cpu_tensors():
         fd.copy_pages([pool], z[:1], z[:1])
 
 
-@pytest.mark.parametrize("name", ["append_kernel.cu", "pages_kernel.cu", "shared_kernel.cuh"])
+@pytest.mark.parametrize("name", ["append_kernel.cu", "pages_kernel.cu", "shared_kernel.cuh", "split_kernel.cuh"])
 def test_no_load_past_the_coherent_path(name):
     """Every kernel of these files starts while the grid before it may still write
     its inputs, so none may read them by loads for constant memory."""
