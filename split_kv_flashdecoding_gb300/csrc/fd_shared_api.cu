@@ -152,6 +152,13 @@ int suffix_chunk(int batch, int num_kv_heads, int64_t tokens, int num_sms)
     return c <= kMostSuffixChunk ? (int)c : 0;
 }
 
+// Where the items' streams add up their O, when one has over kFlush steps (a
+// step is a tile; with one row tile the streams take every other one).
+int64_t flush_bytes(int64_t items, int32_t chunk)
+{
+    return chunk / fd::kSharedTile > fd::kFlush ? items * 2 * fd::kSharedQRows * kHeadDim * 4 : 0;
+}
+
 // Workspace of a plan: header | tickets | the suffix plan's scratch, laid out as in a
 // workspace of its own (from kTicketBytes on) | partial LSE | partial O | sums of O.
 int64_t suffix_bytes(const fd_plan_info &suffix)
@@ -159,11 +166,20 @@ int64_t suffix_bytes(const fd_plan_info &suffix)
     return fd::kTicketBytes + round_up(suffix.workspace_bytes, 256);
 }
 
-// Where the items' streams add up their O, when one has over kFlush steps (a
-// step is a tile; with one row tile the streams take every other one).
-int64_t flush_bytes(int64_t items, int32_t chunk)
+int64_t shared_bytes(const fd_plan_info &suffix, int64_t rows, int64_t items, int32_t chunk)
 {
-    return chunk / fd::kSharedTile > fd::kFlush ? items * 2 * fd::kSharedQRows * kHeadDim * 4 : 0;
+    return suffix_bytes(suffix) + round_up(rows * 4, 256) + rows * kHeadDim * 4 + flush_bytes(items, chunk);
+}
+
+// Whether a plan's workspace holds what its other fields say (a plan is the caller's
+// memory, and the kernels write by those fields).
+bool holds_its_parts(const fd_shared_plan &plan)
+{
+    const fd_plan_info &s = plan.suffix;
+    const int64_t suffix = FD_WORKSPACE_HEADER_BYTES + round_up((int64_t)s.batch * s.num_kv_heads * 4, 256) +
+                           round_up((int64_t)s.num_partial_rows * 4, 256) + (int64_t)s.num_partial_rows * kHeadDim * 4;
+    return s.workspace_bytes >= suffix &&
+           plan.workspace_bytes >= shared_bytes(s, plan.num_partial_rows, plan.num_items, plan.chunk);
 }
 
 int make_plan(int batch, int num_qo_heads, int num_kv_heads, int head_dim, const Prefixes &x,
@@ -213,8 +229,7 @@ int make_plan(int batch, int num_qo_heads, int num_kv_heads, int head_dim, const
     plan->num_partial_rows = (int32_t)z.rows;
     plan->page_size = x.page_size;
     plan->prefix_rows = x.indptr[x.count];
-    plan->workspace_bytes = suffix_bytes(suffix) + round_up(z.rows * 4, 256) + z.rows * kHeadDim * 4 +
-                            flush_bytes(z.items, chunk);
+    plan->workspace_bytes = shared_bytes(suffix, z.rows, z.items, chunk);
     plan->timeout_ns = FD_DEFAULT_TIMEOUT_NS;
     return FD_OK;
 }
@@ -292,7 +307,8 @@ int decode_shared(const fd_shared_plan *plan, const SharedTables &t, const void 
         return rc;
     const bool paged = plan->page_size > 0;
     if (s.batch <= 0 || plan->num_prefixes <= 0 || plan->chunk <= 0 || plan->chunk % fd::kSharedTile != 0 ||
-        plan->num_items < 0 || plan->num_partial_rows < 0 || plan->prefix_rows < 0 || plan->page_size < 0)
+        plan->num_items < 0 || plan->num_partial_rows < 0 || plan->prefix_rows < 0 || plan->page_size < 0 ||
+        plan->prefix_rows > INT32_MAX || !holds_its_parts(*plan))
         return FD_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < plan->workspace_bytes)
         return FD_ERR_WORKSPACE;

@@ -117,6 +117,21 @@ def test_decode_refuses_a_bad_plan():
     assert _call(_plan(paged=True)) == -1
 
 
+def test_decode_refuses_a_plan_that_its_workspace_does_not_hold():
+    """A plan changed by hand: what the kernels would write lies behind the
+    workspace that the plan asks for."""
+    changes = [dict(chunk=128 * 40), dict(num_partial_rows=1 << 20), dict(workspace_bytes=0), dict(prefix_rows=1 << 31),
+               dict(chunk=128 * 40, num_items=1 << 20)]
+    for change in changes:
+        p = _plan()
+        for field, value in change.items():
+            setattr(p, field, value)
+        assert _call(p) == -1, change
+    p = _plan()
+    p.suffix.workspace_bytes -= 1024
+    assert _call(p) == -1
+
+
 def _paged(plan, **kw):
     a = dict(pages=9, req=P(256), ip=P(256), last=P(256), ids=P(256), kv=P(256), kvl=P(256), kvi=P(256), e=3,
              q=P(256), k=P(256), v=P(256), scale=0.1, o=P(256), lse=P(256), ws=P(256), wsb=1 << 40)
