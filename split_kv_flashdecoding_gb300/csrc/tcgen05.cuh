@@ -102,17 +102,7 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b_lo, ui
 #define FD_R4(b) "=r"(r[b]), "=r"(r[b + 1]), "=r"(r[b + 2]), "=r"(r[b + 3])
 #define FD_W4(b) "r"(r[b]), "r"(r[b + 1]), "r"(r[b + 2]), "r"(r[b + 3])
 
-// 32 columns of the warp's 32 lanes: register j of thread t is column j of lane t.
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, uint32_t *r)
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-        : FD_R4(0), FD_R4(4), FD_R4(8), FD_R4(12), FD_R4(16), FD_R4(20), FD_R4(24), FD_R4(28)
-        : "r"(addr));
-}
-
+// 16 columns of the warp's 32 lanes: register j of thread t is column j of lane t.
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, uint32_t *r)
 {
     asm volatile(
