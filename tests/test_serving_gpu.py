@@ -131,6 +131,71 @@ def test_prompt_fork_steps_and_compaction(cuda_device, fp8):
             assert (o - o2).abs().max() < 2e-5 and (lse - lse2).abs().max() < 2e-5
 
 
+def test_int4_cache_through_append_forks_copies_and_compaction(cuda_device):
+    """The same loop over an INT4 cache, whose scales are pools of their own: prompt,
+    forks with copies of codes and scales, steps through decode_paged_int4 over each
+    sample's whole list, ends and a compaction."""
+    gen = torch.Generator().manual_seed(11)
+    rand = lambda n, h: torch.randn((n, h, D), generator=gen).to(torch.bfloat16).cuda()  # noqa: E731
+    L, pages = 150, 64
+    codes = [torch.zeros((pages, P, HKV, D // 2), dtype=torch.uint8, device="cuda") for _ in "kv"]
+    scales = [torch.full((HKV, pages * P), float("nan"), device="cuda") for _ in "kv"]
+    pools = [*codes, *(x for sc in scales for x in sc.view(HKV, pages, P))]
+    rope = fd.plan_rope(D, D, base=500000.0)
+    ws = torch.zeros(fd.pages_workspace_bytes(pages, 16), dtype=torch.uint8, device="cuda")
+    refs = torch.zeros(pages, dtype=torch.int32, device="cuda")
+
+    def fork(refs, parent, own, ids, nxt):
+        cnt = -(-own // P)
+        ids, refs, src, dst = fd.fork_pages(i32(parent), i32(indptr(cnt)), i32(own - (cnt - 1) * P), ids, i32(indptr(nxt)),
+                                            int(np.sum(nxt)), P, refs, workspace=ws)
+        fd.copy_pages(pools, src, dst, workspace=ws)
+        return ids, refs
+
+    def append(new, own, ids, k, v, q):
+        cnt = -(-own // P)
+        return fd.append_paged_int4(q, k, v, *codes, *scales, i32(indptr(new)), i32(indptr(cnt)), i32(own - (cnt - 1) * P),
+                                    ids, rope=rope, workspace=ws)
+
+    def rows(ids, n):
+        at = np.concatenate([np.arange(P) + i * P for i in ids.cpu().numpy()])[:n]
+        return [oracle.int4_codes(c.view(-1, HKV, D // 2)[at]) * sc[:, at].T.double().cpu().numpy()[..., None]
+                for c, sc in zip(codes, scales)], scales[1][:, at].T.double().cpu().numpy()
+
+    ids, refs = fork(refs, np.array([-1]), np.zeros(0, int), i32([]), np.array([-(-L // P)]))
+    k, v = rand(L, HKV), rand(L, HKV)
+    append([L], np.array([L]), ids, k, v, rand(L, HQ))
+    own, values = np.full(5, L), [v.cpu()] * 5
+    cnt = -(-own // P)
+    ids, refs = fork(refs, np.zeros(5, int), np.array([L]), ids, cnt)
+    for step in range(24):
+        n = len(own)
+        if step == 12:   # two samples end, one forks once more; then the cache is compacted
+            parent = np.array([0, 2, 2, 4])
+            ids, refs = fork(refs, parent, own, ids, (-(-own // P))[parent])
+            own, values, n = own[parent], [values[p] for p in parent], 4
+            ids, refs, src, dst = fd.compact_pages(refs, ids, pages // 2, workspace=ws)
+            fd.copy_pages(pools, src, dst, workspace=ws)
+            assert int(refs.nonzero().max()) == int((refs > 0).sum()) - 1
+        nxt = -(-(own + 1) // P)
+        if (nxt > -(-own // P)).any():
+            ids, refs = fork(refs, np.arange(n), own, ids, nxt)
+        own = own + 1
+        k, v = rand(n, HKV), rand(n, HKV)
+        q = append(np.ones(n, int), own, ids, k, v, rand(n, HQ))
+        values = [torch.cat([values[b], v[b: b + 1].cpu()]) for b in range(n)]
+        ip, last = indptr(nxt), (own - (nxt - 1) * P).astype(np.int32)
+        o, lse = fd.decode_paged_int4(q, *codes, *scales, ip, last, i32(ip), i32(last), ids, SCALE)
+        assert fd.get_device_status(ws) == 0
+        for b in range(n):
+            (K, V), sv = rows(ids[ip[b]: ip[b + 1]], int(own[b]))
+            # half a code, and the scale's and the quotient's roundings (7 codes of 2^-24 each)
+            want = values[b].double().numpy()
+            assert np.all(np.abs(V - want) <= sv[..., None] * (0.5 + 2.0 ** -20))
+            ref = attend(q[b].double().cpu().numpy(), K, V)
+            assert_within(errors(o[b].cpu().numpy(), lse[b].cpu().numpy(), *ref), **TIGHT, what=f"step {step} sample {b}")
+
+
 @pytest.mark.parametrize("big", [(64, 32, 8), (4200, 4, 4)], ids=str)
 def test_one_workspace_for_plans_and_page_operators(cuda_device, big):
     """Zeroed once: a small plan, a fork and a compaction leave their partials and
