@@ -328,8 +328,10 @@ __device__ __forceinline__ bool locate_prefix(const SharedParams &p, int32_t j, 
             out.blocks = __shfl_sync(0xffffffffu, blocks, src);
             out.item0 = __shfl_sync(0xffffffffu, item_incl - items, src);
             out.row0 = __shfl_sync(0xffffffffu, row_incl - rows, src);
-            // by int32 sums that may have wrapped: the item and its rows are in range all the same
+            // by int32 sums that may have wrapped: the prefix's items are among the grid's, each
+            // of which one CTA computes, and its rows in range all the same
             return out.item0 >= 0 && out.row0 >= 0 &&
+                   (int64_t)out.item0 + (int64_t)out.splits * out.blocks * p.num_kv_heads <= p.num_items &&
                    (int64_t)out.row0 + (int64_t)out.splits * out.reqs * p.num_qo_heads <= p.num_partial_rows;
         }
         item_carry = __shfl_sync(0xffffffffu, item_incl, 31);

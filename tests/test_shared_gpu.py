@@ -475,6 +475,18 @@ def test_torn_tables_are_flagged(cuda_device, req, pre):
     assert fd.get_device_status(ws) == -6
 
 
+@pytest.mark.parametrize("req", [[0, 63, 128], [0, 65, 128], [0, 64, 128]])
+def test_prefixes_that_need_more_items_than_the_plan_are_flagged(cuda_device, req):
+    """Requests that change prefixes: as many keys and partial rows as planned, but
+    260 query rows of a KV head are two blocks where 256 were one."""
+    i = make(32, 8, [64, 64], [1000, 1000], np.zeros(128, int), room=0)
+    d = {n: i[n].cuda() for n in ("q", "kp", "vp")}
+    p = fd.plan_shared(128, 32, 8, D, [0, 64, 128], [0, 1000, 2000], 0, chunk=128)
+    ws = torch.zeros(p.workspace_bytes, dtype=torch.uint8, device="cuda")
+    fd.decode_shared(p, d["q"], d["kp"], d["vp"], None, None, i32(req), i32([0, 1000, 2000]), None, SCALE, workspace=ws)
+    assert fd.get_device_status(ws) == (0 if req[1] == 64 else -6)
+
+
 def test_page_outside_the_pool_is_flagged(cuda_device):
     i = make(8, 8, [4], [300], np.zeros(4, int), room=0)
     for bad in (-1, 10 ** 6):
