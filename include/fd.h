@@ -65,11 +65,15 @@
  * Launches: the kernels are launched with programmatic stream serialisation:
  * each may begin launching while the previous grid in the stream finishes,
  * and waits for that grid to complete before it reads or writes global
- * memory, so stream order is kept.  The one exception changes no result:
- * before that wait, the split kernel of a long split may prefetch the split's
+ * memory, so stream order is kept.  Two exceptions change no result.  Before
+ * that wait, the split kernel of a long split may prefetch the split's
  * first K/V rows into L2 (a hint), and the paged one reads the page list
- * through L2 to aim those prefetches.  Every value a kernel computes is read
- * after the wait.
+ * through L2 to aim those prefetches; every value it computes is read after the
+ * wait.  And within a call of fd_decode_shared*, the prefixes' kernel starts once
+ * the suffixes' kernel is past its wait, so that all that was written before the
+ * call is there: it reads its inputs and writes its own partials while that kernel
+ * runs, and ends after it.  The merge kernel behind it reads the prefixes' tables
+ * before its wait.
  */
 #ifndef FD_H
 #define FD_H
@@ -477,7 +481,8 @@ int fd_plan_shared_paged(int batch, int num_qo_heads, int num_kv_heads, int head
  * suffix tables that are given to a plan without room), prefix tables beyond it, or a page outside [0, num_pages) set FD_ERR_DEVICE_BOUNDS
  * (the outputs are then not valid).  num_page_entries: entries of
  * kv_page_indices.  O adds up in fp32 with weights of up to 2^40: V of up to 2^80
- * in magnitude.  Workspace: zeroed once, calls that share it in the order of one
+ * in magnitude.  The weights enter the product with V as two 16-bit parts, as in
+ * fd_decode, which leaves 2e-6 of O in the 2-norm, up to 6e-6 with long prefixes.  Workspace: zeroed once, calls that share it in the order of one
  * stream; calls of other plans and the page operators below may be among them.
  */
 int fd_decode_shared(const fd_shared_plan *plan, const int32_t *prefix_req_indptr_dev,

@@ -9,9 +9,9 @@
 // Bound: the copies move each page once in and once out (HBM); the table
 // kernels read and write a few words per page and table entry, so their time
 // is that of short dependent launches, two for a fork and two or three for a
-// compaction: 6.6-7.9 and 5.6-7.5 us a call up to 65536 pages and 51200 entries.  A fork in three
-// launches, with the fresh pages listed by one of its own, took 7.4-7.9 us and
-// 1.9 us more of the host; one launch of an 8-CTA cluster with its barrier
+// compaction: 6.6-8.1 and 5.5-7.5 us a call up to 65536 pages and 51200 entries.  A
+// fork in three launches, with the fresh pages listed by one of its own, took 7.4-7.9
+// us (for 6.7-7.9 then) and 1.9 us more of the host; one launch of an 8-CTA cluster with its barrier
 // between the steps 7.5-10 us at 1000-4096 pages, 22-28 us at 65536.
 #include <cuda_runtime.h>
 

@@ -12,7 +12,7 @@
 // is 64 KB in bf16; 32 requests of 32 heads behind 65536 keys 50-52 us, 5.3 TB/s),
 // above that the tensor cores (a tile of two row tiles 1.9-2.1 us, 1.9 PFLOP/s
 // with the products of both parts of P; 256 requests of 64 heads behind 32768
-// keys 285 us).  The products run on tcgen05
+// keys 281-292 us).  The products run on tcgen05
 // with their accumulators in tensor memory: S and O of one 128-row tile take
 // 256 columns, so a CTA holds two such streams.  With more than 128 rows the
 // streams are two row tiles that share each K and V tile; with fewer, both
@@ -45,7 +45,9 @@
 // the warps of a row on the way.  A row whose later scores are out of that
 // range (its sum over 2^40; a weight over f16's with FP8 K/V) is seen at the
 // end, and the CTA then does its item again with careful steps, which raise m
-// and rescale O.  Careful steps alone took a quarter longer (310 us for 250 of
+// and rescale O.  (One key deep in the prefix 28 nats above a row's first tile, or 6.2
+// with FP8 K/V, does that to every request behind it: 45 requests behind 20001
+// keys 52 us for 31, FP8 56 for 34.)  Careful steps alone took a quarter longer (310 us for 250 of
 // the prefixes' grid, 256 x 64 heads behind 32768 keys): the tensor cores waited
 // for the maximum, the vote of a row's two warps, and then for the weights.
 #pragma once
