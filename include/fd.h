@@ -582,7 +582,8 @@ int fd_plan_rope(int head_dim, int rotary_dim, const fd_rope_config *config, fd_
  *                    stride (elements, a multiple of 8, at least heads * D), so
  *                    they may be parts of one fused projection
  *     q_out          bf16, the rotated queries; q itself is allowed (with its
- *                    stride), other rows that share memory with q, k or v are not
+ *                    stride), and rows between those of q, k and v (with theirs);
+ *                    other memory within theirs is not
  *     append_indptr  int32 [B+1]  request b's new tokens are rows
  *                    append_indptr[b] .. append_indptr[b+1]-1
  *     kv_page_indptr, kv_last_page_len, kv_page_indices   the page tables with
@@ -707,7 +708,8 @@ int fd_compact_pages(int num_pages, const int32_t *page_refs_dev,
  * lists; src[i] < 0: none) within each of num_pools pools.  pools (host array of
  * device pointers, 16-byte aligned): pool j holds num_pages pages of
  * page_bytes[j] bytes (a multiple of 16).  An INT4 cache's scales are
- * num_kv_heads pools each, of page_size * 4 bytes a page.  No page may be both a
+ * num_kv_heads pools each, of page_size * 4 bytes a page.  num_copies times the
+ * 16 KB segments of a page is at most 2^31 - 1.  No page may be both a
  * source and a destination, nor a destination twice (the lists of fork and
  * compact never hold such a pair); what lands in one that is, is undefined.  Ids
  * outside the pool are skipped and set FD_ERR_DEVICE_BOUNDS (workspace may be
