@@ -379,8 +379,14 @@ __device__ __forceinline__ void merge_group(const SplitParams &p, int prefix, in
             for (int u = 1; u < U; ++u)
                 bm = fmaxf(bm, l[u][g]);
             const float m_new = fmaxf(m[g], bm);
-            if (m_new == -INFINITY)   // only empty partials so far (none in practice)
-                continue;
+            if (m_new == -INFINITY) {   // only empty partials so far (none in practice), or NaN
+                bool nan = false;
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    nan |= l[u][g] != l[u][g];
+                if (!nan)
+                    continue;
+            }
             const float f = expf(m[g] - m_new);
             den[g] *= f;
             acc[g].x *= f;
@@ -1441,7 +1447,8 @@ __device__ __forceinline__ void combine_states(const SplitParams &p, const Item 
         o.y *= inv;
         o.z *= inv;
         o.w *= inv;
-        const float lse_nat = den > 0.f ? (mx + log2f(den)) * kLn2 : -INFINITY;
+        // a NaN sum stays one: a later merge must not take the partial for an empty one
+        const float lse_nat = den == 0.f ? -INFINITY : (mx + log2f(den)) * kLn2;
         if (direct) {
             const int64_t row = (int64_t)it.b * p.num_qo_heads + it.kvh * G + g;
             *reinterpret_cast<float4 *>(p.o + row * kHeadDim + 4 * c4) = o;
