@@ -339,6 +339,34 @@ int fd_decode_paged_int4(int batch, int num_qo_heads, int num_kv_heads, int head
                          void *stream);
 
 /*
+ * INT8 KV cache, paged, with a scale per page and KV head.  At FP8's bytes a
+ * value is off by at most 1/254 of its page's largest magnitude (about 0.8 % rms
+ * for normal values) where E4M3's four significant bits leave 2.6 %, and no scale
+ * has to be known beforehand: fd_append_paged_int8 keeps each page's from the
+ * keys that come in.
+ *
+ * Layout: k_pages, v_pages int8 [num_pages, page_size, Hkv, D], two's-complement
+ * codes; k_scale, v_scale (device, fp32) [num_pages, Hs], Hs = Hkv rounded up to
+ * a multiple of 4 (whole 16-byte pieces, so that fd_copy_pages copies them as
+ * pools of Hs * 4 bytes a page; the entries from Hkv on are not used).  The value
+ * of a K element of page p and head h is code * k_scale[p][h], likewise for V.
+ *
+ * fd_decode_paged_int8 -- fd_decode_paged over this cache.  q stays bf16 and O, LSE
+ * fp32; the codes widen to f16 exactly, a page's K scale multiplies its logits in
+ * fp32 and its V scale its softmax weights, as an INT4 row's do.  Any scales, of
+ * either sign; one of +-inf or NaN propagates (as NaN) to the requests that attend
+ * the page.  Workspace and plan as for fd_decode_paged.
+ */
+int fd_decode_paged_int8(int batch, int num_qo_heads, int num_kv_heads, int head_dim,
+                         int page_size, int num_pages, const int32_t *kv_page_indptr_host,
+                         const int32_t *kv_last_page_len_host, const int32_t *kv_page_indptr_dev,
+                         const int32_t *kv_last_page_len_dev, const int32_t *kv_page_indices_dev,
+                         const void *q, const void *k_pages_int8, const void *v_pages_int8,
+                         const float *k_scale, const float *v_scale, float scale,
+                         float *o, float *lse, void *workspace, int64_t workspace_bytes,
+                         void *stream);
+
+/*
  * Graph-capturable decode -- for engines that run decode steps as CUDA graphs
  * with a fixed batch (FD++ §6 integration).  fd_decode plans on the host from
  * the host copy of kv_indptr on every call, which a graph replay cannot

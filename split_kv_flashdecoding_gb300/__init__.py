@@ -15,6 +15,7 @@ Entry points (same names as the C ABI, minus the ``fd_`` prefix):
   plan_paged(...), decode_paged(...)    the same over a paged KV cache (page tables)
   decode_fp8(...), decode_paged_fp8()   FP8 (E4M3) K/V, one scale per KV head
   decode_int4(...), decode_paged_int4() INT4 K/V, one scale per key row and KV head
+  decode_paged_int8(...)                INT8 K/V in pages, one scale per page and KV head
   plan_graph(...), decode_graph(...)    graph-capturable decode (device-side plan)
   merge_states(...)                     merge attention states (sequence shards)
   plan_shared(...), decode_shared(...)  decode over prefixes that requests share
@@ -158,6 +159,8 @@ SIGNATURES = {
                              _P, _P, _P, _I64, _P], _I),
     "fd_decode_int4": ([_I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _I64, _P], _I),
     "fd_decode_paged_int4": ([_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _F,
+                              _P, _P, _P, _I64, _P], _I),
+    "fd_decode_paged_int8": ([_I, _I, _I, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _F,
                               _P, _P, _P, _I64, _P], _I),
     "fd_plan_shared": ([_I, _I, _I, _I, _I, _P, _P, _I64, _I, _I, _PS], _I),
     "fd_plan_shared_paged": ([_I, _I, _I, _I, _I, _I, _P, _P, _P, _I64, _I, _I, _PS], _I),
@@ -570,6 +573,56 @@ def _ws(workspace, dev: int):
     return workspace.data_ptr(), workspace.nbytes
 
 
+def scale_heads(num_kv_heads: int) -> int:
+    """Entries of a page's row of INT8 scales: num_kv_heads rounded up to a multiple of 4."""
+    return -(-num_kv_heads // 4) * 4
+
+
+def _int8_cache(name, k_pages, v_pages, k_scale, v_scale, num_kv_heads, head_dim, dev):
+    """Addresses of an INT8 cache's pools and scales, checked against one another."""
+    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or \
+            k_pages.shape[2:] != (num_kv_heads, head_dim):
+        raise FdError(-1, f"{name}: pools of another shape")
+    shape = (k_pages.shape[0], scale_heads(num_kv_heads))
+    if k_scale.shape != shape or v_scale.shape != shape:
+        raise FdError(-1, f"{name}: scales must be [num_pages, num_kv_heads rounded up to a multiple of 4]")
+    return (_need("k_pages", k_pages, torch.int8, dev), _need("v_pages", v_pages, torch.int8, dev),
+            _need("k_scale", k_scale, torch.float32, dev), _need("v_scale", v_scale, torch.float32, dev))
+
+
+def decode_paged_int8(q, k_pages_int8, v_pages_int8, k_scale, v_scale, kv_page_indptr_host,
+                      kv_last_page_len_host, kv_page_indptr_dev, kv_last_page_len_dev,
+                      kv_page_indices_dev, scale: float, *, o=None, lse=None, workspace=None,
+                      stream=None):
+    """fd_decode_paged_int8: fd_decode_paged over int8 page pools
+    [num_pages, page_size, Hkv, D] with fp32 scales [num_pages, scale_heads(Hkv)]."""
+    B, Hq, D = q.shape
+    num_pages, page_size, Hkv = k_pages_int8.shape[:3]
+    ip, ll = _host_indptr(kv_page_indptr_host), _host_indptr(kv_last_page_len_host)
+    if ip.size != B + 1 or ll.size != B or kv_page_indptr_dev.numel() != B + 1 or \
+            kv_last_page_len_dev.numel() < B or kv_page_indices_dev.numel() < ip[B]:
+        raise FdError(-1, "fd_decode_paged_int8: tables of another length than the batch's")
+    i32, f32, dev = torch.int32, torch.float32, q.get_device()
+    with _on(q, stream):
+        if o is None:
+            o = torch.empty((B, Hq, D), dtype=f32, device=q.device)
+        if lse is None:
+            lse = torch.empty((B, Hq), dtype=f32, device=q.device)
+        if o.shape != q.shape or lse.shape != q.shape[:2]:
+            raise FdError(-1, "fd_decode_paged_int8: o must have q's shape and lse [batch, num_qo_heads]")
+        if workspace is None:
+            need = plan_paged(B, Hq, Hkv, D, page_size, ip, ll).workspace_bytes
+            workspace = torch.zeros(need, dtype=torch.uint8, device=q.device)
+        kp, vp, ks, vs = _int8_cache("fd_decode_paged_int8", k_pages_int8, v_pages_int8, k_scale, v_scale, Hkv, D, dev)
+        _check(lib().fd_decode_paged_int8(
+            B, Hq, Hkv, D, page_size, num_pages, _host_ptr(ip), _host_ptr(ll),
+            _need("kv_page_indptr", kv_page_indptr_dev, i32, dev), _need("kv_last_page_len", kv_last_page_len_dev, i32, dev),
+            _need("kv_page_indices", kv_page_indices_dev, i32, dev), _need("q", q, torch.bfloat16, dev), kp, vp, ks, vs,
+            float(scale), _need("o", o, f32, dev), _need("lse", lse, f32, dev), *_ws(workspace, dev), _stream(stream)),
+            "fd_decode_paged_int8")
+    return o, lse
+
+
 def plan_rope(head_dim: int, rotary_dim: int, *, interleaved: bool = False, base: float = 10000.0,
               scaling=None) -> RopeInfo:
     """fd_plan_rope: the rotary frequencies (host only).  scaling: None,
@@ -958,7 +1011,8 @@ def get_device_status(workspace, stream=None) -> int:
 __all__ = [
     "PlanInfo", "FdError", "lib", "build", "plan", "plan_work_items", "decode_split", "merge",
     "decode", "decode_static_workspace", "plan_paged", "decode_paged", "decode_fp8",
-    "decode_paged_fp8", "decode_int4", "decode_paged_int4", "plan_graph", "decode_graph", "merge_states", "get_device_status",
+    "decode_paged_fp8", "decode_int4", "decode_paged_int4", "decode_paged_int8", "scale_heads",
+    "plan_graph", "decode_graph", "merge_states", "get_device_status",
     "SharedPlan", "plan_shared", "plan_shared_paged", "decode_shared", "decode_shared_paged",
     "decode_shared_fp8", "decode_shared_paged_fp8",
     "RopeInfo", "plan_rope", "append_paged", "append_paged_fp8", "append_paged_int4",

@@ -71,7 +71,7 @@ int fd::make_kv_map(CUtensorMap *map, const void *base, int64_t rows, int num_kv
     return r == CUDA_SUCCESS ? FD_OK : FD_ERR_INVALID_ARG;
 }
 
-// FP8 K or V [rows, Hkv, 128] (one byte per value) as a 2-D tensor of rows x
+// FP8 or INT8 K or V [rows, Hkv, 128] (one byte per value) as a 2-D tensor of rows x
 // Hkv*128 bytes; one box = box_rows rows x the head's 128 bytes, 128-byte
 // swizzle, zero fill past the last row.
 int fd::make_kv_map_fp8(CUtensorMap *map, const void *base, int64_t rows, int num_kv_heads, int box_rows)
@@ -216,7 +216,9 @@ int fd::launch_stage1(const fd_plan_info *info, const void *q, const void *k, co
     int rc;
     const int64_t rows = paged ? (int64_t)paged->num_pages * paged->page_size : info->total_tokens;
     const int box_rows = paged && paged->page_size % kBoxRows != 0 ? 16 : kBoxRows;
-    if (kv_type == fd::kKvTypeFp8) {
+    if (kv_type == fd::kKvTypeInt8 && !paged)
+        return FD_ERR_INVALID_ARG;
+    if (kv_type == fd::kKvTypeFp8 || kv_type == fd::kKvTypeInt8) {
         if ((rc = make_kv_map_fp8(&maps.k, k, rows, info->num_kv_heads, box_rows)) != FD_OK ||
             (rc = make_kv_map_fp8(&maps.v, v, rows, info->num_kv_heads, box_rows)) != FD_OK)
             return rc;
@@ -272,6 +274,7 @@ int fd::launch_stage1(const fd_plan_info *info, const void *q, const void *k, co
     p.v_data = static_cast<const uint8_t *>(v);
     p.k_scale = quant ? quant->k_scale : nullptr;
     p.v_scale = quant ? quant->v_scale : nullptr;
+    p.scale_heads = fd::scale_heads(info->num_kv_heads);
     // Persistent grid: at most one wave of resident CTAs on the plan's SMs.
     p.num_work = info->num_work;
     const int64_t slots = (int64_t)info->num_sms * fd::split_ctas_per_sm();
@@ -428,7 +431,7 @@ extern "C" int fd_plan_paged(int batch, int num_qo_heads, int num_kv_heads, int 
 
 namespace {
 
-// fd_decode_paged, fd_decode_paged_fp8 and fd_decode_paged_int4 (quant non-null).
+// fd_decode_paged, fd_decode_paged_fp8, _int4 and _int8 (quant non-null).
 int decode_paged(int batch, int num_qo_heads, int num_kv_heads, int head_dim, int page_size,
                  int num_pages, const int32_t *kv_page_indptr_host,
                  const int32_t *kv_last_page_len_host, const int32_t *kv_page_indptr_dev,
@@ -570,6 +573,25 @@ extern "C" int fd_decode_paged_int4(int batch, int num_qo_heads, int num_kv_head
     return decode_paged(batch, num_qo_heads, num_kv_heads, head_dim, page_size, num_pages,
                         kv_page_indptr_host, kv_last_page_len_host, kv_page_indptr_dev,
                         kv_last_page_len_dev, kv_page_indices_dev, q, k_pages_int4, v_pages_int4,
+                        scale, o, lse, workspace, workspace_bytes, stream, &f);
+}
+
+extern "C" int fd_decode_paged_int8(int batch, int num_qo_heads, int num_kv_heads, int head_dim,
+                                    int page_size, int num_pages,
+                                    const int32_t *kv_page_indptr_host,
+                                    const int32_t *kv_last_page_len_host,
+                                    const int32_t *kv_page_indptr_dev,
+                                    const int32_t *kv_last_page_len_dev,
+                                    const int32_t *kv_page_indices_dev, const void *q,
+                                    const void *k_pages_int8, const void *v_pages_int8,
+                                    const float *k_scale, const float *v_scale, float scale,
+                                    float *o, float *lse, void *workspace, int64_t workspace_bytes,
+                                    void *stream)
+{
+    const QuantKV f{fd::kKvTypeInt8, k_scale, v_scale};
+    return decode_paged(batch, num_qo_heads, num_kv_heads, head_dim, page_size, num_pages,
+                        kv_page_indptr_host, kv_last_page_len_host, kv_page_indptr_dev,
+                        kv_last_page_len_dev, kv_page_indices_dev, q, k_pages_int8, v_pages_int8,
                         scale, o, lse, workspace, workspace_bytes, stream, &f);
 }
 

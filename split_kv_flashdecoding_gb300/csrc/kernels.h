@@ -63,22 +63,26 @@ struct SplitParams {
     int32_t num_pages;
     int32_t num_page_entries;   // kv_indptr[B]
     int32_t last_len_param[kParamIndptr];
-    // Element type of K/V (kKvTypeBf16, kKvTypeFp8, kKvTypeInt4), dequantised in
+    // Element type of K/V (kKvTypeBf16, .. kKvTypeInt8), dequantised in
     // registers.  FP8 (E4M3): one byte per element; k_scale, v_scale [Hkv]
     // (device) multiply the head's K and V values.  INT4: two four-bit codes
     // per byte, and one scale per key row and head (k_scale, v_scale
     // [Hkv][kv_rows] fp32), loaded without tensor maps from k_data / v_data.
+    // INT8 (paged): one byte per element, and one scale per page and head
+    // (k_scale, v_scale [num_pages][scale_heads] fp32).
     int32_t kv_type;
     int32_t kv_rows;            // rows of K/V: T keys, or num_pages * page_size
     const uint8_t *k_data;      // K and V themselves
     const uint8_t *v_data;
     const float *k_scale;
     const float *v_scale;
+    int32_t scale_heads;        // INT8: num_kv_heads rounded up to a multiple of 4
 };
 
 constexpr int kKvTypeBf16 = 0;
 constexpr int kKvTypeFp8 = 1;
 constexpr int kKvTypeInt4 = 2;
+constexpr int kKvTypeInt8 = 3;
 
 // The split kernel's TMA descriptors of K and V (INT4 K/V: not read).
 struct KvMaps {
@@ -108,10 +112,12 @@ struct MergeParams {
 cudaError_t launch_split(const KvMaps &maps, const SplitParams &p, int group, int num_ctas,
                          cudaStream_t stream);
 
-// The same for FP8 and INT4 K/V (p.kv_type); launch_split dispatches to them.
+// The same for FP8, INT4 and INT8 K/V (p.kv_type); launch_split dispatches to them.
 cudaError_t launch_split_fp8(const KvMaps &maps, const SplitParams &p, int group, int num_ctas,
                              cudaStream_t stream);
 cudaError_t launch_split_int4(const KvMaps &maps, const SplitParams &p, int group, int num_ctas,
+                              cudaStream_t stream);
+cudaError_t launch_split_int8(const KvMaps &maps, const SplitParams &p, int group, int num_ctas,
                               cudaStream_t stream);
 
 // Resident split-kernel CTAs per SM the launch shape is built for.

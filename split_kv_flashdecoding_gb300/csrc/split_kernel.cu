@@ -16,6 +16,7 @@ cudaError_t launch_split(const KvMaps &maps, const SplitParams &p, int group, in
     case kKvTypeBf16: return launch_split_dt<kKvBf16>(maps, p, group, num_ctas, stream);
     case kKvTypeFp8: return launch_split_fp8(maps, p, group, num_ctas, stream);
     case kKvTypeInt4: return launch_split_int4(maps, p, group, num_ctas, stream);
+    case kKvTypeInt8: return launch_split_int8(maps, p, group, num_ctas, stream);
     default: return cudaErrorInvalidValue;
     }
 }

@@ -1,6 +1,6 @@
 // split_kernel.cuh -- stage 1 of split-KV decode attention on sm_103a (the
 // kernel templates; split_kernel.cu instantiates them for bf16 K/V and
-// split_kernel_fp8.cu for FP8 E4M3 K/V).
+// split_kernel_fp8.cu, _int4.cu and _int8.cu for quantised K/V).
 //
 // "FlashDecoding++: sequence-dimension KV split parallelism for LLM serving"
 // (techknowgenie.com), §2 (each block keeps the query on chip and copies only
@@ -62,7 +62,7 @@ namespace {
 constexpr int kHalfBytes = kTile * 128;   // 32 keys x 64 bf16
 
 enum KvLayout { kKvRagged = 0, kKvPaged = 1, kKvPaged16 = 2 };
-enum KvType { kKvBf16 = 0, kKvFp8 = 1, kKvInt4 = 2 };
+enum KvType { kKvBf16 = 0, kKvFp8 = 1, kKvInt4 = 2, kKvInt8 = 3 };
 
 // One pipeline stage holds K then V for kTile = 32 keys of one KV head.
 //  bf16: a tensor's key row r (0..31), column half h (64 columns of 128 bytes,
@@ -80,18 +80,30 @@ enum KvType { kKvBf16 = 0, kKvFp8 = 1, kKvInt4 = 2 };
 //    a consumer warp's own lanes on ragged one-item calls, the producer warp's
 //    otherwise): with 64-byte rows and per-row scales, TMA boxes cost more
 //    copy-engine time per byte than the copies do.
+//  INT8 (paged only): the rows as for FP8; beside the ring, per stage, the scales
+//    of the pages of rows 0..15 and 16..31 (K's two, V's two), each copied by a
+//    lane of the producer warp (four arrivals more on the full barrier).
 template <int KV, int DT>
 struct Stage {
     static constexpr bool kFp8 = DT == kKvFp8;
     static constexpr bool kInt4 = DT == kKvInt4;
+    static constexpr bool kInt8 = DT == kKvInt8;
+    static constexpr bool kByte = kFp8 || kInt8;   // one byte a value, 128-byte rows
+    static constexpr bool kScales = kInt4 || kInt8;   // scales in the stage
     static constexpr bool kDirect = kInt4;
-    static constexpr int kRowBytes = kInt4 ? kHeadDim / 2 : kFp8 ? kHeadDim : 2 * kHeadDim;
-    static constexpr int kFullArrivals = kDirect ? 32 : 1;   // full barrier: arrivals per phase
+    static constexpr bool kWarpIssue = kDirect || kInt8;   // every producer lane takes part in issue()
+    static constexpr int kScaleLanes = 4;                  // INT8: lanes that copy a scale each
+    static constexpr int kRowBytes = kInt4 ? kHeadDim / 2 : kByte ? kHeadDim : 2 * kHeadDim;
+    static constexpr int kFullArrivals = kDirect ? 32 : kInt8 ? 1 + kScaleLanes : 1;   // full barrier: arrivals per phase
     static constexpr int kTensorBytes = kTile * kRowBytes;
     static constexpr int kBoxRows = KV == kKvPaged16 ? 16 : kTile;
     static constexpr int kKsOff = 2 * kTensorBytes;            // INT4 scales
     static constexpr int kVsOff = kKsOff + kTile * 4;
     static constexpr int kBytes = kInt4 ? kVsOff + kTile * 4 : 2 * kTensorBytes;
+    // INT8 scales: behind the ring, so that every stage's boxes start on a swizzle
+    // pattern without padding
+    static constexpr int kSideBytes = kInt8 ? 4 * kScaleLanes : 0;
+    static constexpr int kSideKs = 0, kSideVs = 8;
     static constexpr int kHalfStride = KV == kKvPaged16 ? 2048 : kHalfBytes;
     static constexpr int kBlockStride = KV == kKvPaged16 ? 4096 : 2048;
     // a TMA copy's shared-memory destination must be 128-byte aligned
@@ -104,7 +116,7 @@ struct Stage {
     {
         if constexpr (kInt4)
             return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
-        else if constexpr (kFp8)
+        else if constexpr (kByte)
             return r * 128 + ((c ^ (r & 7)) << 4);
         else
             return (c >> 3) * kHalfStride + (r >> 4) * kBlockStride + (r & 15) * 128 +
@@ -118,6 +130,14 @@ constexpr int kNoExp = -1000;                  // INT4 V-scale exponent before a
 __device__ __forceinline__ float pow2i(int k)
 {
     return k < -126 ? 0.f : k > 127 ? INFINITY : __int_as_float((127 + k) << 23);
+}
+
+// A bound of two V scales' magnitudes; NaN where either is (fmaxf drops it).
+__device__ __forceinline__ float v_bound(float a, float b)
+{
+    a = fabsf(a);
+    b = fabsf(b);
+    return a != a || b != b ? __int_as_float(0x7fffffff) : fmaxf(a, b);
 }
 
 enum Misc { kAbort, kIssued, kDescs, kLast, kFinalK, kMiscCount };
@@ -146,13 +166,13 @@ __device__ __forceinline__ Item read_item(const volatile int *d)
 // Shared memory of the one-item kernel: [stage ring | full[NS] empty[NS] |
 // item descriptor | misc].  The consumer-state combine and the stage-2 merge
 // of the CTA's item work over the drained ring.
-template <int G, int NC, int NS, int SB>
+template <int G, int NC, int NS, int SB, int SIDE = 0>
 struct SingleLayout {
     static_assert(NS % NC == 0, "each stage must belong to one consumer warp");
     static_assert(G >= 1 && G <= kMaxGroup, "group size");
     static constexpr int kWarps = NC + 1;
     static_assert(kWarps * G * (kHeadDim + 2) * 4 <= NS * SB, "the merge fits the ring");
-    static constexpr int kOffBar = NS * SB;
+    static constexpr int kOffBar = NS * (SB + SIDE);
     static constexpr int kOffDesc = kOffBar + 2 * NS * 8;
     static constexpr int kOffMisc = kOffDesc + kDescInts * 4;
     static constexpr int kOffFills = kOffMisc + kMiscCount * 4;   // copies issued into each stage
@@ -167,7 +187,7 @@ struct SingleLayout {
 // item_empty[4] (consumers and epilogue warp are done with the slot),
 // state_full[2], state_empty[2] (a finished item's consumer states, handed to
 // the epilogue warp).
-template <int G, int NC, int NS, int SB>
+template <int G, int NC, int NS, int SB, int SIDE = 0>
 struct PersistentLayout {
     static_assert(NS % NC == 0, "each stage must belong to one consumer warp");
     static_assert(G >= 1 && G <= kMaxGroup, "group size");
@@ -179,7 +199,7 @@ struct PersistentLayout {
     static constexpr int kStateBytes = (NC * G * (kHeadDim + 2) * 4 + 127) / 128 * 128;
     static_assert(kWarps * G * (kHeadDim + 2) * 4 <= NS * SB,
                   "the last item's merge works over the drained ring");
-    static constexpr int kOffQ = NS * SB;
+    static constexpr int kOffQ = (NS * (SB + SIDE) + 127) / 128 * 128;
     static constexpr int kOffState = kOffQ + kDescSlots * kQSlot;
     static constexpr int kOffBar = kOffState + 2 * kStateBytes;
     static constexpr int kNumBars = 2 * NS + 2 * kDescSlots + 4;
@@ -308,6 +328,42 @@ __device__ __forceinline__ void int4x8_to_f16x2x4(uint32_t x, uint32_t (&r)[4])
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[1]) : "r"(t1), "r"(kSixteenth), "r"(kMinus72));
     asm("sub.f16x2 %0, %1, %2;" : "=r"(r[2]) : "r"(t2), "r"(k1032));
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[3]) : "r"(t3), "r"(kSixteenth), "r"(kMinus72));
+}
+
+// Two's-complement bytes of x -> f16x2: lo = bytes A and B, hi = bytes C and D
+// (the first of each in the low half).  A byte with its
+// sign bit flipped is u = n + 128; under the exponent byte of 1024 it is the f16
+// 1024 + u, and subtracting 1152 leaves n, exactly.
+template <int A, int B, int C, int D>
+__device__ __forceinline__ void int8x4_to_f16x2x2(uint32_t x, uint32_t &lo, uint32_t &hi)
+{
+    const uint32_t u = x ^ 0x80808080u;
+    constexpr uint32_t k1024 = 0x64646464u, k1152 = 0x64806480u;
+    lo = __byte_perm(u, k1024, 0x4040u | A | (B << 8));
+    hi = __byte_perm(u, k1024, 0x4040u | C | (D << 8));
+    asm("sub.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(k1152));
+    asm("sub.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(k1152));
+}
+
+// A word of a key row, four bytes in order, to f16 (bytes 0, 1 and 2, 3); and a
+// word that ldmatrix.trans gave, two bytes of one key and two of the next, to the
+// first byte of both keys and the second.  FP8 and INT8.
+template <int DT>
+__device__ __forceinline__ void widen_row(uint32_t x, uint32_t &lo, uint32_t &hi)
+{
+    if constexpr (DT == kKvInt8)
+        int8x4_to_f16x2x2<0, 1, 2, 3>(x, lo, hi);
+    else
+        e4m3x4_to_f16x2x2(x, lo, hi);
+}
+
+template <int DT>
+__device__ __forceinline__ void widen_pair(uint32_t x, uint32_t &first, uint32_t &second)
+{
+    if constexpr (DT == kKvInt8)
+        int8x4_to_f16x2x2<0, 2, 1, 3>(x, first, second);
+    else
+        e4m3x4_to_f16x2x2(__byte_perm(x, 0u, 0x3120), first, second);
 }
 
 // 16 zero bytes to shared memory (32-bit shared address, 16-byte aligned).
@@ -469,6 +525,10 @@ __device__ __forceinline__ void merge_group(const SplitParams &p, int prefix, in
 //    same order.  For P V, ldmatrix.trans gives lane (g, t4) dims 16c + 2g and
 //    +1 of keys 2t4 and 2t4+1, so one tile of columns takes the even dims and
 //    one the odd: o_acc[2c + e] holds dims 16c + 4t4 + e (and + 2).
+//  INT8: as FP8, the codes widened to f16 (exact) by integer operations; the
+//    scale of a key's page multiplies its logit, and its V scale its weight in
+//    P V.  Pages are whole 16-key halves of a tile, so a scale is uniform over
+//    one of the MMA's k-steps of keys.
 //  INT4: mma.sync f16; the four-bit codes are widened to f16 (exact) in
 //    registers.  An ldmatrix of the 64-byte key rows gives lane (g, t4) dims
 //    32c + 8t4 .. +7 of key g in one word; nibbles j and j + 4 pair up, so
@@ -479,7 +539,7 @@ __device__ __forceinline__ void merge_group(const SplitParams &p, int prefix, in
 //    32c + 4g .. +3 of keys 2t4 and 2t4 + 1, so o_acc[4c + j] holds dims
 //    32c + 8t4 + j (and + 4).
 template <int KV, int DT>
-__device__ __forceinline__ void consume_tile(uint32_t st, int n_valid, const uint32_t (&qa)[8][2],
+__device__ __forceinline__ void consume_tile(uint32_t st, uint32_t side, int n_valid, const uint32_t (&qa)[8][2],
                                              float qk_scale, int lane, float &m_run, float &l_part,
                                              float (&o_acc)[16][4], int &v_exp)
 {
@@ -493,9 +553,9 @@ __device__ __forceinline__ void consume_tile(uint32_t st, int n_valid, const uin
     // get P = 0, but 0 * NaN would still reach O: a tile that ends early has
     // its V rows from n_valid on zeroed (the stage is this warp's alone).  The
     // proxy fence orders these writes before the stage's next TMA refill.
-    // INT4 needs none: its codes are finite, and a masked key's V scale is
-    // replaced by 0 before P V.
-    if constexpr (!S::kInt4) {
+    // INT4 and INT8 need none: their codes are finite, a masked key's weight is 0,
+    // and its V scale is replaced by 0 before P V.
+    if constexpr (!S::kScales) {
         if (n_valid < kTile) {
             constexpr int kChunks = S::kRowBytes / 16;
             const uint32_t vt = st + S::kTensorBytes;
@@ -526,7 +586,7 @@ __device__ __forceinline__ void consume_tile(uint32_t st, int n_valid, const uin
                 mma_f16(sc[jn], qa[2 * c + 1][0], 0u, qa[2 * c + 1][1], 0u, b[2], b[3]);
             }
         }
-    } else if constexpr (S::kFp8) {
+    } else if constexpr (S::kByte) {
 #pragma unroll
         for (int jn = 0; jn < 4; ++jn) {
 #pragma unroll
@@ -537,7 +597,7 @@ __device__ __forceinline__ void consume_tile(uint32_t st, int n_valid, const uin
                 for (int m = 0; m < 4; ++m) {
                     const int c = 4 * hc + m;
                     uint32_t b0, b1;   // dims 16c + 4t4 (+1), 16c + 4t4 + 2 (+3)
-                    e4m3x4_to_f16x2x2(kb[m], b0, b1);
+                    widen_row<DT>(kb[m], b0, b1);
                     mma_f16(sc[jn], qa[c][0], 0u, qa[c][1], 0u, b0, b1);
                 }
             }
@@ -571,6 +631,8 @@ __device__ __forceinline__ void consume_tile(uint32_t st, int n_valid, const uin
             float logit = sc[jn][e] * qk_scale;
             if constexpr (S::kInt4)
                 logit = sc[jn][e] * lds_f32(ks_base + 4 * key) * qk_scale;
+            if constexpr (S::kInt8)
+                logit = sc[jn][e] * (lds_f32(side + S::kSideKs + 4 * (jn >> 1)) * qk_scale);
             const float v = key < n_valid ? logit : -INFINITY;
             x[2 * jn + e] = v;
             mt = fmaxf(mt, v);
@@ -594,10 +656,16 @@ __device__ __forceinline__ void consume_tile(uint32_t st, int n_valid, const uin
     // subnormal range, whatever the scales.  When v_exp grows, O is rescaled
     // by the same exact power of two, together with the softmax rescale;
     // write_state multiplies 2^v_exp back.
+    // INT8: the same with the two scales of the tile's 16-key halves.
     float vs[2][4] = {};
     float oscale = alpha;
-    if constexpr (S::kInt4) {
+    if constexpr (S::kScales) {
         float vmax = 0.f;
+        if constexpr (S::kInt8) {
+            vs[0][0] = lds_f32(side + S::kSideVs);
+            vs[1][0] = n_valid > 16 ? lds_f32(side + S::kSideVs + 4) : 0.f;
+            vmax = v_bound(vs[0][0], vs[1][0]);
+        } else {
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
             const int k0 = 16 * ks + 2 * t4;   // keys k0 (+1) and k0 + 8 (+9)
@@ -613,6 +681,7 @@ __device__ __forceinline__ void consume_tile(uint32_t st, int n_valid, const uin
         // lanes of one t4 hold the same keys: the warp's 32 keys in 2 steps
         vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 1));
         vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
+        }
         if (!(vmax <= 0.f)) {   // a nonzero, inf or NaN scale: vmax < 2^e
             const int e = ((__float_as_int(vmax) >> 23) & 0xFF) - 126;
             if (e > v_exp) {
@@ -634,11 +703,18 @@ __device__ __forceinline__ void consume_tile(uint32_t st, int n_valid, const uin
     // 2ks, 2ks+1); rows 0-7 hi, rows 8-15 lo = P - hi, in the MMA's type.
     uint32_t pa[2][4];
     // INT4: 2^-v_exp (NaN-propagating 0 once an infinite or NaN scale was seen)
-    const float vinv = S::kInt4 ? (v_exp == kNoExp ? 1.f : pow2i(-v_exp)) : 1.f;
+    const float vinv = S::kScales ? (v_exp == kNoExp ? 1.f : pow2i(-v_exp)) : 1.f;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
         float p0 = x[4 * ks], p1 = x[4 * ks + 1];
         float p2 = x[4 * ks + 2], p3 = x[4 * ks + 3];
+        if constexpr (S::kInt8) {
+            const float w = vs[ks][0] * vinv;
+            p0 *= w;
+            p1 *= w;
+            p2 *= w;
+            p3 *= w;
+        }
         if constexpr (S::kInt4) {
             // keys 16ks + 2t4 (+1) and 16ks + 8 + 2t4 (+1)
             p0 *= vs[ks][0] * vinv;
@@ -646,7 +722,7 @@ __device__ __forceinline__ void consume_tile(uint32_t st, int n_valid, const uin
             p2 *= vs[ks][2] * vinv;
             p3 *= vs[ks][3] * vinv;
         }
-        if constexpr (S::kFp8 || S::kInt4) {
+        if constexpr (S::kByte || S::kInt4) {
             const float h0 = f16_round(p0), h1 = f16_round(p1);
             const float h2 = f16_round(p2), h3 = f16_round(p3);
             pa[ks][0] = pack_f16(h0, h1);
@@ -687,7 +763,7 @@ __device__ __forceinline__ void consume_tile(uint32_t st, int n_valid, const uin
                 }
             }
         }
-    } else if constexpr (S::kFp8) {
+    } else if constexpr (S::kByte) {
         const uint32_t vt = st + S::kTensorBytes;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
@@ -703,8 +779,8 @@ __device__ __forceinline__ void consume_tile(uint32_t st, int n_valid, const uin
                     // bytes of vb: key 2t4 (dim 2g, 2g+1), key 2t4+1 (dim 2g, 2g+1);
                     // regrouped as (key 2t4, key 2t4+1) of dim 2g, then of dim 2g+1
                     uint32_t lo_even, lo_odd, hi_even, hi_odd;
-                    e4m3x4_to_f16x2x2(__byte_perm(vb[2 * h], 0u, 0x3120), lo_even, lo_odd);
-                    e4m3x4_to_f16x2x2(__byte_perm(vb[2 * h + 1], 0u, 0x3120), hi_even, hi_odd);
+                    widen_pair<DT>(vb[2 * h], lo_even, lo_odd);
+                    widen_pair<DT>(vb[2 * h + 1], hi_even, hi_odd);
                     mma_f16(o_acc[2 * c], pa[ks][0], pa[ks][1], pa[ks][2], pa[ks][3], lo_even, hi_even);
                     mma_f16(o_acc[2 * c + 1], pa[ks][0], pa[ks][1], pa[ks][2], pa[ks][3], lo_odd,
                             hi_odd);
@@ -859,6 +935,8 @@ struct TileSource {
     //  cp.async (INT4, every lane): the lane's share of the 16-byte chunks of
     //    both tensors (rows past the end of K/V zero-filled) and the K and V
     //    scale of row `lane`, then one arrival once its copies have landed.
+    //  INT8 (every lane): lane 0 the boxes as for FP8; the first four lanes copy
+    //    the scales of the boxes' pages (a tile of one box: the same page twice).
     __device__ __forceinline__ void issue(int g, int kvh, int32_t ya, int32_t yb) const
     {
         const int s = g % NS;
@@ -868,8 +946,18 @@ struct TileSource {
             copy_direct(dst, kvh, ya, yb);
             cp_async_mbar_arrive(bar);
         } else {
-            mbar_arrive_expect_tx(bar, SL::kBytes);
-            if constexpr (SL::kFp8) {
+            if constexpr (SL::kInt8) {
+                if (lane < SL::kScaleLanes) {
+                    const int32_t page = (SL::kBoxRows < kTile && (lane & 1) ? yb : ya) / p.page_size;
+                    const float *scales = lane < 2 ? p.k_scale : p.v_scale;
+                    cp_async_4(smem_addr(ring) + NS * SL::kBytes + s * SL::kSideBytes + 4 * lane, scales + (int64_t)page * p.scale_heads + kvh, 4);
+                    cp_async_mbar_arrive(bar);
+                }
+                if (lane != 0)
+                    return;
+            }
+            mbar_arrive_expect_tx(bar, 2 * SL::kTensorBytes);
+            if constexpr (SL::kByte) {
                 const int32_t x = kvh * kHeadDim;
                 tma_load_2d(dst, tm_k, x, ya, bar, pol);
                 tma_load_2d(dst + SL::kTensorBytes, tm_v, x, ya, bar, pol);
@@ -942,7 +1030,7 @@ __device__ __forceinline__ KeyIndex key_index(const SplitParams &p, bool paged)
 // COLS: the same registers as the B operand of S^T = K Q^T, column g holding
 // query row g mod G (every column filled).
 //  bf16: qa[c] = dims 16c + 2t4 (+1) and 16c + 8 + 2t4 (+1), as stored; 1.
-//  FP8 (f16 MMA): qa[c] = dims 16c + 4t4 (+1) and 16c + 4t4 + 2 (+3), the order
+//  FP8 and INT8 (f16 MMA): qa[c] = dims 16c + 4t4 (+1) and 16c + 4t4 + 2 (+3), the order
 //    consume_tile reads K in.  Each row is first scaled by the power of two
 //    that puts its largest magnitude in [2^8, 2^9), so every bf16 value of the
 //    row converts to f16 exactly (values below 2^-22 of the row's maximum
@@ -992,7 +1080,7 @@ __device__ __forceinline__ float load_q(const uint16_t *qrows, int lane, uint32_
             qa[2 * c + 1][1] = f16pair(__byte_perm(raw[c].y, raw[c].w, 0x7632));   // dims +3, +7
         }
         return __int_as_float((127 - sh) << 23);
-    } else if constexpr (DT == kKvFp8) {
+    } else if constexpr (DT == kKvFp8 || DT == kKvInt8) {
         const uint2 *row = reinterpret_cast<const uint2 *>(qrows + (valid ? g_row : 0) * kHeadDim);
         uint2 raw[8];
         float amax = 0.f;
@@ -1058,7 +1146,7 @@ __device__ __forceinline__ void write_state(uint8_t *state, int warp, int lane,
                     (o_acc[n][1] + o_acc[n][3]) * vscale, (o_acc[n + 1][1] + o_acc[n + 1][3]) * vscale,
                     (o_acc[n + 2][1] + o_acc[n + 2][3]) * vscale, (o_acc[n + 3][1] + o_acc[n + 3][3]) * vscale);
             }
-        } else if constexpr (DT == kKvFp8) {
+        } else if constexpr (DT == kKvFp8 || DT == kKvInt8) {
             float *dst = comb_acc + (warp * G + g_row) * kHeadDim + 4 * t4;
 #pragma unroll
             for (int c = 0; c < 8; ++c)   // dims 16c + 4t4 + (0, 1, 2, 3)
@@ -1089,7 +1177,7 @@ template <int G, int KV, int DT>
 struct RowConsumer {
     float o_acc[16][4];
     float m_run, l_part, qk;
-    int v_exp;   // INT4: see consume_tile
+    int v_exp;   // INT4 and INT8: see consume_tile
 
     __device__ __forceinline__ void begin(float qk_row, int)
     {
@@ -1101,20 +1189,20 @@ struct RowConsumer {
         for (int n = 0; n < 16; ++n)
             o_acc[n][0] = o_acc[n][1] = o_acc[n][2] = o_acc[n][3] = 0.f;
     }
-    __device__ __forceinline__ void tile(uint32_t st, int n_valid, const uint32_t (&qa)[8][2], int lane)
+    __device__ __forceinline__ void tile(uint32_t st, uint32_t side, int n_valid, const uint32_t (&qa)[8][2], int lane)
     {
-        consume_tile<KV, DT>(st, n_valid, qa, qk, lane, m_run, l_part, o_acc, v_exp);
+        consume_tile<KV, DT>(st, side, n_valid, qa, qk, lane, m_run, l_part, o_acc, v_exp);
     }
     // fp8_vscale: the head's V scale (FP8 K/V; ignored otherwise)
     template <int NC>
     __device__ __forceinline__ void write(uint8_t *state, int warp, int lane, float fp8_vscale) const
     {
-        const float vscale = DT == kKvInt4 ? (v_exp == kNoExp ? 1.f : pow2i(v_exp)) : fp8_vscale;
+        const float vscale = Stage<KV, DT>::kScales ? (v_exp == kNoExp ? 1.f : pow2i(v_exp)) : fp8_vscale;
         write_state<G, NC, DT>(state, warp, lane, o_acc, m_run, l_part, vscale);
     }
 };
 
-// The column form for FP8 and INT4 K/V with G <= 4: S^T = K Q^T and
+// The column form for FP8, INT4 and INT8 K/V with G <= 4: S^T = K Q^T and
 // O^T = V^T P^T, the tile's keys (scores) and the head's dims (output) in the
 // MMA's 16 rows and the query heads in its 8 columns, so every MMA row carries
 // data: half the MMAs and half the output accumulators of the row form, whose
@@ -1128,16 +1216,16 @@ struct RowConsumer {
 //  2t4 and 2t4 + 1 (m[e], l[e], qk[e]: column 2t4 + e).  P^T as the B operand
 //  is the transpose of the score fragments (movmatrix).  Output m-block n
 //  holds, for the lane's two columns, dims dim0(n, g) (c0, c1) and
-//  dim0(n, g) + 1 (c2, c3): INT4 n = 2c + jp -> 32c + 4g + 2jp, FP8 n = c ->
+//  dim0(n, g) + 1 (c2, c3): INT4 n = 2c + jp -> 32c + 4g + 2jp, FP8 and INT8 n = c ->
 //  16c + 2g (the orders ldmatrix.trans and the widenings give).
 template <int G, int KV, int DT>
 struct ColumnConsumer {
     static_assert(G == 1 || G == 2 || G == 4, "column form: two columns per head");
-    static_assert(DT == kKvFp8 || DT == kKvInt4, "column form: FP8 or INT4 K/V");
-    static constexpr bool kInt4 = DT == kKvInt4;
+    static_assert(DT != kKvBf16, "column form: quantised K/V");
+    static constexpr bool kInt4 = DT == kKvInt4, kInt8 = DT == kKvInt8;
     float o[8][4];
     float m[2], l[2], qk[2], lo[2];
-    int v_exp;   // INT4: see consume_tile
+    int v_exp;   // INT4 and INT8: see consume_tile
 
     static __device__ __forceinline__ int dim0(int n, int g)
     {
@@ -1161,13 +1249,13 @@ struct ColumnConsumer {
             o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     }
 
-    __device__ __forceinline__ void tile(uint32_t st, int n_valid, const uint32_t (&qa)[8][2], int lane)
+    __device__ __forceinline__ void tile(uint32_t st, uint32_t side, int n_valid, const uint32_t (&qa)[8][2], int lane)
     {
         using S = Stage<KV, DT>;
         const int g = lane >> 2, lr = lane & 7, lm = lane >> 3;
 
         // FP8: V rows past the last key zeroed, as in consume_tile
-        if constexpr (!kInt4) {
+        if constexpr (!S::kScales) {
             if (n_valid < kTile) {
                 constexpr int kChunks = S::kRowBytes / 16;
                 const uint32_t vt = st + S::kTensorBytes;
@@ -1211,8 +1299,8 @@ struct ColumnConsumer {
 #pragma unroll
                     for (int mc = 0; mc < 4; ++mc) {
                         uint32_t a0, a1, a2, a3;
-                        e4m3x4_to_f16x2x2(k0[mc], a0, a2);
-                        e4m3x4_to_f16x2x2(k1[mc], a1, a3);
+                        widen_row<DT>(k0[mc], a0, a2);
+                        widen_row<DT>(k1[mc], a1, a3);
                         mma_f16(s[mb], a0, a1, a2, a3, qa[4 * hc + mc][0], qa[4 * hc + mc][1]);
                     }
                 }
@@ -1225,15 +1313,27 @@ struct ColumnConsumer {
         const uint32_t ks_base = st + S::kKsOff, vs_base = st + S::kVsOff;
         float x[2][4], vs[2][2];
         float mt0 = -INFINITY, mt1 = -INFINITY, vmax = 0.f;
+        float vs8[2] = {0.f, 0.f};   // INT8: the V scales of the tile's 16-key halves
+        if constexpr (kInt8) {
+            vs8[0] = lds_f32(side + S::kSideVs);
+            vs8[1] = n_valid > 16 ? lds_f32(side + S::kSideVs + 4) : 0.f;
+            vmax = v_bound(vs8[0], vs8[1]);
+        }
 #pragma unroll
-        for (int mb = 0; mb < 2; ++mb)
+        for (int mb = 0; mb < 2; ++mb) {
+            float qk0 = qk[0], qk1 = qk[1];
+            if constexpr (kInt8) {
+                const float ks = lds_f32(side + S::kSideKs + 4 * mb);
+                qk0 *= ks;
+                qk1 *= ks;
+            }
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 const int key = 16 * mb + 8 * hf + g;
                 const bool ok = key < n_valid;
                 const float ksc = kInt4 ? lds_f32(ks_base + 4 * key) : 1.f;
-                const float v0 = ok ? s[mb][2 * hf] * ksc * qk[0] : -INFINITY;
-                const float v1 = ok ? s[mb][2 * hf + 1] * ksc * qk[1] : -INFINITY;
+                const float v0 = ok ? s[mb][2 * hf] * ksc * qk0 : -INFINITY;
+                const float v1 = ok ? s[mb][2 * hf + 1] * ksc * qk1 : -INFINITY;
                 x[mb][2 * hf] = v0;
                 x[mb][2 * hf + 1] = v1;
                 mt0 = fmaxf(mt0, v0);
@@ -1243,6 +1343,7 @@ struct ColumnConsumer {
                     vmax = fmaxf(vmax, fabsf(vs[mb][hf]));
                 }
             }
+        }
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) {
             mt0 = fmaxf(mt0, __shfl_xor_sync(0xffffffffu, mt0, sh));
@@ -1266,7 +1367,7 @@ struct ColumnConsumer {
             }
         l[0] = fmaf(l[0], os0, ps0);
         l[1] = fmaf(l[1], os1, ps1);
-        if constexpr (kInt4) {
+        if constexpr (S::kScales) {
             if (!(vmax <= 0.f)) {   // a nonzero, inf or NaN scale: vmax < 2^e
                 const int e = ((__float_as_int(vmax) >> 23) & 0xFF) - 126;
                 if (e > v_exp) {
@@ -1291,15 +1392,15 @@ struct ColumnConsumer {
         // + 8 in b1, column g): the weights (INT4: p * v_scale * 2^-v_exp) as
         // f16 (hi columns) or their remainder after f16 (lo columns), packed
         // per key row and transposed
-        const float vinv = kInt4 && v_exp != kNoExp ? pow2i(-v_exp) : 1.f;
+        const float vinv = S::kScales && v_exp != kNoExp ? pow2i(-v_exp) : 1.f;
         uint32_t pt[2][2];
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 float p0 = x[mb][2 * hf], p1 = x[mb][2 * hf + 1];
-                if constexpr (kInt4) {
-                    const float w = vs[mb][hf] * vinv;
+                if constexpr (S::kScales) {
+                    const float w = (kInt8 ? vs8[mb] : vs[mb][hf]) * vinv;
                     p0 *= w;
                     p1 *= w;
                 }
@@ -1345,8 +1446,8 @@ struct ColumnConsumer {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {   // chunk c = 2 cp + h
                         uint32_t a0, a1, a2, a3;
-                        e4m3x4_to_f16x2x2(__byte_perm(vb[2 * h], 0u, 0x3120), a0, a1);
-                        e4m3x4_to_f16x2x2(__byte_perm(vb[2 * h + 1], 0u, 0x3120), a2, a3);
+                        widen_pair<DT>(vb[2 * h], a0, a1);
+                        widen_pair<DT>(vb[2 * h + 1], a2, a3);
                         mma_f16(o[2 * cp + h], a0, a1, a2, a3, pt[ks][0], pt[ks][1]);
                     }
                 }
@@ -1364,7 +1465,7 @@ struct ColumnConsumer {
         float *comb_m = comb_acc + NC * G * kHeadDim;
         float *comb_l = comb_m + NC * G;
         const int g = lane >> 2, t4 = lane & 3;
-        const float vscale = !kInt4 ? fp8_vscale : v_exp == kNoExp ? 1.f : pow2i(v_exp);
+        const float vscale = DT == kKvFp8 ? fp8_vscale : v_exp == kNoExp ? 1.f : pow2i(v_exp);
         float lt[2] = {l[0], l[1]};
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) {
@@ -1408,9 +1509,9 @@ struct ColumnConsumer {
     }
 };
 
-// FP8 and INT4 K/V with G <= 4 take the column form.
+// FP8, INT4 and INT8 K/V with G <= 4 take the column form.
 template <int G, int DT>
-constexpr bool kColumnForm = (DT == kKvFp8 || DT == kKvInt4) && G <= 4;
+constexpr bool kColumnForm = DT != kKvBf16 && G <= 4;
 template <int G, int KV, int DT>
 using Consumer = std::conditional_t<kColumnForm<G, DT>, ColumnConsumer<G, KV, DT>, RowConsumer<G, KV, DT>>;
 
@@ -1565,7 +1666,7 @@ template <class SG>
 __device__ __forceinline__ void prefetch_box(const CUtensorMap *tm_k, const CUtensorMap *tm_v, int kvh,
                                              int32_t y)
 {
-    if constexpr (SG::kFp8) {
+    if constexpr (SG::kByte) {
         tma_prefetch_l2_2d(tm_k, kvh * kHeadDim, y);
         tma_prefetch_l2_2d(tm_v, kvh * kHeadDim, y);
     } else {
@@ -1584,7 +1685,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, MIN_CTAS)
                     const __grid_constant__ SplitParams p)
 {
     using SG = Stage<KV, DT>;
-    using L = SingleLayout<G, NC, NS, SG::kBytes>;
+    using L = SingleLayout<G, NC, NS, SG::kBytes, SG::kSideBytes>;
     constexpr bool paged = KV != kKvRagged;
     constexpr bool warp_loop = paged || SG::kDirect;   // the whole producer warp runs the issue loop
     // Ragged FP8 and INT4: each consumer warp refills its own stages (see the
@@ -1651,11 +1752,11 @@ __global__ void __launch_bounds__((NC + 1) * 32, MIN_CTAS)
         // outside the pool are skipped.
         constexpr int kPrologueBytes = 256 * 1024;
         constexpr int kPrefetchTiles = kPrologueBytes / SG::kBytes;   // per CTA
-        // FP8 in a paged cache runs none: with 2 KB page boxes the prologue's
+        // FP8 and INT8 in a paged cache run none: with 2 KB page boxes the prologue's
         // prefetches only queue ahead of the stage copies (measured, P = 16:
         // 64k 38.6 -> 35.7 us without it, 128k 67.8 -> 63.9 us, cold 64k
         // 44.6 -> 40.5 us; P = 32: 30.3 -> 29.4 us).
-        if constexpr (!SG::kDirect && !(paged && SG::kFp8)) {
+        if constexpr (!SG::kDirect && !(paged && SG::kByte)) {
             if (early_derive && found && c.len > 0) {   // warp-uniform
                 const int32_t len = split_len_for(c.len, c.splits);
                 const int32_t t0p = c.s * len;
@@ -1716,7 +1817,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, MIN_CTAS)
             for (int i = 0; i < first; ++i) {
                 int32_t ya = 0, yb = 0;
                 src.tile_rows(i, ya, yb);
-                if (SG::kDirect || lane == 0)
+                if (SG::kWarpIssue || lane == 0)
                     src.issue(i, kvh, ya, yb);
             }
         }
@@ -1742,14 +1843,14 @@ __global__ void __launch_bounds__((NC + 1) * 32, MIN_CTAS)
                     } else if (misc[kAbort]) {
                         go = 0;
                     }
-                    if (go && !SG::kDirect)
+                    if (go && !SG::kWarpIssue)
                         src.issue(i, kvh, ya, yb);
                 }
                 if constexpr (warp_loop)
                     go = __shfl_sync(0xffffffffu, go, 0);
                 if (!go)
                     break;
-                if constexpr (SG::kDirect)
+                if constexpr (SG::kWarpIssue)
                     src.issue(i, kvh, ya, yb);
                 issued = i + 1;
             }
@@ -1801,7 +1902,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, MIN_CTAS)
                     const int i = warp + NC * k;
                     cp_async_wait_group<D - 1>();
                     __syncwarp();   // every lane's copies of the tile have landed
-                    cs.tile(ring + (i % NS) * SG::kBytes, min(kTile, it.t1 - (it.t0 + i * kTile)), qa, lane);
+                    cs.tile(ring + (i % NS) * SG::kBytes, 0u, min(kTile, it.t1 - (it.t0 + i * kTile)), qa, lane);
                     __syncwarp();   // every lane is done reading the stage
                     fill(k + D);
                 }
@@ -1817,7 +1918,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, MIN_CTAS)
                             report(p.status, FD_ERR_TIMEOUT);
                         break;
                     }
-                    cs.tile(ring + s * SG::kBytes, min(kTile, it.t1 - (it.t0 + i * kTile)), qa, lane);
+                    cs.tile(ring + s * SG::kBytes, ring + NS * SG::kBytes + s * SG::kSideBytes, min(kTile, it.t1 - (it.t0 + i * kTile)), qa, lane);
                     __syncwarp();
                     if constexpr (self_refill) {
                         // FP8: lane 0 refills the stage it just freed with the
@@ -1916,7 +2017,7 @@ __global__ void __launch_bounds__((NC + 2) * 32, MIN_CTAS)
                                const __grid_constant__ SplitParams p)
 {
     using SG = Stage<KV, DT>;
-    using L = PersistentLayout<G, NC, NS, SG::kBytes>;
+    using L = PersistentLayout<G, NC, NS, SG::kBytes, SG::kSideBytes>;
     constexpr bool paged = KV != kKvRagged;
     constexpr bool warp_loop = paged || SG::kDirect;   // the whole producer warp runs the issue loop
     constexpr int kProducer = NC;   // the epilogue warp is NC + 1
@@ -2001,7 +2102,7 @@ __global__ void __launch_bounds__((NC + 2) * 32, MIN_CTAS)
                         } else if (misc[kAbort]) {
                             go = 0;
                         }
-                        if (go && !SG::kDirect)
+                        if (go && !SG::kWarpIssue)
                             src.issue(gt, kvh, ya, yb);
                     }
                     if constexpr (warp_loop)
@@ -2010,7 +2111,7 @@ __global__ void __launch_bounds__((NC + 2) * 32, MIN_CTAS)
                         stop = 1;
                         break;
                     }
-                    if constexpr (SG::kDirect)
+                    if constexpr (SG::kWarpIssue)
                         src.issue(gt, kvh, ya, yb);
                     ++gt;
                 }
@@ -2152,7 +2253,7 @@ __global__ void __launch_bounds__((NC + 2) * 32, MIN_CTAS)
                     ok = false;
                     break;
                 }
-                cs.tile(ring + s * SG::kBytes, min(kTile, it.t1 - (it.t0 + i * kTile)), qa, lane);
+                cs.tile(ring + s * SG::kBytes, ring + NS * SG::kBytes + s * SG::kSideBytes, min(kTile, it.t1 - (it.t0 + i * kTile)), qa, lane);
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_addr(&bars[NS + s]));
@@ -2333,6 +2434,21 @@ constexpr int kNCInt4ColsP = FD_SPLIT_INT4_COLUMN_PWARPS;   // persistent kernel
 constexpr int kNCFp8Cols = FD_SPLIT_FP8_COLUMN_WARPS;
 constexpr int kNCFp8ColsP = FD_SPLIT_FP8_COLUMN_PWARPS;
 
+#ifndef FD_SPLIT_INT8_ROW_WARPS
+#define FD_SPLIT_INT8_ROW_WARPS 4
+#endif
+#ifndef FD_SPLIT_INT8_ROW_PWARPS
+#define FD_SPLIT_INT8_ROW_PWARPS 4
+#endif
+#ifndef FD_SPLIT_INT8_COLUMN_WARPS
+#define FD_SPLIT_INT8_COLUMN_WARPS 4
+#endif
+#ifndef FD_SPLIT_INT8_COLUMN_PWARPS
+#define FD_SPLIT_INT8_COLUMN_PWARPS 4
+#endif
+constexpr int kNCInt8 = FD_SPLIT_INT8_ROW_WARPS, kNCInt8P = FD_SPLIT_INT8_ROW_PWARPS;
+constexpr int kNCInt8Cols = FD_SPLIT_INT8_COLUMN_WARPS, kNCInt8ColsP = FD_SPLIT_INT8_COLUMN_PWARPS;
+
 // One wave of items: one item per CTA.  More: the persistent kernel on
 // num_ctas CTAs.
 template <int G, int KV, int DT>
@@ -2342,13 +2458,17 @@ cudaError_t launch_g(const KvMaps &m, const SplitParams &p, int num_ctas, cudaSt
     // consumer warps of the one-item and the persistent kernel; FP8 and INT4
     // tiles are half the bytes or less, so their rings hold two stages per
     // consumer warp
-    constexpr int NC1 = DT == kKvInt4 ? (cols ? kNCInt4Cols : kNCInt4) : DT == kKvFp8 && cols ? kNCFp8Cols : kNC;
-    constexpr int NCP = DT == kKvInt4 && cols ? kNCInt4ColsP : DT == kKvFp8 && cols ? kNCFp8ColsP : kNC;
+    constexpr int NC1 = DT == kKvInt4   ? (cols ? kNCInt4Cols : kNCInt4)
+                        : DT == kKvInt8 ? (cols ? kNCInt8Cols : kNCInt8)
+                        : DT == kKvFp8 && cols ? kNCFp8Cols : kNC;
+    constexpr int NCP = DT == kKvInt4 && cols  ? kNCInt4ColsP
+                        : DT == kKvInt8        ? (cols ? kNCInt8ColsP : kNCInt8P)
+                        : DT == kKvFp8 && cols ? kNCFp8ColsP : kNC;
     constexpr int NS1 = DT == kKvBf16 ? kNS : 2 * NC1;
     constexpr int NS = DT == kKvBf16 ? kNS : 2 * NCP;
     using SG = Stage<KV, DT>;
-    using LS = SingleLayout<G, NC1, NS1, SG::kBytes>;
-    using LP = PersistentLayout<G, NCP, NS, SG::kBytes>;
+    using LS = SingleLayout<G, NC1, NS1, SG::kBytes, SG::kSideBytes>;
+    using LP = PersistentLayout<G, NCP, NS, SG::kBytes, SG::kSideBytes>;
     static_assert(kMinCtas * (LS::kAlloc + 1024) <= 233472 && kMinCtas * (LP::kAlloc + 1024) <= 233472,
                   "the resident CTAs must fit in shared memory");
     if (num_ctas >= p.num_work) {   // one wave: one item (or, device-side plan, at most one) per CTA
@@ -2375,7 +2495,11 @@ cudaError_t launch_split_dt(const KvMaps &m, const SplitParams &p, int group, in
     auto by_layout = [&](auto g) -> cudaError_t {
         constexpr int G = decltype(g)::value;
         switch (kv) {
-        case kKvRagged: return launch_g<G, kKvRagged, DT>(m, p, num_ctas, stream);
+        case kKvRagged:
+            if constexpr (DT == kKvInt8)   // its scales are of pages
+                return cudaErrorInvalidValue;
+            else
+                return launch_g<G, kKvRagged, DT>(m, p, num_ctas, stream);
         case kKvPaged: return launch_g<G, kKvPaged, DT>(m, p, num_ctas, stream);
         default: return launch_g<G, kKvPaged16, DT>(m, p, num_ctas, stream);
         }

@@ -10,13 +10,20 @@
 
 namespace fd {
 
-// Quantised K/V: the element type (kKvTypeFp8 or kKvTypeInt4) and the device
-// scales -- FP8: [Hkv] each; INT4: [Hkv][rows] each.
+// Quantised K/V: the element type (kKvTypeFp8, kKvTypeInt4 or kKvTypeInt8) and
+// the device scales -- FP8: [Hkv] each; INT4: [Hkv][rows] each; INT8:
+// [num_pages][scale_heads(Hkv)] each.
 struct QuantKV {
     int type;
     const float *k_scale;
     const float *v_scale;
 };
+
+// Floats of a page's row of INT8 scales: whole 16-byte pieces, as page copies take.
+constexpr int scale_heads(int num_kv_heads)
+{
+    return (num_kv_heads + 3) / 4 * 4;
+}
 
 // The page-pool description of a paged KV cache (see fd_decode_paged).
 struct PagedKV {
@@ -46,7 +53,7 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 // K or V [rows, Hkv, 128] bf16 as a tensor map of one head's box_rows rows.
 int make_kv_map(CUtensorMap *map, const void *base, int64_t rows, int num_kv_heads, int box_rows);
 
-// FP8 K or V [rows, Hkv, 128], one byte a value, likewise.
+// FP8 or INT8 K or V [rows, Hkv, 128], one byte a value, likewise.
 int make_kv_map_fp8(CUtensorMap *map, const void *base, int64_t rows, int num_kv_heads, int box_rows);
 
 // Argument checks and the split kernel's launch (see fd_api.cu).  early_next: see
