@@ -80,30 +80,23 @@ enum KvType { kKvBf16 = 0, kKvFp8 = 1, kKvInt4 = 2, kKvInt8 = 3 };
 //    a consumer warp's own lanes on ragged one-item calls, the producer warp's
 //    otherwise): with 64-byte rows and per-row scales, TMA boxes cost more
 //    copy-engine time per byte than the copies do.
-//  INT8 (paged only): the rows as for FP8; beside the ring, per stage, the scales
-//    of the pages of rows 0..15 and 16..31 (K's two, V's two), each copied by a
-//    lane of the producer warp (four arrivals more on the full barrier).
+//  INT8 (paged only): the rows as for FP8; the consumers look the scales of a
+//    tile's pages up themselves (PageScaleFeed).
 template <int KV, int DT>
 struct Stage {
     static constexpr bool kFp8 = DT == kKvFp8;
     static constexpr bool kInt4 = DT == kKvInt4;
     static constexpr bool kInt8 = DT == kKvInt8;
     static constexpr bool kByte = kFp8 || kInt8;   // one byte a value, 128-byte rows
-    static constexpr bool kScales = kInt4 || kInt8;   // scales in the stage
+    static constexpr bool kScales = kInt4 || kInt8;   // scales by row or page
     static constexpr bool kDirect = kInt4;
-    static constexpr bool kWarpIssue = kDirect || kInt8;   // every producer lane takes part in issue()
-    static constexpr int kScaleLanes = 4;                  // INT8: lanes that copy a scale each
     static constexpr int kRowBytes = kInt4 ? kHeadDim / 2 : kByte ? kHeadDim : 2 * kHeadDim;
-    static constexpr int kFullArrivals = kDirect ? 32 : kInt8 ? 1 + kScaleLanes : 1;   // full barrier: arrivals per phase
+    static constexpr int kFullArrivals = kDirect ? 32 : 1;   // full barrier: arrivals per phase
     static constexpr int kTensorBytes = kTile * kRowBytes;
     static constexpr int kBoxRows = KV == kKvPaged16 ? 16 : kTile;
     static constexpr int kKsOff = 2 * kTensorBytes;            // INT4 scales
     static constexpr int kVsOff = kKsOff + kTile * 4;
     static constexpr int kBytes = kInt4 ? kVsOff + kTile * 4 : 2 * kTensorBytes;
-    // INT8 scales: behind the ring, so that every stage's boxes start on a swizzle
-    // pattern without padding
-    static constexpr int kSideBytes = kInt8 ? 4 * kScaleLanes : 0;
-    static constexpr int kSideKs = 0, kSideVs = 8;
     static constexpr int kHalfStride = KV == kKvPaged16 ? 2048 : kHalfBytes;
     static constexpr int kBlockStride = KV == kKvPaged16 ? 4096 : 2048;
     // a TMA copy's shared-memory destination must be 128-byte aligned
@@ -140,6 +133,85 @@ __device__ __forceinline__ float v_bound(float a, float b)
     return a != a || b != b ? __int_as_float(0x7fffffff) : fmaxf(a, b);
 }
 
+// INT8: the scales of the pages that hold a tile's keys 0..15 and 16..31.
+struct PageScales {
+    float k[2], v[2];
+};
+
+// INT8: a consumer warp's scales, tile by tile (its tiles are `NC` apart).  Lanes 0..3
+// hold one each (K of the two halves, V of them): the scale of the next tile and the
+// page id of the one after are on their way while a tile is worked on, so that the
+// two dependent loads cost the warp no time and the producer nothing.  (Copied into
+// the stages by the producer, whose box a tile sets the pace: 64k keys 39.5 us for
+// pages of 64.)  Of a half past the last key: 0.
+template <bool ON, int NC>
+struct PageScaleFeed {
+    const SplitParams &p;
+    int32_t base, pg, off, left;       // page-list entry of the lane's next id; keys from it on
+    int32_t pages_on, rows_on, kvh;
+    int32_t id;                        // of the tile after next, -1: none
+    float scale;                       // of the next tile
+
+    __device__ __forceinline__ PageScaleFeed(const SplitParams &p_) : p(p_) {}
+
+    __device__ __forceinline__ int32_t next_id()
+    {
+        const int32_t x = left > 0 ? p.page_indices[base + pg] : -1;
+        left -= NC * kTile;
+        pg += pages_on;
+        off += rows_on;
+        if (off >= p.page_size) {
+            off -= p.page_size;
+            ++pg;
+        }
+        return x;
+    }
+
+    __device__ __forceinline__ float load(int32_t x) const
+    {
+        if (x == -1)
+            return 0.f;
+        const int lane = threadIdx.x & 31;
+        // (the producer reports a page outside the pool and reads page 0 for it)
+        const int64_t page = x < 0 || x >= p.num_pages ? 0 : x;
+        return (lane < 2 ? p.k_scale : p.v_scale)[page * p.scale_heads + kvh];
+    }
+
+    // An item of keys t0 .. t1 of the request whose page list starts at `base_`, its
+    // tiles from tile i on.
+    __device__ __forceinline__ void begin(int32_t base_, int32_t t0, int32_t t1, int kvh_, int i)
+    {
+        if constexpr (ON) {
+            const int lane = threadIdx.x & 31;
+            const int32_t key = t0 + i * kTile + 16 * (lane & 1);
+            base = base_;
+            kvh = kvh_;
+            pg = key / p.page_size;
+            off = key % p.page_size;
+            left = lane < 4 ? t1 - key : 0;
+            pages_on = NC * kTile / p.page_size;
+            rows_on = NC * kTile % p.page_size;
+            const int32_t first = next_id();
+            id = next_id();
+            scale = load(first);
+        }
+    }
+
+    __device__ __forceinline__ PageScales take()
+    {
+        PageScales s{};
+        if constexpr (ON) {
+            s.k[0] = __shfl_sync(0xffffffffu, scale, 0);
+            s.k[1] = __shfl_sync(0xffffffffu, scale, 1);
+            s.v[0] = __shfl_sync(0xffffffffu, scale, 2);
+            s.v[1] = __shfl_sync(0xffffffffu, scale, 3);
+            scale = load(id);
+            id = next_id();
+        }
+        return s;
+    }
+};
+
 enum Misc { kAbort, kIssued, kDescs, kLast, kFinalK, kMiscCount };
 
 // An item (one split of one KV head) as the producer hands it to the other
@@ -166,13 +238,13 @@ __device__ __forceinline__ Item read_item(const volatile int *d)
 // Shared memory of the one-item kernel: [stage ring | full[NS] empty[NS] |
 // item descriptor | misc].  The consumer-state combine and the stage-2 merge
 // of the CTA's item work over the drained ring.
-template <int G, int NC, int NS, int SB, int SIDE = 0>
+template <int G, int NC, int NS, int SB>
 struct SingleLayout {
     static_assert(NS % NC == 0, "each stage must belong to one consumer warp");
     static_assert(G >= 1 && G <= kMaxGroup, "group size");
     static constexpr int kWarps = NC + 1;
     static_assert(kWarps * G * (kHeadDim + 2) * 4 <= NS * SB, "the merge fits the ring");
-    static constexpr int kOffBar = NS * (SB + SIDE);
+    static constexpr int kOffBar = NS * SB;
     static constexpr int kOffDesc = kOffBar + 2 * NS * 8;
     static constexpr int kOffMisc = kOffDesc + kDescInts * 4;
     static constexpr int kOffFills = kOffMisc + kMiscCount * 4;   // copies issued into each stage
@@ -187,7 +259,7 @@ struct SingleLayout {
 // item_empty[4] (consumers and epilogue warp are done with the slot),
 // state_full[2], state_empty[2] (a finished item's consumer states, handed to
 // the epilogue warp).
-template <int G, int NC, int NS, int SB, int SIDE = 0>
+template <int G, int NC, int NS, int SB>
 struct PersistentLayout {
     static_assert(NS % NC == 0, "each stage must belong to one consumer warp");
     static_assert(G >= 1 && G <= kMaxGroup, "group size");
@@ -199,7 +271,7 @@ struct PersistentLayout {
     static constexpr int kStateBytes = (NC * G * (kHeadDim + 2) * 4 + 127) / 128 * 128;
     static_assert(kWarps * G * (kHeadDim + 2) * 4 <= NS * SB,
                   "the last item's merge works over the drained ring");
-    static constexpr int kOffQ = (NS * (SB + SIDE) + 127) / 128 * 128;
+    static constexpr int kOffQ = NS * SB;
     static constexpr int kOffState = kOffQ + kDescSlots * kQSlot;
     static constexpr int kOffBar = kOffState + 2 * kStateBytes;
     static constexpr int kNumBars = 2 * NS + 2 * kDescSlots + 4;
@@ -539,7 +611,7 @@ __device__ __forceinline__ void merge_group(const SplitParams &p, int prefix, in
 //    32c + 4g .. +3 of keys 2t4 and 2t4 + 1, so o_acc[4c + j] holds dims
 //    32c + 8t4 + j (and + 4).
 template <int KV, int DT>
-__device__ __forceinline__ void consume_tile(uint32_t st, uint32_t side, int n_valid, const uint32_t (&qa)[8][2],
+__device__ __forceinline__ void consume_tile(uint32_t st, const PageScales &ps, int n_valid, const uint32_t (&qa)[8][2],
                                              float qk_scale, int lane, float &m_run, float &l_part,
                                              float (&o_acc)[16][4], int &v_exp)
 {
@@ -632,7 +704,7 @@ __device__ __forceinline__ void consume_tile(uint32_t st, uint32_t side, int n_v
             if constexpr (S::kInt4)
                 logit = sc[jn][e] * lds_f32(ks_base + 4 * key) * qk_scale;
             if constexpr (S::kInt8)
-                logit = sc[jn][e] * (lds_f32(side + S::kSideKs + 4 * (jn >> 1)) * qk_scale);
+                logit = sc[jn][e] * (ps.k[jn >> 1] * qk_scale);
             const float v = key < n_valid ? logit : -INFINITY;
             x[2 * jn + e] = v;
             mt = fmaxf(mt, v);
@@ -662,8 +734,8 @@ __device__ __forceinline__ void consume_tile(uint32_t st, uint32_t side, int n_v
     if constexpr (S::kScales) {
         float vmax = 0.f;
         if constexpr (S::kInt8) {
-            vs[0][0] = lds_f32(side + S::kSideVs);
-            vs[1][0] = n_valid > 16 ? lds_f32(side + S::kSideVs + 4) : 0.f;
+            vs[0][0] = ps.v[0];
+            vs[1][0] = ps.v[1];
             vmax = v_bound(vs[0][0], vs[1][0]);
         } else {
 #pragma unroll
@@ -935,8 +1007,6 @@ struct TileSource {
     //  cp.async (INT4, every lane): the lane's share of the 16-byte chunks of
     //    both tensors (rows past the end of K/V zero-filled) and the K and V
     //    scale of row `lane`, then one arrival once its copies have landed.
-    //  INT8 (every lane): lane 0 the boxes as for FP8; the first four lanes copy
-    //    the scales of the boxes' pages (a tile of one box: the same page twice).
     __device__ __forceinline__ void issue(int g, int kvh, int32_t ya, int32_t yb) const
     {
         const int s = g % NS;
@@ -946,17 +1016,7 @@ struct TileSource {
             copy_direct(dst, kvh, ya, yb);
             cp_async_mbar_arrive(bar);
         } else {
-            if constexpr (SL::kInt8) {
-                if (lane < SL::kScaleLanes) {
-                    const int32_t page = (SL::kBoxRows < kTile && (lane & 1) ? yb : ya) / p.page_size;
-                    const float *scales = lane < 2 ? p.k_scale : p.v_scale;
-                    cp_async_4(smem_addr(ring) + NS * SL::kBytes + s * SL::kSideBytes + 4 * lane, scales + (int64_t)page * p.scale_heads + kvh, 4);
-                    cp_async_mbar_arrive(bar);
-                }
-                if (lane != 0)
-                    return;
-            }
-            mbar_arrive_expect_tx(bar, 2 * SL::kTensorBytes);
+            mbar_arrive_expect_tx(bar, SL::kBytes);
             if constexpr (SL::kByte) {
                 const int32_t x = kvh * kHeadDim;
                 tma_load_2d(dst, tm_k, x, ya, bar, pol);
@@ -1189,9 +1249,9 @@ struct RowConsumer {
         for (int n = 0; n < 16; ++n)
             o_acc[n][0] = o_acc[n][1] = o_acc[n][2] = o_acc[n][3] = 0.f;
     }
-    __device__ __forceinline__ void tile(uint32_t st, uint32_t side, int n_valid, const uint32_t (&qa)[8][2], int lane)
+    __device__ __forceinline__ void tile(uint32_t st, const PageScales &ps, int n_valid, const uint32_t (&qa)[8][2], int lane)
     {
-        consume_tile<KV, DT>(st, side, n_valid, qa, qk, lane, m_run, l_part, o_acc, v_exp);
+        consume_tile<KV, DT>(st, ps, n_valid, qa, qk, lane, m_run, l_part, o_acc, v_exp);
     }
     // fp8_vscale: the head's V scale (FP8 K/V; ignored otherwise)
     template <int NC>
@@ -1249,7 +1309,7 @@ struct ColumnConsumer {
             o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
     }
 
-    __device__ __forceinline__ void tile(uint32_t st, uint32_t side, int n_valid, const uint32_t (&qa)[8][2], int lane)
+    __device__ __forceinline__ void tile(uint32_t st, const PageScales &ps, int n_valid, const uint32_t (&qa)[8][2], int lane)
     {
         using S = Stage<KV, DT>;
         const int g = lane >> 2, lr = lane & 7, lm = lane >> 3;
@@ -1315,15 +1375,15 @@ struct ColumnConsumer {
         float mt0 = -INFINITY, mt1 = -INFINITY, vmax = 0.f;
         float vs8[2] = {0.f, 0.f};   // INT8: the V scales of the tile's 16-key halves
         if constexpr (kInt8) {
-            vs8[0] = lds_f32(side + S::kSideVs);
-            vs8[1] = n_valid > 16 ? lds_f32(side + S::kSideVs + 4) : 0.f;
+            vs8[0] = ps.v[0];
+            vs8[1] = ps.v[1];
             vmax = v_bound(vs8[0], vs8[1]);
         }
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb) {
             float qk0 = qk[0], qk1 = qk[1];
             if constexpr (kInt8) {
-                const float ks = lds_f32(side + S::kSideKs + 4 * mb);
+                const float ks = ps.k[mb];
                 qk0 *= ks;
                 qk1 *= ks;
             }
@@ -1685,7 +1745,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, MIN_CTAS)
                     const __grid_constant__ SplitParams p)
 {
     using SG = Stage<KV, DT>;
-    using L = SingleLayout<G, NC, NS, SG::kBytes, SG::kSideBytes>;
+    using L = SingleLayout<G, NC, NS, SG::kBytes>;
     constexpr bool paged = KV != kKvRagged;
     constexpr bool warp_loop = paged || SG::kDirect;   // the whole producer warp runs the issue loop
     // Ragged FP8 and INT4: each consumer warp refills its own stages (see the
@@ -1817,7 +1877,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, MIN_CTAS)
             for (int i = 0; i < first; ++i) {
                 int32_t ya = 0, yb = 0;
                 src.tile_rows(i, ya, yb);
-                if (SG::kWarpIssue || lane == 0)
+                if (SG::kDirect || lane == 0)
                     src.issue(i, kvh, ya, yb);
             }
         }
@@ -1843,14 +1903,14 @@ __global__ void __launch_bounds__((NC + 1) * 32, MIN_CTAS)
                     } else if (misc[kAbort]) {
                         go = 0;
                     }
-                    if (go && !SG::kWarpIssue)
+                    if (go && !SG::kDirect)
                         src.issue(i, kvh, ya, yb);
                 }
                 if constexpr (warp_loop)
                     go = __shfl_sync(0xffffffffu, go, 0);
                 if (!go)
                     break;
-                if constexpr (SG::kWarpIssue)
+                if constexpr (SG::kDirect)
                     src.issue(i, kvh, ya, yb);
                 issued = i + 1;
             }
@@ -1902,13 +1962,15 @@ __global__ void __launch_bounds__((NC + 1) * 32, MIN_CTAS)
                     const int i = warp + NC * k;
                     cp_async_wait_group<D - 1>();
                     __syncwarp();   // every lane's copies of the tile have landed
-                    cs.tile(ring + (i % NS) * SG::kBytes, 0u, min(kTile, it.t1 - (it.t0 + i * kTile)), qa, lane);
+                    cs.tile(ring + (i % NS) * SG::kBytes, PageScales{}, min(kTile, it.t1 - (it.t0 + i * kTile)), qa, lane);
                     __syncwarp();   // every lane is done reading the stage
                     fill(k + D);
                 }
                 cp_async_wait_group<0>();
             } else {
                 const TileSource<NS, KV, DT> rsrc(p, &tm_k, &tm_v, smem, bars, lane);
+                PageScaleFeed<DT == kKvInt8, NC> feed(p);
+                feed.begin(it.base, it.t0, it.t1, kvh, warp);
                 int i = warp;
                 for (; i < n_tiles; i += NC) {
                     const int s = i % NS;
@@ -1918,7 +1980,7 @@ __global__ void __launch_bounds__((NC + 1) * 32, MIN_CTAS)
                             report(p.status, FD_ERR_TIMEOUT);
                         break;
                     }
-                    cs.tile(ring + s * SG::kBytes, ring + NS * SG::kBytes + s * SG::kSideBytes, min(kTile, it.t1 - (it.t0 + i * kTile)), qa, lane);
+                    cs.tile(ring + s * SG::kBytes, feed.take(), min(kTile, it.t1 - (it.t0 + i * kTile)), qa, lane);
                     __syncwarp();
                     if constexpr (self_refill) {
                         // FP8: lane 0 refills the stage it just freed with the
@@ -2017,7 +2079,7 @@ __global__ void __launch_bounds__((NC + 2) * 32, MIN_CTAS)
                                const __grid_constant__ SplitParams p)
 {
     using SG = Stage<KV, DT>;
-    using L = PersistentLayout<G, NC, NS, SG::kBytes, SG::kSideBytes>;
+    using L = PersistentLayout<G, NC, NS, SG::kBytes>;
     constexpr bool paged = KV != kKvRagged;
     constexpr bool warp_loop = paged || SG::kDirect;   // the whole producer warp runs the issue loop
     constexpr int kProducer = NC;   // the epilogue warp is NC + 1
@@ -2102,7 +2164,7 @@ __global__ void __launch_bounds__((NC + 2) * 32, MIN_CTAS)
                         } else if (misc[kAbort]) {
                             go = 0;
                         }
-                        if (go && !SG::kWarpIssue)
+                        if (go && !SG::kDirect)
                             src.issue(gt, kvh, ya, yb);
                     }
                     if constexpr (warp_loop)
@@ -2111,7 +2173,7 @@ __global__ void __launch_bounds__((NC + 2) * 32, MIN_CTAS)
                         stop = 1;
                         break;
                     }
-                    if constexpr (SG::kWarpIssue)
+                    if constexpr (SG::kDirect)
                         src.issue(gt, kvh, ya, yb);
                     ++gt;
                 }
@@ -2243,6 +2305,8 @@ __global__ void __launch_bounds__((NC + 2) * 32, MIN_CTAS)
             const int n_tiles = (it.t1 - it.t0 + kTile - 1) / kTile;
             // this warp's tiles of the item: stream tiles g = warp (mod NC)
             const int first = it.gt0 + ((warp - it.gt0 % NC) + NC) % NC;
+            PageScaleFeed<DT == kKvInt8, NC> feed(p);
+            feed.begin(it.base, it.t0, it.t1, it.kvh, first - it.gt0);
             for (int g = first; g < it.gt0 + n_tiles; g += NC) {
                 const int i = g - it.gt0;
                 const int s = g % NS;
@@ -2253,7 +2317,7 @@ __global__ void __launch_bounds__((NC + 2) * 32, MIN_CTAS)
                     ok = false;
                     break;
                 }
-                cs.tile(ring + s * SG::kBytes, ring + NS * SG::kBytes + s * SG::kSideBytes, min(kTile, it.t1 - (it.t0 + i * kTile)), qa, lane);
+                cs.tile(ring + s * SG::kBytes, feed.take(), min(kTile, it.t1 - (it.t0 + i * kTile)), qa, lane);
                 __syncwarp();
                 if (lane == 0)
                     mbar_arrive(smem_addr(&bars[NS + s]));
@@ -2467,8 +2531,8 @@ cudaError_t launch_g(const KvMaps &m, const SplitParams &p, int num_ctas, cudaSt
     constexpr int NS1 = DT == kKvBf16 ? kNS : 2 * NC1;
     constexpr int NS = DT == kKvBf16 ? kNS : 2 * NCP;
     using SG = Stage<KV, DT>;
-    using LS = SingleLayout<G, NC1, NS1, SG::kBytes, SG::kSideBytes>;
-    using LP = PersistentLayout<G, NCP, NS, SG::kBytes, SG::kSideBytes>;
+    using LS = SingleLayout<G, NC1, NS1, SG::kBytes>;
+    using LP = PersistentLayout<G, NCP, NS, SG::kBytes>;
     static_assert(kMinCtas * (LS::kAlloc + 1024) <= 233472 && kMinCtas * (LP::kAlloc + 1024) <= 233472,
                   "the resident CTAs must fit in shared memory");
     if (num_ctas >= p.num_work) {   // one wave: one item (or, device-side plan, at most one) per CTA
