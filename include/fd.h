@@ -665,6 +665,32 @@ int fd_append_paged_int4(int batch, int num_tokens, int num_qo_heads, int num_kv
                          void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
+ * fd_append_paged_int8 -- fd_append_paged into an INT8 cache (fd_decode_paged_int8),
+ * keeping each page's scales.  For a page that gets new keys and a KV head, with m
+ * the largest magnitude of the new keys' values (K's rotated, in fp32) and s0 the
+ * page's scale (0 where the page holds no key of the request from before):
+ *     scale = max(s0, m / 127, 2^-126),   code = round(value / scale)
+ * to nearest even, and where the scale grows the codes from before are carried over
+ * as round(code * (s0 / scale)).  So a page's first keys need no scale, whatever
+ * the page's entries held, and a key's value is off by at most half a step of its
+ * page's scale for each time it was rounded.  An infinity or NaN among the values makes
+ * the page's scale one, and its codes 0: the values of the page's head are then NaN.
+ * k_scale, v_scale [num_pages, Hs]: read and written.  Every page that gets new keys
+ * belongs to one request of the call (a shared, partly filled page is copied first, as
+ * fd_fork_pages lists it); num_tokens * (num_kv_heads + 2) is
+ * at most 2^31 - 1.
+ */
+int fd_append_paged_int8(int batch, int num_tokens, int num_qo_heads, int num_kv_heads,
+                         int head_dim, int page_size, int num_pages, const fd_rope_info *rope,
+                         const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                         const void *v, int64_t v_stride, const int32_t *append_indptr_dev,
+                         const int32_t *kv_page_indptr_dev, const int32_t *kv_last_page_len_dev,
+                         const int32_t *kv_page_indices_dev, int num_page_entries,
+                         const int32_t *positions_dev, void *q_out, int64_t q_out_stride,
+                         void *k_pages_int8, void *v_pages_int8, float *k_scale, float *v_scale,
+                         void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
  * Page tables on the device.  page_refs int32 [num_pages] counts how many
  * table entries (of these tables, or of others the program keeps, such as a
  * shared prefix's) hold each page; 0 is a free page.  fd_fork_pages and

@@ -22,7 +22,8 @@ Entry points (same names as the C ABI, minus the ``fd_`` prefix):
   plan_shared_paged(), decode_shared_paged()  (each prefix attended once), ragged and paged;
   decode_shared_fp8(), decode_shared_paged_fp8()  FP8 (E4M3) K/V
   plan_rope(...), append_paged(...)     rotary positions and the write of new keys and
-  append_paged_fp8(), append_paged_int4()  values into a paged cache
+  append_paged_fp8(), append_paged_int4(), values into a paged cache
+  append_paged_int8()
   fork_pages(...), compact_pages(...)   next page tables on the device, and the page
   copy_pages(...)                       copies they need
   get_device_status(workspace)          read and clear the kernels' error word
@@ -174,6 +175,7 @@ SIGNATURES = {
     "fd_append_paged": (_APPEND + [_P, _I64, _P], _I),
     "fd_append_paged_fp8": (_APPEND + [_P, _P, _P, _I64, _P], _I),
     "fd_append_paged_int4": (_APPEND + [_P, _P, _P, _I64, _P], _I),
+    "fd_append_paged_int8": (_APPEND + [_P, _P, _P, _I64, _P], _I),
     "fd_pages_workspace_bytes": ([_I, _I, ctypes.POINTER(ctypes.c_int64)], _I),
     "fd_fork_pages": ([_I, _I, _I, _I, _P, _P, _P, _P, _I, _P, _I, _P, _P, _P, _P, _P, _P, _I64, _P], _I),
     "fd_compact_pages": ([_I, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _I64, _P], _I),
@@ -728,6 +730,19 @@ def append_paged_int4(q, k, v, k_pages_int4, v_pages_int4, k_scale, v_scale, app
                    workspace, stream, (_need("k_scale", k_scale, f32, k.get_device()), _need("v_scale", v_scale, f32, k.get_device())))
 
 
+def append_paged_int8(q, k, v, k_pages_int8, v_pages_int8, k_scale, v_scale, append_indptr,
+                      kv_page_indptr, kv_last_page_len, kv_page_indices, *, rope=None, positions=None,
+                      q_out=None, workspace=None, stream=None):
+    """fd_append_paged_int8: append_paged into int8 pools
+    [num_pages, page_size, Hkv, D], with the scales fp32 [num_pages, scale_heads(Hkv)]
+    of the pages that get keys raised where these need it."""
+    _, _, ks, vs = _int8_cache("fd_append_paged_int8", k_pages_int8, v_pages_int8, k_scale, v_scale, k.shape[1],
+                               k.shape[2], k.get_device())
+    return _append("fd_append_paged_int8", (torch.int8,), 1, q, k, v, k_pages_int8, v_pages_int8,
+                   append_indptr, kv_page_indptr, kv_last_page_len, kv_page_indices, rope, positions, q_out,
+                   workspace, stream, (ks, vs))
+
+
 def pages_workspace_bytes(num_pages: int, new_batch: int = 0) -> int:
     """fd_pages_workspace_bytes: workspace of fork_pages (new_batch children) or
     compact_pages (new_batch 0)."""
@@ -810,7 +825,7 @@ def compact_pages(page_refs, kv_page_indices, max_moves: int, *, limit: int = 0,
 def copy_pages(pools, src, dst, *, workspace=None, stream=None):
     """fd_copy_pages: page src[i] -> dst[i] (int32 CUDA tensors; src < 0: none)
     of every pool in `pools`, contiguous CUDA tensors [num_pages, ...] (K and V
-    of all layers; an INT4 cache's scales [Hkv, num_pages * page_size] as
+    of all layers, an INT8 cache's scales; an INT4 cache's scales [Hkv, num_pages * page_size] as
     ``*scales.view(Hkv, num_pages, page_size)``)."""
     if not pools or src.numel() == 0:
         return
@@ -1015,7 +1030,7 @@ __all__ = [
     "plan_graph", "decode_graph", "merge_states", "get_device_status",
     "SharedPlan", "plan_shared", "plan_shared_paged", "decode_shared", "decode_shared_paged",
     "decode_shared_fp8", "decode_shared_paged_fp8",
-    "RopeInfo", "plan_rope", "append_paged", "append_paged_fp8", "append_paged_int4",
+    "RopeInfo", "plan_rope", "append_paged", "append_paged_fp8", "append_paged_int4", "append_paged_int8",
     "pages_workspace_bytes", "fork_pages", "compact_pages", "copy_pages", "workspace_bytes", "num_sms",
     "status_string",
     "TILE_TOKENS", "WORKSPACE_HEADER_BYTES", "DEFAULT_TIMEOUT_NS",

@@ -17,11 +17,13 @@ struct AppendParams {
     int64_t q_stride, k_stride, v_stride, q_out_stride;   // elements
     void *k_pages, *v_pages;
     const float *k_scale, *v_scale;   // FP8: [Hkv], read
-    float *k_scale_out, *v_scale_out; // INT4: [Hkv][num_pages * page_size], written
+    // written: INT4 [Hkv][num_pages * page_size]; INT8 [num_pages][scale_heads], read too
+    float *k_scale_out, *v_scale_out;
     const int32_t *append_indptr, *kv_page_indptr, *kv_last_page_len, *kv_page_indices, *positions;
     int *status;
     int32_t batch, num_tokens, num_qo_heads, num_kv_heads, page_size, num_pages, num_page_entries;
     int32_t tokens_per_cta;
+    int32_t scale_heads, page_ctas, blocks_per_page, warps_per_head;   // INT8
     fd_rope_info rope;           // rotary_dim 0: no rotation
 };
 

@@ -10,6 +10,7 @@
 #include "cache_kernels.h"
 #include "fd.h"
 #include "kernels.h"
+#include "stage1.h"
 
 using fd::aligned;
 using fd::as_stream;
@@ -164,8 +165,11 @@ int append(int batch, int num_tokens, int num_qo_heads, int num_kv_heads, int he
         return FD_ERR_INVALID_ARG;
     if (kv_type == fd::kKvTypeFp8 && (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4)))
         return FD_ERR_INVALID_ARG;
-    if (kv_type == fd::kKvTypeInt4 &&
+    if ((kv_type == fd::kKvTypeInt4 || kv_type == fd::kKvTypeInt8) &&
         (!k_scale_out || !v_scale_out || !aligned(k_scale_out, 4) || !aligned(v_scale_out, 4)))
+        return FD_ERR_INVALID_ARG;
+
+    if (kv_type == fd::kKvTypeInt8 && (int64_t)num_tokens * (num_kv_heads + 2) > INT32_MAX)   // its grid
         return FD_ERR_INVALID_ARG;
 
     fd::AppendParams p;
@@ -184,6 +188,7 @@ int append(int batch, int num_tokens, int num_qo_heads, int num_kv_heads, int he
     p.v_scale = v_scale;
     p.k_scale_out = k_scale_out;
     p.v_scale_out = v_scale_out;
+    p.scale_heads = fd::scale_heads(num_kv_heads);
     p.append_indptr = append_indptr_dev;
     p.kv_page_indptr = kv_page_indptr_dev;
     p.kv_last_page_len = kv_last_page_len_dev;
@@ -251,6 +256,23 @@ extern "C" int fd_append_paged_int4(int batch, int num_tokens, int num_qo_heads,
                   q_stride, k, k_stride, v, v_stride, append_indptr_dev, kv_page_indptr_dev,
                   kv_last_page_len_dev, kv_page_indices_dev, num_page_entries, positions_dev, q_out,
                   q_out_stride, k_pages_int4, v_pages_int4, nullptr, nullptr, k_scale, v_scale, fd::kKvTypeInt4,
+                  workspace, workspace_bytes, stream);
+}
+
+extern "C" int fd_append_paged_int8(int batch, int num_tokens, int num_qo_heads, int num_kv_heads, int head_dim,
+                                    int page_size, int num_pages, const fd_rope_info *rope, const void *q,
+                                    int64_t q_stride, const void *k, int64_t k_stride, const void *v,
+                                    int64_t v_stride, const int32_t *append_indptr_dev,
+                                    const int32_t *kv_page_indptr_dev, const int32_t *kv_last_page_len_dev,
+                                    const int32_t *kv_page_indices_dev, int num_page_entries,
+                                    const int32_t *positions_dev, void *q_out, int64_t q_out_stride,
+                                    void *k_pages_int8, void *v_pages_int8, float *k_scale, float *v_scale,
+                                    void *workspace, int64_t workspace_bytes, void *stream)
+{
+    return append(batch, num_tokens, num_qo_heads, num_kv_heads, head_dim, page_size, num_pages, rope, q,
+                  q_stride, k, k_stride, v, v_stride, append_indptr_dev, kv_page_indptr_dev,
+                  kv_last_page_len_dev, kv_page_indices_dev, num_page_entries, positions_dev, q_out,
+                  q_out_stride, k_pages_int8, v_pages_int8, nullptr, nullptr, k_scale, v_scale, fd::kKvTypeInt8,
                   workspace, workspace_bytes, stream);
 }
 

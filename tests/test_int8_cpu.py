@@ -5,6 +5,7 @@ import numpy as np
 import pytest
 
 import split_kv_flashdecoding_gb300 as fd
+from tests.test_cache_cpu import _append
 
 P = ctypes.c_void_p
 
@@ -42,3 +43,20 @@ def test_bindings_refuse_wrong_caches():
         fd.decode_paged_int8(q, pool, pool, scale, scale, [0, 1, 2], [3], z, z, z, 0.1)
     with pytest.raises(fd.FdError):   # not on a GPU
         fd.decode_paged_int8(q, pool, pool, scale, scale, [0, 1], [3], z, z, z, 0.1)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=-1), -1), (dict(n=-1), -1), (dict(hkv=0), -1), (dict(hq=-1), -1), (dict(entries=-1), -1),
+    (dict(d=64), -2), (dict(page=8), -2), (dict(pages=0), -1), (dict(pages=1 << 28), -1), (dict(ws=None), -3),
+    (dict(wsb=255), -3), (dict(q=None), -1), (dict(vp=None), -1), (dict(k=P(264)), -1), (dict(kp=P(264)), -1),
+    (dict(sk=None), -1), (dict(sv=P(258)), -1), (dict(n=1 << 28, hkv=8), -1), (dict(batch=0), 0), (dict(n=0), 0),
+], ids=str)
+def test_append_int8_refusals(kw, code):
+    assert _append("fd_append_paged_int8", **kw) == code
+
+
+def test_append_int8_refuses_queries_written_over_inputs():
+    base, pool = 1 << 20, P(1 << 30)
+    inputs = dict(n=5, hq=8, hkv=4, q=P(base), qs=2176, k=P(base + 2 * 1024), ks=2176, v=P(base + 2 * 1536), vs=2176)
+    for at in (8, 512, 1600):
+        assert _append("fd_append_paged_int8", **inputs, qo=P(base + 2 * at), qos=2176, kp=pool, vp=pool) == -1
