@@ -59,8 +59,9 @@
  * lay their tickets and partials out by batch and KV heads, so a workspace of theirs
  * serves calls of one batch and head count (with fd_append_paged* and
  * fd_copy_pages, which use the header alone); zero it again before another use.
- * fd_decode_shared* of any plans, fd_fork_pages, fd_compact_pages, fd_append_paged*
- * and fd_copy_pages may all share one that is large enough for each.
+ * fd_decode_shared* and fd_prefill_paged_int8 of any plans, fd_fork_pages,
+ * fd_compact_pages, fd_append_paged* and fd_copy_pages may all share one that is large
+ * enough for each.
  *
  * Launches: the kernels are launched with programmatic stream serialisation:
  * each may begin launching while the previous grid in the stream finishes,
@@ -550,6 +551,64 @@ int fd_decode_shared_paged_fp8(const fd_shared_plan *plan, int num_pages,
                            const void *k_pages_fp8, const void *v_pages_fp8, const float *k_scale,
                            const float *v_scale, float scale, float *o,
                            float *lse, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
+ * ---- Attention of many query tokens a request over an INT8 paged cache ----
+ *
+ * For prompts, chunks of a prompt behind cached keys, the check of several drafted
+ * tokens (causal), and for cross attention to an encoder's states of another length
+ * (all keys).  The cache is fd_decode_paged_int8's; for causal calls it holds the
+ * tokens' own keys (fd_append_paged_int8 before the call).
+ *
+ *     q          bf16 [num_tokens, Hq, D], heads contiguous, any token stride (elements,
+ *                a multiple of 8, at least Hq * D)
+ *     q_indptr   int32 [B+1]  request b's tokens are rows q_indptr[b] .. q_indptr[b+1]-1
+ *     the page tables of fd_decode_paged, L_b keys for request b
+ *     o          bf16 [num_tokens, Hq, D]; lse fp32 [num_tokens, Hq], or NULL
+ * Token t of T attends keys 0 .. L_b - T + t (causal), its own the last of them, or all
+ * L_b.  A token that sees no key (none there, or causal with T > L_b) gets O = 0,
+ * LSE = -inf.  Rows of q and o from q_indptr[B] on are not touched.
+ *
+ * Scores and sums are fp32; a softmax weight is rounded once, to f16 (2^-11 of it at
+ * most), O once, to bf16.  Scales as fd_append_paged_int8 leaves them, positive: one
+ * of NaN or +-inf makes what attends its page NaN; V scales less than 2^-40 of those
+ * near the split's first keys count as that.
+ *
+ * The plan is made once on the host for the tokens and tables and a call takes device
+ * data only, makes no host-synchronising call and may be captured in a CUDA graph; the
+ * tables on the device must hold what the plan was made for (tables beyond it set
+ * FD_ERR_DEVICE_BOUNDS, as a page outside the pool does; the outputs are then not
+ * valid).  Workspace: zeroed once, shared as fd_decode_shared's is.
+ */
+typedef struct fd_prefill_plan {
+    int32_t batch, num_tokens;
+    int32_t num_qo_heads, num_kv_heads, head_dim;
+    int32_t page_size;
+    int32_t causal;
+    int32_t chunk;             /* max keys per split, a multiple of 128 */
+    int32_t num_items;         /* CTAs */
+    int32_t num_partial_rows;  /* partial (O, LSE) rows of requests with several splits */
+    int32_t num_merged_rows;   /* rows that they are merged into */
+    int32_t num_page_entries;  /* kv_page_indptr[B] */
+    int64_t workspace_bytes;
+    int64_t timeout_ns;        /* as in fd_plan_info */
+} fd_prefill_plan;
+
+/*
+ * fd_plan_prefill_paged -- host only (no CUDA call unless num_sms == 0).  chunk: 0, or
+ * the most keys of a split (a multiple of 128, up to 262144).
+ */
+int fd_plan_prefill_paged(int batch, int num_qo_heads, int num_kv_heads, int head_dim, int page_size,
+                          const int32_t *q_indptr_host, const int32_t *kv_page_indptr_host,
+                          const int32_t *kv_last_page_len_host, int causal, int num_sms, int chunk,
+                          fd_prefill_plan *plan);
+
+int fd_prefill_paged_int8(const fd_prefill_plan *plan, int num_pages, const int32_t *q_indptr_dev,
+                          const int32_t *kv_page_indptr_dev, const int32_t *kv_last_page_len_dev,
+                          const int32_t *kv_page_indices_dev, const void *q, int64_t q_stride,
+                          const void *k_pages_int8, const void *v_pages_int8, const float *k_scale,
+                          const float *v_scale, float scale, void *o, float *lse, void *workspace,
+                          int64_t workspace_bytes, void *stream);
 
 /*
  * ---- Writing and rearranging a paged cache ----

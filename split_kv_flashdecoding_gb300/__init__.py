@@ -21,6 +21,8 @@ Entry points (same names as the C ABI, minus the ``fd_`` prefix):
   plan_shared(...), decode_shared(...)  decode over prefixes that requests share
   plan_shared_paged(), decode_shared_paged()  (each prefix attended once), ragged and paged;
   decode_shared_fp8(), decode_shared_paged_fp8()  FP8 (E4M3) K/V
+  plan_prefill_paged(...),              attention of one to many tokens a request over an
+  prefill_paged_int8(...)               INT8 cache: causal, or over all keys
   plan_rope(...), append_paged(...)     rotary positions and the write of new keys and
   append_paged_fp8(), append_paged_int4(), values into a paged cache
   append_paged_int8()
@@ -103,6 +105,14 @@ class SharedPlan(ctypes.Structure):
     ]
 
 
+class PrefillPlan(ctypes.Structure):
+    """Mirror of fd_prefill_plan (include/fd.h)."""
+    _fields_ = [(name, ctypes.c_int32) for name in (
+        "batch", "num_tokens", "num_qo_heads", "num_kv_heads", "head_dim", "page_size", "causal", "chunk",
+        "num_items", "num_partial_rows", "num_merged_rows", "num_page_entries")] + [
+        ("workspace_bytes", ctypes.c_int64), ("timeout_ns", ctypes.c_int64)]
+
+
 class RopeInfo(ctypes.Structure):
     """Mirror of fd_rope_info (include/fd.h)."""
     _fields_ = [
@@ -136,6 +146,7 @@ _lib = None
 _P, _I, _I64, _F = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_float
 _PI = ctypes.POINTER(PlanInfo)
 _PS = ctypes.POINTER(SharedPlan)
+_PP = ctypes.POINTER(PrefillPlan)
 _APPEND = [_I, _I, _I, _I, _I, _I, _I, _P, _P, _I64, _P, _I64, _P, _I64, _P, _P, _P, _P, _I, _P, _P,
            _I64, _P, _P]
 SIGNATURES = {
@@ -171,6 +182,8 @@ SIGNATURES = {
     "fd_decode_shared_fp8": ([_PS, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _F, _P, _P, _P, _I64, _P], _I),
     "fd_decode_shared_paged_fp8": ([_PS, _I, _P, _P, _P, _P, _P, _P, _P, _I, _P, _P, _P, _P, _P, _F, _P,
                                     _P, _P, _I64, _P], _I),
+    "fd_plan_prefill_paged": ([_I, _I, _I, _I, _I, _P, _P, _P, _I, _I, _I, _PP], _I),
+    "fd_prefill_paged_int8": ([_PP, _I, _P, _P, _P, _P, _P, _I64, _P, _P, _P, _P, _F, _P, _P, _P, _I64, _P], _I),
     "fd_plan_rope": ([_I, _I, ctypes.POINTER(RopeConfig), ctypes.POINTER(RopeInfo)], _I),
     "fd_append_paged": (_APPEND + [_P, _I64, _P], _I),
     "fd_append_paged_fp8": (_APPEND + [_P, _P, _P, _I64, _P], _I),
@@ -1018,6 +1031,57 @@ def decode_shared_paged_fp8(plan, q, k_pages_fp8, v_pages_fp8, k_scale, v_scale,
                                 scale, o, lse, workspace, stream)
 
 
+def plan_prefill_paged(batch: int, num_qo_heads: int, num_kv_heads: int, head_dim: int, page_size: int, q_indptr,
+                       kv_page_indptr, kv_last_page_len, *, causal: bool = True, num_sms: int = 0, chunk: int = 0,
+                       timeout_ns: int | None = None) -> PrefillPlan:
+    """fd_plan_prefill_paged: a plan for these query tokens and page tables (host
+    int32: q_indptr [B+1], kv_page_indptr [B+1], kv_last_page_len [B])."""
+    qi, ip, ll = _host_indptr(q_indptr), _host_indptr(kv_page_indptr), _host_indptr(kv_last_page_len)
+    if qi.size != batch + 1 or ip.size != batch + 1 or ll.size != batch:
+        raise FdError(-1, "indptrs must have batch+1 entries, last-page lengths batch")
+    plan_ = PrefillPlan()
+    _check(lib().fd_plan_prefill_paged(batch, num_qo_heads, num_kv_heads, head_dim, page_size, _host_ptr(qi),
+                                       _host_ptr(ip), _host_ptr(ll), int(bool(causal)), num_sms, chunk,
+                                       ctypes.byref(plan_)), "fd_plan_prefill_paged")
+    if timeout_ns is not None:
+        plan_.timeout_ns = timeout_ns
+    return plan_
+
+
+def prefill_paged_int8(plan, q, k_pages_int8, v_pages_int8, k_scale, v_scale, q_indptr, kv_page_indptr,
+                       kv_last_page_len, kv_page_indices, scale: float, *, o=None, lse=None, workspace=None,
+                       stream=None):
+    """fd_prefill_paged_int8: q [N,Hq,D] bf16 (any token stride, N at least the plan's
+    tokens) over an INT8 cache -> (O bf16 [N,Hq,D], LSE fp32 [N,Hq]); tables int32 CUDA
+    tensors."""
+    name, i32, f32, dev = "fd_prefill_paged_int8", torch.int32, torch.float32, q.get_device()
+    B, Hkv, D = plan.batch, plan.num_kv_heads, plan.head_dim
+    if q.dim() != 3 or q.shape[0] < plan.num_tokens or q.shape[1:] != (plan.num_qo_heads, D):
+        raise FdError(-1, f"{name}: q is not of the plan's tokens and heads")
+    if q_indptr.numel() != B + 1 or kv_page_indptr.numel() != B + 1 or kv_last_page_len.numel() < B or \
+            kv_page_indices.numel() < plan.num_page_entries:
+        raise FdError(-1, f"{name}: tables of another length than the plan's")
+    if k_pages_int8.dim() != 4 or k_pages_int8.shape[1] != plan.page_size:
+        raise FdError(-1, f"{name}: pools of another shape")
+    with _on(q, stream):
+        if o is None:
+            o = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+        if lse is None:
+            lse = torch.empty(q.shape[:2], dtype=f32, device=q.device)
+        if o.shape != q.shape or lse.shape != q.shape[:2]:
+            raise FdError(-1, f"{name}: o must have q's shape and lse [tokens, num_qo_heads]")
+        if workspace is None:
+            workspace = torch.zeros(plan.workspace_bytes, dtype=torch.uint8, device=q.device)
+        kp, vp, ks, vs = _int8_cache(name, k_pages_int8, v_pages_int8, k_scale, v_scale, Hkv, D, dev)
+        _check(lib().fd_prefill_paged_int8(
+            ctypes.byref(plan), k_pages_int8.shape[0], _need("q_indptr", q_indptr, i32, dev),
+            _need("kv_page_indptr", kv_page_indptr, i32, dev), _need("kv_last_page_len", kv_last_page_len, i32, dev),
+            _need("kv_page_indices", kv_page_indices, i32, dev), _ptr(q), _heads("q", q, dev), kp, vp, ks, vs,
+            float(scale), _need("o", o, torch.bfloat16, dev), _need("lse", lse, f32, dev), *_ws(workspace, dev),
+            _stream(stream)), name)
+    return o, lse
+
+
 def get_device_status(workspace, stream=None) -> int:
     """fd_get_device_status: synchronise, read and clear the kernels' status word."""
     return lib().fd_get_device_status(_ptr(workspace), _stream(stream))
@@ -1030,6 +1094,7 @@ __all__ = [
     "plan_graph", "decode_graph", "merge_states", "get_device_status",
     "SharedPlan", "plan_shared", "plan_shared_paged", "decode_shared", "decode_shared_paged",
     "decode_shared_fp8", "decode_shared_paged_fp8",
+    "PrefillPlan", "plan_prefill_paged", "prefill_paged_int8",
     "RopeInfo", "plan_rope", "append_paged", "append_paged_fp8", "append_paged_int4", "append_paged_int8",
     "pages_workspace_bytes", "fork_pages", "compact_pages", "copy_pages", "workspace_bytes", "num_sms",
     "status_string",

@@ -22,7 +22,7 @@ ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 CUDA_SOURCES = ["split_kernel.cu", "split_kernel_fp8.cu", "split_kernel_int4.cu", "split_kernel_int8.cu",
                 "merge_kernel.cu",
                 "fd_api.cu", "fd_static_ws.cu", "append_kernel.cu", "pages_kernel.cu", "fd_cache_api.cu",
-                "shared_kernel.cu", "fd_shared_api.cu"]
+                "shared_kernel.cu", "fd_shared_api.cu", "prefill_kernel.cu", "fd_prefill_api.cu"]
 HOST_SOURCES = ["plan.cpp"]
 
 

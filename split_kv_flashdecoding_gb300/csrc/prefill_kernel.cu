@@ -1,0 +1,915 @@
+// prefill_kernel.cu -- attention of one to many query tokens a request over an INT8
+// paged cache with a scale per page and KV head, on sm_103a: prompts, chunks of them
+// behind cached keys, checks of drafted tokens (causal), cross attention (all keys).
+//
+// Mathematics: the T * G queries of a request and KV head are the rows of one
+// matrix; with integer codes C and page scales k, v of a key's page,
+//     e_j = c k <q, C_K,j> + log2 v,  P_j = exp2(e_j - E),  O = (sum_j P_j C_V,j) / l,
+//     l = sum_j P_j / v,
+// c = scale log2 e and E near the row's largest e.  So both scales are numbers of a
+// 16-key group of a tile (pages are whole groups): the K scale goes into the factor
+// of the score, the V scale into the addend of the exponent, and the codes go into
+// the products as they are.  V scales count from one near the split's first ones
+// (v_ref), those more than 2^40 below it as 2^-40 of it.
+//
+// Every (request, block of 256 rows, split of the keys, KV head) is one CTA.  The
+// products run on tcgen05 in f16 with their accumulators in tensor memory: two
+// streams of S (P over it) and O, 256 columns each: two row tiles that share each K
+// and V tile, or, with up to 128 rows, alternate key tiles of one row tile.  A
+// weight enters the second product as one f16 value (2^-12 of it on the average;
+// the output is bf16), so a tile costs the two products of the definition.
+//
+// Four warps load the codes straight into registers, a tile ahead, and widen them
+// into operand tiles in shared memory.  (Raw tiles by TMA would pass through shared
+// memory twice more, and its bandwidth is what the products share with the
+// widening: per key tile of two row tiles they read 192 KB of operands, the
+// widening writes 64 KB, in 2048 cycles of the products.)
+//
+// Warps: 0-15 the softmax -- two warpgroups a stream, one a half of the tile's keys;
+// a thread owns a row and 64 of its scores.  16 issues the products of both streams
+// in turn, 17-20 load and widen.
+//
+// A row's reference E is the largest e of its tiles up to the last one (the first
+// tile: of itself), exchanged between the row's two warps by shared memory, and is
+// raised, with O rescaled, when that is over 2^kRaise above it: so no step waits for
+// its own maximum.  A score so far above all before it that its weight is over
+// f16's range is seen at the end, and the CTA then does its item again with the
+// maximum of every step before its weights.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "api_util.h"
+#include "device_common.cuh"
+#include "int8_widen.cuh"
+#include "prefill_kernels.h"
+#include "tc_stream.cuh"
+#include "tcgen05.cuh"
+
+namespace fd {
+namespace {
+
+constexpr int kTileRows = 128;                              // query rows of a tensor-core tile
+constexpr int kBufBytes = kPrefillTile * kHeadDim * 2;      // an f16 tile: 32 KB
+constexpr int kHalfBytes = kBufBytes / 2;
+constexpr int kBuffers = 7;                                 // Q tiles and the ring together
+constexpr int kMaxRing = kBuffers - 1;
+constexpr int kScaleSlots = 8;
+constexpr int kSoftmaxThreads = 512;
+constexpr int kStreamWarps = 8;
+constexpr int kMmaWarp = 16, kLoadWarp = 17, kLoadWarps = 4;
+constexpr int kThreads = 32 * (kLoadWarp + kLoadWarps);
+constexpr int kTmemCols = 512;
+constexpr int kStreamCols = 256;                            // S (and P over it) 128, O 128
+constexpr float kRaise = 3.f;                               // log2: what raises E
+constexpr float kBias = 1.f;                                // weights are 2^kBias larger: of small ones' bits
+constexpr int kOutStride = kHeadDim + 4;                    // floats between rows of the epilogue's staging
+constexpr int kGroups = kPrefillTile / 16;
+constexpr float kLeastV = -40.f, kMostV = 100.f;            // log2 of a V scale over v_ref
+
+struct PrefillSmem {
+    uint64_t full[kMaxRing], empty[kMaxRing];
+    uint64_t scales_ready[kScaleSlots];
+    uint64_t s_full[2], p_ready[2][2], o_done[2];
+    uint64_t q_ready, drain;
+    uint32_t tmem;
+    int abort, redo;
+    // the CTA's item
+    int ok, q0, tokens, len, base, kvh, row0, rows, key0, keys, splits, part_row, q_tiles;
+    float v_ref;
+    float2 scale[kScaleSlots][kGroups];   // a tile's groups: K scale, log2 (V scale / v_ref)
+    union {
+        float q_scale[kPrefillRows];                        // before the first step: a row's factor
+        __nv_bfloat16 row_max[2][2][2][kTileRows];          // [parity][stream][half]
+    };
+};
+struct PrefillEnd {   // at the end, behind the staged rows
+    float row_sum[2][2][kTileRows];
+    float row_ref[kTileRows];
+};
+constexpr int kEndOffset = kPrefillRows * kOutStride * 4;
+static_assert(kEndOffset + (int)sizeof(PrefillEnd) <= kBuffers * kBufBytes, "the epilogue works over the ring");
+constexpr int kPrefillAlloc = kBuffers * kBufBytes + (int)((sizeof(PrefillSmem) + 15) / 16 * 16);
+static_assert(kPrefillAlloc <= 232448, "shared memory of one CTA");
+
+__device__ __forceinline__ uint32_t pack_f16x2(float2 a)
+{
+    const __half2 h = __floats2half2_rn(a.x, a.y);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b)
+{
+    const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+struct RequestCoord {
+    int32_t q0, tokens;        // first token and their number
+    int32_t base, len;         // first page-list entry, keys
+    int32_t splits, blocks;
+    int32_t item0, row0, merge0;   // items, partial rows and merged rows of the requests before
+};
+
+// One request's numbers; one outside the tokens or the list has none of them (false).
+__device__ __forceinline__ bool size_request(const PrefillParams &p, int b, int32_t &q0, int32_t &tokens,
+                                             int32_t &base, int32_t &len, int32_t &splits, int32_t &blocks)
+{
+    q0 = __ldcg(p.q_indptr + b);
+    base = __ldcg(p.page_indptr + b);
+    tokens = len = splits = blocks = 0;
+    const int32_t q1 = __ldcg(p.q_indptr + b + 1), e1 = __ldcg(p.page_indptr + b + 1);
+    const int32_t last = __ldcg(p.last_len + b);
+    const int64_t keys = e1 == base ? 0 : (int64_t)(e1 - base - 1) * p.page_size + last;
+    if (q0 < 0 || q0 > q1 || q1 > p.num_tokens || base < 0 || base > e1 || e1 > p.page_entries ||
+        (e1 != base && (last < 1 || last > p.page_size)) || keys > INT32_MAX - kPrefillTile)
+        return false;
+    tokens = q1 - q0;
+    len = (int32_t)keys;
+    splits = prefill_splits(len, p.chunk);
+    blocks = (int32_t)(((int64_t)tokens * p.group + kPrefillRows - 1) / kPrefillRows);
+    return true;
+}
+
+// Whole warp: reports tables that need other items or rows than the plan has.
+__device__ __forceinline__ void check_tables(const PrefillParams &p)
+{
+    int64_t items = 0, rows = 0;
+    bool good = true;
+    for (int b = threadIdx.x & 31; b < p.batch; b += 32) {
+        int32_t q0, tokens, base, len, splits, blocks;
+        good &= size_request(p, b, q0, tokens, base, len, splits, blocks);
+        items += (int64_t)splits * blocks * p.num_kv_heads;
+        rows += splits > 1 ? (int64_t)splits * tokens * p.num_qo_heads : 0;
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        items += __shfl_xor_sync(0xffffffffu, items, o);
+        rows += __shfl_xor_sync(0xffffffffu, rows, o);
+    }
+    if (!good || items != p.num_items || rows != p.num_partial_rows)
+        report(p.status, FD_ERR_DEVICE_BOUNDS);
+}
+
+// Whole warp: the request that holds item `j` (or, by_row, merged row `j`).  False
+// when there is none or the tables are outside what the plan was made for.
+__device__ __forceinline__ bool locate_request(const PrefillParams &p, int32_t j, bool by_row, RequestCoord &out)
+{
+    const int lane = threadIdx.x & 31;
+    int32_t item_carry = 0, row_carry = 0, merge_carry = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += 32) {
+        const int b = b0 + lane;
+        int32_t q0 = 0, tokens = 0, base = 0, len = 0, splits = 0, blocks = 0;
+        if (b < p.batch)
+            size_request(p, b, q0, tokens, base, len, splits, blocks);
+        const int64_t items64 = (int64_t)splits * blocks * p.num_kv_heads;
+        const int64_t merge64 = splits > 1 ? (int64_t)tokens * p.num_qo_heads : 0;
+        const int64_t rows64 = merge64 * splits;
+        const bool fits = items64 <= p.num_items && rows64 <= p.num_partial_rows && merge64 <= p.merge_rows;
+        const int32_t items = fits ? (int32_t)items64 : 0, rows = fits ? (int32_t)rows64 : 0;
+        const int32_t merge = fits ? (int32_t)merge64 : 0;
+        int32_t item_incl = items, row_incl = rows, merge_incl = merge;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t t = __shfl_up_sync(0xffffffffu, item_incl, o);
+            const int32_t u = __shfl_up_sync(0xffffffffu, row_incl, o);
+            const int32_t w = __shfl_up_sync(0xffffffffu, merge_incl, o);
+            if (lane >= o) {
+                item_incl += t;
+                row_incl += u;
+                merge_incl += w;
+            }
+        }
+        item_incl += item_carry;
+        row_incl += row_carry;
+        merge_incl += merge_carry;
+        const bool hit = by_row ? j >= merge_incl - merge && j < merge_incl : j >= item_incl - items && j < item_incl;
+        const unsigned mask = __ballot_sync(0xffffffffu, hit);
+        if (mask) {
+            const int src = __ffs(mask) - 1;
+            out.q0 = __shfl_sync(0xffffffffu, q0, src);
+            out.tokens = __shfl_sync(0xffffffffu, tokens, src);
+            out.base = __shfl_sync(0xffffffffu, base, src);
+            out.len = __shfl_sync(0xffffffffu, len, src);
+            out.splits = __shfl_sync(0xffffffffu, splits, src);
+            out.blocks = __shfl_sync(0xffffffffu, blocks, src);
+            out.item0 = __shfl_sync(0xffffffffu, item_incl - items, src);
+            out.row0 = __shfl_sync(0xffffffffu, row_incl - rows, src);
+            out.merge0 = __shfl_sync(0xffffffffu, merge_incl - merge, src);
+            // by int32 sums that may have wrapped: in range all the same
+            const int64_t m = out.splits > 1 ? (int64_t)out.tokens * p.num_qo_heads : 0;
+            return out.item0 >= 0 && out.row0 >= 0 && out.merge0 >= 0 &&
+                   (int64_t)out.item0 + (int64_t)out.splits * out.blocks * p.num_kv_heads <= p.num_items &&
+                   (int64_t)out.row0 + m * out.splits <= p.num_partial_rows && out.merge0 + m <= p.merge_rows;
+        }
+        item_carry = __shfl_sync(0xffffffffu, item_incl, 31);
+        row_carry = __shfl_sync(0xffffffffu, row_incl, 31);
+        merge_carry = __shfl_sync(0xffffffffu, merge_incl, 31);
+    }
+    return false;
+}
+
+// Operand tiles: 128 rows x 128 f16 values, [64-value half][128 rows][128 bytes],
+// 128-byte swizzle.
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillParams p)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    PrefillSmem *sm = reinterpret_cast<PrefillSmem *>(smem + kBuffers * kBufBytes);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    // One thread: all barriers before their first phase.
+    auto init_barriers = [&](bool again) {
+        auto init = [&](uint64_t *bar, uint32_t count) {
+            if (again)
+                mbar_inval(smem_addr(bar));
+            mbar_init(smem_addr(bar), count);
+        };
+        for (int i = 0; i < kMaxRing; ++i) {
+            init(&sm->full[i], kLoadWarps);
+            init(&sm->empty[i], 1);
+        }
+        for (int i = 0; i < kScaleSlots; ++i)
+            init(&sm->scales_ready[i], 1);
+        for (int s = 0; s < 2; ++s) {
+            init(&sm->s_full[s], 1);
+            init(&sm->p_ready[s][0], kStreamWarps);
+            init(&sm->p_ready[s][1], kStreamWarps);
+            init(&sm->o_done[s], 1);
+        }
+        init(&sm->q_ready, kSoftmaxThreads / 32);
+        init(&sm->drain, 1);
+        fence_mbar_init();
+    };
+    if (warp == kMmaWarp)
+        tmem_alloc(smem_addr(&sm->tmem), kTmemCols);
+    griddep_wait();
+    if (warp == kLoadWarp) {
+        RequestCoord c;
+        const int w = blockIdx.x;
+        // operand tiles of a 1024-byte swizzle pattern: the base must be aligned
+        const bool found = locate_request(p, w, false, c) && (smem_addr(smem) & 1023) == 0;
+        if (lane == 0) {
+            sm->ok = found;
+            sm->q_tiles = 1;
+            sm->keys = 0;
+            if (found) {
+                // a request's last blocks first: with a causal mask they have the most keys
+                const int rest = w - c.item0, sb = rest / p.num_kv_heads;
+                const int split = sb % c.splits, block = c.blocks - 1 - sb / c.splits;
+                const int len = prefill_split_len(c.len, c.splits);
+                sm->kvh = rest % p.num_kv_heads;
+                sm->q0 = c.q0;
+                sm->tokens = c.tokens;
+                sm->len = c.len;
+                sm->base = c.base;
+                sm->row0 = block * kPrefillRows;
+                sm->rows = min(c.tokens * p.group - sm->row0, kPrefillRows);
+                sm->key0 = split * len;
+                const int last_token = (sm->row0 + sm->rows - 1) / p.group;
+                const int end = p.causal ? min(c.len, c.len - c.tokens + last_token + 1) : c.len;
+                sm->keys = max(0, min(end - sm->key0, len));
+                sm->splits = c.splits;
+                sm->part_row = c.row0 + split;
+                sm->q_tiles = sm->rows > kTileRows ? 2 : 1;
+            } else {
+                report(p.status, FD_ERR_DEVICE_BOUNDS);
+            }
+            init_barriers(false);
+            sm->abort = 0;
+            sm->redo = 0;
+            sm->v_ref = 1.f;
+        }
+    }
+    if (warp == kLoadWarp + 1 && blockIdx.x == 0)
+        check_tables(p);
+    tcgen05_fence_before();
+    __syncthreads();
+    tcgen05_fence_after();
+    const uint32_t tmem = sm->tmem;
+    const bool ok = sm->ok;
+    const int q_tiles = sm->q_tiles;
+    const bool two = q_tiles == 2;
+    const int nw = kBuffers - q_tiles;   // operand tiles of the ring
+    const int n = (sm->keys + kPrefillTile - 1) / kPrefillTile;
+    // local steps of stream s: every tile (two row tiles) or every other one
+    auto steps = [&](int s) { return two ? n : (n + 1 - s) / 2; };
+    const uint32_t q_smem = smem_addr(smem), ring = q_smem + q_tiles * kBufBytes;
+    uint8_t *ring_ptr = smem + q_tiles * kBufBytes;
+    // Position pos of the stream (see Place) holds K of tile t, or V of tile t.
+    auto at_pos = [&](int pos, bool &is_k) {
+        is_k = pos == 0 || ((pos & 1) && pos < 2 * n - 1);
+        return is_k ? (pos + 1) / 2 : pos == 2 * n - 1 ? n - 1 : (pos - 2) / 2;
+    };
+
+    // At most two passes over the item: the second with careful steps, when the
+    // first left f16's range.
+    float c2 = 0.f;   // softmax warps: what a score of codes is multiplied by
+    for (int pass = 0; pass < 2; ++pass) {
+        const bool careful = pass > 0;
+        if (warp == kMmaWarp && n > 0) {
+            // ------------------------------------------------------ the products
+            // A wait that gave up is reported; the products then work on what there
+            // is, so that no branch depends on it.
+            constexpr uint32_t id_s = mma_idesc(128, kPrefillTile, false, false);
+            constexpr uint32_t id_o = mma_idesc(128, kHeadDim, false, true);
+            const uint32_t leader = elect_one();
+            const int steps0 = steps(0), steps1 = steps(1);
+            const uint32_t q_lo = smem_desc_lo(q_smem, 16);
+            const uint32_t k_lo = smem_desc_lo(ring, 16);
+            const uint32_t v_lo = smem_desc_lo(ring, kHalfBytes);
+            constexpr uint32_t hi = smem_desc_hi(1024);
+            constexpr uint32_t kBuf16 = kBufBytes / 16;
+            Place k_at(0, nw), v_at(n > 1 ? 2 : 1, nw);
+            int k_tile = 0, v_tile = 0;
+            wait_phase(&sm->q_ready, 0, p, sm);
+            // S of stream s's next step: K of its tile; frees the buffer after the
+            // last stream that takes it.
+            auto scores = [&](int s) {
+                wait_phase(&sm->full[k_at.slot], k_at.phase, p, sm);
+                tcgen05_fence_after();
+                const uint32_t qa = q_lo + (two ? s : 0) * kBuf16, ka = k_lo + k_at.slot * kBuf16;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {   // 16 head dimensions a step
+                    const uint32_t off = ((k >> 2) * kHalfBytes + (k & 3) * 32) / 16;
+                    mma_ss(tmem + s * kStreamCols, qa + off, hi, ka + off, hi, id_s, k > 0, leader);
+                }
+                tcgen05_commit(smem_addr(&sm->s_full[s]), leader);
+                if (!two || s == 1) {
+                    tcgen05_commit(smem_addr(&sm->empty[k_at.slot]), leader);
+                    k_at.advance(k_tile == 0 ? 1 : 2);
+                    ++k_tile;
+                }
+            };
+            // O += P V of stream s's step i: each half of the keys is ready in two
+            // parts of 32.
+            auto values = [&](int s, int i, bool last) {
+                wait_phase(&sm->full[v_at.slot], v_at.phase, p, sm);
+                const uint32_t pa = tmem + s * kStreamCols, va = v_lo + v_at.slot * kBuf16;
+#pragma unroll
+                for (int part = 0; part < 2; ++part) {
+                    wait_phase(&sm->p_ready[s][part], i & 1, p, sm);
+                    tcgen05_fence_after();
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {   // 16 keys a step
+                        const int k = (j >> 1) * 4 + part * 2 + (j & 1);
+                        mma_ts(pa + 128, pa + 16 * k, va + k * 2 * 1024 / 16, hi, id_o, i > 0 || part > 0 || j > 0,
+                               leader);
+                    }
+                }
+                if (!two || s == 1) {
+                    tcgen05_commit(smem_addr(&sm->empty[v_at.slot]), leader);
+                    v_at.advance(v_tile == n - 2 ? 1 : 2);
+                    ++v_tile;
+                }
+                if (last)
+                    tcgen05_commit(smem_addr(&sm->o_done[s]), leader);
+            };
+            scores(0);
+            if (steps1 > 0)
+                scores(1);
+            for (int i = 0; i < steps0; ++i) {
+                values(0, i, i == steps0 - 1);
+                if (i + 1 < steps0)
+                    scores(0);
+                if (i < steps1)
+                    values(1, i, i == steps1 - 1);
+                if (i + 1 < steps1)
+                    scores(1);
+            }
+            // whatever the others saw, the products in flight end before tensor
+            // memory is freed
+            tcgen05_commit(smem_addr(&sm->drain), leader);
+            mbar_wait(smem_addr(&sm->drain), 0, kDrainTimeoutNs);
+            __syncwarp();
+        } else if (warp >= kLoadWarp && n > 0) {
+            // --------------------------------------- codes to f16 operand tiles
+            // A warp's unit of work is 8 rows of one half of the head, 16 values a
+            // lane: the lanes of a quarter warp are two rows r and r ^ 5 and four
+            // chunks of 16 bytes, whose 32 bytes of f16 meet no bank twice.  Unit j of a
+            // tile lies in its 16-key group j.  All of a warp's units of a tile are
+            // loaded a tile ahead of their widening.
+            const int me = warp - kLoadWarp;   // rows 8 (me / 2) of each group, half me % 2
+            const int r8 = (lane >> 3) ^ (((lane >> 2) & 1) * 5), cc = lane & 3;
+            const int row = (me >> 1) * 8 + r8;
+            const uint32_t lane_dst = (me >> 1) * 1024 + (me & 1) * kHalfBytes + r8 * 128 + (((2 * cc) ^ r8) << 4);
+            const int64_t row_bytes = (int64_t)p.num_kv_heads * kHeadDim;
+            const int lane_off = sm->kvh * kHeadDim + ((me & 1) * 4 + cc) * 16;
+            // The lane's group (lane % 8) of a tile: its page id two tiles ahead, its
+            // scale (warp 0: lanes 0-7 K's, 8-15 V's) one tile ahead.
+            const int key_g = sm->key0 + 16 * (lane & 7);
+            int pg = key_g / p.page_size, off = key_g % p.page_size, left = sm->keys - 16 * (lane & 7);
+            const int pages_on = kPrefillTile / p.page_size, rows_on = kPrefillTile % p.page_size;
+            struct Spot {
+                int id, off;   // page (-1: past the last key) and row in it
+            };
+            auto look_up = [&]() {
+                Spot x{left > 0 ? __ldcg(p.page_indices + sm->base + pg) : -1, left > 0 ? off : -1};
+                left -= kPrefillTile;
+                pg += pages_on;
+                off += rows_on;
+                if (off >= p.page_size) {
+                    off -= p.page_size;
+                    ++pg;
+                }
+                return x;
+            };
+            auto page_of = [&](const Spot &x) {   // page 0 for what is not there
+                if (x.off >= 0 && (x.id < 0 || x.id >= p.num_pages))
+                    report(p.status, FD_ERR_DEVICE_BOUNDS);
+                return x.off < 0 || x.id < 0 || x.id >= p.num_pages ? 0 : x.id;
+            };
+            auto scale_of = [&](const Spot &x) {
+                const float *from = lane < 8 ? p.k_scale : p.v_scale;
+                return me == 0 && lane < 16 ? __ldcg(from + (int64_t)page_of(x) * p.scale_heads + sm->kvh) : 1.f;
+            };
+            Spot here = look_up();                // of the next K tile
+            Spot ahead = look_up();
+            float scale = scale_of(here), ref_log = 0.f;
+            int row_k = 0, row_v = 0;             // pool rows of the lane's group: newest K tile, the one before
+            auto issue = [&](int pos, uint4 (&x)[kGroups]) {
+                bool is_k;
+                const int t = at_pos(pos, is_k);
+                if (is_k) {
+                    row_v = row_k;
+                    row_k = page_of(here) * p.page_size + max(here.off, 0);
+                }
+                const int8_t *from = (is_k ? p.k : p.v) + lane_off;
+                const int rows_of = is_k || t == n - 1 ? row_k : row_v;   // K of tile t + 1 has gone before V of t
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j)
+                    x[j] = __ldcg(reinterpret_cast<const uint4 *>(
+                        from + (int64_t)(__shfl_sync(0xffffffffu, rows_of, j) + row) * row_bytes));
+                if (!is_k)
+                    return;
+                if (me == 0) {   // the tile's scales
+                    if (t == 0) {
+                        float m = lane >= 8 && lane < 16 && left + 2 * kPrefillTile > 0 ? scale : 0.f;
+#pragma unroll
+                        for (int o = 1; o < 32; o <<= 1)
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        // pages of zeros have the smallest scale: no reference
+                        const float ref = m > 8.7e-19f && m < 1.2e18f ? m : 1.f;   // 2^-60, 2^60
+                        ref_log = log2f(ref);
+                        if (lane == 0)
+                            sm->v_ref = ref;
+                    }
+                    float lv = fminf(fmaxf(log2f(scale) - ref_log, kLeastV), kMostV);
+                    if (!(scale >= 0.f && scale < INFINITY))
+                        lv = __int_as_float(0x7fffffff);
+                    const float v = __shfl_sync(0xffffffffu, lv, (lane & 7) + 8);
+                    if (lane < 8)
+                        sm->scale[t % kScaleSlots][lane] = make_float2(scale, v);
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&sm->scales_ready[t % kScaleSlots]));
+                    scale = scale_of(ahead);
+                }
+                here = ahead;
+                ahead = look_up();
+            };
+            Place to(0, nw);
+            auto put = [&](int pos, uint4 (&x)[kGroups]) -> bool {
+                bool go = true;
+                if (pos >= nw)
+                    go = wait_phase(&sm->empty[to.slot], to.phase ^ 1, p, sm);
+                if (!__all_sync(0xffffffffu, go))
+                    return false;
+                uint8_t *dst0 = ring_ptr + to.slot * kBufBytes + lane_dst;
+                uint8_t *dst1 = ring_ptr + to.slot * kBufBytes + (lane_dst ^ 16);
+#pragma unroll
+                for (int j = 0; j < kGroups; ++j) {
+                    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                    uint32_t f[8];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        int8x4_to_f16x2x2<0, 1, 2, 3>(w[q], f[2 * q], f[2 * q + 1]);
+                    *reinterpret_cast<uint4 *>(dst0 + j * 2048) = make_uint4(f[0], f[1], f[2], f[3]);
+                    *reinterpret_cast<uint4 *>(dst1 + j * 2048) = make_uint4(f[4], f[5], f[6], f[7]);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&sm->full[to.slot]));
+                to.advance(1);
+                return true;
+            };
+            uint4 x0[kGroups], x1[kGroups];
+            issue(0, x0);
+#pragma unroll 1
+            for (int pos = 0; pos < 2 * n; pos += 2) {   // 2 n positions
+                issue(pos + 1, x1);
+                if (!put(pos, x0))
+                    break;
+                if (pos + 2 < 2 * n)
+                    issue(pos + 2, x0);
+                if (!put(pos + 1, x1))
+                    break;
+            }
+        } else if (warp < kMmaWarp) {
+            // -------------------------------------------------------- the softmax
+            const int s = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
+            const int trow = quad * 32 + lane;   // row of the stream's tile: lane of tensor memory
+            const uint32_t s_col = tmem + ((uint32_t)quad << 21) + s * kStreamCols + half * 64, o_col = s_col + 128;
+            const int pair_bar = 2 + s * 4 + quad;   // barrier of the two warps that share rows
+            if (ok && !careful) {
+                // Q rows as f16 into shared memory, a tile [half][128 rows][128 bytes]; a
+                // negative factor of the scores turns q around.  Each row times the
+                // power of two that puts its largest magnitude in [2^8, 2^9): exact down
+                // to 2^-22 of it.
+                const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+                for (int i = tid; i < q_tiles * kTileRows * 16; i += kSoftmaxThreads) {
+                    const int r = i >> 4, ch = i & 15;
+                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < sm->rows) {
+                        const int gr = sm->row0 + r;
+                        const uint16_t *from = p.q + (sm->q0 + gr / p.group) * p.q_stride +
+                                               (sm->kvh * p.group + gr % p.group) * kHeadDim;
+                        v = __ldcg(reinterpret_cast<const uint4 *>(from) + ch);
+                    }
+                    uint32_t w[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
+                    float amax = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 a = bf16x2_to_float2(w[j]);
+                        amax = fmaxf(amax, fmaxf(fabsf(a.x), fabsf(a.y)));
+                    }
+#pragma unroll
+                    for (int o = 1; o < 16; o <<= 1)
+                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+                    int sh = 0;
+                    if (amax > 0.f) {
+                        int e;
+                        frexpf(amax, &e);
+                        sh = min(max(9 - e, -100), 100);
+                    }
+                    const float up = __int_as_float((127 + sh) << 23);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 a = bf16x2_to_float2(w[j]);
+                        w[j] = pack_f16x2(make_float2(a.x * up, a.y * up));
+                    }
+                    if (ch == 0)
+                        sm->q_scale[r] = __int_as_float((127 - sh) << 23);
+                    const int rr = r & 127;
+                    *reinterpret_cast<uint4 *>(smem + (r >> 7) * kBufBytes + (ch >> 3) * kHalfBytes + rr * 128 +
+                                               (((ch & 7) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            __syncwarp();
+            if (lane == 0 && ok)
+                mbar_arrive(smem_addr(&sm->q_ready));
+            const int r_mine = (two ? s * kTileRows : 0) + trow;
+            if (!careful) {
+                barrier(1, kSoftmaxThreads);   // q_scale is written
+                c2 = fabsf(p.scale) * kLog2e * (ok ? sm->q_scale[r_mine] : 0.f);
+                barrier(1, kSoftmaxThreads);   // row_max takes its place
+            }
+            // keys of the item that the row sees
+            const int token = min((sm->row0 + r_mine) / p.group, sm->tokens - 1);
+            const int sees = ok && p.causal ? min(sm->keys, sm->len - sm->tokens + token + 1 - sm->key0) : sm->keys;
+            float ref = -INFINITY, l = 0.f;   // E, and the row's sum over this half of the keys
+            float m_own = -INFINITY;          // the largest e of this half
+            bool go = ok;
+            auto load = [&](uint32_t (&r)[16], int j16) { tmem_ld16(s_col + 16 * j16, r); };
+            auto ready = [&](uint32_t (&r)[16]) {
+                tmem_wait_ld();
+                settle(r);
+            };
+            auto publish = [&](int part) {
+                tmem_wait_st();
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(smem_addr(&sm->p_ready[s][part]));
+            };
+            for (int i = 0; i < steps(s); ++i) {
+                // After an error the steps go on without work, so that the barriers
+                // of a row's two warps always meet.
+                const int t = two ? i : 2 * i + s;
+                if (go)
+                    go = __all_sync(0xffffffffu,
+                                    wait_phase(&sm->s_full[s], i & 1, p, sm) &&
+                                        wait_phase(&sm->scales_ready[t % kScaleSlots], (t / kScaleSlots) & 1, p, sm));
+                const float2 *group = sm->scale[t % kScaleSlots] + half * 4;
+                const int valid = sees - t * kPrefillTile - half * 64;
+                uint32_t r0[16], r1[16];
+                tcgen05_fence_after();
+                if (go)
+                    load(r0, 0);
+                if (i == 0 || careful) {   // E from this tile's own scores
+                    if (go) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            if (c > 0)
+                                load(r0, c);
+                            ready(r0);
+                            float mt = -INFINITY;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                mt = fmaxf(mt, j < valid - 16 * c ? __uint_as_float(r0[j]) : -INFINITY);
+                            const float2 g = group[c];
+                            m_own = fmaxf(m_own, fmaf(mt, c2 * g.x, g.y));
+                        }
+                        load(r0, 0);
+                    }
+                    sm->row_max[(i + 1) & 1][s][half][trow] = __float2bfloat16_rn(m_own);
+                }
+                barrier(pair_bar, 64);
+                {
+                    // as bf16 on both sides: the two warps must agree
+                    const float both = fmaxf(__bfloat162float(sm->row_max[(i + 1) & 1][s][0][trow]),
+                                             __bfloat162float(sm->row_max[(i + 1) & 1][s][1][trow]));
+                    const bool up = both > ref + kRaise || (ref == -INFINITY && both > ref);
+                    if (__any_sync(0xffffffffu, up)) {
+                        const float f = !up ? 1.f : ref == -INFINITY ? 0.f : ex2(ref - both);
+                        ref = up ? both : ref;
+                        l *= f;
+                        if (i > 0 && go) {   // the products up to the last step are done: s_full followed them
+                            tmem_wait_ld();
+                            settle(r0);
+#pragma unroll 1
+                            for (int c = 0; c < 4; ++c) {
+                                uint32_t o[16];
+                                tmem_ld16(o_col + 16 * c, o);
+                                tmem_wait_ld();
+                                settle(o);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st16(o_col + 16 * c, o);
+                            }
+                        }
+                    }
+                }
+                if (!go)
+                    continue;
+                const float base = kBias - (ref == -INFINITY ? 0.f : ref);
+                float mx = -INFINITY;
+                // 16 scores to weights, over their columns
+                auto weights = [&](const uint32_t (&r)[16], int j16) {
+                    const float2 g = group[j16];
+                    const float c = c2 * g.x, off = g.y + base;
+                    const int v16 = valid - 16 * j16;
+                    float2 x[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        x[j] = fma2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])),
+                                    make_float2(c, c), make_float2(off, off));
+                    if (v16 < 16) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            x[j].x = 2 * j < v16 ? x[j].x : -INFINITY;
+                            x[j].y = 2 * j + 1 < v16 ? x[j].y : -INFINITY;
+                        }
+                    }
+                    uint32_t w[8];
+                    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        mx = fmaxf(mx, fmaxf(x[j].x, x[j].y));
+                        const float2 e = make_float2(ex2(x[j].x), ex2(x[j].y));
+                        sum = add2(sum, e);
+                        w[j] = pack_f16x2(e);
+                    }
+                    tmem_st8(s_col + 16 * j16, w);
+                    // (a group that the row does not see counts nothing, whatever its scale)
+                    const float part = sum.x + sum.y;
+                    l = part == 0.f ? l : fmaf(part, ex2(-g.y), l);
+                };
+                // the next 16 scores on their way meanwhile
+                ready(r0);
+                load(r1, 1);
+                weights(r0, 0);
+                ready(r1);
+                load(r0, 2);
+                weights(r1, 1);
+                publish(0);
+                ready(r0);
+                load(r1, 3);
+                weights(r0, 2);
+                ready(r1);
+                weights(r1, 3);
+                m_own = fmaxf(m_own, mx - base);
+                sm->row_max[i & 1][s][half][trow] = __float2bfloat16_rn(m_own);
+                publish(1);
+            }
+            // ------------------------------------------------------- the output
+            for (int x = 0; x < 2; ++x)   // both streams' products are done with the ring
+                if (go && steps(x) > 0)
+                    go = __all_sync(0xffffffffu, wait_phase(&sm->o_done[x], 0, p, sm));
+            tcgen05_fence_after();
+            if (go && !careful && steps(s) > 0) {   // a weight over f16's range
+                uint32_t o[16];
+                tmem_ld16(o_col, o);
+                tmem_wait_ld();
+                settle(o);
+                if (!(fabsf(__uint_as_float(o[0])) < INFINITY))
+                    sm->redo = 1;
+            }
+            barrier(1, kSoftmaxThreads);
+            if (careful || !sm->redo) {
+                float *stage = reinterpret_cast<float *>(smem);   // [q_tiles * 128][kOutStride]
+                PrefillEnd *end = reinterpret_cast<PrefillEnd *>(smem + kEndOffset);
+                float *mine = stage + r_mine * kOutStride + half * 64;
+                if (go)
+                    end->row_sum[s][half][trow] = l;
+                if (!two && s == 1) {
+                    // one row tile: stream 1 hands its state to stream 0
+                    if (go && half == 0)
+                        end->row_ref[trow] = ref;
+                    if (go && steps(1) > 0) {
+#pragma unroll 1
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t o[16];
+                            tmem_ld16(o_col + 16 * c, o);
+                            tmem_wait_ld();
+                            settle(o);
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4)
+                                *reinterpret_cast<uint4 *>(mine + 16 * c + j) =
+                                    make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
+                        }
+                    }
+                }
+                barrier(1, kSoftmaxThreads);
+                if (go && (two || s == 0)) {
+                    float f0 = 1.f, f1 = 0.f, m = ref, den = end->row_sum[s][0][trow] + end->row_sum[s][1][trow];
+                    const bool join = !two && steps(1) > 0;
+                    if (join) {
+                        const float m1 = end->row_ref[trow], l1 = end->row_sum[1][0][trow] + end->row_sum[1][1][trow];
+                        m = fmaxf(ref, m1);
+                        f0 = ref == -INFINITY ? 0.f : ex2(ref - m);
+                        f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+                        den = den * f0 + l1 * f1;
+                    }
+                    // a row that sees no key: O = 0, LSE = -inf
+                    const float inv = den == 0.f ? 0.f : sm->v_ref / den;
+                    f0 *= inv;
+                    f1 *= inv;
+#pragma unroll 1
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t o[16];
+                        if (n > 0) {
+                            tmem_ld16(o_col + 16 * c, o);
+                            tmem_wait_ld();
+                            settle(o);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 16; j += 4) {
+                            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                            float4 *d = reinterpret_cast<float4 *>(mine + 16 * c + j);
+                            if (inv != 0.f) {
+                                v = make_float4(__uint_as_float(o[j]) * f0, __uint_as_float(o[j + 1]) * f0,
+                                                __uint_as_float(o[j + 2]) * f0, __uint_as_float(o[j + 3]) * f0);
+                                if (join) {
+                                    const float4 w = *d;
+                                    v.x = fmaf(w.x, f1, v.x);
+                                    v.y = fmaf(w.y, f1, v.y);
+                                    v.z = fmaf(w.z, f1, v.z);
+                                    v.w = fmaf(w.w, f1, v.w);
+                                }
+                            }
+                            *d = v;
+                        }
+                    }
+                    if (half == 0 && r_mine < sm->rows) {
+                        const int gr = sm->row0 + r_mine;
+                        const int64_t at = (int64_t)(gr / p.group) * p.num_qo_heads + sm->kvh * p.group + gr % p.group;
+                        const float lse = den == 0.f ? -INFINITY : (m + log2f(den) - kBias) * kLn2;
+                        if (sm->splits > 1)
+                            p.partial_lse[sm->part_row + at * sm->splits] = lse;
+                        else if (p.lse)
+                            p.lse[(int64_t)sm->q0 * p.num_qo_heads + at] = lse;
+                    }
+                }
+                barrier(1, kSoftmaxThreads);
+                if (go) {   // whole rows, a warp at a time
+                    for (int r = warp; r < sm->rows; r += kSoftmaxThreads / 32) {
+                        const int gr = sm->row0 + r;
+                        const int64_t at = (int64_t)(gr / p.group) * p.num_qo_heads + sm->kvh * p.group + gr % p.group;
+                        const float4 v = *reinterpret_cast<const float4 *>(stage + r * kOutStride + 4 * lane);
+                        if (sm->splits > 1) {
+                            float *dst = p.partial_o + (sm->part_row + at * sm->splits) * kHeadDim;
+                            reinterpret_cast<float4 *>(dst)[lane] = v;
+                        } else {
+                            uint16_t *dst = p.o + ((int64_t)sm->q0 * p.num_qo_heads + at) * kHeadDim;
+                            reinterpret_cast<uint2 *>(dst)[lane] =
+                                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+                        }
+                    }
+                }
+            }
+        }
+        tcgen05_fence_before();
+        __syncthreads();
+        if (careful || !sm->redo || sm->abort)
+            break;
+        if (warp == kLoadWarp && lane == 0)
+            init_barriers(true);   // every phase of the first pass has completed
+        __syncthreads();
+        tcgen05_fence_after();
+    }
+    griddep_launch_dependents();
+    if (warp == kMmaWarp) {
+        tcgen05_fence_after();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+// Stage 2, a warp a row: the merge by LSE of the partials of the requests with
+// several splits, lane = 4 output columns, kMergeBatch partials of loads in flight.
+constexpr int kMergeWarps = 4;
+constexpr int kMergeBatch = 8;
+
+__global__ void __launch_bounds__(kMergeWarps * 32) prefill_merge_kernel(const __grid_constant__ PrefillParams p)
+{
+    const int lane = threadIdx.x & 31;
+    const int row = blockIdx.x * kMergeWarps + (threadIdx.x >> 5);
+    griddep_wait();
+    griddep_launch_dependents();
+    if (row >= p.merge_rows)
+        return;
+    RequestCoord c;
+    if (!locate_request(p, row, true, c)) {
+        if (lane == 0)
+            report(p.status, FD_ERR_DEVICE_BOUNDS);
+        return;
+    }
+    const int64_t first = c.row0 + (int64_t)(row - c.merge0) * c.splits;
+    const int64_t out = (int64_t)c.q0 * p.num_qo_heads + (row - c.merge0);
+    const float *lse_in = p.partial_lse + first;
+    const float4 *o_in = reinterpret_cast<const float4 *>(p.partial_o + first * kHeadDim) + lane;
+    float m = -INFINITY, den = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = 0; i0 < c.splits; i0 += kMergeBatch) {
+        float l[kMergeBatch];
+        float4 v[kMergeBatch];
+#pragma unroll
+        for (int u = 0; u < kMergeBatch; ++u) {
+            l[u] = -INFINITY;
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (i0 + u < c.splits) {
+                l[u] = __ldcg(lse_in + i0 + u);
+                v[u] = __ldcg(o_in + (int64_t)(i0 + u) * (kHeadDim / 4));
+            }
+        }
+        float m_new = m;
+        bool nan = false;
+#pragma unroll
+        for (int u = 0; u < kMergeBatch; ++u) {
+            m_new = fmaxf(m_new, l[u]);
+            nan |= l[u] != l[u];
+        }
+        if (m_new == -INFINITY && !nan)
+            continue;
+        const float f = expf(m - m_new);
+        den *= f;
+        acc.x *= f;
+        acc.y *= f;
+        acc.z *= f;
+        acc.w *= f;
+#pragma unroll
+        for (int u = 0; u < kMergeBatch; ++u) {
+            const float w = expf(l[u] - m_new);
+            if (w == 0.f)   // a split without a key that the row sees
+                continue;
+            den += w;
+            acc.x = fmaf(w, v[u].x, acc.x);
+            acc.y = fmaf(w, v[u].y, acc.y);
+            acc.z = fmaf(w, v[u].z, acc.z);
+            acc.w = fmaf(w, v[u].w, acc.w);
+        }
+        m = m_new;
+    }
+    const float inv = den == 0.f ? 0.f : 1.f / den;
+    reinterpret_cast<uint2 *>(p.o + out * kHeadDim)[lane] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (lane == 0 && p.lse)
+        p.lse[out] = den == 0.f ? -INFINITY : m + logf(den);
+}
+
+}  // namespace
+
+cudaError_t launch_prefill(const PrefillParams &p, cudaStream_t stream)
+{
+    static bool configured[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess)
+        return e;
+    if (dev >= 64 || !configured[dev]) {
+        e = cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kPrefillAlloc);
+        if (e != cudaSuccess)
+            return e;
+        if (dev < 64)
+            configured[dev] = true;
+    }
+    e = launch_dependent(prefill_kernel, dim3((unsigned)p.num_items), kThreads, kPrefillAlloc, stream, p);
+    if (e != cudaSuccess || p.merge_rows == 0)
+        return e;
+    return launch_dependent(prefill_merge_kernel, dim3((unsigned)((p.merge_rows + kMergeWarps - 1) / kMergeWarps)),
+                            kMergeWarps * 32, 0, stream, p);
+}
+
+}  // namespace fd

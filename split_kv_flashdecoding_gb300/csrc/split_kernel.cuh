@@ -54,6 +54,7 @@
 #include <cuda_runtime.h>
 
 #include "device_common.cuh"
+#include "int8_widen.cuh"
 #include "kernels.h"
 
 namespace fd {
@@ -400,21 +401,6 @@ __device__ __forceinline__ void int4x8_to_f16x2x4(uint32_t x, uint32_t (&r)[4])
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[1]) : "r"(t1), "r"(kSixteenth), "r"(kMinus72));
     asm("sub.f16x2 %0, %1, %2;" : "=r"(r[2]) : "r"(t2), "r"(k1032));
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r[3]) : "r"(t3), "r"(kSixteenth), "r"(kMinus72));
-}
-
-// Two's-complement bytes of x -> f16x2: lo = bytes A and B, hi = bytes C and D
-// (the first of each in the low half).  A byte with its
-// sign bit flipped is u = n + 128; under the exponent byte of 1024 it is the f16
-// 1024 + u, and subtracting 1152 leaves n, exactly.
-template <int A, int B, int C, int D>
-__device__ __forceinline__ void int8x4_to_f16x2x2(uint32_t x, uint32_t &lo, uint32_t &hi)
-{
-    const uint32_t u = x ^ 0x80808080u;
-    constexpr uint32_t k1024 = 0x64646464u, k1152 = 0x64806480u;
-    lo = __byte_perm(u, k1024, 0x4040u | A | (B << 8));
-    hi = __byte_perm(u, k1024, 0x4040u | C | (D << 8));
-    asm("sub.f16x2 %0, %0, %1;" : "+r"(lo) : "r"(k1152));
-    asm("sub.f16x2 %0, %0, %1;" : "+r"(hi) : "r"(k1152));
 }
 
 // A word of a key row, four bytes in order, to f16 (bytes 0, 1 and 2, 3); and a

@@ -60,3 +60,70 @@ def test_append_int8_refuses_queries_written_over_inputs():
     inputs = dict(n=5, hq=8, hkv=4, q=P(base), qs=2176, k=P(base + 2 * 1024), ks=2176, v=P(base + 2 * 1536), vs=2176)
     for at in (8, 512, 1600):
         assert _append("fd_append_paged_int8", **inputs, qo=P(base + 2 * at), qos=2176, kp=pool, vp=pool) == -1
+
+
+def _plan_prefill(**kw):
+    a = dict(batch=2, hq=8, hkv=4, d=128, page=16, qi=[0, 5, 7], ip=[0, 2, 3], last=[3, 16], causal=1, sms=152, chunk=0)
+    a.update(kw)
+    for x in ("qi", "ip", "last"):
+        a[x] = None if a[x] is None else np.array(a[x], dtype=np.int32).ctypes.data_as(P)
+    plan = fd.PrefillPlan()
+    return fd.lib().fd_plan_prefill_paged(*a.values(), ctypes.byref(plan)), plan
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(batch=-1), -1), (dict(hq=0), -1), (dict(hkv=0), -1), (dict(hkv=3), -1), (dict(hq=12), -2), (dict(hq=64), -2),
+    (dict(d=64), -2), (dict(page=8), -2), (dict(page=0), -2), (dict(qi=None), -1), (dict(ip=None), -1),
+    (dict(last=None), -1), (dict(qi=[1, 5, 7]), -1), (dict(qi=[0, 5, 4]), -1), (dict(ip=[0, 3, 2]), -1),
+    (dict(last=[0, 16]), -1), (dict(last=[3, 17]), -1), (dict(chunk=64), -1), (dict(chunk=-128), -1),
+    (dict(chunk=1 << 19), -1), (dict(sms=-1), -1), (dict(qi=[0, 5, 2 ** 31 - 1]), -1), (dict(), 0),
+    (dict(qi=[0, 0, 0]), 0), (dict(ip=[0, 0, 0], last=[0, 0]), 0),
+], ids=str)
+def test_plan_prefill_refusals(kw, code):
+    assert _plan_prefill(**kw)[0] == code
+
+
+def test_plan_prefill_counts():
+    rc, p = _plan_prefill(hq=32, hkv=8, qi=[0, 100, 101], ip=[0, 63, 64], last=[16, 1], chunk=256)
+    # 400 rows a KV head: 2 blocks, 1008 keys: 4 splits; 4 rows: 1 block, 1 split
+    assert rc == 0 and p.num_items == 2 * 4 * 8 + 8 and p.num_merged_rows == 100 * 32 and p.num_partial_rows == 100 * 32 * 4
+    assert p.workspace_bytes >= 256 + p.num_partial_rows * 129 * 4
+    assert _plan_prefill(qi=[0, 0, 0])[1].num_items == 0
+    # few rows behind many keys are split over the SMs, many rows are not
+    assert _plan_prefill(batch=1, hq=32, hkv=8, qi=[0, 4], ip=[0, 4096], last=[16])[1].num_items >= 140
+    assert _plan_prefill(batch=1, hq=32, hkv=8, qi=[0, 40000], ip=[0, 2500], last=[16])[1].num_merged_rows == 0
+
+
+def _prefill(plan=None, **kw):
+    plan = plan or _plan_prefill()[1]
+    a = dict(pages=4, qi=P(256), ip=P(256), last=P(256), ids=P(256), q=P(256), qs=1024,
+             k=P(256), v=P(256), ks=P(256), vs=P(256), scale=0.1, o=P(256), lse=P(256), ws=P(256), wsb=1 << 30)
+    a.update(kw)
+    return fd.lib().fd_prefill_paged_int8(ctypes.byref(plan), *a.values(), None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(pages=0), -1), (dict(pages=1 << 28), -1), (dict(qi=None), -1), (dict(ip=None), -1),
+    (dict(last=None), -1), (dict(ids=None), -1), (dict(q=None), -1), (dict(q=P(264)), -1), (dict(qs=1016), -1),
+    (dict(qs=1028), -1), (dict(k=None), -1), (dict(v=P(264)), -1), (dict(ks=None), -1), (dict(vs=P(258)), -1),
+    (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1), (dict(o=None), -1), (dict(o=P(264)), -1),
+    (dict(lse=P(258)), -1), (dict(ws=None), -3), (dict(wsb=1000), -3), (dict(ws=P(264)), -1),
+], ids=str)
+def test_prefill_refusals(kw, code):
+    assert _prefill(**kw) == code
+
+
+@pytest.mark.parametrize("field,value,code", [
+    ("num_items", -1, -1), ("num_partial_rows", 1 << 20, -1), ("num_merged_rows", 1 << 20, -1), ("chunk", 100, -1),
+    ("head_dim", 64, -2), ("page_size", 8, -2), ("num_kv_heads", 3, -1), ("num_qo_heads", 12, -2), ("workspace_bytes", 0, -1),
+    ("num_tokens", -1, -1), ("num_page_entries", -1, -1),
+])
+def test_prefill_refuses_plans_that_do_not_hold_together(field, value, code):
+    plan = _plan_prefill()[1]
+    setattr(plan, field, value)
+    assert _prefill(plan) == code
+
+
+def test_prefill_of_nothing_is_nothing():
+    assert fd.lib().fd_prefill_paged_int8(None, *[0] * 1, *[None] * 5, 0, *[None] * 4, 0.1, *[None] * 3, 0, None) == -1
+    assert _prefill(_plan_prefill(qi=[0, 0, 0])[1], q=None, o=None) == 0
