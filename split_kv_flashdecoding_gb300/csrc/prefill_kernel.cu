@@ -25,10 +25,13 @@
 // a thread owns a row and 64 of its scores.  16-19 load and widen, 20 issues the
 // products of both streams in turn, 21 looks up the tiles' scales.
 //
-// A row's reference E is the largest e of its tiles up to the last one (the first
-// tile: of itself), exchanged between the row's two warps by shared memory, and is
-// raised, with O rescaled, when that is over 2^kRaise above it: so no step waits for
-// its own maximum.  A score so far above all before it that its weight is over
+// A row's reference E comes from the tiles up to the last one (the first tile's from
+// its own largest e): of each half of a tile the log of its sum of weights, which
+// costs no comparisons; it is up to log2 64 above the largest e, but then the row's sum
+// is that much larger, too, and what f16 loses of small weights is as little of it.  It
+// is exchanged between the row's two warps by shared memory, and E is raised, with O
+// rescaled, when that is over 2^kRaise above it: so no step waits for its own
+// maximum.  A score so far above all before it that its weight is over
 // f16's range is seen at the end, and the CTA then does its item again with the
 // maximum of every step before its weights.
 #include <type_traits>
@@ -60,7 +63,7 @@ constexpr int kLoadWarp = 16, kLoadWarps = 4, kMmaWarp = 20, kScaleWarp = 21;   
 constexpr int kThreads = 768;
 // Registers a thread: at the launch, and after the warpgroups have shared them out,
 // four of the softmax, the loads, the products.
-constexpr int kRegs = 80, kSoftmaxRegs = 88, kLoadRegs = 80, kMmaRegs = 40;
+constexpr int kRegs = 80, kSoftmaxRegs = 96, kLoadRegs = 56, kMmaRegs = 40;
 static_assert(4 * kSoftmaxRegs + kLoadRegs + kMmaRegs <= kThreads / 128 * kRegs, "no more than the launch has");
 static_assert(kThreads * kRegs <= 65536, "registers of an SM");
 constexpr int kTmemCols = 512;
@@ -74,14 +77,14 @@ constexpr float kLeastV = -40.f, kMostV = 100.f;            // log2 of a V scale
 struct PrefillSmem {
     uint64_t full[kMaxRing], empty[kMaxRing];
     uint64_t scales_ready[kScaleSlots], scales_free[kScaleSlots];
-    uint64_t s_full[2], p_ready[2][2], o_done[2];
+    uint64_t s_full[2], p_ready[2], o_done[2];
     uint64_t q_ready, drain;
     uint32_t tmem;
     int abort, redo;
     // the CTA's item
     int ok, q0, tokens, len, base, kvh, row0, rows, key0, keys, splits, part_row, q_tiles;
     float v_ref;
-    float2 scale[kScaleSlots][kGroups];   // a tile's groups: K scale, log2 (V scale / v_ref)
+    float4 scale[kScaleSlots][kGroups];   // a tile's groups: K scale, log2 (V scale / v_ref), v_ref / V scale
     union {
         float q_scale[kPrefillRows];                        // before the first step: a row's factor
         __nv_bfloat16 row_max[2][2][2][kTileRows];          // [parity][stream][half]
@@ -277,8 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
         for (int s = 0; s < 2; ++s) {
             init(&sm->s_full[s], 1);
-            init(&sm->p_ready[s][0], kStreamWarps);
-            init(&sm->p_ready[s][1], kStreamWarps);
+            init(&sm->p_ready[s], kStreamWarps);
             init(&sm->o_done[s], 1);
         }
         init(&sm->q_ready, kSoftmaxThreads / 32);
@@ -394,8 +396,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         !__all_sync(0xffffffffu, wait_phase(&sm->scales_free[t % kScaleSlots],
                                                             (t / kScaleSlots - 1) & 1, p, sm)))
                         break;
+                    // (v no number: what sees the group is NaN by its weights; what does not
+                    // see it adds 0 times a number)
                     if (lane < 8)
-                        sm->scale[t % kScaleSlots][lane] = make_float2(scale, v);
+                        sm->scale[t % kScaleSlots][lane] = make_float4(scale, v, v == v ? exp2f(-v) : 1.f, 0.f);
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(smem_addr(&sm->scales_ready[t % kScaleSlots]));
@@ -438,22 +442,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     ++k_tile;
                 }
             };
-            // O += P V of stream s's step i: each half of the keys is ready in two
-            // parts of 32.
+            // O += P V of stream s's step i.  (Published in two parts, for the products
+            // to start on the first, the weights cost a prompt 2 % more.)
             auto values = [&](int s, int i, bool last) {
                 wait_phase(&sm->full[v_at.slot], v_at.phase, p, sm);
+                wait_phase(&sm->p_ready[s], i & 1, p, sm);
+                tcgen05_fence_after();
                 const uint32_t pa = tmem + s * kStreamCols, va = v_lo + v_at.slot * kBuf16;
 #pragma unroll
-                for (int part = 0; part < 2; ++part) {
-                    wait_phase(&sm->p_ready[s][part], i & 1, p, sm);
-                    tcgen05_fence_after();
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {   // 16 keys a step
-                        const int k = (j >> 1) * 4 + part * 2 + (j & 1);
-                        mma_ts(pa + 128, pa + 16 * k, va + k * 2 * 1024 / 16, hi, id_o, i > 0 || part > 0 || j > 0,
-                               leader);
-                    }
-                }
+                for (int k = 0; k < 8; ++k)   // 16 keys a step
+                    mma_ts(pa + 128, pa + 16 * k, va + k * 2 * 1024 / 16, hi, id_o, i > 0 || k > 0, leader);
                 if (!two || s == 1) {
                     tcgen05_commit(smem_addr(&sm->empty[v_at.slot]), leader);
                     v_at.advance(v_tile == n - 2 ? 1 : 2);
@@ -481,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             __syncwarp();
         } while (another_pass(pass++));
     } else if (warp >= kLoadWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
         int pass = 0;
         do {
             if (n == 0)
@@ -534,21 +533,25 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     go = wait_phase(&sm->empty[to.slot], to.phase ^ 1, p, sm);
                 if (!__all_sync(0xffffffffu, go))
                     break;
-                uint4 x[kGroups];
-#pragma unroll
-                for (int j = 0; j < kGroups; ++j)
-                    x[j] = *reinterpret_cast<const uint4 *>(raw_ptr + (pos % kRawTiles) * kRawBytes + j * 512);
+                const uint8_t *src = raw_ptr + (pos % kRawTiles) * kRawBytes;
                 uint8_t *dst0 = ring_ptr + to.slot * kBufBytes + lane_dst;
                 uint8_t *dst1 = ring_ptr + to.slot * kBufBytes + (lane_dst ^ 16);
 #pragma unroll
-                for (int j = 0; j < kGroups; ++j) {
-                    const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                    uint32_t f[8];
+                for (int h = 0; h < kGroups; h += 4) {
+                    uint4 x[4];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        int8x4_to_f16x2x2<0, 1, 2, 3>(w[q], f[2 * q], f[2 * q + 1]);
-                    *reinterpret_cast<uint4 *>(dst0 + j * 2048) = make_uint4(f[0], f[1], f[2], f[3]);
-                    *reinterpret_cast<uint4 *>(dst1 + j * 2048) = make_uint4(f[4], f[5], f[6], f[7]);
+                    for (int j = 0; j < 4; ++j)
+                        x[j] = *reinterpret_cast<const uint4 *>(src + (h + j) * 512);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                        uint32_t f[8];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            int8x4_to_f16x2x2<0, 1, 2, 3>(w[q], f[2 * q], f[2 * q + 1]);
+                        *reinterpret_cast<uint4 *>(dst0 + (h + j) * 2048) = make_uint4(f[0], f[1], f[2], f[3]);
+                        *reinterpret_cast<uint4 *>(dst1 + (h + j) * 2048) = make_uint4(f[4], f[5], f[6], f[7]);
+                    }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
@@ -638,13 +641,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 tmem_wait_ld();
                 settle(r);
             };
-            auto publish = [&](int part) {
-                tmem_wait_st();
-                tcgen05_fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&sm->p_ready[s][part]));
-            };
             for (int i = 0; i < steps(s); ++i) {
                 // After an error the steps go on without work, so that the barriers
                 // of a row's two warps always meet.
@@ -653,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     go = __all_sync(0xffffffffu,
                                     wait_phase(&sm->s_full[s], i & 1, p, sm) &&
                                         wait_phase(&sm->scales_ready[t % kScaleSlots], (t / kScaleSlots) & 1, p, sm));
-                const float2 *group = sm->scale[t % kScaleSlots] + half * 4;
+                const float4 *group = sm->scale[t % kScaleSlots] + half * 4;
                 const int valid = sees - t * kPrefillTile - half * 64;
                 uint32_t r0[16], r1[16];
                 tcgen05_fence_after();
@@ -670,7 +666,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                             for (int j = 0; j < 16; ++j)
                                 mt = fmaxf(mt, j < valid - 16 * c ? __uint_as_float(r0[j]) : -INFINITY);
-                            const float2 g = group[c];
+                            const float4 g = group[c];
                             m_own = fmaxf(m_own, fmaf(mt, c2 * g.x, g.y));
                         }
                         load(r0, 0);
@@ -707,10 +703,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 if (!go)
                     continue;
                 const float base = kBias - (ref == -INFINITY ? 0.f : ref);
-                float mx = -INFINITY;
+                float sum_tile = 0.f;   // of the half's weights
                 // 16 scores to weights, over their columns
                 auto weights = [&](const uint32_t (&r)[16], int j16, auto cut) {
-                    const float2 g = group[j16];
+                    const float4 g = group[j16];
                     const float2 c = make_float2(c2 * g.x, c2 * g.x), off = make_float2(g.y + base, g.y + base);
                     uint32_t w[8];
                     float2 sum = make_float2(0.f, 0.f);
@@ -721,15 +717,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             x.x = 16 * j16 + 2 * j < valid ? x.x : -INFINITY;
                             x.y = 16 * j16 + 2 * j + 1 < valid ? x.y : -INFINITY;
                         }
-                        mx = fmaxf(mx, fmaxf(x.x, x.y));
                         const float2 e = make_float2(ex2(x.x), ex2(x.y));
                         sum = add2(sum, e);
                         w[j] = pack_f16x2(e);
                     }
                     tmem_st8(s_col + 16 * j16, w);
-                    // (a group that the row does not see counts nothing, whatever its scale)
                     const float part = sum.x + sum.y;
-                    l = part == 0.f ? l : fmaf(part, ex2(-g.y), l);
+                    sum_tile += part;
+                    l = fmaf(part, g.z, l);
                 };
                 // The tile's 64 scores, the next 16 on their way meanwhile.
                 auto tile = [&](auto cut) {
@@ -739,7 +734,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     ready(r1);
                     load(r0, 2);
                     weights(r1, 1, cut);
-                    publish(0);
                     ready(r0);
                     load(r1, 3);
                     weights(r0, 2, cut);
@@ -751,11 +745,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     tile(std::true_type{});
                 else
                     tile(std::false_type{});
-                m_own = fmaxf(m_own, mx - base);
+                m_own = fmaxf(m_own, __log2f(sum_tile) - base);
                 sm->row_max[i & 1][s][half][trow] = __float2bfloat16_rn(m_own);
-                publish(1);
-                if (lane == 0)
+                tmem_wait_st();
+                tcgen05_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(smem_addr(&sm->p_ready[s]));
                     mbar_arrive(smem_addr(&sm->scales_free[t % kScaleSlots]));
+                }
             }
             // ------------------------------------------------------- the output
             for (int x = 0; x < 2; ++x)   // both streams' products are done with the ring
