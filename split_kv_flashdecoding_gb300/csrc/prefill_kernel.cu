@@ -21,17 +21,18 @@
 //
 // Four warps copy the codes into shared memory and widen them into operand tiles.
 //
-// Warps: 0-15 the softmax -- two warpgroups a stream, one a half of the tile's keys;
-// a thread owns a row and 64 of its scores.  16-19 load and widen, 20 issues the
-// products of both streams in turn, 21 looks up the tiles' scales.
+// Warps: 0-7 the softmax, a warpgroup a stream; a thread owns a row and all of its
+// scores, 128 in registers.  (Two threads a row, 64 scores each, took 3600 cycles a
+// tile of two row tiles for XXXX: the streams wait for the chain scores -> weights ->
+// products, and more registers a thread shorten it.)  8-11 load and widen, 12 issues
+// the products of both streams in turn, 13 looks up the tiles' scales.
 //
 // A row's reference E comes from the tiles up to the last one (the first tile's from
-// its own largest e): of each half of a tile the log of its sum of weights, which
-// costs no comparisons; it is up to log2 64 above the largest e, but then the row's sum
-// is that much larger, too, and what f16 loses of small weights is as little of it.  It
-// is exchanged between the row's two warps by shared memory, and E is raised, with O
-// rescaled, when that is over 2^kRaise above it: so no step waits for its own
-// maximum.  A score so far above all before it that its weight is over
+// its own largest e): of each the log of its sum of weights, which costs no
+// comparisons; it is up to log2 128 above the largest e, but then the row's sum is that
+// much larger, too, and what f16 loses of small weights is as little of it.  E is
+// raised, with O rescaled, when that is over 2^kRaise above it: so no step waits for
+// its own maximum.  A score so far above all before it that its weight is over
 // f16's range is seen at the end, and the CTA then does its item again with the
 // maximum of every step before its weights.
 #include <type_traits>
@@ -57,14 +58,14 @@ constexpr int kBuffers = 7;                                 // Q tiles and the r
 constexpr int kRawTiles = 4, kRawBytes = kBufBytes / 2;      // tiles of codes on their way
 constexpr int kMaxRing = kBuffers - 1 - kRawTiles / 2;
 constexpr int kScaleSlots = 4;
-constexpr int kSoftmaxThreads = 512;
-constexpr int kStreamWarps = 8;
-constexpr int kLoadWarp = 16, kLoadWarps = 4, kMmaWarp = 20, kScaleWarp = 21;   // (and two warps without work)
-constexpr int kThreads = 768;
+constexpr int kSoftmaxThreads = 256;
+constexpr int kStreamWarps = 4;
+constexpr int kLoadWarp = 8, kLoadWarps = 4, kMmaWarp = 12, kScaleWarp = 13;   // (and two warps without work)
+constexpr int kThreads = 512;
 // Registers a thread: at the launch, and after the warpgroups have shared them out,
-// four of the softmax, the loads, the products.
-constexpr int kRegs = 80, kSoftmaxRegs = 96, kLoadRegs = 56, kMmaRegs = 40;
-static_assert(4 * kSoftmaxRegs + kLoadRegs + kMmaRegs <= kThreads / 128 * kRegs, "no more than the launch has");
+// two of the softmax, the loads, the products.
+constexpr int kRegs = 128, kSoftmaxRegs = 184, kLoadRegs = 80, kMmaRegs = 56;
+static_assert(2 * kSoftmaxRegs + kLoadRegs + kMmaRegs <= kThreads / 128 * kRegs, "no more than the launch has");
 static_assert(kThreads * kRegs <= 65536, "registers of an SM");
 constexpr int kTmemCols = 512;
 constexpr int kStreamCols = 256;                            // S (and P over it) 128, O 128
@@ -85,14 +86,10 @@ struct PrefillSmem {
     int ok, q0, tokens, len, base, kvh, row0, rows, key0, keys, splits, part_row, q_tiles;
     float v_ref;
     float4 scale[kScaleSlots][kGroups];   // a tile's groups: K scale, log2 (V scale / v_ref), v_ref / V scale
-    union {
-        float q_scale[kPrefillRows];                        // before the first step: a row's factor
-        __nv_bfloat16 row_max[2][2][2][kTileRows];          // [parity][stream][half]
-    };
+    float q_scale[kPrefillRows];          // a row's factor
 };
-struct PrefillEnd {   // at the end, behind the staged rows
-    float row_sum[2][2][kTileRows];
-    float row_ref[kTileRows];
+struct PrefillEnd {   // at the end, behind the staged rows: stream 1's state, one row tile
+    float row_sum[kTileRows], row_ref[kTileRows];
 };
 constexpr int kEndOffset = kPrefillRows * kOutStride * 4;
 static_assert(kEndOffset + (int)sizeof(PrefillEnd) <= kBuffers * kBufBytes, "the epilogue works over the ring");
@@ -451,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const uint32_t pa = tmem + s * kStreamCols, va = v_lo + v_at.slot * kBuf16;
 #pragma unroll
                 for (int k = 0; k < 8; ++k)   // 16 keys a step
-                    mma_ts(pa + 128, pa + 16 * k, va + k * 2 * 1024 / 16, hi, id_o, i > 0 || k > 0, leader);
+                    mma_ts(pa + 128, pa + 8 * k, va + k * 2 * 1024 / 16, hi, id_o, i > 0 || k > 0, leader);
                 if (!two || s == 1) {
                     tcgen05_commit(smem_addr(&sm->empty[v_at.slot]), leader);
                     v_at.advance(v_tile == n - 2 ? 1 : 2);
@@ -572,16 +569,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         do {
             const bool careful = pass > 0;
             // -------------------------------------------------------- the softmax
-            const int s = warp >> 3, half = (warp >> 2) & 1, quad = warp & 3;
+            const int s = warp >> 2, quad = warp & 3;
             const int trow = quad * 32 + lane;   // row of the stream's tile: lane of tensor memory
-            const uint32_t s_col = tmem + ((uint32_t)quad << 21) + s * kStreamCols + half * 64, o_col = s_col + 128;
-            const int pair_bar = 2 + s * 4 + quad;   // barrier of the two warps that share rows
+            const uint32_t s_col = tmem + ((uint32_t)quad << 21) + s * kStreamCols, o_col = s_col + 128;
             if (ok && !careful) {
                 // Q rows as f16 into shared memory, a tile [half][128 rows][128 bytes]; a
                 // negative factor of the scores turns q around.  Each row times the
                 // power of two that puts its largest magnitude in [2^8, 2^9): exact down
                 // to 2^-22 of it.
                 const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+#pragma unroll 4
                 for (int i = tid; i < q_tiles * kTileRows * 16; i += kSoftmaxThreads) {
                     const int r = i >> 4, ch = i & 15;
                     uint4 v = make_uint4(0u, 0u, 0u, 0u);
@@ -628,125 +625,106 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             if (!careful) {
                 barrier(1, kSoftmaxThreads);   // q_scale is written
                 c2 = fabsf(p.scale) * kLog2e * (ok ? sm->q_scale[r_mine] : 0.f);
-                barrier(1, kSoftmaxThreads);   // row_max takes its place
             }
             // keys of the item that the row sees
             const int token = min((sm->row0 + r_mine) / p.group, sm->tokens - 1);
             const int sees = ok && p.causal ? min(sm->keys, sm->len - sm->tokens + token + 1 - sm->key0) : sm->keys;
-            float ref = -INFINITY, l = 0.f;   // E, and the row's sum over this half of the keys
-            float m_own = -INFINITY;          // the largest e of this half
+            float ref = -INFINITY, l = 0.f;   // E, and the row's sum
+            float most = -INFINITY;           // what E follows
             bool go = ok;
-            auto load = [&](uint32_t (&r)[16], int j16) { tmem_ld16(s_col + 16 * j16, r); };
-            auto ready = [&](uint32_t (&r)[16]) {
+            // E raised to `most`, where that is far above it, and O with it.
+            auto follow = [&](bool first) {
+                const bool up = most > ref + kRaise || (ref == -INFINITY && most > ref);
+                if (!__any_sync(0xffffffffu, up))
+                    return;
+                const float f = !up ? 1.f : ref == -INFINITY ? 0.f : ex2(ref - most);
+                ref = up ? most : ref;
+                l *= f;
+                if (first)
+                    return;
+                // the products up to the last step are done: s_full followed them
+#pragma unroll 1
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t o[16];
+                    tmem_ld16(o_col + 16 * c, o);
+                    tmem_wait_ld();
+                    settle(o);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                    tmem_st16(o_col + 16 * c, o);
+                }
+            };
+            for (int i = 0; i < steps(s) && go; ++i) {
+                const int t = two ? i : 2 * i + s;
+                go = __all_sync(0xffffffffu,
+                                wait_phase(&sm->s_full[s], i & 1, p, sm) &&
+                                    wait_phase(&sm->scales_ready[t % kScaleSlots], (t / kScaleSlots) & 1, p, sm));
+                if (!go)
+                    break;
+                const float4 *group = sm->scale[t % kScaleSlots];
+                const int valid = sees - t * kPrefillTile;
+                tcgen05_fence_after();
+                if (i == 0 || careful) {   // E from this tile's own scores
+#pragma unroll 1
+                    for (int c = 0; c < kGroups; ++c) {
+                        uint32_t x[16];
+                        tmem_ld16(s_col + 16 * c, x);
+                        tmem_wait_ld();
+                        settle(x);
+                        float mt = -INFINITY;
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            mt = fmaxf(mt, 16 * c + j < valid ? __uint_as_float(x[j]) : -INFINITY);
+                        const float4 g = group[c];
+                        most = fmaxf(most, fmaf(mt, c2 * g.x, g.y));
+                    }
+                }
+                follow(i == 0);
+                uint32_t r[kPrefillTile];   // the row's scores, then its weights
+#pragma unroll
+                for (int c = 0; c < kGroups; ++c)
+                    tmem_ld16(s_col + 16 * c, r + 16 * c);
+                const float base = kBias - (ref == -INFINITY ? 0.f : ref);
+                float sum_tile = 0.f;
                 tmem_wait_ld();
                 settle(r);
-            };
-            for (int i = 0; i < steps(s); ++i) {
-                // After an error the steps go on without work, so that the barriers
-                // of a row's two warps always meet.
-                const int t = two ? i : 2 * i + s;
-                if (go)
-                    go = __all_sync(0xffffffffu,
-                                    wait_phase(&sm->s_full[s], i & 1, p, sm) &&
-                                        wait_phase(&sm->scales_ready[t % kScaleSlots], (t / kScaleSlots) & 1, p, sm));
-                const float4 *group = sm->scale[t % kScaleSlots] + half * 4;
-                const int valid = sees - t * kPrefillTile - half * 64;
-                uint32_t r0[16], r1[16];
-                tcgen05_fence_after();
-                if (go)
-                    load(r0, 0);
-                if (i == 0 || careful) {   // E from this tile's own scores
-                    if (go) {
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) {
-                            if (c > 0)
-                                load(r0, c);
-                            ready(r0);
-                            float mt = -INFINITY;
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                mt = fmaxf(mt, j < valid - 16 * c ? __uint_as_float(r0[j]) : -INFINITY);
-                            const float4 g = group[c];
-                            m_own = fmaxf(m_own, fmaf(mt, c2 * g.x, g.y));
-                        }
-                        load(r0, 0);
-                    }
-                    sm->row_max[(i + 1) & 1][s][half][trow] = __float2bfloat16_rn(m_own);
-                }
-                barrier(pair_bar, 64);
-                {
-                    // as bf16 on both sides: the two warps must agree
-                    const float both = fmaxf(__bfloat162float(sm->row_max[(i + 1) & 1][s][0][trow]),
-                                             __bfloat162float(sm->row_max[(i + 1) & 1][s][1][trow]));
-                    const bool up = both > ref + kRaise || (ref == -INFINITY && both > ref);
-                    if (__any_sync(0xffffffffu, up)) {
-                        const float f = !up ? 1.f : ref == -INFINITY ? 0.f : ex2(ref - both);
-                        ref = up ? both : ref;
-                        l *= f;
-                        if (i > 0 && go) {   // the products up to the last step are done: s_full followed them
-                            tmem_wait_ld();
-                            settle(r0);
-#pragma unroll 1
-                            for (int c = 0; c < 4; ++c) {
-                                uint32_t o[16];
-                                tmem_ld16(o_col + 16 * c, o);
-                                tmem_wait_ld();
-                                settle(o);
-#pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                                tmem_st16(o_col + 16 * c, o);
-                            }
-                        }
-                    }
-                }
-                if (!go)
-                    continue;
-                const float base = kBias - (ref == -INFINITY ? 0.f : ref);
-                float sum_tile = 0.f;   // of the half's weights
-                // 16 scores to weights, over their columns
-                auto weights = [&](const uint32_t (&r)[16], int j16, auto cut) {
-                    const float4 g = group[j16];
-                    const float2 c = make_float2(c2 * g.x, c2 * g.x), off = make_float2(g.y + base, g.y + base);
-                    uint32_t w[8];
+                // 16 scores to weights; the weights of 16 keys are 8 columns, over those of
+                // the first half of the scores
+                auto weights = [&](int c, auto cut) {
+                    const float4 g = group[c];
+                    const float2 f = make_float2(c2 * g.x, c2 * g.x), off = make_float2(g.y + base, g.y + base);
                     float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                        float2 x = fma2(make_float2(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1])), c, off);
+                        const int at = 16 * c + 2 * j;
+                        float2 x = fma2(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), f, off);
                         if constexpr (decltype(cut)::value) {
-                            x.x = 16 * j16 + 2 * j < valid ? x.x : -INFINITY;
-                            x.y = 16 * j16 + 2 * j + 1 < valid ? x.y : -INFINITY;
+                            x.x = at < valid ? x.x : -INFINITY;
+                            x.y = at + 1 < valid ? x.y : -INFINITY;
                         }
                         const float2 e = make_float2(ex2(x.x), ex2(x.y));
                         sum = add2(sum, e);
-                        w[j] = pack_f16x2(e);
+                        r[8 * c + j] = pack_f16x2(e);
                     }
-                    tmem_st8(s_col + 16 * j16, w);
                     const float part = sum.x + sum.y;
                     sum_tile += part;
                     l = fmaf(part, g.z, l);
                 };
-                // The tile's 64 scores, the next 16 on their way meanwhile.
                 auto tile = [&](auto cut) {
-                    ready(r0);
-                    load(r1, 1);
-                    weights(r0, 0, cut);
-                    ready(r1);
-                    load(r0, 2);
-                    weights(r1, 1, cut);
-                    ready(r0);
-                    load(r1, 3);
-                    weights(r0, 2, cut);
-                    ready(r1);
-                    weights(r1, 3, cut);
+#pragma unroll
+                    for (int c = 0; c < kGroups; c += 2) {
+                        weights(c, cut);
+                        weights(c + 1, cut);
+                        tmem_st16(s_col + 8 * c, r + 8 * c);
+                    }
                 };
                 // (compares and selects for each score of every tile took 13 % of a prompt)
-                if (__any_sync(0xffffffffu, valid < 64))
+                if (__any_sync(0xffffffffu, valid < kPrefillTile))
                     tile(std::true_type{});
                 else
                     tile(std::false_type{});
-                m_own = fmaxf(m_own, __log2f(sum_tile) - base);
-                sm->row_max[i & 1][s][half][trow] = __float2bfloat16_rn(m_own);
+                most = fmaxf(most, __log2f(sum_tile) - base);
                 tmem_wait_st();
                 tcgen05_fence_before();
                 __syncwarp();
@@ -772,16 +750,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             if (careful || !sm->redo) {
                 float *stage = reinterpret_cast<float *>(smem);   // [q_tiles * 128][kOutStride]
                 PrefillEnd *end = reinterpret_cast<PrefillEnd *>(smem + kEndOffset);
-                float *mine = stage + r_mine * kOutStride + half * 64;
-                if (go)
-                    end->row_sum[s][half][trow] = l;
-                if (!two && s == 1) {
+                float *mine = stage + r_mine * kOutStride;
+                if (!two && s == 1 && go) {
                     // one row tile: stream 1 hands its state to stream 0
-                    if (go && half == 0)
-                        end->row_ref[trow] = ref;
-                    if (go && steps(1) > 0) {
+                    end->row_sum[trow] = l;
+                    end->row_ref[trow] = ref;
+                    if (steps(1) > 0) {
 #pragma unroll 1
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < 8; ++c) {
                             uint32_t o[16];
                             tmem_ld16(o_col + 16 * c, o);
                             tmem_wait_ld();
@@ -793,23 +769,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         }
                     }
                 }
-                barrier(1, kSoftmaxThreads);
+                if (!two)
+                    barrier(1, kSoftmaxThreads);
                 if (go && (two || s == 0)) {
-                    float f0 = 1.f, f1 = 0.f, m = ref, den = end->row_sum[s][0][trow] + end->row_sum[s][1][trow];
+                    float f0 = 1.f, f1 = 0.f, m = ref, den = l;
                     const bool join = !two && steps(1) > 0;
                     if (join) {
-                        const float m1 = end->row_ref[trow], l1 = end->row_sum[1][0][trow] + end->row_sum[1][1][trow];
+                        const float m1 = end->row_ref[trow];
                         m = fmaxf(ref, m1);
                         f0 = ref == -INFINITY ? 0.f : ex2(ref - m);
                         f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
-                        den = den * f0 + l1 * f1;
+                        den = l * f0 + end->row_sum[trow] * f1;
                     }
                     // a row that sees no key: O = 0, LSE = -inf
                     const float inv = den == 0.f ? 0.f : sm->v_ref / den;
                     f0 *= inv;
                     f1 *= inv;
 #pragma unroll 1
-                    for (int c = 0; c < 4; ++c) {
+                    for (int c = 0; c < 8; ++c) {
                         uint32_t o[16];
                         if (n > 0) {
                             tmem_ld16(o_col + 16 * c, o);
@@ -834,7 +811,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             *d = v;
                         }
                     }
-                    if (half == 0 && r_mine < sm->rows) {
+                    if (r_mine < sm->rows) {
                         const int gr = sm->row0 + r_mine;
                         const int64_t at = (int64_t)(gr / p.group) * p.num_qo_heads + sm->kvh * p.group + gr % p.group;
                         const float lse = den == 0.f ? -INFINITY : (m + log2f(den) - kBias) * kLn2;
