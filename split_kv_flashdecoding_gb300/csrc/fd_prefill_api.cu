@@ -272,6 +272,7 @@ extern "C" int fd_prefill_paged_int8(const fd_prefill_plan *plan, int num_pages,
     p.num_qo_heads = x.num_qo_heads;
     p.num_kv_heads = x.num_kv_heads;
     p.group = group;
+    p.group_log2 = group == 8 ? 3 : group / 2;
     p.page_size = x.page_size;
     p.num_pages = num_pages;
     p.page_entries = x.num_page_entries;

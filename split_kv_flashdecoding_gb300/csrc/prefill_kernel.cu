@@ -55,8 +55,8 @@ constexpr int kTileRows = 128;                              // query rows of a t
 constexpr int kBufBytes = kPrefillTile * kHeadDim * 2;      // an f16 tile: 32 KB
 constexpr int kHalfBytes = kBufBytes / 2;
 constexpr int kBuffers = 7;                                 // Q tiles and the ring together
-constexpr int kRawTiles = 4, kRawBytes = kBufBytes / 2;      // tiles of codes on their way
-constexpr int kMaxRing = kBuffers - 1 - kRawTiles / 2;
+constexpr int kRing = 4;                                    // operand tiles of K and V
+constexpr int kRawBytes = kBufBytes / 2;                    // a tile of codes: those on their way take the rest
 constexpr int kScaleSlots = 4;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kStreamWarps = 4;
@@ -76,7 +76,7 @@ constexpr int kGroups = kPrefillTile / 16;
 constexpr float kLeastV = -40.f, kMostV = 100.f;            // log2 of a V scale over v_ref
 
 struct PrefillSmem {
-    uint64_t full[kMaxRing], empty[kMaxRing];
+    uint64_t full[kRing], empty[kRing];
     uint64_t scales_ready[kScaleSlots], scales_free[kScaleSlots];
     uint64_t s_full[2], p_ready[2], o_done[2];
     uint64_t q_ready, drain;
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 mbar_inval(smem_addr(bar));
             mbar_init(smem_addr(bar), count);
         };
-        for (int i = 0; i < kMaxRing; ++i) {
+        for (int i = 0; i < kRing; ++i) {
             init(&sm->full[i], kLoadWarps);
             init(&sm->empty[i], 1);
         }
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 sm->row0 = block * kPrefillRows;
                 sm->rows = min(c.tokens * p.group - sm->row0, kPrefillRows);
                 sm->key0 = split * len;
-                const int last_token = (sm->row0 + sm->rows - 1) / p.group;
+                const int last_token = (sm->row0 + sm->rows - 1) >> p.group_log2;
                 const int end = p.causal ? min(c.len, c.len - c.tokens + last_token + 1) : c.len;
                 sm->keys = max(0, min(end - sm->key0, len));
                 sm->splits = c.splits;
@@ -333,7 +333,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const bool ok = sm->ok;
     const int q_tiles = sm->q_tiles;
     const bool two = q_tiles == 2;
-    const int nw = kBuffers - kRawTiles / 2 - q_tiles;   // operand tiles of the ring: 3 or 4
     const int n = (sm->keys + kPrefillTile - 1) / kPrefillTile;
     // local steps of stream s: every tile (two row tiles) or every other one
     auto steps = [&](int s) { return two ? n : (n + 1 - s) / 2; };
@@ -418,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             const uint32_t v_lo = smem_desc_lo(ring, kHalfBytes);
             constexpr uint32_t hi = smem_desc_hi(1024);
             constexpr uint32_t kBuf16 = kBufBytes / 16;
-            Place k_at(0, nw), v_at(n > 1 ? 2 : 1, nw);
+            Place k_at(0, kRing), v_at(n > 1 ? 2 : 1, kRing);
             int k_tile = 0, v_tile = 0;
             wait_phase(&sm->q_ready, 0, p, sm);
             // S of stream s's next step: K of its tile; frees the buffer after the
@@ -486,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             // lane: the lanes of a quarter warp are two rows r and r ^ 5 and four
             // chunks of 16 bytes, whose 32 bytes of f16 meet no bank twice.  Unit j of a
             // tile lies in its 16-key group j.  The codes come by 16-byte asynchronous
-            // copies, kRawTiles tiles ahead, each to a place of its lane's own: a lane
+            // copies, two or four tiles ahead, each to a place of its lane's own: a lane
             // waits for its own copies alone.  (Loads into registers a tile ahead: 2.9
             // us a tile of one row tile; their latency showed.)
             const int me = warp - kLoadWarp;   // rows 8 (me / 2) of each group, half me % 2
@@ -499,9 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             GroupPages pages(p, sm->key0, sm->keys, sm->base);
             GroupPages::Spot here = pages.next();
             int row_k = 0, row_v = 0;   // pool rows of the lane's group: newest K tile, the one before
-            const uint32_t raw = ring + nw * kBufBytes + me * (kRawBytes / kLoadWarps) + lane * 16;
-            uint8_t *raw_ptr = ring_ptr + nw * kBufBytes + me * (kRawBytes / kLoadWarps) + lane * 16;
-            auto issue = [&](int pos) {
+            const uint32_t raw = ring + kRing * kBufBytes + me * (kRawBytes / kLoadWarps) + lane * 16;
+            uint8_t *raw_ptr = ring_ptr + kRing * kBufBytes + me * (kRawBytes / kLoadWarps) + lane * 16;
+            auto issue = [&](int pos, int place) {
                 bool is_k;
                 const int t = at_pos(pos, is_k);
                 if (is_k) {
@@ -513,54 +512,63 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const int rows_of = is_k || t == n - 1 ? row_k : row_v;   // K of tile t + 1 has gone before V of t
 #pragma unroll
                 for (int j = 0; j < kGroups; ++j)
-                    cp_async_16(raw + (pos % kRawTiles) * kRawBytes + j * 512,
+                    cp_async_16(raw + place * kRawBytes + j * 512,
                                 from + (int64_t)(__shfl_sync(0xffffffffu, rows_of, j) + row) * row_bytes);
             };
-            Place to(0, nw);
-            for (int pos = 0; pos < kRawTiles; ++pos) {
-                if (pos < 2 * n)
-                    issue(pos);
-                cp_async_commit();
-            }
-#pragma unroll 1
-            for (int pos = 0; pos < 2 * n; ++pos) {
-                cp_async_wait_group<kRawTiles - 1>();
-                bool go = true;
-                if (pos >= nw)
-                    go = wait_phase(&sm->empty[to.slot], to.phase ^ 1, p, sm);
-                if (!__all_sync(0xffffffffu, go))
-                    break;
-                const uint8_t *src = raw_ptr + (pos % kRawTiles) * kRawBytes;
-                uint8_t *dst0 = ring_ptr + to.slot * kBufBytes + lane_dst;
-                uint8_t *dst1 = ring_ptr + to.slot * kBufBytes + (lane_dst ^ 16);
-#pragma unroll
-                for (int h = 0; h < kGroups; h += 4) {
-                    uint4 x[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        x[j] = *reinterpret_cast<const uint4 *>(src + (h + j) * 512);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
-                        uint32_t f[8];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            int8x4_to_f16x2x2<0, 1, 2, 3>(w[q], f[2 * q], f[2 * q + 1]);
-                        *reinterpret_cast<uint4 *>(dst0 + (h + j) * 2048) = make_uint4(f[0], f[1], f[2], f[3]);
-                        *reinterpret_cast<uint4 *>(dst1 + (h + j) * 2048) = make_uint4(f[4], f[5], f[6], f[7]);
-                    }
+            // `Ahead` tiles of codes on their way: two beside two Q tiles, else four.  (Three
+            // operand tiles and four of codes made the products wait for each V tile.)
+            auto stream = [&](auto ahead) {
+                constexpr int kAhead = decltype(ahead)::value;
+                Place to(0, kRing);
+                for (int pos = 0; pos < kAhead; ++pos) {
+                    if (pos < 2 * n)
+                        issue(pos, pos);
+                    cp_async_commit();
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(smem_addr(&sm->full[to.slot]));
-                to.advance(1);
-                // the place's codes have gone into the operand tile
-                if (pos + kRawTiles < 2 * n)
-                    issue(pos + kRawTiles);
-                cp_async_commit();
-            }
-            cp_async_wait_group<0>();
+#pragma unroll 1
+                for (int pos = 0; pos < 2 * n; ++pos) {
+                    cp_async_wait_group<kAhead - 1>();
+                    bool go = true;
+                    if (pos >= kRing)
+                        go = wait_phase(&sm->empty[to.slot], to.phase ^ 1, p, sm);
+                    if (!__all_sync(0xffffffffu, go))
+                        break;
+                    const uint8_t *src = raw_ptr + (pos % kAhead) * kRawBytes;
+                    uint8_t *dst0 = ring_ptr + to.slot * kBufBytes + lane_dst;
+                    uint8_t *dst1 = ring_ptr + to.slot * kBufBytes + (lane_dst ^ 16);
+#pragma unroll
+                    for (int h = 0; h < kGroups; h += 4) {
+                        uint4 x[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+                            x[j] = *reinterpret_cast<const uint4 *>(src + (h + j) * 512);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                            uint32_t f[8];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                int8x4_to_f16x2x2<0, 1, 2, 3>(w[q], f[2 * q], f[2 * q + 1]);
+                            *reinterpret_cast<uint4 *>(dst0 + (h + j) * 2048) = make_uint4(f[0], f[1], f[2], f[3]);
+                            *reinterpret_cast<uint4 *>(dst1 + (h + j) * 2048) = make_uint4(f[4], f[5], f[6], f[7]);
+                        }
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&sm->full[to.slot]));
+                    to.advance(1);
+                    // the place's codes have gone into the operand tile
+                    if (pos + kAhead < 2 * n)
+                        issue(pos + kAhead, pos % kAhead);
+                    cp_async_commit();
+                }
+                cp_async_wait_group<0>();
+            };
+            if (two)
+                stream(std::integral_constant<int, 2>{});
+            else
+                stream(std::integral_constant<int, 4>{});
         } while (another_pass(pass++));
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -578,32 +586,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 // power of two that puts its largest magnitude in [2^8, 2^9): exact down
                 // to 2^-22 of it.
                 const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
-#pragma unroll 4
-                for (int i = tid; i < q_tiles * kTileRows * 16; i += kSoftmaxThreads) {
-                    const int r = i >> 4, ch = i & 15;
-                    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < sm->rows) {
-                        const int gr = sm->row0 + r;
-                        const uint16_t *from = p.q + (sm->q0 + gr / p.group) * p.q_stride +
-                                               (sm->kvh * p.group + gr % p.group) * kHeadDim;
-                        v = __ldcg(reinterpret_cast<const uint4 *>(from) + ch);
-                    }
-                    uint32_t w[4] = {v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip};
-                    float amax = 0.f;
+                // a thread: chunk tid % 16 of every 16th row, all its loads in flight at once
+                // (four at a time: 12 us)
+                constexpr int kRowsOnce = kSoftmaxThreads / 16;
+                const int ch = tid & 15;
+                uint4 v[kPrefillRows / kRowsOnce];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 a = bf16x2_to_float2(w[j]);
-                        amax = fmaxf(amax, fmaxf(fabsf(a.x), fabsf(a.y)));
+                for (int k = 0; k < kPrefillRows / kRowsOnce; ++k) {
+                    const int r = k * kRowsOnce + (tid >> 4), gr = sm->row0 + r;
+                    v[k] = make_uint4(0u, 0u, 0u, 0u);
+                    if (r < sm->rows) {
+                        const uint16_t *from = p.q + (sm->q0 + (gr >> p.group_log2)) * p.q_stride +
+                                               ((sm->kvh << p.group_log2) + (gr & (p.group - 1))) * kHeadDim;
+                        v[k] = __ldcg(reinterpret_cast<const uint4 *>(from) + ch);
                     }
+                }
+#pragma unroll
+                for (int k = 0; k < kPrefillRows / kRowsOnce; ++k) {
+                    if (k * kRowsOnce >= q_tiles * kTileRows)
+                        break;
+                    const int r = k * kRowsOnce + (tid >> 4), rr = r & (kTileRows - 1);
+                    uint32_t w[4] = {v[k].x ^ flip, v[k].y ^ flip, v[k].z ^ flip, v[k].w ^ flip};
+                    uint32_t most = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
+                                             __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
+                    most = max(most << 16, most & 0xffff0000u);   // of the bits of magnitudes
 #pragma unroll
                     for (int o = 1; o < 16; o <<= 1)
-                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-                    int sh = 0;
-                    if (amax > 0.f) {
-                        int e;
-                        frexpf(amax, &e);
-                        sh = min(max(9 - e, -100), 100);
-                    }
+                        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+                    const int sh = min(max(9 + 126 - (int)(most >> 23), -100), 100);
                     const float up = __int_as_float((127 + sh) << 23);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -612,7 +622,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     }
                     if (ch == 0)
                         sm->q_scale[r] = __int_as_float((127 - sh) << 23);
-                    const int rr = r & 127;
                     *reinterpret_cast<uint4 *>(smem + (r >> 7) * kBufBytes + (ch >> 3) * kHalfBytes + rr * 128 +
                                                (((ch & 7) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
@@ -627,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 c2 = fabsf(p.scale) * kLog2e * (ok ? sm->q_scale[r_mine] : 0.f);
             }
             // keys of the item that the row sees
-            const int token = min((sm->row0 + r_mine) / p.group, sm->tokens - 1);
+            const int token = min((sm->row0 + r_mine) >> p.group_log2, sm->tokens - 1);
             const int sees = ok && p.causal ? min(sm->keys, sm->len - sm->tokens + token + 1 - sm->key0) : sm->keys;
             float ref = -INFINITY, l = 0.f;   // E, and the row's sum
             float most = -INFINITY;           // what E follows
@@ -667,17 +676,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 tcgen05_fence_after();
                 if (i == 0 || careful) {   // E from this tile's own scores
 #pragma unroll 1
-                    for (int c = 0; c < kGroups; ++c) {
-                        uint32_t x[16];
-                        tmem_ld16(s_col + 16 * c, x);
+                    for (int c0 = 0; c0 < kGroups; c0 += 4) {
+                        uint32_t x[64];
+#pragma unroll
+                        for (int c = 0; c < 4; ++c)
+                            tmem_ld16(s_col + 16 * (c0 + c), x + 16 * c);
                         tmem_wait_ld();
                         settle(x);
-                        float mt = -INFINITY;
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            mt = fmaxf(mt, 16 * c + j < valid ? __uint_as_float(x[j]) : -INFINITY);
-                        const float4 g = group[c];
-                        most = fmaxf(most, fmaf(mt, c2 * g.x, g.y));
+                        for (int c = 0; c < 4; ++c) {
+                            float mt = -INFINITY;
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                mt = fmaxf(mt, 16 * (c0 + c) + j < valid ? __uint_as_float(x[16 * c + j]) : -INFINITY);
+                            const float4 g = group[c0 + c];
+                            most = fmaxf(most, fmaf(mt, c2 * g.x, g.y));
+                        }
                     }
                 }
                 follow(i == 0);
@@ -785,56 +799,51 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     const float inv = den == 0.f ? 0.f : sm->v_ref / den;
                     f0 *= inv;
                     f1 *= inv;
-#pragma unroll 1
+                    // A thread writes its row, 32 bytes of bf16 (a sector) at a time.
+                    const int gr = sm->row0 + r_mine;
+                    const int64_t at = (int64_t)(gr >> p.group_log2) * p.num_qo_heads +
+                                       (sm->kvh << p.group_log2) + (gr & (p.group - 1));
+                    const bool partial = sm->splits > 1, has_row = r_mine < sm->rows;
+                    float *part = p.partial_o + (sm->part_row + at * sm->splits) * kHeadDim;
+                    uint16_t *out = p.o + ((int64_t)sm->q0 * p.num_qo_heads + at) * kHeadDim;
+#pragma unroll 2
                     for (int c = 0; c < 8; ++c) {
                         uint32_t o[16];
+                        float v[16];
                         if (n > 0) {
                             tmem_ld16(o_col + 16 * c, o);
                             tmem_wait_ld();
                             settle(o);
                         }
 #pragma unroll
-                        for (int j = 0; j < 16; j += 4) {
-                            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                            float4 *d = reinterpret_cast<float4 *>(mine + 16 * c + j);
-                            if (inv != 0.f) {
-                                v = make_float4(__uint_as_float(o[j]) * f0, __uint_as_float(o[j + 1]) * f0,
-                                                __uint_as_float(o[j + 2]) * f0, __uint_as_float(o[j + 3]) * f0);
-                                if (join) {
-                                    const float4 w = *d;
-                                    v.x = fmaf(w.x, f1, v.x);
-                                    v.y = fmaf(w.y, f1, v.y);
-                                    v.z = fmaf(w.z, f1, v.z);
-                                    v.w = fmaf(w.w, f1, v.w);
-                                }
-                            }
-                            *d = v;
+                        for (int j = 0; j < 16; ++j)
+                            v[j] = inv == 0.f ? 0.f : __uint_as_float(o[j]) * f0;
+                        if (join && inv != 0.f) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                v[j] = fmaf(mine[16 * c + j], f1, v[j]);
+                        }
+                        if (!has_row)
+                            continue;
+                        if (partial) {
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4)
+                                *reinterpret_cast<float4 *>(part + 16 * c + j) =
+                                    make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; j += 8)
+                                *reinterpret_cast<uint4 *>(out + 16 * c + j) =
+                                    make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
+                                               pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7]));
                         }
                     }
-                    if (r_mine < sm->rows) {
-                        const int gr = sm->row0 + r_mine;
-                        const int64_t at = (int64_t)(gr / p.group) * p.num_qo_heads + sm->kvh * p.group + gr % p.group;
+                    if (has_row) {
                         const float lse = den == 0.f ? -INFINITY : (m + log2f(den) - kBias) * kLn2;
-                        if (sm->splits > 1)
+                        if (partial)
                             p.partial_lse[sm->part_row + at * sm->splits] = lse;
                         else if (p.lse)
                             p.lse[(int64_t)sm->q0 * p.num_qo_heads + at] = lse;
-                    }
-                }
-                barrier(1, kSoftmaxThreads);
-                if (go) {   // whole rows, a warp at a time
-                    for (int r = warp; r < sm->rows; r += kSoftmaxThreads / 32) {
-                        const int gr = sm->row0 + r;
-                        const int64_t at = (int64_t)(gr / p.group) * p.num_qo_heads + sm->kvh * p.group + gr % p.group;
-                        const float4 v = *reinterpret_cast<const float4 *>(stage + r * kOutStride + 4 * lane);
-                        if (sm->splits > 1) {
-                            float *dst = p.partial_o + (sm->part_row + at * sm->splits) * kHeadDim;
-                            reinterpret_cast<float4 *>(dst)[lane] = v;
-                        } else {
-                            uint16_t *dst = p.o + ((int64_t)sm->q0 * p.num_qo_heads + at) * kHeadDim;
-                            reinterpret_cast<uint2 *>(dst)[lane] =
-                                make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
-                        }
                     }
                 }
             }

@@ -42,7 +42,7 @@ struct PrefillParams {
     float *lse;                      // [num_tokens, Hq], or null
     float *partial_o, *partial_lse;  // rows of requests with several splits
     int *status;
-    int32_t batch, num_tokens, num_qo_heads, num_kv_heads, group;
+    int32_t batch, num_tokens, num_qo_heads, num_kv_heads, group, group_log2;
     int32_t page_size, num_pages, page_entries, scale_heads;
     int32_t causal, chunk, num_items, num_partial_rows, merge_rows;
     float scale;
