@@ -78,7 +78,7 @@ constexpr float kLeastV = -40.f, kMostV = 100.f;            // log2 of a V scale
 struct PrefillSmem {
     uint64_t full[kRing], empty[kRing];
     uint64_t scales_ready[kScaleSlots], scales_free[kScaleSlots];
-    uint64_t s_full[2], p_ready[2], o_done[2];
+    uint64_t s_full[2], p_ready[2][2], o_done[2];
     uint64_t q_ready, drain;
     uint32_t tmem;
     int abort, redo;
@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
         for (int s = 0; s < 2; ++s) {
             init(&sm->s_full[s], 1);
-            init(&sm->p_ready[s], kStreamWarps);
+            init(&sm->p_ready[s][0], kStreamWarps);
+            init(&sm->p_ready[s][1], kStreamWarps);
             init(&sm->o_done[s], 1);
         }
         init(&sm->q_ready, kSoftmaxThreads / 32);
@@ -438,16 +439,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     ++k_tile;
                 }
             };
-            // O += P V of stream s's step i.  (Published in two parts, for the products
-            // to start on the first, the weights cost a prompt 2 % more.)
+            // O += P V of stream s's step i, as each half of the weights is ready.
             auto values = [&](int s, int i, bool last) {
                 wait_phase(&sm->full[v_at.slot], v_at.phase, p, sm);
-                wait_phase(&sm->p_ready[s], i & 1, p, sm);
-                tcgen05_fence_after();
                 const uint32_t pa = tmem + s * kStreamCols, va = v_lo + v_at.slot * kBuf16;
 #pragma unroll
-                for (int k = 0; k < 8; ++k)   // 16 keys a step
+                for (int k = 0; k < 8; ++k) {   // 16 keys a step
+                    if (k % 4 == 0) {
+                        wait_phase(&sm->p_ready[s][k / 4], i & 1, p, sm);
+                        tcgen05_fence_after();
+                    }
                     mma_ts(pa + 128, pa + 8 * k, va + k * 2 * 1024 / 16, hi, id_o, i > 0 || k > 0, leader);
+                }
                 if (!two || s == 1) {
                     tcgen05_commit(smem_addr(&sm->empty[v_at.slot]), leader);
                     v_at.advance(v_tile == n - 2 ? 1 : 2);
@@ -725,12 +728,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     sum_tile += part;
                     l = fmaf(part, g.z, l);
                 };
+                auto publish = [&](int part) {
+                    tmem_wait_st();
+                    tcgen05_fence_before();
+                    __syncwarp();
+                    if (lane == 0)
+                        mbar_arrive(smem_addr(&sm->p_ready[s][part]));
+                };
                 auto tile = [&](auto cut) {
 #pragma unroll
                     for (int c = 0; c < kGroups; c += 2) {
                         weights(c, cut);
                         weights(c + 1, cut);
                         tmem_st16(s_col + 8 * c, r + 8 * c);
+                        if (c == 2)
+                            publish(0);
                     }
                 };
                 // (compares and selects for each score of every tile took 13 % of a prompt)
@@ -738,14 +750,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     tile(std::true_type{});
                 else
                     tile(std::false_type{});
-                most = fmaxf(most, __log2f(sum_tile) - base);
-                tmem_wait_st();
-                tcgen05_fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(smem_addr(&sm->p_ready[s]));
+                publish(1);
+                if (lane == 0)
                     mbar_arrive(smem_addr(&sm->scales_free[t % kScaleSlots]));
-                }
+                most = fmaxf(most, __log2f(sum_tile) - base);
             }
             // ------------------------------------------------------- the output
             for (int x = 0; x < 2; ++x)   // both streams' products are done with the ring
