@@ -219,6 +219,9 @@ def _check(rc: int, what: str):
 
 
 def _host_indptr(kv_indptr) -> np.ndarray:
+    if type(kv_indptr) is np.ndarray and kv_indptr.dtype == np.int32 and kv_indptr.ndim == 1 and \
+            kv_indptr.flags.c_contiguous:
+        return kv_indptr
     try:
         import torch
         if isinstance(kv_indptr, torch.Tensor):
@@ -860,7 +863,7 @@ def copy_pages(pools, src, dst, *, workspace=None, stream=None):
 
 
 def _host_ptr(a):
-    return a.ctypes.data_as(ctypes.c_void_p)
+    return a.ctypes.data
 
 
 def plan_shared(batch: int, num_qo_heads: int, num_kv_heads: int, head_dim: int, prefix_req_indptr,

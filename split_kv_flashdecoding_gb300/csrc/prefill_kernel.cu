@@ -91,8 +91,13 @@ struct PrefillSmem {
 struct PrefillEnd {   // at the end, behind the staged rows: stream 1's state, one row tile
     float row_sum[kTileRows], row_ref[kTileRows];
 };
-constexpr int kEndOffset = kPrefillRows * kOutStride * 4;
-static_assert(kEndOffset + (int)sizeof(PrefillEnd) <= kBuffers * kBufBytes, "the epilogue works over the ring");
+// One row tile: stream 1's O [128][kOutStride], the rest of its state, staged rows.
+constexpr int kEndOffset = kTileRows * kOutStride * 4;
+constexpr int kStageOffset = kEndOffset + (int)sizeof(PrefillEnd);
+constexpr int kRowStage = kHeadDim * 4 + 16;            // bytes between staged rows
+static_assert(kStageOffset % 16 == 0 && kStageOffset + kTileRows * kRowStage <= kBuffers * kBufBytes &&
+                  kPrefillRows * kRowStage <= kBuffers * kBufBytes,
+              "the epilogue works over the ring");
 constexpr int kPrefillAlloc = kBuffers * kBufBytes + (int)((sizeof(PrefillSmem) + 15) / 16 * 16);
 static_assert(kPrefillAlloc <= 232448, "shared memory of one CTA");
 
@@ -273,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
         for (int i = 0; i < kScaleSlots; ++i) {
             init(&sm->scales_ready[i], 1);
-            init(&sm->scales_free[i], sm->q_tiles * kStreamWarps);
+            init(&sm->scales_free[i], 2 * kStreamWarps);   // both streams', or twice the one's
         }
         for (int s = 0; s < 2; ++s) {
             init(&sm->s_full[s], 1);
@@ -319,11 +324,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             } else {
                 report(p.status, FD_ERR_DEVICE_BOUNDS);
             }
-            init_barriers(false);
-            sm->abort = 0;
-            sm->redo = 0;
-            sm->v_ref = 1.f;
         }
+    }
+    if (warp == kScaleWarp && lane == 0) {
+        init_barriers(false);
+        sm->abort = 0;
+        sm->redo = 0;
+        sm->v_ref = 1.f;
     }
     if (warp == kLoadWarp + 1 && blockIdx.x == 0)
         check_tables(p);
@@ -590,44 +597,57 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 // to 2^-22 of it.
                 const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
                 // a thread: chunk tid % 16 of every 16th row, all its loads in flight at once
-                // (four at a time: 12 us)
-                constexpr int kRowsOnce = kSoftmaxThreads / 16;
+                // (four at a time, with divisions by the group: 12 us)
+                constexpr int kRowsOnce = kSoftmaxThreads / 16, kOfTile = kTileRows / kRowsOnce;
                 const int ch = tid & 15;
-                uint4 v[kPrefillRows / kRowsOnce];
+                uint4 v[2][kOfTile];
 #pragma unroll
-                for (int k = 0; k < kPrefillRows / kRowsOnce; ++k) {
+                for (int k = 0; k < 2 * kOfTile; ++k) {
                     const int r = k * kRowsOnce + (tid >> 4), gr = sm->row0 + r;
-                    v[k] = make_uint4(0u, 0u, 0u, 0u);
+                    v[k / kOfTile][k % kOfTile] = make_uint4(0u, 0u, 0u, 0u);
                     if (r < sm->rows) {
                         const uint16_t *from = p.q + (sm->q0 + (gr >> p.group_log2)) * p.q_stride +
                                                ((sm->kvh << p.group_log2) + (gr & (p.group - 1))) * kHeadDim;
-                        v[k] = __ldcg(reinterpret_cast<const uint4 *>(from) + ch);
+                        v[k / kOfTile][k % kOfTile] = __ldcg(reinterpret_cast<const uint4 *>(from) + ch);
                     }
                 }
+                auto to_tile = [&](uint4 (&x)[kOfTile], int tile) {
+                    uint32_t w[kOfTile][4], most[kOfTile];
 #pragma unroll
-                for (int k = 0; k < kPrefillRows / kRowsOnce; ++k) {
-                    if (k * kRowsOnce >= q_tiles * kTileRows)
-                        break;
-                    const int r = k * kRowsOnce + (tid >> 4), rr = r & (kTileRows - 1);
-                    uint32_t w[4] = {v[k].x ^ flip, v[k].y ^ flip, v[k].z ^ flip, v[k].w ^ flip};
-                    uint32_t most = __vmaxu2(__vmaxu2(w[0] & 0x7fff7fffu, w[1] & 0x7fff7fffu),
-                                             __vmaxu2(w[2] & 0x7fff7fffu, w[3] & 0x7fff7fffu));
-                    most = max(most << 16, most & 0xffff0000u);   // of the bits of magnitudes
+                    for (int k = 0; k < kOfTile; ++k) {
+                        w[k][0] = x[k].x ^ flip;
+                        w[k][1] = x[k].y ^ flip;
+                        w[k][2] = x[k].z ^ flip;
+                        w[k][3] = x[k].w ^ flip;
+                        const uint32_t m = __vmaxu2(__vmaxu2(w[k][0] & 0x7fff7fffu, w[k][1] & 0x7fff7fffu),
+                                                    __vmaxu2(w[k][2] & 0x7fff7fffu, w[k][3] & 0x7fff7fffu));
+                        most[k] = max(m << 16, m & 0xffff0000u);   // of the bits of magnitudes
+                    }
 #pragma unroll
                     for (int o = 1; o < 16; o <<= 1)
-                        most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-                    const int sh = min(max(9 + 126 - (int)(most >> 23), -100), 100);
-                    const float up = __int_as_float((127 + sh) << 23);
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 a = bf16x2_to_float2(w[j]);
-                        w[j] = pack_f16x2(make_float2(a.x * up, a.y * up));
+                        for (int k = 0; k < kOfTile; ++k)
+                            most[k] = max(most[k], __shfl_xor_sync(0xffffffffu, most[k], o));
+#pragma unroll
+                    for (int k = 0; k < kOfTile; ++k) {
+                        const int rr = k * kRowsOnce + (tid >> 4);
+                        const int sh = min(max(9 + 126 - (int)(most[k] >> 23), -100), 100);
+                        const float up = __int_as_float((127 + sh) << 23);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 a = bf16x2_to_float2(w[k][j]);
+                            w[k][j] = pack_f16x2(make_float2(a.x * up, a.y * up));
+                        }
+                        if (ch == 0)
+                            sm->q_scale[tile * kTileRows + rr] = __int_as_float((127 - sh) << 23);
+                        *reinterpret_cast<uint4 *>(smem + tile * kBufBytes + (ch >> 3) * kHalfBytes + rr * 128 +
+                                                   (((ch & 7) ^ (rr & 7)) << 4)) =
+                            make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
                     }
-                    if (ch == 0)
-                        sm->q_scale[r] = __int_as_float((127 - sh) << 23);
-                    *reinterpret_cast<uint4 *>(smem + (r >> 7) * kBufBytes + (ch >> 3) * kHalfBytes + rr * 128 +
-                                               (((ch & 7) ^ (rr & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
+                };
+                to_tile(v[0], 0);
+                if (two)
+                    to_tile(v[1], 1);
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
             __syncwarp();
@@ -751,7 +771,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 else
                     tile(std::false_type{});
                 publish(1);
-                if (lane == 0)
+                if (lane == 0 || (lane == 1 && !two))
                     mbar_arrive(smem_addr(&sm->scales_free[t % kScaleSlots]));
                 most = fmaxf(most, __log2f(sum_tile) - base);
             }
@@ -807,13 +827,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     const float inv = den == 0.f ? 0.f : sm->v_ref / den;
                     f0 *= inv;
                     f1 *= inv;
-                    // A thread writes its row, 32 bytes of bf16 (a sector) at a time.
-                    const int gr = sm->row0 + r_mine;
-                    const int64_t at = (int64_t)(gr >> p.group_log2) * p.num_qo_heads +
-                                       (sm->kvh << p.group_log2) + (gr & (p.group - 1));
-                    const bool partial = sm->splits > 1, has_row = r_mine < sm->rows;
-                    float *part = p.partial_o + (sm->part_row + at * sm->splits) * kHeadDim;
-                    uint16_t *out = p.o + ((int64_t)sm->q0 * p.num_qo_heads + at) * kHeadDim;
+                    // The warp's 32 rows through shared memory, so that whole rows are written
+                    // (by its threads, a row each: 4 us of the store unit).
+                    const int first = r_mine - lane;
+                    const bool partial = sm->splits > 1;
+                    uint8_t *rows = smem + (two ? 0 : kStageOffset) + first * kRowStage;
+                    auto row_of = [&](int r) {   // of the request's rows [token][head]
+                        const int gr = sm->row0 + r;
+                        return (int64_t)(gr >> p.group_log2) * p.num_qo_heads + (sm->kvh << p.group_log2) +
+                               (gr & (p.group - 1));
+                    };
 #pragma unroll 2
                     for (int c = 0; c < 8; ++c) {
                         uint32_t o[16];
@@ -831,27 +854,42 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             for (int j = 0; j < 16; ++j)
                                 v[j] = fmaf(mine[16 * c + j], f1, v[j]);
                         }
-                        if (!has_row)
-                            continue;
                         if (partial) {
+                            float4 *to = reinterpret_cast<float4 *>(rows + lane * kRowStage) + 4 * c;
 #pragma unroll
-                            for (int j = 0; j < 16; j += 4)
-                                *reinterpret_cast<float4 *>(part + 16 * c + j) =
-                                    make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+                            for (int j = 0; j < 4; ++j)
+                                to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                         } else {
+                            uint4 *to = reinterpret_cast<uint4 *>(rows + lane * kRowStage) + 2 * c;
 #pragma unroll
-                            for (int j = 0; j < 16; j += 8)
-                                *reinterpret_cast<uint4 *>(out + 16 * c + j) =
-                                    make_uint4(pack_bf16x2(v[j], v[j + 1]), pack_bf16x2(v[j + 2], v[j + 3]),
-                                               pack_bf16x2(v[j + 4], v[j + 5]), pack_bf16x2(v[j + 6], v[j + 7]));
+                            for (int j = 0; j < 2; ++j)
+                                to[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]),
+                                                   pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                                   pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
+                                                   pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
                         }
                     }
-                    if (has_row) {
+                    if (r_mine < sm->rows) {
                         const float lse = den == 0.f ? -INFINITY : (m + log2f(den) - kBias) * kLn2;
                         if (partial)
-                            p.partial_lse[sm->part_row + at * sm->splits] = lse;
+                            p.partial_lse[sm->part_row + row_of(r_mine) * sm->splits] = lse;
                         else if (p.lse)
-                            p.lse[(int64_t)sm->q0 * p.num_qo_heads + at] = lse;
+                            p.lse[(int64_t)sm->q0 * p.num_qo_heads + row_of(r_mine)] = lse;
+                    }
+                    __syncwarp();
+                    const int count = min(sm->rows - first, 32);
+                    if (partial) {
+#pragma unroll 4
+                        for (int r = 0; r < count; ++r)
+                            reinterpret_cast<uint4 *>(p.partial_o + (sm->part_row + row_of(first + r) * sm->splits) *
+                                                                        kHeadDim)[lane] =
+                                reinterpret_cast<const uint4 *>(rows + r * kRowStage)[lane];
+                    } else {   // two rows at once
+#pragma unroll 4
+                        for (int r = lane >> 4; r < count; r += 2)
+                            reinterpret_cast<uint4 *>(p.o + ((int64_t)sm->q0 * p.num_qo_heads + row_of(first + r)) *
+                                                                kHeadDim)[lane & 15] =
+                                reinterpret_cast<const uint4 *>(rows + r * kRowStage)[lane & 15];
                     }
                 }
             }
