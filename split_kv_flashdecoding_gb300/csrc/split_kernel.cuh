@@ -2484,20 +2484,17 @@ constexpr int kNCInt4ColsP = FD_SPLIT_INT4_COLUMN_PWARPS;   // persistent kernel
 constexpr int kNCFp8Cols = FD_SPLIT_FP8_COLUMN_WARPS;
 constexpr int kNCFp8ColsP = FD_SPLIT_FP8_COLUMN_PWARPS;
 
-#ifndef FD_SPLIT_INT8_ROW_WARPS
-#define FD_SPLIT_INT8_ROW_WARPS 4
-#endif
-#ifndef FD_SPLIT_INT8_ROW_PWARPS
-#define FD_SPLIT_INT8_ROW_PWARPS 4
-#endif
-#ifndef FD_SPLIT_INT8_COLUMN_WARPS
-#define FD_SPLIT_INT8_COLUMN_WARPS 4
-#endif
-#ifndef FD_SPLIT_INT8_COLUMN_PWARPS
-#define FD_SPLIT_INT8_COLUMN_PWARPS 4
-#endif
-constexpr int kNCInt8 = FD_SPLIT_INT8_ROW_WARPS, kNCInt8P = FD_SPLIT_INT8_ROW_PWARPS;
-constexpr int kNCInt8Cols = FD_SPLIT_INT8_COLUMN_WARPS, kNCInt8ColsP = FD_SPLIT_INT8_COLUMN_PWARPS;
+// INT8.  Column form: three consumer warps, which with the producer warps of two CTAs
+// spread evenly over the SM's schedulers (64 ragged requests, 64-key pages: 202 us
+// with three, 214 with four, 219 with five; 64k in one wave: 30.7, 32.1 and 31.5), and
+// four in one wave of splits so short that they all have a tile at once (2048 keys:
+// 8.2 for 9.1 with three).  Row form: four, and three in the persistent kernel over
+// 16-row boxes, of which the producer issues twice as many (16 requests of 64 heads
+// and 32768 keys: pages of 32 223 with four, 243 with three; of 16 281 and 267).
+constexpr int kNCInt8 = 4, kNCInt8Cols = 3, kNCInt8Short = 4, kNCInt8ColsP = 3;
+template <int KV>
+constexpr int kNCInt8P = KV == kKvPaged16 ? 3 : 4;
+constexpr int kInt8ShortTiles = 2 * kNCInt8Short;
 
 // One wave of items: one item per CTA.  More: the persistent kernel on
 // num_ctas CTAs.
@@ -2512,7 +2509,7 @@ cudaError_t launch_g(const KvMaps &m, const SplitParams &p, int num_ctas, cudaSt
                         : DT == kKvInt8 ? (cols ? kNCInt8Cols : kNCInt8)
                         : DT == kKvFp8 && cols ? kNCFp8Cols : kNC;
     constexpr int NCP = DT == kKvInt4 && cols  ? kNCInt4ColsP
-                        : DT == kKvInt8        ? (cols ? kNCInt8ColsP : kNCInt8P)
+                        : DT == kKvInt8        ? (cols ? kNCInt8ColsP : kNCInt8P<KV>)
                         : DT == kKvFp8 && cols ? kNCFp8ColsP : kNC;
     constexpr int NS1 = DT == kKvBf16 ? kNS : 2 * NC1;
     constexpr int NS = DT == kKvBf16 ? kNS : 2 * NCP;
@@ -2522,6 +2519,15 @@ cudaError_t launch_g(const KvMaps &m, const SplitParams &p, int num_ctas, cudaSt
     static_assert(kMinCtas * (LS::kAlloc + 1024) <= 233472 && kMinCtas * (LP::kAlloc + 1024) <= 233472,
                   "the resident CTAs must fit in shared memory");
     if (num_ctas >= p.num_work) {   // one wave: one item (or, device-side plan, at most one) per CTA
+        if constexpr (DT == kKvInt8 && cols) {
+            if (p.chunk <= kInt8ShortTiles * kTile) {
+                constexpr int NSS = 2 * kNCInt8Short;
+                using LSS = SingleLayout<G, kNCInt8Short, NSS, SG::kBytes>;
+                static bool configured_short[64] = {};
+                return launch_kernel(split_kv_kernel<G, kNCInt8Short, NSS, kMinCtas, KV, DT>, configured_short,
+                                     LSS::kAlloc, LSS::kWarps * 32, p.num_work, m, p, stream);
+            }
+        }
         static bool configured[64] = {};
         return launch_kernel(split_kv_kernel<G, NC1, NS1, kMinCtas, KV, DT>, configured, LS::kAlloc,
                              LS::kWarps * 32, p.num_work, m, p, stream);
