@@ -23,9 +23,10 @@
 //
 // Warps: 0-7 the softmax, a warpgroup a stream; a thread owns a row and all of its
 // scores, 128 in registers.  (Two threads a row, 64 scores each, took 3600 cycles a
-// tile of two row tiles for XXXX: the streams wait for the chain scores -> weights ->
-// products, and more registers a thread shorten it.)  8-11 load and widen, 12 issues
-// the products of both streams in turn, 13 looks up the tiles' scales.
+// tile of two row tiles, this form 3300 in its place and 3100 with the steps since: the
+// streams wait for the chain scores -> weights -> products, and a thread that needs no
+// other one shortens it.)  8-11 load and widen, 12 issues the products of both streams
+// in turn, 13 looks up the tiles' scales.
 //
 // A row's reference E comes from the tiles up to the last one (the first tile's from
 // its own largest e): of each the log of its sum of weights, which costs no
@@ -491,19 +492,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             if (n == 0)
                 continue;
             // --------------------------------------- codes to f16 operand tiles
-            // A warp's unit of work is 8 rows of one half of the head, 16 values a
-            // lane: the lanes of a quarter warp are two rows r and r ^ 5 and four
-            // chunks of 16 bytes, whose 32 bytes of f16 meet no bank twice.  Unit j of a
-            // tile lies in its 16-key group j.  The codes come by 16-byte asynchronous
-            // copies, two or four tiles ahead, each to a place of its lane's own: a lane
-            // waits for its own copies alone.  (Loads into registers a tile ahead: 2.9
-            // us a tile of one row tile; their latency showed.)
-            const int me = warp - kLoadWarp;   // rows 8 (me / 2) of each group, half me % 2
+            // A warp has two 16-key groups of each tile; its unit of work is 8 rows of one
+            // half of the head, 16 values a lane: the lanes of a quarter warp are two rows
+            // r and r ^ 5 and four chunks of 16 bytes, whose 32 bytes of f16 meet no bank
+            // twice.  (A unit of each of the eight groups, eight page rows to ask the other
+            // lanes for: 443 us of 438 for 8192 queries and keys of 16 heads.)  The codes
+            // come by 16-byte asynchronous copies, two or four tiles ahead, each to a place
+            // of its lane's own: a lane waits for its own copies alone.  (Loads into
+            // registers a tile ahead: 2.9 us a tile of one row tile; their latency showed.)
+            const int me = warp - kLoadWarp;
             const int r8 = (lane >> 3) ^ (((lane >> 2) & 1) * 5), cc = lane & 3;
-            const int row = (me >> 1) * 8 + r8;
-            const uint32_t lane_dst = (me >> 1) * 1024 + (me & 1) * kHalfBytes + r8 * 128 + (((2 * cc) ^ r8) << 4);
+            const uint32_t lane_dst = me * 4096 + r8 * 128 + (((2 * cc) ^ r8) << 4);
             const int64_t row_bytes = (int64_t)p.num_kv_heads * kHeadDim;
-            const int lane_off = sm->kvh * kHeadDim + ((me & 1) * 4 + cc) * 16;
+            const int lane_off = sm->kvh * kHeadDim + cc * 16;
             // The lane's group (lane % 8) of a tile: its page id a tile ahead.
             GroupPages pages(p, sm->key0, sm->keys, sm->base);
             GroupPages::Spot here = pages.next();
@@ -519,11 +520,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     here = pages.next();
                 }
                 const int8_t *from = (is_k ? p.k : p.v) + lane_off;
-                const int rows_of = is_k || t == n - 1 ? row_k : row_v;   // K of tile t + 1 has gone before V of t
+                const int row = is_k || t == n - 1 ? row_k : row_v;   // (K of tile t + 1 has gone before V of t)
 #pragma unroll
-                for (int j = 0; j < kGroups; ++j)
-                    cp_async_16(raw + place * kRawBytes + j * 512,
-                                from + (int64_t)(__shfl_sync(0xffffffffu, rows_of, j) + row) * row_bytes);
+                for (int g = 0; g < 2; ++g) {
+                    const int rows_of = __shfl_sync(0xffffffffu, row, 2 * me + g);
+                    const int8_t *at = from + (int64_t)(rows_of + r8) * row_bytes;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)   // rows 8 (j / 2) of the group, half j % 2
+                        cp_async_16(raw + place * kRawBytes + (4 * g + j) * 512,
+                                    at + (j >> 1) * 8 * row_bytes + (j & 1) * 64);
+                }
             };
             // `Ahead` tiles of codes on their way: two beside two Q tiles, else four.  (Three
             // operand tiles and four of codes made the products wait for each V tile.)
@@ -547,7 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     uint8_t *dst0 = ring_ptr + to.slot * kBufBytes + lane_dst;
                     uint8_t *dst1 = ring_ptr + to.slot * kBufBytes + (lane_dst ^ 16);
 #pragma unroll
-                    for (int h = 0; h < kGroups; h += 4) {
+                    for (int h = 0; h < 8; h += 4) {   // the units of a group
                         uint4 x[4];
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
@@ -555,12 +561,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
                             const uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+                            const int unit = h / 4 * 2048 + (j >> 1) * 1024 + (j & 1) * kHalfBytes;
                             uint32_t f[8];
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
                                 int8x4_to_f16x2x2<0, 1, 2, 3>(w[q], f[2 * q], f[2 * q + 1]);
-                            *reinterpret_cast<uint4 *>(dst0 + (h + j) * 2048) = make_uint4(f[0], f[1], f[2], f[3]);
-                            *reinterpret_cast<uint4 *>(dst1 + (h + j) * 2048) = make_uint4(f[4], f[5], f[6], f[7]);
+                            *reinterpret_cast<uint4 *>(dst0 + unit) = make_uint4(f[0], f[1], f[2], f[3]);
+                            *reinterpret_cast<uint4 *>(dst1 + unit) = make_uint4(f[4], f[5], f[6], f[7]);
                         }
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
