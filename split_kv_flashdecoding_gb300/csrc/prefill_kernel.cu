@@ -570,15 +570,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             *reinterpret_cast<uint4 *>(dst1 + unit) = make_uint4(f[4], f[5], f[6], f[7]);
                         }
                     }
+                    // the place's codes have gone into the operand tile
+                    if (pos + kAhead < 2 * n)
+                        issue(pos + kAhead, pos % kAhead);
+                    cp_async_commit();
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(smem_addr(&sm->full[to.slot]));
                     to.advance(1);
-                    // the place's codes have gone into the operand tile
-                    if (pos + kAhead < 2 * n)
-                        issue(pos + kAhead, pos % kAhead);
-                    cp_async_commit();
                 }
                 cp_async_wait_group<0>();
             };
