@@ -727,7 +727,7 @@ int fd_append_paged_int4(int batch, int num_tokens, int num_qo_heads, int num_kv
  * fd_append_paged_int8 -- fd_append_paged into an INT8 cache (fd_decode_paged_int8),
  * keeping each page's scales.  For a page that gets new keys and a KV head, with m
  * the largest magnitude of the new keys' values (K's rotated, in fp32) and s0 the
- * page's scale (0 where the page holds no key of the request from before):
+ * page's scale, not below 0 (0 where the page holds no key of the request from before):
  *     scale = max(s0, m / 127, 2^-126),   code = round(value / scale)
  * to nearest even, and where the scale grows the codes from before are carried over
  * as round(code * (s0 / scale)).  So a page's first keys need no scale, whatever

@@ -411,6 +411,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
 constexpr int kPageWarps = kThreads / 32;
 constexpr int kAngleRows = 64;     // tokens of a page whose angles are in shared memory at once
 constexpr int kGroupRows = 16;     // rows that a warp holds
+constexpr int kMostWarpsPerHead = kAngleRows / kGroupRows;
 constexpr float kSmallestScale = 1.17549435e-38f;
 
 struct PageWork {
@@ -626,7 +627,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_c
         // Groups part, part + wph, ..; K's angles are there for 64 rows at a time.
         auto each_group = [&](auto &&work_on) {
 #pragma unroll 1
-            for (int g0 = 0; g0 < groups; g0 += kAngleRows / kGroupRows) {
+            for (int g0 = 0; g0 < groups; g0 += kMostWarpsPerHead) {
                 const int from = g0 * kGroupRows;
                 if (rotate && have_angles != from) {
                     __syncthreads();   // the others are done with those before
@@ -635,7 +636,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_c
                     have_angles = from;
                 }
 #pragma unroll 1
-                for (int g = g0 + part; g < min(groups, g0 + kAngleRows / kGroupRows); g += wph) {
+                for (int g = g0 + part; g < min(groups, g0 + kMostWarpsPerHead); g += wph) {
                     if (!held)
                         load(g);
                     work_on(g, from);
@@ -721,12 +722,12 @@ cudaError_t launch_append_int8(const AppendParams &params, cudaStream_t stream)
     const int64_t pages = p.num_tokens / p.page_size + 2 * some;
     p.page_ctas = (int32_t)(pages < p.num_tokens ? pages : p.num_tokens);
     // Warps a head: as many as hold a page's new rows (of which a step's are one or
-    // two) in registers, and for few heads as many as there are.
+    // two) in registers, and for few heads as many as there are; up to four, which
+    // hold the rows that have their angles in shared memory at once.
     const int64_t rows = (p.num_tokens + p.page_ctas - 1) / p.page_ctas;
     p.warps_per_head = 1;
-    while (p.warps_per_head < kAngleRows / kGroupRows && p.warps_per_head * kGroupRows < rows)
-        p.warps_per_head *= 2;
-    while (p.warps_per_head < kPageWarps && kPageWarps / p.warps_per_head / 2 >= p.num_kv_heads)
+    while (p.warps_per_head < kMostWarpsPerHead &&
+           (p.warps_per_head * kGroupRows < rows || kPageWarps / p.warps_per_head / 2 >= p.num_kv_heads))
         p.warps_per_head *= 2;
     const int steps = 2 * ((p.num_kv_heads * p.warps_per_head + kPageWarps - 1) / kPageWarps);
     // Blocks a page: one (its angles are computed once) where that fills the SMs

@@ -27,6 +27,7 @@ SHAPES = [
     ("many_heads", [9, 40], [100, 7], 20, 20, 128),
     ("large_pages", [0, 1000, 5], [2500, 300, 1], 8, 4, 1024),
     ("large_pages_one_head", [600], [700], 1, 1, 1024),
+    ("one_head_pages_of_128", [0, 30], [300, 90], 4, 1, 128),
 ]
 
 
