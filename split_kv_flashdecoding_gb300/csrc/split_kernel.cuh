@@ -175,7 +175,8 @@ struct PageScaleFeed {
         const int lane = threadIdx.x & 31;
         // (the producer reports a page outside the pool and reads page 0 for it)
         const int64_t page = x < 0 || x >= p.num_pages ? 0 : x;
-        return (lane < 2 ? p.k_scale : p.v_scale)[page * p.scale_heads + kvh];
+        const float s = (lane < 2 ? p.k_scale : p.v_scale)[page * p.scale_heads + kvh];
+        return fabsf(s) < INFINITY ? s : __int_as_float(0x7fffffff);   // (-inf as a score would be a weight of 0)
     }
 
     // An item of keys t0 .. t1 of the request whose page list starts at `base_`, its

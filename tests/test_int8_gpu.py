@@ -113,6 +113,22 @@ def test_int8_scales_that_are_no_numbers_reach_their_request_alone(cuda_device, 
     assert not torch.isfinite(o[1, g: 2 * g]).any()
 
 
+@pytest.mark.parametrize("which", ["ks", "vs"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("hq", [1, 8])
+def test_int8_no_number_is_nan_whatever_the_codes(cuda_device, which, value, sign, hq):
+    # scores of one sign, an infinite scale of either: not a weight of 0, nor an infinity
+    t, c, _ = make("all", hq, 1, [300, 1], 16, "quantised", cuda_device)
+    c["k"].fill_(3 * sign)
+    c["v"].fill_(5)
+    q = torch.ones((2, hq, D), dtype=torch.bfloat16, device=cuda_device)
+    for b, page in ((0, 7), (1, 0)):
+        c[which][int(t["ids"][t["ip"][b] + page]), 0] = value
+    o, lse = run(t, c, q)
+    assert bool(o.isnan().all()) and (which == "vs" or bool(lse.isnan().all()))
+
+
 def test_int8_pages_outside_the_pool_are_flagged(cuda_device):
     t, c, q = make("bad", 8, 8, [100], 16, "random", cuda_device)
     need = fd.plan_paged(1, 8, 8, D, 16, t["ip"], t["last"]).workspace_bytes
