@@ -401,10 +401,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         !__all_sync(0xffffffffu, wait_phase(&sm->scales_free[t % kScaleSlots],
                                                             (t / kScaleSlots - 1) & 1, p, sm)))
                         break;
-                    // (v no number: what sees the group is NaN by its weights; what does not
-                    // see it adds 0 times a number)
+                    // (no number, an infinity or below 0, which would take -inf or the least
+                    // score for the largest: what sees the group is NaN by its weights; what
+                    // does not see it adds 0 times a number)
+                    const float k = scale >= 0.f && scale < INFINITY ? scale : __int_as_float(0x7fffffff);
                     if (lane < 8)
-                        sm->scale[t % kScaleSlots][lane] = make_float4(scale, v, v == v ? exp2f(-v) : 1.f, 0.f);
+                        sm->scale[t % kScaleSlots][lane] = make_float4(k, v, v == v ? exp2f(-v) : 1.f, 0.f);
                     __syncwarp();
                     if (lane == 0)
                         mbar_arrive(smem_addr(&sm->scales_ready[t % kScaleSlots]));

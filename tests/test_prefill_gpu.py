@@ -179,6 +179,22 @@ def test_prefill_scales_that_are_no_numbers_reach_what_sees_them(cuda_device, wh
     assert bool(close.all(-1)[~bad].all())
 
 
+@pytest.mark.parametrize("which", ["ks", "vs"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf"), -0.01])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("tokens", [20, 200])
+def test_prefill_no_number_is_nan_whatever_the_codes(cuda_device, which, value, sign, tokens):
+    # scores of one sign and a scale that append never leaves: not a weight of 0, nor an infinity
+    t, c, q, qi = make("all", 4, 1, [tokens, 1], [300, 1], 16, cuda_device)
+    c["k"].fill_(3 * sign)
+    c["v"].fill_(5)
+    q.fill_(1.0)
+    for page in (0, int(t["ip"][1])):   # the first page of either request
+        c[which][int(t["ids"][page]), 0] = value
+    o, _ = run(t, c, q, qi, True)
+    assert bool(o.isnan().all())
+
+
 def test_prefill_rows_behind_the_last_key_and_foreign_pages_do_not_matter(cuda_device):
     t, c, q, qi = make("leak", 16, 4, [30, 70, 16], [45, 70, 16], 48, cuda_device)
     want = run(t, c, q, qi, True)
