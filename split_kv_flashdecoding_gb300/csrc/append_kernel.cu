@@ -562,6 +562,7 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r)
 // Blocks: for each page with new keys, the steps of its heads, K's then V's, shared by
 // blocks_per_page of them (a step: a head for every warps_per_head warps, which share
 // its rows); then the queries'.
+template <bool kInterleaved>
 __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_constant__ AppendParams p)
 {
     __shared__ __align__(16) float2 s_cs[kAngleRows][kHeadDim / 2];
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_c
             unpack8(raw[i][0], a);
             unpack8(raw[i][1], b);
             if (rotate && turns0 && r < n)
-                turn_unit(a, b, s_cs[r - from], c0, c1, turns1, p.rope.interleaved);
+                turn_unit(a, b, s_cs[r - from], c0, c1, turns1, kInterleaved);
         };
         if (held)
             load(part);
@@ -742,7 +743,8 @@ cudaError_t launch_append_int8(const AppendParams &params, cudaStream_t stream)
     const int64_t grid = (int64_t)p.page_ctas * p.blocks_per_page + q_ctas;
     if (grid > INT32_MAX)
         return cudaErrorInvalidValue;
-    return launch_dependent(append_int8_kernel, dim3((unsigned)grid), kThreads, 0, stream, p);
+    return launch_dependent(p.rope.interleaved ? append_int8_kernel<true> : append_int8_kernel<false>,
+                            dim3((unsigned)grid), kThreads, 0, stream, p);
 }
 
 cudaError_t launch_append(const AppendParams &params, int kv_type, cudaStream_t stream)

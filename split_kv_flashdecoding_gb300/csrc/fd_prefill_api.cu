@@ -64,7 +64,7 @@ PlanSize size_of(const Requests &x, int32_t chunk)
 
 // Costs in SM cycles: a 128-key tile of one and of two 128-row tiles, a CTA's start
 // and end, a partial row's write and read over all SMs, the merge's launch.
-constexpr int64_t kTileOne = 2400, kTileTwo = 3300, kItemCost = 16000;
+constexpr int64_t kTileOne = 2300, kTileTwo = 3120, kItemCost = 20000;
 constexpr double kRowCost = 0.25, kMergeCost = 6000;
 
 // Time of the grid for chunk length c: its CTAs go, in launch order, to the SM that

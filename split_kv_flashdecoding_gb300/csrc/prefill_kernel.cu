@@ -21,6 +21,16 @@
 //
 // Four warps copy the codes into shared memory and widen them into operand tiles.
 //
+// Bound: the tensor cores at many rows (2048 cycles for the products of two row tiles
+// with 128 keys), one chain of scores, weights and products a stream beside it: 3100
+// cycles.  32 heads, 8192 queries and keys 432 us, 1.27 PFLOP/s, of which an item's start
+// and end (queries 3.7 us, first weights 3.6, output 2.6, with nothing beside them) are
+// a sixth; 32768 queries and keys 5.9 ms, 1.49 PFLOP/s; 64 heads, a chunk of 2048 behind
+// cached keys, 30001 in all, 1.55 ms, 1.34 PFLOP/s.  At few rows the bytes: 2400 cycles
+// a tile of 32 KB of codes, 3.3 TB/s; the widening's chain (copies, loads, stores,
+// hand-over), the weights' and the copies' latency each take a part of it, and leaving
+// any one out saves 3 to 15 %.
+//
 // Warps: 0-7 the softmax, a warpgroup a stream; a thread owns a row and all of its
 // scores, 128 in registers.  (Two threads a row, 64 scores each, took 3600 cycles a
 // tile of two row tiles, this form 3300 in its place and 3100 with the steps since: the

@@ -1,5 +1,6 @@
 """Host side of the INT8 cache's operators: refusals, before any CUDA call."""
 import ctypes
+import os
 
 import numpy as np
 import pytest
@@ -21,8 +22,6 @@ def _decode(**kw):
              o=P(256), lse=P(256), ws=P(256), wsb=1 << 30)
     a.update(kw)
     return fd.lib().fd_decode_paged_int8(*a.values(), None)
-
-
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -127,3 +126,12 @@ def test_prefill_refuses_plans_that_do_not_hold_together(field, value, code):
 def test_prefill_of_nothing_is_nothing():
     assert fd.lib().fd_prefill_paged_int8(None, *[0] * 1, *[None] * 5, 0, *[None] * 4, 0.1, *[None] * 3, 0, None) == -1
     assert _prefill(_plan_prefill(qi=[0, 0, 0])[1], q=None, o=None) == 0
+
+
+@pytest.mark.parametrize("name", ["prefill_kernel.cu", "tc_stream.cuh"])
+def test_no_load_past_the_coherent_path(name):
+    """The kernels start while the grid before them may still write their inputs."""
+    source = open(os.path.join(os.path.dirname(fd.__file__), "csrc", name)).read()
+    code = "\n".join(line.split("//")[0] for line in source.splitlines())
+    for word in ("__ldg", "ld.global.nc", "__restrict__"):
+        assert word not in code, word
