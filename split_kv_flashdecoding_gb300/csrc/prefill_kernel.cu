@@ -25,7 +25,7 @@
 // with 128 keys), one chain of scores, weights and products a stream beside it: 3100
 // cycles.  32 heads, 8192 queries and keys 432 us, 1.27 PFLOP/s, of which an item's start
 // and end (queries 3.7 us, first weights 3.6, output 2.6, with nothing beside them) are
-// a sixth; 32768 queries and keys 5.9 ms, 1.49 PFLOP/s; 64 heads, a chunk of 2048 behind
+// a sixth; 32768 queries and keys 5.9 ms, 1.49 PFLOP/s; 64 heads, a chunk of 2047 behind
 // cached keys, 30001 in all, 1.55 ms, 1.34 PFLOP/s.  At few rows the bytes: 2400 cycles
 // a tile of 32 KB of codes, 3.3 TB/s; the widening's chain (copies, loads, stores,
 // hand-over), the weights' and the copies' latency each take a part of it, and leaving

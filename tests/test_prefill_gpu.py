@@ -2,9 +2,9 @@
 that codes and page scales stand for.
 
 Tolerances, per value of O: half a step of bf16 (2^-8 of it), and for the softmax
-weights w_j, each rounded to f16 once (2^-11 of it at most; below 2^-14 of the row's
-reference, which is within 2^4 of the row's largest weight, by 2^-24 of it at most)
-and off by up to 2e-5 through the rounding of their fp32 logits (30 * 4 * 2^-24, twice):
+weights w_j, each rounded to f16 once (2^-11 of it at most; one below 2^-15 of the
+row's reference by 2^-26 of that at most, where the row's sum is at least the
+reference: 2^-19 covers 128 such keys' errors of one sign) and off by up to 2e-5 through the rounding of their fp32 logits (30 * 4 * 2^-24, twice):
 (2^-11 + 2^-15) A + 2^-19 max|v| with A = sum_j w_j |v_j|.  LSE is fp32: 2e-5, as for
 single tokens, where a row's logits are below 30 or so."""
 import math
