@@ -598,11 +598,11 @@ def scale_heads(num_kv_heads: int) -> int:
 
 def _int8_cache(name, k_pages, v_pages, k_scale, v_scale, num_kv_heads, head_dim, dev):
     """Addresses of an INT8 cache's pools and scales, checked against one another."""
-    if k_pages.dim() != 4 or k_pages.shape != v_pages.shape or \
-            k_pages.shape[2:] != (num_kv_heads, head_dim):
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape or shape[2] != num_kv_heads or shape[3] != head_dim:
         raise FdError(-1, f"{name}: pools of another shape")
-    shape = (k_pages.shape[0], scale_heads(num_kv_heads))
-    if k_scale.shape != shape or v_scale.shape != shape:
+    rows = (shape[0], scale_heads(num_kv_heads))
+    if k_scale.shape != rows or v_scale.shape != rows:
         raise FdError(-1, f"{name}: scales must be [num_pages, num_kv_heads rounded up to a multiple of 4]")
     return (_need("k_pages", k_pages, torch.int8, dev), _need("v_pages", v_pages, torch.int8, dev),
             _need("k_scale", k_scale, torch.float32, dev), _need("v_scale", v_scale, torch.float32, dev))
@@ -614,8 +614,10 @@ def decode_paged_int8(q, k_pages_int8, v_pages_int8, k_scale, v_scale, kv_page_i
                       stream=None):
     """fd_decode_paged_int8: fd_decode_paged over int8 page pools
     [num_pages, page_size, Hkv, D] with fp32 scales [num_pages, scale_heads(Hkv)]."""
-    B, Hq, D = q.shape
-    num_pages, page_size, Hkv = k_pages_int8.shape[:3]
+    shape, pool = q.shape, k_pages_int8.shape
+    if len(shape) != 3 or len(pool) != 4:
+        raise FdError(-1, "fd_decode_paged_int8: q must be [batch, num_qo_heads, head_dim], pools of four dimensions")
+    (B, Hq, D), (num_pages, page_size, Hkv, _) = shape, pool
     ip, ll = _host_indptr(kv_page_indptr_host), _host_indptr(kv_last_page_len_host)
     if ip.size != B + 1 or ll.size != B or kv_page_indptr_dev.numel() != B + 1 or \
             kv_last_page_len_dev.numel() < B or kv_page_indices_dev.numel() < ip[B]:
@@ -626,7 +628,7 @@ def decode_paged_int8(q, k_pages_int8, v_pages_int8, k_scale, v_scale, kv_page_i
             o = torch.empty((B, Hq, D), dtype=f32, device=q.device)
         if lse is None:
             lse = torch.empty((B, Hq), dtype=f32, device=q.device)
-        if o.shape != q.shape or lse.shape != q.shape[:2]:
+        if o.shape != shape or lse.shape != (B, Hq):
             raise FdError(-1, "fd_decode_paged_int8: o must have q's shape and lse [batch, num_qo_heads]")
         if workspace is None:
             need = plan_paged(B, Hq, Hkv, D, page_size, ip, ll).workspace_bytes
@@ -863,6 +865,8 @@ def copy_pages(pools, src, dst, *, workspace=None, stream=None):
 
 
 def _host_ptr(a):
+    if a.size and a.flags.writeable:   # (a.ctypes builds an object that holds the array: 0.8 us of a call)
+        return ctypes.addressof(ctypes.c_char.from_buffer(a))
     return a.ctypes.data
 
 
