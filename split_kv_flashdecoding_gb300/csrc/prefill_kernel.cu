@@ -717,6 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const int valid = sees - t * kPrefillTile;
                 tcgen05_fence_after();
                 if (i == 0 || careful) {   // E from this tile's own scores
+                    const bool all = __all_sync(0xffffffffu, valid >= kPrefillTile);
 #pragma unroll 1
                     for (int c0 = 0; c0 < kGroups; c0 += 4) {
                         uint32_t x[64];
@@ -728,9 +729,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
                             float mt = -INFINITY;
+                            if (all) {
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                mt = fmaxf(mt, 16 * (c0 + c) + j < valid ? __uint_as_float(x[16 * c + j]) : -INFINITY);
+                                for (int j = 0; j < 16; ++j)
+                                    mt = fmaxf(mt, __uint_as_float(x[16 * c + j]));
+                            } else {
+#pragma unroll
+                                for (int j = 0; j < 16; ++j)
+                                    mt = fmaxf(mt, 16 * (c0 + c) + j < valid ? __uint_as_float(x[16 * c + j]) : -INFINITY);
+                            }
                             const float4 g = group[c0 + c];
                             most = fmaxf(most, fmaf(mt, c2 * g.x, g.y));
                         }
