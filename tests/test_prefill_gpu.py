@@ -250,6 +250,49 @@ def test_prefill_is_the_same_each_time_and_replayed(cuda_device):
     assert fd.get_device_status(ws) == 0
 
 
+def test_prefill_of_many_requests(cuda_device):
+    # more requests than a warp looks at at once, some without tokens, keys or both; in
+    # splits of 128 keys those of 129 on have partial rows
+    rng = np.random.RandomState(5)
+    tokens, keys = rng.randint(0, 4, 700), rng.randint(0, 300, 700)
+    keys[rng.rand(700) < 0.1] = 0
+    t, c, q, qi = make("many", 4, 2, list(tokens), list(keys), 16, cuda_device)
+    for causal in (True, False):
+        for chunk in (0, 128):
+            plan = plan_of(t, q, 2, qi, causal, chunk=chunk)
+            compare(run(t, c, q, qi, causal, plan=plan), t, c, q, qi, causal, what=f"{causal} {chunk}")
+
+
+def test_prefill_calls_at_once(cuda_device):
+    """Calls of other plans, and single tokens, on three streams, a workspace each."""
+    sets = [make("one", 32, 8, [300, 70], [3000, 2000], 32, cuda_device),
+            make("other", 16, 16, [40, 1, 7], [700, 5000, 90], 48, cuda_device)]
+    tab = [dev_tables(x[0], cuda_device) + [torch.from_numpy(x[3]).to(cuda_device)] for x in sets]
+    plans = [plan_of(x[0], x[2], x[1]["k"].shape[2], x[3], True) for x in sets]
+    want = [run(*x, True, plan=p) for x, p in zip(sets, plans)]
+    t, c = sets[0][:2]
+    q1 = sets[0][2][:2].contiguous()
+    single = fd.decode_paged_int8(q1, c["k"], c["v"], c["ks"], c["vs"], t["ip"], t["last"], *tab[0][:3], D ** -0.5)
+    ws = [torch.zeros(p.workspace_bytes, dtype=torch.uint8, device=cuda_device) for p in plans]
+    ws.append(torch.zeros(fd.plan_paged(2, 32, 8, D, 32, t["ip"], t["last"]).workspace_bytes, dtype=torch.uint8,
+                          device=cuda_device))
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for (t, c, q, _), p, w, s, tb in zip(sets, plans, ws, streams, tab):
+            got.append(fd.prefill_paged_int8(p, q, c["k"], c["v"], c["ks"], c["vs"], tb[3], *tb[:3], D ** -0.5, workspace=w,
+                                             stream=s))
+        t, c = sets[0][:2]
+        got.append(fd.decode_paged_int8(q1, c["k"], c["v"], c["ks"], c["vs"], t["ip"], t["last"], *tab[0][:3], D ** -0.5,
+                                        workspace=ws[2], stream=streams[2]))
+    torch.cuda.synchronize()
+    for n, (o, lse) in enumerate(got):
+        w = (want + [single])[n % 3]
+        assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+    assert all(fd.get_device_status(w) == 0 for w in ws)
+
+
 def test_prefill_far_rows_of_a_large_pool(cuda_device):
     page, hkv, pages, dev = 16, 8, 300000, cuda_device   # 4.9e9 bytes a pool
     rng = np.random.RandomState(8)
