@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                     for (int k = 0; k < kOfTile; ++k) {
                         const int rr = k * kRowsOnce + (tid >> 4);
-                        const int sh = min(max(9 + 126 - (int)(most[k] >> 23), -100), 100);
+                        const int sh = min(max(9 + 126 - (int)(most[k] >> 23), -119), 126);   // 2^-sh, too, is normal
                         const float up = __int_as_float((127 + sh) << 23);
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {

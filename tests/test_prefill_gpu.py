@@ -250,6 +250,16 @@ def test_prefill_is_the_same_each_time_and_replayed(cuda_device):
     assert fd.get_device_status(ws) == 0
 
 
+@pytest.mark.parametrize("log2", [118, 60, -60, -105])
+def test_prefill_queries_of_any_size(cuda_device, log2):
+    # bf16 reaches beyond f16 on both sides; the factor of the scores brings these back
+    t, c, q, qi = make("sizes", 8, 2, [70, 3], [300, 200], 16, cuda_device)
+    big = (q.double() * 2.0 ** log2).to(torch.bfloat16)
+    assert torch.equal(big.double(), q.double() * 2.0 ** log2)
+    got = run(t, c, big, qi, True, scale=D ** -0.5 * 2.0 ** -log2)
+    compare(got, t, c, q, qi, True, what=str(log2))
+
+
 def test_prefill_of_many_requests(cuda_device):
     # more requests than a warp looks at at once, some without tokens, keys or both; in
     # splits of 128 keys those of 129 on have partial rows
