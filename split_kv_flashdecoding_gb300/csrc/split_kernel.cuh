@@ -1143,7 +1143,7 @@ __device__ __forceinline__ float load_q(const uint16_t *qrows, int lane, uint32_
         if (amax > 0.f) {
             int e;
             frexpf(amax, &e);   // amax in [2^(e-1), 2^e)
-            sh = min(max(9 - e, -100), 100);
+            sh = min(max(9 - e, -119), 126);   // of every bf16; 2^-sh, too, is normal
         }
         const float up = __int_as_float((127 + sh) << 23);   // 2^sh, exact
 #pragma unroll

@@ -129,6 +129,17 @@ def test_int8_no_number_is_nan_whatever_the_codes(cuda_device, which, value, sig
     assert bool(o.isnan().all()) and (which == "vs" or bool(lse.isnan().all()))
 
 
+@pytest.mark.parametrize("log2", [118, 60, -60, -105])
+@pytest.mark.parametrize("hq", [4, 32])
+def test_int8_queries_of_any_size(cuda_device, hq, log2):
+    # bf16 reaches beyond f16 on both sides; the factor of the scores brings these back
+    t, c, q = make("sizes", hq, 4, [300, 20], 32, "quantised", cuda_device)
+    big = (q.double() * 2.0 ** log2).to(torch.bfloat16)
+    assert torch.equal(big.double(), q.double() * 2.0 ** log2)
+    got = run(t, c, big, scale=D ** -0.5 * 2.0 ** -log2)
+    compare(got, attention(q, t, c, D ** -0.5), str(log2))
+
+
 def test_int8_pages_outside_the_pool_are_flagged(cuda_device):
     t, c, q = make("bad", 8, 8, [100], 16, "random", cuda_device)
     need = fd.plan_paged(1, 8, 8, D, 16, t["ip"], t["last"]).workspace_bytes
