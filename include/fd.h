@@ -572,7 +572,7 @@ int fd_decode_shared_paged_fp8(const fd_shared_plan *plan, int num_pages,
  * Scores and sums are fp32; a softmax weight is rounded once, to f16 (2^-11 of it at
  * most), O once, to bf16.  Scales as fd_append_paged_int8 leaves them, not below 0: one
  * that is, and one of NaN or +-inf, makes what attends its page NaN; V scales less than
- * 2^-40 of those near the split's first keys count as that.
+ * 2^-40 of those near the split's first keys, or more than 2^100, count as that.
  *
  * The plan is made once on the host for the tokens and tables and a call takes device
  * data only, makes no host-synchronising call and may be captured in a CUDA graph; the

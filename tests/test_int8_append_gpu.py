@@ -115,6 +115,27 @@ def test_append_int8_matches_64_bits(cuda_device, name, cached, new, hq, hkv, pa
         assert np.array_equal(codes[untouched], before[part][untouched])
 
 
+@pytest.mark.parametrize("log2", [100, 30, -30, -100])
+def test_append_int8_values_of_any_size(cuda_device, log2):
+    cached, new, hkv, page = [5, 0, 40], [20, 70, 1], 4, 32
+    i = make(cached, new, 4, hkv, page, seed=3)
+    i["qkv"] *= np.float32(2.0 ** log2)
+    t, tables = to_dev(i, cuda_device)
+    rng = np.random.RandomState(7)
+    c = pools(i, rng, cuda_device)
+    before = {x: c[x].cpu().numpy() for x in c}
+    info = fd.plan_rope(D, 128)
+    call(t, c, tables, rope=info)
+    x = {k: v.double().cpu().numpy() for k, v in t.items()}
+    for part in ("k", "v"):
+        y, mag = rotated(x["k"], i["key"], 128, False, 10000.0, None) if part == "k" else (x["v"], np.abs(x["v"]))
+        val, tol, s, st = expected(i, cached, new, before[part], before[part + "s"], y, mag)
+        got_s = c[part + "s"].double().cpu().numpy()
+        assert np.all(np.abs(got_s - s) <= st)
+        got = c[part].cpu().numpy().astype(np.float64) * got_s[:, None, :hkv, None]
+        assert np.all(np.abs(got - val) <= tol)
+
+
 def test_append_int8_without_queries_or_rotation_uses_key_positions(cuda_device):
     i = make([5, 40], [20, 3], 8, 4, 16, seed=2)
     t, tables = to_dev(i, cuda_device)
