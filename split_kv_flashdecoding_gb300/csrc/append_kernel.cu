@@ -408,9 +408,10 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
 // Bound: bytes, as above.  A warp holds 16 rows of a head (8 lanes a row, 16 values
 // each) in registers, from the maximum to the codes, when the page has no more new
 // keys than its warps hold; else it reads them a second time, out of L2.  A kernel a
-// rotary layout: with both in one the warps waited for instructions (12345 tokens 64.0
-// us for 62.2).  Measured: 32768 tokens of 32 + 8 + 8 heads 148.5 us, 5.0 TB/s, of which
-// the page blocks alone take 91; 64 tokens 5.0 us, the chain.
+// rotary layout, and no divisions beside the quotients of pack8_int8: with both in one the
+// warps waited for instructions (12345 tokens 64.0 us for 62.2, then 58.8).  Measured:
+// 32768 tokens of 32 + 8 + 8 heads 143.6 us, 5.1 TB/s, of which the page blocks alone take
+// 81; 64 tokens 4.75 us, the chain.
 constexpr int kPageWarps = kThreads / 32;
 constexpr int kAngleRows = 64;     // tokens of a page whose angles are in shared memory at once
 constexpr int kGroupRows = 16;     // rows that a warp holds
@@ -522,9 +523,10 @@ __device__ __forceinline__ float max_or_nan(float a, float b)
 // Eight values over a scale (quotients of at most 127 in magnitude), rounded to whole
 // numbers, as bytes.  The quotient is rounded to fp32 as a division would (a step of
 // Markstein's, as in pack4_over: many values of a page are half-way between codes, its
-// largest being 127), then 1.5 * 2^23 + y has rint(y) in its low bits.  plain: the
-// scale is far from the ends of fp32's range.
-__device__ __forceinline__ uint2 pack8_int8(const float (&x)[8], float scale, float inv, bool plain)
+// largest being 127), then 1.5 * 2^23 + y has rint(y) in its low bits.  up: 1, or for a
+// scale near the ends of fp32's range the power of two that the caller has put into
+// `scale` (a value that it takes below fp32's range has the code 0 either way).
+__device__ __forceinline__ uint2 pack8_int8(const float (&x)[8], float scale, float inv, float up)
 {
     const float2 inv2 = make_float2(inv, inv), minus = make_float2(-scale, -scale);
     const float2 magic = make_float2(12582912.f, 12582912.f);
@@ -534,13 +536,11 @@ __device__ __forceinline__ uint2 pack8_int8(const float (&x)[8], float scale, fl
         float2 y[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const float2 v = make_float2(x[4 * i + 2 * j], x[4 * i + 2 * j + 1]);
-            if (plain) {
-                y[j] = mul2(v, inv2);
-                y[j] = fma2(fma2(y[j], minus, v), inv2, y[j]);
-            } else {
-                y[j] = make_float2(__fdiv_rn(v.x, scale), __fdiv_rn(v.y, scale));
-            }
+            float2 v = make_float2(x[4 * i + 2 * j], x[4 * i + 2 * j + 1]);
+            if (up != 1.f)
+                v = mul2(v, make_float2(up, up));
+            y[j] = mul2(v, inv2);
+            y[j] = fma2(fma2(y[j], minus, v), inv2, y[j]);
             y[j] = add2(y[j], magic);
         }
         w[i] = __byte_perm(__byte_perm(__float_as_uint(y[0].x), __float_as_uint(y[0].y), 0x0040),
@@ -681,8 +681,9 @@ __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_c
         }
         const float s = max_or_nan(s0, max_or_nan(__fdiv_rn(__uint_as_float(bits), 127.f), kSmallestScale));
         // a page whose scale is no number has the codes 0: its values are NaN
-        const bool number = s < INFINITY, plain = s > 1e-15f && s < 1e15f;
-        const float inv = __fdiv_rn(1.f, s);
+        const bool number = s < INFINITY;
+        const float up = s > 1e-15f && s < 1e15f ? 1.f : s < 1.f ? 0x1p100f : 0x1p-100f;
+        const float s_up = s * up, inv = __fdiv_rn(1.f, s_up);
         if (mine && work.place > 0 && s != s0) {
             const float r = number ? __fdiv_rn(s0, s) : 0.f;
 #pragma unroll 1
@@ -700,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_c
                 const int r = g * kGroupRows + 4 * i + row4;
                 float a[8], b[8];
                 unit(i, r, from, a, b);
-                uint2 x = pack8_int8(a, s, inv, plain), y = pack8_int8(b, s, inv, plain);
+                uint2 x = pack8_int8(a, s_up, inv, up), y = pack8_int8(b, s_up, inv, up);
                 if (!number)
                     x = y = make_uint2(0u, 0u);
                 if (mine && r < n) {
