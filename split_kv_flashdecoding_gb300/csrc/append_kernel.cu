@@ -405,17 +405,16 @@ __global__ void __launch_bounds__(kThreads, 4) append_kernel(const __grid_consta
 // grows while its page fills, so a code is carried over at most as often as a key
 // with a new largest value arrives (about 1/(f + 1) of single-token steps).
 //
-// Bound: bytes, as above.  A warp holds 16 rows of a head (8 lanes a row, 16 values
+// Bound: bytes, as above.  A warp holds 16 or 4 rows of a head (8 lanes a row, 16 values
 // each) in registers, from the maximum to the codes, when the page has no more new
 // keys than its warps hold; else it reads them a second time, out of L2.  A kernel a
 // rotary layout, and no divisions beside the quotients of pack8_int8: with both in one the
 // warps waited for instructions (12345 tokens 64.0 us for 62.2, then 58.8).  Measured:
-// 32768 tokens of 32 + 8 + 8 heads 143.6 us, 5.1 TB/s, of which the page blocks alone take
-// 81; 64 tokens 4.75 us, the chain.
+// 32768 tokens of 32 + 8 + 8 heads 139.8 us, 5.3 TB/s, of which the page blocks alone take
+// 74; 64 tokens 4.4 us, the chain.
 constexpr int kPageWarps = kThreads / 32;
 constexpr int kAngleRows = 64;     // tokens of a page whose angles are in shared memory at once
-constexpr int kGroupRows = 16;     // rows that a warp holds
-constexpr int kMostWarpsPerHead = kAngleRows / kGroupRows;
+constexpr int kFewRows = 4, kManyRows = 16;   // rows that a warp holds
 constexpr float kSmallestScale = 1.17549435e-38f;
 
 struct PageWork {
@@ -562,29 +561,34 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r)
     return out;
 }
 
-// Blocks: for each page with new keys, the steps of its heads, K's then V's, shared by
-// blocks_per_page of them (a step: a head for every warps_per_head warps, which share
-// its rows); then the queries'.
-template <bool kInterleaved>
-__global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_constant__ AppendParams p)
+// Warps a head: as many as hold a page's new rows in registers, and for few heads as
+// many as there are; no more than hold the rows that have their angles in shared
+// memory at once.
+__host__ __device__ __forceinline__ int warps_per_head(int64_t rows, int num_kv_heads)
 {
-    __shared__ __align__(16) float2 s_cs[kAngleRows][kHeadDim / 2];
-    __shared__ PageWork s_work;
-    __shared__ int s_scan[kPageWarps];
-    __shared__ uint32_t s_max[2][kPageWarps];
+    const int group = rows <= kFewRows ? kFewRows : kManyRows;
+    const int most = kAngleRows / group < kPageWarps ? kAngleRows / group : kPageWarps;
+    int wph = 1;
+    while (wph < most && (wph * group < rows || kPageWarps / wph / 2 >= num_kv_heads))
+        wph *= 2;
+    return wph;
+}
 
-    if (blockIdx.x >= p.page_ctas * p.blocks_per_page) {
-        append_tokens<kKvTypeInt8>(p, blockIdx.x - p.page_ctas * p.blocks_per_page);
-        return;
-    }
-    griddep_wait();
-    griddep_launch_dependents();
-    find_page(p, blockIdx.x / p.blocks_per_page, s_work, s_scan);
-    if (s_work.page < 0)
-        return;
-    const PageWork work = s_work;
+struct PageSmem {
+    float2 cs[kAngleRows][kHeadDim / 2];   // (cos, sin) of the rows' angles
+    PageWork work;
+    int scan[kPageWarps];
+    uint32_t most[2][kPageWarps];
+};
+
+// The new keys of one page, for part `at` of its heads, K's then V's: a step is a head
+// for every `wph` warps, which share its rows, kGroupRows a warp at once.
+template <bool kInterleaved, int kGroupRows>
+__device__ __forceinline__ void append_page(const AppendParams &p, PageSmem &sm, const PageWork work, int wph, int at)
+{
+    constexpr int kAngleGroups = kAngleRows / kGroupRows;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int wph = p.warps_per_head, part = warp % wph;
+    const int part = warp % wph;
     const int steps = (p.num_kv_heads * wph + kPageWarps - 1) / kPageWarps;   // of K, and of V
     const int u = lane & 7, row4 = lane >> 3;
     const int rot = p.rope.rotary_dim, pairs = rot / 2;
@@ -600,10 +604,9 @@ __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_c
         const int j = tid & (kHeadDim / 2 - 1);
         if (j < pairs)
             for (int r = from + tid / (kHeadDim / 2); r < min(n, from + kAngleRows); r += kThreads / (kHeadDim / 2))
-                put_angle(p.rope, p.positions ? p.positions[work.token + r] : work.key + r, j, s_cs[r - from]);
+                put_angle(p.rope, p.positions ? p.positions[work.token + r] : work.key + r, j, sm.cs[r - from]);
     };
     int have_angles = -1;   // the first row of those in shared memory
-    const int at = blockIdx.x % p.blocks_per_page;
     const int first = 2 * steps * at / p.blocks_per_page, last = 2 * steps * (at + 1) / p.blocks_per_page;
 #pragma unroll 1
     for (int it = first; it < last; ++it) {
@@ -612,14 +615,12 @@ __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_c
         const bool mine = head < p.num_kv_heads;
         const int64_t stride = is_v ? p.v_stride : p.k_stride;
         const uint16_t *src = (is_v ? p.v : p.k) + work.token * stride + (mine ? head : 0) * kHeadDim;
-        float *scales = (is_v ? p.v_scale_out : p.k_scale_out) + (int64_t)work.page * p.scale_heads + (mine ? head : 0);
-        uint8_t *rows = static_cast<uint8_t *>(is_v ? p.v_pages : p.k_pages) +
-                        ((int64_t)work.page * p.page_size * p.num_kv_heads + (mine ? head : 0)) * kHeadDim;
+        float *const scales = (is_v ? p.v_scale_out : p.k_scale_out) + (int64_t)work.page * p.scale_heads + (mine ? head : 0);
         const bool rotate = !is_v && rot > 0;
-        uint4 raw[4][2];   // rows 4 i + row4 of a group
+        uint4 raw[kGroupRows / 4][2];   // rows 4 i + row4 of a group
         auto load = [&](int g) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kGroupRows / 4; ++i) {
                 const int r = g * kGroupRows + 4 * i + row4;
                 raw[i][0] = raw[i][1] = make_uint4(0u, 0u, 0u, 0u);
                 if (mine && r < n) {
@@ -631,7 +632,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_c
         // Groups part, part + wph, ..; K's angles are there for 64 rows at a time.
         auto each_group = [&](auto &&work_on) {
 #pragma unroll 1
-            for (int g0 = 0; g0 < groups; g0 += kMostWarpsPerHead) {
+            for (int g0 = 0; g0 < groups; g0 += kAngleGroups) {
                 const int from = g0 * kGroupRows;
                 if (rotate && have_angles != from) {
                     __syncthreads();   // the others are done with those before
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_c
                     have_angles = from;
                 }
 #pragma unroll 1
-                for (int g = g0 + part; g < min(groups, g0 + kMostWarpsPerHead); g += wph) {
+                for (int g = g0 + part; g < min(groups, g0 + kAngleGroups); g += wph) {
                     if (!held)
                         load(g);
                     work_on(g, from);
@@ -651,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_c
             unpack8(raw[i][0], a);
             unpack8(raw[i][1], b);
             if (rotate && turns0 && r < n)
-                turn_unit(a, b, s_cs[r - from], c0, c1, turns1, kInterleaved);
+                turn_unit(a, b, sm.cs[r - from], c0, c1, turns1, kInterleaved);
         };
         if (held)
             load(part);
@@ -659,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_c
         uint32_t bits = 0;
         each_group([&](int g, int from) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kGroupRows / 4; ++i) {
                 if (g * kGroupRows + 4 * i >= n)   // (a step's page has one row)
                     break;
                 if (is_v) {
@@ -674,16 +675,20 @@ __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_c
         bits = __reduce_max_sync(0xffffffffu, bits);
         if (wph > 1) {
             if (lane == 0)
-                s_max[it & 1][warp] = bits;
+                sm.most[it & 1][warp] = bits;
             __syncthreads();
             for (int w = 0; w < wph; ++w)
-                bits = max(bits, s_max[it & 1][warp - part + w]);
+                bits = max(bits, sm.most[it & 1][warp - part + w]);
         }
         const float s = max_or_nan(s0, max_or_nan(__fdiv_rn(__uint_as_float(bits), 127.f), kSmallestScale));
         // a page whose scale is no number has the codes 0: its values are NaN
         const bool number = s < INFINITY;
         const float up = s > 1e-15f && s < 1e15f ? 1.f : s < 1.f ? 0x1p100f : 0x1p-100f;
         const float s_up = s * up, inv = __fdiv_rn(1.f, s_up);
+        if (mine && part == 0 && lane == 0)
+            *scales = s;   // (all have read s0: the exchange of the maxima)
+        uint8_t *const rows = static_cast<uint8_t *>(is_v ? p.v_pages : p.k_pages) +
+                              ((int64_t)work.page * p.page_size * p.num_kv_heads + (mine ? head : 0)) * kHeadDim;
         if (mine && work.place > 0 && s != s0) {
             const float r = number ? __fdiv_rn(s0, s) : 0.f;
 #pragma unroll 1
@@ -695,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_c
         }
         each_group([&](int g, int from) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kGroupRows / 4; ++i) {
                 if (g * kGroupRows + 4 * i >= n)
                     break;
                 const int r = g * kGroupRows + 4 * i + row4;
@@ -711,9 +716,32 @@ __global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_c
                 }
             }
         });
-        if (mine && part == 0 && lane == 0)
-            *scales = s;
     }
+}
+
+// Blocks: blocks_per_page for each page with new keys, then the queries'.
+template <bool kInterleaved>
+__global__ void __launch_bounds__(kThreads, 3) append_int8_kernel(const __grid_constant__ AppendParams p)
+{
+    __shared__ __align__(16) PageSmem sm;
+    const int block = blockIdx.x, page_blocks = p.page_ctas * p.blocks_per_page;
+    if (block >= page_blocks) {
+        append_tokens<kKvTypeInt8>(p, block - page_blocks);
+        return;
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+    find_page(p, block / p.blocks_per_page, sm.work, sm.scan);
+    if (sm.work.page < 0)
+        return;
+    // Up to four rows (a step's, drafted tokens'): code and registers for no more, 64
+    // tokens 4.4 us for 4.95 and 256 of 64 + 8 + 8 heads 7.0 for 7.9.
+    const PageWork work = sm.work;
+    const int at = block % p.blocks_per_page;
+    if (work.rows <= kFewRows)
+        append_page<kInterleaved, kFewRows>(p, sm, work, warps_per_head(work.rows, p.num_kv_heads), at);
+    else
+        append_page<kInterleaved, kManyRows>(p, sm, work, warps_per_head(work.rows, p.num_kv_heads), at);
 }
 
 }  // namespace
@@ -726,15 +754,8 @@ cudaError_t launch_append_int8(const AppendParams &params, cudaStream_t stream)
     const int64_t some = p.batch < p.num_tokens ? p.batch : p.num_tokens;
     const int64_t pages = p.num_tokens / p.page_size + 2 * some;
     p.page_ctas = (int32_t)(pages < p.num_tokens ? pages : p.num_tokens);
-    // Warps a head: as many as hold a page's new rows (of which a step's are one or
-    // two) in registers, and for few heads as many as there are; up to four, which
-    // hold the rows that have their angles in shared memory at once.
     const int64_t rows = (p.num_tokens + p.page_ctas - 1) / p.page_ctas;
-    p.warps_per_head = 1;
-    while (p.warps_per_head < kMostWarpsPerHead &&
-           (p.warps_per_head * kGroupRows < rows || kPageWarps / p.warps_per_head / 2 >= p.num_kv_heads))
-        p.warps_per_head *= 2;
-    const int steps = 2 * ((p.num_kv_heads * p.warps_per_head + kPageWarps - 1) / kPageWarps);
+    const int steps = 2 * ((p.num_kv_heads * warps_per_head(rows, p.num_kv_heads) + kPageWarps - 1) / kPageWarps);
     // Blocks a page: one (its angles are computed once) where that fills the SMs
     // twice, more for fewer pages and for those whose rows are read twice.
     const int64_t fill = 152 * 2, want = rows > kAngleRows ? 4 * fill : fill;
@@ -747,8 +768,8 @@ cudaError_t launch_append_int8(const AppendParams &params, cudaStream_t stream)
     const int64_t grid = (int64_t)p.page_ctas * p.blocks_per_page + q_ctas;
     if (grid > INT32_MAX)
         return cudaErrorInvalidValue;
-    return launch_dependent(p.rope.interleaved ? append_int8_kernel<true> : append_int8_kernel<false>,
-                            dim3((unsigned)grid), kThreads, 0, stream, p);
+    const auto kernel = p.rope.interleaved ? append_int8_kernel<true> : append_int8_kernel<false>;
+    return launch_dependent(kernel, dim3((unsigned)grid), kThreads, 0, stream, p);
 }
 
 cudaError_t launch_append(const AppendParams &params, int kv_type, cudaStream_t stream)

@@ -23,7 +23,7 @@ struct AppendParams {
     int *status;
     int32_t batch, num_tokens, num_qo_heads, num_kv_heads, page_size, num_pages, num_page_entries;
     int32_t tokens_per_cta;
-    int32_t scale_heads, page_ctas, blocks_per_page, warps_per_head;   // INT8
+    int32_t scale_heads, page_ctas, blocks_per_page;   // INT8
     fd_rope_info rope;           // rotary_dim 0: no rotation
 };
 
