@@ -27,6 +27,8 @@ SHAPES = [
     ("many_heads", [9, 40], [100, 7], 20, 20, 128),
     ("large_pages", [0, 1000, 5], [2500, 300, 1], 8, 4, 1024),
     ("large_pages_one_head", [600], [700], 1, 1, 1024),
+    ("mixed", [5, 0, 31, 100, 62, 7], [1, 300, 3, 70, 4, 5], 32, 8, 64),
+    ("few_rows_one_head", [14, 0, 3], [4, 3, 2], 2, 1, 16),
     ("one_head_pages_of_128", [0, 30], [300, 90], 4, 1, 128),
 ]
 
