@@ -569,10 +569,15 @@ int fd_decode_shared_paged_fp8(const fd_shared_plan *plan, int num_pages,
  * L_b.  A token that sees no key (none there, or causal with T > L_b) gets O = 0,
  * LSE = -inf.  Rows of q and o from q_indptr[B] on are not touched.
  *
- * Scores and sums are fp32; a softmax weight is rounded once, to f16 (2^-11 of it at
- * most), O once, to bf16.  Scales as fd_append_paged_int8 leaves them, not below 0: one
- * that is, and one of NaN or +-inf, makes what attends its page NaN; V scales less than
- * 2^-40 of those near the split's first keys, or more than 2^100, count as that.
+ * Scores and sums are fp32; a softmax weight is rounded once, to f16, O once, to bf16.
+ * The first is off by 2^-11 of the weight or, when that is more, by 2^-26 of the largest
+ * sum of weights over 128 keys of the split before it; a few times 128 keys further on,
+ * when all of these had far smaller sums, by 2^-35 of that.  (Beside a key that takes 99 %
+ * of a row's weight and has V = 0, O is within 0.5 % of its norm for 30000 keys.)
+ *
+ * Scales as fd_append_paged_int8 leaves them, not below 0: one that is, and one of NaN or
+ * +-inf, makes what attends its page NaN; V scales less than 2^-40 of those near the
+ * split's first keys, or more than 2^100, count as that.
  *
  * The plan is made once on the host for the tokens and tables and a call takes device
  * data only, makes no host-synchronising call and may be captured in a CUDA graph; the

@@ -46,6 +46,15 @@
 // its own maximum.  A score so far above all before it that its weight is over
 // f16's range is seen at the end, and the CTA then does its item again with the
 // maximum of every step before its weights.
+//
+// E goes down, too, when the tiles since the largest have stayed far below it: a key
+// that takes nearly all of a row's weight, its V near 0, would otherwise push the
+// others' weights below f16's smallest number, of which O consists (a first key with 99 %
+// of 131072 keys' weight: O off by 9 % of its norm, so 0.2 %).  It waits for some tiles
+// (kFade), because a score 2^15 times E is still in range, and with E at each tile's
+// own level many items of wide-spread scores would be done twice (64 heads, a chunk of
+// 2047 tokens behind 30001 keys: 1545 us with E at the largest, 1560 to 1580 so, 1753
+// without waiting; 2000 with E at the largest and weights 2^6 times larger).
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -80,8 +89,16 @@ static_assert(2 * kSoftmaxRegs + kLoadRegs + kMmaRegs <= kThreads / 128 * kRegs,
 static_assert(kThreads * kRegs <= 65536, "registers of an SM");
 constexpr int kTmemCols = 512;
 constexpr int kStreamCols = 256;                            // S (and P over it) 128, O 128
-constexpr float kRaise = 3.f;                               // log2: what raises E
-constexpr float kBias = 1.f;                                // weights are 2^kBias larger: of small ones' bits
+// In log2.  The tiles' level is that of the last one, or of one before it less kFade a
+// tile since then, and less what the last one is under it, beyond kGap and up to kFall.
+// E follows it, down to kDeep below the largest, when it is more than kRaise above or
+// kLower below E; then E goes another kRaise down.
+constexpr float kRaise = 3.f, kLower = 6.f, kDeep = 10.f;
+constexpr float kFade = 0.25f, kGap = 6.f, kFall = 8.f;
+// Weights are 2^kBias larger than over E: of small ones' bits.  Careful steps, whose
+// weights over E are at most 2^kRaise, have as much as f16 takes.
+constexpr float kBias = 1.f, kCarefulBias = 12.f;
+static_assert(kBias + kDeep + kRaise < 16 && kCarefulBias + kRaise < 16, "a weight of the largest so far is in range");
 constexpr int kOutStride = kHeadDim + 4;                    // floats between rows of the epilogue's staging
 constexpr int kGroups = kPrefillTile / 16;
 constexpr float kLeastV = -40.f, kMostV = 100.f;            // log2 of a V scale over v_ref
@@ -681,15 +698,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             const int token = min((sm->row0 + r_mine) >> p.group_log2, sm->tokens - 1);
             const int sees = ok && p.causal ? min(sm->keys, sm->len - sm->tokens + token + 1 - sm->key0) : sm->keys;
             float ref = -INFINITY, l = 0.f;   // E, and the row's sum
-            float most = -INFINITY;           // what E follows
+            float most = -INFINITY, level = -INFINITY;   // what E follows: the largest, the tiles' level
+            const float bias = careful ? kCarefulBias : kBias;
             bool go = ok;
-            // E raised to `most`, where that is far above it, and O with it.
+            // E to the tiles' level, when it is far from there, and O with it.
             auto follow = [&](bool first) {
-                const bool up = most > ref + kRaise || (ref == -INFINITY && most > ref);
-                if (!__any_sync(0xffffffffu, up))
+                float to = careful ? most : fmaxf(level, most - kDeep);
+                const bool low = to < ref - kLower, far = to > ref + kRaise || low;
+                to = low ? to - kRaise : to;
+                if (!__any_sync(0xffffffffu, far))
                     return;
-                const float f = !up ? 1.f : ref == -INFINITY ? 0.f : ex2(ref - most);
-                ref = up ? most : ref;
+                const float f = !far ? 1.f : ref == -INFINITY ? 0.f : ex2(ref - to);
+                ref = far ? to : ref;
                 l *= f;
                 if (first)
                     return;
@@ -748,7 +768,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
                 for (int c = 0; c < kGroups; ++c)
                     tmem_ld16(s_col + 16 * c, r + 16 * c);
-                const float base = kBias - (ref == -INFINITY ? 0.f : ref);
+                const float base = bias - (ref == -INFINITY ? 0.f : ref);
                 float sum_tile = 0.f;
                 tmem_wait_ld();
                 settle(r);
@@ -799,7 +819,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 publish(1);
                 if (lane == 0 || (lane == 1 && !two))
                     mbar_arrive(smem_addr(&sm->scales_free[t % kScaleSlots]));
-                most = fmaxf(most, __log2f(sum_tile) - base);
+                const float here = __log2f(sum_tile) - base;
+                level = fmaxf(here, level - kFade - fminf(fmaxf(level - here - kGap, 0.f), kFall));
+                most = fmaxf(most, here);
             }
             // ------------------------------------------------------- the output
             for (int x = 0; x < 2; ++x)   // both streams' products are done with the ring
@@ -896,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         }
                     }
                     if (r_mine < sm->rows) {
-                        const float lse = den == 0.f ? -INFINITY : (m + log2f(den) - kBias) * kLn2;
+                        const float lse = den == 0.f ? -INFINITY : (m + log2f(den) - bias) * kLn2;
                         if (partial)
                             p.partial_lse[sm->part_row + row_of(r_mine) * sm->splits] = lse;
                         else if (p.lse)
