@@ -575,9 +575,11 @@ int fd_decode_shared_paged_fp8(const fd_shared_plan *plan, int num_pages,
  * when all of these had far smaller sums, by 2^-35 of that.  (Beside a key that takes 99 %
  * of a row's weight and has V = 0, O is within 0.5 % of its norm for 30000 keys.)
  *
- * Scales as fd_append_paged_int8 leaves them, not below 0: one that is, and one of NaN or
- * +-inf, makes what attends its page NaN; V scales less than 2^-40 of those near the
- * split's first keys, or more than 2^100, count as that.
+ * Scales of any size, as fd_append_paged_int8 leaves them, not below 0: one that is, and
+ * one of NaN or +-inf, makes what attends its page NaN.  V scales of 2^-126 (pages of
+ * values below 2^-119, if not of zeros) may count as up to 2^-60 of the largest of the
+ * split's first 128 keys.  A call takes two to three times as long where V scales are 2^20
+ * of that one or more, or 2^-40 or less, but not 2^-126.
  *
  * The plan is made once on the host for the tokens and tables and a call takes device
  * data only, makes no host-synchronising call and may be captured in a CUDA graph; the

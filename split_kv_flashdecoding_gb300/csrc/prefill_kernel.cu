@@ -9,8 +9,10 @@
 // c = scale log2 e and E near the row's largest e.  So both scales are numbers of a
 // 16-key group of a tile (pages are whole groups): the K scale goes into the factor
 // of the score, the V scale into the addend of the exponent, and the codes go into
-// the products as they are.  V scales count from one near the split's first ones
-// (v_ref), those more than 2^40 below it as 2^-40 of it.
+// the products as they are.  V scales count from the largest of the split's first tile
+// (v_ref).  Where others are 2^20 of it or more, or 2^-40 or less, the CTA does its item a
+// second time with l summed by itself, over the row's largest score: O and l then have
+// references of their own, and no range of scales that one of them cannot hold.
 //
 // Every (request, block of 256 rows, split of the keys, KV head) is one CTA.  The
 // products run on tcgen05 in f16 with their accumulators in tensor memory: two
@@ -101,7 +103,12 @@ constexpr float kBias = 1.f, kCarefulBias = 12.f;
 static_assert(kBias + kDeep + kRaise < 16 && kCarefulBias + kRaise < 16, "a weight of the largest so far is in range");
 constexpr int kOutStride = kHeadDim + 4;                    // floats between rows of the epilogue's staging
 constexpr int kGroups = kPrefillTile / 16;
-constexpr float kLeastV = -40.f, kMostV = 100.f;            // log2 of a V scale over v_ref
+// log2 of a V scale over v_ref in a first pass, and what one of 2^-126, that of a page of
+// zeros, counts as at the least.  A row's sum is of weights over E, divided by the
+// scales: with 128 keys of the largest scale and score E is 2^(kMostV + 7), a key of a page
+// of zeros and the same score 2^-87 of that, and one of 2^-39 of its weight still a number.
+constexpr float kLeastV = -40.f, kMostV = 20.f, kZeroV = -60.f;
+constexpr float kSmallestScale = 1.17549435e-38f;
 
 struct PrefillSmem {
     uint64_t full[kRing], empty[kRing];
@@ -109,15 +116,15 @@ struct PrefillSmem {
     uint64_t s_full[2], p_ready[2][2], o_done[2];
     uint64_t q_ready, drain;
     uint32_t tmem;
-    int abort, redo;
+    int abort, redo, wide;
     // the CTA's item
     int ok, q0, tokens, len, base, kvh, row0, rows, key0, keys, splits, part_row, q_tiles;
-    float v_ref;
+    float v_ref, ref_log;                 // a V scale, and its log2
     float4 scale[kScaleSlots][kGroups];   // a tile's groups: K scale, log2 (V scale / v_ref), v_ref / V scale
     float q_scale[kPrefillRows];          // a row's factor
 };
 struct PrefillEnd {   // at the end, behind the staged rows: stream 1's state, one row tile
-    float row_sum[kTileRows], row_ref[kTileRows];
+    float row_sum[kTileRows], row_ref[kTileRows], row_top[kTileRows];
 };
 // One row tile: stream 1's O [128][kOutStride], the rest of its state, staged rows.
 constexpr int kEndOffset = kTileRows * kOutStride * 4;
@@ -358,7 +365,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         init_barriers(false);
         sm->abort = 0;
         sm->redo = 0;
+        sm->wide = 0;
         sm->v_ref = 1.f;
+        sm->ref_log = 0.f;
     }
     if (warp == kLoadWarp + 1 && blockIdx.x == 0)
         check_tables(p);
@@ -381,11 +390,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
 
     // At most two passes over the item: the second with careful steps, when the
-    // first left f16's range.  The whole CTA, at a pass's end: whether another follows.
-    auto another_pass = [&](int pass) {
+    // first left f16's range or met V scales far from its reference.  The whole CTA, at
+    // the first one's end: whether the second follows.
+    auto another_pass = [&] {
         tcgen05_fence_before();
         __syncthreads();
-        if (pass > 0 || !sm->redo || sm->abort)
+        if (!sm->redo || sm->abort)
             return false;
         if (warp == kLoadWarp && lane == 0)
             init_barriers(true);   // every phase of the first pass has completed
@@ -403,24 +413,37 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 GroupPages pages(p, sm->key0, sm->keys, sm->base);
                 auto scale_of = [&](const GroupPages::Spot &x) {
                     const float *from = (lane < 8 ? p.k_scale : p.v_scale) + sm->kvh;
-                    return lane < 16 && x.off >= 0 ? __ldcg(from + (int64_t)pages.page_of(x) * p.scale_heads) : 0.f;
+                    return lane < 16 && x.off >= 0 ? __ldcg(from + (int64_t)pages.page_of(x) * p.scale_heads)
+                                                   : kSmallestScale;
                 };
+                const bool wide = pass > 0 && sm->wide;
                 float scale = scale_of(pages.next()), ref_log = 0.f;
                 GroupPages::Spot ahead = pages.next();
 #pragma unroll 1
                 for (int t = 0; t < n; ++t) {
                     if (t == 0) {
-                        float m = lane >= 8 ? scale : 0.f;
+                        // pages of zeros have the smallest scale: no reference
+                        float m = lane >= 8 && scale > kSmallestScale && scale < INFINITY ? scale : 0.f;
 #pragma unroll
                         for (int o = 1; o < 32; o <<= 1)
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        // pages of zeros have the smallest scale: no reference
-                        const float ref = m > 8.7e-19f && m < 1.2e18f ? m : 1.f;   // 2^-60, 2^60
+                        const float ref = m > 0.f ? m : kSmallestScale;
                         ref_log = log2f(ref);
-                        if (lane == 0)
+                        if (lane == 0) {
                             sm->v_ref = ref;
+                            sm->ref_log = ref_log;
+                        }
                     }
-                    float lv = fminf(fmaxf(log2f(scale) - ref_log, kLeastV), kMostV);
+                    float lv = log2f(scale) - ref_log;
+                    if (!wide) {
+                        // far from the reference: in a second pass (its results do not count)
+                        const bool zero = scale == kSmallestScale;
+                        const bool out = lane >= 8 && !zero && scale >= 0.f && scale < INFINITY &&
+                                         !(lv >= kLeastV && lv <= kMostV);
+                        if (out)
+                            sm->redo = sm->wide = 1;
+                        lv = zero ? fmaxf(lv, kZeroV) : fminf(fmaxf(lv, kLeastV), kMostV);
+                    }
                     if (!(scale >= 0.f && scale < INFINITY))
                         lv = __int_as_float(0x7fffffff);
                     const float v = __shfl_sync(0xffffffffu, lv, (lane & 7) + 8);
@@ -513,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             tcgen05_commit(smem_addr(&sm->drain), leader);
             mbar_wait(smem_addr(&sm->drain), 0, kDrainTimeoutNs);
             __syncwarp();
-        } while (another_pass(pass++));
+        } while (pass++ == 0 && another_pass());
     } else if (warp >= kLoadWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLoadRegs));
         int pass = 0;
@@ -615,92 +638,96 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 stream(std::integral_constant<int, 2>{});
             else
                 stream(std::integral_constant<int, 4>{});
-        } while (another_pass(pass++));
+        } while (pass++ == 0 && another_pass());
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
-        float c2 = 0.f;   // what a score of codes is multiplied by
-        int pass = 0;
-        do {
-            const bool careful = pass > 0;
-            // -------------------------------------------------------- the softmax
-            const int s = warp >> 2, quad = warp & 3;
-            const int trow = quad * 32 + lane;   // row of the stream's tile: lane of tensor memory
-            const uint32_t s_col = tmem + ((uint32_t)quad << 21) + s * kStreamCols, o_col = s_col + 128;
-            if (ok && !careful) {
-                // Q rows as f16 into shared memory, a tile [half][128 rows][128 bytes]; a
-                // negative factor of the scores turns q around.  Each row times the
-                // power of two that puts its largest magnitude in [2^8, 2^9): exact down
-                // to 2^-22 of it.
-                const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
-                // a thread: chunk tid % 16 of every 16th row, all its loads in flight at once
-                // (four at a time, with divisions by the group: 12 us)
-                constexpr int kRowsOnce = kSoftmaxThreads / 16, kOfTile = kTileRows / kRowsOnce;
-                const int ch = tid & 15;
-                uint4 v[2][kOfTile];
+        // -------------------------------------------------------- the softmax
+        const int s = warp >> 2, quad = warp & 3;
+        const int trow = quad * 32 + lane;   // row of the stream's tile: lane of tensor memory
+        const uint32_t s_col = tmem + ((uint32_t)quad << 21) + s * kStreamCols, o_col = s_col + 128;
+        if (ok) {
+            // Q rows as f16 into shared memory, a tile [half][128 rows][128 bytes]; a
+            // negative factor of the scores turns q around.  Each row times the
+            // power of two that puts its largest magnitude in [2^8, 2^9): exact down
+            // to 2^-22 of it.
+            const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+            // a thread: chunk tid % 16 of every 16th row, all its loads in flight at once
+            // (four at a time, with divisions by the group: 12 us)
+            constexpr int kRowsOnce = kSoftmaxThreads / 16, kOfTile = kTileRows / kRowsOnce;
+            const int ch = tid & 15;
+            uint4 v[2][kOfTile];
 #pragma unroll
-                for (int k = 0; k < 2 * kOfTile; ++k) {
-                    const int r = k * kRowsOnce + (tid >> 4), gr = sm->row0 + r;
-                    v[k / kOfTile][k % kOfTile] = make_uint4(0u, 0u, 0u, 0u);
-                    if (r < sm->rows) {
-                        const uint16_t *from = p.q + (sm->q0 + (gr >> p.group_log2)) * p.q_stride +
-                                               ((sm->kvh << p.group_log2) + (gr & (p.group - 1))) * kHeadDim;
-                        v[k / kOfTile][k % kOfTile] = __ldcg(reinterpret_cast<const uint4 *>(from) + ch);
-                    }
+            for (int k = 0; k < 2 * kOfTile; ++k) {
+                const int r = k * kRowsOnce + (tid >> 4), gr = sm->row0 + r;
+                v[k / kOfTile][k % kOfTile] = make_uint4(0u, 0u, 0u, 0u);
+                if (r < sm->rows) {
+                    const uint16_t *from = p.q + (sm->q0 + (gr >> p.group_log2)) * p.q_stride +
+                                           ((sm->kvh << p.group_log2) + (gr & (p.group - 1))) * kHeadDim;
+                    v[k / kOfTile][k % kOfTile] = __ldcg(reinterpret_cast<const uint4 *>(from) + ch);
                 }
-                auto to_tile = [&](uint4 (&x)[kOfTile], int tile) {
-                    uint32_t w[kOfTile][4], most[kOfTile];
-#pragma unroll
-                    for (int k = 0; k < kOfTile; ++k) {
-                        w[k][0] = x[k].x ^ flip;
-                        w[k][1] = x[k].y ^ flip;
-                        w[k][2] = x[k].z ^ flip;
-                        w[k][3] = x[k].w ^ flip;
-                        const uint32_t m = __vmaxu2(__vmaxu2(w[k][0] & 0x7fff7fffu, w[k][1] & 0x7fff7fffu),
-                                                    __vmaxu2(w[k][2] & 0x7fff7fffu, w[k][3] & 0x7fff7fffu));
-                        most[k] = max(m << 16, m & 0xffff0000u);   // of the bits of magnitudes
-                    }
-#pragma unroll
-                    for (int o = 1; o < 16; o <<= 1)
-#pragma unroll
-                        for (int k = 0; k < kOfTile; ++k)
-                            most[k] = max(most[k], __shfl_xor_sync(0xffffffffu, most[k], o));
-#pragma unroll
-                    for (int k = 0; k < kOfTile; ++k) {
-                        const int rr = k * kRowsOnce + (tid >> 4);
-                        const int sh = min(max(9 + 126 - (int)(most[k] >> 23), -119), 126);   // 2^-sh, too, is normal
-                        const float up = __int_as_float((127 + sh) << 23);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 a = bf16x2_to_float2(w[k][j]);
-                            w[k][j] = pack_f16x2(make_float2(a.x * up, a.y * up));
-                        }
-                        if (ch == 0)
-                            sm->q_scale[tile * kTileRows + rr] = __int_as_float((127 - sh) << 23);
-                        *reinterpret_cast<uint4 *>(smem + tile * kBufBytes + (ch >> 3) * kHalfBytes + rr * 128 +
-                                                   (((ch & 7) ^ (rr & 7)) << 4)) =
-                            make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
-                    }
-                };
-                to_tile(v[0], 0);
-                if (two)
-                    to_tile(v[1], 1);
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
-            __syncwarp();
-            if (lane == 0 && ok)
-                mbar_arrive(smem_addr(&sm->q_ready));
-            const int r_mine = (two ? s * kTileRows : 0) + trow;
-            if (!careful) {
-                barrier(1, kSoftmaxThreads);   // q_scale is written
-                c2 = fabsf(p.scale) * kLog2e * (ok ? sm->q_scale[r_mine] : 0.f);
-            }
-            // keys of the item that the row sees
-            const int token = min((sm->row0 + r_mine) >> p.group_log2, sm->tokens - 1);
-            const int sees = ok && p.causal ? min(sm->keys, sm->len - sm->tokens + token + 1 - sm->key0) : sm->keys;
-            float ref = -INFINITY, l = 0.f;   // E, and the row's sum
+            auto to_tile = [&](uint4 (&x)[kOfTile], int tile) {
+                uint32_t w[kOfTile][4], most[kOfTile];
+#pragma unroll
+                for (int k = 0; k < kOfTile; ++k) {
+                    w[k][0] = x[k].x ^ flip;
+                    w[k][1] = x[k].y ^ flip;
+                    w[k][2] = x[k].z ^ flip;
+                    w[k][3] = x[k].w ^ flip;
+                    const uint32_t m = __vmaxu2(__vmaxu2(w[k][0] & 0x7fff7fffu, w[k][1] & 0x7fff7fffu),
+                                                __vmaxu2(w[k][2] & 0x7fff7fffu, w[k][3] & 0x7fff7fffu));
+                    most[k] = max(m << 16, m & 0xffff0000u);   // of the bits of magnitudes
+                }
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1)
+#pragma unroll
+                    for (int k = 0; k < kOfTile; ++k)
+                        most[k] = max(most[k], __shfl_xor_sync(0xffffffffu, most[k], o));
+#pragma unroll
+                for (int k = 0; k < kOfTile; ++k) {
+                    const int rr = k * kRowsOnce + (tid >> 4);
+                    const int sh = min(max(9 + 126 - (int)(most[k] >> 23), -119), 126);   // 2^-sh, too, is normal
+                    const float up = __int_as_float((127 + sh) << 23);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 a = bf16x2_to_float2(w[k][j]);
+                        w[k][j] = pack_f16x2(make_float2(a.x * up, a.y * up));
+                    }
+                    if (ch == 0)
+                        sm->q_scale[tile * kTileRows + rr] = __int_as_float((127 - sh) << 23);
+                    *reinterpret_cast<uint4 *>(smem + tile * kBufBytes + (ch >> 3) * kHalfBytes + rr * 128 +
+                                               (((ch & 7) ^ (rr & 7)) << 4)) =
+                        make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+                }
+            };
+            to_tile(v[0], 0);
+            if (two)
+                to_tile(v[1], 1);
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncwarp();
+        if (lane == 0 && ok)
+            mbar_arrive(smem_addr(&sm->q_ready));
+        const int r_mine = (two ? s * kTileRows : 0) + trow;
+        barrier(1, kSoftmaxThreads);   // q_scale is written
+        // what a score of codes is multiplied by
+        const float c2 = fabsf(p.scale) * kLog2e * (ok ? sm->q_scale[r_mine] : 0.f);
+        // keys of the item that the row sees
+        const int token = min((sm->row0 + r_mine) >> p.group_log2, sm->tokens - 1);
+        const int sees = ok && p.causal ? min(sm->keys, sm->len - sm->tokens + token + 1 - sm->key0) : sm->keys;
+        float ref, l;   // E, and the row's sum
+        // What the sum counts from: E less the bias or, for V scales of any size, the row's
+        // largest score.
+        float top;
+        bool go = ok;
+        // All of the row's tiles; careful: a maximum of every step before its weights.
+        auto all_steps = [&](auto careful_t) {
+            constexpr bool careful = decltype(careful_t)::value;
             float most = -INFINITY, level = -INFINITY;   // what E follows: the largest, the tiles' level
-            const float bias = careful ? kCarefulBias : kBias;
-            bool go = ok;
+            constexpr float bias = careful ? kCarefulBias : kBias;
+            const bool wide = careful && sm->wide;
+            ref = top = -INFINITY;
+            l = 0.f;
             // E to the tiles' level, when it is far from there, and O with it.
             auto follow = [&](bool first) {
                 float to = careful ? most : fmaxf(level, most - kDeep);
@@ -710,7 +737,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     return;
                 const float f = !far ? 1.f : ref == -INFINITY ? 0.f : ex2(ref - to);
                 ref = far ? to : ref;
-                l *= f;
+                if (!wide)
+                    l *= f;
                 if (first)
                     return;
                 // the products up to the last step are done: s_full followed them
@@ -736,6 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 const float4 *group = sm->scale[t % kScaleSlots];
                 const int valid = sees - t * kPrefillTile;
                 tcgen05_fence_after();
+                float here_top = -INFINITY;
                 if (i == 0 || careful) {   // E from this tile's own scores
                     const bool all = __all_sync(0xffffffffu, valid >= kPrefillTile);
 #pragma unroll 1
@@ -760,40 +789,17 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             }
                             const float4 g = group[c0 + c];
                             most = fmaxf(most, fmaf(mt, c2 * g.x, g.y));
+                            here_top = fmaxf(here_top, mt * (c2 * g.x));
                         }
                     }
                 }
+                if (wide && here_top > top) {
+                    l *= ex2(top - here_top);
+                    top = here_top;
+                }
                 follow(i == 0);
-                uint32_t r[kPrefillTile];   // the row's scores, then its weights
-#pragma unroll
-                for (int c = 0; c < kGroups; ++c)
-                    tmem_ld16(s_col + 16 * c, r + 16 * c);
                 const float base = bias - (ref == -INFINITY ? 0.f : ref);
                 float sum_tile = 0.f;
-                tmem_wait_ld();
-                settle(r);
-                // 16 scores to weights; the weights of 16 keys are 8 columns, over those of
-                // the first half of the scores
-                auto weights = [&](int c, auto cut) {
-                    const float4 g = group[c];
-                    const float2 f = make_float2(c2 * g.x, c2 * g.x), off = make_float2(g.y + base, g.y + base);
-                    float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int at = 16 * c + 2 * j;
-                        float2 x = fma2(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), f, off);
-                        if constexpr (decltype(cut)::value) {
-                            x.x = at < valid ? x.x : -INFINITY;
-                            x.y = at + 1 < valid ? x.y : -INFINITY;
-                        }
-                        const float2 e = make_float2(ex2(x.x), ex2(x.y));
-                        sum = add2(sum, e);
-                        r[8 * c + j] = pack_f16x2(e);
-                    }
-                    const float part = sum.x + sum.y;
-                    sum_tile += part;
-                    l = fmaf(part, g.z, l);
-                };
                 auto publish = [&](int part) {
                     tmem_wait_st();
                     tcgen05_fence_before();
@@ -801,148 +807,239 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     if (lane == 0)
                         mbar_arrive(smem_addr(&sm->p_ready[s][part]));
                 };
-                auto tile = [&](auto cut) {
+                if constexpr (careful) {
+                    // 16 scores at a time, rarely run and short; for V scales of any size with a
+                    // second exponential, over `top`
+                    const float from = top == -INFINITY ? 0.f : top;
+#pragma unroll 1
+                    for (int c = 0; c < kGroups; ++c) {
+                        const float4 g = group[c];
+                        uint32_t x[16];
+                        tmem_ld16(s_col + 16 * c, x);
+                        tmem_wait_ld();
+                        settle(x);
+                        if (wide) {
+                            const float less = g.y == g.y ? from : g.y;   // (no number: neither is the sum)
 #pragma unroll
-                    for (int c = 0; c < kGroups; c += 2) {
-                        weights(c, cut);
-                        weights(c + 1, cut);
-                        tmem_st16(s_col + 8 * c, r + 8 * c);
-                        if (c == 2)
+                            for (int j = 0; j < 16; ++j)
+                                l += 16 * c + j < valid ? ex2(fmaf(__uint_as_float(x[j]), c2 * g.x, -less)) : 0.f;
+                        }
+                        float part = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            float e[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                e[k] = fmaf(__uint_as_float(x[j + k]), c2 * g.x, g.y + base);
+                                e[k] = 16 * c + j + k < valid ? ex2(e[k]) : 0.f;
+                                part += e[k];
+                            }
+                            x[j / 2] = pack_f16x2(make_float2(e[0], e[1]));
+                        }
+                        if (!wide)
+                            l = fmaf(part, g.z, l);
+                        tmem_st8(s_col + 8 * c, x);   // (over the first half of the scores, as below)
+                        if (c == 3)
                             publish(0);
                     }
-                };
-                // (compares and selects for each score of every tile took 13 % of a prompt)
-                if (__any_sync(0xffffffffu, valid < kPrefillTile))
-                    tile(std::true_type{});
-                else
-                    tile(std::false_type{});
+                } else {
+                    uint32_t r[kPrefillTile];   // the row's scores, then its weights
+#pragma unroll
+                    for (int c = 0; c < kGroups; ++c)
+                        tmem_ld16(s_col + 16 * c, r + 16 * c);
+                    tmem_wait_ld();
+                    settle(r);
+                    // 16 scores to weights; the weights of 16 keys are 8 columns, over those of
+                    // the first half of the scores
+                    auto weights = [&](int c, auto cut) {
+                        const float4 g = group[c];
+                        const float2 f = make_float2(c2 * g.x, c2 * g.x), off = make_float2(g.y + base, g.y + base);
+                        float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int at = 16 * c + 2 * j;
+                            float2 x = fma2(make_float2(__uint_as_float(r[at]), __uint_as_float(r[at + 1])), f, off);
+                            if constexpr (decltype(cut)::value) {
+                                x.x = at < valid ? x.x : -INFINITY;
+                                x.y = at + 1 < valid ? x.y : -INFINITY;
+                            }
+                            const float2 e = make_float2(ex2(x.x), ex2(x.y));
+                            sum = add2(sum, e);
+                            r[8 * c + j] = pack_f16x2(e);
+                        }
+                        const float part = sum.x + sum.y;
+                        sum_tile += part;
+                        l = fmaf(part, g.z, l);
+                    };
+                    auto tile = [&](auto cut) {
+#pragma unroll
+                        for (int c = 0; c < kGroups; c += 2) {
+                            weights(c, cut);
+                            weights(c + 1, cut);
+                            tmem_st16(s_col + 8 * c, r + 8 * c);
+                            if (c == 2)
+                                publish(0);
+                        }
+                    };
+                    // (compares and selects for each score of every tile took 13 % of a prompt)
+                    if (__any_sync(0xffffffffu, valid < kPrefillTile))
+                        tile(std::true_type{});
+                    else
+                        tile(std::false_type{});
+                }
                 publish(1);
                 if (lane == 0 || (lane == 1 && !two))
                     mbar_arrive(smem_addr(&sm->scales_free[t % kScaleSlots]));
-                const float here = __log2f(sum_tile) - base;
-                level = fmaxf(here, level - kFade - fminf(fmaxf(level - here - kGap, 0.f), kFall));
-                most = fmaxf(most, here);
+                if constexpr (!careful) {
+                    const float here = __log2f(sum_tile) - base;
+                    level = fmaxf(here, level - kFade - fminf(fmaxf(level - here - kGap, 0.f), kFall));
+                    most = fmaxf(most, here);
+                }
             }
-            // ------------------------------------------------------- the output
-            for (int x = 0; x < 2; ++x)   // both streams' products are done with the ring
+            if (!wide)
+                top = ref - bias;
+            // both streams' products are done with the ring
+            for (int x = 0; x < 2; ++x)
                 if (go && steps(x) > 0)
                     go = __all_sync(0xffffffffu, wait_phase(&sm->o_done[x], 0, p, sm));
             tcgen05_fence_after();
-            if (go && !careful && steps(s) > 0) {   // a weight over f16's range
-                uint32_t o[16];
-                tmem_ld16(o_col, o);
-                tmem_wait_ld();
-                settle(o);
-                if (!(fabsf(__uint_as_float(o[0])) < INFINITY))
-                    sm->redo = 1;
-            }
-            barrier(1, kSoftmaxThreads);
-            if (careful || !sm->redo) {
-                float *stage = reinterpret_cast<float *>(smem);   // [q_tiles * 128][kOutStride]
-                PrefillEnd *end = reinterpret_cast<PrefillEnd *>(smem + kEndOffset);
-                float *mine = stage + r_mine * kOutStride;
-                if (!two && s == 1 && go) {
-                    // one row tile: stream 1 hands its state to stream 0
-                    end->row_sum[trow] = l;
-                    end->row_ref[trow] = ref;
-                    if (steps(1) > 0) {
+        };
+        all_steps(std::false_type{});
+        if (go && steps(s) > 0) {   // a weight over f16's range
+            uint32_t o[16];
+            tmem_ld16(o_col, o);
+            tmem_wait_ld();
+            settle(o);
+            if (!(fabsf(__uint_as_float(o[0])) < INFINITY))
+                sm->redo = 1;
+        }
+        if (another_pass()) {
+            if (lane == 0 && ok)
+                mbar_arrive(smem_addr(&sm->q_ready));
+            all_steps(std::true_type{});
+        } else if (sm->redo) {
+            go = false;
+        }
+        // ------------------------------------------------------- the output
+        barrier(1, kSoftmaxThreads);   // in place of the ring
+        float *stage = reinterpret_cast<float *>(smem);   // [q_tiles * 128][kOutStride]
+        PrefillEnd *end = reinterpret_cast<PrefillEnd *>(smem + kEndOffset);
+        float *mine = stage + r_mine * kOutStride;
+        if (!two && s == 1 && go) {
+            // one row tile: stream 1 hands its state to stream 0
+            end->row_sum[trow] = l;
+            end->row_ref[trow] = ref;
+            end->row_top[trow] = top;
+            if (steps(1) > 0) {
 #pragma unroll 1
-                        for (int c = 0; c < 8; ++c) {
-                            uint32_t o[16];
-                            tmem_ld16(o_col + 16 * c, o);
-                            tmem_wait_ld();
-                            settle(o);
+                for (int c = 0; c < 8; ++c) {
+                    uint32_t o[16];
+                    tmem_ld16(o_col + 16 * c, o);
+                    tmem_wait_ld();
+                    settle(o);
 #pragma unroll
-                            for (int j = 0; j < 16; j += 4)
-                                *reinterpret_cast<uint4 *>(mine + 16 * c + j) =
-                                    make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
-                        }
-                    }
-                }
-                if (!two)
-                    barrier(1, kSoftmaxThreads);
-                if (go && (two || s == 0)) {
-                    float f0 = 1.f, f1 = 0.f, m = ref, den = l;
-                    const bool join = !two && steps(1) > 0;
-                    if (join) {
-                        const float m1 = end->row_ref[trow];
-                        m = fmaxf(ref, m1);
-                        f0 = ref == -INFINITY ? 0.f : ex2(ref - m);
-                        f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
-                        den = l * f0 + end->row_sum[trow] * f1;
-                    }
-                    // a row that sees no key: O = 0, LSE = -inf
-                    const float inv = den == 0.f ? 0.f : sm->v_ref / den;
-                    f0 *= inv;
-                    f1 *= inv;
-                    // The warp's 32 rows through shared memory, so that whole rows are written
-                    // (by its threads, a row each: 4 us of the store unit).
-                    const int first = r_mine - lane;
-                    const bool partial = sm->splits > 1;
-                    uint8_t *rows = smem + (two ? 0 : kStageOffset) + first * kRowStage;
-                    auto row_of = [&](int r) {   // of the request's rows [token][head]
-                        const int gr = sm->row0 + r;
-                        return (int64_t)(gr >> p.group_log2) * p.num_qo_heads + (sm->kvh << p.group_log2) +
-                               (gr & (p.group - 1));
-                    };
-#pragma unroll 2
-                    for (int c = 0; c < 8; ++c) {
-                        uint32_t o[16];
-                        float v[16];
-                        if (n > 0) {
-                            tmem_ld16(o_col + 16 * c, o);
-                            tmem_wait_ld();
-                            settle(o);
-                        }
-#pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            v[j] = inv == 0.f ? 0.f : __uint_as_float(o[j]) * f0;
-                        if (join && inv != 0.f) {
-#pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                v[j] = fmaf(mine[16 * c + j], f1, v[j]);
-                        }
-                        if (partial) {
-                            float4 *to = reinterpret_cast<float4 *>(rows + lane * kRowStage) + 4 * c;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                        } else {
-                            uint4 *to = reinterpret_cast<uint4 *>(rows + lane * kRowStage) + 2 * c;
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-                                to[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]),
-                                                   pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                                   pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
-                                                   pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
-                        }
-                    }
-                    if (r_mine < sm->rows) {
-                        const float lse = den == 0.f ? -INFINITY : (m + log2f(den) - bias) * kLn2;
-                        if (partial)
-                            p.partial_lse[sm->part_row + row_of(r_mine) * sm->splits] = lse;
-                        else if (p.lse)
-                            p.lse[(int64_t)sm->q0 * p.num_qo_heads + row_of(r_mine)] = lse;
-                    }
-                    __syncwarp();
-                    const int count = min(sm->rows - first, 32);
-                    if (partial) {
-#pragma unroll 4
-                        for (int r = 0; r < count; ++r)
-                            reinterpret_cast<uint4 *>(p.partial_o + (sm->part_row + row_of(first + r) * sm->splits) *
-                                                                        kHeadDim)[lane] =
-                                reinterpret_cast<const uint4 *>(rows + r * kRowStage)[lane];
-                    } else {   // two rows at once
-#pragma unroll 4
-                        for (int r = lane >> 4; r < count; r += 2)
-                            reinterpret_cast<uint4 *>(p.o + ((int64_t)sm->q0 * p.num_qo_heads + row_of(first + r)) *
-                                                                kHeadDim)[lane & 15] =
-                                reinterpret_cast<const uint4 *>(rows + r * kRowStage)[lane & 15];
-                    }
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<uint4 *>(mine + 16 * c + j) =
+                            make_uint4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                 }
             }
-        } while (another_pass(pass++));
+        }
+        if (!two)
+            barrier(1, kSoftmaxThreads);
+        if (go && (two || s == 0)) {
+            float f0 = 1.f, f1 = 0.f, m = ref, den = l;
+            const bool join = !two && steps(1) > 0;
+            if (join) {
+                const float m1 = end->row_ref[trow], top1 = end->row_top[trow], my_top = top;
+                m = fmaxf(ref, m1);
+                top = fmaxf(my_top, top1);
+                f0 = ref == -INFINITY ? 0.f : ex2(ref - m);
+                f1 = m1 == -INFINITY ? 0.f : ex2(m1 - m);
+                den = l * (my_top == -INFINITY ? 0.f : ex2(my_top - top)) +
+                      end->row_sum[trow] * (top1 == -INFINITY ? 0.f : ex2(top1 - top));
+            }
+            // a row that sees no key: O = 0, LSE = -inf
+            const float inv = den == 0.f ? 0.f : 1.f / den;
+            // O = (O over E) 2^(E - bias - top) v_ref / den, the powers in two halves
+            // where these are numbers of any size
+            float up = inv, last = sm->v_ref;
+            if (sm->wide) {
+                last = ex2(0.5f * (m - kCarefulBias - top + sm->ref_log));
+                up *= last;
+            }
+            f0 *= up;
+            f1 *= up;
+            // The warp's 32 rows through shared memory, so that whole rows are written
+            // (by its threads, a row each: 4 us of the store unit).
+            const int first = r_mine - lane;
+            const bool partial = sm->splits > 1;
+            uint8_t *rows = smem + (two ? 0 : kStageOffset) + first * kRowStage;
+            auto row_of = [&](int r) {   // of the request's rows [token][head]
+                const int gr = sm->row0 + r;
+                return (int64_t)(gr >> p.group_log2) * p.num_qo_heads + (sm->kvh << p.group_log2) +
+                       (gr & (p.group - 1));
+            };
+#pragma unroll 2
+            for (int c = 0; c < 8; ++c) {
+                uint32_t o[16];
+                float v[16];
+                if (n > 0) {
+                    tmem_ld16(o_col + 16 * c, o);
+                    tmem_wait_ld();
+                    settle(o);
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    v[j] = inv == 0.f ? 0.f : __uint_as_float(o[j]) * f0;
+                if (join && inv != 0.f) {
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        v[j] = fmaf(mine[16 * c + j], f1, v[j]);
+                }
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                    v[j] *= last;
+                if (partial) {
+                    float4 *to = reinterpret_cast<float4 *>(rows + lane * kRowStage) + 4 * c;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        to[j] = make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                } else {
+                    uint4 *to = reinterpret_cast<uint4 *>(rows + lane * kRowStage) + 2 * c;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        to[j] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]),
+                                           pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                           pack_bf16x2(v[8 * j + 4], v[8 * j + 5]),
+                                           pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+                }
+            }
+            if (r_mine < sm->rows) {
+                const float lse = den == 0.f ? -INFINITY : (top + log2f(den)) * kLn2;
+                if (partial)
+                    p.partial_lse[sm->part_row + row_of(r_mine) * sm->splits] = lse;
+                else if (p.lse)
+                    p.lse[(int64_t)sm->q0 * p.num_qo_heads + row_of(r_mine)] = lse;
+            }
+            __syncwarp();
+            const int count = min(sm->rows - first, 32);
+            if (partial) {
+#pragma unroll 4
+                for (int r = 0; r < count; ++r)
+                    reinterpret_cast<uint4 *>(p.partial_o + (sm->part_row + row_of(first + r) * sm->splits) *
+                                                                kHeadDim)[lane] =
+                        reinterpret_cast<const uint4 *>(rows + r * kRowStage)[lane];
+            } else {   // two rows at once
+#pragma unroll 4
+                for (int r = lane >> 4; r < count; r += 2)
+                    reinterpret_cast<uint4 *>(p.o + ((int64_t)sm->q0 * p.num_qo_heads + row_of(first + r)) *
+                                                        kHeadDim)[lane & 15] =
+                        reinterpret_cast<const uint4 *>(rows + r * kRowStage)[lane & 15];
+            }
+        }
     }
+    tcgen05_fence_before();
+    __syncthreads();   // the output has been read from tensor memory
     griddep_launch_dependents();
     if (warp == kMmaWarp) {
         tcgen05_fence_after();

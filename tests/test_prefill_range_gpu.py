@@ -1,13 +1,14 @@
-"""fd_prefill_paged_int8 where f16's range of softmax weights ends, against attention in 64
-bits."""
+"""fd_prefill_paged_int8 where f16's range of softmax weights and fp32's of V scales end,
+against attention in 64 bits."""
 import math
 
 import numpy as np
 import pytest
 import torch
 
-from tests.int8_util import D, attention, cache, indptr, tables
-from tests.test_prefill_gpu import plan_of, run
+import split_kv_flashdecoding_gb300 as fd
+from tests.int8_util import D, attention, cache, dev_tables, indptr, tables
+from tests.test_prefill_gpu import make, plan_of, run
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +50,80 @@ def test_prefill_of_keys_beside_one_that_takes_nearly_all(cuda_device, share, ke
         off = float(((o.double() - want).norm(dim=-1) / want.norm(dim=-1)).max())
         assert off <= 2.0 ** -8 + 2.0 ** -7, f"{chunk}: {off}"
         assert float((lse.double() - lse_want).abs().max()) <= 2e-5
+
+
+def compare_by_row(got, t, c, q, qi, causal, what):
+    """O against 64 bits, each row by its own keys' V scales.  Half a step of bf16; the
+    weights' f16 (2^-11); exponents of up to 2^8, rounded a few times by 2^-17, in the
+    weights' and in the sum's (2^-13); of weights that f16 does not have, 2^-36 of the
+    largest each, 2^-24 of the row's values as if all of its codes were 127."""
+    o, lse = got
+    want, lse_want = attention(q, t, c, D ** -0.5, qi, causal)
+    a, _ = attention(q, t, dict(c, v=c["v"].clamp(min=-127).abs()), D ** -0.5, qi, causal)
+    most, _ = attention(q, t, dict(c, v=torch.full_like(c["v"], 127)), D ** -0.5, qi, causal)
+    tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 2.0 ** -13) * a.abs() + 2.0 ** -24 * most.abs() + 2.0 ** -133
+    over = (o.double() - want).abs() / tol
+    assert float(over.max()) <= 1, f"{what}: {float(over.max())} of the tolerance"
+    assert float((lse.double() - lse_want).abs().max()) <= 2e-5, what
+
+
+@pytest.mark.parametrize("tokens", [20, 300])
+@pytest.mark.parametrize("log2", [-110, -63, -41, 41, 100])
+def test_prefill_v_values_of_any_size(cuda_device, tokens, log2):
+    t, c, q, qi = make("vsize", 4, 2, [tokens], [700], 16, cuda_device)
+    c["vs"] *= 2.0 ** log2
+    for causal in (True, False):
+        compare_by_row(run(t, c, q, qi, causal), t, c, q, qi, causal, f"{causal}")
+
+
+@pytest.mark.parametrize("tokens", [20, 300])
+@pytest.mark.parametrize("first", ["zeros", "ordinary", "large", "no scale"])
+@pytest.mark.parametrize("log2", [-110, -63, -45, 30, 90])
+def test_prefill_v_values_far_from_the_first_ones(cuda_device, tokens, first, log2):
+    """A tile of zeros, or of values of another size, before values of one size."""
+    t, c, q, qi = make("vfirst", 4, 2, [tokens], [700], 16, cuda_device)
+    plain = c["vs"].clone()
+    c["vs"] *= 2.0 ** log2
+    for j in range(8 if first != "large" else 3):
+        page = int(t["ids"][j])
+        if first == "zeros":
+            c["v"][page] = 0
+            c["vs"][page] = 2.0 ** -126
+        elif first == "no scale":
+            c["vs"][page] = 0
+        else:
+            c["vs"][page] = plain[page] * 2.0 ** (20 if first == "large" else 0)
+    for causal in (True, False):
+        compare_by_row(run(t, c, q, qi, causal), t, c, q, qi, causal, f"{causal}")
+    o, _ = run(t, c, q[-1:], indptr([1]), True)
+    od, _ = fd.decode_paged_int8(q[-1:], c["k"], c["v"], c["ks"], c["vs"], t["ip"], t["last"], *dev_tables(t, cuda_device), D ** -0.5)
+    assert float((o.double() - od.double()).abs().max()) <= 2.0 ** -7 * float(od.abs().max())
+
+
+@pytest.mark.parametrize("tokens", [20, 300])
+@pytest.mark.parametrize("chunk", [0, 256])
+def test_prefill_v_scales_over_all_of_fp32(cuda_device, tokens, chunk):
+    """A page's scale anywhere between 2^-110 and 2^110, some 0: each row as exact as its
+    own keys allow, whichever pages it sees first."""
+    t, c, q, qi = make("vall", 4, 2, [tokens, 3], [900, 40], 16, cuda_device)
+    rng = np.random.RandomState(tokens)
+    e = torch.from_numpy(rng.randint(-110, 110, (t["num_pages"], 4))).to(cuda_device)
+    c["vs"] *= torch.exp2(e[:, : c["vs"].shape[1]].float())
+    c["vs"][torch.from_numpy(t["ids"][::7].astype(np.int64)).to(cuda_device)] = 0
+    for causal in (True, False):
+        got = run(t, c, q, qi, causal, plan=plan_of(t, q, 2, qi, causal, chunk=chunk))
+        compare_by_row(got, t, c, q, qi, causal, f"{causal}")
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -1.0])
+@pytest.mark.parametrize("tokens", [20, 200])
+def test_prefill_v_scales_far_apart_and_no_numbers(cuda_device, tokens, value):
+    t, c, q, qi = make("vbad", 8, 4, [tokens], [300], 16, cuda_device)
+    c["vs"][int(t["ids"][3])] *= 2.0 ** 60
+    c["vs"][int(t["ids"][17]), 1] = value   # keys 272 .. 287, head 1
+    o, lse = run(t, c, q, qi, True)
+    first = max(0, tokens - 300 + 272)
+    bad = torch.zeros(o.shape[:2], dtype=torch.bool, device=cuda_device)
+    bad[first:tokens, 2:4] = True
+    assert torch.equal(o.isnan().all(-1), bad) and torch.equal(o.isnan().any(-1), bad)
+    assert torch.equal(lse.isnan(), bad)
