@@ -572,7 +572,7 @@ int fd_decode_shared_paged_fp8(const fd_shared_plan *plan, int num_pages,
  * Scores and sums are fp32; a softmax weight is rounded once, to f16, O once, to bf16.
  * The first is off by 2^-11 of the weight or, when that is more, by 2^-26 of the largest
  * sum of weights over 128 keys of the split before it; a few times 128 keys further on,
- * when all of these had far smaller sums, by 2^-35 of that.  (Beside a key that takes 99 %
+ * when all of these had far smaller sums, by 2^-32 of that.  (Beside a key that takes 99 %
  * of a row's weight and has V = 0, O is within 0.5 % of its norm for 30000 keys.)
  *
  * Scales of any size, as fd_append_paged_int8 leaves them, not below 0: one that is, and

@@ -52,11 +52,12 @@
 // E goes down, too, when the tiles since the largest have stayed far below it: a key
 // that takes nearly all of a row's weight, its V near 0, would otherwise push the
 // others' weights below f16's smallest number, of which O consists (a first key with 99 %
-// of 131072 keys' weight: O off by 9 % of its norm, so 0.2 %).  It waits for some tiles
-// (kFade), because a score 2^15 times E is still in range, and with E at each tile's
-// own level many items of wide-spread scores would be done twice (64 heads, a chunk of
-// 2047 tokens behind 30001 keys: 1545 us with E at the largest, 1560 to 1580 so, 1753
-// without waiting; 2000 with E at the largest and weights 2^6 times larger).
+// of 131072 keys' weight: O off by 9 % of its norm, so 0.3 %).  It waits for some tiles
+// (kFade), and does not go all the way (kDeep), because a score over f16's range costs a
+// second pass, and with E at each tile's own level many items of wide-spread scores
+// would have one: 64 heads, a chunk of 2047 tokens behind 30001 keys, 1532 us with E at
+// the largest, 1549 so, 1753 without waiting, and 2003 for 1571 in an older form whose E
+// was at the largest and whose weights were 2^5 times larger.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -94,9 +95,9 @@ constexpr int kStreamCols = 256;                            // S (and P over it)
 // In log2.  The tiles' level is that of the last one, or of one before it less kFade a
 // tile since then, and less what the last one is under it, beyond kGap and up to kFall.
 // E follows it, down to kDeep below the largest, when it is more than kRaise above or
-// kLower below E; then E goes another kRaise down.
-constexpr float kRaise = 3.f, kLower = 6.f, kDeep = 10.f;
-constexpr float kFade = 0.25f, kGap = 6.f, kFall = 8.f;
+// kLower below E.
+constexpr float kRaise = 3.f, kLower = 6.f, kDeep = 7.f;
+constexpr float kFade = 0.125f, kGap = 6.f, kFall = 8.f;
 // Weights are 2^kBias larger than over E: of small ones' bits.  Careful steps, whose
 // weights over E are at most 2^kRaise, have as much as f16 takes.
 constexpr float kBias = 1.f, kCarefulBias = 12.f;
@@ -730,9 +731,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             l = 0.f;
             // E to the tiles' level, when it is far from there, and O with it.
             auto follow = [&](bool first) {
-                float to = careful ? most : fmaxf(level, most - kDeep);
-                const bool low = to < ref - kLower, far = to > ref + kRaise || low;
-                to = low ? to - kRaise : to;
+                const float to = careful ? most : fmaxf(level, most - kDeep);
+                const bool far = to > ref + kRaise || to < ref - kLower;
                 if (!__any_sync(0xffffffffu, far))
                     return;
                 const float f = !far ? 1.f : ref == -INFINITY ? 0.f : ex2(ref - to);
