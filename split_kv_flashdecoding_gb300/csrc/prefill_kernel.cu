@@ -520,18 +520,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                 if (last)
                     tcgen05_commit(smem_addr(&sm->o_done[s]), leader);
             };
-            scores(0);
-            if (steps1 > 0)
-                scores(1);
-            for (int i = 0; i < steps0; ++i) {
-                values(0, i, i == steps0 - 1);
-                if (i + 1 < steps0)
-                    scores(0);
-                if (i < steps1)
-                    values(1, i, i == steps1 - 1);
-                if (i + 1 < steps1)
-                    scores(1);
-            }
+            // One copy of each for both streams: with two the roles' loops waited for
+            // instructions (a prompt of 32768 tokens 5930 us for 5880).
+#pragma unroll 1
+            for (int i = -1; i < steps0; ++i)
+#pragma unroll 1
+                for (int s = 0; s < 2; ++s) {
+                    const int last = (s == 0 ? steps0 : steps1) - 1;
+                    if (i >= 0 && i <= last)
+                        values(s, i, i == last);
+                    if (i < last)
+                        scores(s);
+                }
             // whatever the others saw, the products in flight end before tensor
             // memory is freed
             tcgen05_commit(smem_addr(&sm->drain), leader);
