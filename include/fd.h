@@ -406,7 +406,8 @@ int fd_decode_graph(const fd_plan_info *info, const int32_t *kv_indptr_dev,
  *
  * For each row r: M = max_s lse_states[s][r], w_s = exp(lse_states[s][r] - M),
  * o[r] = sum_s w_s o_states[s][r] / sum_s w_s, lse[r] = M + ln sum_s w_s; a
- * row whose states are all -inf (no keys in any shard) gets o = 0, lse = -inf.
+ * row whose states are all -inf (no keys in any shard) gets o = 0, lse = -inf, one with
+ * a NaN among them NaN in o and lse.
  * o_states fp32 [num_states, rows, head_dim], lse_states fp32 [num_states,
  * rows], o [rows, head_dim], lse [rows], all on the device; rows = B * Hq.
  */

@@ -147,7 +147,8 @@ namespace {
 // Merge of R attention states per row (the sequence-sharded exchange): for
 // row r, M = max_s LSE_s, w_s = exp(LSE_s - M), O = sum_s w_s O_s / sum_s w_s,
 // LSE = M + ln sum_s w_s; a row whose states are all empty (LSE = -inf) gets
-// O = 0, LSE = -inf.  One warp per row, lane = 4 columns (one float4).
+// O = 0, LSE = -inf, and one with a NaN among its LSEs NaN in both: a further merge
+// must not take it for an empty one.  One warp per row, lane = 4 columns (one float4).
 constexpr int kStatesWarps = 4;
 
 __global__ void __launch_bounds__(kStatesWarps * 32)
@@ -160,11 +161,15 @@ __global__ void __launch_bounds__(kStatesWarps * 32)
     const int row = blockIdx.x * kStatesWarps + (threadIdx.x >> 5);
     if (row < rows) {
         float m = -INFINITY;
-        for (int s = 0; s < num_states; ++s)
-            m = fmaxf(m, __ldg(lse_states + (int64_t)s * rows + row));
+        bool nan = false;   // (fmaxf drops it)
+        for (int s = 0; s < num_states; ++s) {
+            const float x = __ldg(lse_states + (int64_t)s * rows + row);
+            m = fmaxf(m, x);
+            nan |= x != x;
+        }
         float den = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (m != -INFINITY) {
+        if (m != -INFINITY || nan) {
             for (int s = 0; s < num_states; ++s) {
                 const int64_t r = (int64_t)s * rows + row;
                 const float w = expf(__ldg(lse_states + r) - m);
@@ -176,11 +181,11 @@ __global__ void __launch_bounds__(kStatesWarps * 32)
                 acc.w = fmaf(w, v.w, acc.w);
             }
         }
-        const float inv = den > 0.f ? 1.f / den : 0.f;
+        const float inv = den == 0.f ? 0.f : 1.f / den;
         reinterpret_cast<float4 *>(o + (int64_t)row * kHeadDim)[lane] =
             make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         if (lane == 0)
-            lse[row] = den > 0.f ? m + logf(den) : -INFINITY;
+            lse[row] = den == 0.f ? -INFINITY : m + logf(den);
     }
     griddep_launch_dependents();
 }
