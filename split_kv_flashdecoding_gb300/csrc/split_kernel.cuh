@@ -1112,7 +1112,7 @@ __device__ __forceinline__ float load_q(const uint16_t *qrows, int lane, uint32_
         if (amax > 0.f) {
             int e;
             frexpf(amax, &e);
-            sh = min(max(9 - e, -100), 100);
+            sh = min(max(9 - e, -119), 126);   // of every bf16; 2^-sh, too, is normal
         }
         const float up = __int_as_float((127 + sh) << 23);
         auto f16pair = [&](uint32_t pair) {   // a bf16x2 pair -> f16x2, times 2^sh (exact)
