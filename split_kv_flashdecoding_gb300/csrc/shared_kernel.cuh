@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(kThreads<DT>, 1)
                         if (amax > 0.f) {
                             int e;
                             frexpf(amax, &e);
-                            sh = min(max(9 - e, -100), 100);
+                            sh = min(max(9 - e, -119), 126);   // of every bf16; 2^-sh, too, is normal
                         }
                         const float up = __int_as_float((127 + sh) << 23);
 #pragma unroll
