@@ -605,6 +605,10 @@ typedef struct fd_prefill_plan {
 /*
  * fd_plan_prefill_paged -- host only (no CUDA call unless num_sms == 0).  chunk: 0, or
  * the most keys of a split (a multiple of 128, up to 262144).
+ *
+ * A split has at most 262144 keys, so a request with more is cut whatever its tokens, and
+ * each split of it takes 516 bytes of workspace a token and query head: 262145 tokens of 32
+ * heads 8.7 GB.  Plans of more than 2^31 - 1 CTAs or such rows are FD_ERR_UNSUPPORTED.
  */
 int fd_plan_prefill_paged(int batch, int num_qo_heads, int num_kv_heads, int head_dim, int page_size,
                           const int32_t *q_indptr_host, const int32_t *kv_page_indptr_host,

@@ -20,6 +20,7 @@ namespace {
 
 constexpr int kHeadDim = 128;
 constexpr int kMaxSlots = 1024;   // SMs the plan can balance over
+constexpr int kMostMerged = INT32_MAX - 64;   // the merge's grid counts rows up to its last CTA's
 
 // The plan's view of its requests.
 struct Requests {
@@ -184,8 +185,9 @@ extern "C" int fd_plan_prefill_paged(int batch, int num_qo_heads, int num_kv_hea
     if (chunk == 0)
         chunk = choose_chunk(x, num_sms);
     const PlanSize z = size_of(x, chunk);
-    if (z.items > INT32_MAX || z.rows > INT32_MAX / kHeadDim || z.merge > INT32_MAX - 64)
-        return FD_ERR_INVALID_ARG;
+    // CTAs and rows are counted in 32 bits (what lies in a row, and its bytes, in 64)
+    if (z.items > INT32_MAX || z.rows > INT32_MAX || z.merge > kMostMerged)
+        return FD_ERR_UNSUPPORTED;
     memset(plan, 0, sizeof *plan);
     plan->batch = batch;
     plan->num_tokens = q_indptr_host[batch];
@@ -216,7 +218,7 @@ extern "C" int fd_prefill_paged_int8(const fd_prefill_plan *plan, int num_pages,
     const fd_prefill_plan &x = *plan;
     if (x.batch < 0 || x.num_tokens < 0 || x.num_qo_heads <= 0 || x.num_kv_heads <= 0 ||
         x.num_qo_heads % x.num_kv_heads != 0 || x.num_items < 0 || x.num_partial_rows < 0 || x.num_merged_rows < 0 ||
-        x.num_merged_rows > x.num_partial_rows || x.num_page_entries < 0 || x.chunk <= 0 ||
+        x.num_merged_rows > x.num_partial_rows || x.num_merged_rows > kMostMerged || x.num_page_entries < 0 || x.chunk <= 0 ||
         x.chunk % fd::kPrefillTile != 0 || x.workspace_bytes < prefill_bytes(x.num_partial_rows))
         return FD_ERR_INVALID_ARG;
     const int group = x.num_qo_heads / x.num_kv_heads;

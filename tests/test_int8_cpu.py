@@ -135,3 +135,25 @@ def test_no_load_past_the_coherent_path(name):
     code = "\n".join(line.split("//")[0] for line in source.splitlines())
     for word in ("__ldg", "ld.global.nc", "__restrict__"):
         assert word not in code, word
+
+
+@pytest.mark.parametrize("keys", [262144, 262145, 400000])
+@pytest.mark.parametrize("hq,hkv", [(32, 8), (64, 8)])
+def test_plan_prefill_of_long_prompts(keys, hq, hkv):
+    """From 262145 keys on a request is cut, and has its partial rows, whatever its tokens."""
+    pages = -(-keys // 16)
+    rc, p = _plan_prefill(batch=1, hq=hq, hkv=hkv, qi=[0, keys], ip=[0, pages], last=[keys - 16 * (pages - 1)])
+    splits = -(-keys // 262144)
+    assert rc == 0 and p.num_partial_rows == (0 if splits == 1 else splits * keys * hq)
+    assert p.workspace_bytes >= p.num_partial_rows * 516
+
+
+def test_plan_prefill_beyond_32_bits_of_rows():
+    kw = dict(batch=1, hq=32, hkv=8, ip=[0, 18750], last=[16])   # 300000 keys, two splits
+    rc, p = _plan_prefill(qi=[0, (1 << 25) - 1], **kw)
+    assert rc == 0 and p.num_partial_rows == ((1 << 25) - 1) * 64
+    assert _plan_prefill(qi=[0, 1 << 25], **kw)[0] == -2
+    plan = _plan_prefill()[1]
+    plan.num_merged_rows = plan.num_partial_rows = 2 ** 31 - 1
+    plan.workspace_bytes = 1 << 62
+    assert _prefill(plan, wsb=(1 << 63) - 1) == -1

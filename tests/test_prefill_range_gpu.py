@@ -127,3 +127,23 @@ def test_prefill_v_scales_far_apart_and_no_numbers(cuda_device, tokens, value):
     bad[first:tokens, 2:4] = True
     assert torch.equal(o.isnan().all(-1), bad) and torch.equal(o.isnan().any(-1), bad)
     assert torch.equal(lse.isnan(), bad)
+
+
+def test_prefill_of_many_partial_rows(cuda_device):
+    """More than 2^24 partial rows of 512 bytes: offsets in values beyond 32 bits.  O within
+    half a step of bf16, and 2^-10 of sum w |v| for the weights' f16 and the logits."""
+    tokens, keys = 70000, 1024
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    t, c, _, _ = make("rows", 32, 8, [1], [keys], 16, cuda_device)
+    gen = torch.Generator(cuda_device).manual_seed(1)
+    q = torch.randn((tokens, 32, D), device=cuda_device, generator=gen, dtype=torch.bfloat16)
+    qi = indptr([tokens])
+    plan = plan_of(t, q, 8, qi, False, chunk=128)
+    assert plan.num_partial_rows * D > 2 ** 31
+    o, lse = run(t, c, q, qi, False, plan=plan)
+    at = torch.tensor([0, 1, 64, 32767, 32768, 65535, 65536, 69998, 69999], device=cuda_device)
+    want, lse_want = attention(q[at], t, c, D ** -0.5, indptr([len(at)]), False)
+    a, _ = attention(q[at], t, dict(c, v=c["v"].clamp(min=-127).abs()), D ** -0.5, indptr([len(at)]), False)
+    assert float(((o[at].double() - want).abs() / (2.0 ** -8 * want.abs() + 2.0 ** -10 * a)).max()) <= 1
+    assert float((lse[at].double() - lse_want).abs().max()) <= 2e-5
