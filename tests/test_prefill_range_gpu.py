@@ -147,3 +147,21 @@ def test_prefill_of_many_partial_rows(cuda_device):
     a, _ = attention(q[at], t, dict(c, v=c["v"].clamp(min=-127).abs()), D ** -0.5, indptr([len(at)]), False)
     assert float(((o[at].double() - want).abs() / (2.0 ** -8 * want.abs() + 2.0 ** -10 * a)).max()) <= 1
     assert float((lse[at].double() - lse_want).abs().max()) <= 2e-5
+
+
+@pytest.mark.parametrize("which", ["ks", "vs"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf"), -0.5])
+@pytest.mark.parametrize("tokens", [20, 200])
+def test_prefill_scales_that_are_no_numbers_reach_all_that_see_them(cuda_device, which, value, tokens):
+    """O and LSE of each row that attends the page are NaN, all others as without it (two
+    roundings of bf16, since a second pass may have other references)."""
+    t, c, q, qi = make("nan", 8, 4, [tokens, 30], [300, 200], 16, cuda_device)
+    want, lse_want = run(t, c, q, qi, True)
+    c[which][int(t["ids"][17]), 1] = value   # keys 272 .. 287 of the first request, head 1
+    o, lse = run(t, c, q, qi, True)
+    bad = torch.zeros(o.shape[:2], dtype=torch.bool, device=cuda_device)
+    bad[max(0, tokens - 300 + 272): tokens, 2:4] = True
+    assert torch.equal(o.isnan().all(-1), bad) and torch.equal(o.isnan().any(-1), bad)
+    assert torch.equal(lse.isnan(), bad)
+    close = (o.float() - want.float()).abs() <= 2.0 ** -7 * want.float().abs() + 2.0 ** -9
+    assert bool(close.all(-1)[~bad].all()) and float((lse - lse_want)[~bad].abs().max()) <= 4e-5
