@@ -807,9 +807,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                     if (lane == 0)
                         mbar_arrive(smem_addr(&sm->p_ready[s][part]));
                 };
-                if constexpr (careful) {
-                    // 16 scores at a time, rarely run and short; for V scales of any size with a
-                    // second exponential, over `top`
+                if (careful && wide) {
+                    // 16 scores at a time, rarely run and short: two exponentials each, over E and
+                    // over `top`
                     const float from = top == -INFINITY ? 0.f : top;
 #pragma unroll 1
                     for (int c = 0; c < kGroups; ++c) {
@@ -818,13 +818,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                         tmem_ld16(s_col + 16 * c, x);
                         tmem_wait_ld();
                         settle(x);
-                        if (wide) {
-                            const float less = g.y == g.y ? from : g.y;   // (no number: neither is the sum)
+                        const float less = g.y == g.y ? from : g.y;   // (no number: neither is the sum)
 #pragma unroll
-                            for (int j = 0; j < 16; ++j)
-                                l += 16 * c + j < valid ? ex2(fmaf(__uint_as_float(x[j]), c2 * g.x, -less)) : 0.f;
-                        }
-                        float part = 0.f;
+                        for (int j = 0; j < 16; ++j)
+                            l += 16 * c + j < valid ? ex2(fmaf(__uint_as_float(x[j]), c2 * g.x, -less)) : 0.f;
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
                             float e[2];
@@ -832,12 +829,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
                             for (int k = 0; k < 2; ++k) {
                                 e[k] = fmaf(__uint_as_float(x[j + k]), c2 * g.x, g.y + base);
                                 e[k] = 16 * c + j + k < valid ? ex2(e[k]) : 0.f;
-                                part += e[k];
                             }
                             x[j / 2] = pack_f16x2(make_float2(e[0], e[1]));
                         }
-                        if (!wide)
-                            l = fmaf(part, g.z, l);
                         tmem_st8(s_col + 8 * c, x);   // (over the first half of the scores, as below)
                         if (c == 3)
                             publish(0);
