@@ -577,10 +577,11 @@ int fd_decode_shared_paged_fp8(const fd_shared_plan *plan, int num_pages,
  * of a row's weight and has V = 0, O is within 0.5 % of its norm for 30000 keys.)
  *
  * Scales of any size, as fd_append_paged_int8 leaves them, not below 0: one that is, and
- * one of NaN or +-inf, makes what attends its page NaN.  V scales of 2^-126 (pages of
- * values below 2^-119, if not of zeros) may count as up to 2^-60 of the largest of the
- * split's first 128 keys.  A call takes two to three times as long where V scales are 2^20
- * of that one or more, or 2^-40 or less, but not 2^-126.
+ * one of NaN or +-inf, makes what attends its page NaN.  With R the largest V scale of a
+ * split's first 128 keys (1 where all are of pages of zeros), one of 2^-126 (a page of values
+ * below 2^-119, if not of zeros) may count as up to 2^-60 R.  Where others are 2^20 R or more,
+ * or 2^-40 R or less, or where a score is some 2^12 times all before it, the split's rows
+ * are attended twice: such a call takes two to three times as long.
  *
  * The plan is made once on the host for the tokens and tables and a call takes device
  * data only, makes no host-synchronising call and may be captured in a CUDA graph; the

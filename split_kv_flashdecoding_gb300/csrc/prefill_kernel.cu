@@ -423,12 +423,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll 1
                 for (int t = 0; t < n; ++t) {
                     if (t == 0) {
-                        // pages of zeros have the smallest scale: no reference
+                        // pages of zeros have the smallest scale: no reference (1 where all have)
                         float m = lane >= 8 && scale > kSmallestScale && scale < INFINITY ? scale : 0.f;
 #pragma unroll
                         for (int o = 1; o < 32; o <<= 1)
                             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        const float ref = m > 0.f ? m : kSmallestScale;
+                        const float ref = m > 0.f ? m : 1.f;
                         ref_log = log2f(ref);
                         if (lane == 0) {
                             sm->v_ref = ref;
