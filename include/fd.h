@@ -568,7 +568,8 @@ int fd_decode_shared_paged_fp8(const fd_shared_plan *plan, int num_pages,
  *     o          bf16 [num_tokens, Hq, D]; lse fp32 [num_tokens, Hq], or NULL
  * Token t of T attends keys 0 .. L_b - T + t (causal), its own the last of them, or all
  * L_b.  A token that sees no key (none there, or causal with T > L_b) gets O = 0,
- * LSE = -inf.  Rows of q and o from q_indptr[B] on are not touched.
+ * LSE = -inf.  Rows of q and o from q_indptr[B] on are not touched.  o may be q itself
+ * where its tokens follow one another (stride Hq * D), and shares no value with it otherwise.
  *
  * Scores and sums are fp32; a softmax weight is rounded once, to f16, O once, to bf16.
  * The first is off by 2^-11 of the weight or, when that is more, by 2^-26 of the largest

@@ -46,4 +46,18 @@ cudaError_t launch_dependent(Kernel kern, dim3 grid, int threads, int smem_bytes
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// Whether rows of `na` values, `sa` apart, from a on share a value with rows of `nb`
+// values, `sb` apart, from b on: n rows each, 16-bit values.  Rows that lie between
+// one another at different distances count as if they did.
+inline bool rows_overlap(const void *a, int64_t na, int64_t sa, const void *b, int64_t nb, int64_t sb, int64_t n)
+{
+    const int64_t x = (int64_t)(reinterpret_cast<uintptr_t>(a) / 2), y = (int64_t)(reinterpret_cast<uintptr_t>(b) / 2);
+    if (x + (n - 1) * sa + na <= y || y + (n - 1) * sb + nb <= x)
+        return false;
+    if (n == 1 || sa != sb)
+        return true;
+    const int64_t d = ((x - y) % sa + sa) % sa;   // where a's rows begin behind b's, up to whole rows
+    return d < nb || d + na > sa;
+}
+
 }  // namespace fd

@@ -36,20 +36,6 @@ bool overlap(const int32_t *a, int64_t na, const int32_t *b, int64_t nb)
     return na > 0 && nb > 0 && x < y + nb * sizeof(int32_t) && y < x + na * sizeof(int32_t);
 }
 
-// Whether rows of `na` values, `sa` apart, from a on share a value with rows of `nb`
-// values, `sb` apart, from b on: n rows each, 16-bit values.  Rows that lie between
-// one another at different distances count as if they did.
-bool rows_overlap(const void *a, int64_t na, int64_t sa, const void *b, int64_t nb, int64_t sb, int64_t n)
-{
-    const int64_t x = (int64_t)(reinterpret_cast<uintptr_t>(a) / 2), y = (int64_t)(reinterpret_cast<uintptr_t>(b) / 2);
-    if (x + (n - 1) * sa + na <= y || y + (n - 1) * sb + nb <= x)
-        return false;
-    if (n == 1 || sa != sb)
-        return true;
-    const int64_t d = ((x - y) % sa + sa) % sa;   // where a's rows begin behind b's, up to whole rows
-    return d < nb || d + na > sa;
-}
-
 bool finite_positive(double x)
 {
     return x > 0 && x <= 1e300;
@@ -159,9 +145,9 @@ int append(int batch, int num_tokens, int num_qo_heads, int num_kv_heads, int he
     // The rotated queries may go over the queries themselves; elsewhere they would
     // change what other threads still read.
     const bool in_place = q_out == q && (q_out_stride == q_stride || num_tokens == 1);
-    if (has_q && ((!in_place && rows_overlap(q_out, q_row, q_out_stride, q, q_row, q_stride, num_tokens)) ||
-                  rows_overlap(q_out, q_row, q_out_stride, k, kv_row, k_stride, num_tokens) ||
-                  rows_overlap(q_out, q_row, q_out_stride, v, kv_row, v_stride, num_tokens)))
+    if (has_q && ((!in_place && fd::rows_overlap(q_out, q_row, q_out_stride, q, q_row, q_stride, num_tokens)) ||
+                  fd::rows_overlap(q_out, q_row, q_out_stride, k, kv_row, k_stride, num_tokens) ||
+                  fd::rows_overlap(q_out, q_row, q_out_stride, v, kv_row, v_stride, num_tokens)))
         return FD_ERR_INVALID_ARG;
     if (kv_type == fd::kKvTypeFp8 && (!k_scale || !v_scale || !aligned(k_scale, 4) || !aligned(v_scale, 4)))
         return FD_ERR_INVALID_ARG;

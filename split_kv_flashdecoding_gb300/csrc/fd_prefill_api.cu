@@ -227,6 +227,12 @@ extern "C" int fd_prefill_paged_int8(const fd_prefill_plan *plan, int num_pages,
         return FD_ERR_UNSUPPORTED;
     if ((int64_t)x.num_tokens * group > INT32_MAX - fd::kPrefillRows)
         return FD_ERR_INVALID_ARG;
+    // O may go over the queries themselves, which a CTA has read before it writes; elsewhere
+    // it would change what others still read.
+    const int64_t row = (int64_t)x.num_qo_heads * kHeadDim;
+    if (q && o && x.num_items > 0 && !(o == q && (q_stride == row || x.num_tokens == 1)) &&
+        fd::rows_overlap(o, row, row, q, row, q_stride, x.num_tokens))
+        return FD_ERR_INVALID_ARG;
     if (!workspace || workspace_bytes < x.workspace_bytes)
         return FD_ERR_WORKSPACE;
     if (!aligned(workspace, 16))

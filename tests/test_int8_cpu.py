@@ -157,3 +157,14 @@ def test_plan_prefill_beyond_32_bits_of_rows():
     plan.num_merged_rows = plan.num_partial_rows = 2 ** 31 - 1
     plan.workspace_bytes = 1 << 62
     assert _prefill(plan, wsb=(1 << 63) - 1) == -1
+
+
+def test_prefill_refuses_outputs_over_other_queries():
+    """o over q itself is one thing, over other rows of it another (-3: without a workspace
+    it goes no further)."""
+    q, row = 1 << 20, 2 * 8 * 128   # bytes of a token's heads, 7 tokens
+    for o in (q, q + 7 * row, q - 7 * row):
+        assert _prefill(o=P(o), q=P(q), qs=1024, ws=None) == -3
+    for o in (q + 16, q + row, q - row, q + 7 * row - 16, q - 7 * row + 16):
+        assert _prefill(o=P(o), q=P(q), qs=1024, ws=None) == -1
+    assert _prefill(o=P(q), q=P(q), qs=1032, ws=None) == -1

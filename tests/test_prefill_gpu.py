@@ -361,3 +361,14 @@ def test_prefill_waits_are_bounded(cuda_device):
                           *dev_tables(t, cuda_device), D ** -0.5, workspace=ws)
     assert fd.get_device_status(ws) == -5
     compare(run(t, c, q, qi, True), t, c, q, qi, True)
+
+
+@pytest.mark.parametrize("chunk", [0, 128])
+def test_prefill_over_its_own_queries(cuda_device, chunk):
+    t, c, q, qi = make("over", 8, 4, [300, 1, 40], [300, 700, 640], 16, cuda_device)
+    for causal in (True, False):
+        plan = plan_of(t, q, 4, qi, causal, chunk=chunk)
+        want = run(t, c, q, qi, causal, plan=plan)
+        x = q.clone()
+        o, lse = run(t, c, x, qi, causal, plan=plan, o=x)
+        assert o.data_ptr() == x.data_ptr() and torch.equal(x, want[0]) and torch.equal(lse, want[1])
