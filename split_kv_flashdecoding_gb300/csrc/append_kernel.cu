@@ -7,7 +7,9 @@
 // * 2^64, and position * step_i modulo 2^64 is the exact fraction of a turn of
 // that step (the plan's rounding of f_i, 2^-53 of it, is all that a far
 // position loses), so one integer product replaces a long range reduction.
-// The arithmetic is fp32; each output is rounded once.
+// The fraction is rounded to fp32 for its sine and cosine (the angle by 2^-25 of a half
+// turn, 9e-8, at most, as much as these are rounded by themselves).  The arithmetic is
+// fp32; each output is rounded once.
 //
 // Bound: bytes of q (in and out), k, v and the cache rows.  A CTA takes one
 // token (short calls, whose time is the chain token -> request -> page -> row)

@@ -25,10 +25,12 @@
 //
 // Bound: the tensor cores at many rows (2048 cycles for the products of two row tiles
 // with 128 keys), one chain of scores, weights and products a stream beside it: 3100
-// cycles.  32 heads, 8192 queries and keys 432 us, 1.27 PFLOP/s, of which an item's start
+// cycles.  32 heads, 8192 queries and keys 414 us, 1.33 PFLOP/s, of which an item's start
 // and end (queries 3.7 us, first weights 3.6, output 2.6, with nothing beside them) are
-// a sixth; 32768 queries and keys 5.9 ms, 1.49 PFLOP/s; 64 heads, a chunk of 2047 behind
-// cached keys, 30001 in all, 1.55 ms, 1.34 PFLOP/s.  At few rows the bytes: 2400 cycles
+// a sixth; 32768 queries and keys 5.8 ms, 1.50 PFLOP/s; 64 heads, a chunk of 2047 behind
+// 30001 cached keys, 1.53 ms, 1.36 PFLOP/s.  The roles' loops together are near
+// what the SM holds of instructions: the same steps in other code ran up to 8 % slower
+// (stalls for instructions 1.1 an issue for 0.6).  At few rows the bytes: 2400 cycles
 // a tile of 32 KB of codes, 3.3 TB/s; the widening's chain (copies, loads, stores,
 // hand-over), the weights' and the copies' latency each take a part of it, and leaving
 // any one out saves 3 to 15 %.
@@ -43,7 +45,7 @@
 // A row's reference E comes from the tiles up to the last one (the first tile's from
 // its own largest e): of each the log of its sum of weights, which costs no
 // comparisons; it is up to log2 128 above the largest e, but then the row's sum is that
-// much larger, too, and what f16 loses of small weights is as little of it.  E is
+// much larger, too, and what f16 loses of weights near the others is as little of it.  E is
 // raised, with O rescaled, when that is over 2^kRaise above it: so no step waits for
 // its own maximum.  A score so far above all before it that its weight is over
 // f16's range is seen at the end, and the CTA then does its item again with the
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
             // half of the head, 16 values a lane: the lanes of a quarter warp are two rows
             // r and r ^ 5 and four chunks of 16 bytes, whose 32 bytes of f16 meet no bank
             // twice.  (A unit of each of the eight groups, eight page rows to ask the other
-            // lanes for: 443 us of 438 for 8192 queries and keys of 16 heads.)  The codes
+            // lanes for: 443 us of 438 for 8192 queries and keys of 32 heads.)  The codes
             // come by 16-byte asynchronous copies, two or four tiles ahead, each to a place
             // of its lane's own: a lane waits for its own copies alone.  (Loads into
             // registers a tile ahead: 2.9 us a tile of one row tile; their latency showed.)
