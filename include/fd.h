@@ -354,9 +354,10 @@ int fd_decode_paged_int4(int batch, int num_qo_heads, int num_kv_heads, int head
  *
  * fd_decode_paged_int8 -- fd_decode_paged over this cache.  q stays bf16 and O, LSE
  * fp32; the codes widen to f16 exactly, a page's K scale multiplies its logits in
- * fp32 and its V scale its softmax weights, as an INT4 row's do.  Any scales, of
- * either sign; one of +-inf or NaN propagates (as NaN) to the requests that attend
- * the page.  Workspace and plan as for fd_decode_paged.
+ * fp32 and its V scale its softmax weights, as an INT4 row's do (the two together are
+ * kept to 2^-22 of themselves and 2^-40 of the request's largest weight and V scale).  Any
+ * scales, of either sign; one of +-inf or NaN propagates (as NaN) to the requests that
+ * attend the page.  Workspace and plan as for fd_decode_paged.
  */
 int fd_decode_paged_int8(int batch, int num_qo_heads, int num_kv_heads, int head_dim,
                          int page_size, int num_pages, const int32_t *kv_page_indptr_host,

@@ -118,12 +118,35 @@ struct Stage {
     }
 };
 constexpr int kMaxGroup = 8;                   // rows 8-15 of the MMA carry the lo part of P
-constexpr int kNoExp = -1000;                  // INT4 V-scale exponent before any nonzero scale
 
 // 2^k as a float, exactly, for k in [-126, 127]; 0 below, +inf above.
 __device__ __forceinline__ float pow2i(int k)
 {
     return k < -126 ? 0.f : k > 127 ? INFINITY : __int_as_float((127 + k) << 23);
+}
+
+// f16 weights (FP8, INT4 and INT8 K/V) are 2^kWeightUp larger, so that those far below the
+// row's largest, 1, stay above f16's smallest number: hi and lo are 2^-22 of a weight down
+// to 2^-17 and 2^-40 below.  (At 1, beside a first key with 99 % of 65536 keys' weight and
+// V = 0, O was off by 0.3 to 1.3 % of its norm.)  The sums of weights are as they were, and
+// O's power is taken back where the state is written: of normal weights no bit changes.
+constexpr int kWeightUp = 15;
+constexpr int kNoExp = kWeightUp - 126;        // V-scale exponent before any scale of 2^kNoExp
+
+// The exponent of the largest V scale seen so far (INT4, INT8: scale < 2^v_exp; 129 with an
+// infinite or NaN one), from kNoExp on, and the powers of two on weights and O that go with
+// it: all normal numbers.
+__device__ __forceinline__ int scale_exponent(float vmax)
+{
+    return max(((__float_as_int(vmax) >> 23) & 0xFF) - 126, kNoExp);
+}
+__device__ __forceinline__ float weight_factor(int v_exp)
+{
+    return __int_as_float((127 + kWeightUp - v_exp) << 23);
+}
+__device__ __forceinline__ float output_factor(int v_exp)
+{
+    return __int_as_float((127 - kWeightUp + v_exp) << 23);
 }
 
 // A bound of two V scales' magnitudes; NaN where either is (fmaxf drops it).
@@ -710,11 +733,11 @@ __device__ __forceinline__ void consume_tile(uint32_t st, const PageScales &ps, 
     l_part = fmaf(l_part, alpha, psum);
     // INT4: the tile's V scales (0 for masked keys: another request's row or
     // past the end is never read).  P V runs in f16, so the weights enter it as
-    // p * v_scale * 2^-v_exp, where 2^v_exp bounds every V scale seen so far
-    // by this warp: the products stay in [-1, 1], far from f16's overflow and
-    // subnormal range, whatever the scales.  When v_exp grows, O is rescaled
+    // p * v_scale * 2^(kWeightUp - v_exp), where 2^v_exp bounds every V scale seen so far
+    // by this warp: the products stay within f16's range, and those of scales down to
+    // 2^-39 of the largest in its normal one.  When v_exp grows, O is rescaled
     // by the same exact power of two, together with the softmax rescale;
-    // write_state multiplies 2^v_exp back.
+    // write_state takes the power back.
     // INT8: the same with the two scales of the tile's 16-key halves.
     float vs[2][4] = {};
     float oscale = alpha;
@@ -742,9 +765,9 @@ __device__ __forceinline__ void consume_tile(uint32_t st, const PageScales &ps, 
         vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, 2));
         }
         if (!(vmax <= 0.f)) {   // a nonzero, inf or NaN scale: vmax < 2^e
-            const int e = ((__float_as_int(vmax) >> 23) & 0xFF) - 126;
+            const int e = scale_exponent(vmax);
             if (e > v_exp) {
-                oscale *= pow2i(v_exp - e);   // 0 when v_exp is still kNoExp
+                oscale *= pow2i(v_exp - e);
                 v_exp = e;
             }
         }
@@ -761,14 +784,13 @@ __device__ __forceinline__ void consume_tile(uint32_t st, const PageScales &ps, 
     // P as the A operand: k-step ks covers keys 16ks .. 16ks+15 (n-tiles
     // 2ks, 2ks+1); rows 0-7 hi, rows 8-15 lo = P - hi, in the MMA's type.
     uint32_t pa[2][4];
-    // INT4: 2^-v_exp (NaN-propagating 0 once an infinite or NaN scale was seen)
-    const float vinv = S::kScales ? (v_exp == kNoExp ? 1.f : pow2i(-v_exp)) : 1.f;
+    const float vinv = S::kScales ? weight_factor(v_exp) : S::kFp8 ? (float)(1 << kWeightUp) : 1.f;
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
         float p0 = x[4 * ks], p1 = x[4 * ks + 1];
         float p2 = x[4 * ks + 2], p3 = x[4 * ks + 3];
-        if constexpr (S::kInt8) {
-            const float w = vs[ks][0] * vinv;
+        if constexpr (S::kByte) {
+            const float w = S::kInt8 ? vs[ks][0] * vinv : vinv;
             p0 *= w;
             p1 *= w;
             p2 *= w;
@@ -1244,7 +1266,8 @@ struct RowConsumer {
     template <int NC>
     __device__ __forceinline__ void write(uint8_t *state, int warp, int lane, float fp8_vscale) const
     {
-        const float vscale = Stage<KV, DT>::kScales ? (v_exp == kNoExp ? 1.f : pow2i(v_exp)) : fp8_vscale;
+        const float vscale = Stage<KV, DT>::kScales ? output_factor(v_exp)
+                                                     : fp8_vscale * (DT == kKvFp8 ? output_factor(0) : 1.f);
         write_state<G, NC, DT>(state, warp, lane, o_acc, m_run, l_part, vscale);
     }
 };
@@ -1416,9 +1439,9 @@ struct ColumnConsumer {
         l[1] = fmaf(l[1], os1, ps1);
         if constexpr (S::kScales) {
             if (!(vmax <= 0.f)) {   // a nonzero, inf or NaN scale: vmax < 2^e
-                const int e = ((__float_as_int(vmax) >> 23) & 0xFF) - 126;
+                const int e = scale_exponent(vmax);
                 if (e > v_exp) {
-                    const float f = pow2i(v_exp - e);   // 0 when v_exp is still kNoExp
+                    const float f = pow2i(v_exp - e);
                     os0 *= f;
                     os1 *= f;
                     v_exp = e;
@@ -1436,21 +1459,19 @@ struct ColumnConsumer {
         }
 
         // ---- P^T (B operand of k-step mb: keys 16 mb + 2t4 (+1) in b0,
-        // + 8 in b1, column g): the weights (INT4: p * v_scale * 2^-v_exp) as
-        // f16 (hi columns) or their remainder after f16 (lo columns), packed
+        // + 8 in b1, column g): the weights (with their power of two, INT4 and
+        // INT8 with the V scale) as f16 (hi columns) or their remainder after f16 (lo columns), packed
         // per key row and transposed
-        const float vinv = S::kScales && v_exp != kNoExp ? pow2i(-v_exp) : 1.f;
+        const float vinv = S::kScales ? weight_factor(v_exp) : (float)(1 << kWeightUp);
         uint32_t pt[2][2];
 #pragma unroll
         for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 float p0 = x[mb][2 * hf], p1 = x[mb][2 * hf + 1];
-                if constexpr (S::kScales) {
-                    const float w = (kInt8 ? vs8[mb] : vs[mb][hf]) * vinv;
-                    p0 *= w;
-                    p1 *= w;
-                }
+                const float w = S::kScales ? (kInt8 ? vs8[mb] : vs[mb][hf]) * vinv : vinv;
+                p0 *= w;
+                p1 *= w;
                 p0 = fmaf(-lo[0], f16_round(p0), p0);
                 p1 = fmaf(-lo[1], f16_round(p1), p1);
                 pt[mb][hf] = movmatrix_trans(pack_f16(p0, p1));
@@ -1512,7 +1533,7 @@ struct ColumnConsumer {
         float *comb_m = comb_acc + NC * G * kHeadDim;
         float *comb_l = comb_m + NC * G;
         const int g = lane >> 2, t4 = lane & 3;
-        const float vscale = DT == kKvFp8 ? fp8_vscale : v_exp == kNoExp ? 1.f : pow2i(v_exp);
+        const float vscale = DT == kKvFp8 ? fp8_vscale * output_factor(0) : output_factor(v_exp);
         float lt[2] = {l[0], l[1]};
 #pragma unroll
         for (int sh = 4; sh < 32; sh <<= 1) {
