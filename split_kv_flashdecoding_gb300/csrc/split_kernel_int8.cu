@@ -10,9 +10,9 @@
 //
 // Bound: with pages of 16 keys the copy engine's rate a box, as for FP8; else the
 // consumers' arithmetic beside the copies.  32 query heads over 65536 keys of 8 KV
-// heads take 37.3 us in pages of 16 (FP8 36.3) and 31 in pages of 64 (28.7); 64
-// requests of up to 16384 keys in pages of 64 203 us, 5.2 TB/s (199); 16 of 64 heads
-// over 32768 keys in pages of 32 224 us, 4.8 TB/s (204).
+// heads take 37.3 us in pages of 16 (FP8 36.1) and 31 in pages of 64 (28.3); 64
+// requests of up to 16384 keys in pages of 64 202 us, 5.2 TB/s (197); 16 of 64 heads
+// over 32768 keys in pages of 32 222 us, 4.8 TB/s (204).
 #include "split_kernel.cuh"
 
 namespace fd {
